@@ -17,6 +17,12 @@ Calls (same names as the C ABI):
   hadamard32        stand-alone 32-point block rotation
   mxfp4_tensor_amax device max-abs and NVFP4 per-tensor exponent
                     (tensor_amax, nvfp4_tensor_exp)
+  mxfp4_rmsnorm_quantize   residual addition + root-mean-square norm +
+                    quantization in one pass; mxfp4_rmsnorm_backward
+  mxfp4_swiglu_quantize    gated activation + quantization in one pass;
+                    mxfp4_swiglu_backward
+  mxfp4_gemv        a few activation rows (bf16 or MXFP8) times a 4-bit
+                    weight matrix (MXFP4 or NVFP4)
 """
 from .binding import (  # noqa: F401
     BLOCK_1X32,
@@ -45,6 +51,11 @@ from .binding import (  # noqa: F401
     mxfp4_gemm,
     mxfp4_gemm_noalloc,
     mxfp4_gemm_quantize,
+    mxfp4_gemv,
+    mxfp4_rmsnorm_backward,
+    mxfp4_rmsnorm_quantize,
+    mxfp4_swiglu_backward,
+    mxfp4_swiglu_quantize,
     mxfp8_gemm,
     gemm_workspace_size,
     nvfp4_gemm,
@@ -54,3 +65,4 @@ from .binding import (  # noqa: F401
     scale_numel,
 )
 from .linear import LinearRecipe, Mxfp4Linear, mxfp4_linear, recipe_1d, recipe_2d_sr  # noqa: F401
+from .ffn import Mxfp4FeedForward, rmsnorm, swiglu  # noqa: F401

@@ -8,6 +8,7 @@ pass, and forwards raw pointers plus the current CUDA stream to the C ABI.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -123,6 +124,22 @@ def load_library(path: str) -> ctypes.CDLL:
     L.mxfp4_tensor_amax.argtypes = [P, i32, i64, i64, i64, P, P, P]
     L.hadamard32.restype = i32
     L.hadamard32.argtypes = [P, i32, i64, i64, i64, ctypes.c_uint32, i32, P, P]
+    f32 = ctypes.c_float
+    L.mxfp4_rmsnorm_quantize.restype = i32
+    L.mxfp4_rmsnorm_quantize.argtypes = [P, i32, i64, i64, i64, P, i64, P, i32, f32, P, i64, P, i32, i64, P,
+                                         ctypes.POINTER(_CParams), P, P, P]
+    L.mxfp4_rmsnorm_backward_workspace_size.restype = sz
+    L.mxfp4_rmsnorm_backward_workspace_size.argtypes = [i64, i64]
+    L.mxfp4_rmsnorm_backward.restype = i32
+    L.mxfp4_rmsnorm_backward.argtypes = [P, i32, i64, P, i32, i64, P, i32, P, P, i64, i64, i64, P, i64, P, P,
+                                         sz, P]
+    L.mxfp4_swiglu_quantize.restype = i32
+    L.mxfp4_swiglu_quantize.argtypes = [P, i64, P, i64, i32, i64, i64, P, i32, i64, ctypes.POINTER(_CParams),
+                                        P, P, P]
+    L.mxfp4_swiglu_backward.restype = i32
+    L.mxfp4_swiglu_backward.argtypes = [P, i32, i64, P, i64, P, i64, i32, i64, i64, P, i64, P, i64, P]
+    L.mxfp4_gemv.restype = i32
+    L.mxfp4_gemv.argtypes = [P, i32, i64, P, P, P, i32, i32, i32, i64, i64, i64, P, i32, i64, P]
     L.mxfp4_status_string.restype = ctypes.c_char_p
     L.mxfp4_status_string.argtypes = [i32]
     L.mxfp4_last_error.restype = ctypes.c_char_p
@@ -491,6 +508,274 @@ def nvfp4_tensor_exp(x: torch.Tensor, stream=None) -> int:
     host (synchronizes the stream)."""
     _, k = tensor_amax(x, stream=stream)
     return int(k.item())
+
+
+def _on_its_stream(call):
+    """Runs `call` with its `stream` argument as PyTorch's current stream, so
+    that what it allocates (outputs, workspaces) belongs to the stream that
+    its kernels run on."""
+    @functools.wraps(call)
+    def on_stream(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        with torch.cuda.stream(stream):
+            return call(*args, **kw)
+    return on_stream
+
+
+_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
+
+
+def _dtype_of(t: torch.Tensor, name: str) -> int:
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{name} must be bfloat16 or float32 (got {t.dtype})")
+    return dt
+
+
+def _rows_ld(t: torch.Tensor, name: str, rows: int, cols: int) -> int:
+    """Leading dimension of a CUDA matrix [rows, cols] with unit column stride.
+    The stride of a single row (or of an empty matrix) is never used."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} must be [{rows}, {cols}] (got {list(t.shape)})")
+    if rows * cols and t.stride(1) != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return t.stride(0) if rows > 1 and cols else cols
+
+
+def _vector(t: torch.Tensor, name: str, n: int) -> None:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous vector of {n} elements (got {list(t.shape)})")
+
+
+def _same_device(*ts) -> None:
+    devs = {t.device for t in ts if t is not None}
+    if len(devs) > 1:
+        raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
+
+
+def _row_out(row: QuantParams, q, s, rows: int, cols: int, dev):
+    """Codes and scales of a quantized output, allocated or checked."""
+    if q is None:
+        q = torch.empty((rows, row.code_cols(cols)), dtype=torch.uint8, device=dev)
+    else:
+        _buffer(q, rows * row.code_cols(cols), torch.uint8, "q")
+    if s is None:
+        s = _scales_out(rows, cols, row, dev)
+    else:
+        _buffer(s, scale_numel(rows, cols, row.block), torch.uint8, "s")
+    return q, s
+
+
+@_on_its_stream
+def mxfp4_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor | None = None,
+                           row: QuantParams | None = None, *, residual: torch.Tensor | None = None,
+                           eps: float = 1e-6, y_dtype: torch.dtype | None = None, with_rstd: bool = False,
+                           h=None, y=None, rstd=None, q=None, s=None, stream=None):
+    """Residual addition, root-mean-square norm and quantization in one pass:
+    h = x + residual (rounded to x's type), y = h * weight / sqrt(mean(h^2) + eps).
+
+    x, residual [rows, cols] bf16 or fp32 (one type); weight [cols] bf16 or
+    fp32 (None: ones). `row` asks for the quantized y (1x32 or 1x16 blocks,
+    nearest-even), `y_dtype` (or `y`) for y itself, `with_rstd` (or `rstd`) for
+    the reciprocal root mean squares that the backward pass needs. Returns
+    (q, s, y, h, rstd), None for what was not asked for; h comes back when
+    there is a residual (or `h` is given; it may be `x` or `residual`
+    themselves: updated in place)."""
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    rows, cols = x.shape
+    dev = x.device
+    ldx, dt = _rows_ld(x, "x", rows, cols), _dtype_of(x, "x")
+    ldr = ldh = ldy = cols
+    if residual is not None:
+        if residual.dtype != x.dtype:
+            raise TypeError(f"residual must have x's type {x.dtype} (got {residual.dtype})")
+        ldr = _rows_ld(residual, "residual", rows, cols)
+        if h is None:
+            h = torch.empty((rows, cols), dtype=x.dtype, device=dev)
+    wdt = DTYPE_F32
+    if weight is not None:
+        _vector(weight, "weight", cols)
+        wdt = _dtype_of(weight, "weight")
+    if h is not None:
+        if h.dtype != x.dtype:
+            raise TypeError(f"h must have x's type {x.dtype} (got {h.dtype})")
+        ldh = _rows_ld(h, "h", rows, cols)
+    if y is None and y_dtype is not None:
+        y = torch.empty((rows, cols), dtype=y_dtype, device=dev)
+    ydt = DTYPE_F32
+    if y is not None:
+        ydt, ldy = _dtype_of(y, "y"), _rows_ld(y, "y", rows, cols)
+    if rstd is not None:
+        _buffer(rstd, rows, torch.float32, "rstd")
+    elif with_rstd:
+        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    rp = None
+    if row is not None:
+        q, s = _row_out(row, q, s, rows, cols, dev)
+        rp = ctypes.byref(row._c())
+    else:
+        q = s = None
+    _same_device(x, residual, weight, h, y, rstd, q, s)
+    _check(lib().mxfp4_rmsnorm_quantize(
+        _ptr(x), dt, rows, cols, ldx, _ptr(residual), ldr, _ptr(weight), wdt, eps, _ptr(h), ldh,
+        _ptr(y), ydt, ldy, _ptr(rstd), rp, _ptr(q), _ptr(s), _stream(x, stream)))
+    return q, s, y, h, rstd
+
+
+@_on_its_stream
+def mxfp4_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor | None, rstd: torch.Tensor,
+                           *, dh: torch.Tensor | None = None, dx=None, dw=None, with_dw: bool = True,
+                           workspace=None, stream=None):
+    """Gradients of mxfp4_rmsnorm_quantize: (dx, dw) from dy (of y), h and rstd
+    (what the forward call returned; h is x without a residual) and dh (of h,
+    through the residual stream; None: none). dx, in h's type, is the gradient
+    of x and of residual alike (it may be dh itself); dw is in weight's type,
+    None without a weight or with `with_dw` false."""
+    if h.dim() != 2:
+        raise ValueError("h must be 2-D")
+    rows, cols = h.shape
+    dev = h.device
+    ldh, hdt = _rows_ld(h, "h", rows, cols), _dtype_of(h, "h")
+    ldy, ydt = _rows_ld(dy, "dy", rows, cols), _dtype_of(dy, "dy")
+    _buffer(rstd, rows, torch.float32, "rstd")
+    ldd = cols
+    if dh is not None:
+        if dh.dtype != h.dtype:
+            raise TypeError(f"dh must have h's type {h.dtype} (got {dh.dtype})")
+        ldd = _rows_ld(dh, "dh", rows, cols)
+    if dx is None:
+        dx = torch.empty((rows, cols), dtype=h.dtype, device=dev)
+    elif dx.dtype != h.dtype:
+        raise TypeError(f"dx must have h's type {h.dtype} (got {dx.dtype})")
+    ldx = _rows_ld(dx, "dx", rows, cols)
+    wdt, nbytes = DTYPE_F32, 0
+    if weight is not None:
+        _vector(weight, "weight", cols)
+        wdt = _dtype_of(weight, "weight")
+        if dw is None and with_dw:
+            dw = torch.empty(cols, dtype=weight.dtype, device=dev)
+    elif dw is not None:
+        raise ValueError("dw needs a weight")
+    if dw is not None:
+        _buffer(dw, cols, weight.dtype, "dw")
+        nbytes = int(lib().mxfp4_rmsnorm_backward_workspace_size(rows, cols))
+        if workspace is None:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        else:
+            _buffer(workspace, nbytes, torch.uint8, "workspace")
+    _same_device(h, dy, rstd, weight, dh, dx, dw, workspace if dw is not None else None)
+    _check(lib().mxfp4_rmsnorm_backward(
+        _ptr(dy), ydt, ldy, _ptr(h), hdt, ldh, _ptr(weight), wdt, _ptr(rstd), _ptr(dh), ldd, rows, cols,
+        _ptr(dx), ldx, _ptr(dw), _ptr(workspace if dw is not None else None), nbytes, _stream(h, stream)))
+    return dx, dw
+
+
+@_on_its_stream
+def mxfp4_swiglu_quantize(gate: torch.Tensor, up: torch.Tensor, row: QuantParams | None = None, *,
+                          y_dtype: torch.dtype | None = None, y=None, q=None, s=None, stream=None):
+    """y = gate / (1 + exp(-gate)) * up, quantized with `row` and/or stored in
+    `y_dtype` (or into `y`). gate and up [rows, cols] bf16 or fp32 (one type),
+    with any row strides that are multiples of 8. Returns (q, s, y), None for
+    what was not asked for."""
+    if gate.dim() != 2:
+        raise ValueError("gate must be 2-D")
+    rows, cols = gate.shape
+    dev = gate.device
+    ldg, dt = _rows_ld(gate, "gate", rows, cols), _dtype_of(gate, "gate")
+    if up.dtype != gate.dtype:
+        raise TypeError(f"up must have gate's type {gate.dtype} (got {up.dtype})")
+    ldu = _rows_ld(up, "up", rows, cols)
+    if y is None and y_dtype is not None:
+        y = torch.empty((rows, cols), dtype=y_dtype, device=dev)
+    ydt, ldy = DTYPE_F32, cols
+    if y is not None:
+        ydt, ldy = _dtype_of(y, "y"), _rows_ld(y, "y", rows, cols)
+    rp = None
+    if row is not None:
+        q, s = _row_out(row, q, s, rows, cols, dev)
+        rp = ctypes.byref(row._c())
+    else:
+        q = s = None
+    _same_device(gate, up, y, q, s)
+    _check(lib().mxfp4_swiglu_quantize(_ptr(gate), ldg, _ptr(up), ldu, dt, rows, cols, _ptr(y), ydt, ldy, rp,
+                                       _ptr(q), _ptr(s), _stream(gate, stream)))
+    return q, s, y
+
+
+@_on_its_stream
+def mxfp4_swiglu_backward(dy: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, *, dgate=None, dup=None,
+                          stream=None):
+    """Gradients (dgate, dup), in gate's type, of mxfp4_swiglu_quantize from dy
+    (bf16 or fp32). dgate may be gate itself and dup up itself."""
+    if gate.dim() != 2:
+        raise ValueError("gate must be 2-D")
+    rows, cols = gate.shape
+    ldg, dt = _rows_ld(gate, "gate", rows, cols), _dtype_of(gate, "gate")
+    ldu, ldy, ydt = _rows_ld(up, "up", rows, cols), _rows_ld(dy, "dy", rows, cols), _dtype_of(dy, "dy")
+    if dgate is None:
+        dgate = torch.empty((rows, cols), dtype=gate.dtype, device=gate.device)
+    if dup is None:
+        dup = torch.empty((rows, cols), dtype=gate.dtype, device=gate.device)
+    for t, n in ((up, "up"), (dgate, "dgate"), (dup, "dup")):
+        if t.dtype != gate.dtype:
+            raise TypeError(f"{n} must have gate's type {gate.dtype} (got {t.dtype})")
+    _same_device(gate, up, dy, dgate, dup)
+    _check(lib().mxfp4_swiglu_backward(
+        _ptr(dy), ydt, ldy, _ptr(gate), ldg, _ptr(up), ldu, dt, rows, cols,
+        _ptr(dgate), _rows_ld(dgate, "dgate", rows, cols), _ptr(dup), _rows_ld(dup, "dup", rows, cols),
+        _stream(gate, stream)))
+    return dgate, dup
+
+
+_GEMV_CODES = {FORMAT_E4M3: 1, FORMAT_E5M2: 2}     # MXFP4_GEMV_X_*; bf16 is 0
+
+
+@_on_its_stream
+def mxfp4_gemv(x: torch.Tensor, qw: torch.Tensor, sw: torch.Tensor, N: int, K: int,
+               w: QuantParams | None = None, *, sx: torch.Tensor | None = None, x_format: int = FORMAT_E4M3,
+               out_dtype: torch.dtype = torch.bfloat16, y=None, stream=None):
+    """y[M, N] = x W^T for a few rows x [M, K] and a 4-bit weight matrix W [N, K]:
+    codes qw [N, K/2] and scales sw as mxfp4_quantize wrote them with `w` (its
+    block, scale_layout and tensor_exp; default 1x32, row-major).
+
+    x is bf16, or uint8 codes of `x_format` (FORMAT_E4M3 / FORMAT_E5M2) with
+    row-major E8M0 scales sx [M, K/32], as the quantized norm and activation
+    write them. y in out_dtype (or y's own: bf16 or fp32)."""
+    w = QuantParams() if w is None else w
+    if w.elem_format != FORMAT_E2M1:
+        raise ValueError("the weights must be 4-bit (E2M1) codes")
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    M = x.shape[0]
+    ldx = _rows_ld(x, "x", M, K)
+    if x.dtype == torch.bfloat16:
+        if sx is not None:
+            raise ValueError("sx goes with one-byte codes; x is bfloat16")
+        kind = 0
+    elif x.dtype == torch.uint8:
+        if sx is None:
+            raise ValueError("one-byte codes need their scales sx")
+        if x_format not in _GEMV_CODES:
+            raise ValueError(f"x_format {x_format} is not E4M3 or E5M2")
+        _buffer(sx, M * (K // 32), torch.uint8, "sx")
+        kind = _GEMV_CODES[x_format]
+    else:
+        raise TypeError(f"x must be bfloat16 or uint8 codes (got {x.dtype})")
+    _buffer(qw, N * K // 2, torch.uint8, "qw")
+    _buffer(sw, scale_numel(N, K, w.block), torch.uint8, "sw")
+    if y is None:
+        y = torch.empty((M, N), dtype=out_dtype, device=x.device)
+    ydt, ldy = _dtype_of(y, "y"), _rows_ld(y, "y", M, N)
+    _same_device(x, sx, qw, sw, y)
+    _check(lib().mxfp4_gemv(_ptr(x), kind, ldx, _ptr(sx), _ptr(qw), _ptr(sw), w.block, w.scale_layout,
+                            w.tensor_exp, M, N, K, _ptr(y), ydt, ldy, _stream(x, stream)))
+    return y
 
 
 def device_status(stream=None) -> int:

@@ -29,8 +29,10 @@ UNITS = {
     "api.cu": [],
     "quant.cu": ["--fmad=false"],
     "gemm.cu": ["--fmad=false"],
+    "ffn.cu": [],
+    "gemv.cu": [],
 }
-HEADERS = ["internal.h", "mx_device.cuh", "ptx.cuh", "quant_device.cuh", "tma_host.h"]
+HEADERS = ["internal.h", "mx_device.cuh", "ptx.cuh", "quant_device.cuh", "row_device.cuh", "tma_host.h"]
 
 
 def nvcc() -> str:

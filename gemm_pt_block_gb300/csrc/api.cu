@@ -1,6 +1,6 @@
 // api.cu -- the extern "C" entry points declared in include/mxfp4.h:
 // argument validation, status codes and the thread-local error detail; the
-// work itself is enqueued by the launchers in quant.cu and gemm.cu.
+// work itself is enqueued by the launchers in quant.cu, gemm.cu, ffn.cu and gemv.cu.
 #include <cstdarg>
 #include <cstdint>
 #include <cmath>
@@ -381,6 +381,275 @@ mxfp4_status mxfp4_tensor_amax(const void* x, int32_t x_dtype, int64_t rows, int
   return from_cuda(mx::launch_amax(x, x_dtype == MXFP4_DTYPE_F32, rows, cols, ld_x, amax, tensor_exp,
                                    static_cast<cudaStream_t>(stream)),
                    "mxfp4_tensor_amax launch");
+}
+
+namespace {
+// A [rows, cols] matrix operand of the norm, activation and few-row calls.
+mxfp4_status check_matrix(const char* fn, const char* name, const void* p, int32_t dtype, int64_t rows,
+                          int64_t cols, int64_t ld) {
+  if (dtype != MXFP4_DTYPE_BF16 && dtype != MXFP4_DTYPE_F32)
+    return fail(MXFP4_ERR_INVALID_ARG, "%s: bad dtype %d of %s", fn, dtype, name);
+  if (!p && rows * cols > 0) return fail(MXFP4_ERR_INVALID_ARG, "%s: %s is NULL", fn, name);
+  if (ld < cols || ld > kMaxElems)
+    return fail(MXFP4_ERR_SHAPE, "%s: leading dimension %lld of %s (cols %lld)", fn, (long long)ld, name,
+                (long long)cols);
+  if (rows > 1 && too_large(rows, ld)) return fail(MXFP4_ERR_SHAPE, "%s: %s too large (more than 2^40 elements)", fn, name);
+  if (!aligned16(p) || ld % 8 != 0)
+    return fail(MXFP4_ERR_ALIGN, "%s: %s must be 16-byte aligned with a leading dimension %% 8 == 0", fn, name);
+  return MXFP4_OK;
+}
+
+mxfp4_status check_dims(const char* fn, int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 0 || cols % 32 != 0)
+    return fail(MXFP4_ERR_SHAPE, "%s: rows (%lld) must be >= 0 and cols (%lld) a non-negative multiple of 32", fn,
+                (long long)rows, (long long)cols);
+  if (cols >= ((int64_t)1 << 31) || too_large(rows, cols))
+    return fail(MXFP4_ERR_SHAPE, "%s: tensor too large (cols below 2^31, at most 2^40 elements)", fn);
+  return MXFP4_OK;
+}
+
+int64_t elem_bytes(int32_t dtype) { return dtype == MXFP4_DTYPE_F32 ? 4 : 2; }
+
+// Bytes from the first to the last element of a [rows, cols] output (what a
+// bounds-checking build lets a call store to).
+uint64_t extent(int64_t rows, int64_t cols, int64_t ld, int32_t dtype) {
+  if (rows == 0 || cols == 0) return 0;
+  const int64_t n = ((rows - 1) * ld + cols) * elem_bytes(dtype);
+  return (uint64_t)(n > g_extent_shrink ? n - g_extent_shrink : 0);
+}
+
+// The quantized output of the norm and activation calls: 1x32 or 1x16 blocks,
+// nearest-even, no rotation.
+mxfp4_status check_row_quant(const char* fn, const mxfp4_quant_params* p, uint8_t* q, uint8_t* s, int64_t rows,
+                             int64_t cols, mx::RowQuant* o) {
+  *o = mx::RowQuant{};
+  if (!p) return MXFP4_OK;
+  if (p->block != MXFP4_BLOCK_1X32 && p->block != MXFP4_BLOCK_1X16)
+    return fail(MXFP4_ERR_UNSUPPORTED, "%s: output blocks are 1x32 or 1x16", fn);
+  if (p->rounding == MXFP4_ROUND_SR || p->wht)
+    return fail(MXFP4_ERR_UNSUPPORTED, "%s: stochastic rounding and rotation are mxfp4_quantize's", fn);
+  mx::OrientArgs a{};
+  if (mxfp4_status st = check_params(p, q, s, rows, cols, fn, &a)) return st;
+  o->fmt = a.nv ? mx::RowQuant::kNvfp4
+                : a.e5m2 ? mx::RowQuant::kE5m2 : a.e4m3 ? mx::RowQuant::kE4m3 : mx::RowQuant::kE2m1;
+  o->roundup = a.roundup;
+  o->mma = a.mma_layout;
+  o->p2k = a.nv_p2k;
+  o->zmul = a.nv_zmul;
+  o->q = q;
+  o->s = s;
+  o->q_bytes = a.q_bytes;
+  o->s_bytes = a.s_bytes;
+  return MXFP4_OK;
+}
+
+mxfp4_status check_vector(const char* fn, const char* name, const void* p, int32_t dtype) {
+  if (dtype != MXFP4_DTYPE_BF16 && dtype != MXFP4_DTYPE_F32)
+    return fail(MXFP4_ERR_INVALID_ARG, "%s: bad dtype %d of %s", fn, dtype, name);
+  if (!aligned16(p)) return fail(MXFP4_ERR_ALIGN, "%s: %s must be 16-byte aligned", fn, name);
+  return MXFP4_OK;
+}
+}  // namespace
+
+mxfp4_status mxfp4_rmsnorm_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ld_x,
+                                    const void* residual, int64_t ld_residual, const void* weight,
+                                    int32_t weight_dtype, float eps, void* h, int64_t ld_h, void* y,
+                                    int32_t y_dtype, int64_t ld_y, float* rstd, const mxfp4_quant_params* row,
+                                    uint8_t* q, uint8_t* s, void* stream) {
+  const char* fn = "mxfp4_rmsnorm_quantize";
+  mxfp4_status st = check_dims(fn, rows, cols);
+  if (st) return st;
+  if ((st = check_matrix(fn, "x", x, x_dtype, rows, cols, ld_x))) return st;
+  if (residual && (st = check_matrix(fn, "residual", residual, x_dtype, rows, cols, ld_residual))) return st;
+  if (h && (st = check_matrix(fn, "h", h, x_dtype, rows, cols, ld_h))) return st;
+  if (y && (st = check_matrix(fn, "y", y, y_dtype, rows, cols, ld_y))) return st;
+  if (weight && (st = check_vector(fn, "weight", weight, weight_dtype))) return st;
+  if (reinterpret_cast<uintptr_t>(rstd) & 3u) return fail(MXFP4_ERR_ALIGN, "%s: rstd must be 4-byte aligned", fn);
+  if (!(eps >= 0.0f && eps <= 1.0e30f)) return fail(MXFP4_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", fn);
+  if (!row && !y && !h && !rstd) return fail(MXFP4_ERR_INVALID_ARG, "%s: no output is asked for", fn);
+  mx::NormArgs a{};
+  if ((st = check_row_quant(fn, row, q, s, rows, cols, &a.quant))) return st;
+  a.x = x;
+  a.r = residual;
+  a.w = weight;
+  a.h = h;
+  a.y = y;
+  a.rstd = rstd;
+  a.rows = rows;
+  a.cols = cols;
+  a.ld_x = ld_x;
+  a.ld_r = ld_residual;
+  a.ld_h = ld_h;
+  a.ld_y = ld_y;
+  a.h_bytes = h ? extent(rows, cols, ld_h, x_dtype) : 0;
+  a.y_bytes = y ? extent(rows, cols, ld_y, y_dtype) : 0;
+  a.eps = eps;
+  a.y_f32 = y_dtype == MXFP4_DTYPE_F32;
+  return from_cuda(mx::launch_rmsnorm(a, x_dtype == MXFP4_DTYPE_F32, weight && weight_dtype == MXFP4_DTYPE_F32,
+                                      static_cast<cudaStream_t>(stream)),
+                   fn);
+}
+
+size_t mxfp4_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols) {
+  if (rows <= 0 || cols <= 0 || cols >= ((int64_t)1 << 31)) return 0;
+  return (size_t)mx::norm_dw_slices(rows) * (size_t)cols * sizeof(float);
+}
+
+mxfp4_status mxfp4_rmsnorm_backward(const void* dy, int32_t dy_dtype, int64_t ld_dy, const void* h, int32_t h_dtype,
+                                    int64_t ld_h, const void* weight, int32_t weight_dtype, const float* rstd,
+                                    const void* dh, int64_t ld_dh, int64_t rows, int64_t cols, void* dx,
+                                    int64_t ld_dx, void* dw, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+  const char* fn = "mxfp4_rmsnorm_backward";
+  mxfp4_status st = check_dims(fn, rows, cols);
+  if (st) return st;
+  if ((st = check_matrix(fn, "dy", dy, dy_dtype, rows, cols, ld_dy))) return st;
+  if ((st = check_matrix(fn, "h", h, h_dtype, rows, cols, ld_h))) return st;
+  if (dh && (st = check_matrix(fn, "dh", dh, h_dtype, rows, cols, ld_dh))) return st;
+  if ((st = check_matrix(fn, "dx", dx, h_dtype, rows, cols, ld_dx))) return st;
+  if ((weight || dw) && (st = check_vector(fn, "weight", weight, weight_dtype))) return st;
+  if ((st = check_vector(fn, "dw", dw, MXFP4_DTYPE_F32))) return st;
+  if (!rstd && rows > 0) return fail(MXFP4_ERR_INVALID_ARG, "%s: rstd is NULL", fn);
+  if (reinterpret_cast<uintptr_t>(rstd) & 3u) return fail(MXFP4_ERR_ALIGN, "%s: rstd must be 4-byte aligned", fn);
+  const size_t need = dw ? mxfp4_rmsnorm_backward_workspace_size(rows, cols) : 0;
+  if (need && !workspace) return fail(MXFP4_ERR_INVALID_ARG, "%s: workspace is NULL", fn);
+  if (need && workspace_bytes < need)
+    return fail(MXFP4_ERR_INVALID_ARG, "%s: workspace of %zu bytes, %zu are needed", fn, workspace_bytes, need);
+  if (!aligned16(workspace)) return fail(MXFP4_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
+  mx::NormGradArgs a{};
+  a.dy = dy;
+  a.h = h;
+  a.w = weight;
+  a.dh = dh;
+  a.rstd = rstd;
+  a.dx = dx;
+  a.dw = dw;
+  a.ws = static_cast<float*>(workspace);
+  a.rows = rows;
+  a.cols = cols;
+  a.ld_dy = ld_dy;
+  a.ld_h = ld_h;
+  a.ld_dh = ld_dh;
+  a.ld_dx = ld_dx;
+  a.dx_bytes = extent(rows, cols, ld_dx, h_dtype);
+  a.ws_bytes = need;
+  return from_cuda(mx::launch_rmsnorm_grad(a, h_dtype == MXFP4_DTYPE_F32, dy_dtype == MXFP4_DTYPE_F32,
+                                           (weight || dw) && weight_dtype == MXFP4_DTYPE_F32,
+                                           static_cast<cudaStream_t>(stream)),
+                   fn);
+}
+
+mxfp4_status mxfp4_swiglu_quantize(const void* gate, int64_t ld_gate, const void* up, int64_t ld_up, int32_t dtype,
+                                   int64_t rows, int64_t cols, void* y, int32_t y_dtype, int64_t ld_y,
+                                   const mxfp4_quant_params* row, uint8_t* q, uint8_t* s, void* stream) {
+  const char* fn = "mxfp4_swiglu_quantize";
+  mxfp4_status st = check_dims(fn, rows, cols);
+  if (st) return st;
+  if ((st = check_matrix(fn, "gate", gate, dtype, rows, cols, ld_gate))) return st;
+  if ((st = check_matrix(fn, "up", up, dtype, rows, cols, ld_up))) return st;
+  if (y && (st = check_matrix(fn, "y", y, y_dtype, rows, cols, ld_y))) return st;
+  if (!row && !y) return fail(MXFP4_ERR_INVALID_ARG, "%s: no output is asked for", fn);
+  mx::SwigluArgs a{};
+  if ((st = check_row_quant(fn, row, q, s, rows, cols, &a.quant))) return st;
+  a.g = gate;
+  a.u = up;
+  a.y = y;
+  a.rows = rows;
+  a.cols = cols;
+  a.ld_g = ld_gate;
+  a.ld_u = ld_up;
+  a.ld_y = ld_y;
+  a.y_bytes = y ? extent(rows, cols, ld_y, y_dtype) : 0;
+  a.y_f32 = y_dtype == MXFP4_DTYPE_F32;
+  return from_cuda(mx::launch_swiglu(a, dtype == MXFP4_DTYPE_F32, static_cast<cudaStream_t>(stream)), fn);
+}
+
+mxfp4_status mxfp4_swiglu_backward(const void* dy, int32_t dy_dtype, int64_t ld_dy, const void* gate,
+                                   int64_t ld_gate, const void* up, int64_t ld_up, int32_t dtype, int64_t rows,
+                                   int64_t cols, void* dgate, int64_t ld_dgate, void* dup, int64_t ld_dup,
+                                   void* stream) {
+  const char* fn = "mxfp4_swiglu_backward";
+  mxfp4_status st = check_dims(fn, rows, cols);
+  if (st) return st;
+  if ((st = check_matrix(fn, "dy", dy, dy_dtype, rows, cols, ld_dy))) return st;
+  if ((st = check_matrix(fn, "gate", gate, dtype, rows, cols, ld_gate))) return st;
+  if ((st = check_matrix(fn, "up", up, dtype, rows, cols, ld_up))) return st;
+  if ((st = check_matrix(fn, "dgate", dgate, dtype, rows, cols, ld_dgate))) return st;
+  if ((st = check_matrix(fn, "dup", dup, dtype, rows, cols, ld_dup))) return st;
+  mx::SwigluGradArgs a{};
+  a.dy = dy;
+  a.g = gate;
+  a.u = up;
+  a.dg = dgate;
+  a.du = dup;
+  a.rows = rows;
+  a.cols = cols;
+  a.ld_dy = ld_dy;
+  a.ld_g = ld_gate;
+  a.ld_u = ld_up;
+  a.ld_dg = ld_dgate;
+  a.ld_du = ld_dup;
+  a.dg_bytes = extent(rows, cols, ld_dgate, dtype);
+  a.du_bytes = extent(rows, cols, ld_dup, dtype);
+  return from_cuda(mx::launch_swiglu_grad(a, dtype == MXFP4_DTYPE_F32, dy_dtype == MXFP4_DTYPE_F32,
+                                          static_cast<cudaStream_t>(stream)),
+                   fn);
+}
+
+mxfp4_status mxfp4_gemv(const void* x, int32_t x_kind, int64_t ld_x, const uint8_t* sx, const uint8_t* qw,
+                        const uint8_t* sw, int32_t block, int32_t scale_layout, int32_t tensor_exp, int64_t M,
+                        int64_t N, int64_t K, void* y, int32_t y_dtype, int64_t ld_y, void* stream) {
+  const char* fn = "mxfp4_gemv";
+  if (x_kind != MXFP4_GEMV_X_BF16 && x_kind != MXFP4_GEMV_X_E4M3 && x_kind != MXFP4_GEMV_X_E5M2)
+    return fail(MXFP4_ERR_INVALID_ARG, "%s: bad x_kind %d", fn, x_kind);
+  if (y_dtype != MXFP4_DTYPE_BF16 && y_dtype != MXFP4_DTYPE_F32)
+    return fail(MXFP4_ERR_INVALID_ARG, "%s: bad y_dtype %d", fn, y_dtype);
+  if (block != MXFP4_BLOCK_1X32 && block != MXFP4_BLOCK_32X32 && block != MXFP4_BLOCK_64X64 &&
+      block != MXFP4_BLOCK_1X16)
+    return fail(MXFP4_ERR_INVALID_ARG, "%s: bad block %d", fn, block);
+  if (scale_layout != MXFP4_LAYOUT_ROWMAJOR && scale_layout != MXFP4_LAYOUT_MMA)
+    return fail(MXFP4_ERR_INVALID_ARG, "%s: bad scale_layout %d", fn, scale_layout);
+  const bool nv = block == MXFP4_BLOCK_1X16;
+  if (nv ? (tensor_exp < -100 || tensor_exp > 100) : tensor_exp != 0)
+    return fail(MXFP4_ERR_INVALID_ARG, "%s: bad tensor_exp %d", fn, tensor_exp);
+  if (M < 0 || N < 0 || K < 0 || K % 32 != 0)
+    return fail(MXFP4_ERR_SHAPE, "%s: M, N >= 0 and K a non-negative multiple of 32 (got %lld, %lld, %lld)", fn,
+                (long long)M, (long long)N, (long long)K);
+  if (M > 65536 || N > (1ll << 30) || K > (1ll << 30) || too_large(N, K))
+    return fail(MXFP4_ERR_SHAPE, "%s: dimensions too large (M up to 65536, N and K up to 2^30, N K up to 2^40)", fn);
+  if (scale_layout == MXFP4_LAYOUT_MMA && (N % 128 != 0 || K % 128 != 0))
+    return fail(MXFP4_ERR_SHAPE, "%s: tensor-core scale layout needs N %% 128 == 0 and K %% 128 == 0", fn);
+  const bool codes = x_kind != MXFP4_GEMV_X_BF16;
+  if (ld_x < K || ld_y < N || ld_x > kMaxElems || ld_y > kMaxElems || (M > 1 && (too_large(M, ld_x) || too_large(M, ld_y))))
+    return fail(MXFP4_ERR_SHAPE, "%s: ld_x (%lld) < K or ld_y (%lld) < N, or too large", fn, (long long)ld_x,
+                (long long)ld_y);
+  if (M * N > 0) {
+    if (!y) return fail(MXFP4_ERR_INVALID_ARG, "%s: y is NULL", fn);
+    if (K > 0 && (!x || !qw || !sw || (codes && !sx)))
+      return fail(MXFP4_ERR_INVALID_ARG, "%s: x, qw, sw (and sx with one-byte x) must be non-NULL", fn);
+  }
+  if (!aligned16(x) || !aligned16(qw) || !aligned16(sw) || ld_x % (codes ? 16 : 8) != 0)
+    return fail(MXFP4_ERR_ALIGN, "%s: x, qw and sw must be 16-byte aligned, rows of x multiples of 16 bytes", fn);
+  if (reinterpret_cast<uintptr_t>(y) % elem_bytes(y_dtype))
+    return fail(MXFP4_ERR_ALIGN, "%s: y must be aligned to its element", fn);
+  mx::GemvArgs a{};
+  a.x = x;
+  a.sx = sx;
+  a.qw = qw;
+  a.sw = sw;
+  a.y = y;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.ld_x = ld_x;
+  a.ld_y = ld_y;
+  a.y_bytes = extent(M, N, ld_y, y_dtype);
+  a.p2k = nv ? ldexpf(1.0f, tensor_exp) : 1.0f;
+  a.x_kind = x_kind;
+  a.nv = nv;
+  a.mma = scale_layout == MXFP4_LAYOUT_MMA;
+  a.y_f32 = y_dtype == MXFP4_DTYPE_F32;
+  return from_cuda(mx::launch_gemv(a, static_cast<cudaStream_t>(stream)), fn);
 }
 
 mxfp4_status mxfp4_device_status(void* stream) {

@@ -1256,9 +1256,12 @@ cudaError_t read_device_error(cudaStream_t st, uint32_t* err) {
     e = cudaMemcpyToSymbol(g_gemm_error, &zero, sizeof(uint32_t));
     if (e != cudaSuccess) return e;
   }
-  uint32_t qerr = 0;
-  e = read_quant_error(&qerr);
-  if (!*err) *err = qerr;
+  for (auto read : {read_quant_error, read_ffn_error, read_gemv_error}) {
+    uint32_t other = 0;
+    e = read(&other);
+    if (e != cudaSuccess) return e;
+    if (!*err) *err = other;
+  }
   return e;
 }
 

@@ -37,6 +37,69 @@ struct OrientArgs {
 // Device error word value of a store outside its output (bounds-checking builds).
 constexpr uint32_t kErrBounds = 7;
 
+// A row-wise quantized output of the norm and activation kernels: 1x32 blocks
+// with an E8M0 scale, or 1x16 blocks with an E4M3 scale (NVFP4), nearest-even.
+struct RowQuant {
+  enum : int32_t { kNone = 0, kE2m1, kE4m3, kE5m2, kNvfp4 };
+  int32_t fmt;
+  int32_t roundup;
+  int32_t mma;        // scale layout: 0 row-major, 1 tensor-core tiles
+  float p2k, zmul;    // NVFP4: 2^tensor_exp and 2^-tensor_exp / 6
+  uint8_t *q, *s;
+  uint64_t q_bytes, s_bytes;  // extents
+};
+
+// Leading dimensions in elements; *_bytes: extent of an output from its pointer.
+struct NormArgs {
+  const void *x, *r, *w;  // r, w: may be NULL
+  void *h, *y;            // each may be NULL; h has x's type
+  float* rstd;            // may be NULL
+  int64_t rows, cols, ld_x, ld_r, ld_h, ld_y;
+  uint64_t h_bytes, y_bytes;
+  float eps;
+  bool y_f32;
+  RowQuant quant;
+};
+
+struct NormGradArgs {
+  const void *dy, *h, *w, *dh;  // w, dh: may be NULL
+  const float* rstd;
+  void *dx, *dw;                // dw: may be NULL
+  float* ws;                    // norm_dw_slices(rows) x cols partial sums (with dw)
+  int64_t rows, cols, ld_dy, ld_h, ld_dh, ld_dx;
+  uint64_t dx_bytes, ws_bytes;
+};
+
+struct SwigluArgs {
+  const void *g, *u;
+  void* y;  // may be NULL
+  int64_t rows, cols, ld_g, ld_u, ld_y;
+  uint64_t y_bytes;
+  bool y_f32;
+  RowQuant quant;
+};
+
+struct SwigluGradArgs {
+  const void *dy, *g, *u;
+  void *dg, *du;
+  int64_t rows, cols, ld_dy, ld_g, ld_u, ld_dg, ld_du;
+  uint64_t dg_bytes, du_bytes;
+};
+
+// Few-row product with 4-bit weights.
+struct GemvArgs {
+  enum : int32_t { kXBf16 = 0, kXE4m3, kXE5m2 };
+  const void* x;      // bf16 [M, ld_x], or one-byte codes [M, ld_x]
+  const uint8_t* sx;  // E8M0 [M, K/32] (codes)
+  const uint8_t *qw, *sw;
+  void* y;
+  int64_t M, N, K, ld_x, ld_y;
+  uint64_t y_bytes;
+  float p2k;          // NVFP4: 2^tensor_exp
+  int32_t x_kind;
+  bool nv, mma, y_f32;
+};
+
 // Fills keys, sm_*, xw and sgn from seed and sign_mask.
 void prepare_orient(OrientArgs* o);
 
@@ -70,8 +133,16 @@ cudaError_t launch_gemm(const uint8_t* qa, const uint8_t* sa, const uint8_t* qb,
                         const uint8_t* sb, int64_t M, int64_t N, int64_t K, void* c,
                         bool c_bf16, int64_t ldc, const OrientArgs* qout, const OrientArgs* qcol,
                         void* ws, size_t ws_bytes, cudaStream_t st, const char** why);
-// Reads and clears the quantizer's device error word.
+cudaError_t launch_rmsnorm(const NormArgs& a, bool x_f32, bool w_f32, cudaStream_t st);
+int norm_dw_slices(int64_t rows);
+cudaError_t launch_rmsnorm_grad(const NormGradArgs& a, bool h_f32, bool dy_f32, bool w_f32, cudaStream_t st);
+cudaError_t launch_swiglu(const SwigluArgs& a, bool f32, cudaStream_t st);
+cudaError_t launch_swiglu_grad(const SwigluGradArgs& a, bool f32, bool dy_f32, cudaStream_t st);
+cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t st);
+// Each reads and clears the device error word of its translation unit.
 cudaError_t read_quant_error(uint32_t* err);
+cudaError_t read_ffn_error(uint32_t* err);
+cudaError_t read_gemv_error(uint32_t* err);
 // Reads and clears the device error words (synchronizes st).
 cudaError_t read_device_error(cudaStream_t st, uint32_t* err);
 // MXFP8 GEMM (E4M3, or E5M2 with e5m2, codes [M, K], [N, K] bytes, both

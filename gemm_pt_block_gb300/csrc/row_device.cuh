@@ -1,0 +1,160 @@
+// row_device.cuh -- eight-element vectors and row-wise quantization of values
+// held eight to a lane (the norm and activation kernels, sm_103a).
+#pragma once
+#include <cstdint>
+
+#include "internal.h"
+#include "mx_device.cuh"
+
+#ifndef MX_BOUNDS_FAIL
+#error "define MX_BOUNDS_FAIL() before including row_device.cuh"
+#endif
+
+namespace mx {
+
+// Eight consecutive elements as they lie in memory: bf16 (uint16_t) 16 bytes,
+// fp32 32 bytes.
+template <typename T>
+struct Vec8;
+template <>
+struct Vec8<uint16_t> {
+  uint4 a;
+};
+template <>
+struct Vec8<float> {
+  uint4 a, b;
+};
+
+// Loads of data that the kernel reads once. Not the read-only path: an output
+// may lie in place of an input.
+__device__ __forceinline__ uint4 load16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void load8(const uint16_t* p, Vec8<uint16_t>& v) { v.a = load16(p); }
+__device__ __forceinline__ void load8(const float* p, Vec8<float>& v) {
+  v.a = load16(p);
+  v.b = load16(p + 4);
+}
+// Loads of data that other rows read again (weights).
+__device__ __forceinline__ void load8_cached(const uint16_t* p, Vec8<uint16_t>& v) {
+  v.a = __ldg(reinterpret_cast<const uint4*>(p));
+}
+__device__ __forceinline__ void load8_cached(const float* p, Vec8<float>& v) {
+  v.a = __ldg(reinterpret_cast<const uint4*>(p));
+  v.b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+}
+
+__device__ __forceinline__ void unpack8(const Vec8<uint16_t>& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.a.x, v.a.y, v.a.z, v.a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void unpack8(const Vec8<float>& v, float (&f)[8]) {
+  const uint32_t w[8] = {v.a.x, v.a.y, v.a.z, v.a.w, v.b.x, v.b.y, v.b.z, v.b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+}
+
+// Two fp32 values to a bf16 pair, nearest-even (a in the low half).
+__device__ __forceinline__ uint32_t bf16x2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ void pack8(const float (&f)[8], Vec8<uint16_t>& v) {
+  v.a = make_uint4(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]), bf16x2(f[6], f[7]));
+}
+__device__ __forceinline__ void pack8(const float (&f)[8], Vec8<float>& v) {
+  v.a = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  v.b = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
+}
+
+// Stores v at p; bounds-checking builds skip and report a store outside the
+// `bytes` bytes at base.
+template <typename V>
+__device__ __forceinline__ void put_at(void* p, const V& v, const void* base, uint64_t bytes) {
+#ifdef MXFP4_BOUNDS_CHECK
+  const uint8_t *b = static_cast<const uint8_t*>(base), *a = static_cast<const uint8_t*>(p);
+  if (a < b || a + sizeof(V) > b + bytes) {
+    MX_BOUNDS_FAIL();
+    return;
+  }
+#else
+  (void)base;
+  (void)bytes;
+#endif
+  *static_cast<V*>(p) = v;
+}
+__device__ __forceinline__ void store8(uint16_t* p, const Vec8<uint16_t>& v, const void* base, uint64_t bytes) {
+  put_at(p, v.a, base, bytes);
+}
+__device__ __forceinline__ void store8(float* p, const Vec8<float>& v, const void* base, uint64_t bytes) {
+  put_at(p, v.a, base, bytes);
+  put_at(p + 4, v.b, base, bytes);
+}
+// Eight fp32 values to a matrix of bf16 or fp32 elements.
+__device__ __forceinline__ void store8_as(void* base, bool f32, int64_t at, const float (&f)[8], uint64_t bytes) {
+  if (f32) {
+    Vec8<float> v;
+    pack8(f, v);
+    store8(static_cast<float*>(base) + at, v, base, bytes);
+  } else {
+    Vec8<uint16_t> v;
+    pack8(f, v);
+    store8(static_cast<uint16_t*>(base) + at, v, base, bytes);
+  }
+}
+
+// Quantizes the eight values f that this lane holds of output row `row`,
+// columns col .. col + 7, and stores codes and scales. Lanes 4 i .. 4 i + 3 of
+// the warp hold one 32-run (columns of a multiple of 32 first), so a block's
+// max-abs is two exchanges away (one for 1x16 blocks). Every lane of the warp
+// calls this; one with `live` false holds nothing and stores nothing. The
+// maximum is taken over the bit patterns of |f|, which orders infinity and NaN
+// above every finite value: a block that holds either gets the scale format's
+// NaN as its scale and zero codes, and so dequantizes to NaN.
+__device__ __forceinline__ void quantize8(const RowQuant& o, float (&f)[8], bool live, int64_t row,
+                                          int64_t col, int64_t cols) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  const bool nv = o.fmt == RowQuant::kNvfp4;
+  if (!nv) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const bool bad = m >= 0x7F800000u;
+  const float M = bad ? 0.0f : __uint_as_float(m);
+  uint32_t code;
+  float mul;
+  if (nv) {
+    const NvScale s = nv_scale(M, o.roundup, o.p2k, o.zmul);
+    code = bad ? 0x7Fu : s.code;
+    mul = s.rcp;
+  } else {
+    const int e = scale_exponent(M, o.roundup, o.fmt != RowQuant::kE2m1, o.fmt == RowQuant::kE5m2);
+    code = bad ? 0xFFu : (uint32_t)(e + 127);
+    mul = inv_scale(e);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = bad ? 0.0f : __fmul_rn(f[i], mul);
+  if (!live) return;
+  if (o.fmt == RowQuant::kE4m3 || o.fmt == RowQuant::kE5m2) {
+    const bool e5 = o.fmt == RowQuant::kE5m2;
+    const uint2 c = e5 ? make_uint2(e5m2x4(f[0], f[1], f[2], f[3]), e5m2x4(f[4], f[5], f[6], f[7]))
+                       : make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
+    put_at(o.q + row * cols + col, c, o.q, o.q_bytes);
+  } else {
+    put_at(o.q + ((row * cols + col) >> 1), e2m1x8(f[0], f[1], f[2], f[3], f[4], f[5], f[6], f[7]), o.q,
+           o.q_bytes);
+  }
+  const int64_t kb = nv ? col >> 4 : col >> 5, nkb = nv ? cols >> 4 : cols >> 5;
+  if ((col & (nv ? 15 : 31)) == 0)
+    put_at(o.s + (o.mma ? mma_scale_offset(row, kb, nkb) : row * nkb + kb), (uint8_t)code, o.s, o.s_bytes);
+}
+
+}  // namespace mx

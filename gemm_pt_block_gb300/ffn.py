@@ -1,0 +1,142 @@
+"""Feed-forward block on the library's kernels, for training and for decoding.
+
+    h = x + residual;  n = rmsnorm(h);  (g, u) = n W_gate_up^T;
+    a = g / (1 + exp(-g)) * u;  y = a W_down^T
+
+The block returns (y, h): y joins the residual stream h in the next block's
+norm (y as its x, h as its residual), so that no addition runs by itself.
+
+Training (`forward`): both products through the MXFP4 linear layer, the norm
+and the activation through their fused kernels, gradients for everything.
+
+Decoding (`decode`): a few rows of x against weights quantized once
+(`quantize_weights`). The norm and the activation write MXFP8 (E4M3) codes
+with their scales, which the few-row product reads as they are; the weights
+stay in the codes and tensor-core scale layout of the training products.
+"""
+from __future__ import annotations
+
+import torch
+
+from .binding import (BLOCK_1X32, FORMAT_E4M3, LAYOUT_ROWMAJOR, ROUND_RTN, SCALE_ROUNDUP, QuantParams,
+                      mxfp4_gemv, mxfp4_quantize, mxfp4_rmsnorm_backward, mxfp4_rmsnorm_quantize,
+                      mxfp4_swiglu_backward, mxfp4_swiglu_quantize)
+from .linear import LinearRecipe, Mxfp4Linear
+
+
+def _readable(t: torch.Tensor) -> torch.Tensor:
+    """t, or a copy of it that the kernels can read (unit column stride, rows
+    on 16-byte boundaries): autograd may hand over expanded gradients."""
+    ok = t.stride(-1) == 1 and t.stride(0) >= t.shape[1] and t.stride(0) % 8 == 0 and t.data_ptr() % 16 == 0
+    return t if ok else t.contiguous()
+
+
+class _RmsNormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, weight, eps, out_dtype):
+        ctx.set_materialize_grads(False)
+        x = _readable(x)
+        _, _, y, h, rstd = mxfp4_rmsnorm_quantize(
+            x, weight, residual=None if residual is None else _readable(residual), eps=eps, y_dtype=out_dtype,
+            with_rstd=True)
+        ctx.save_for_backward(x if h is None else h, weight, rstd)
+        return y if h is None else (y, h)
+
+    @staticmethod
+    def backward(ctx, dy, dh=None):
+        h, weight, rstd = ctx.saved_tensors
+        need_x, need_r, need_w = ctx.needs_input_grad[:3]
+        if dy is None:                                   # y unused: only the stream's gradient passes
+            return dh if need_x else None, dh if need_r else None, None, None, None
+        dx, dw = mxfp4_rmsnorm_backward(_readable(dy), h, weight, rstd, dh=None if dh is None else _readable(dh),
+                                        with_dw=need_w)
+        return dx if need_x else None, dx if need_r else None, dw, None, None
+
+
+def rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+            eps: float = 1e-6, out_dtype: torch.dtype = torch.bfloat16):
+    """Differentiable root-mean-square norm over the last dimension (a multiple
+    of 32): y in out_dtype, or (y, h) with h = x + residual when a residual is
+    given. x and residual share one type (bf16 or fp32)."""
+    lead, D = x.shape[:-1], x.shape[-1]
+    r = None if residual is None else residual.reshape(-1, D)
+    out = _RmsNormFn.apply(x.reshape(-1, D), r, weight, eps, out_dtype)
+    if residual is None:
+        return out.reshape(*lead, D)
+    return out[0].reshape(*lead, D), out[1].reshape(*lead, D)
+
+
+class _SwigluFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, gate, up, out_dtype):
+        gate, up = _readable(gate), _readable(up)
+        ctx.save_for_backward(gate, up)
+        return mxfp4_swiglu_quantize(gate, up, y_dtype=out_dtype)[2]
+
+    @staticmethod
+    def backward(ctx, dy):
+        gate, up = ctx.saved_tensors
+        rows, cols = gate.shape
+        # one buffer for both halves: the gradient of the product that wrote them side by side
+        both = torch.empty((rows, 2 * cols), dtype=gate.dtype, device=gate.device)
+        dgate, dup = mxfp4_swiglu_backward(_readable(dy), gate, up, dgate=both[:, :cols], dup=both[:, cols:])
+        return dgate, dup, None
+
+
+def swiglu(gate: torch.Tensor, up: torch.Tensor, out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """Differentiable gate / (1 + exp(-gate)) * up in out_dtype; the last
+    dimension is a multiple of 32, gate and up share one type (bf16 or fp32)."""
+    lead, F = gate.shape[:-1], gate.shape[-1]
+    return _SwigluFn.apply(gate.reshape(-1, F), up.reshape(-1, F), out_dtype).reshape(*lead, F)
+
+
+class Mxfp4FeedForward(torch.nn.Module):
+    """Pre-norm feed-forward block (see the module's text). dim and hidden are
+    multiples of 128; training rows too, decoding rows are free."""
+
+    def __init__(self, dim: int, hidden: int, recipe: LinearRecipe | None = None, eps: float = 1e-6,
+                 device=None, dtype: torch.dtype = torch.bfloat16):
+        super().__init__()
+        if dim % 128 or hidden % 128:
+            raise ValueError(f"dim and hidden must be multiples of 128 (got {dim}, {hidden})")
+        self.dim, self.hidden, self.eps = dim, hidden, eps
+        self.norm = torch.nn.Parameter(torch.ones(dim, device=device, dtype=dtype))
+        self.gate_up = Mxfp4Linear(dim, 2 * hidden, recipe, device=device, dtype=dtype, out_dtype=torch.bfloat16)
+        self.down = Mxfp4Linear(hidden, dim, recipe, device=device, dtype=dtype, out_dtype=torch.bfloat16)
+        self._decode = None
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None):
+        """(y, h) for bf16 x (and residual) [..., dim] with a multiple of 128 rows."""
+        if residual is None:
+            n, h = rmsnorm(x, self.norm, None, self.eps), x
+        else:
+            n, h = rmsnorm(x, self.norm, residual, self.eps)
+        gu = self.gate_up(n)
+        return self.down(swiglu(gu[..., :self.hidden], gu[..., self.hidden:])), h
+
+    @torch.no_grad()
+    def quantize_weights(self) -> None:
+        """Quantizes the weights for `decode`, once; call it again after they change."""
+        self._decode = []
+        for layer in (self.gate_up, self.down):
+            p = layer.recipe.w_row
+            if p.wht:
+                raise ValueError("decoding needs weights quantized without rotation along their rows")
+            q, s, _, _ = mxfp4_quantize(layer.weight.detach(), p)
+            self._decode.append((q, s, p))
+
+    @torch.no_grad()
+    def decode(self, x: torch.Tensor, residual: torch.Tensor | None = None):
+        """(y, h) for a few rows of bf16 x (and residual) [..., dim], without gradients."""
+        if self._decode is None:
+            raise RuntimeError("quantize_weights() has not been called")
+        lead = x.shape[:-1]
+        x2 = _readable(x.reshape(-1, self.dim))
+        r2 = None if residual is None else _readable(residual.reshape(-1, self.dim))
+        p8 = QuantParams(BLOCK_1X32, SCALE_ROUNDUP, ROUND_RTN, LAYOUT_ROWMAJOR, elem_format=FORMAT_E4M3)
+        q, s, _, h, _ = mxfp4_rmsnorm_quantize(x2, self.norm, p8, residual=r2, eps=self.eps)
+        (qg, sg, pg), (qd, sd, pd) = self._decode
+        gu = mxfp4_gemv(q, qg, sg, 2 * self.hidden, self.dim, pg, sx=s)
+        qa, sa, _ = mxfp4_swiglu_quantize(gu[:, :self.hidden], gu[:, self.hidden:], p8)
+        y = mxfp4_gemv(qa, qd, sd, self.dim, self.hidden, pd, sx=sa)
+        return y.reshape(*lead, self.dim), (x if h is None else h.reshape(*lead, self.dim))

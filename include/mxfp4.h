@@ -362,6 +362,105 @@ mxfp4_status hadamard32(const void* x, int32_t x_dtype, int64_t rows, int64_t co
 mxfp4_status mxfp4_tensor_amax(const void* x, int32_t x_dtype, int64_t rows, int64_t cols,
                                int64_t ld_x, float* amax, int32_t* tensor_exp, void* stream);
 
+/* ---- The operators around a feed-forward block's products ----------------
+ * (the pages have no counterpart: what a user of the products needs on either
+ * side of them). Common rules: matrices are row-major bf16 or fp32, 16-byte
+ * aligned, with a leading dimension that is a multiple of 8 elements and at
+ * least cols, at most 2^40 elements; cols is a multiple of 32 below 2^31; rows
+ * may be any number, 0 included. Sums and every step before the last rounding
+ * are fp32. Results have the same bits on every call. The calls only enqueue
+ * kernels, allocate nothing and can be captured into a CUDA graph. Outputs
+ * must not overlap inputs or each other except where said.
+ *
+ * A quantized output (row, q, s) is what mxfp4_quantize would write for the
+ * fp32 values before their rounding to any other type: E2M1, E4M3 or E5M2 in
+ * 1x32 blocks or NVFP4's 1x16 blocks, either scale mode and layout (the
+ * tensor-core layout needs rows and cols multiples of 128), nearest-even, no
+ * rotation; other params return MXFP4_ERR_UNSUPPORTED. A block that holds an
+ * infinity or a NaN gets the scale format's NaN (E8M0 0xFF, E4M3 0x7F) as its
+ * scale and zero codes: it dequantizes to NaN. */
+
+/* Residual addition, root-mean-square norm and quantization in one pass:
+ *   h = x + residual, rounded to x_dtype (h = x without residual);
+ *   rstd[r] = 1 / sqrt(sum_c h[r, c]^2 / cols + eps);
+ *   y[r, c] = h[r, c] * weight[c] * rstd[r].
+ *  x, residual (NULL: none), h [rows, cols] in x_dtype; weight [cols] in
+ *  weight_dtype (NULL: ones); y [rows, cols] in y_dtype. h, y, rstd [rows] and
+ *  the quantized y (row, q, s) are outputs, each NULL when not wanted, one at
+ *  least not NULL. h may be x or residual themselves (same pointer and leading
+ *  dimension): the residual stream is then updated in place. The sum of
+ *  squares must stay below fp32's largest value. */
+mxfp4_status mxfp4_rmsnorm_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t cols,
+                                    int64_t ld_x, const void* residual, int64_t ld_residual,
+                                    const void* weight, int32_t weight_dtype, float eps, void* h,
+                                    int64_t ld_h, void* y, int32_t y_dtype, int64_t ld_y,
+                                    float* rstd, const mxfp4_quant_params* row, uint8_t* q,
+                                    uint8_t* s, void* stream);
+
+/* Its gradients. With n = h * rstd and dn = dy * weight:
+ *   dx[r, c] = (dn - n * (sum_c dn n) / cols) * rstd[r] + dh[r, c],
+ *   dw[c] = sum_r dy[r, c] n[r, c].
+ *  dy [rows, cols] in dy_dtype is the gradient of y (quantization passes it
+ *  through unchanged), dh (NULL: none) in h_dtype the gradient that reaches h
+ *  through the residual stream, h and rstd what the forward call left. dx in
+ *  h_dtype is the gradient of x and of residual alike and may be dh itself
+ *  (same pointer and leading dimension). dw [cols] in weight_dtype (NULL: not
+ *  wanted) takes the partial sums in workspace, device memory of
+ *  mxfp4_rmsnorm_backward_workspace_size(rows, cols) bytes, 16-byte aligned. */
+mxfp4_status mxfp4_rmsnorm_backward(const void* dy, int32_t dy_dtype, int64_t ld_dy, const void* h,
+                                    int32_t h_dtype, int64_t ld_h, const void* weight,
+                                    int32_t weight_dtype, const float* rstd, const void* dh,
+                                    int64_t ld_dh, int64_t rows, int64_t cols, void* dx,
+                                    int64_t ld_dx, void* dw, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/* Bytes of mxfp4_rmsnorm_backward's workspace (0 for non-positive sizes). */
+size_t mxfp4_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols);
+
+/* Gated activation and quantization in one pass:
+ *   y[r, c] = gate / (1 + exp(-gate)) * up.
+ *  gate, up [rows, cols] in dtype, each with its own leading dimension (the
+ *  two halves of one product's output, for instance); y (NULL: not wanted) in
+ *  y_dtype; the quantized y as above (row NULL: not wanted). */
+mxfp4_status mxfp4_swiglu_quantize(const void* gate, int64_t ld_gate, const void* up, int64_t ld_up,
+                                   int32_t dtype, int64_t rows, int64_t cols, void* y,
+                                   int32_t y_dtype, int64_t ld_y, const mxfp4_quant_params* row,
+                                   uint8_t* q, uint8_t* s, void* stream);
+
+/* Its gradients, with t = 1 / (1 + exp(-gate)):
+ *   dgate = dy * up * t * (1 + gate * (1 - t)),   dup = dy * gate * t.
+ *  dy in dy_dtype; gate, up, dgate, dup in dtype. dgate may be gate itself and
+ *  dup up itself (same pointer and leading dimension). */
+mxfp4_status mxfp4_swiglu_backward(const void* dy, int32_t dy_dtype, int64_t ld_dy,
+                                   const void* gate, int64_t ld_gate, const void* up, int64_t ld_up,
+                                   int32_t dtype, int64_t rows, int64_t cols, void* dgate,
+                                   int64_t ld_dgate, void* dup, int64_t ld_dup, void* stream);
+
+/* Activations of mxfp4_gemv: bf16, or MXFP8 codes of either format. */
+enum { MXFP4_GEMV_X_BF16 = 0, MXFP4_GEMV_X_E4M3 = 1, MXFP4_GEMV_X_E5M2 = 2 };
+
+/* Product of a few activation rows with a 4-bit weight matrix (decoding, where
+ * the block-scaled GEMM's 128-row tiles would be empty):
+ *   y[m, n] = sum_k x[m, k] W[n, k]
+ *  W   E2M1 codes qw [N, K/2] with scales sw as mxfp4_quantize writes them:
+ *      block 1x32, 32x32 or 64x64 (E8M0, [N, K/32]) or 1x16 (NVFP4: E4M3,
+ *      [N, K/16], under 2^tensor_exp), in either scale layout (the tensor-core
+ *      layout needs N and K multiples of 128): the weights of mxfp4_gemm and
+ *      nvfp4_gemm serve as they are.
+ *  x   [M, K] with leading dimension ld_x: bf16 (x_kind MXFP4_GEMV_X_BF16, sx
+ *      ignored), or one-byte E4M3 / E5M2 codes with row-major E8M0 scales
+ *      sx [M, K/32] (the quantized outputs above).
+ *  y   [M, N] in y_dtype, leading dimension ld_y >= N (any), aligned to its
+ *      element.
+ * Products are exact and summed in fp32 (in a fixed order) whatever x holds; a
+ * NaN scale makes what it enters NaN. M may be 0 .. 65536 (the weights are
+ * read again for every 32 rows of x), N any, K a multiple of 32, rows of x
+ * multiples of 16 bytes; x, qw, sw 16-byte aligned. */
+mxfp4_status mxfp4_gemv(const void* x, int32_t x_kind, int64_t ld_x, const uint8_t* sx,
+                        const uint8_t* qw, const uint8_t* sw, int32_t block, int32_t scale_layout,
+                        int32_t tensor_exp, int64_t M, int64_t N, int64_t K, void* y,
+                        int32_t y_dtype, int64_t ld_y, void* stream);
+
 /* Human-readable name of a status code (static string). */
 const char* mxfp4_status_string(mxfp4_status s);
 
