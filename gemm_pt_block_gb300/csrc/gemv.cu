@@ -45,32 +45,31 @@ __device__ uint32_t g_gemv_error;
 namespace mx {
 namespace {
 
-constexpr int kRows = 128;                 // rows of W per CTA
+constexpr int kRows = 128;                 // most rows of W per CTA
 constexpr int kStageK = 256;               // K per stage
+constexpr int kBlocks = kStageK / 32;
 constexpr int kRowBytes = kStageK / 2;     // code bytes per row and stage
-constexpr int kMmaWarps = 8;               // 4 groups of 32 rows x 2 halves of a stage
+constexpr int kParts = 2;                  // parts of a stage's blocks, each a warp's
+constexpr int kMmaWarps = 8;               // (up to four) groups of 32 rows x kParts
 constexpr int kConvWarps = 4;
 constexpr int kThreads = (kMmaWarps + 1 + kConvWarps) * 32;
 constexpr int kWBytes = kRows * kRowBytes;
 constexpr int kMaxTokens = 32;
-#ifndef GEMV_WANT
-#define GEMV_WANT 456
-#define GEMV_MAX_SPLITS 8
-#endif
+constexpr int kSms = 152;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 // Shared memory of one CTA for tiles of TT rows of x.
 template <int TT, bool NV>
 struct Smem {
   static constexpr int kX = TT * kStageK * 2;            // f16 [block][token][32]
-  static constexpr int kSw = kRows * kStageK / (NV ? 16 : 32);
+  static constexpr int kSw = 2 * kRows * kStageK / (NV ? 16 : 32);  // two 128-row tiles of scales
   static constexpr int kSx = TT * (kStageK / 32) * 4;    // float [block][token]
   static constexpr int kStage = kWBytes + kX + kSw + kSx;
-  static constexpr int kStages = TT == 32 ? 6 : TT == 16 ? 4 : 5;
+  static constexpr int kStages = TT == 32 ? 5 : TT == 16 ? 4 : NV ? 4 : 5;
   static constexpr int kCtl = 256;
   static constexpr int kBytes = kStages * kStage + kCtl + 1024;
-  static constexpr int kRed = 132 * TT * 4;              // partial sums, in place of the first W stages
-  static_assert(kRed <= kWBytes * 2, "partial sums fit the ring");
+  // partial sums [part][token][rows + 4] in place of the W stages
+  static_assert(kParts * (kRows + 4) * TT * 4 <= kStages * kWBytes, "partial sums fit the ring");
 };
 
 struct Ctl {
@@ -131,37 +130,15 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t r;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(a));
-  return r;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 r;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
-  return r;
-}
-__device__ __forceinline__ float2 lds64f(uint32_t a) {
-  float2 r;
-  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(r.x), "=f"(r.y) : "r"(a));
-  return r;
-}
-__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-               : "memory");
-}
-__device__ __forceinline__ void stsf(uint32_t a, float v) {
-  asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
-}
 __device__ __forceinline__ float lds_cluster(uint32_t a) {
   float r;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(r) : "r"(a));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(r) : "r"(a) : "memory");
   return r;
 }
 
@@ -169,11 +146,12 @@ __device__ __forceinline__ float lds_cluster(uint32_t a) {
 // elements 8 t .. 8 t + 7 of block b, a row at a time.
 template <int TT>
 __device__ __forceinline__ void convert_x(const GemvArgs& a, int64_t m0, int tokens, int64_t k0, int lane,
-                                          uint32_t xs, uint32_t sxs) {
+                                          uint8_t* xs, float* sxs) {
   const int b = lane >> 2, t = lane & 3;
   const int64_t k = k0 + b * 32 + t * 8;
   const bool live = k < a.K;
-  const uint32_t dst = xs + b * (TT * 64) + t * 16, sdst = sxs + b * (TT * 4);
+  uint8_t* dst = xs + b * (TT * 64) + t * 16;
+  float* sdst = sxs + b * TT;
   if (a.x_kind == GemvArgs::kXBf16) {
     const uint16_t* p = static_cast<const uint16_t*>(a.x) + m0 * a.ld_x + k;
 #pragma unroll 1
@@ -200,8 +178,8 @@ __device__ __forceinline__ void convert_x(const GemvArgs& a, int64_t m0, int tok
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           h[j] = f16x2(__fmul_rn(__uint_as_float(w[j] << 16), f), __fmul_rn(__uint_as_float(w[j] & 0xFFFF0000u), f));
-        sts128(dst + (m + i) * 64, make_uint4(h[0], h[1], h[2], h[3]));
-        if (t == 0) stsf(sdst + (m + i) * 4, E == 14u ? __uint_as_float(0x00400000u) : __uint_as_float((E - 14u) << 23));
+        *reinterpret_cast<uint4*>(dst + (m + i) * 64) = make_uint4(h[0], h[1], h[2], h[3]);
+        if (t == 0) sdst[m + i] = E == 14u ? __uint_as_float(0x00400000u) : __uint_as_float((E - 14u) << 23);
       }
     }
   } else {
@@ -225,8 +203,8 @@ __device__ __forceinline__ void convert_x(const GemvArgs& a, int64_t m0, int tok
                                         e5m2x2_f16x2(v[i].y >> 16))
                            : make_uint4(e4m3x2_f16x2(v[i].x), e4m3x2_f16x2(v[i].x >> 16), e4m3x2_f16x2(v[i].y),
                                         e4m3x2_f16x2(v[i].y >> 16));
-        sts128(dst + (m + i) * 64, h);
-        if (t == 0) stsf(sdst + (m + i) * 4, __uint_as_float(e8m0x2_bf16x2(s[i]) << 16));
+        *reinterpret_cast<uint4*>(dst + (m + i) * 64) = h;
+        if (t == 0) sdst[m + i] = __uint_as_float(e8m0x2_bf16x2(s[i]) << 16);
       }
     }
   }
@@ -236,12 +214,14 @@ __device__ __forceinline__ void convert_x(const GemvArgs& a, int64_t m0, int tok
 // (128 rows x 4 columns, 512 bytes) that the multiplying warps read: lane l
 // brings rows l, l + 32, l + 64, l + 96. Rows past N repeat the last one.
 template <bool NV>
-__device__ __forceinline__ void convert_sw(const GemvArgs& a, int64_t n0, int64_t k0, int lane, uint32_t sws) {
+__device__ __forceinline__ void convert_sw(const GemvArgs& a, int groups, int64_t n0, int64_t k0, int lane,
+                                           uint8_t* sws) {
   constexpr int kCols = kStageK / (NV ? 16 : 32);
   const int64_t cols = a.K / (NV ? 16 : 32), c0 = k0 / (NV ? 16 : 32);
-  uint32_t v[kCols / 4][4];
+  uint32_t v[kCols / 4][4] = {};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
+    if (j >= groups) break;
     const uint8_t* p = a.sw + min(n0 + lane + 32 * j, a.N - 1) * cols + c0;
     if ((cols & 3) == 0) {
 #pragma unroll
@@ -258,73 +238,81 @@ __device__ __forceinline__ void convert_sw(const GemvArgs& a, int64_t n0, int64_
     }
   }
 #pragma unroll
-  for (int c = 0; c < kCols / 4; ++c) sts128(sws + c * 512 + lane * 16, make_uint4(v[c][0], v[c][1], v[c][2], v[c][3]));
+  for (int c = 0; c < kCols / 4; ++c)
+    *reinterpret_cast<uint4*>(sws + c * 512 + lane * 16) = make_uint4(v[c][0], v[c][1], v[c][2], v[c][3]);
 }
 
 template <int NT, bool NV>
 __global__ void __launch_bounds__(kThreads, NT == 4 ? 1 : 2)
-gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int splits) {
+gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int groups, const int splits) {
   constexpr int TT = 8 * NT;
   using S = Smem<TT, NV>;
   constexpr int ST = S::kStages;
+  constexpr int kPer = NV ? 16 : 32;
   extern __shared__ uint8_t smem_raw[];
-  const uint32_t base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t ws = base, xs = ws + ST * kWBytes, sws = xs + ST * S::kX, sxs = sws + ST * S::kSw,
-                 ctls = sxs + ST * S::kSx;
-  Ctl* ctl = reinterpret_cast<Ctl*>(smem_raw + (ctls - ptx::smem_u32(smem_raw)));
+  uint8_t* const base = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t *const ws = base, *const xs = ws + ST * kWBytes, *const sws = xs + ST * S::kX;
+  float* const sxs = reinterpret_cast<float*>(sws + ST * S::kSw);
+  Ctl* const ctl = reinterpret_cast<Ctl*>(sws + ST * (S::kSw + S::kSx));
   const uint32_t full_w = ptx::smem_u32(ctl->full_w), full_x = ptx::smem_u32(ctl->full_x),
                  empty = ptx::smem_u32(ctl->empty);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = (int)(blockIdx.x % splits);
-  const int64_t n0 = (int64_t)(blockIdx.x / splits) * kRows, m0 = (int64_t)blockIdx.y * kMaxTokens;
+  const int mma_warps = groups * kParts, rows = 32 * groups;
+  const int rank = (int)(blockIdx.x % (unsigned)splits);
+  const int64_t n0 = (int64_t)(blockIdx.x / (unsigned)splits) * rows, m0 = (int64_t)blockIdx.y * kMaxTokens;
   const int tokens = (int)min((int64_t)TT, a.M - m0);
-  const int64_t stages = (a.K + kStageK - 1) / kStageK;
-  const int64_t s0 = stages * rank / splits, s1 = stages * (rank + 1) / splits;
+  const int stages = (int)((a.K + kStageK - 1) / kStageK);
+  const int s0 = (int)((int64_t)stages * rank / splits), s1 = (int)((int64_t)stages * (rank + 1) / splits);
 
   if (threadIdx.x == 0) {
+    ptx::prefetch_tensormap(&tm);
     for (int i = 0; i < ST; ++i) {
       ptx::mbar_init(full_w + 8 * i, 1);
       ptx::mbar_init(full_x + 8 * i, 1);
-      ptx::mbar_init(empty + 8 * i, kMmaWarps);
+      ptx::mbar_init(empty + 8 * i, mma_warps);
     }
     ctl->abort = 0;
     ptx::fence_mbar_init();
   }
   __syncthreads();
 
-  float acc[2][NT][4];
+  float2 acc[2][NT][2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int r = 0; r < 2; ++r)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[i][n][c] = 0.0f;
-  const int g = lane >> 2, t = lane & 3, wr = warp & 3, half = (warp >> 2) & 1;
+    for (int n = 0; n < NT; ++n) acc[r][n][0] = acc[r][n][1] = make_float2(0.0f, 0.0f);
+  const int g = lane >> 2, t = lane & 3, part = warp / groups, wr = warp - part * groups;
 
   if (warp == kMmaWarps) {
     // ---- producer: codes by TMA, tensor-core scales as they lie in memory
     if (lane == 0) {
-      ptx::prefetch_tensormap(&tm);
-      int64_t done = s0;
-      for (int64_t s = s0; s < s1; ++s, ++done) {
-        const int i = (int)((s - s0) % ST);
-        const uint32_t round = (uint32_t)((s - s0) / ST);
+      const int64_t cols = a.K / kPer, tile0 = n0 >> 7, tiles = ((n0 + rows - 1) >> 7) - tile0 + 1;
+      const int64_t last = (a.N >> 7) - 1;               // the scale array's last row tile
+      int i = 0, s = s0;
+      uint32_t round = 0;
+      for (; s < s1; ++s) {
         if (round && !wait_bar(empty + 8 * i, (round - 1) & 1, ctl)) break;
-        uint32_t bytes = kWBytes;
-        const int64_t cols = a.K / (NV ? 16 : 32), c0 = s * (kStageK / (NV ? 16 : 32));
-        uint32_t sb = 0;
+        uint32_t bytes = (uint32_t)rows * kRowBytes, sb = 0;
+        const int64_t c0 = (int64_t)s * (kStageK / kPer);
         if (a.mma) {
-          sb = (uint32_t)min((int64_t)S::kSw, (cols - c0) * kRows);
-          bytes += sb;
+          sb = (uint32_t)min((int64_t)(S::kSw / 2), (cols - c0) * kRows);
+          bytes += sb * (uint32_t)tiles;
         }
         ptx::mbar_arrive_expect_tx(full_w + 8 * i, bytes);
-        ptx::tma_load_2d(ws + i * kWBytes, &tm, (int32_t)(s * kRowBytes), (int32_t)n0, full_w + 8 * i);
-        if (a.mma) ptx::bulk_load(sws + i * S::kSw, a.sw + n0 * cols + c0 * kRows, sb, full_w + 8 * i);
+        ptx::tma_load_2d(ptx::smem_u32(ws + i * kWBytes), &tm, s * kRowBytes, (int32_t)n0, full_w + 8 * i);
+        if (a.mma)
+          for (int64_t j = 0; j < tiles; ++j)
+            ptx::bulk_load(ptx::smem_u32(sws + i * S::kSw + j * (S::kSw / 2)),
+                           a.sw + min(tile0 + j, last) * 128 * cols + c0 * kRows, sb, full_w + 8 * i);
+        if (++i == ST) {
+          i = 0;
+          ++round;
+        }
       }
       // after an abort: the last load into each slot lands (bounded wait) before the CTA's memory goes
       if (*reinterpret_cast<volatile uint32_t*>(&ctl->abort)) {
-        const int64_t issued = done - s0;
-        for (int64_t r = issued > ST ? issued - ST : 0; r < issued; ++r) {
+        const int issued = s - s0;
+        for (int r = issued > ST ? issued - ST : 0; r < issued; ++r) {
           const uint64_t t0 = ptx::globaltimer_ns();
           while (!ptx::mbar_try_wait(full_w + 8 * (uint32_t)(r % ST), (uint32_t)(r / ST) & 1) &&
                  ptx::globaltimer_ns() - t0 < kWaitLimitNs / 10) {
@@ -335,36 +323,42 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
     __syncwarp();
   } else if (warp > kMmaWarps) {
     // ---- converters: whole stages in turn
-    for (int64_t s = s0 + (warp - kMmaWarps - 1); s < s1; s += kConvWarps) {
-      const int i = (int)((s - s0) % ST);
+    for (int s = s0 + (warp - kMmaWarps - 1); s < s1; s += kConvWarps) {
+      const int i = (s - s0) % ST;
       const uint32_t round = (uint32_t)((s - s0) / ST);
       if (round && !wait_bar(empty + 8 * i, (round - 1) & 1, ctl)) break;
-      if (!a.mma) convert_sw<NV>(a, n0, s * kStageK, lane, sws + i * S::kSw);
-      convert_x<TT>(a, m0, tokens, s * kStageK, lane, xs + i * S::kX, sxs + i * S::kSx);
+      const int64_t k0 = (int64_t)s * kStageK;
+      if (!a.mma) convert_sw<NV>(a, groups, n0, k0, lane, sws + i * S::kSw);
+      convert_x<TT>(a, m0, tokens, k0, lane, xs + i * S::kX, sxs + i * (S::kSx / 4));
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(full_x + 8 * i);
     }
-  } else {
-    // ---- multiplying warps: rows 32 wr .. 32 wr + 31, four 32-blocks of every stage
+  } else if (warp < mma_warps) {
+    // ---- multiplying warps: rows 32 wr .. 32 wr + 31, 32-blocks 4 part .. 4 part + 3 of every stage.
+    // Blocks past K need no case of their own: their codes (TMA's fill), their x and its factor are
+    // finite (zeros), and their scales are taken as zero bytes.
     uint32_t chunk[4];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) chunk[b] = (uint32_t)((((4 * half + b) ^ g) << 4) + 4 * t + (32 * wr + g) * kRowBytes);
-    const uint32_t xoff = half * 4 * (TT * 64) + g * 64 + t * 16, sxoff = half * 4 * (TT * 4) + 8 * t,
-                   swoff = (NV ? half * 1024 : half * 512) + g * 16 + wr * 4;
-    for (int64_t s = s0; s < s1; ++s) {
-      const int i = (int)((s - s0) % ST);
-      const uint32_t parity = (uint32_t)((s - s0) / ST) & 1;
+    for (int b = 0; b < 4; ++b) chunk[b] = (uint32_t)(((4 * part + b) ^ g) << 4) + 4 * t + (32 * wr + g) * kRowBytes;
+    // where this warp's 32 rows stand among the 128-row tiles of scales
+    const int64_t nw = n0 + 32 * wr;
+    const uint32_t tile = a.mma ? (uint32_t)((nw >> 7) - (n0 >> 7)) : 0u, quarter = a.mma ? (uint32_t)(nw >> 5) & 3u : wr;
+    const uint32_t swoff = tile * (S::kSw / 2) + part * (NV ? 1024 : 512) + g * 16 + quarter * 4;
+    const uint32_t xoff = 4 * part * (TT * 64) + g * 64 + t * 16, sxoff = 4 * part * TT + 2 * t;
+    int i = 0;
+    uint32_t parity = 0;
+    for (int s = s0; s < s1; ++s) {
       if (!wait_bar(full_w + 8 * i, parity, ctl) || !wait_bar(full_x + 8 * i, parity, ctl)) break;
-      const int blocks = (int)min((int64_t)4, (a.K - s * kStageK) / 32 - 4 * half);
-      const uint32_t w = ws + i * kWBytes, x = xs + i * S::kX + xoff, sx = sxs + i * S::kSx + sxoff,
-                     sw = sws + i * S::kSw + swoff;
+      const bool live = s * kBlocks + 4 * part < (int)(a.K >> 5);
+      const uint8_t *w = ws + i * kWBytes, *x = xs + i * S::kX + xoff, *sw = sws + i * S::kSw + swoff;
+      const float* sx = sxs + i * (S::kSx / 4) + sxoff;
       uint32_t sc[4][2];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t v = lds32(sw + j * 128);
+        const uint32_t v = live ? *reinterpret_cast<const uint32_t*>(sw + j * 128) : 0u;
         if (NV) {
           sc[j][0] = v;
-          sc[j][1] = lds32(sw + 512 + j * 128);
+          sc[j][1] = live ? *reinterpret_cast<const uint32_t*>(sw + 512 + j * 128) : 0u;
         } else {
           sc[j][0] = e8m0x2_bf16x2(v);
           sc[j][1] = e8m0x2_bf16x2(v >> 16);
@@ -372,12 +366,11 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
       }
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        if (b >= blocks) break;
         uint32_t q[4][4];
         float f[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          e2m1x8_f16(lds32(w + chunk[b] + j * 8 * kRowBytes), q[j]);
+          e2m1x8_f16(*reinterpret_cast<const uint32_t*>(w + chunk[b] + j * 8 * kRowBytes), q[j]);
           if (NV) {
             // this lane's eight elements lie in 16-block t / 2 of the run
             const uint32_t d = __byte_perm(sc[j][b >> 1], 0, (2 * (b & 1) + (t >> 1)) * 0x11);
@@ -390,8 +383,8 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const uint4 v = lds128(x + b * (TT * 64) + n * 512);
-          const float2 fx = lds64f(sx + b * (TT * 4) + n * 32);
+          const uint4 v = *reinterpret_cast<const uint4*>(x + b * (TT * 64) + n * 512);
+          const float2 fx = *reinterpret_cast<const float2*>(sx + b * TT + n * 8);
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -399,52 +392,59 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
             mma16816(c, q[2 * r][2], q[2 * r + 1][2], q[2 * r][3], q[2 * r + 1][3], v.z, v.w);
             const float2 p0 = NV ? fx : f2mul(fx, make_float2(f[2 * r], f[2 * r]));
             const float2 p1 = NV ? fx : f2mul(fx, make_float2(f[2 * r + 1], f[2 * r + 1]));
-            float2 u = f2fma(make_float2(c[0], c[1]), p0, make_float2(acc[r][n][0], acc[r][n][1]));
-            acc[r][n][0] = u.x;
-            acc[r][n][1] = u.y;
-            u = f2fma(make_float2(c[2], c[3]), p1, make_float2(acc[r][n][2], acc[r][n][3]));
-            acc[r][n][2] = u.x;
-            acc[r][n][3] = u.y;
+            acc[r][n][0] = f2fma(make_float2(c[0], c[1]), p0, acc[r][n][0]);
+            acc[r][n][1] = f2fma(make_float2(c[2], c[3]), p1, acc[r][n][1]);
           }
         }
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(empty + 8 * i);
+      if (++i == ST) {
+        i = 0;
+        parity ^= 1u;
+      }
     }
   }
 
-  // ---- sums of the two halves, then of the cluster's slices, in fixed order
+  // ---- sums of the parts, then of the cluster's slices, in fixed order
   __syncthreads();  // every load has landed and been read (or the CTA has aborted)
   const bool ok = *reinterpret_cast<volatile uint32_t*>(&ctl->abort) == 0;
-  const uint32_t red = ws;  // float [token][132]
-  for (int h = 1; h >= 0; --h) {
-    if (ok && warp < kMmaWarps && half == h) {
+  float* const red = reinterpret_cast<float*>(ws);  // [part][token][rows + 4]
+  const int ld = rows + 4, plane = TT * ld;
+  if (ok && warp < mma_warps) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
+    for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t at = red + (uint32_t)((8 * n + 2 * t + (c & 1)) * 132 + 32 * wr + 16 * r + 8 * (c >> 1) + g) * 4;
-            float v = acc[r][n][c];
-            if (h == 0) v = __fadd_rn(v, __uint_as_float(lds32(at)));
-            stsf(at, v);
-          }
-    }
-    __syncthreads();
+        for (int c = 0; c < 2; ++c) {
+          float* d = red + part * plane + (8 * n + 2 * t) * ld + 32 * wr + 16 * r + 8 * c + g;
+          d[0] = acc[r][n][c].x;
+          d[ld] = acc[r][n][c].y;
+        }
   }
-  if (splits > 1) ptx::cluster_sync();
+  __syncthreads();
+  const int total = tokens * rows;
+  if (splits > 1) {
+    if (ok)
+      for (int e = threadIdx.x; e < total; e += kThreads) {
+        float* d = red + e / rows * ld + e % rows;
+        *d = __fadd_rn(d[0], d[plane]);
+      }
+    __syncwarp();
+    ptx::cluster_sync();
+  }
   if (ok) {
-    const int rows = kRows / splits;
-    for (int e = threadIdx.x; e < tokens * rows; e += kThreads) {
-      const int m = e / rows, r = rank * rows + e % rows;
+    for (int e = total * rank / splits + threadIdx.x; e < total * (rank + 1) / splits; e += kThreads) {
+      const int m = e / rows, r = e % rows;
       const int64_t n = n0 + r;
       if (n >= a.N) continue;
-      const uint32_t at = red + (uint32_t)(m * 132 + r) * 4;
+      const float* d = red + m * ld + r;
       float v = 0.0f;
       if (splits == 1) {
-        v = __uint_as_float(lds32(at));
+        v = __fadd_rn(d[0], d[plane]);
       } else {
+        const uint32_t at = ptx::smem_u32(d);
         for (int c = 0; c < splits; ++c) v = __fadd_rn(v, lds_cluster(ptx::mapa(at, (uint32_t)c)));
       }
       if (NV) v = __fmul_rn(v, a.p2k);
@@ -460,7 +460,7 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
 }
 
 template <int NT, bool NV>
-cudaError_t launch(const CUtensorMap& tm, const GemvArgs& a, int splits, cudaStream_t st) {
+cudaError_t launch(const GemvArgs& a, int groups, int splits, cudaStream_t st) {
   constexpr int bytes = Smem<8 * NT, NV>::kBytes;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -476,8 +476,11 @@ cudaError_t launch(const CUtensorMap& tm, const GemvArgs& a, int splits, cudaStr
       set[dev] = true;
     }
   }
+  CUtensorMap tm;
+  if (!make_tma_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.qw, a.N, a.K / 2, a.K / 2, 32 * groups, kRowBytes))
+    return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.N + kRows - 1) / kRows) * (unsigned)splits,
+  cfg.gridDim = dim3((unsigned)((a.N + 32 * groups - 1) / (32 * groups)) * (unsigned)splits,
                      (unsigned)((a.M + kMaxTokens - 1) / kMaxTokens));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = bytes;
@@ -488,8 +491,8 @@ cudaError_t launch(const CUtensorMap& tm, const GemvArgs& a, int splits, cudaStr
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gemv_kernel<NT, NV>, tm, a, splits);
+  cfg.numAttrs = splits > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, gemv_kernel<NT, NV>, tm, a, groups, splits);
 }
 
 }  // namespace
@@ -501,20 +504,25 @@ cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t st) {
     const size_t es = a.y_f32 ? 4 : 2;
     return cudaMemset2DAsync(a.y, a.ld_y * es, 0, a.N * es, a.M, st);
   }
-  CUtensorMap tm;
-  if (!make_tma_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.qw, a.N, a.K / 2, a.K / 2, kRows, kRowBytes))
-    return cudaErrorInvalidValue;
-  // K is split until there are about three CTAs an SM.
+  const int nt = a.M <= 8 ? 1 : a.M <= 16 ? 2 : 4;
+  // K is split until two thirds of the SMs have a CTA (a CTA alone on its SM is
+  // bound by its own latency), and on to three CTAs an SM where each keeps 16
+  // stages to itself (shorter ones lose more to filling and emptying the ring).
   const int64_t tiles = (a.N + kRows - 1) / kRows * ((a.M + kMaxTokens - 1) / kMaxTokens);
   const int64_t stages = (a.K + kStageK - 1) / kStageK;
-  int splits = 1;
-  while (splits < GEMV_MAX_SPLITS && tiles * splits < GEMV_WANT && 2 * splits <= stages) splits *= 2;
-  const int nt = a.M <= 8 ? 1 : a.M <= 16 ? 2 : 4;
+  int groups = 4, splits = 1;
+  while (splits < 8 && ((3 * tiles * splits < 2 * kSms && 2 * splits <= stages) ||
+                        (2 * tiles * splits <= 3 * kSms && 32 * splits <= stages)))
+    splits *= 2;
+#ifdef GEMV_TUNE
+  if (getenv("GEMV_R")) groups = atoi(getenv("GEMV_R"));
+  if (getenv("GEMV_S")) splits = atoi(getenv("GEMV_S"));
+#endif
   if (a.nv)
-    return nt == 1 ? launch<1, true>(tm, a, splits, st)
-                   : nt == 2 ? launch<2, true>(tm, a, splits, st) : launch<4, true>(tm, a, splits, st);
-  return nt == 1 ? launch<1, false>(tm, a, splits, st)
-                 : nt == 2 ? launch<2, false>(tm, a, splits, st) : launch<4, false>(tm, a, splits, st);
+    return nt == 1 ? launch<1, true>(a, groups, splits, st)
+                   : nt == 2 ? launch<2, true>(a, groups, splits, st) : launch<4, true>(a, groups, splits, st);
+  return nt == 1 ? launch<1, false>(a, groups, splits, st)
+                 : nt == 2 ? launch<2, false>(a, groups, splits, st) : launch<4, false>(a, groups, splits, st);
 }
 
 cudaError_t read_gemv_error(uint32_t* err) {
