@@ -434,6 +434,7 @@ mxfp4_status check_row_quant(const char* fn, const mxfp4_quant_params* p, uint8_
                 : a.e5m2 ? mx::RowQuant::kE5m2 : a.e4m3 ? mx::RowQuant::kE4m3 : mx::RowQuant::kE2m1;
   o->roundup = a.roundup;
   o->mma = a.mma_layout;
+  o->packed = cols % (a.nv ? 64 : 128) == 0 && (reinterpret_cast<uintptr_t>(s) & 3u) == 0;
   o->p2k = a.nv_p2k;
   o->zmul = a.nv_zmul;
   o->q = q;
@@ -492,7 +493,7 @@ mxfp4_status mxfp4_rmsnorm_quantize(const void* x, int32_t x_dtype, int64_t rows
 
 size_t mxfp4_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols) {
   if (rows <= 0 || cols <= 0 || cols >= ((int64_t)1 << 31)) return 0;
-  return (size_t)mx::norm_dw_slices(rows) * (size_t)cols * sizeof(float);
+  return (size_t)mx::norm_dw_slices(rows, cols) * (size_t)cols * sizeof(float);
 }
 
 mxfp4_status mxfp4_rmsnorm_backward(const void* dy, int32_t dy_dtype, int64_t ld_dy, const void* h, int32_t h_dtype,

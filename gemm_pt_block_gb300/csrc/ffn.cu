@@ -6,6 +6,7 @@
 
 #include "internal.h"
 #include "mx_device.cuh"
+#include "ptx.cuh"
 
 namespace mx {
 namespace {
@@ -25,18 +26,20 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sum over the CTA, the same bits in every thread (fixed order).
-template <int kThreads>
-__device__ __forceinline__ float block_sum(float v, float* part) {
+// Sum over the CTA's `warps` warps, the same bits in every thread (fixed
+// order, a tree: rounding errors grow with the logarithm of the row's length).
+__device__ __forceinline__ float block_sum(float v, float* part, int warps) {
   v = warp_sum(v);
-  if (kThreads == 32) return v;
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  if (warps == 1) return v;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) part[threadIdx.x >> 5] = v;
   __syncthreads();
-  float s = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) s = __fadd_rn(s, part[i]);
-  __syncthreads();
-  return s;
+  return warp_sum(lane < warps ? part[lane] : 0.0f);
+}
+
+__device__ __forceinline__ float sum8(const float (&f)[8]) {
+  return __fadd_rn(__fadd_rn(__fadd_rn(f[0], f[1]), __fadd_rn(f[2], f[3])),
+                   __fadd_rn(__fadd_rn(f[4], f[5]), __fadd_rn(f[6], f[7])));
 }
 
 // ------------------------------------------------------------------ norm ---
@@ -44,120 +47,332 @@ __device__ __forceinline__ float block_sum(float v, float* part) {
 // norm is taken of the rounded h, so that the backward pass, which reads it
 // back, differentiates the same function:
 //   y_i = (h_i w_i) rstd,   rstd = 1 / sqrt(sum h^2 / D + eps).
-// bf16 products h_i w_i are exact in fp32, so y has two roundings. One CTA per
-// row, two passes over it; the second reads h back (from x and r, out of L2).
-constexpr int kRowThreads = 256;
-
+// bf16 products h_i w_i are exact in fp32, so y has two roundings.
 template <typename T>
-__device__ __forceinline__ void stream_of(const NormArgs& a, const T* x, const T* r, int64_t c, float (&h)[8],
-                                          Vec8<T>& raw) {
-  load8(x + c, raw);
-  unpack8(raw, h);
-  if (r) {
-    float f[8];
-    load8(r + c, raw);
-    unpack8(raw, f);
+__device__ __forceinline__ void add_stream(Vec8<T>& x, const Vec8<T>& r, float (&h)[8]) {
+  float f[8];
+  unpack8(x, h);
+  unpack8(r, f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = __fadd_rn(h[i], f[i]);
-    pack8(h, raw);
+  for (int i = 0; i < 8; ++i) h[i] = __fadd_rn(h[i], f[i]);
+  pack8(h, x);
+  unpack8(x, h);
+}
+
+__device__ __forceinline__ float reciprocal_rms(float sum, const NormArgs& a) {
+  return __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, (float)a.cols), a.eps));
+}
+
+// Eight outputs of a row whose norm is known: y and the quantized y.
+template <typename T, typename W>
+__device__ __forceinline__ void norm_out8(const NormArgs& a, const Vec8<T>& raw, bool live, int64_t row, int64_t c,
+                                          float rstd, const RowOut& out) {
+  float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (live) {
+    float h[8];
     unpack8(raw, h);
+    if (a.w) {
+      Vec8<W> wv;
+      load8_cached(static_cast<const W*>(a.w) + c, wv);
+      unpack8(wv, f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = __fmul_rn(__fmul_rn(h[i], f[i]), rstd);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = __fmul_rn(h[i], rstd);
+    }
+    if (a.y) store8_as(a.y, a.y_f32, row * a.ld_y + c, f, a.y_bytes);
+  }
+  if (a.quant.fmt != RowQuant::kNone) quantize8(a.quant, f, live, out, (uint32_t)c);
+}
+
+// A row in registers: kChunks vectors of eight elements to a thread, all loads
+// in flight at once, one pass over HBM. Rows of one warp (blockDim.x = 32)
+// share a CTA (blockDim.y of them), longer ones have a CTA each; several CTAs
+// an SM keep its loads going through one another's sums.
+template <typename T, typename W, int kChunks, int kMaxThreads>
+__global__ void __launch_bounds__(kMaxThreads) norm_rows_kernel(const NormArgs a) {
+  __shared__ float part[32];
+  const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  if (row >= a.rows) return;  // whole warps: only one-warp rows share a CTA
+  const T* x = static_cast<const T*>(a.x) + row * a.ld_x;
+  const T* r = static_cast<const T*>(a.r) + row * a.ld_r;
+  Vec8<T> v[kChunks], u[kChunks];
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    const int64_t c = (int64_t)(i * blockDim.x + threadIdx.x) * 8;
+    v[i] = Vec8<T>{};
+    if (c < a.cols) load8(x + c, v[i]);
+  }
+  if (a.r) {
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      const int64_t c = (int64_t)(i * blockDim.x + threadIdx.x) * 8;
+      u[i] = Vec8<T>{};
+      if (c < a.cols) load8(r + c, u[i]);
+    }
+  }
+  float s[kChunks];
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    const int64_t c = (int64_t)(i * blockDim.x + threadIdx.x) * 8;
+    float h[8];
+    if (a.r)
+      add_stream(v[i], u[i], h);
+    else
+      unpack8(v[i], h);
+    if (a.h && c < a.cols) store8(static_cast<T*>(a.h) + row * a.ld_h + c, v[i], a.h, a.h_bytes);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = __fmul_rn(h[j], h[j]);
+    s[i] = sum8(h);
+  }
+#pragma unroll
+  for (int d = 1; d < kChunks; d *= 2)
+#pragma unroll
+    for (int i = 0; i < kChunks; i += 2 * d) s[i] = __fadd_rn(s[i], s[i + d]);
+  const float rstd = reciprocal_rms(block_sum(s[0], part, blockDim.x >> 5), a);
+  if (a.rstd && threadIdx.x == 0) put_at(a.rstd + row, rstd, a.rstd, a.rows * sizeof(float));
+  if (!a.y && a.quant.fmt == RowQuant::kNone) return;
+  const RowOut out = row_out(a.quant, row, a.cols);
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    const int64_t c = (int64_t)(i * blockDim.x + threadIdx.x) * 8;
+    norm_out8<T, W>(a, v[i], c < a.cols, row, c, rstd, out);
   }
 }
 
+// Rows longer than a CTA's registers hold: two passes, the second one reading
+// x and r again (out of L2 for all but the longest).
+constexpr int kRowThreads = 1024;
+
 template <typename T, typename W>
-__global__ void __launch_bounds__(kRowThreads) norm_rows_kernel(const NormArgs a) {
-  __shared__ float part[kRowThreads / 32];
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const T* x = static_cast<const T*>(a.x) + row * a.ld_x;
-    const T* r = a.r ? static_cast<const T*>(a.r) + row * a.ld_r : nullptr;
-    float sum = 0.0f, h[8];
-    Vec8<T> raw;
-    for (int64_t c = threadIdx.x * 8; c < a.cols; c += kRowThreads * 8) {
-      stream_of(a, x, r, c, h, raw);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum = __fmaf_rn(h[i], h[i], sum);
+__global__ void __launch_bounds__(kRowThreads) norm_long_rows_kernel(const NormArgs a) {
+  __shared__ float part[32];
+  const int64_t row = blockIdx.x;
+  const T* x = static_cast<const T*>(a.x) + row * a.ld_x;
+  const T* r = static_cast<const T*>(a.r) + row * a.ld_r;
+  float sum = 0.0f, h[8];
+  Vec8<T> v, u;
+  for (int64_t c = threadIdx.x * 8; c < a.cols; c += kRowThreads * 8) {
+    load8(x + c, v);
+    if (a.r) {
+      load8(r + c, u);
+      add_stream(v, u, h);
+    } else {
+      unpack8(v, h);
     }
-    const float rstd = __frsqrt_rn(__fadd_rn(__fdiv_rn(block_sum<kRowThreads>(sum, part), (float)a.cols), a.eps));
-    if (a.rstd && threadIdx.x == 0) put_at(a.rstd + row, rstd, a.rstd, a.rows * sizeof(float));
-    for (int64_t c0 = 0; c0 < a.cols; c0 += kRowThreads * 8) {
-      const int64_t c = c0 + threadIdx.x * 8;
-      const bool live = c < a.cols;
-      float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      if (live) {
-        stream_of(a, x, r, c, h, raw);
-        if (a.h) store8(static_cast<T*>(a.h) + row * a.ld_h + c, raw, a.h, a.h_bytes);
-        if (a.w) {
-          Vec8<W> wv;
-          load8_cached(static_cast<const W*>(a.w) + c, wv);
-          unpack8(wv, f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] = __fmul_rn(__fmul_rn(h[i], f[i]), rstd);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] = __fmul_rn(h[i], rstd);
-        }
-        if (a.y) store8_as(a.y, a.y_f32, row * a.ld_y + c, f, a.y_bytes);
+    for (int i = 0; i < 8; ++i) h[i] = __fmul_rn(h[i], h[i]);
+    sum = __fadd_rn(sum, sum8(h));
+  }
+  const float rstd = reciprocal_rms(block_sum(sum, part, kRowThreads / 32), a);
+  if (a.rstd && threadIdx.x == 0) put_at(a.rstd + row, rstd, a.rstd, a.rows * sizeof(float));
+  const RowOut out = row_out(a.quant, row, a.cols);
+  for (int64_t c0 = 0; c0 < a.cols; c0 += kRowThreads * 8) {
+    const int64_t c = c0 + threadIdx.x * 8;
+    v = Vec8<T>{};
+    if (c < a.cols) {
+      load8(x + c, v);
+      if (a.r) {
+        load8(r + c, u);
+        add_stream(v, u, h);
       }
-      if (a.quant.fmt != RowQuant::kNone) quantize8(a.quant, f, live, row, c, a.cols);
+      if (a.h) store8(static_cast<T*>(a.h) + row * a.ld_h + c, v, a.h, a.h_bytes);
     }
+    norm_out8<T, W>(a, v, c < a.cols, row, c, rstd, out);
   }
 }
 
 // Gradients. With n = h rstd and dn = dy w:
 //   dx = (dn - n mean(dn n)) rstd + dh,   dw = sum over rows of dy n
 // (dh: what reaches h past the norm, through the residual stream).
+//
+// One kernel reads dy, h and dh once: persistent CTAs take rows in turn, whole
+// rows come by bulk copies into a ring of shared memory a few rows ahead, and
+// every thread keeps its columns' part of dw in registers over all of its
+// CTA's rows. The CTAs' parts go to the workspace and a second kernel sums
+// them in order (no atomics: dw has the same bits on every call).
+constexpr int kGradChunks = 2;
+constexpr int kGradSmem = 192 << 10;    // of the SM's 228 KB
+constexpr int kGradMaxStages = 8;
+constexpr int kSms = 152;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+
+// Bounded wait (about 2 s) of one thread; on expiry the device error word is set.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  while (!ptx::mbar_try_wait_sleep(bar, parity, 100000u)) {
+    if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
+      atomicExch(&g_ffn_error, 6u);  // MXFP4_ERR_TIMEOUT
+      return false;
+    }
+  }
+  return true;
+}
+
+template <typename T>
+__device__ __forceinline__ void load8_shared(const uint8_t* row, int64_t c, float (&f)[8]) {
+  Vec8<T> v = *reinterpret_cast<const Vec8<T>*>(row + c * sizeof(T));
+  unpack8(v, f);
+}
+
 template <typename T, typename G, typename W>
-__global__ void __launch_bounds__(kRowThreads) norm_dx_kernel(const NormGradArgs a) {
-  __shared__ float part[kRowThreads / 32];
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const T* hp = static_cast<const T*>(a.h) + row * a.ld_h;
-    const G* dp = static_cast<const G*>(a.dy) + row * a.ld_dy;
-    const float rstd = a.rstd[row];
-    float h[8], d[8], w[8], sum = 0.0f;
-    for (int pass = 0; pass < 2; ++pass) {
-      const float mean = pass ? __fdiv_rn(block_sum<kRowThreads>(sum, part), (float)a.cols) : 0.0f;
-      for (int64_t c = threadIdx.x * 8; c < a.cols; c += kRowThreads * 8) {
-        Vec8<T> hv;
-        Vec8<G> dv;
-        load8(hp + c, hv);
-        load8(dp + c, dv);
-        unpack8(hv, h);
-        unpack8(dv, d);
+__global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradArgs a, const int stages) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float part[2][32];
+  __shared__ uint64_t full[kGradMaxStages];
+  const uint32_t bars = ptx::smem_u32(full), tid = threadIdx.x, warps = blockDim.x >> 5;
+  const uint32_t h_bytes = (uint32_t)a.cols * sizeof(T), d_bytes = (uint32_t)a.cols * sizeof(G);
+  const uint32_t stage_bytes = d_bytes + h_bytes * (a.dh ? 2u : 1u);
+  const uint64_t gstep = gridDim.x;
+  if (tid == 0) {
+    for (int i = 0; i < stages; ++i) ptx::mbar_init(bars + 8 * i, 1);
+    ptx::fence_mbar_init();
+  }
+  __syncthreads();
+  auto fetch = [&](int64_t row, int slot) {
+    const uint32_t dst = ptx::smem_u32(ring) + slot * stage_bytes, bar = bars + 8 * slot;
+    ptx::mbar_arrive_expect_tx(bar, stage_bytes);
+    ptx::bulk_load(dst, static_cast<const G*>(a.dy) + row * a.ld_dy, d_bytes, bar);
+    ptx::bulk_load(dst + d_bytes, static_cast<const T*>(a.h) + row * a.ld_h, h_bytes, bar);
+    if (a.dh) ptx::bulk_load(dst + d_bytes + h_bytes, static_cast<const T*>(a.dh) + row * a.ld_dh, h_bytes, bar);
+  };
+  if (tid == 0)
+    for (int i = 0; i < stages && blockIdx.x + i * gstep < (uint64_t)a.rows; ++i) fetch(blockIdx.x + i * gstep, i);
+
+  Vec8<W> wv[kGradChunks];
+  float acc[kGradChunks][8];
+#pragma unroll
+  for (int i = 0; i < kGradChunks; ++i) {
+    const int64_t c = (int64_t)(i * blockDim.x + tid) * 8;
+    if (a.w && c < a.cols) load8_cached(static_cast<const W*>(a.w) + c, wv[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
+  }
+  int slot = 0, turn = 0;
+  uint32_t parity = 0;
+  float rstd = blockIdx.x < a.rows ? __ldg(a.rstd + blockIdx.x) : 0.0f;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gstep) {
+    const float next = row + gstep < a.rows ? __ldg(a.rstd + row + gstep) : 0.0f;
+    if (!wait_bar(bars + 8 * slot, parity)) break;  // every thread waits on the same bar: all give up alike
+    const uint8_t* dy = ring + slot * stage_bytes;
+    const uint8_t *h = dy + d_bytes, *dh = h + h_bytes;
+    // the row is read twice from shared memory: kept in registers between the
+    // passes, its values would leave too few for two CTAs an SM
+    float n[8], d[8], f[8], sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kGradChunks; ++i) {
+      const int64_t c = (int64_t)(i * blockDim.x + tid) * 8;
+      if (c < a.cols) {
+        load8_shared<G>(dy, c, d);
+        load8_shared<T>(h, c, n);
+        if (a.w) unpack8(wv[i], f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          n[j] = __fmul_rn(n[j], rstd);
+          acc[i][j] = __fmaf_rn(d[j], n[j], acc[i][j]);
+          sum = __fmaf_rn(a.w ? __fmul_rn(d[j], f[j]) : d[j], n[j], sum);
+        }
+      }
+    }
+    // one barrier a row: the partial sums alternate between two buffers, and
+    // past it every thread is done with the row before this one
+    const float mean = __fdiv_rn(block_sum(sum, part[turn], warps), (float)a.cols);
+    turn ^= 1;
+    if (warps == 1) __syncwarp();
+    const int64_t ahead = row + (stages - 1) * (int64_t)gstep;
+    if (tid == 0 && row != blockIdx.x && ahead < a.rows) fetch(ahead, slot == 0 ? stages - 1 : slot - 1);
+#pragma unroll
+    for (int i = 0; i < kGradChunks; ++i) {
+      const int64_t c = (int64_t)(i * blockDim.x + tid) * 8;
+      if (c < a.cols) {
+        load8_shared<G>(dy, c, d);
+        load8_shared<T>(h, c, n);
         if (a.w) {
-          Vec8<W> wv;
-          load8_cached(static_cast<const W*>(a.w) + c, wv);
-          unpack8(wv, w);
+          unpack8(wv[i], f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) d[j] = __fmul_rn(d[j], f[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] = __fmul_rn(__fmaf_rn(-__fmul_rn(n[j], rstd), mean, d[j]), rstd);
+        if (a.dh) {
+          load8_shared<T>(dh, c, f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) d[j] = __fadd_rn(d[j], f[j]);
+        }
+        Vec8<T> o;
+        pack8(d, o);
+        store8(static_cast<T*>(a.dx) + row * a.ld_dx + c, o, a.dx, a.dx_bytes);
+      }
+    }
+    rstd = next;
+    if (++slot == stages) {
+      slot = 0;
+      parity ^= 1u;
+    }
+  }
+  if (a.dw) {
+#pragma unroll
+    for (int i = 0; i < kGradChunks; ++i) {
+      const int64_t c = (int64_t)(i * blockDim.x + tid) * 8;
+      if (c < a.cols) store8_as(a.ws, true, (int64_t)blockIdx.x * a.cols + c, acc[i], a.ws_bytes);
+    }
+  }
+}
+
+// Rows too long for that ring: dx in two passes over the row, and dw from a
+// second reading of dy and h by columns.
+template <typename T, typename G, typename W>
+__global__ void __launch_bounds__(kRowThreads) norm_long_dx_kernel(const NormGradArgs a) {
+  __shared__ float part[32];
+  const int64_t row = blockIdx.x;
+  const T* hp = static_cast<const T*>(a.h) + row * a.ld_h;
+  const G* dp = static_cast<const G*>(a.dy) + row * a.ld_dy;
+  const float rstd = a.rstd[row];
+  float h[8], d[8], w[8], sum = 0.0f, mean = 0.0f;
+  for (int pass = 0; pass < 2; ++pass) {
+    if (pass) mean = __fdiv_rn(block_sum(sum, part, kRowThreads / 32), (float)a.cols);
+    for (int64_t c = threadIdx.x * 8; c < a.cols; c += kRowThreads * 8) {
+      Vec8<T> hv;
+      Vec8<G> dv;
+      load8(hp + c, hv);
+      load8(dp + c, dv);
+      unpack8(hv, h);
+      unpack8(dv, d);
+      if (a.w) {
+        Vec8<W> wv;
+        load8_cached(static_cast<const W*>(a.w) + c, wv);
+        unpack8(wv, w);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        h[i] = __fmul_rn(h[i], rstd);
+        if (a.w) d[i] = __fmul_rn(d[i], w[i]);
+        if (!pass) sum = __fmaf_rn(d[i], h[i], sum);
+      }
+      if (pass) {
+        if (a.dh) {
+          load8(static_cast<const T*>(a.dh) + row * a.ld_dh + c, hv);
+          unpack8(hv, w);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          h[i] = __fmul_rn(h[i], rstd);
-          if (a.w) d[i] = __fmul_rn(d[i], w[i]);
-          if (!pass) sum = __fmaf_rn(d[i], h[i], sum);
+          d[i] = __fmul_rn(__fmaf_rn(-h[i], mean, d[i]), rstd);
+          if (a.dh) d[i] = __fadd_rn(d[i], w[i]);
         }
-        if (pass) {
-          if (a.dh) {
-            load8(static_cast<const T*>(a.dh) + row * a.ld_dh + c, hv);
-            unpack8(hv, w);
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            d[i] = __fmul_rn(__fmaf_rn(-h[i], mean, d[i]), rstd);
-            if (a.dh) d[i] = __fadd_rn(d[i], w[i]);
-          }
-          pack8(d, hv);
-          store8(static_cast<T*>(a.dx) + row * a.ld_dx + c, hv, a.dx, a.dx_bytes);
-        }
+        pack8(d, hv);
+        store8(static_cast<T*>(a.dx) + row * a.ld_dx + c, hv, a.dx, a.dx_bytes);
       }
     }
   }
 }
 
-// dw: every CTA row slice (blockIdx.y) sums its rows into one row of the
-// workspace, in order; the sum over slices follows in the next kernel, so dw
-// has the same bits on every call.
+constexpr int kColThreads = 256;
+
 template <typename T, typename G>
-__global__ void __launch_bounds__(kRowThreads) norm_dw_kernel(const NormGradArgs a) {
-  const int64_t c = ((int64_t)blockIdx.x * kRowThreads + threadIdx.x) * 8;
+__global__ void __launch_bounds__(kColThreads) norm_long_dw_kernel(const NormGradArgs a) {
+  const int64_t c = ((int64_t)blockIdx.x * kColThreads + threadIdx.x) * 8;
   if (c >= a.cols) return;
   float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0}, h[8], d[8];
   for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
@@ -174,13 +389,22 @@ __global__ void __launch_bounds__(kRowThreads) norm_dw_kernel(const NormGradArgs
   store8_as(a.ws, true, (int64_t)blockIdx.y * a.cols + c, acc, a.ws_bytes);
 }
 
+// dw from the partial sums: a CTA takes 32 columns, its eight warps every
+// eighth slice, and the warps' sums are added in order.
 template <typename W>
-__global__ void __launch_bounds__(kRowThreads) norm_dw_sum_kernel(const float* __restrict__ ws, int slices,
-                                                                  int64_t cols, W* dw) {
-  const int64_t c = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
-  if (c >= cols) return;
+__global__ void __launch_bounds__(256) norm_dw_sum_kernel(const float* __restrict__ ws, int slices, int64_t cols,
+                                                          W* dw) {
+  __shared__ float part[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   float s = 0.0f;
-  for (int i = 0; i < slices; ++i) s = __fadd_rn(s, ws[i * cols + c]);
+#pragma unroll 8
+  for (int i = warp; i < slices; i += 8) s = __fadd_rn(s, ws[i * cols + c]);
+  part[warp][lane] = s;
+  __syncthreads();
+  if (warp) return;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) s = __fadd_rn(s, part[i][lane]);
   if (sizeof(W) == 4)
     put_at(dw + c, s, dw, cols * sizeof(W));
   else
@@ -200,35 +424,49 @@ __device__ __forceinline__ float sigmoid(float g) {
   return __fdividef(g < 0.0f ? t : 1.0f, __fadd_rn(1.0f, t));
 }
 
+// A CTA is blockDim.y rows of blockDim.x threads; a thread takes kActChunks
+// vectors of its row, blockDim.x apart, so that 2 x kActChunks loads are in
+// flight. Rows go on past the grid's height.
+constexpr int kActChunks = 2;
+
 template <typename T>
 __global__ void __launch_bounds__(kActThreads) swiglu_kernel(const SwigluArgs a) {
-  const int64_t vecs = a.cols >> 3, total = a.rows * vecs;
-  for (int64_t v0 = (int64_t)blockIdx.x * kActThreads; v0 < total; v0 += (int64_t)gridDim.x * kActThreads) {
-    const int64_t v = v0 + threadIdx.x;
-    const bool live = v < total;
-    const int64_t row = live ? v / vecs : 0, c = live ? (v - row * vecs) * 8 : 0;
-    float g[8] = {0, 0, 0, 0, 0, 0, 0, 0}, u[8];
-    if (live) {
-      Vec8<T> gv, uv;
-      load8(static_cast<const T*>(a.g) + row * a.ld_g + c, gv);
-      load8(static_cast<const T*>(a.u) + row * a.ld_u + c, uv);
-      unpack8(gv, g);
-      unpack8(uv, u);
+  const int64_t c0 = ((int64_t)blockIdx.x * kActChunks * blockDim.x + threadIdx.x) * 8;
+  for (int64_t r0 = (int64_t)blockIdx.y * blockDim.y; r0 < a.rows; r0 += (int64_t)gridDim.y * blockDim.y) {
+    const int64_t row = r0 + threadIdx.y;
+    if (row >= a.rows) return;  // whole warps
+    Vec8<T> gv[kActChunks], uv[kActChunks];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] = __fmul_rn(__fmul_rn(g[i], sigmoid(g[i])), u[i]);
-      if (a.y) store8_as(a.y, a.y_f32, row * a.ld_y + c, g, a.y_bytes);
+    for (int i = 0; i < kActChunks; ++i) {
+      const int64_t c = c0 + (int64_t)i * blockDim.x * 8;
+      gv[i] = uv[i] = Vec8<T>{};
+      if (c < a.cols) {
+        load8(static_cast<const T*>(a.g) + row * a.ld_g + c, gv[i]);
+        load8(static_cast<const T*>(a.u) + row * a.ld_u + c, uv[i]);
+      }
     }
-    if (a.quant.fmt != RowQuant::kNone) quantize8(a.quant, g, live, row, c, a.cols);
+    const RowOut out = row_out(a.quant, row, a.cols);
+#pragma unroll
+    for (int i = 0; i < kActChunks; ++i) {
+      const int64_t c = c0 + (int64_t)i * blockDim.x * 8;
+      float g[8], u[8];
+      unpack8(gv[i], g);
+      unpack8(uv[i], u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] = __fmul_rn(__fmul_rn(g[j], sigmoid(g[j])), u[j]);
+      if (a.y && c < a.cols) store8_as(a.y, a.y_f32, row * a.ld_y + c, g, a.y_bytes);
+      if (a.quant.fmt != RowQuant::kNone) quantize8(a.quant, g, c < a.cols, out, (uint32_t)c);
+    }
   }
 }
 
 // With s = 1 / (1 + e^-g): dg = dy u s (1 + g (1 - s)), du = dy g s.
 template <typename T, typename G>
 __global__ void __launch_bounds__(kActThreads) swiglu_grad_kernel(const SwigluGradArgs a) {
-  const int64_t vecs = a.cols >> 3, total = a.rows * vecs;
-  for (int64_t v = (int64_t)blockIdx.x * kActThreads + threadIdx.x; v < total;
-       v += (int64_t)gridDim.x * kActThreads) {
-    const int64_t row = v / vecs, c = (v - row * vecs) * 8;
+  const int64_t c = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 8;
+  if (c >= a.cols) return;
+  for (int64_t row = (int64_t)blockIdx.y * blockDim.y + threadIdx.y; row < a.rows;
+       row += (int64_t)gridDim.y * blockDim.y) {
     float g[8], u[8], d[8];
     Vec8<T> gv, uv;
     Vec8<G> dv;
@@ -252,38 +490,113 @@ __global__ void __launch_bounds__(kActThreads) swiglu_grad_kernel(const SwigluGr
   }
 }
 
-unsigned grid_for(int64_t items) { return (unsigned)(items < (1 << 20) ? items : (1 << 20)); }
+// Block and grid of the activation kernels: rows of up to 256 threads (a
+// multiple of 32), shorter rows side by side in one CTA.
+void act_shape(int64_t rows, int64_t vecs, int chunks, dim3* grid, dim3* block) {
+  const int64_t per_row = (vecs + chunks - 1) / chunks;
+  const unsigned x = per_row >= kActThreads ? kActThreads : (unsigned)((per_row + 31) / 32 * 32);
+  const unsigned y = kActThreads / x;
+  const int64_t tall = (rows + y - 1) / y;
+  *block = dim3(x, y);
+  *grid = dim3((unsigned)((per_row + x - 1) / x), (unsigned)(tall < 65535 ? tall : 65535));
+}
+
+// The gradient kernel's shape for rows of `cols`: threads (kGradChunks vectors
+// each), and CTAs an SM so that about 1024 threads share it.
+int grad_threads(int64_t cols) { return (int)((cols / 8 + 32 * kGradChunks - 1) / (32 * kGradChunks) * 32); }
+int grad_ctas(int64_t cols) {
+  const int t = grad_threads(cols);
+  return t >= 1024 ? 1 : t <= 128 ? 8 : 1024 / t;
+}
 
 }  // namespace
 
-int norm_dw_slices(int64_t rows) { return (int)(rows < 256 ? rows : 256); }
+// Rows of partial sums that the workspace holds, for either way of taking dw.
+int norm_dw_slices(int64_t rows, int64_t cols) {
+  const int64_t most = cols <= 1024 * 8 * kGradChunks ? (int64_t)kSms * grad_ctas(cols) : 256;
+  return (int)(rows < most ? rows : most < 256 ? 256 : most);
+}
+
+namespace {
+template <typename T, typename W>
+void launch_norm(const NormArgs& a, cudaStream_t st) {
+  const int64_t vecs = a.cols / 8;
+  const unsigned rows = (unsigned)a.rows;
+  if (vecs <= 128) {
+    // one warp a row, eight rows a CTA
+    const dim3 grid((unsigned)((a.rows + 7) / 8)), block(32, 8);
+    if (vecs <= 32)
+      norm_rows_kernel<T, W, 1, 256><<<grid, block, 0, st>>>(a);
+    else
+      norm_rows_kernel<T, W, 4, 256><<<grid, block, 0, st>>>(a);
+  } else if (vecs <= 1024 && a.rows <= kSms) {
+    // an SM or more to each row: the widest CTA has the shortest way through it
+    norm_rows_kernel<T, W, 1, 1024><<<rows, (unsigned)((vecs + 31) / 32 * 32), 0, st>>>(a);
+  } else if (vecs <= 1024) {
+    norm_rows_kernel<T, W, 4, 256><<<rows, (unsigned)((vecs + 127) / 128 * 32), 0, st>>>(a);
+  } else if (vecs <= 2048) {
+    norm_rows_kernel<T, W, 2, 1024><<<rows, (unsigned)((vecs + 63) / 64 * 32), 0, st>>>(a);
+  } else if (sizeof(T) == 2 && vecs <= 4096) {
+    norm_rows_kernel<T, W, 4, 1024><<<rows, (unsigned)((vecs + 127) / 128 * 32), 0, st>>>(a);
+  } else {
+    norm_long_rows_kernel<T, W><<<rows, kRowThreads, 0, st>>>(a);
+  }
+}
+}  // namespace
 
 cudaError_t launch_rmsnorm(const NormArgs& a, bool x_f32, bool w_f32, cudaStream_t st) {
   if (a.rows == 0 || a.cols == 0) return cudaSuccess;
   (void)cudaGetLastError();  // drop a stale error left by an earlier call
-  const unsigned grid = grid_for(a.rows);
   if (x_f32 && w_f32)
-    norm_rows_kernel<float, float><<<grid, kRowThreads, 0, st>>>(a);
+    launch_norm<float, float>(a, st);
   else if (x_f32)
-    norm_rows_kernel<float, uint16_t><<<grid, kRowThreads, 0, st>>>(a);
+    launch_norm<float, uint16_t>(a, st);
   else if (w_f32)
-    norm_rows_kernel<uint16_t, float><<<grid, kRowThreads, 0, st>>>(a);
+    launch_norm<uint16_t, float>(a, st);
   else
-    norm_rows_kernel<uint16_t, uint16_t><<<grid, kRowThreads, 0, st>>>(a);
+    launch_norm<uint16_t, uint16_t>(a, st);
   return cudaGetLastError();
 }
 
 namespace {
 template <typename T, typename G, typename W>
-void norm_grad(const NormGradArgs& a, cudaStream_t st) {
-  if (a.rows > 0) norm_dx_kernel<T, G, W><<<grid_for(a.rows), kRowThreads, 0, st>>>(a);
-  if (!a.dw) return;
-  const int slices = norm_dw_slices(a.rows);
-  if (slices)
-    norm_dw_kernel<T, G><<<dim3((unsigned)((a.cols / 8 + kRowThreads - 1) / kRowThreads), slices), kRowThreads, 0,
-                           st>>>(a);
-  norm_dw_sum_kernel<W><<<(unsigned)((a.cols + kRowThreads - 1) / kRowThreads), kRowThreads, 0, st>>>(
-      a.ws, slices, a.cols, static_cast<W*>(a.dw));
+cudaError_t norm_grad(const NormGradArgs& a, cudaStream_t st) {
+  int slices = 0;
+  const int64_t stage = a.cols * (int64_t)(sizeof(G) + sizeof(T) * (a.dh ? 2 : 1));
+  int ctas = grad_ctas(a.cols);
+  while (ctas > 1 && 2 * stage * ctas > kGradSmem) --ctas;
+  if (a.cols <= 1024 * 8 * kGradChunks && 2 * stage <= kGradSmem) {
+    if (a.rows > 0) {
+      int dev = 0;
+      cudaError_t e = cudaGetDevice(&dev);
+      if (e != cudaSuccess) return e;
+      if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+      {
+        static bool set[kMaxDevices] = {};
+        static std::mutex mu;
+        std::lock_guard<std::mutex> lock(mu);
+        if (!set[dev]) {
+          e = cudaFuncSetAttribute(norm_grad_kernel<T, G, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradSmem);
+          if (e != cudaSuccess) return e;
+          set[dev] = true;
+        }
+      }
+      const int64_t fit = kGradSmem / (stage * ctas);
+      const int stages = (int)(fit < kGradMaxStages ? fit : kGradMaxStages);
+      slices = (int)(a.rows < (int64_t)kSms * ctas ? a.rows : (int64_t)kSms * ctas);
+      norm_grad_kernel<T, G, W><<<slices, grad_threads(a.cols), stages * stage, st>>>(a, stages);
+    }
+  } else if (a.rows > 0) {
+    norm_long_dx_kernel<T, G, W><<<(unsigned)a.rows, kRowThreads, 0, st>>>(a);
+    if (a.dw) {
+      slices = (int)(a.rows < 256 ? a.rows : 256);
+      norm_long_dw_kernel<T, G><<<dim3((unsigned)((a.cols / 8 + kColThreads - 1) / kColThreads), slices), kColThreads,
+                                  0, st>>>(a);
+    }
+  }
+  if (a.dw)
+    norm_dw_sum_kernel<W><<<(unsigned)(a.cols / 32), 256, 0, st>>>(a.ws, slices, a.cols, static_cast<W*>(a.dw));
+  return cudaGetLastError();
 }
 }  // namespace
 
@@ -292,41 +605,42 @@ cudaError_t launch_rmsnorm_grad(const NormGradArgs& a, bool h_f32, bool dy_f32, 
   (void)cudaGetLastError();
   using B = uint16_t;
   switch ((h_f32 ? 4 : 0) | (dy_f32 ? 2 : 0) | (w_f32 ? 1 : 0)) {
-    case 0: norm_grad<B, B, B>(a, st); break;
-    case 1: norm_grad<B, B, float>(a, st); break;
-    case 2: norm_grad<B, float, B>(a, st); break;
-    case 3: norm_grad<B, float, float>(a, st); break;
-    case 4: norm_grad<float, B, B>(a, st); break;
-    case 5: norm_grad<float, B, float>(a, st); break;
-    case 6: norm_grad<float, float, B>(a, st); break;
-    default: norm_grad<float, float, float>(a, st);
+    case 0: return norm_grad<B, B, B>(a, st);
+    case 1: return norm_grad<B, B, float>(a, st);
+    case 2: return norm_grad<B, float, B>(a, st);
+    case 3: return norm_grad<B, float, float>(a, st);
+    case 4: return norm_grad<float, B, B>(a, st);
+    case 5: return norm_grad<float, B, float>(a, st);
+    case 6: return norm_grad<float, float, B>(a, st);
+    default: return norm_grad<float, float, float>(a, st);
   }
-  return cudaGetLastError();
 }
 
 cudaError_t launch_swiglu(const SwigluArgs& a, bool f32, cudaStream_t st) {
   if (a.rows == 0 || a.cols == 0) return cudaSuccess;
   (void)cudaGetLastError();
-  const unsigned grid = grid_for((a.rows * (a.cols / 8) + kActThreads - 1) / kActThreads);
+  dim3 grid, block;
+  act_shape(a.rows, a.cols / 8, kActChunks, &grid, &block);
   if (f32)
-    swiglu_kernel<float><<<grid, kActThreads, 0, st>>>(a);
+    swiglu_kernel<float><<<grid, block, 0, st>>>(a);
   else
-    swiglu_kernel<uint16_t><<<grid, kActThreads, 0, st>>>(a);
+    swiglu_kernel<uint16_t><<<grid, block, 0, st>>>(a);
   return cudaGetLastError();
 }
 
 cudaError_t launch_swiglu_grad(const SwigluGradArgs& a, bool f32, bool dy_f32, cudaStream_t st) {
   if (a.rows == 0 || a.cols == 0) return cudaSuccess;
   (void)cudaGetLastError();
-  const unsigned grid = grid_for((a.rows * (a.cols / 8) + kActThreads - 1) / kActThreads);
+  dim3 grid, block;
+  act_shape(a.rows, a.cols / 8, 1, &grid, &block);
   if (f32 && dy_f32)
-    swiglu_grad_kernel<float, float><<<grid, kActThreads, 0, st>>>(a);
+    swiglu_grad_kernel<float, float><<<grid, block, 0, st>>>(a);
   else if (f32)
-    swiglu_grad_kernel<float, uint16_t><<<grid, kActThreads, 0, st>>>(a);
+    swiglu_grad_kernel<float, uint16_t><<<grid, block, 0, st>>>(a);
   else if (dy_f32)
-    swiglu_grad_kernel<uint16_t, float><<<grid, kActThreads, 0, st>>>(a);
+    swiglu_grad_kernel<uint16_t, float><<<grid, block, 0, st>>>(a);
   else
-    swiglu_grad_kernel<uint16_t, uint16_t><<<grid, kActThreads, 0, st>>>(a);
+    swiglu_grad_kernel<uint16_t, uint16_t><<<grid, block, 0, st>>>(a);
   return cudaGetLastError();
 }
 

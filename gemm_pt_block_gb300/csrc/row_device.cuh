@@ -111,50 +111,74 @@ __device__ __forceinline__ void store8_as(void* base, bool f32, int64_t at, cons
   }
 }
 
-// Quantizes the eight values f that this lane holds of output row `row`,
-// columns col .. col + 7, and stores codes and scales. Lanes 4 i .. 4 i + 3 of
-// the warp hold one 32-run (columns of a multiple of 32 first), so a block's
-// max-abs is two exchanges away (one for 1x16 blocks). Every lane of the warp
-// calls this; one with `live` false holds nothing and stores nothing. The
-// maximum is taken over the bit patterns of |f|, which orders infinity and NaN
-// above every finite value: a block that holds either gets the scale format's
-// NaN as its scale and zero codes, and so dequantizes to NaN.
-__device__ __forceinline__ void quantize8(const RowQuant& o, float (&f)[8], bool live, int64_t row,
-                                          int64_t col, int64_t cols) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+// Largest of three magnitudes; NaN if one of them is.
+__device__ __forceinline__ float absmax3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
+  return r;
+}
+
+// Where the codes and scales of one output row lie.
+struct RowOut {
+  uint8_t *q, *s;
+};
+__device__ __forceinline__ RowOut row_out(const RowQuant& o, int64_t row, int64_t cols) {
+  RowOut r;
+  const int64_t nkb = o.fmt == RowQuant::kNvfp4 ? cols >> 4 : cols >> 5;
+  r.q = o.q + (o.fmt == RowQuant::kE4m3 || o.fmt == RowQuant::kE5m2 ? row * cols : (row * cols) >> 1);
+  r.s = o.s + (o.mma ? mma_scale_offset(row, 0, nkb) : row * nkb);
+  return r;
+}
+
+// Quantizes the eight values f that this lane holds of one output row, columns
+// col .. col + 7, and stores codes and scales. Lanes 4 i .. 4 i + 3 of the warp
+// hold one 32-run (columns of a multiple of 32 first), so a block's max-abs is
+// two exchanges away (one for 1x16 blocks). Every lane of the warp calls this;
+// one with `live` false holds zeros and stores nothing. The maximum keeps a
+// NaN: a block that holds an infinity or a NaN gets the scale format's NaN as
+// its scale and zero codes, and so dequantizes to NaN. With o.packed the scales
+// of four neighbouring blocks are stored as one word.
+__device__ __forceinline__ void quantize8(const RowQuant& o, float (&f)[8], bool live, const RowOut& out,
+                                          uint32_t col) {
   const bool nv = o.fmt == RowQuant::kNvfp4;
-  if (!nv) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  const bool bad = m >= 0x7F800000u;
-  const float M = bad ? 0.0f : __uint_as_float(m);
+  float m = absmax3_nan(absmax3_nan(f[0], f[1], f[2]), absmax3_nan(f[3], f[4], f[5]), absmax3_nan(f[6], f[7], 0.0f));
+  m = absmax3_nan(m, __shfl_xor_sync(0xffffffffu, m, 1), 0.0f);
+  if (!nv) m = absmax3_nan(m, __shfl_xor_sync(0xffffffffu, m, 2), 0.0f);
+  const bool bad = __float_as_uint(m) >= 0x7F800000u;
   uint32_t code;
   float mul;
   if (nv) {
-    const NvScale s = nv_scale(M, o.roundup, o.p2k, o.zmul);
+    const NvScale s = nv_scale(bad ? 0.0f : m, o.roundup, o.p2k, o.zmul);
     code = bad ? 0x7Fu : s.code;
     mul = s.rcp;
   } else {
-    const int e = scale_exponent(M, o.roundup, o.fmt != RowQuant::kE2m1, o.fmt == RowQuant::kE5m2);
+    const int e = scale_exponent(m, o.roundup, o.fmt != RowQuant::kE2m1, o.fmt == RowQuant::kE5m2);
     code = bad ? 0xFFu : (uint32_t)(e + 127);
     mul = inv_scale(e);
   }
+  if (bad) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = bad ? 0.0f : __fmul_rn(f[i], mul);
-  if (!live) return;
-  if (o.fmt == RowQuant::kE4m3 || o.fmt == RowQuant::kE5m2) {
-    const bool e5 = o.fmt == RowQuant::kE5m2;
-    const uint2 c = e5 ? make_uint2(e5m2x4(f[0], f[1], f[2], f[3]), e5m2x4(f[4], f[5], f[6], f[7]))
-                       : make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
-    put_at(o.q + row * cols + col, c, o.q, o.q_bytes);
-  } else {
-    put_at(o.q + ((row * cols + col) >> 1), e2m1x8(f[0], f[1], f[2], f[3], f[4], f[5], f[6], f[7]), o.q,
-           o.q_bytes);
+    for (int i = 0; i < 8; ++i) f[i] = 0.0f;
   }
-  const int64_t kb = nv ? col >> 4 : col >> 5, nkb = nv ? cols >> 4 : cols >> 5;
-  if ((col & (nv ? 15 : 31)) == 0)
-    put_at(o.s + (o.mma ? mma_scale_offset(row, kb, nkb) : row * nkb + kb), (uint8_t)code, o.s, o.s_bytes);
+  const float2 mm = make_float2(mul, mul), a = f2mul(make_float2(f[0], f[1]), mm), b = f2mul(make_float2(f[2], f[3]), mm),
+               c = f2mul(make_float2(f[4], f[5]), mm), d = f2mul(make_float2(f[6], f[7]), mm);
+  if (live) {
+    if (o.fmt == RowQuant::kE4m3)
+      put_at(out.q + col, make_uint2(e4m3x4(a.x, a.y, b.x, b.y), e4m3x4(c.x, c.y, d.x, d.y)), o.q, o.q_bytes);
+    else if (o.fmt == RowQuant::kE5m2)
+      put_at(out.q + col, make_uint2(e5m2x4(a.x, a.y, b.x, b.y), e5m2x4(c.x, c.y, d.x, d.y)), o.q, o.q_bytes);
+    else
+      put_at(out.q + (col >> 1), e2m1x8(a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y), o.q, o.q_bytes);
+  }
+  const uint32_t kb = nv ? col >> 4 : col >> 5, at = o.mma ? ((kb >> 2) << 9) + (kb & 3) : kb;
+  if (o.packed) {
+    const int d1 = nv ? 2 : 4;
+    code |= __shfl_down_sync(0xffffffffu, code, d1) << 8;
+    code |= __shfl_down_sync(0xffffffffu, code, 2 * d1) << 16;
+    if (live && (kb & 3) == 0 && (col & (nv ? 15 : 31)) == 0) put_at(out.s + at, code, o.s, o.s_bytes);
+  } else if (live && (col & (nv ? 15 : 31)) == 0) {
+    put_at(out.s + at, (uint8_t)code, o.s, o.s_bytes);
+  }
 }
 
 }  // namespace mx
