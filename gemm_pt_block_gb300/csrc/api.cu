@@ -433,6 +433,8 @@ mxfp4_status check_row_quant(const char* fn, const mxfp4_quant_params* p, uint8_
   o->fmt = a.nv ? mx::RowQuant::kNvfp4
                 : a.e5m2 ? mx::RowQuant::kE5m2 : a.e4m3 ? mx::RowQuant::kE4m3 : mx::RowQuant::kE2m1;
   o->roundup = a.roundup;
+  o->emax = a.e5m2 ? 15 : a.e4m3 ? 8 : 2;
+  o->over = !a.roundup ? 0x7FFFFFu : a.e4m3 ? 0x600000u : 0x400000u;  // 1.75 2^emax, E2M1 1.5 2^emax
   o->mma = a.mma_layout;
   o->packed = cols % (a.nv ? 64 : 128) == 0 && (reinterpret_cast<uintptr_t>(s) & 3u) == 0;
   o->p2k = a.nv_p2k;

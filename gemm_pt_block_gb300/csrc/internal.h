@@ -45,6 +45,8 @@ struct RowQuant {
   int32_t roundup;
   int32_t mma;        // scale layout: 0 row-major, 1 tensor-core tiles
   int32_t packed;     // rows hold whole words of four scales (and s is 4-byte aligned)
+  int32_t emax;       // E8M0: exponent of the elements' largest value (2, 8 or 15)
+  uint32_t over;      // E8M0: fractions of the maximum above this round the scale up
   float p2k, zmul;    // NVFP4: 2^tensor_exp and 2^-tensor_exp / 6
   uint8_t *q, *s;
   uint64_t q_bytes, s_bytes;  // extents
