@@ -8,7 +8,6 @@ pass, and forwards raw pointers plus the current CUDA stream to the C ABI.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from dataclasses import dataclass
 
@@ -510,19 +509,16 @@ def nvfp4_tensor_exp(x: torch.Tensor, stream=None) -> int:
     return int(k.item())
 
 
-def _on_its_stream(call):
-    """Runs `call` with its `stream` argument as PyTorch's current stream, so
-    that what it allocates (outputs, workspaces) belongs to the stream that
-    its kernels run on."""
-    @functools.wraps(call)
-    def on_stream(*args, stream=None, **kw):
-        if stream is None:
-            return call(*args, **kw)
-        with torch.cuda.stream(stream):
-            return call(*args, **kw)
-    return on_stream
+def _on(stream, call, *args, **kw):
+    """`call` with `stream` as PyTorch's current stream, so that what it
+    allocates (outputs, workspaces) belongs to the stream that its kernels
+    run on."""
+    with torch.cuda.stream(stream):
+        return call(*args, **kw)
 
 
+# Code of a matrix's type in the C ABI. Small calls are bound by the host: what
+# follows keeps each argument to one look at it.
 _DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
 
 
@@ -533,45 +529,59 @@ def _dtype_of(t: torch.Tensor, name: str) -> int:
     return dt
 
 
-def _rows_ld(t: torch.Tensor, name: str, rows: int, cols: int) -> int:
-    """Leading dimension of a CUDA matrix [rows, cols] with unit column stride.
-    The stride of a single row (or of an empty matrix) is never used."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+def _rows_ld(t: torch.Tensor, name: str, rows: int, cols: int, dev: int) -> int:
+    """Leading dimension of a matrix [rows, cols] on CUDA device `dev` with unit
+    column stride. The stride of a single row (or of an empty matrix) is never
+    used."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on device {dev} (got {t.device})")
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}, {cols}] (got {list(t.shape)})")
-    if rows * cols and t.stride(1) != 1 and cols > 1:
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1 and rows:
         raise ValueError(f"{name} must have unit column stride")
-    return t.stride(0) if rows > 1 and cols else cols
+    return ld if rows > 1 and cols else cols
 
 
-def _vector(t: torch.Tensor, name: str, n: int) -> None:
+def _device_of(t: torch.Tensor, name: str) -> int:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D (got {list(t.shape)})")
+    return t.get_device()
+
+
+def _vector(t: torch.Tensor, name: str, n: int, dev: int) -> None:
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on device {dev} (got {t.device})")
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be a contiguous vector of {n} elements (got {list(t.shape)})")
 
 
-def _same_device(*ts) -> None:
-    devs = {t.device for t in ts if t is not None}
-    if len(devs) > 1:
-        raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
+def _dense(t: torch.Tensor, numel: int, dtype: torch.dtype, name: str, dev: int) -> None:
+    """A buffer of at least `numel` dense elements on device `dev`."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on device {dev} (got {t.device})")
+    if t.dtype != dtype or t.numel() < numel or not t.is_contiguous():
+        _buffer(t, numel, dtype, name)
 
 
-def _row_out(row: QuantParams, q, s, rows: int, cols: int, dev):
+def _row_out(row: QuantParams, q, s, rows: int, cols: int, device, dev: int):
     """Codes and scales of a quantized output, allocated or checked."""
     if q is None:
-        q = torch.empty((rows, row.code_cols(cols)), dtype=torch.uint8, device=dev)
+        q = torch.empty((rows, row.code_cols(cols)), dtype=torch.uint8, device=device)
     else:
-        _buffer(q, rows * row.code_cols(cols), torch.uint8, "q")
+        _dense(q, rows * row.code_cols(cols), torch.uint8, "q", dev)
     if s is None:
-        s = _scales_out(rows, cols, row, dev)
+        s = _scales_out(rows, cols, row, device)
     else:
-        _buffer(s, scale_numel(rows, cols, row.block), torch.uint8, "s")
+        _dense(s, scale_numel(rows, cols, row.block), torch.uint8, "s", dev)
     return q, s
 
 
-@_on_its_stream
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def mxfp4_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor | None = None,
                            row: QuantParams | None = None, *, residual: torch.Tensor | None = None,
                            eps: float = 1e-6, y_dtype: torch.dtype | None = None, with_rstd: bool = False,
@@ -586,49 +596,51 @@ def mxfp4_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor | None = None,
     (q, s, y, h, rstd), None for what was not asked for; h comes back when
     there is a residual (or `h` is given; it may be `x` or `residual`
     themselves: updated in place)."""
-    if x.dim() != 2:
-        raise ValueError("x must be 2-D")
+    if stream is not None:
+        return _on(stream, mxfp4_rmsnorm_quantize, x, weight, row, residual=residual, eps=eps, y_dtype=y_dtype,
+                   with_rstd=with_rstd, h=h, y=y, rstd=rstd, q=q, s=s)
+    dev = _device_of(x, "x")
+    device, dtype = x.device, x.dtype
     rows, cols = x.shape
-    dev = x.device
-    ldx, dt = _rows_ld(x, "x", rows, cols), _dtype_of(x, "x")
+    ldx, dt = _rows_ld(x, "x", rows, cols, dev), _dtype_of(x, "x")
     ldr = ldh = ldy = cols
+    px, pr, pw, ph, py, ps = x.data_ptr(), None, None, None, None, None
+    wdt = ydt = DTYPE_F32
     if residual is not None:
-        if residual.dtype != x.dtype:
-            raise TypeError(f"residual must have x's type {x.dtype} (got {residual.dtype})")
-        ldr = _rows_ld(residual, "residual", rows, cols)
+        if residual.dtype != dtype:
+            raise TypeError(f"residual must have x's type {dtype} (got {residual.dtype})")
+        ldr, pr = _rows_ld(residual, "residual", rows, cols, dev), residual.data_ptr()
         if h is None:
-            h = torch.empty((rows, cols), dtype=x.dtype, device=dev)
-    wdt = DTYPE_F32
+            h = torch.empty((rows, cols), dtype=dtype, device=device)
     if weight is not None:
-        _vector(weight, "weight", cols)
-        wdt = _dtype_of(weight, "weight")
+        _vector(weight, "weight", cols, dev)
+        wdt, pw = _dtype_of(weight, "weight"), weight.data_ptr()
     if h is not None:
-        if h.dtype != x.dtype:
-            raise TypeError(f"h must have x's type {x.dtype} (got {h.dtype})")
-        ldh = _rows_ld(h, "h", rows, cols)
+        if h.dtype != dtype:
+            raise TypeError(f"h must have x's type {dtype} (got {h.dtype})")
+        ldh, ph = _rows_ld(h, "h", rows, cols, dev), h.data_ptr()
     if y is None and y_dtype is not None:
-        y = torch.empty((rows, cols), dtype=y_dtype, device=dev)
-    ydt = DTYPE_F32
+        y = torch.empty((rows, cols), dtype=y_dtype, device=device)
     if y is not None:
-        ydt, ldy = _dtype_of(y, "y"), _rows_ld(y, "y", rows, cols)
+        ydt, ldy, py = _dtype_of(y, "y"), _rows_ld(y, "y", rows, cols, dev), y.data_ptr()
     if rstd is not None:
-        _buffer(rstd, rows, torch.float32, "rstd")
+        _dense(rstd, rows, torch.float32, "rstd", dev)
     elif with_rstd:
-        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
-    rp = None
+        rstd = torch.empty(rows, dtype=torch.float32, device=device)
+    if rstd is not None:
+        ps = rstd.data_ptr()
     if row is not None:
-        q, s = _row_out(row, q, s, rows, cols, dev)
-        rp = ctypes.byref(row._c())
+        q, s = _row_out(row, q, s, rows, cols, device, dev)
+        rp, pq, pc = ctypes.byref(row._c()), q.data_ptr(), s.data_ptr()
     else:
-        q = s = None
-    _same_device(x, residual, weight, h, y, rstd, q, s)
-    _check(lib().mxfp4_rmsnorm_quantize(
-        _ptr(x), dt, rows, cols, ldx, _ptr(residual), ldr, _ptr(weight), wdt, eps, _ptr(h), ldh,
-        _ptr(y), ydt, ldy, _ptr(rstd), rp, _ptr(q), _ptr(s), _stream(x, stream)))
+        q = s = rp = pq = pc = None
+    st = lib().mxfp4_rmsnorm_quantize(px, dt, rows, cols, ldx, pr, ldr, pw, wdt, eps, ph, ldh, py, ydt, ldy, ps, rp,
+                                      pq, pc, _raw_stream(dev))
+    if st:
+        _check(st)
     return q, s, y, h, rstd
 
 
-@_on_its_stream
 def mxfp4_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor | None, rstd: torch.Tensor,
                            *, dh: torch.Tensor | None = None, dx=None, dw=None, with_dw: bool = True,
                            workspace=None, stream=None):
@@ -637,106 +649,113 @@ def mxfp4_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tens
     through the residual stream; None: none). dx, in h's type, is the gradient
     of x and of residual alike (it may be dh itself); dw is in weight's type,
     None without a weight or with `with_dw` false."""
-    if h.dim() != 2:
-        raise ValueError("h must be 2-D")
+    if stream is not None:
+        return _on(stream, mxfp4_rmsnorm_backward, dy, h, weight, rstd, dh=dh, dx=dx, dw=dw, with_dw=with_dw,
+                   workspace=workspace)
+    dev = _device_of(h, "h")
+    device, dtype = h.device, h.dtype
     rows, cols = h.shape
-    dev = h.device
-    ldh, hdt = _rows_ld(h, "h", rows, cols), _dtype_of(h, "h")
-    ldy, ydt = _rows_ld(dy, "dy", rows, cols), _dtype_of(dy, "dy")
-    _buffer(rstd, rows, torch.float32, "rstd")
-    ldd = cols
+    ldh, hdt = _rows_ld(h, "h", rows, cols, dev), _dtype_of(h, "h")
+    ldy, ydt = _rows_ld(dy, "dy", rows, cols, dev), _dtype_of(dy, "dy")
+    _dense(rstd, rows, torch.float32, "rstd", dev)
+    ldd = ldx = cols
+    pw = pd = pg = pws = None
     if dh is not None:
-        if dh.dtype != h.dtype:
-            raise TypeError(f"dh must have h's type {h.dtype} (got {dh.dtype})")
-        ldd = _rows_ld(dh, "dh", rows, cols)
+        if dh.dtype != dtype:
+            raise TypeError(f"dh must have h's type {dtype} (got {dh.dtype})")
+        ldd, pd = _rows_ld(dh, "dh", rows, cols, dev), dh.data_ptr()
     if dx is None:
-        dx = torch.empty((rows, cols), dtype=h.dtype, device=dev)
-    elif dx.dtype != h.dtype:
-        raise TypeError(f"dx must have h's type {h.dtype} (got {dx.dtype})")
-    ldx = _rows_ld(dx, "dx", rows, cols)
+        dx = torch.empty((rows, cols), dtype=dtype, device=device)
+    else:
+        if dx.dtype != dtype:
+            raise TypeError(f"dx must have h's type {dtype} (got {dx.dtype})")
+        ldx = _rows_ld(dx, "dx", rows, cols, dev)
     wdt, nbytes = DTYPE_F32, 0
+    L = lib()
     if weight is not None:
-        _vector(weight, "weight", cols)
-        wdt = _dtype_of(weight, "weight")
-        if dw is None and with_dw:
-            dw = torch.empty(cols, dtype=weight.dtype, device=dev)
+        _vector(weight, "weight", cols, dev)
+        wdt, pw = _dtype_of(weight, "weight"), weight.data_ptr()
+        if dw is not None:
+            _dense(dw, cols, weight.dtype, "dw", dev)
+        elif with_dw:
+            dw = torch.empty(cols, dtype=weight.dtype, device=device)
     elif dw is not None:
         raise ValueError("dw needs a weight")
     if dw is not None:
-        _buffer(dw, cols, weight.dtype, "dw")
-        nbytes = int(lib().mxfp4_rmsnorm_backward_workspace_size(rows, cols))
+        nbytes = L.mxfp4_rmsnorm_backward_workspace_size(rows, cols)
         if workspace is None:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
         else:
-            _buffer(workspace, nbytes, torch.uint8, "workspace")
-    _same_device(h, dy, rstd, weight, dh, dx, dw, workspace if dw is not None else None)
-    _check(lib().mxfp4_rmsnorm_backward(
-        _ptr(dy), ydt, ldy, _ptr(h), hdt, ldh, _ptr(weight), wdt, _ptr(rstd), _ptr(dh), ldd, rows, cols,
-        _ptr(dx), ldx, _ptr(dw), _ptr(workspace if dw is not None else None), nbytes, _stream(h, stream)))
+            _dense(workspace, nbytes, torch.uint8, "workspace", dev)
+        pg, pws = dw.data_ptr(), workspace.data_ptr()
+    st = L.mxfp4_rmsnorm_backward(dy.data_ptr(), ydt, ldy, h.data_ptr(), hdt, ldh, pw, wdt, rstd.data_ptr(), pd, ldd,
+                                  rows, cols, dx.data_ptr(), ldx, pg, pws, nbytes, _raw_stream(dev))
+    if st:
+        _check(st)
     return dx, dw
 
 
-@_on_its_stream
 def mxfp4_swiglu_quantize(gate: torch.Tensor, up: torch.Tensor, row: QuantParams | None = None, *,
                           y_dtype: torch.dtype | None = None, y=None, q=None, s=None, stream=None):
     """y = gate / (1 + exp(-gate)) * up, quantized with `row` and/or stored in
     `y_dtype` (or into `y`). gate and up [rows, cols] bf16 or fp32 (one type),
     with any row strides that are multiples of 8. Returns (q, s, y), None for
     what was not asked for."""
-    if gate.dim() != 2:
-        raise ValueError("gate must be 2-D")
+    if stream is not None:
+        return _on(stream, mxfp4_swiglu_quantize, gate, up, row, y_dtype=y_dtype, y=y, q=q, s=s)
+    dev = _device_of(gate, "gate")
+    device = gate.device
     rows, cols = gate.shape
-    dev = gate.device
-    ldg, dt = _rows_ld(gate, "gate", rows, cols), _dtype_of(gate, "gate")
+    ldg, dt = _rows_ld(gate, "gate", rows, cols, dev), _dtype_of(gate, "gate")
     if up.dtype != gate.dtype:
         raise TypeError(f"up must have gate's type {gate.dtype} (got {up.dtype})")
-    ldu = _rows_ld(up, "up", rows, cols)
+    ldu = _rows_ld(up, "up", rows, cols, dev)
     if y is None and y_dtype is not None:
-        y = torch.empty((rows, cols), dtype=y_dtype, device=dev)
-    ydt, ldy = DTYPE_F32, cols
+        y = torch.empty((rows, cols), dtype=y_dtype, device=device)
+    ydt, ldy, py = DTYPE_F32, cols, None
     if y is not None:
-        ydt, ldy = _dtype_of(y, "y"), _rows_ld(y, "y", rows, cols)
-    rp = None
+        ydt, ldy, py = _dtype_of(y, "y"), _rows_ld(y, "y", rows, cols, dev), y.data_ptr()
     if row is not None:
-        q, s = _row_out(row, q, s, rows, cols, dev)
-        rp = ctypes.byref(row._c())
+        q, s = _row_out(row, q, s, rows, cols, device, dev)
+        rp, pq, pc = ctypes.byref(row._c()), q.data_ptr(), s.data_ptr()
     else:
-        q = s = None
-    _same_device(gate, up, y, q, s)
-    _check(lib().mxfp4_swiglu_quantize(_ptr(gate), ldg, _ptr(up), ldu, dt, rows, cols, _ptr(y), ydt, ldy, rp,
-                                       _ptr(q), _ptr(s), _stream(gate, stream)))
+        q = s = rp = pq = pc = None
+    st = lib().mxfp4_swiglu_quantize(gate.data_ptr(), ldg, up.data_ptr(), ldu, dt, rows, cols, py, ydt, ldy, rp, pq,
+                                     pc, _raw_stream(dev))
+    if st:
+        _check(st)
     return q, s, y
 
 
-@_on_its_stream
 def mxfp4_swiglu_backward(dy: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, *, dgate=None, dup=None,
                           stream=None):
     """Gradients (dgate, dup), in gate's type, of mxfp4_swiglu_quantize from dy
     (bf16 or fp32). dgate may be gate itself and dup up itself."""
-    if gate.dim() != 2:
-        raise ValueError("gate must be 2-D")
+    if stream is not None:
+        return _on(stream, mxfp4_swiglu_backward, dy, gate, up, dgate=dgate, dup=dup)
+    dev = _device_of(gate, "gate")
+    dtype = gate.dtype
     rows, cols = gate.shape
-    ldg, dt = _rows_ld(gate, "gate", rows, cols), _dtype_of(gate, "gate")
-    ldu, ldy, ydt = _rows_ld(up, "up", rows, cols), _rows_ld(dy, "dy", rows, cols), _dtype_of(dy, "dy")
+    ldg, dt = _rows_ld(gate, "gate", rows, cols, dev), _dtype_of(gate, "gate")
+    ldu, ldy, ydt = _rows_ld(up, "up", rows, cols, dev), _rows_ld(dy, "dy", rows, cols, dev), _dtype_of(dy, "dy")
     if dgate is None:
-        dgate = torch.empty((rows, cols), dtype=gate.dtype, device=gate.device)
+        dgate = torch.empty((rows, cols), dtype=dtype, device=gate.device)
     if dup is None:
-        dup = torch.empty((rows, cols), dtype=gate.dtype, device=gate.device)
-    for t, n in ((up, "up"), (dgate, "dgate"), (dup, "dup")):
-        if t.dtype != gate.dtype:
-            raise TypeError(f"{n} must have gate's type {gate.dtype} (got {t.dtype})")
-    _same_device(gate, up, dy, dgate, dup)
-    _check(lib().mxfp4_swiglu_backward(
-        _ptr(dy), ydt, ldy, _ptr(gate), ldg, _ptr(up), ldu, dt, rows, cols,
-        _ptr(dgate), _rows_ld(dgate, "dgate", rows, cols), _ptr(dup), _rows_ld(dup, "dup", rows, cols),
-        _stream(gate, stream)))
+        dup = torch.empty((rows, cols), dtype=dtype, device=gate.device)
+    if not up.dtype == dgate.dtype == dup.dtype == dtype:
+        raise TypeError(f"up, dgate and dup must have gate's type {dtype} (got {up.dtype}, {dgate.dtype}, {dup.dtype})")
+    st = lib().mxfp4_swiglu_backward(
+        dy.data_ptr(), ydt, ldy, gate.data_ptr(), ldg, up.data_ptr(), ldu, dt, rows, cols, dgate.data_ptr(),
+        _rows_ld(dgate, "dgate", rows, cols, dev), dup.data_ptr(), _rows_ld(dup, "dup", rows, cols, dev),
+        _raw_stream(dev))
+    if st:
+        _check(st)
     return dgate, dup
 
 
 _GEMV_CODES = {FORMAT_E4M3: 1, FORMAT_E5M2: 2}     # MXFP4_GEMV_X_*; bf16 is 0
 
 
-@_on_its_stream
 def mxfp4_gemv(x: torch.Tensor, qw: torch.Tensor, sw: torch.Tensor, N: int, K: int,
                w: QuantParams | None = None, *, sx: torch.Tensor | None = None, x_format: int = FORMAT_E4M3,
                out_dtype: torch.dtype = torch.bfloat16, y=None, stream=None):
@@ -747,34 +766,39 @@ def mxfp4_gemv(x: torch.Tensor, qw: torch.Tensor, sw: torch.Tensor, N: int, K: i
     x is bf16, or uint8 codes of `x_format` (FORMAT_E4M3 / FORMAT_E5M2) with
     row-major E8M0 scales sx [M, K/32], as the quantized norm and activation
     write them. y in out_dtype (or y's own: bf16 or fp32)."""
+    if stream is not None:
+        return _on(stream, mxfp4_gemv, x, qw, sw, N, K, w, sx=sx, x_format=x_format, out_dtype=out_dtype, y=y)
     w = QuantParams() if w is None else w
     if w.elem_format != FORMAT_E2M1:
         raise ValueError("the weights must be 4-bit (E2M1) codes")
-    if x.dim() != 2:
-        raise ValueError("x must be 2-D")
+    dev = _device_of(x, "x")
     M = x.shape[0]
-    ldx = _rows_ld(x, "x", M, K)
+    ldx = _rows_ld(x, "x", M, K, dev)
+    kind, psx = 0, None
     if x.dtype == torch.bfloat16:
         if sx is not None:
             raise ValueError("sx goes with one-byte codes; x is bfloat16")
-        kind = 0
     elif x.dtype == torch.uint8:
         if sx is None:
             raise ValueError("one-byte codes need their scales sx")
-        if x_format not in _GEMV_CODES:
+        kind = _GEMV_CODES.get(x_format)
+        if kind is None:
             raise ValueError(f"x_format {x_format} is not E4M3 or E5M2")
-        _buffer(sx, M * (K // 32), torch.uint8, "sx")
-        kind = _GEMV_CODES[x_format]
+        _dense(sx, M * (K // 32), torch.uint8, "sx", dev)
+        psx = sx.data_ptr()
     else:
         raise TypeError(f"x must be bfloat16 or uint8 codes (got {x.dtype})")
-    _buffer(qw, N * K // 2, torch.uint8, "qw")
-    _buffer(sw, scale_numel(N, K, w.block), torch.uint8, "sw")
+    _dense(qw, N * K // 2, torch.uint8, "qw", dev)
+    _dense(sw, scale_numel(N, K, w.block), torch.uint8, "sw", dev)
+    ldy = N
     if y is None:
         y = torch.empty((M, N), dtype=out_dtype, device=x.device)
-    ydt, ldy = _dtype_of(y, "y"), _rows_ld(y, "y", M, N)
-    _same_device(x, sx, qw, sw, y)
-    _check(lib().mxfp4_gemv(_ptr(x), kind, ldx, _ptr(sx), _ptr(qw), _ptr(sw), w.block, w.scale_layout,
-                            w.tensor_exp, M, N, K, _ptr(y), ydt, ldy, _stream(x, stream)))
+    else:
+        ldy = _rows_ld(y, "y", M, N, dev)
+    st = lib().mxfp4_gemv(x.data_ptr(), kind, ldx, psx, qw.data_ptr(), sw.data_ptr(), w.block, w.scale_layout,
+                          w.tensor_exp, M, N, K, y.data_ptr(), _dtype_of(y, "y"), ldy, _raw_stream(dev))
+    if st:
+        _check(st)
     return y
 
 
