@@ -80,13 +80,13 @@ static_assert(sizeof(Ctl) <= 256, "control block");
 
 // Bounded wait (about 2 s): on expiry the CTA stops issuing work and the
 // library's device error word is set.
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, Ctl* ctl) {
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint32_t* abort) {
   if (ptx::mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = ptx::globaltimer_ns();
   while (!ptx::mbar_try_wait_sleep(bar, parity, 100000u)) {
-    if (*reinterpret_cast<volatile uint32_t*>(&ctl->abort)) return false;
+    if (*reinterpret_cast<volatile uint32_t*>(abort)) return false;
     if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
-      *reinterpret_cast<volatile uint32_t*>(&ctl->abort) = 1u;
+      *reinterpret_cast<volatile uint32_t*>(abort) = 1u;
       atomicExch(&g_gemv_error, 6u);  // MXFP4_ERR_TIMEOUT
       return false;
     }
@@ -242,13 +242,95 @@ __device__ __forceinline__ void convert_sw(const GemvArgs& a, int groups, int64_
     *reinterpret_cast<uint4*>(sws + c * 512 + lane * 16) = make_uint4(v[c][0], v[c][1], v[c][2], v[c][3]);
 }
 
+// The producer thread: stages s0 .. s1 - 1 of the CTA's codes by TMA, and
+// tensor-core scale tiles (two row tiles of them where the CTA's rows span two)
+// as they lie in memory, into rings of ST slots.
+template <bool NV, int ST>
+__device__ void produce(const CUtensorMap& tm, const GemvArgs& a, int64_t n0, int rows, int s0, int s1, uint8_t* ws,
+                        uint8_t* sws, uint32_t full, uint32_t empty, uint32_t* abort) {
+  constexpr int kPer = NV ? 16 : 32, kTile = kRows * kStageK / kPer;
+  const int64_t cols = a.K / kPer, tile0 = n0 >> 7, tiles = ((n0 + rows - 1) >> 7) - tile0 + 1;
+  const int64_t last = (a.N >> 7) - 1;  // the scale array's last row tile
+  int i = 0, s = s0;
+  uint32_t round = 0;
+  for (; s < s1; ++s) {
+    if (round && !wait_bar(empty + 8 * i, (round - 1) & 1, abort)) break;
+    uint32_t bytes = (uint32_t)rows * kRowBytes, sb = 0;
+    const int64_t c0 = (int64_t)s * (kStageK / kPer);
+    if (a.mma) {
+      sb = (uint32_t)min((int64_t)kTile, (cols - c0) * kRows);
+      bytes += sb * (uint32_t)tiles;
+    }
+    ptx::mbar_arrive_expect_tx(full + 8 * i, bytes);
+    ptx::tma_load_2d(ptx::smem_u32(ws + i * kWBytes), &tm, s * kRowBytes, (int32_t)n0, full + 8 * i);
+    if (a.mma)
+      for (int64_t j = 0; j < tiles; ++j)
+        ptx::bulk_load(ptx::smem_u32(sws + (2 * i + j) * kTile),
+                       a.sw + min(tile0 + j, last) * 128 * cols + c0 * kRows, sb, full + 8 * i);
+    if (++i == ST) {
+      i = 0;
+      ++round;
+    }
+  }
+  // after an abort: the last load into each slot lands (bounded wait) before the CTA's memory goes
+  if (*reinterpret_cast<volatile uint32_t*>(abort)) {
+    const int issued = s - s0;
+    for (int r = issued > ST ? issued - ST : 0; r < issued; ++r) {
+      const uint64_t t0 = ptx::globaltimer_ns();
+      while (!ptx::mbar_try_wait(full + 8 * (uint32_t)(r % ST), (uint32_t)(r / ST) & 1) &&
+             ptx::globaltimer_ns() - t0 < kWaitLimitNs / 10) {
+      }
+    }
+  }
+}
+
+// The CTA's sums, `planes` of them [token][ld] a plane apart in its shared
+// memory, and those of the cluster's other slices of K, added in fixed order
+// and stored. Every thread of the CTA calls it, the planes written and visible.
+__device__ __forceinline__ void finish(const GemvArgs& a, float* red, int ld, int plane, int planes, int rows,
+                                       int tokens, int rank, int splits, int64_t n0, int64_t m0, float factor,
+                                       bool ok) {
+  const int total = tokens * rows;
+  if (splits > 1) {
+    if (ok && planes > 1)
+      for (int e = threadIdx.x; e < total; e += blockDim.x) {
+        float* d = red + e / rows * ld + e % rows;
+        *d = __fadd_rn(d[0], d[plane]);
+      }
+    __syncwarp();
+    ptx::cluster_sync();
+  }
+  if (ok) {
+    for (int e = total * rank / splits + threadIdx.x; e < total * (rank + 1) / splits; e += blockDim.x) {
+      const int m = e / rows, r = e % rows;
+      const int64_t n = n0 + r;
+      if (n >= a.N) continue;
+      const float* d = red + m * ld + r;
+      float v = 0.0f;
+      if (splits == 1) {
+        v = planes > 1 ? __fadd_rn(d[0], d[plane]) : d[0];
+      } else {
+        const uint32_t at = ptx::smem_u32(d);
+        for (int c = 0; c < splits; ++c) v = __fadd_rn(v, lds_cluster(ptx::mapa(at, (uint32_t)c)));
+      }
+      v = __fmul_rn(v, factor);
+      const int64_t o = (m0 + m) * a.ld_y + n;
+      if (a.y_f32)
+        put_at(static_cast<float*>(a.y) + o, v, a.y, a.y_bytes);
+      else
+        put_at(static_cast<uint16_t*>(a.y) + o, (uint16_t)bf16x2(v, 0.0f), a.y, a.y_bytes);
+    }
+  }
+  __syncwarp();
+  if (splits > 1) ptx::cluster_sync();  // peers read this CTA's sums until here
+}
+
 template <int NT, bool NV>
 __global__ void __launch_bounds__(kThreads, NT == 4 ? 1 : 2)
 gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int groups, const int splits) {
   constexpr int TT = 8 * NT;
   using S = Smem<TT, NV>;
   constexpr int ST = S::kStages;
-  constexpr int kPer = NV ? 16 : 32;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const base = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t *const ws = base, *const xs = ws + ST * kWBytes, *const sws = xs + ST * S::kX;
@@ -284,49 +366,14 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
   const int g = lane >> 2, t = lane & 3, part = warp / groups, wr = warp - part * groups;
 
   if (warp == kMmaWarps) {
-    // ---- producer: codes by TMA, tensor-core scales as they lie in memory
-    if (lane == 0) {
-      const int64_t cols = a.K / kPer, tile0 = n0 >> 7, tiles = ((n0 + rows - 1) >> 7) - tile0 + 1;
-      const int64_t last = (a.N >> 7) - 1;               // the scale array's last row tile
-      int i = 0, s = s0;
-      uint32_t round = 0;
-      for (; s < s1; ++s) {
-        if (round && !wait_bar(empty + 8 * i, (round - 1) & 1, ctl)) break;
-        uint32_t bytes = (uint32_t)rows * kRowBytes, sb = 0;
-        const int64_t c0 = (int64_t)s * (kStageK / kPer);
-        if (a.mma) {
-          sb = (uint32_t)min((int64_t)(S::kSw / 2), (cols - c0) * kRows);
-          bytes += sb * (uint32_t)tiles;
-        }
-        ptx::mbar_arrive_expect_tx(full_w + 8 * i, bytes);
-        ptx::tma_load_2d(ptx::smem_u32(ws + i * kWBytes), &tm, s * kRowBytes, (int32_t)n0, full_w + 8 * i);
-        if (a.mma)
-          for (int64_t j = 0; j < tiles; ++j)
-            ptx::bulk_load(ptx::smem_u32(sws + i * S::kSw + j * (S::kSw / 2)),
-                           a.sw + min(tile0 + j, last) * 128 * cols + c0 * kRows, sb, full_w + 8 * i);
-        if (++i == ST) {
-          i = 0;
-          ++round;
-        }
-      }
-      // after an abort: the last load into each slot lands (bounded wait) before the CTA's memory goes
-      if (*reinterpret_cast<volatile uint32_t*>(&ctl->abort)) {
-        const int issued = s - s0;
-        for (int r = issued > ST ? issued - ST : 0; r < issued; ++r) {
-          const uint64_t t0 = ptx::globaltimer_ns();
-          while (!ptx::mbar_try_wait(full_w + 8 * (uint32_t)(r % ST), (uint32_t)(r / ST) & 1) &&
-                 ptx::globaltimer_ns() - t0 < kWaitLimitNs / 10) {
-          }
-        }
-      }
-    }
+    if (lane == 0) produce<NV, ST>(tm, a, n0, rows, s0, s1, ws, sws, full_w, empty, &ctl->abort);
     __syncwarp();
   } else if (warp > kMmaWarps) {
     // ---- converters: whole stages in turn
     for (int s = s0 + (warp - kMmaWarps - 1); s < s1; s += kConvWarps) {
       const int i = (s - s0) % ST;
       const uint32_t round = (uint32_t)((s - s0) / ST);
-      if (round && !wait_bar(empty + 8 * i, (round - 1) & 1, ctl)) break;
+      if (round && !wait_bar(empty + 8 * i, (round - 1) & 1, &ctl->abort)) break;
       const int64_t k0 = (int64_t)s * kStageK;
       if (!a.mma) convert_sw<NV>(a, groups, n0, k0, lane, sws + i * S::kSw);
       convert_x<TT>(a, m0, tokens, k0, lane, xs + i * S::kX, sxs + i * (S::kSx / 4));
@@ -348,7 +395,10 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
     int i = 0;
     uint32_t parity = 0;
     for (int s = s0; s < s1; ++s) {
-      if (!wait_bar(full_w + 8 * i, parity, ctl) || !wait_bar(full_x + 8 * i, parity, ctl)) break;
+      // the whole warp leaves the wait together: lanes that saw the phase end at different polls would
+      // go through the products below in parts
+      const bool in = wait_bar(full_w + 8 * i, parity, &ctl->abort) && wait_bar(full_x + 8 * i, parity, &ctl->abort);
+      if (!__all_sync(0xffffffffu, in)) break;
       const bool live = s * kBlocks + 4 * part < (int)(a.K >> 5);
       const uint8_t *w = ws + i * kWBytes, *x = xs + i * S::kX + xoff, *sw = sws + i * S::kSw + swoff;
       const float* sx = sxs + i * (S::kSx / 4) + sxoff;
@@ -397,6 +447,9 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
           }
         }
       }
+      // The loads above have to be done before the slot goes back to the producer. The arrival alone
+      // did not keep the last block's behind it in compiled code (slots were refilled under them).
+      __threadfence_block();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(empty + 8 * i);
       if (++i == ST) {
@@ -424,65 +477,307 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
         }
   }
   __syncthreads();
-  const int total = tokens * rows;
-  if (splits > 1) {
-    if (ok)
-      for (int e = threadIdx.x; e < total; e += kThreads) {
-        float* d = red + e / rows * ld + e % rows;
-        *d = __fadd_rn(d[0], d[plane]);
-      }
-    __syncwarp();
-    ptx::cluster_sync();
-  }
-  if (ok) {
-    for (int e = total * rank / splits + threadIdx.x; e < total * (rank + 1) / splits; e += kThreads) {
-      const int m = e / rows, r = e % rows;
-      const int64_t n = n0 + r;
-      if (n >= a.N) continue;
-      const float* d = red + m * ld + r;
-      float v = 0.0f;
-      if (splits == 1) {
-        v = __fadd_rn(d[0], d[plane]);
-      } else {
-        const uint32_t at = ptx::smem_u32(d);
-        for (int c = 0; c < splits; ++c) v = __fadd_rn(v, lds_cluster(ptx::mapa(at, (uint32_t)c)));
-      }
-      if (NV) v = __fmul_rn(v, a.p2k);
-      const int64_t o = (m0 + m) * a.ld_y + n;
-      if (a.y_f32)
-        put_at(static_cast<float*>(a.y) + o, v, a.y, a.y_bytes);
-      else
-        put_at(static_cast<uint16_t*>(a.y) + o, (uint16_t)bf16x2(v, 0.0f), a.y, a.y_bytes);
-    }
-  }
-  __syncwarp();
-  if (splits > 1) ptx::cluster_sync();  // peers read this CTA's sums until here
+  finish(a, red, ld, plane, kParts, rows, tokens, rank, splits, n0, m0, NV ? a.p2k : 1.0f, ok);
 }
 
-template <int NT, bool NV>
-cudaError_t launch(const GemvArgs& a, int groups, int splits, cudaStream_t st) {
-  constexpr int bytes = Smem<8 * NT, NV>::kBytes;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  {
-    static bool set[kMaxDevices] = {};
-    static std::mutex mu;
-    std::lock_guard<std::mutex> lock(mu);
-    if (!set[dev]) {
-      e = cudaFuncSetAttribute(gemv_kernel<NT, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-      if (e != cudaSuccess) return e;
-      set[dev] = true;
+// ---------------------------------------------------- more rows of x ---
+// Above eight rows the products of mma.sync and their operands' reads grow with
+// the rows; here the weights become bf16 once, in shared memory, and tcgen05
+// multiplies them with up to 64 rows of x for one instruction's issue:
+//  * 128 rows of W are the M of the instruction, the rows of x its N; x goes in
+//    as bf16 (E4M3 and E5M2 codes times their factor are exact in bf16), so
+//    both operands are exact and the sums fp32, in tensor memory;
+//  * eight warps turn codes into bf16: a code's three magnitude bits, moved to
+//    bits 8..6 of a bf16 word, are the subnormal that is 2^-126 times its value
+//    (zero and the half included), so one packed product with 2^126 times the
+//    block's scale gives code x scale exactly. Scales above 2 (E8M0) take a
+//    second product; NVFP4's scales go in 2^-26 smaller, which the end undoes;
+//  * the pairs that one word of codes gives are elements (i, i + 4) of its
+//    eight: x is laid down in the same order instead of reordering W.
+// Bound by the conversion's issue slots (about 3 instructions a weight), which
+// the number of rows does not change.
+constexpr int kTcTokens = 32;
+constexpr int kTcStages = 3;                // of kStageK
+constexpr int kTcK = 64;                    // K per tensor-core buffer
+constexpr int kTcBufs = 2, kTcBufsX = 4;    // of the weights, of x
+constexpr int kTcDeq = 8, kTcConv = 4;      // converting warps: weights, x
+// Sums kept in tensor memory, the buffers in turn, added at the end: the
+// tensor cores round every K = 16 step of a sum toward zero, so one sum over
+// all of K drifts by up to K / 16 units of its last place (measured: 1.1e-5 of
+// sum |x w| at K = 16384), and eight drift by an eighth of that.
+constexpr int kTcSums = 8;
+constexpr int kTcThreads = (kTcDeq + 2 + kTcConv) * 32;
+constexpr int kTcA = kRows * kTcK * 2, kTcB = kTcTokens * kTcK * 2;
+
+struct TcCtl {
+  uint64_t full_w[kTcStages], empty_w[kTcStages], full_a[kTcBufs], empty_a[kTcBufs], full_b[kTcBufsX],
+      empty_b[kTcBufsX], acc_full;
+  uint32_t tmem, abort;
+};
+
+template <bool NV>
+constexpr int tc_smem() {
+  return kTcBufs * kTcA + kTcBufsX * kTcB + kTcStages * (kWBytes + 2 * kRows * kStageK / (NV ? 16 : 32)) + (int)sizeof(TcCtl) +
+         1024;
+}
+
+__device__ __forceinline__ uint32_t hmul2_bf16(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Eight codes to bf16 pairs (0, 4), (1, 5), (2, 6), (3, 7) of 2^-126 times their values.
+__device__ __forceinline__ void e2m1x8_bf16_tiny(uint32_t v, uint32_t (&r)[4]) {
+  r[0] = ((v << 12) & 0x80008000u) | ((v << 6) & 0x01C001C0u);
+  r[1] = ((v << 8) & 0x80008000u) | ((v << 2) & 0x01C001C0u);
+  r[2] = ((v << 4) & 0x80008000u) | ((v >> 2) & 0x01C001C0u);
+  r[3] = (v & 0x80008000u) | ((v >> 6) & 0x01C001C0u);
+}
+
+template <bool NV>
+__global__ void __launch_bounds__(kTcThreads, 2)
+gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int splits) {
+  constexpr int kPer = NV ? 16 : 32, kTile = kRows * kStageK / kPer;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const base = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t *const ws = base, *const as = ws + kTcStages * kWBytes, *const bs = as + kTcBufs * kTcA,
+                 *const sws = bs + kTcBufsX * kTcB;
+  TcCtl* const ctl = reinterpret_cast<TcCtl*>(sws + kTcStages * 2 * kTile);
+  const uint32_t full_w = ptx::smem_u32(ctl->full_w), empty_w = ptx::smem_u32(ctl->empty_w),
+                 full_a = ptx::smem_u32(ctl->full_a), empty_a = ptx::smem_u32(ctl->empty_a),
+                 full_b = ptx::smem_u32(ctl->full_b), empty_b = ptx::smem_u32(ctl->empty_b),
+                 acc_full = ptx::smem_u32(&ctl->acc_full);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)(blockIdx.x % (unsigned)splits);
+  const int64_t n0 = (int64_t)(blockIdx.x / (unsigned)splits) * kRows, m0 = (int64_t)blockIdx.y * kTcTokens;
+  const int tokens = (int)min((int64_t)kTcTokens, a.M - m0), cols_n = (tokens + 15) & ~15;
+  const int stages = (int)((a.K + kStageK - 1) / kStageK);
+  const int s0 = (int)((int64_t)stages * rank / splits), s1 = (int)((int64_t)stages * (rank + 1) / splits);
+  // buffers of kTcK that hold anything (the last stage may be short)
+  const int bufs = (int)min((int64_t)(s1 - s0) * (kStageK / kTcK), (a.K - (int64_t)s0 * kStageK + kTcK - 1) / kTcK);
+
+  if (threadIdx.x == 0) {
+    ptx::prefetch_tensormap(&tm);
+    for (int i = 0; i < kTcStages; ++i) {
+      ptx::mbar_init(full_w + 8 * i, 1);
+      ptx::mbar_init(empty_w + 8 * i, kTcDeq);
+    }
+    for (int i = 0; i < kTcBufs; ++i) {
+      ptx::mbar_init(full_a + 8 * i, kTcDeq);
+      ptx::mbar_init(empty_a + 8 * i, 1);
+    }
+    for (int i = 0; i < kTcBufsX; ++i) {
+      ptx::mbar_init(full_b + 8 * i, 1);
+      ptx::mbar_init(empty_b + 8 * i, 1);
+    }
+    ptx::mbar_init(acc_full, 1);
+    ctl->abort = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == kTcDeq + 1) {
+    ptx::tmem_alloc(ptx::smem_u32(&ctl->tmem), kTcSums * kTcTokens);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = ctl->tmem;
+
+  if (warp == kTcDeq) {
+    if (lane == 0) produce<NV, kTcStages>(tm, a, n0, kRows, s0, s1, ws, sws, full_w, empty_w, &ctl->abort);
+    __syncwarp();
+  } else if (warp == kTcDeq + 1) {
+    // ---- the thread that issues the products
+    if (lane == 0) {
+      // bf16 operands (1 at bits 7 and 10), fp32 sums (1 at bit 4), K-major, N / 8 and M / 16
+      const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(cols_n >> 3) << 17) | ((kRows >> 4) << 24);
+      for (int b = 0; b < bufs; ++b) {
+        const int i = b % kTcBufs, ix = b % kTcBufsX;
+        if (!wait_bar(full_a + 8 * i, (uint32_t)(b / kTcBufs) & 1, &ctl->abort) ||
+            !wait_bar(full_b + 8 * ix, (uint32_t)(b / kTcBufsX) & 1, &ctl->abort))
+          break;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < kTcK / 16; ++k)
+          ptx::mma_f16(tmem + (b % kTcSums) * kTcTokens, ptx::smem_desc(ptx::smem_u32(as + i * kTcA) + k * 32, 16, 1024, 2),
+                       ptx::smem_desc(ptx::smem_u32(bs + ix * kTcB) + k * 32, 16, 1024, 2), idesc, b >= kTcSums || k != 0);
+        ptx::tc_commit(empty_a + 8 * i);
+        ptx::tc_commit(empty_b + 8 * ix);
+      }
+      // completes when the products issued so far have: nothing reads shared or
+      // writes tensor memory past it, after an abort either (bounded wait there)
+      ptx::tc_commit(acc_full);
+      const uint64_t t0 = ptx::globaltimer_ns();
+      while (!ptx::mbar_try_wait(acc_full, 0) && ptx::globaltimer_ns() - t0 < kWaitLimitNs / 10) {
+      }
+    }
+    __syncwarp();
+  } else if (warp > kTcDeq + 1) {
+    // ---- x: whole buffers in turn, a lane eight elements (16 bytes of bf16) of every fourth row,
+    // in the weights' order. A buffer's loads are all in flight before its slot is waited for.
+    const int c = lane & 7;
+    for (int b = warp - kTcDeq - 2; b < bufs; b += kTcConv) {
+      const int i = b % kTcBufsX;
+      const uint32_t round = (uint32_t)(b / kTcBufsX);
+      const int64_t k = (int64_t)s0 * kStageK + (int64_t)b * kTcK + 8 * c;
+      const bool live = k < a.K;
+      uint4 w[kTcTokens / 4];  // bf16 pairs (0, 1), (2, 3), (4, 5), (6, 7); or codes and their scale
+#pragma unroll
+      for (int e = 0; e < kTcTokens / 4; ++e) {
+        const int64_t m = m0 + 4 * e + (lane >> 3);
+        w[e] = make_uint4(0, 0, 0, 0);
+        if (!live || m >= m0 + tokens) continue;
+        if (a.x_kind == GemvArgs::kXBf16) {
+          w[e] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + m * a.ld_x + k));
+        } else {
+          const uint2 q = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.x) + m * a.ld_x + k));
+          w[e] = make_uint4(q.x, q.y, __ldg(a.sx + m * (a.K >> 5) + (k >> 5)), 0);
+        }
+      }
+      if (round && !wait_bar(empty_b + 8 * i, (round - 1) & 1, &ctl->abort)) break;
+#pragma unroll
+      for (int e = 0; e < kTcTokens / 4; ++e) {
+        const int m = 4 * e + (lane >> 3);
+        if (4 * e >= tokens) break;
+        if (a.x_kind != GemvArgs::kXBf16) {
+          const float f = __uint_as_float(e8m0x2_bf16x2(w[e].z) << 16);
+          const bool e5 = a.x_kind == GemvArgs::kXE5m2;
+          uint32_t h[4] = {w[e].x, w[e].x >> 16, w[e].y, w[e].y >> 16};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            h[j] = e5 ? e5m2x2_f16x2(h[j]) : e4m3x2_f16x2(h[j]);
+            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+            h[j] = bf16x2(__fmul_rn(v.x, f), __fmul_rn(v.y, f));
+          }
+          w[e] = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+        *reinterpret_cast<uint4*>(bs + i * kTcB + m * 128 + ((c ^ (m & 7)) << 4)) =
+            make_uint4(__byte_perm(w[e].x, w[e].z, 0x5410), __byte_perm(w[e].x, w[e].z, 0x7632),
+                       __byte_perm(w[e].y, w[e].w, 0x5410), __byte_perm(w[e].y, w[e].w, 0x7632));
+      }
+      ptx::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(full_b + 8 * i);
+    }
+  } else {
+    // ---- weights: a thread has one row and one of a buffer's two 32-blocks
+    constexpr int kWords = NV ? 4 : 2;  // of a row's scales in a stage
+    const int r = threadIdx.x & 127, half = threadIdx.x >> 7;
+    const int64_t cols = a.K / kPer;
+    const uint8_t* row_sw = a.sw + min(n0 + r, a.N - 1) * cols;  // row-major scales
+    uint32_t sc[kWords] = {}, ahead[kWords] = {};
+    auto fetch = [&](int s) {  // row-major scales of stage s
+      const int64_t c0 = (int64_t)s * (kStageK / kPer);
+#pragma unroll
+      for (int e = 0; e < kWords; ++e) {
+        ahead[e] = 0;
+        if ((cols & 3) == 0) {
+          if (c0 + 4 * e < cols) ahead[e] = __ldg(reinterpret_cast<const uint32_t*>(row_sw + c0) + e);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (c0 + 4 * e + q < cols) ahead[e] |= (uint32_t)__ldg(row_sw + c0 + 4 * e + q) << (8 * q);
+        }
+      }
+    };
+    if (!a.mma) fetch(s0);
+    bool go = true;
+    for (int st = 0; go && st < s1 - s0; ++st) {
+      const int slot = st % kTcStages;
+      if (!a.mma) {
+#pragma unroll
+        for (int e = 0; e < kWords; ++e) sc[e] = ahead[e];
+        if (st + 1 < s1 - s0) fetch(s0 + st + 1);
+      }
+      if (!wait_bar(full_w + 8 * slot, (uint32_t)(st / kTcStages) & 1, &ctl->abort)) break;
+      if (a.mma) {
+        const int live = (int)min((int64_t)kWords, (cols - (int64_t)(s0 + st) * (kStageK / kPer)) / 4);
+#pragma unroll
+        for (int e = 0; e < kWords; ++e)  // words past K were not copied
+          sc[e] = e < live ? *reinterpret_cast<const uint32_t*>(sws + slot * 2 * kTile + e * 512 + (r & 31) * 16 + (r >> 5) * 4)
+                           : 0u;
+      }
+#pragma unroll
+      for (int j = 0; j < kStageK / kTcK; ++j) {
+        const int b = st * (kStageK / kTcK) + j, i = j % kTcBufs;
+        if (b >= bufs) break;
+        const uint32_t round = (uint32_t)(b / kTcBufs);
+        const uint4 v = *reinterpret_cast<const uint4*>(ws + slot * kWBytes + r * kRowBytes + (((2 * j + half) ^ (r & 7)) << 4));
+        uint32_t f0, f1, g = 0;  // factors of the two halves of the block; second factor (E8M0 above 2)
+        if (NV) {
+          const uint32_t h = e4m3x2_f16x2(sc[j] >> (16 * half));
+          const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&h));
+          f0 = bf16x2(q.x * 0x1p100f, q.x * 0x1p100f);
+          f1 = bf16x2(q.y * 0x1p100f, q.y * 0x1p100f);
+        } else {
+          // 2^126 2^(c - 127), in two factors above 2^127
+          const uint32_t c = (sc[j >> 1] >> (16 * (j & 1) + 8 * half)) & 0xFFu;
+          f0 = c <= 128u ? (c + 126u) << 7 : c == 255u ? 0x7FC0u : 254u << 7;
+          g = c <= 128u || c == 255u ? 0u : (c - 1u) << 7;
+          f0 |= f0 << 16;
+          g |= g << 16;
+          f1 = f0;
+        }
+        if (round && !(go = wait_bar(empty_a + 8 * i, (round - 1) & 1, &ctl->abort))) break;
+        uint8_t* dst = as + i * kTcA + r * 128;
+        const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t q[4];
+          e2m1x8_bf16_tiny(words[w], q);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) q[e] = hmul2_bf16(q[e], w < 2 ? f0 : f1);
+          if (!NV && g) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) q[e] = hmul2_bf16(q[e], g);
+          }
+          *reinterpret_cast<uint4*>(dst + (((4 * half + w) ^ (r & 7)) << 4)) = make_uint4(q[0], q[1], q[2], q[3]);
+        }
+        ptx::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(full_a + 8 * i);
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(empty_w + 8 * slot);
     }
   }
-  CUtensorMap tm;
-  if (!make_tma_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.qw, a.N, a.K / 2, a.K / 2, 32 * groups, kRowBytes))
-    return cudaErrorInvalidValue;
+
+  // ---- the sums leave tensor memory: warp w has rows 32 w .. 32 w + 31
+  float* const red = reinterpret_cast<float*>(ws);  // [token][132], in place of the codes
+  constexpr int ld = kRows + 4;
+  __syncthreads();  // the issuing thread has seen its last product complete (or the CTA has aborted)
+  const bool ok = *reinterpret_cast<volatile uint32_t*>(&ctl->abort) == 0;
+  ptx::tc_fence_after();
+  if (warp < 4) {
+    for (int c = 0; c < cols_n; c += 16) {
+      float f[16] = {};
+      for (int j = 0; j < kTcSums && j < bufs; ++j) {
+        uint32_t v[16];
+        ptx::tmem_ld_32x32b_x16(tmem + ((uint32_t)(32 * warp) << 16) + j * kTcTokens + c, v);
+        ptx::tc_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) f[e] = __fadd_rn(f[e], __uint_as_float(v[e]));
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) red[(c + e) * ld + 32 * warp + lane] = f[e];
+    }
+    ptx::tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == kTcDeq + 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kTcSums * kTcTokens);
+  }
+  finish(a, red, ld, 0, 1, kRows, tokens, rank, splits, n0, m0, NV ? a.p2k * 0x1p26f : 1.0f, ok);
+}
+
+template <typename... P, typename... Q>
+cudaError_t launch_cluster(void (*kernel)(P...), dim3 grid, int threads, int bytes, int splits, cudaStream_t st,
+                           Q... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.N + 32 * groups - 1) / (32 * groups)) * (unsigned)splits,
-                     (unsigned)((a.M + kMaxTokens - 1) / kMaxTokens));
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -492,7 +787,50 @@ cudaError_t launch(const GemvArgs& a, int groups, int splits, cudaStream_t st) {
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = splits > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, gemv_kernel<NT, NV>, tm, a, groups, splits);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Lets a kernel use `bytes` of dynamic shared memory, once per device.
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, bool (&set)[kMaxDevices]) {
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(mu);
+  if (set[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  set[dev] = e == cudaSuccess;
+  return e;
+}
+
+bool codes_map(CUtensorMap* tm, const GemvArgs& a, int rows) {
+  return make_tma_2d(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.qw, a.N, a.K / 2, a.K / 2, rows, kRowBytes);
+}
+
+template <int NT, bool NV>
+cudaError_t launch(const GemvArgs& a, int groups, int splits, cudaStream_t st) {
+  constexpr int bytes = Smem<8 * NT, NV>::kBytes;
+  static bool set[kMaxDevices] = {};
+  if (cudaError_t e = allow_smem(gemv_kernel<NT, NV>, bytes, set)) return e;
+  CUtensorMap tm;
+  if (!codes_map(&tm, a, 32 * groups)) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)((a.N + 32 * groups - 1) / (32 * groups)) * (unsigned)splits,
+                  (unsigned)((a.M + kMaxTokens - 1) / kMaxTokens));
+  return launch_cluster(gemv_kernel<NT, NV>, grid, kThreads, bytes, splits, st, tm, a, groups, splits);
+}
+
+template <bool NV>
+cudaError_t launch_tc(const GemvArgs& a, int splits, cudaStream_t st) {
+  constexpr int bytes = tc_smem<NV>();
+  static bool set[kMaxDevices] = {};
+  if (cudaError_t e = allow_smem(gemv_tc_kernel<NV>, bytes, set)) return e;
+  CUtensorMap tm;
+  if (!codes_map(&tm, a, kRows)) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)((a.N + kRows - 1) / kRows) * (unsigned)splits,
+                  (unsigned)((a.M + kTcTokens - 1) / kTcTokens));
+  return launch_cluster(gemv_tc_kernel<NV>, grid, kTcThreads, bytes, splits, st, tm, a, splits);
 }
 
 }  // namespace
@@ -515,9 +853,14 @@ cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t st) {
                         (2 * tiles * splits <= 3 * kSms && 32 * splits <= stages)))
     splits *= 2;
 #ifdef GEMV_TUNE
+  if (getenv("GEMV_TC") && atoi(getenv("GEMV_TC"))) {
+    splits = atoi(getenv("GEMV_S"));
+    return a.nv ? launch_tc<true>(a, splits, st) : launch_tc<false>(a, splits, st);
+  }
   if (getenv("GEMV_R")) groups = atoi(getenv("GEMV_R"));
   if (getenv("GEMV_S")) splits = atoi(getenv("GEMV_S"));
 #endif
+  if (a.M > 8) return a.nv ? launch_tc<true>(a, splits, st) : launch_tc<false>(a, splits, st);
   if (a.nv)
     return nt == 1 ? launch<1, true>(a, groups, splits, st)
                    : nt == 2 ? launch<2, true>(a, groups, splits, st) : launch<4, true>(a, groups, splits, st);

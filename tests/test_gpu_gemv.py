@@ -209,6 +209,27 @@ def test_strides_and_guard_bytes(M, N, K, dt):
     a.check(f"gemv {M}x{N}x{K}")
 
 
+@pytest.mark.parametrize("M,nv,layout", [(1, False, 0), (2, False, 0), (8, True, 0), (3, False, 1), (12, False, 0),
+                                         (32, True, 0), (20, False, 1)])
+def test_every_stage_of_a_long_sum_on_every_run(M, nv, layout):
+    """Long K, many CTAs, many runs: a slot of a kernel's ring that is refilled
+    under its readers shows as an element of another stage."""
+    import gemm_pt_block_gb300 as mx
+
+    N, K = 28672, 16384
+    q, s, _ = weights(N, K, nv, 25, 120, 124)
+    sw = torch.from_numpy(oracle.scales_to_mma(s.cpu().numpy())).to(DEV) if layout else s
+    x, _, x64, _ = activations(M, K, "bf16", 26)
+    y = mx.mxfp4_gemv(x, q, sw, N, K, wparams(nv, layout), out_dtype=F32)
+    rows = list(range(0, N, 997))
+    v = E2M1.to(DEV)[torch.stack((q[rows] & 15, q[rows] >> 4), -1).view(len(rows), K).long()]
+    f = s[rows].view(torch.float8_e4m3fn).double() if nv else torch.exp2(s[rows].double() - 127)
+    check(y[:, rows], x64, v * f.repeat_interleave(16 if nv else 32, 1))
+    for _ in range(30):
+        assert torch.equal(mx.mxfp4_gemv(x, q, sw, N, K, wparams(nv, layout), out_dtype=F32), y)
+    assert mx.device_status() == 0
+
+
 def test_empty_sizes():
     import gemm_pt_block_gb300 as mx
 
