@@ -139,6 +139,10 @@ def load_library(path: str) -> ctypes.CDLL:
     L.mxfp4_swiglu_backward.argtypes = [P, i32, i64, P, i64, P, i64, i32, i64, i64, P, i64, P, i64, P]
     L.mxfp4_gemv.restype = i32
     L.mxfp4_gemv.argtypes = [P, i32, i64, P, P, P, i32, i32, i32, i64, i64, i64, P, i32, i64, P]
+    L.mxfp4_gemv_ex.restype = i32
+    L.mxfp4_gemv_ex.argtypes = [P, i32, i64, P, P, P, i32, i32, i32, i64, i64, i64, P, i32, i64, P, sz, P]
+    L.mxfp4_gemv_workspace_size.restype = sz
+    L.mxfp4_gemv_workspace_size.argtypes = [i32, i32, i64, i64, i64]
     L.mxfp4_status_string.restype = ctypes.c_char_p
     L.mxfp4_status_string.argtypes = [i32]
     L.mxfp4_last_error.restype = ctypes.c_char_p
@@ -753,21 +757,27 @@ def mxfp4_swiglu_backward(dy: torch.Tensor, gate: torch.Tensor, up: torch.Tensor
     return dgate, dup
 
 
+_GEMV_WORKSPACE_FROM = 1 << 22      # weights; below, the library asks for no workspace
 _GEMV_CODES = {FORMAT_E4M3: 1, FORMAT_E5M2: 2}     # MXFP4_GEMV_X_*; bf16 is 0
 
 
 def mxfp4_gemv(x: torch.Tensor, qw: torch.Tensor, sw: torch.Tensor, N: int, K: int,
                w: QuantParams | None = None, *, sx: torch.Tensor | None = None, x_format: int = FORMAT_E4M3,
-               out_dtype: torch.dtype = torch.bfloat16, y=None, stream=None):
+               out_dtype: torch.dtype = torch.bfloat16, y=None, workspace=None, stream=None):
     """y[M, N] = x W^T for a few rows x [M, K] and a 4-bit weight matrix W [N, K]:
     codes qw [N, K/2] and scales sw as mxfp4_quantize wrote them with `w` (its
     block, scale_layout and tensor_exp; default 1x32, row-major).
 
     x is bf16, or uint8 codes of `x_format` (FORMAT_E4M3 / FORMAT_E5M2) with
     row-major E8M0 scales sx [M, K/32], as the quantized norm and activation
-    write them. y in out_dtype (or y's own: bf16 or fp32)."""
+    write them. y in out_dtype (or y's own: bf16 or fp32).
+
+    `workspace`: None (default) lets the call use a scratch tensor where the
+    product gains by one (mxfp4_gemv_ex), a CUDA uint8 tensor supplies it,
+    False runs without one."""
     if stream is not None:
-        return _on(stream, mxfp4_gemv, x, qw, sw, N, K, w, sx=sx, x_format=x_format, out_dtype=out_dtype, y=y)
+        return _on(stream, mxfp4_gemv, x, qw, sw, N, K, w, sx=sx, x_format=x_format, out_dtype=out_dtype, y=y,
+                   workspace=workspace)
     w = QuantParams() if w is None else w
     if w.elem_format != FORMAT_E2M1:
         raise ValueError("the weights must be 4-bit (E2M1) codes")
@@ -795,8 +805,18 @@ def mxfp4_gemv(x: torch.Tensor, qw: torch.Tensor, sw: torch.Tensor, N: int, K: i
         y = torch.empty((M, N), dtype=out_dtype, device=x.device)
     else:
         ldy = _rows_ld(y, "y", M, N, dev)
-    st = lib().mxfp4_gemv(x.data_ptr(), kind, ldx, psx, qw.data_ptr(), sw.data_ptr(), w.block, w.scale_layout,
-                          w.tensor_exp, M, N, K, y.data_ptr(), _dtype_of(y, "y"), ldy, _raw_stream(dev))
+    L, pws, nbytes = lib(), None, 0
+    if workspace is None:
+        if N * K >= _GEMV_WORKSPACE_FROM:
+            nbytes = L.mxfp4_gemv_workspace_size(kind, w.block, M, N, K)
+            if nbytes:
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+                pws = workspace.data_ptr()
+    elif workspace is not False:
+        _dense(workspace, 0, torch.uint8, "workspace", dev)
+        pws, nbytes = workspace.data_ptr(), workspace.numel()
+    st = L.mxfp4_gemv_ex(x.data_ptr(), kind, ldx, psx, qw.data_ptr(), sw.data_ptr(), w.block, w.scale_layout,
+                         w.tensor_exp, M, N, K, y.data_ptr(), _dtype_of(y, "y"), ldy, pws, nbytes, _raw_stream(dev))
     if st:
         _check(st)
     return y

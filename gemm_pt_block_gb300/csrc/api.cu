@@ -602,6 +602,25 @@ mxfp4_status mxfp4_swiglu_backward(const void* dy, int32_t dy_dtype, int64_t ld_
 mxfp4_status mxfp4_gemv(const void* x, int32_t x_kind, int64_t ld_x, const uint8_t* sx, const uint8_t* qw,
                         const uint8_t* sw, int32_t block, int32_t scale_layout, int32_t tensor_exp, int64_t M,
                         int64_t N, int64_t K, void* y, int32_t y_dtype, int64_t ld_y, void* stream) {
+  return mxfp4_gemv_ex(x, x_kind, ld_x, sx, qw, sw, block, scale_layout, tensor_exp, M, N, K, y, y_dtype, ld_y,
+                       nullptr, 0, stream);
+}
+
+size_t mxfp4_gemv_workspace_size(int32_t x_kind, int32_t block, int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K <= 0 || M > 65536 || N > (1ll << 30) || K > (1ll << 30)) return 0;
+  mx::GemvArgs a{};
+  a.x_kind = x_kind;
+  a.nv = block == MXFP4_BLOCK_1X16;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  return (size_t)mx::gemv_workspace_bytes(a);
+}
+
+mxfp4_status mxfp4_gemv_ex(const void* x, int32_t x_kind, int64_t ld_x, const uint8_t* sx, const uint8_t* qw,
+                           const uint8_t* sw, int32_t block, int32_t scale_layout, int32_t tensor_exp, int64_t M,
+                           int64_t N, int64_t K, void* y, int32_t y_dtype, int64_t ld_y, void* workspace,
+                           size_t workspace_bytes, void* stream) {
   const char* fn = "mxfp4_gemv";
   if (x_kind != MXFP4_GEMV_X_BF16 && x_kind != MXFP4_GEMV_X_E4M3 && x_kind != MXFP4_GEMV_X_E5M2)
     return fail(MXFP4_ERR_INVALID_ARG, "%s: bad x_kind %d", fn, x_kind);
@@ -635,7 +654,10 @@ mxfp4_status mxfp4_gemv(const void* x, int32_t x_kind, int64_t ld_x, const uint8
     return fail(MXFP4_ERR_ALIGN, "%s: x, qw and sw must be 16-byte aligned, rows of x multiples of 16 bytes", fn);
   if (reinterpret_cast<uintptr_t>(y) % elem_bytes(y_dtype))
     return fail(MXFP4_ERR_ALIGN, "%s: y must be aligned to its element", fn);
+  if (!aligned16(workspace)) return fail(MXFP4_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
   mx::GemvArgs a{};
+  a.ws = static_cast<uint8_t*>(workspace);
+  a.ws_bytes = workspace ? workspace_bytes : 0;
   a.x = x;
   a.sx = sx;
   a.qw = qw;

@@ -772,21 +772,297 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const i
   finish(a, red, ld, 0, 1, kRows, tokens, rank, splits, n0, m0, NV ? a.p2k * 0x1p26f : 1.0f, ok);
 }
 
+// ------------------------------------- MXFP4 weights on the MXFP8 products ---
+// kind::mxf8f6f4 multiplies E2M1 by E4M3 or E5M2, each side with its E8M0 scale
+// per 32: the weights go in as they lie in memory and nothing is converted per
+// weight. x comes as MXFP8 codes, or is written as a sum of MXFP8 vectors:
+// digit 1 is bf16 x rounded to E4M3 under its block's scale 2^e, digit 2 what
+// that leaves under 2^(e - 4), digit 3 what is left then under 2^(e - 8). Each
+// digit is a row of the instruction's N, and a token's digits are added at the
+// end. E4M3 keeps four significant bits and bf16 has eight, so the digits are
+// exact for magnitudes down to 2^-18 of their block's largest, and off by at
+// most 2^-26 of it below (two digits: 2^-22, which an outlier in a block of
+// small values shows: measured 4.6e-5 of sum |x w|). A block that holds an
+// infinity or a NaN has the NaN scale: its token's sums are NaN.
+//
+// A small kernel makes the digits and their scale tiles once, in the caller's
+// workspace; the product's CTAs start under it (programmatic launch) and have
+// their first weights in flight when it ends. A CTA streams 128 rows of W, 128
+// of K a stage: TMA spreads the codes into the 8-bit containers that the
+// instruction reads, one thread issues the products, and the row-major scales,
+// where W has those, are arranged into a tile by a warp.
+constexpr int kMxN = 96;                    // most digit rows per CTA
+constexpr int kMxK = 128;
+constexpr int kMxA = kRows * kMxK, kMxTile = 512;
+// the ring for up to kN digit rows: two CTAs an SM
+template <int kN>
+struct MxRing {
+  static constexpr int kStages = kN <= 64 ? 4 : 3, kB = kN * kMxK;
+  static constexpr int kBytes = kStages * (kMxA + kB + 2 * kMxTile) + 1024 + 256;
+};
+constexpr int kMxConv = 4;
+constexpr int kMxThreads = (2 + kMxConv) * 32;
+constexpr uint32_t kMxTmem = 256, kMxSfa = 248, kMxSfb = 252;  // columns: all, and where the scales are
+
+struct MxCtl {
+  uint64_t full[4], empty[4], acc_full;
+  uint32_t tmem, abort;
+};
+static_assert(sizeof(MxCtl) <= 256, "control block");
+
+// How x is spread over the N of the instruction: `digits` rows a token,
+// `tokens` tokens a CTA, `tiles` of them; n the rows rounded up to 16.
+struct MxShape {
+  int digits, tokens, tiles, n;
+};
+MxShape mx_shape(const GemvArgs& a) {
+  MxShape s;
+  s.digits = a.x_kind != GemvArgs::kXBf16 ? 1 : 3;
+  const int most = s.digits == 3 ? kMxN / 3 : 64;
+  s.tokens = (int)(a.M < most ? a.M : most);
+  s.tiles = (int)((a.M + s.tokens - 1) / s.tokens);
+  s.n = (s.digits * s.tokens + 15) & ~15;
+  return s;
+}
+int64_t mx_codes_bytes(const GemvArgs& a, const MxShape& s) { return (int64_t)s.tiles * s.n * a.K; }
+int64_t mx_bytes(const GemvArgs& a, const MxShape& s) {
+  return mx_codes_bytes(a, s) + (int64_t)s.tiles * (a.K / kMxK) * kMxTile;
+}
+
+// x to digit codes [tile][n][K] and scale tiles [tile][K / 128][512]; four lanes
+// a 32-block.
+__global__ void __launch_bounds__(256) gemv_digits_kernel(const GemvArgs a, const MxShape s) {
+  ptx::launch_dependents();
+  uint8_t *const codes = a.ws, *const scales = a.ws + (int64_t)s.tiles * s.n * a.K;
+  const int64_t nkb = a.K >> 5, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 2;
+  const int64_t m = blockIdx.y, kb = i;
+  const int t = threadIdx.x & 3;
+  const bool live = kb < nkb;
+  const int64_t k = live ? kb * 32 + 8 * t : 0;
+  const int tile = (int)(m / s.tokens), row = (int)(m % s.tokens);
+  uint8_t* q = codes + ((int64_t)tile * s.n + row) * a.K + k;
+  uint8_t* f = scales + ((int64_t)tile * (a.K / kMxK) + kb / 4) * kMxTile + kb % 4;
+  auto put_scale = [&](int r, uint32_t c) {
+    if (live && t == 0) put_at(f + (r & 31) * 16 + (r >> 5) * 4, (uint8_t)c, a.ws, a.ws_bytes);
+  };
+  if (a.x_kind != GemvArgs::kXBf16) {
+    if (!live) return;
+    put_at(q, __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.x) + m * a.ld_x + k)), a.ws, a.ws_bytes);
+    put_scale(row, __ldg(a.sx + m * nkb + kb));
+    return;
+  }
+  const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + m * a.ld_x + k));
+  Vec8<uint16_t> raw{v};
+  float x[8];
+  unpack8(raw, x);
+  float top = absmax3_nan(absmax3_nan(x[0], x[1], x[2]), absmax3_nan(x[3], x[4], x[5]), absmax3_nan(x[6], x[7], 0.0f));
+  top = absmax3_nan(top, __shfl_xor_sync(0xffffffffu, top, 1), 0.0f);
+  top = absmax3_nan(top, __shfl_xor_sync(0xffffffffu, top, 2), 0.0f);
+  const bool bad = __float_as_uint(top) >= 0x7F800000u;
+  // the smallest scale under which nothing saturates (448 = 1.75 2^8), kept so that the last digit has one too
+  const int e = max(scale_exponent(top, true, true), -127 + 4 * (s.digits - 1));
+  float2 r[4];
+  const float2 inv = make_float2(inv_scale(e), inv_scale(e));
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r[j] = bad ? make_float2(0.0f, 0.0f) : f2mul(make_float2(x[2 * j], x[2 * j + 1]), inv);
+  for (int d = 0; d < s.digits; ++d) {
+    uint32_t c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      asm("{.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %2, %1;\n\tcvt.u32.u16 %0, t;}"
+          : "=r"(c[j]) : "f"(r[j].x), "f"(r[j].y));
+      const uint32_t h = e4m3x2_f16x2(c[j]);
+      const float2 got = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      r[j] = f2mul(f2sub(r[j], got), make_float2(16.0f, 16.0f));  // exact: what this digit leaves, 2^4 finer
+    }
+    if (live)
+      put_at(q + (int64_t)d * s.tokens * a.K, make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16)), a.ws, a.ws_bytes);
+    put_scale(d * s.tokens + row, bad ? 255u : (uint32_t)(e - 4 * d + 127));
+  }
+}
+
+template <int kN>
+__global__ void __launch_bounds__(kMxThreads, 2)
+gemv_mx_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const GemvArgs a,
+               const MxShape sh, const uint8_t* scales, const int splits) {
+  constexpr int kMxStages = MxRing<kN>::kStages, kMxB = MxRing<kN>::kB;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const base = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+  // per stage: A, then B; the scale tiles of all stages after them (1024-byte alignment of A and B)
+  uint8_t *const as = base, *const bs = as + kMxStages * kMxA, *const sfa = bs + kMxStages * kMxB,
+                 *const sfb = sfa + kMxStages * kMxTile;
+  MxCtl* const ctl = reinterpret_cast<MxCtl*>(sfb + kMxStages * kMxTile);
+  const uint32_t full = ptx::smem_u32(ctl->full), empty = ptx::smem_u32(ctl->empty),
+                 acc_full = ptx::smem_u32(&ctl->acc_full);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)(blockIdx.x % (unsigned)splits);
+  const int64_t n0 = (int64_t)(blockIdx.x / (unsigned)splits) * kRows, m0 = (int64_t)blockIdx.y * sh.tokens;
+  const int tokens = (int)min((int64_t)sh.tokens, a.M - m0);
+  const int stages = (int)(a.K / kMxK), sums = min(4, (int)kMxSfa / sh.n);
+  const int s0 = (int)((int64_t)stages * rank / splits), s1 = (int)((int64_t)stages * (rank + 1) / splits);
+
+  if (threadIdx.x == 0) {
+    ptx::prefetch_tensormap(&tm_w);
+    ptx::prefetch_tensormap(&tm_x);
+    for (int i = 0; i < kMxStages; ++i) {
+      ptx::mbar_init(full + 8 * i, a.mma ? 1 : 2);
+      ptx::mbar_init(empty + 8 * i, 1);
+    }
+    ptx::mbar_init(acc_full, 1);
+    ctl->abort = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_u32(&ctl->tmem), kMxTmem);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = ctl->tmem;
+
+  if (warp == 0) {
+    // ---- producer
+    if (lane == 0) {
+      // the spread codes count with the bytes they have in memory, half of what they take here
+      const uint32_t bytes = kMxA / 2 + (uint32_t)sh.n * kMxK + kMxTile * (a.mma ? 2u : 1u);
+      auto weights = [&](int s, int i) {
+        ptx::mbar_arrive_expect_tx(full + 8 * i, bytes);
+        ptx::tma_load_2d(ptx::smem_u32(as + i * kMxA), &tm_w, s * kMxK, (int32_t)n0, full + 8 * i);
+        if (a.mma)
+          ptx::bulk_load(ptx::smem_u32(sfa + i * kMxTile), a.sw + (n0 >> 7) * (a.K * 4) + (int64_t)s * kMxTile, kMxTile,
+                         full + 8 * i);
+      };
+      auto digits = [&](int s, int i) {
+        ptx::tma_load_2d(ptx::smem_u32(bs + i * kMxB), &tm_x, s * kMxK, (int32_t)blockIdx.y * sh.n, full + 8 * i);
+        ptx::bulk_load(ptx::smem_u32(sfb + i * kMxTile), scales + ((int64_t)blockIdx.y * stages + s) * kMxTile, kMxTile,
+                       full + 8 * i);
+      };
+      // the first weights, then, once the digits are written, all the rest
+      const int first = min(kMxStages, s1 - s0);
+      for (int j = 0; j < first; ++j) weights(s0 + j, j);
+      ptx::wait_prior_grid();
+      for (int j = 0; j < first; ++j) digits(s0 + j, j);
+      int s = s0 + first;
+      for (; s < s1; ++s) {
+        const int i = (s - s0) % kMxStages;
+        if (!wait_bar(empty + 8 * i, (uint32_t)((s - s0) / kMxStages - 1) & 1, &ctl->abort)) break;
+        weights(s, i);
+        digits(s, i);
+      }
+      // after an abort: the last load into each slot lands (bounded wait) before the CTA's memory goes
+      if (*reinterpret_cast<volatile uint32_t*>(&ctl->abort)) {
+        const int issued = s - s0;
+        for (int r = issued > kMxStages ? issued - kMxStages : 0; r < issued; ++r) {
+          const uint64_t t0 = ptx::globaltimer_ns();
+          while (!ptx::mbar_try_wait(full + 8 * (r % kMxStages), (uint32_t)(r / kMxStages) & 1) &&
+                 ptx::globaltimer_ns() - t0 < kWaitLimitNs / 10) {
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---- the thread that issues the products
+    if (lane == 0) {
+      const uint32_t xfmt = a.x_kind == GemvArgs::kXE5m2 ? 1u : 0u;
+      // A E2M1 (5 at bits 7-9), B E4M3 (0) or E5M2 (1 at bits 10-12), E8M0 scales (bit 23), N / 8, M / 16;
+      // which byte of a row's scale word: bits 4-5 (B) and 29-30 (A)
+      const uint32_t idesc = (5u << 7) | (xfmt << 10) | ((uint32_t)(sh.n >> 3) << 17) | (1u << 23) | ((kRows >> 4) << 24);
+      for (int s = 0; s < s1 - s0; ++s) {
+        const int i = s % kMxStages;
+        if (!wait_bar(full + 8 * i, (uint32_t)(s / kMxStages) & 1, &ctl->abort)) break;
+        ptx::tc_fence_after();
+        ptx::tc_cp_32x128b_warpx4(tmem + kMxSfa, ptx::smem_desc(ptx::smem_u32(sfa + i * kMxTile), 0, 128, 0));
+        ptx::tc_cp_32x128b_warpx4(tmem + kMxSfb, ptx::smem_desc(ptx::smem_u32(sfb + i * kMxTile), 0, 128, 0));
+#pragma unroll
+        for (int k = 0; k < kMxK / 32; ++k)
+          ptx::mma_mxf8f6f4(tmem + (s % sums) * sh.n, ptx::smem_desc(ptx::smem_u32(as + i * kMxA) + k * 32, 16, 1024, 2),
+                            ptx::smem_desc(ptx::smem_u32(bs + i * kMxB) + k * 32, 16, 1024, 2),
+                            idesc | (k << 4) | (k << 29), tmem + kMxSfa, tmem + kMxSfb, s >= sums || k != 0);
+        ptx::tc_commit(empty + 8 * i);
+      }
+      // completes when the products issued so far have (after an abort too: bounded wait)
+      ptx::tc_commit(acc_full);
+      const uint64_t t0 = ptx::globaltimer_ns();
+      while (!ptx::mbar_try_wait(acc_full, 0) && ptx::globaltimer_ns() - t0 < kWaitLimitNs / 10) {
+      }
+    }
+    __syncwarp();
+  } else if (!a.mma) {
+    // ---- row-major weight scales into tiles, whole stages in turn: lane l brings rows l, l + 32, l + 64, l + 96
+    const int64_t nkb = a.K >> 5;  // a multiple of four: words
+    for (int s = s0 + warp - 2; s < s1; s += kMxConv) {
+      const int i = (s - s0) % kMxStages;
+      uint32_t v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[j] = __ldg(reinterpret_cast<const uint32_t*>(a.sw + min(n0 + lane + 32 * j, a.N - 1) * nkb) + s);
+      if (s - s0 >= kMxStages && !wait_bar(empty + 8 * i, (uint32_t)((s - s0) / kMxStages - 1) & 1, &ctl->abort)) break;
+      *reinterpret_cast<uint4*>(sfa + i * kMxTile + lane * 16) = make_uint4(v[0], v[1], v[2], v[3]);
+      ptx::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(full + 8 * i);
+    }
+  }
+
+  // ---- the sums leave tensor memory, a token's digits added: warp w has rows 32 w .. 32 w + 31
+  float* const red = reinterpret_cast<float*>(as);  // [token][132], in place of the codes
+  constexpr int ld = kRows + 4;
+  __syncthreads();  // the issuing thread has seen its last product complete (or the CTA has aborted)
+  const bool ok = *reinterpret_cast<volatile uint32_t*>(&ctl->abort) == 0;
+  ptx::tc_fence_after();
+  if (warp < 4) {
+    for (int c = 0; c < sh.n; c += 16) {
+      float f[16] = {};
+      for (int j = 0; j < sums && j < s1 - s0; ++j) {
+        uint32_t v[16];
+        ptx::tmem_ld_32x32b_x16(tmem + ((uint32_t)(32 * warp) << 16) + j * sh.n + c, v);
+        ptx::tc_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) f[e] = __fadd_rn(f[e], __uint_as_float(v[e]));
+      }
+      // a row's digits are sh.tokens columns apart: the first digit's column stores, the others add
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int col = c + e, m = col % sh.tokens;
+        if (col >= sh.digits * sh.tokens) break;
+        float* d = red + m * ld + 32 * warp + lane;
+        *d = col < sh.tokens ? f[e] : __fadd_rn(*d, f[e]);
+      }
+    }
+    ptx::tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kMxTmem);
+  }
+  finish(a, red, ld, 0, 1, kRows, tokens, rank, splits, n0, m0, 1.0f, ok);
+}
+
 template <typename... P, typename... Q>
-cudaError_t launch_cluster(void (*kernel)(P...), dim3 grid, int threads, int bytes, int splits, cudaStream_t st,
-                           Q... args) {
+cudaError_t launch_cluster(void (*kernel)(P...), dim3 grid, int threads, int bytes, int splits, bool under_prior,
+                           cudaStream_t st, Q... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)splits;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  unsigned n = 0;
+  if (splits > 1) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = (unsigned)splits;
+    at[n].val.clusterDim.y = 1;
+    at[n++].val.clusterDim.z = 1;
+  }
+  if (under_prior) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
   cfg.attrs = at;
-  cfg.numAttrs = splits > 1 ? 1 : 0;
+  cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -818,7 +1094,7 @@ cudaError_t launch(const GemvArgs& a, int groups, int splits, cudaStream_t st) {
   if (!codes_map(&tm, a, 32 * groups)) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)((a.N + 32 * groups - 1) / (32 * groups)) * (unsigned)splits,
                   (unsigned)((a.M + kMaxTokens - 1) / kMaxTokens));
-  return launch_cluster(gemv_kernel<NT, NV>, grid, kThreads, bytes, splits, st, tm, a, groups, splits);
+  return launch_cluster(gemv_kernel<NT, NV>, grid, kThreads, bytes, splits, false, st, tm, a, groups, splits);
 }
 
 template <bool NV>
@@ -830,10 +1106,38 @@ cudaError_t launch_tc(const GemvArgs& a, int splits, cudaStream_t st) {
   if (!codes_map(&tm, a, kRows)) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)((a.N + kRows - 1) / kRows) * (unsigned)splits,
                   (unsigned)((a.M + kTcTokens - 1) / kTcTokens));
-  return launch_cluster(gemv_tc_kernel<NV>, grid, kTcThreads, bytes, splits, st, tm, a, splits);
+  return launch_cluster(gemv_tc_kernel<NV>, grid, kTcThreads, bytes, splits, false, st, tm, a, splits);
+}
+
+template <int kN>
+cudaError_t launch_mx(const GemvArgs& a, const MxShape& sh, int splits, cudaStream_t st) {
+  static bool set[kMaxDevices] = {};
+  if (cudaError_t e = allow_smem(gemv_mx_kernel<kN>, MxRing<kN>::kBytes, set)) return e;
+  const uint8_t* scales = a.ws + mx_codes_bytes(a, sh);
+  CUtensorMap tw, tx;
+  if (!make_tma_4bit(&tw, a.qw, a.N, a.K, kRows) ||
+      !make_tma_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.ws, (int64_t)sh.tiles * sh.n, a.K, a.K, sh.n, kMxK))
+    return cudaErrorInvalidValue;
+  gemv_digits_kernel<<<dim3((unsigned)((a.K / 32 + 63) / 64), (unsigned)a.M), 256, 0, st>>>(a, sh);
+  if (cudaError_t e = cudaGetLastError()) return e;
+  const dim3 grid((unsigned)((a.N + kRows - 1) / kRows) * (unsigned)splits, (unsigned)sh.tiles);
+  return launch_cluster(gemv_mx_kernel<kN>, grid, kMxThreads, MxRing<kN>::kBytes, splits, true, st, tw, tx, a, sh,
+                        scales, splits);
+}
+
+cudaError_t launch_mx(const GemvArgs& a, int splits, cudaStream_t st) {
+  const MxShape sh = mx_shape(a);
+  return sh.n <= 64 ? launch_mx<64>(a, sh, splits, st) : launch_mx<kMxN>(a, sh, splits, st);
 }
 
 }  // namespace
+
+// Whether the MXFP8 products can take it: whole 128-deep steps of MXFP4 weights.
+static bool mx_fits(const GemvArgs& a) {
+  return !a.nv && a.M > 0 && a.M <= 32768 && a.N > 0 && a.K >= kMxK && a.K % kMxK == 0 && (reinterpret_cast<uintptr_t>(a.qw) & 31u) == 0;
+}
+
+int64_t gemv_workspace_bytes(const GemvArgs& a) { return mx_fits(a) ? mx_bytes(a, mx_shape(a)) : 0; }
 
 cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t st) {
   if (a.M == 0 || a.N == 0) return cudaSuccess;
@@ -853,6 +1157,7 @@ cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t st) {
                         (2 * tiles * splits <= 3 * kSms && 32 * splits <= stages)))
     splits *= 2;
 #ifdef GEMV_TUNE
+  if (getenv("GEMV_TC") && atoi(getenv("GEMV_TC")) == 2) return launch_mx(a, atoi(getenv("GEMV_S")), st);
   if (getenv("GEMV_TC") && atoi(getenv("GEMV_TC"))) {
     splits = atoi(getenv("GEMV_S"));
     return a.nv ? launch_tc<true>(a, splits, st) : launch_tc<false>(a, splits, st);
@@ -860,6 +1165,7 @@ cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t st) {
   if (getenv("GEMV_R")) groups = atoi(getenv("GEMV_R"));
   if (getenv("GEMV_S")) splits = atoi(getenv("GEMV_S"));
 #endif
+  if (a.ws && mx_fits(a) && a.ws_bytes >= (uint64_t)mx_bytes(a, mx_shape(a))) return launch_mx(a, splits, st);
   if (a.M > 8) return a.nv ? launch_tc<true>(a, splits, st) : launch_tc<false>(a, splits, st);
   if (a.nv)
     return nt == 1 ? launch<1, true>(a, groups, splits, st)

@@ -98,6 +98,8 @@ struct GemvArgs {
   void* y;
   int64_t M, N, K, ld_x, ld_y;
   uint64_t y_bytes;
+  uint8_t* ws;        // optional workspace of ws_bytes
+  uint64_t ws_bytes;
   float p2k;          // NVFP4: 2^tensor_exp
   int32_t x_kind;
   bool nv, mma, y_f32;
@@ -142,6 +144,8 @@ cudaError_t launch_rmsnorm_grad(const NormGradArgs& a, bool h_f32, bool dy_f32, 
 cudaError_t launch_swiglu(const SwigluArgs& a, bool f32, cudaStream_t st);
 cudaError_t launch_swiglu_grad(const SwigluGradArgs& a, bool f32, bool dy_f32, cudaStream_t st);
 cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t st);
+// Workspace that launch_gemv would use for these arguments (0: none).
+int64_t gemv_workspace_bytes(const GemvArgs& a);
 // Each reads and clears the device error word of its translation unit.
 cudaError_t read_quant_error(uint32_t* err);
 cudaError_t read_ffn_error(uint32_t* err);

@@ -55,6 +55,23 @@ inline bool make_tma_2d(CUtensorMap* m, CUtensorMapDataType dt, uint32_t elem_by
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Packed 4-bit matrix [rows, cols] (cols % 128 == 0, base 32-byte aligned, rows
+// contiguous) loaded in boxes of box_rows x 128 elements into 8-bit containers
+// as kind::mxf8f6f4 reads them: sixteen elements as 8 bytes and 8 bytes of
+// padding, 128-byte swizzle.
+inline bool make_tma_4bit(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, uint32_t box_rows) {
+  auto fn = tma_encode_fn();
+  if (!fn) return false;
+  ensure_context();
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(cols / 2)};
+  const cuuint32_t box[2] = {128, box_rows};
+  const cuuint32_t es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Byte array [rows, row_bytes] (row_bytes % 16 == 0, base 16-byte aligned)
 // written by tiled stores of box_rows x box_bytes boxes, unswizzled: the box's
 // image in shared memory is row-major. Stores are clipped at the edges.

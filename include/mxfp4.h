@@ -461,6 +461,24 @@ mxfp4_status mxfp4_gemv(const void* x, int32_t x_kind, int64_t ld_x, const uint8
                         int32_t tensor_exp, int64_t M, int64_t N, int64_t K, void* y,
                         int32_t y_dtype, int64_t ld_y, void* stream);
 
+/* mxfp4_gemv with an optional workspace, caller-owned device memory, 16-byte
+ * aligned (NULL or too small: not used). With at least
+ * mxfp4_gemv_workspace_size(x_kind, block, M, N, K) bytes (0: none would be
+ * used; E8M0 scales, K a multiple of 128 and a large W have one), and qw
+ * 32-byte aligned, the product runs on the block-scaled MXFP8 tensor-core
+ * instruction, which reads the 4-bit codes and their scales as they are; x is
+ * first written to the workspace as the sum of three E4M3 vectors with block
+ * scales (of one if it is MXFP8 codes already). That sum is x to 2^-26 of its
+ * 32-block's largest magnitude; a row of x that holds an infinity or a NaN
+ * gives NaN. The weights are read again for every 32 rows of bf16 x and every
+ * 64 of codes. The workspace contents are scratch. */
+mxfp4_status mxfp4_gemv_ex(const void* x, int32_t x_kind, int64_t ld_x, const uint8_t* sx,
+                           const uint8_t* qw, const uint8_t* sw, int32_t block,
+                           int32_t scale_layout, int32_t tensor_exp, int64_t M, int64_t N,
+                           int64_t K, void* y, int32_t y_dtype, int64_t ld_y, void* workspace,
+                           size_t workspace_bytes, void* stream);
+size_t mxfp4_gemv_workspace_size(int32_t x_kind, int32_t block, int64_t M, int64_t N, int64_t K);
+
 /* Human-readable name of a status code (static string). */
 const char* mxfp4_status_string(mxfp4_status s);
 
