@@ -787,33 +787,43 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const i
 //
 // A small kernel makes the digits and their scale tiles once, in the caller's
 // workspace; the product's CTAs start under it (programmatic launch) and have
-// their first weights in flight when it ends. A CTA streams 128 rows of W, 128
-// of K a stage: TMA spreads the codes into the 8-bit containers that the
+// their first weights in flight when it ends. They stream 128 rows of W, 128 of
+// K a stage: TMA spreads the codes into the 8-bit containers that the
 // instruction reads, one thread issues the products, and the row-major scales,
 // where W has those, are arranged into a tile by a warp.
+//
+// One CTA an SM takes an equal run of all (row tile, stage) units, its ring
+// going on from one tile to the next, so that every SM streams to the end
+// (28672 x 8192 has 224 tiles: a CTA each on 152 SMs took 32 us). A tile
+// that several CTAs share goes to the workspace in parts; the CTA that adds the
+// last part sums them in CTA order, so the result does not depend on timing.
 constexpr int kMxN = 96;                    // most digit rows per CTA
 constexpr int kMxK = 128;
 constexpr int kMxA = kRows * kMxK, kMxTile = 512;
-// the ring for up to kN digit rows: two CTAs an SM
 template <int kN>
 struct MxRing {
-  static constexpr int kStages = kN <= 64 ? 4 : 3, kB = kN * kMxK;
-  static constexpr int kBytes = kStages * (kMxA + kB + 2 * kMxTile) + 1024 + 256;
+  static constexpr int kB = kN * kMxK;
+  static constexpr int kStages = kN <= 32 ? 10 : kN <= 64 ? 8 : 6;  // even: see the issuing threads
+  static constexpr int kBytes = kStages * (kMxA + kB + 2 * kMxTile) + 1024 + 512;
 };
-constexpr int kMxConv = 4;
-constexpr int kMxThreads = (2 + kMxConv) * 32;
-constexpr uint32_t kMxTmem = 256, kMxSfa = 248, kMxSfb = 252;  // columns: all, and where the scales are
+constexpr int kMxIss = 2, kMxEpi = 4, kMxConv = 4;  // warps: issuing, sums out of tensor memory, row-major scales
+constexpr int kMxThreads = (2 + kMxIss + kMxEpi + kMxConv) * 32;
+// Tensor-memory columns: two buffers of sums (one filled while the other leaves), and four slots of scales
+// (A's four columns, then B's), so that a stage's copies do not wait for the products of the one before.
+constexpr uint32_t kMxTmem = 512, kMxBuf = 240, kMxSf = 480;
 
 struct MxCtl {
-  uint64_t full[4], empty[4], acc_full;
-  uint32_t tmem, abort;
+  uint64_t full[10], empty[10], acc_full[2], acc_empty[2], drain[2];
+  uint32_t tmem, abort, last;
 };
-static_assert(sizeof(MxCtl) <= 256, "control block");
+static_assert(sizeof(MxCtl) <= 512, "control block");
 
-// How x is spread over the N of the instruction: `digits` rows a token,
-// `tokens` tokens a CTA, `tiles` of them; n the rows rounded up to 16.
+// How x is spread over the N of the instruction (`digits` rows a token,
+// `tokens` tokens a tile, `tiles` of them; n the rows rounded up to 16), and the
+// work over `ctas` CTAs.
 struct MxShape {
-  int digits, tokens, tiles, n;
+  int digits, tokens, tiles, n, ctas;
+  int64_t stages, units;  // stages of K; (row tile, token tile, stage) units
 };
 MxShape mx_shape(const GemvArgs& a) {
   MxShape s;
@@ -822,24 +832,42 @@ MxShape mx_shape(const GemvArgs& a) {
   s.tokens = (int)(a.M < most ? a.M : most);
   s.tiles = (int)((a.M + s.tokens - 1) / s.tokens);
   s.n = (s.digits * s.tokens + 15) & ~15;
+  s.stages = a.K / kMxK;
+  s.units = (a.N + kRows - 1) / kRows * s.tiles * s.stages;
+  // eight stages to a CTA at least: shorter runs lose more to filling the ring and adding parts
+  const int64_t want = (s.units + 7) / 8;
+  s.ctas = (int)(want < kSms ? want : kSms);
   return s;
 }
-int64_t mx_codes_bytes(const GemvArgs& a, const MxShape& s) { return (int64_t)s.tiles * s.n * a.K; }
-int64_t mx_bytes(const GemvArgs& a, const MxShape& s) {
-  return mx_codes_bytes(a, s) + (int64_t)s.tiles * (a.K / kMxK) * kMxTile;
+// The workspace: codes [tile][n][K], scale tiles [tile][K / 128][512], parts
+// [cta][2][token][128] of fp32, a counter for each row and token tile.
+struct MxSpace {
+  int64_t scales, parts, counters, bytes;
+};
+__host__ __device__ inline MxSpace mx_space(const MxShape& s) {
+  MxSpace w;
+  w.scales = (int64_t)s.tiles * s.n * s.stages * kMxK;
+  w.parts = w.scales + s.tiles * s.stages * kMxTile;
+  w.counters = w.parts + (int64_t)s.ctas * 2 * s.tokens * kRows * 4;
+  w.bytes = w.counters + s.units / s.stages * 4;
+  return w;
 }
 
 // x to digit codes [tile][n][K] and scale tiles [tile][K / 128][512]; four lanes
 // a 32-block.
 __global__ void __launch_bounds__(256) gemv_digits_kernel(const GemvArgs a, const MxShape s) {
   ptx::launch_dependents();
-  uint8_t *const codes = a.ws, *const scales = a.ws + (int64_t)s.tiles * s.n * a.K;
+  const MxSpace w = mx_space(s);
+  uint8_t *const codes = a.ws, *const scales = a.ws + w.scales;
+  if (blockIdx.y == 0)
+    for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < s.units / s.stages; c += (int64_t)gridDim.x * 256)
+      put_at(reinterpret_cast<uint32_t*>(a.ws + w.counters) + c, 0u, a.ws, a.ws_bytes);
   const int64_t nkb = a.K >> 5, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 2;
   const int64_t m = blockIdx.y, kb = i;
   const int t = threadIdx.x & 3;
   const bool live = kb < nkb;
   const int64_t k = live ? kb * 32 + 8 * t : 0;
-  const int tile = (int)(m / s.tokens), row = (int)(m % s.tokens);
+  const int tile = (int)(m / s.tokens), row = (int)(m % s.tokens) * s.digits;
   uint8_t* q = codes + ((int64_t)tile * s.n + row) * a.K + k;
   uint8_t* f = scales + ((int64_t)tile * (a.K / kMxK) + kb / 4) * kMxTile + kb % 4;
   auto put_scale = [&](int r, uint32_t c) {
@@ -876,39 +904,40 @@ __global__ void __launch_bounds__(256) gemv_digits_kernel(const GemvArgs a, cons
       r[j] = f2mul(f2sub(r[j], got), make_float2(16.0f, 16.0f));  // exact: what this digit leaves, 2^4 finer
     }
     if (live)
-      put_at(q + (int64_t)d * s.tokens * a.K, make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16)), a.ws, a.ws_bytes);
-    put_scale(d * s.tokens + row, bad ? 255u : (uint32_t)(e - 4 * d + 127));
+      put_at(q + (int64_t)d * a.K, make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16)), a.ws, a.ws_bytes);
+    put_scale(row + d, bad ? 255u : (uint32_t)(e - 4 * d + 127));
   }
 }
 
 template <int kN>
-__global__ void __launch_bounds__(kMxThreads, 2)
+__global__ void __launch_bounds__(kMxThreads, 1)
 gemv_mx_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const GemvArgs a,
-               const MxShape sh, const uint8_t* scales, const int splits) {
-  constexpr int kMxStages = MxRing<kN>::kStages, kMxB = MxRing<kN>::kB;
+               const MxShape sh) {
+  constexpr int ST = MxRing<kN>::kStages, kB = MxRing<kN>::kB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const base = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
-  // per stage: A, then B; the scale tiles of all stages after them (1024-byte alignment of A and B)
-  uint8_t *const as = base, *const bs = as + kMxStages * kMxA, *const sfa = bs + kMxStages * kMxB,
-                 *const sfb = sfa + kMxStages * kMxTile;
-  MxCtl* const ctl = reinterpret_cast<MxCtl*>(sfb + kMxStages * kMxTile);
+  // A of all stages, then B (both 1024-byte aligned), then the scale tiles
+  uint8_t *const as = base, *const bs = as + ST * kMxA, *const sfa = bs + ST * kB, *const sfb = sfa + ST * kMxTile;
+  MxCtl* const ctl = reinterpret_cast<MxCtl*>(sfb + ST * kMxTile);
   const uint32_t full = ptx::smem_u32(ctl->full), empty = ptx::smem_u32(ctl->empty),
-                 acc_full = ptx::smem_u32(&ctl->acc_full);
+                 acc_full = ptx::smem_u32(ctl->acc_full), acc_empty = ptx::smem_u32(ctl->acc_empty);
+  const MxSpace space = mx_space(sh);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = (int)(blockIdx.x % (unsigned)splits);
-  const int64_t n0 = (int64_t)(blockIdx.x / (unsigned)splits) * kRows, m0 = (int64_t)blockIdx.y * sh.tokens;
-  const int tokens = (int)min((int64_t)sh.tokens, a.M - m0);
-  const int stages = (int)(a.K / kMxK), sums = min(4, (int)kMxSfa / sh.n);
-  const int s0 = (int)((int64_t)stages * rank / splits), s1 = (int)((int64_t)stages * (rank + 1) / splits);
+  const int64_t u0 = sh.units * blockIdx.x / sh.ctas, u1 = sh.units * (blockIdx.x + 1) / sh.ctas;
+  const int per = 4 * sh.n <= (int)kMxBuf ? 2 : 1;  // sums of each issuing thread
 
   if (threadIdx.x == 0) {
     ptx::prefetch_tensormap(&tm_w);
     ptx::prefetch_tensormap(&tm_x);
-    for (int i = 0; i < kMxStages; ++i) {
-      ptx::mbar_init(full + 8 * i, a.mma ? 1 : 2);
+    for (int i = 0; i < ST; ++i) {
+      ptx::mbar_init(full + 8 * i, a.mma ? 2 : 3);
       ptx::mbar_init(empty + 8 * i, 1);
     }
-    ptx::mbar_init(acc_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(acc_full + 8 * i, kMxIss);
+      ptx::mbar_init(acc_empty + 8 * i, kMxEpi);
+    }
+    for (int i = 0; i < kMxIss; ++i) ptx::mbar_init(ptx::smem_u32(&ctl->drain[i]), 1);
     ctl->abort = 0;
     ptx::fence_mbar_init();
   }
@@ -921,124 +950,241 @@ gemv_mx_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
   ptx::tc_fence_after();
   const uint32_t tmem = ctl->tmem;
 
-  if (warp == 0) {
-    // ---- producer
+  // The roles of one thread each run on the latency of their instructions, so
+  // what they do per unit is kept short: addresses go on by additions (64-bit
+  // divisions here took 64 us, and one thread for both kinds of load, with
+  // descriptors made anew, 44 us, at one row of x and 28672 x 8192).
+  if (warp == 0 || warp == kMxThreads / 32 - 1) {
+    // ---- producers: the weights (and their scales where those lie in tiles), and the digits of x
     if (lane == 0) {
+      const bool w = warp == 0;
+      const int last = (int)sh.stages, tiles = sh.tiles;
+      const int64_t t0 = u0 / sh.stages;
+      int64_t row = t0 / tiles;
+      int tile = (int)(t0 % tiles), s = (int)(u0 - t0 * sh.stages);
+      const uint8_t* from = w ? a.sw + (row * last + s) * kMxTile : a.ws + space.scales + ((int64_t)tile * last + s) * kMxTile;
+      const uint32_t big = ptx::smem_u32(w ? as : bs), small = ptx::smem_u32(w ? sfa : sfb), step = w ? kMxA : kB;
       // the spread codes count with the bytes they have in memory, half of what they take here
-      const uint32_t bytes = kMxA / 2 + (uint32_t)sh.n * kMxK + kMxTile * (a.mma ? 2u : 1u);
-      auto weights = [&](int s, int i) {
+      const bool scales = !w || a.mma;
+      const uint32_t bytes = (w ? kMxA / 2 : (uint32_t)sh.n * kMxK) + (scales ? kMxTile : 0);
+      const CUtensorMap* tm = w ? &tm_w : &tm_x;
+      if (!w) ptx::wait_prior_grid();  // the weights start before the digits are written
+      int64_t left = u1 - u0, issued = 0;
+      int i = 0, y = w ? (int)(row * kRows) : tile * sh.n;
+      uint32_t parity = 1;  // the first round finds the slots empty
+      for (; left; --left, ++issued) {
+        if (!wait_bar(empty + 8 * i, parity, &ctl->abort)) break;
         ptx::mbar_arrive_expect_tx(full + 8 * i, bytes);
-        ptx::tma_load_2d(ptx::smem_u32(as + i * kMxA), &tm_w, s * kMxK, (int32_t)n0, full + 8 * i);
-        if (a.mma)
-          ptx::bulk_load(ptx::smem_u32(sfa + i * kMxTile), a.sw + (n0 >> 7) * (a.K * 4) + (int64_t)s * kMxTile, kMxTile,
-                         full + 8 * i);
-      };
-      auto digits = [&](int s, int i) {
-        ptx::tma_load_2d(ptx::smem_u32(bs + i * kMxB), &tm_x, s * kMxK, (int32_t)blockIdx.y * sh.n, full + 8 * i);
-        ptx::bulk_load(ptx::smem_u32(sfb + i * kMxTile), scales + ((int64_t)blockIdx.y * stages + s) * kMxTile, kMxTile,
-                       full + 8 * i);
-      };
-      // the first weights, then, once the digits are written, all the rest
-      const int first = min(kMxStages, s1 - s0);
-      for (int j = 0; j < first; ++j) weights(s0 + j, j);
-      ptx::wait_prior_grid();
-      for (int j = 0; j < first; ++j) digits(s0 + j, j);
-      int s = s0 + first;
-      for (; s < s1; ++s) {
-        const int i = (s - s0) % kMxStages;
-        if (!wait_bar(empty + 8 * i, (uint32_t)((s - s0) / kMxStages - 1) & 1, &ctl->abort)) break;
-        weights(s, i);
-        digits(s, i);
+        ptx::tma_load_2d(big + i * step, tm, s * kMxK, y, full + 8 * i);
+        if (scales) ptx::bulk_load(small + i * kMxTile, from, kMxTile, full + 8 * i);
+        from += kMxTile;
+        if (++i == ST) {
+          i = 0;
+          parity ^= 1u;
+        }
+        if (++s == last) {  // the next token tile, or the next row tile
+          s = 0;
+          if (++tile == tiles) {
+            tile = 0;
+            ++row;
+          }
+          y = w ? (int)(row * kRows) : tile * sh.n;
+          from = w ? a.sw + row * last * kMxTile : a.ws + space.scales + (int64_t)tile * last * kMxTile;
+        }
       }
       // after an abort: the last load into each slot lands (bounded wait) before the CTA's memory goes
       if (*reinterpret_cast<volatile uint32_t*>(&ctl->abort)) {
-        const int issued = s - s0;
-        for (int r = issued > kMxStages ? issued - kMxStages : 0; r < issued; ++r) {
-          const uint64_t t0 = ptx::globaltimer_ns();
-          while (!ptx::mbar_try_wait(full + 8 * (r % kMxStages), (uint32_t)(r / kMxStages) & 1) &&
-                 ptx::globaltimer_ns() - t0 < kWaitLimitNs / 10) {
+        for (int64_t r = issued > ST ? issued - ST : 0; r < issued; ++r) {
+          const uint64_t t = ptx::globaltimer_ns();
+          while (!ptx::mbar_try_wait(full + 8 * (uint32_t)(r % ST), (uint32_t)(r / ST) & 1) &&
+                 ptx::globaltimer_ns() - t < kWaitLimitNs / 10) {
           }
         }
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // ---- the thread that issues the products
+  } else if (warp <= kMxIss) {
+    // ---- two threads issue the products, the even and the odd units of the run, each into sums of its
+    // own: four products and two copies of scales to a unit take one thread longer than their loads
+    // (42 us where two take 28, at one row of x and 28672 x 8192). The ring has an even number of slots,
+    // so a slot is always the same thread's, which sees every phase of its barrier.
     if (lane == 0) {
       const uint32_t xfmt = a.x_kind == GemvArgs::kXE5m2 ? 1u : 0u;
       // A E2M1 (5 at bits 7-9), B E4M3 (0) or E5M2 (1 at bits 10-12), E8M0 scales (bit 23), N / 8, M / 16;
       // which byte of a row's scale word: bits 4-5 (B) and 29-30 (A)
       const uint32_t idesc = (5u << 7) | (xfmt << 10) | ((uint32_t)(sh.n >> 3) << 17) | (1u << 23) | ((kRows >> 4) << 24);
-      for (int s = 0; s < s1 - s0; ++s) {
-        const int i = s % kMxStages;
-        if (!wait_bar(full + 8 * i, (uint32_t)(s / kMxStages) & 1, &ctl->abort)) break;
+      const uint64_t a0 = ptx::smem_desc(ptx::smem_u32(as), 16, 1024, 2), b0 = ptx::smem_desc(ptx::smem_u32(bs), 16, 1024, 2),
+                     fa0 = ptx::smem_desc(ptx::smem_u32(sfa), 0, 128, 0), fb0 = ptx::smem_desc(ptx::smem_u32(sfb), 0, 128, 0);
+      const int me = warp - 1;
+      const uint32_t mine = (uint32_t)(me * per) * sh.n, other = per == 2 ? (uint32_t)sh.n : 0u;
+      int i = me, seg = 0;
+      uint32_t parity = 0, sf = (uint32_t)me * 8;
+      int64_t u = u0 + me;
+      bool go = true;
+      for (int64_t begin = u0; go && begin < u1; ++seg) {
+        const int64_t end = min(u1, (begin / sh.stages + 1) * sh.stages);
+        const int buf = seg & 1;
+        if (seg >= 2 && !wait_bar(acc_empty + 8 * buf, (uint32_t)(seg / 2 - 1) & 1, &ctl->abort)) break;
         ptx::tc_fence_after();
-        ptx::tc_cp_32x128b_warpx4(tmem + kMxSfa, ptx::smem_desc(ptx::smem_u32(sfa + i * kMxTile), 0, 128, 0));
-        ptx::tc_cp_32x128b_warpx4(tmem + kMxSfb, ptx::smem_desc(ptx::smem_u32(sfb + i * kMxTile), 0, 128, 0));
+        const uint32_t d = tmem + buf * kMxBuf + mine;
+        bool begun = false;
+        for (; u < end; u += kMxIss) {
+          if (!(go = wait_bar(full + 8 * i, parity, &ctl->abort))) break;
+          ptx::tc_fence_after();
+          const uint32_t f = tmem + kMxSf + sf;
+          ptx::tc_cp_32x128b_warpx4(f, fa0 + (uint32_t)i * (kMxTile >> 4));
+          ptx::tc_cp_32x128b_warpx4(f + 4, fb0 + (uint32_t)i * (kMxTile >> 4));
+          const uint64_t ad = a0 + (uint32_t)i * (kMxA >> 4), bd = b0 + (uint32_t)i * (kB >> 4);
 #pragma unroll
-        for (int k = 0; k < kMxK / 32; ++k)
-          ptx::mma_mxf8f6f4(tmem + (s % sums) * sh.n, ptx::smem_desc(ptx::smem_u32(as + i * kMxA) + k * 32, 16, 1024, 2),
-                            ptx::smem_desc(ptx::smem_u32(bs + i * kMxB) + k * 32, 16, 1024, 2),
-                            idesc | (k << 4) | (k << 29), tmem + kMxSfa, tmem + kMxSfb, s >= sums || k != 0);
-        ptx::tc_commit(empty + 8 * i);
+          for (int k = 0; k < kMxK / 32; ++k)
+            ptx::mma_mxf8f6f4(d + (k & 1) * other, ad + 2 * k, bd + 2 * k, idesc | (k << 4) | (k << 29), f, f + 4,
+                              begun || k >= per);
+          ptx::tc_commit(empty + 8 * i);
+          begun = true;
+          sf ^= 16;
+          i += kMxIss;
+          if (i >= ST) {
+            i -= ST;
+            parity ^= 1u;
+          }
+        }
+        ptx::tc_commit(acc_full + 8 * buf);
+        begin = end;
       }
-      // completes when the products issued so far have (after an abort too: bounded wait)
-      ptx::tc_commit(acc_full);
+      // the products issued so far complete before the CTA's memory goes (bounded wait; after an abort too)
+      ptx::tc_commit(ptx::smem_u32(&ctl->drain[me]));
       const uint64_t t0 = ptx::globaltimer_ns();
-      while (!ptx::mbar_try_wait(acc_full, 0) && ptx::globaltimer_ns() - t0 < kWaitLimitNs / 10) {
+      while (!ptx::mbar_try_wait(ptx::smem_u32(&ctl->drain[me]), 0) && ptx::globaltimer_ns() - t0 < kWaitLimitNs / 10) {
       }
     }
     __syncwarp();
+  } else if (warp < 1 + kMxIss + kMxEpi) {
+    // ---- sums out of tensor memory: a warp may read the 32 rows of its index modulo four
+    const int quarter = warp & 3, r = 32 * quarter + lane, tid = threadIdx.x - 32 * (1 + kMxIss);
+    ptx::wait_prior_grid();  // the counters are zero from here on
+    float* const parts = reinterpret_cast<float*>(a.ws + space.parts);
+    const int64_t plane = (int64_t)sh.tokens * kRows;
+    int seg = 0;
+    for (int64_t u = u0; u < u1; ++seg) {
+      const int64_t t = u / sh.stages, first = t * sh.stages, end = min(u1, first + sh.stages);
+      const int buf = seg & 1;
+      // the sums that hold something: one unit is one issuing thread's
+      const int j0 = end - u == 1 ? (int)((u - u0) & 1) * per : 0, j1 = end - u == 1 ? j0 + per : kMxIss * per;
+      const bool whole = end - u == sh.stages;
+      const int64_t n = t / sh.tiles * kRows + r, m0 = t % sh.tiles * sh.tokens;
+      const int tokens = (int)min((int64_t)sh.tokens, a.M - m0);
+      // slot 0: the run's first tile, slot 1: its last one
+      float* const part = parts + (2 * (int64_t)blockIdx.x + (u == u0 ? 0 : 1)) * plane + r;
+      // after an abort the warps still go through the barriers below together, moving nothing
+      const bool ok = __all_sync(0xffffffffu, wait_bar(acc_full + 8 * buf, (uint32_t)(seg / 2) & 1, &ctl->abort));
+      ptx::tc_fence_after();
+      auto store = [&](int m, float v) {
+        if (n >= a.N) return;
+        const int64_t o = (m0 + m) * a.ld_y + n;
+        if (a.y_f32)
+          put_at(static_cast<float*>(a.y) + o, v, a.y, a.y_bytes);
+        else
+          put_at(static_cast<uint16_t*>(a.y) + o, (uint16_t)bf16x2(v, 0.0f), a.y, a.y_bytes);
+      };
+      const uint32_t src = tmem + ((uint32_t)(32 * quarter) << 16) + buf * kMxBuf;
+      for (int m = 0; ok && m < tokens; m += 16) {
+        float f[16] = {};
+        for (int j = j0; j < j1; ++j) {
+          if (sh.digits == 1) {
+            uint32_t v[16];
+            ptx::tmem_ld_32x32b_x16(src + j * sh.n + m, v);
+            ptx::tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) f[e] = __fadd_rn(f[e], __uint_as_float(v[e]));
+          } else {
+            // 16 tokens' digits, three to each
+            uint32_t v[3][16];
+#pragma unroll
+            for (int d = 0; d < 3; ++d) ptx::tmem_ld_32x32b_x16(src + j * sh.n + 3 * m + 16 * d, v[d]);
+            ptx::tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float a0 = __uint_as_float(v[3 * e / 16][3 * e % 16]);
+              const float a1 = __uint_as_float(v[(3 * e + 1) / 16][(3 * e + 1) % 16]);
+              const float a2 = __uint_as_float(v[(3 * e + 2) / 16][(3 * e + 2) % 16]);
+              f[e] = __fadd_rn(f[e], __fadd_rn(a0, __fadd_rn(a1, a2)));
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          if (m + e >= tokens) break;
+          if (whole)
+            store(m + e, f[e]);
+          else
+            put_at(part + (m + e) * kRows, f[e], a.ws, a.ws_bytes);
+        }
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(acc_empty + 8 * buf);
+      if (!whole) {
+        // the tile's CTAs are those that have its first and its last unit, and all between
+        const int64_t c0 = ((first + 1) * sh.ctas - 1) / sh.units, c1 = ((first + sh.stages) * sh.ctas - 1) / sh.units;
+        __threadfence();
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (tid == 0)
+          ctl->last = ok && atomicAdd(reinterpret_cast<uint32_t*>(a.ws + space.counters) + t, 1u) == (uint32_t)(c1 - c0);
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (ok && *reinterpret_cast<volatile uint32_t*>(&ctl->last)) {
+          __threadfence();
+          // sixteen tokens' loads of a part in flight together
+          for (int m = 0; m < tokens; m += 16) {
+            float v[16] = {};
+            for (int64_t c = c0; c <= c1; ++c) {
+              const int slot = sh.units * c / sh.ctas >= first ? 0 : 1;
+              const float* from = parts + (2 * c + slot) * plane + m * kRows + r;
+              float w[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) w[e] = m + e < tokens ? __ldcg(from + e * kRows) : 0.0f;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] = __fadd_rn(v[e], w[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (m + e < tokens) store(m + e, v[e]);
+          }
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");  // ctl->last is read before the next tile writes it
+      }
+      u = end;
+    }
   } else if (!a.mma) {
     // ---- row-major weight scales into tiles, whole stages in turn: lane l brings rows l, l + 32, l + 64, l + 96
     const int64_t nkb = a.K >> 5;  // a multiple of four: words
-    for (int s = s0 + warp - 2; s < s1; s += kMxConv) {
-      const int i = (s - s0) % kMxStages;
+    int64_t t = -1, begin = 0, end = 0;  // the tile at hand and its units
+    const uint32_t* row[4];
+    for (int64_t u = u0 + warp - 1 - kMxIss - kMxEpi; u < u1; u += kMxConv) {
+      if (u >= end) {
+        t = u / sh.stages;
+        begin = t * sh.stages;
+        end = begin + sh.stages;
+        const int64_t n0 = t / sh.tiles * kRows;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          row[j] = reinterpret_cast<const uint32_t*>(a.sw + min(n0 + lane + 32 * j, a.N - 1) * nkb);
+      }
+      const int c = (int)(u - u0), i = c % ST;
       uint32_t v[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        v[j] = __ldg(reinterpret_cast<const uint32_t*>(a.sw + min(n0 + lane + 32 * j, a.N - 1) * nkb) + s);
-      if (s - s0 >= kMxStages && !wait_bar(empty + 8 * i, (uint32_t)((s - s0) / kMxStages - 1) & 1, &ctl->abort)) break;
+      for (int j = 0; j < 4; ++j) v[j] = __ldg(row[j] + (u - begin));
+      if (c >= ST && !wait_bar(empty + 8 * i, (uint32_t)(c / ST - 1) & 1, &ctl->abort)) break;
       *reinterpret_cast<uint4*>(sfa + i * kMxTile + lane * 16) = make_uint4(v[0], v[1], v[2], v[3]);
       ptx::fence_proxy_async();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(full + 8 * i);
     }
   }
-
-  // ---- the sums leave tensor memory, a token's digits added: warp w has rows 32 w .. 32 w + 31
-  float* const red = reinterpret_cast<float*>(as);  // [token][132], in place of the codes
-  constexpr int ld = kRows + 4;
-  __syncthreads();  // the issuing thread has seen its last product complete (or the CTA has aborted)
-  const bool ok = *reinterpret_cast<volatile uint32_t*>(&ctl->abort) == 0;
-  ptx::tc_fence_after();
-  if (warp < 4) {
-    for (int c = 0; c < sh.n; c += 16) {
-      float f[16] = {};
-      for (int j = 0; j < sums && j < s1 - s0; ++j) {
-        uint32_t v[16];
-        ptx::tmem_ld_32x32b_x16(tmem + ((uint32_t)(32 * warp) << 16) + j * sh.n + c, v);
-        ptx::tc_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 16; ++e) f[e] = __fadd_rn(f[e], __uint_as_float(v[e]));
-      }
-      // a row's digits are sh.tokens columns apart: the first digit's column stores, the others add
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int col = c + e, m = col % sh.tokens;
-        if (col >= sh.digits * sh.tokens) break;
-        float* d = red + m * ld + 32 * warp + lane;
-        *d = col < sh.tokens ? f[e] : __fadd_rn(*d, f[e]);
-      }
-    }
-    ptx::tc_fence_before();
-  }
   __syncthreads();
   if (warp == 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, kMxTmem);
   }
-  finish(a, red, ld, 0, 1, kRows, tokens, rank, splits, n0, m0, 1.0f, ok);
 }
 
 template <typename... P, typename... Q>
@@ -1110,24 +1256,22 @@ cudaError_t launch_tc(const GemvArgs& a, int splits, cudaStream_t st) {
 }
 
 template <int kN>
-cudaError_t launch_mx(const GemvArgs& a, const MxShape& sh, int splits, cudaStream_t st) {
+cudaError_t launch_mx(const GemvArgs& a, const MxShape& sh, cudaStream_t st) {
   static bool set[kMaxDevices] = {};
   if (cudaError_t e = allow_smem(gemv_mx_kernel<kN>, MxRing<kN>::kBytes, set)) return e;
-  const uint8_t* scales = a.ws + mx_codes_bytes(a, sh);
   CUtensorMap tw, tx;
   if (!make_tma_4bit(&tw, a.qw, a.N, a.K, kRows) ||
       !make_tma_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.ws, (int64_t)sh.tiles * sh.n, a.K, a.K, sh.n, kMxK))
     return cudaErrorInvalidValue;
   gemv_digits_kernel<<<dim3((unsigned)((a.K / 32 + 63) / 64), (unsigned)a.M), 256, 0, st>>>(a, sh);
   if (cudaError_t e = cudaGetLastError()) return e;
-  const dim3 grid((unsigned)((a.N + kRows - 1) / kRows) * (unsigned)splits, (unsigned)sh.tiles);
-  return launch_cluster(gemv_mx_kernel<kN>, grid, kMxThreads, MxRing<kN>::kBytes, splits, true, st, tw, tx, a, sh,
-                        scales, splits);
+  return launch_cluster(gemv_mx_kernel<kN>, dim3((unsigned)sh.ctas), kMxThreads, MxRing<kN>::kBytes, 1, true, st, tw, tx,
+                        a, sh);
 }
 
-cudaError_t launch_mx(const GemvArgs& a, int splits, cudaStream_t st) {
+cudaError_t launch_mx(const GemvArgs& a, cudaStream_t st) {
   const MxShape sh = mx_shape(a);
-  return sh.n <= 64 ? launch_mx<64>(a, sh, splits, st) : launch_mx<kMxN>(a, sh, splits, st);
+  return sh.n <= 32 ? launch_mx<32>(a, sh, st) : sh.n <= 64 ? launch_mx<64>(a, sh, st) : launch_mx<kMxN>(a, sh, st);
 }
 
 }  // namespace
@@ -1137,7 +1281,7 @@ static bool mx_fits(const GemvArgs& a) {
   return !a.nv && a.M > 0 && a.M <= 32768 && a.N > 0 && a.K >= kMxK && a.K % kMxK == 0 && (reinterpret_cast<uintptr_t>(a.qw) & 31u) == 0;
 }
 
-int64_t gemv_workspace_bytes(const GemvArgs& a) { return mx_fits(a) ? mx_bytes(a, mx_shape(a)) : 0; }
+int64_t gemv_workspace_bytes(const GemvArgs& a) { return mx_fits(a) ? mx_space(mx_shape(a)).bytes : 0; }
 
 cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t st) {
   if (a.M == 0 || a.N == 0) return cudaSuccess;
@@ -1157,7 +1301,7 @@ cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t st) {
                         (2 * tiles * splits <= 3 * kSms && 32 * splits <= stages)))
     splits *= 2;
 #ifdef GEMV_TUNE
-  if (getenv("GEMV_TC") && atoi(getenv("GEMV_TC")) == 2) return launch_mx(a, atoi(getenv("GEMV_S")), st);
+  if (getenv("GEMV_TC") && atoi(getenv("GEMV_TC")) == 2 && a.ws && mx_fits(a) && a.ws_bytes >= (uint64_t)mx_space(mx_shape(a)).bytes) return launch_mx(a, st);
   if (getenv("GEMV_TC") && atoi(getenv("GEMV_TC"))) {
     splits = atoi(getenv("GEMV_S"));
     return a.nv ? launch_tc<true>(a, splits, st) : launch_tc<false>(a, splits, st);
@@ -1165,7 +1309,7 @@ cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t st) {
   if (getenv("GEMV_R")) groups = atoi(getenv("GEMV_R"));
   if (getenv("GEMV_S")) splits = atoi(getenv("GEMV_S"));
 #endif
-  if (a.ws && mx_fits(a) && a.ws_bytes >= (uint64_t)mx_bytes(a, mx_shape(a))) return launch_mx(a, splits, st);
+  if (a.ws && mx_fits(a) && a.ws_bytes >= (uint64_t)mx_space(mx_shape(a)).bytes) return launch_mx(a, st);
   if (a.M > 8) return a.nv ? launch_tc<true>(a, splits, st) : launch_tc<false>(a, splits, st);
   if (a.nv)
     return nt == 1 ? launch<1, true>(a, groups, splits, st)
