@@ -482,8 +482,8 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
 
 // ---------------------------------------------------- more rows of x ---
 // Above eight rows the products of mma.sync and their operands' reads grow with
-// the rows; here the weights become bf16 once, in shared memory, and tcgen05
-// multiplies them with up to 64 rows of x for one instruction's issue:
+// the rows; here the weights become bf16 once, in tensor memory, and tcgen05
+// multiplies them with up to 32 rows of x for one instruction's issue:
 //  * 128 rows of W are the M of the instruction, the rows of x its N; x goes in
 //    as bf16 (E4M3 and E5M2 codes times their factor are exact in bf16), so
 //    both operands are exact and the sums fp32, in tensor memory;
@@ -499,15 +499,18 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
 constexpr int kTcTokens = 32;
 constexpr int kTcStages = 3;                // of kStageK
 constexpr int kTcK = 64;                    // K per tensor-core buffer
-constexpr int kTcBufs = 2, kTcBufsX = 4;    // of the weights, of x
+constexpr int kTcBufs = 4, kTcBufsX = 4;    // of the weights (tensor memory), of x (shared memory)
 constexpr int kTcDeq = 8, kTcConv = 4;      // converting warps: weights, x
-// Sums kept in tensor memory, the buffers in turn, added at the end: the
-// tensor cores round every K = 16 step of a sum toward zero, so one sum over
-// all of K drifts by up to K / 16 units of its last place (measured: 1.1e-5 of
-// sum |x w| at K = 16384), and eight drift by an eighth of that.
-constexpr int kTcSums = 8;
+// Sums kept in tensor memory, one for each of a buffer's four products, added
+// at the end: the tensor cores round every K = 16 step of a sum toward zero, so
+// one sum over all of K drifts by up to K / 16 units of its last place
+// (measured: 1.1e-5 of sum |x w| at K = 16384), and four by a quarter of that.
+constexpr int kTcSums = 4;
+// tensor-memory columns: the sums, then the buffers of the weights
+constexpr uint32_t kTcA = kTcSums * kTcTokens, kTcACols = kTcK / 2, kTcTmem = kTcA + kTcBufs * kTcACols;
+static_assert(kTcTmem == 256, "two CTAs an SM");
 constexpr int kTcThreads = (kTcDeq + 2 + kTcConv) * 32;
-constexpr int kTcA = kRows * kTcK * 2, kTcB = kTcTokens * kTcK * 2;
+constexpr int kTcB = kTcTokens * kTcK * 2;
 
 struct TcCtl {
   uint64_t full_w[kTcStages], empty_w[kTcStages], full_a[kTcBufs], empty_a[kTcBufs], full_b[kTcBufsX],
@@ -517,7 +520,7 @@ struct TcCtl {
 
 template <bool NV>
 constexpr int tc_smem() {
-  return kTcBufs * kTcA + kTcBufsX * kTcB + kTcStages * (kWBytes + 2 * kRows * kStageK / (NV ? 16 : 32)) + (int)sizeof(TcCtl) +
+  return kTcBufsX * kTcB + kTcStages * (kWBytes + 2 * kRows * kStageK / (NV ? 16 : 32)) + (int)sizeof(TcCtl) +
          1024;
 }
 
@@ -541,8 +544,7 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const i
   constexpr int kPer = NV ? 16 : 32, kTile = kRows * kStageK / kPer;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const base = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t *const ws = base, *const as = ws + kTcStages * kWBytes, *const bs = as + kTcBufs * kTcA,
-                 *const sws = bs + kTcBufsX * kTcB;
+  uint8_t *const ws = base, *const bs = ws + kTcStages * kWBytes, *const sws = bs + kTcBufsX * kTcB;
   TcCtl* const ctl = reinterpret_cast<TcCtl*>(sws + kTcStages * 2 * kTile);
   const uint32_t full_w = ptx::smem_u32(ctl->full_w), empty_w = ptx::smem_u32(ctl->empty_w),
                  full_a = ptx::smem_u32(ctl->full_a), empty_a = ptx::smem_u32(ctl->empty_a),
@@ -576,7 +578,7 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const i
     ptx::fence_mbar_init();
   }
   if (warp == kTcDeq + 1) {
-    ptx::tmem_alloc(ptx::smem_u32(&ctl->tmem), kTcSums * kTcTokens);
+    ptx::tmem_alloc(ptx::smem_u32(&ctl->tmem), kTcTmem);
     ptx::tmem_relinquish();
   }
   ptx::tc_fence_before();
@@ -600,8 +602,8 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const i
         ptx::tc_fence_after();
 #pragma unroll
         for (int k = 0; k < kTcK / 16; ++k)
-          ptx::mma_f16(tmem + (b % kTcSums) * kTcTokens, ptx::smem_desc(ptx::smem_u32(as + i * kTcA) + k * 32, 16, 1024, 2),
-                       ptx::smem_desc(ptx::smem_u32(bs + ix * kTcB) + k * 32, 16, 1024, 2), idesc, b >= kTcSums || k != 0);
+          ptx::mma_f16_ta(tmem + k * kTcTokens, tmem + kTcA + i * kTcACols + k * 8,
+                          ptx::smem_desc(ptx::smem_u32(bs + ix * kTcB) + k * 32, 16, 1024, 2), idesc, b != 0);
         ptx::tc_commit(empty_a + 8 * i);
         ptx::tc_commit(empty_b + 8 * ix);
       }
@@ -690,7 +692,7 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const i
         for (int e = 0; e < kWords; ++e) sc[e] = ahead[e];
         if (st + 1 < s1 - s0) fetch(s0 + st + 1);
       }
-      if (!wait_bar(full_w + 8 * slot, (uint32_t)(st / kTcStages) & 1, &ctl->abort)) break;
+      if (!__all_sync(0xffffffffu, wait_bar(full_w + 8 * slot, (uint32_t)(st / kTcStages) & 1, &ctl->abort))) break;
       if (a.mma) {
         const int live = (int)min((int64_t)kWords, (cols - (int64_t)(s0 + st) * (kStageK / kPer)) / 4);
 #pragma unroll
@@ -719,25 +721,29 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const i
           g |= g << 16;
           f1 = f0;
         }
-        if (round && !(go = wait_bar(empty_a + 8 * i, (round - 1) & 1, &ctl->abort))) break;
-        uint8_t* dst = as + i * kTcA + r * 128;
+        uint32_t out[16];
         const uint32_t words[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           uint32_t q[4];
           e2m1x8_bf16_tiny(words[w], q);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) q[e] = hmul2_bf16(q[e], w < 2 ? f0 : f1);
-          if (!NV && g) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) q[e] = hmul2_bf16(q[e], g);
-          }
-          *reinterpret_cast<uint4*>(dst + (((4 * half + w) ^ (r & 7)) << 4)) = make_uint4(q[0], q[1], q[2], q[3]);
+          for (int e = 0; e < 4; ++e) out[4 * w + e] = hmul2_bf16(q[e], w < 2 ? f0 : f1);
         }
-        ptx::fence_proxy_async();
+        if (!NV && g) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) out[e] = hmul2_bf16(out[e], g);
+        }
+        // the warp stores together
+        if (round && !(go = __all_sync(0xffffffffu, wait_bar(empty_a + 8 * i, (round - 1) & 1, &ctl->abort)))) break;
+        ptx::tc_fence_after();
+        ptx::tmem_st_32x32b_x16(tmem + ((uint32_t)(r & ~31) << 16) + kTcA + i * kTcACols + 16 * half, out);
+        ptx::tc_wait_st();
+        ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(full_a + 8 * i);
       }
+      // (the loads from this stage's slot are done: what they read has been stored)
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(empty_w + 8 * slot);
     }
@@ -752,7 +758,7 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const i
   if (warp < 4) {
     for (int c = 0; c < cols_n; c += 16) {
       float f[16] = {};
-      for (int j = 0; j < kTcSums && j < bufs; ++j) {
+      for (int j = 0; j < kTcSums; ++j) {
         uint32_t v[16];
         ptx::tmem_ld_32x32b_x16(tmem + ((uint32_t)(32 * warp) << 16) + j * kTcTokens + c, v);
         ptx::tc_wait_ld();
@@ -767,7 +773,7 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const i
   __syncthreads();
   if (warp == kTcDeq + 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, kTcSums * kTcTokens);
+    ptx::tmem_dealloc(tmem, kTcTmem);
   }
   finish(a, red, ld, 0, 1, kRows, tokens, rank, splits, n0, m0, NV ? a.p2k * 0x1p26f : 1.0f, ok);
 }
@@ -800,20 +806,25 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const i
 constexpr int kMxN = 96;                    // most digit rows per CTA
 constexpr int kMxK = 128;
 constexpr int kMxA = kRows * kMxK, kMxTile = 512;
+#ifndef ISS32
+#define ISS32 2
+#endif
+constexpr int kMxEpi = 4, kMxConv = 4;      // warps: sums out of tensor memory, row-major scales
 template <int kN>
 struct MxRing {
   static constexpr int kB = kN * kMxK;
-  static constexpr int kStages = kN <= 32 ? 10 : kN <= 64 ? 8 : 6;  // even: see the issuing threads
+  // issuing threads, and a multiple of them of slots
+  static constexpr int kIss = kN <= 32 ? ISS32 : 2;
+  static constexpr int kStages = kN <= 32 ? (ISS32 == 4 ? 8 : ISS32 == 3 ? 9 : 10) : kN <= 64 ? 8 : 6;
+  static constexpr int kThreads = (2 + kIss + kMxEpi + kMxConv) * 32;
   static constexpr int kBytes = kStages * (kMxA + kB + 2 * kMxTile) + 1024 + 512;
 };
-constexpr int kMxIss = 2, kMxEpi = 4, kMxConv = 4;  // warps: issuing, sums out of tensor memory, row-major scales
-constexpr int kMxThreads = (2 + kMxIss + kMxEpi + kMxConv) * 32;
 // Tensor-memory columns: two buffers of sums (one filled while the other leaves), and four slots of scales
 // (A's four columns, then B's), so that a stage's copies do not wait for the products of the one before.
 constexpr uint32_t kMxTmem = 512, kMxBuf = 240, kMxSf = 480;
 
 struct MxCtl {
-  uint64_t full[10], empty[10], acc_full[2], acc_empty[2], drain[2];
+  uint64_t full[10], empty[10], acc_full[2], acc_empty[2], drain[4];
   uint32_t tmem, abort, last;
 };
 static_assert(sizeof(MxCtl) <= 512, "control block");
@@ -910,10 +921,12 @@ __global__ void __launch_bounds__(256) gemv_digits_kernel(const GemvArgs a, cons
 }
 
 template <int kN>
-__global__ void __launch_bounds__(kMxThreads, 1)
+__global__ void __launch_bounds__(MxRing<kN>::kThreads, 1)
 gemv_mx_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const GemvArgs a,
                const MxShape sh) {
-  constexpr int ST = MxRing<kN>::kStages, kB = MxRing<kN>::kB;
+  constexpr int ST = MxRing<kN>::kStages, kB = MxRing<kN>::kB, kMxIss = MxRing<kN>::kIss,
+                kMxThreads = MxRing<kN>::kThreads;
+  static_assert(ST % kMxIss == 0 && ST >= 4, "a slot is always the same issuing thread's");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const base = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
   // A of all stages, then B (both 1024-byte aligned), then the scale tiles
@@ -924,7 +937,7 @@ gemv_mx_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
   const MxSpace space = mx_space(sh);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t u0 = sh.units * blockIdx.x / sh.ctas, u1 = sh.units * (blockIdx.x + 1) / sh.ctas;
-  const int per = 4 * sh.n <= (int)kMxBuf ? 2 : 1;  // sums of each issuing thread
+  const int per = 2 * kMxIss * sh.n <= (int)kMxBuf ? 2 : 1;  // sums of each issuing thread
 
   if (threadIdx.x == 0) {
     ptx::prefetch_tensormap(&tm_w);
@@ -1018,7 +1031,8 @@ gemv_mx_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       const int me = warp - 1;
       const uint32_t mine = (uint32_t)(me * per) * sh.n, other = per == 2 ? (uint32_t)sh.n : 0u;
       int i = me, seg = 0;
-      uint32_t parity = 0, sf = (uint32_t)me * 8;
+      uint32_t parity = 0;
+      const uint32_t f = tmem + kMxSf + (uint32_t)me * 8;
       int64_t u = u0 + me;
       bool go = true;
       for (int64_t begin = u0; go && begin < u1; ++seg) {
@@ -1031,7 +1045,6 @@ gemv_mx_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
         for (; u < end; u += kMxIss) {
           if (!(go = wait_bar(full + 8 * i, parity, &ctl->abort))) break;
           ptx::tc_fence_after();
-          const uint32_t f = tmem + kMxSf + sf;
           ptx::tc_cp_32x128b_warpx4(f, fa0 + (uint32_t)i * (kMxTile >> 4));
           ptx::tc_cp_32x128b_warpx4(f + 4, fb0 + (uint32_t)i * (kMxTile >> 4));
           const uint64_t ad = a0 + (uint32_t)i * (kMxA >> 4), bd = b0 + (uint32_t)i * (kB >> 4);
@@ -1041,7 +1054,6 @@ gemv_mx_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
                               begun || k >= per);
           ptx::tc_commit(empty + 8 * i);
           begun = true;
-          sf ^= 16;
           i += kMxIss;
           if (i >= ST) {
             i -= ST;
@@ -1068,8 +1080,8 @@ gemv_mx_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
     for (int64_t u = u0; u < u1; ++seg) {
       const int64_t t = u / sh.stages, first = t * sh.stages, end = min(u1, first + sh.stages);
       const int buf = seg & 1;
-      // the sums that hold something: one unit is one issuing thread's
-      const int j0 = end - u == 1 ? (int)((u - u0) & 1) * per : 0, j1 = end - u == 1 ? j0 + per : kMxIss * per;
+      // fewer units than issuing threads: the others' sums hold nothing of this tile
+      const int units = (int)min((int64_t)kMxIss, end - u), from = (int)((u - u0) % kMxIss);
       const bool whole = end - u == sh.stages;
       const int64_t n = t / sh.tiles * kRows + r, m0 = t % sh.tiles * sh.tokens;
       const int tokens = (int)min((int64_t)sh.tokens, a.M - m0);
@@ -1089,7 +1101,8 @@ gemv_mx_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       const uint32_t src = tmem + ((uint32_t)(32 * quarter) << 16) + buf * kMxBuf;
       for (int m = 0; ok && m < tokens; m += 16) {
         float f[16] = {};
-        for (int j = j0; j < j1; ++j) {
+        for (int q = 0; q < units * per; ++q) {
+          const int j = (from * per + q) % (kMxIss * per);
           if (sh.digits == 1) {
             uint32_t v[16];
             ptx::tmem_ld_32x32b_x16(src + j * sh.n + m, v);
@@ -1265,7 +1278,7 @@ cudaError_t launch_mx(const GemvArgs& a, const MxShape& sh, cudaStream_t st) {
     return cudaErrorInvalidValue;
   gemv_digits_kernel<<<dim3((unsigned)((a.K / 32 + 63) / 64), (unsigned)a.M), 256, 0, st>>>(a, sh);
   if (cudaError_t e = cudaGetLastError()) return e;
-  return launch_cluster(gemv_mx_kernel<kN>, dim3((unsigned)sh.ctas), kMxThreads, MxRing<kN>::kBytes, 1, true, st, tw, tx,
+  return launch_cluster(gemv_mx_kernel<kN>, dim3((unsigned)sh.ctas), MxRing<kN>::kThreads, MxRing<kN>::kBytes, 1, true, st, tw, tx,
                         a, sh);
 }
 
