@@ -289,7 +289,7 @@ __device__ void produce(const CUtensorMap& tm, const GemvArgs& a, int64_t n0, in
 // and stored. Every thread of the CTA calls it, the planes written and visible.
 __device__ __forceinline__ void finish(const GemvArgs& a, float* red, int ld, int plane, int planes, int rows,
                                        int tokens, int rank, int splits, int64_t n0, int64_t m0, float factor,
-                                       bool ok) {
+                                       const float* per_token, bool ok) {
   const int total = tokens * rows;
   if (splits > 1) {
     if (ok && planes > 1)
@@ -314,6 +314,7 @@ __device__ __forceinline__ void finish(const GemvArgs& a, float* red, int ld, in
         for (int c = 0; c < splits; ++c) v = __fadd_rn(v, lds_cluster(ptx::mapa(at, (uint32_t)c)));
       }
       v = __fmul_rn(v, factor);
+      if (per_token) v = __fmul_rn(v, __ldcg(per_token + m0 + m));
       const int64_t o = (m0 + m) * a.ld_y + n;
       if (a.y_f32)
         put_at(static_cast<float*>(a.y) + o, v, a.y, a.y_bytes);
@@ -477,7 +478,7 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
         }
   }
   __syncthreads();
-  finish(a, red, ld, plane, kParts, rows, tokens, rank, splits, n0, m0, NV ? a.p2k : 1.0f, ok);
+  finish(a, red, ld, plane, kParts, rows, tokens, rank, splits, n0, m0, NV ? a.p2k : 1.0f, nullptr, ok);
 }
 
 // ---------------------------------------------------- more rows of x ---
@@ -538,9 +539,79 @@ __device__ __forceinline__ void e2m1x8_bf16_tiny(uint32_t v, uint32_t (&r)[4]) {
   r[3] = (v & 0x80008000u) | ((v >> 6) & 0x01C001C0u);
 }
 
-template <bool NV>
+// f16 x of the NVFP4 form: rows [tile][n][K] and a factor for each token, in the workspace.
+struct TcX {
+  int tiles, n;
+  int64_t factors, bytes;
+};
+TcX tc_x(const GemvArgs& a) {
+  TcX x;
+  const int tokens = (int)(a.M < kTcTokens ? a.M : kTcTokens);
+  x.tiles = (int)((a.M + kTcTokens - 1) / kTcTokens);
+  x.n = (tokens + 15) & ~15;
+  x.factors = (int64_t)x.tiles * x.n * a.K * 2;
+  x.bytes = x.factors + a.M * 4;
+  return x;
+}
+
+// One CTA a token: the largest magnitude's exponent E, x 2^(14 - E) as f16, and 2^(E - 14). (As in the
+// conversion for few rows, with one factor for the whole row: exact down to 2^-31 of the row's largest
+// magnitude, off by at most 2^-39 of it below.)
+constexpr int kF16Threads = 512;
+__global__ void __launch_bounds__(kF16Threads) gemv_f16_rows_kernel(const GemvArgs a, const TcX s) {
+  ptx::launch_dependents();
+  __shared__ uint32_t part[kF16Threads / 32];
+  const int64_t m = blockIdx.x, nkb = a.K >> 5;
+  uint8_t* const out = a.ws + ((m / kTcTokens) * s.n + m % kTcTokens) * a.K * 2;
+  const bool codes = a.x_kind != GemvArgs::kXBf16, e5 = a.x_kind == GemvArgs::kXE5m2;
+  auto load = [&](int64_t k, float (&f)[8]) {
+    if (!codes) {
+      Vec8<uint16_t> v{__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + m * a.ld_x + k))};
+      unpack8(v, f);
+      return;
+    }
+    const uint2 q = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.x) + m * a.ld_x + k));
+    const float sx = __uint_as_float(e8m0x2_bf16x2(__ldg(a.sx + m * nkb + (k >> 5))) << 16);
+    const uint32_t c[4] = {q.x, q.x >> 16, q.y, q.y >> 16};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t h = e5 ? e5m2x2_f16x2(c[j]) : e4m3x2_f16x2(c[j]);
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      f[2 * j] = __fmul_rn(v.x, sx);
+      f[2 * j + 1] = __fmul_rn(v.y, sx);
+    }
+  };
+  uint32_t top = 0;
+  float f[8];
+  for (int64_t k = threadIdx.x * 8; k < a.K; k += kF16Threads * 8) {
+    load(k, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
+  __syncthreads();
+  top = __reduce_max_sync(0xffffffffu, part[threadIdx.x % (kF16Threads / 32)]);
+  const uint32_t E = max(top >> 23, 15u);
+  const float scale = __uint_as_float((268u - E) << 23);
+  if (threadIdx.x == 0)
+    put_at(reinterpret_cast<float*>(a.ws + s.factors) + m, __uint_as_float((E - 14u) << 23), a.ws, a.ws_bytes);
+  for (int64_t k = threadIdx.x * 8; k < a.K; k += kF16Threads * 8) {
+    load(k, f);
+    put_at(out + 2 * k, make_uint4(f16x2(f[0] * scale, f[1] * scale), f16x2(f[2] * scale, f[3] * scale),
+                                   f16x2(f[4] * scale, f[5] * scale), f16x2(f[6] * scale, f[7] * scale)),
+           a.ws, a.ws_bytes);
+  }
+}
+
+// kF16: NVFP4 weights with x as f16 in the workspace. E2M1 codes become f16 by
+// conversion, two an instruction, and one packed product with their E4M3 scale
+// (six significant bits: exact) finishes them; x comes by TMA.
+template <bool NV, bool kF16>
 __global__ void __launch_bounds__(kTcThreads, 2)
-gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int splits) {
+gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm_x, const GemvArgs a,
+               const TcX sx, const int splits) {
+  static_assert(NV || !kF16, "E8M0 scales are beyond f16");
   constexpr int kPer = NV ? 16 : 32, kTile = kRows * kStageK / kPer;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const base = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -592,8 +663,8 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const i
   } else if (warp == kTcDeq + 1) {
     // ---- the thread that issues the products
     if (lane == 0) {
-      // bf16 operands (1 at bits 7 and 10), fp32 sums (1 at bit 4), K-major, N / 8 and M / 16
-      const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(cols_n >> 3) << 17) | ((kRows >> 4) << 24);
+      // bf16 operands (1 at bits 7 and 10; f16: 0), fp32 sums (1 at bit 4), K-major, N / 8 and M / 16
+      const uint32_t idesc = (1u << 4) | (kF16 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)(cols_n >> 3) << 17) | ((kRows >> 4) << 24);
       for (int b = 0; b < bufs; ++b) {
         const int i = b % kTcBufs, ix = b % kTcBufsX;
         if (!wait_bar(full_a + 8 * i, (uint32_t)(b / kTcBufs) & 1, &ctl->abort) ||
@@ -615,27 +686,51 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const i
       }
     }
     __syncwarp();
+  } else if (kF16 && warp > kTcDeq + 1) {
+    // ---- x by TMA, once the rows are written
+    if (warp == kTcDeq + 2 && lane == 0) {
+      ptx::wait_prior_grid();
+      for (int b = 0; b < bufs; ++b) {
+        const int i = b % kTcBufsX;
+        if (b >= kTcBufsX && !wait_bar(empty_b + 8 * i, (uint32_t)(b / kTcBufsX - 1) & 1, &ctl->abort)) break;
+        ptx::mbar_arrive_expect_tx(full_b + 8 * i, (uint32_t)sx.n * kTcK * 2);
+        ptx::tma_load_2d(ptx::smem_u32(bs + i * kTcB), &tm_x, s0 * kStageK + b * kTcK, (int)blockIdx.y * sx.n, full_b + 8 * i);
+      }
+      if (*reinterpret_cast<volatile uint32_t*>(&ctl->abort)) {  // loads in flight land before the CTA's memory goes
+        const uint64_t t0 = ptx::globaltimer_ns();
+        while (ptx::globaltimer_ns() - t0 < kWaitLimitNs / 100) {
+        }
+      }
+    }
+    __syncwarp();
   } else if (warp > kTcDeq + 1) {
     // ---- x: whole buffers in turn, a lane eight elements (16 bytes of bf16) of every fourth row,
     // in the weights' order. A buffer's loads are all in flight before its slot is waited for.
     const int c = lane & 7;
+    const int64_t x_bytes = a.x_kind == GemvArgs::kXBf16 ? 2 : 1, x_step = 4 * a.ld_x * x_bytes, s_step = 4 * (a.K >> 5);
+    const uint8_t* const x_rows = static_cast<const uint8_t*>(a.x) + (m0 + (lane >> 3)) * a.ld_x * x_bytes;
+    const uint8_t* const s_rows = a.sx + (m0 + (lane >> 3)) * (a.K >> 5);
     for (int b = warp - kTcDeq - 2; b < bufs; b += kTcConv) {
       const int i = b % kTcBufsX;
       const uint32_t round = (uint32_t)(b / kTcBufsX);
       const int64_t k = (int64_t)s0 * kStageK + (int64_t)b * kTcK + 8 * c;
       const bool live = k < a.K;
       uint4 w[kTcTokens / 4];  // bf16 pairs (0, 1), (2, 3), (4, 5), (6, 7); or codes and their scale
+      const uint8_t* px = x_rows + k * x_bytes;
+      const uint8_t* ps = s_rows + (k >> 5);
 #pragma unroll
       for (int e = 0; e < kTcTokens / 4; ++e) {
-        const int64_t m = m0 + 4 * e + (lane >> 3);
         w[e] = make_uint4(0, 0, 0, 0);
-        if (!live || m >= m0 + tokens) continue;
-        if (a.x_kind == GemvArgs::kXBf16) {
-          w[e] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + m * a.ld_x + k));
-        } else {
-          const uint2 q = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.x) + m * a.ld_x + k));
-          w[e] = make_uint4(q.x, q.y, __ldg(a.sx + m * (a.K >> 5) + (k >> 5)), 0);
+        if (live && 4 * e + (lane >> 3) < tokens) {
+          if (a.x_kind == GemvArgs::kXBf16) {
+            w[e] = __ldg(reinterpret_cast<const uint4*>(px));
+          } else {
+            const uint2 q = __ldg(reinterpret_cast<const uint2*>(px));
+            w[e] = make_uint4(q.x, q.y, __ldg(ps), 0);
+          }
         }
+        px += x_step;
+        ps += s_step;
       }
       if (round && !wait_bar(empty_b + 8 * i, (round - 1) & 1, &ctl->abort)) break;
 #pragma unroll
@@ -707,7 +802,11 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const i
         const uint32_t round = (uint32_t)(b / kTcBufs);
         const uint4 v = *reinterpret_cast<const uint4*>(ws + slot * kWBytes + r * kRowBytes + (((2 * j + half) ^ (r & 7)) << 4));
         uint32_t f0, f1, g = 0;  // factors of the two halves of the block; second factor (E8M0 above 2)
-        if (NV) {
+        if (kF16) {
+          const uint32_t h = e4m3x2_f16x2(sc[j] >> (16 * half));
+          f0 = __byte_perm(h, 0, 0x1010);
+          f1 = __byte_perm(h, 0, 0x3232);
+        } else if (NV) {
           const uint32_t h = e4m3x2_f16x2(sc[j] >> (16 * half));
           const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&h));
           f0 = bf16x2(q.x * 0x1p100f, q.x * 0x1p100f);
@@ -726,9 +825,13 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const i
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           uint32_t q[4];
-          e2m1x8_bf16_tiny(words[w], q);
+          if (kF16)
+            e2m1x8_f16(words[w], q);
+          else
+            e2m1x8_bf16_tiny(words[w], q);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) out[4 * w + e] = hmul2_bf16(q[e], w < 2 ? f0 : f1);
+          for (int e = 0; e < 4; ++e)
+            out[4 * w + e] = kF16 ? hmul2(q[e], w < 2 ? f0 : f1) : hmul2_bf16(q[e], w < 2 ? f0 : f1);
         }
         if (!NV && g) {
 #pragma unroll
@@ -775,7 +878,9 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const i
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, kTcTmem);
   }
-  finish(a, red, ld, 0, 1, kRows, tokens, rank, splits, n0, m0, NV ? a.p2k * 0x1p26f : 1.0f, ok);
+  if (kF16) ptx::wait_prior_grid();  // (the tokens' factors)
+  finish(a, red, ld, 0, 1, kRows, tokens, rank, splits, n0, m0, kF16 ? a.p2k : NV ? a.p2k * 0x1p26f : 1.0f,
+         kF16 ? reinterpret_cast<const float*>(a.ws + sx.factors) : nullptr, ok);
 }
 
 // ------------------------------------- MXFP4 weights on the MXFP8 products ---
@@ -1256,16 +1361,25 @@ cudaError_t launch(const GemvArgs& a, int groups, int splits, cudaStream_t st) {
   return launch_cluster(gemv_kernel<NT, NV>, grid, kThreads, bytes, splits, false, st, tm, a, groups, splits);
 }
 
-template <bool NV>
+template <bool NV, bool kF16>
 cudaError_t launch_tc(const GemvArgs& a, int splits, cudaStream_t st) {
   constexpr int bytes = tc_smem<NV>();
   static bool set[kMaxDevices] = {};
-  if (cudaError_t e = allow_smem(gemv_tc_kernel<NV>, bytes, set)) return e;
-  CUtensorMap tm;
+  if (cudaError_t e = allow_smem(gemv_tc_kernel<NV, kF16>, bytes, set)) return e;
+  CUtensorMap tm, tx;
   if (!codes_map(&tm, a, kRows)) return cudaErrorInvalidValue;
+  const TcX x = tc_x(a);
+  if (kF16) {
+    if (!make_tma_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.ws, (int64_t)x.tiles * x.n, a.K, a.K, x.n, kTcK))
+      return cudaErrorInvalidValue;
+    gemv_f16_rows_kernel<<<(unsigned)a.M, kF16Threads, 0, st>>>(a, x);
+    if (cudaError_t e = cudaGetLastError()) return e;
+  } else {
+    tx = tm;  // not used
+  }
   const dim3 grid((unsigned)((a.N + kRows - 1) / kRows) * (unsigned)splits,
                   (unsigned)((a.M + kTcTokens - 1) / kTcTokens));
-  return launch_cluster(gemv_tc_kernel<NV>, grid, kTcThreads, bytes, splits, false, st, tm, a, splits);
+  return launch_cluster(gemv_tc_kernel<NV, kF16>, grid, kTcThreads, bytes, splits, kF16, st, tm, tx, a, x, splits);
 }
 
 template <int kN>
@@ -1294,7 +1408,16 @@ static bool mx_fits(const GemvArgs& a) {
   return !a.nv && a.M > 0 && a.M <= 32768 && a.N > 0 && a.K >= kMxK && a.K % kMxK == 0 && (reinterpret_cast<uintptr_t>(a.qw) & 31u) == 0;
 }
 
-int64_t gemv_workspace_bytes(const GemvArgs& a) { return mx_fits(a) ? mx_space(mx_shape(a)).bytes : 0; }
+int64_t gemv_workspace_bytes(const GemvArgs& a) {
+  if (mx_fits(a)) return mx_space(mx_shape(a)).bytes;
+  return a.nv && a.M > 8 && a.N > 0 && a.K > 0 ? tc_x(a).bytes : 0;
+}
+
+static cudaError_t tc(const GemvArgs& a, int splits, cudaStream_t st) {
+  if (!a.nv) return launch_tc<false, false>(a, splits, st);
+  return a.ws && a.ws_bytes >= (uint64_t)tc_x(a).bytes ? launch_tc<true, true>(a, splits, st)
+                                                       : launch_tc<true, false>(a, splits, st);
+}
 
 cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t st) {
   if (a.M == 0 || a.N == 0) return cudaSuccess;
@@ -1317,13 +1440,13 @@ cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t st) {
   if (getenv("GEMV_TC") && atoi(getenv("GEMV_TC")) == 2 && a.ws && mx_fits(a) && a.ws_bytes >= (uint64_t)mx_space(mx_shape(a)).bytes) return launch_mx(a, st);
   if (getenv("GEMV_TC") && atoi(getenv("GEMV_TC"))) {
     splits = atoi(getenv("GEMV_S"));
-    return a.nv ? launch_tc<true>(a, splits, st) : launch_tc<false>(a, splits, st);
+    return tc(a, splits, st);
   }
   if (getenv("GEMV_R")) groups = atoi(getenv("GEMV_R"));
   if (getenv("GEMV_S")) splits = atoi(getenv("GEMV_S"));
 #endif
   if (a.ws && mx_fits(a) && a.ws_bytes >= (uint64_t)mx_space(mx_shape(a)).bytes) return launch_mx(a, st);
-  if (a.M > 8) return a.nv ? launch_tc<true>(a, splits, st) : launch_tc<false>(a, splits, st);
+  if (a.M > 8) return tc(a, splits, st);
   if (a.nv)
     return nt == 1 ? launch<1, true>(a, groups, splits, st)
                    : nt == 2 ? launch<2, true>(a, groups, splits, st) : launch<4, true>(a, groups, splits, st);

@@ -110,6 +110,65 @@ def test_tensor_core_scales(M, N, K, nv, kind):
     assert torch.equal(y, mx.mxfp4_gemv(x, q, s, N, K, wparams(nv), out_dtype=F32, **kw))
 
 
+WORKSPACE_SHAPES = [(1, 1, 128), (1, 130, 256), (2, 128, 1024), (5, 1000, 128), (7, 257, 2176), (10, 64, 640),
+                    (16, 300, 384), (17, 129, 4096), (21, 513, 1152), (22, 128, 256), (32, 1024, 1024), (33, 96, 512),
+                    (64, 200, 256), (65, 128, 896), (130, 65, 384), (9, 40, 96), (31, 200, 800), (40, 128, 224)]
+
+
+@pytest.mark.parametrize("M,N,K", WORKSPACE_SHAPES)
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "e5m2"])
+@pytest.mark.parametrize("nv", [False, True], ids=["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("layout", [0, 1], ids=["rows", "tiles"])
+def test_with_a_workspace(M, N, K, kind, nv, layout):
+    import gemm_pt_block_gb300 as mx
+
+    if layout and (N % 128 or K % 128):
+        pytest.skip("the tensor-core layout has whole tiles")
+    need = mx.lib().mxfp4_gemv_workspace_size({"bf16": 0, "e4m3": 1, "e5m2": 2}[kind], 3 if nv else 0, M, N, K)
+    if not need:
+        pytest.skip("no workspace would be used")
+    q, s, w64 = weights(N, K, nv, 27)
+    x, _, x64, kw = activations(M, K, kind, 28)
+    sw = torch.from_numpy(oracle.scales_to_mma(s.cpu().numpy())).to(DEV) if layout else s
+    a = Arena([need, M * N * 4])
+    ws, y = a.region(0, torch.uint8, (need,)), a.region(1, F32, (M, N))
+    mx.mxfp4_gemv(x, q, sw, N, K, wparams(nv, layout), y=y, workspace=ws, **kw)
+    check(y, x64, w64)
+    a.check(f"gemv {M}x{N}x{K} with a workspace")
+    first = y.clone()
+    y.fill_(7.0)
+    ws.fill_(0xFF)                                          # nothing of it is kept from call to call
+    mx.mxfp4_gemv(x, q, sw, N, K, wparams(nv, layout), y=y, workspace=ws, **kw)
+    assert torch.equal(y, first)
+    # one byte short: not used
+    mx.mxfp4_gemv(x, q, sw, N, K, wparams(nv, layout), y=y, workspace=ws[:need - 1], **kw)
+    assert torch.equal(y, mx.mxfp4_gemv(x, q, sw, N, K, wparams(nv, layout), out_dtype=F32, workspace=False, **kw))
+    assert mx.device_status() == 0
+
+
+def test_workspace_non_finite_rows_scales_and_zero_rows():
+    import gemm_pt_block_gb300 as mx
+
+    M, N, K = 12, 200, 512
+    for nv in (False, True):
+        q, s, w64 = weights(N, K, nv, 29)
+        x, _, x64, _ = activations(M, K, "bf16", 30)
+        x = x.clone()
+        x[1, 40], x[2, 41], x[3] = float("inf"), float("nan"), 0.0
+        x[4] = x[4] * 2.0 ** -100
+        x[5] = (x[5].float() * 2.0 ** 100).to(BF16)
+        s[7, 2] = 0x7F if nv else 255
+        need = mx.lib().mxfp4_gemv_workspace_size(0, 3 if nv else 0, M, N, K)
+        assert need > 0
+        ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+        y = mx.mxfp4_gemv(x, q, s, N, K, wparams(nv), out_dtype=F32, workspace=ws)
+        fine = [m for m in range(M) if m not in (1, 2)]
+        cols = [n for n in range(N) if n != 7]
+        assert torch.isnan(y[:, 7]).all() and torch.isnan(y[2]).all() and not torch.isfinite(y[1]).any()
+        check(y[fine][:, cols], x[fine].double(), w64[cols])
+        assert (y[3][cols] == 0).all()
+
+
 @pytest.mark.parametrize("block", ["1x32", "32x32", "64x64", "1x16"])
 def test_weights_of_the_quantizer(block):
     """The codes and scales that the training products use, as they are."""
