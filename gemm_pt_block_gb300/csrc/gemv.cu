@@ -54,22 +54,20 @@ constexpr int kMmaWarps = 8;               // (up to four) groups of 32 rows x k
 constexpr int kConvWarps = 4;
 constexpr int kThreads = (kMmaWarps + 1 + kConvWarps) * 32;
 constexpr int kWBytes = kRows * kRowBytes;
-constexpr int kMaxTokens = 32;
+constexpr int kTokens = 8;                 // rows of x: the N of one product
 constexpr int kSms = 152;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
-// Shared memory of one CTA for tiles of TT rows of x.
-template <int TT, bool NV>
+// Shared memory of one CTA.
+template <bool NV>
 struct Smem {
-  static constexpr int kX = TT * kStageK * 2;            // f16 [block][token][32]
+  static constexpr int kX = kTokens * kStageK * 2;            // f16 [block][token][32]
   static constexpr int kSw = 2 * kRows * kStageK / (NV ? 16 : 32);  // two 128-row tiles of scales
-  static constexpr int kSx = TT * (kStageK / 32) * 4;    // float [block][token]
-  static constexpr int kStage = kWBytes + kX + kSw + kSx;
-  static constexpr int kStages = TT == 32 ? 5 : TT == 16 ? 4 : NV ? 4 : 5;
-  static constexpr int kCtl = 256;
-  static constexpr int kBytes = kStages * kStage + kCtl + 1024;
+  static constexpr int kSx = kTokens * kBlocks * 4;           // float [block][token]
+  static constexpr int kStages = NV ? 4 : 5;
+  static constexpr int kBytes = kStages * (kWBytes + kX + kSw + kSx) + 256 + 1024;
   // partial sums [part][token][rows + 4] in place of the W stages
-  static_assert(kParts * (kRows + 4) * TT * 4 <= kStages * kWBytes, "partial sums fit the ring");
+  static_assert(kParts * (kRows + 4) * kTokens * 4 <= kStages * kWBytes, "partial sums fit the ring");
 };
 
 struct Ctl {
@@ -144,14 +142,13 @@ __device__ __forceinline__ float lds_cluster(uint32_t a) {
 
 // One stage of x rows m0 .. m0 + tokens - 1, K from k0: lane 4 b + t brings
 // elements 8 t .. 8 t + 7 of block b, a row at a time.
-template <int TT>
 __device__ __forceinline__ void convert_x(const GemvArgs& a, int64_t m0, int tokens, int64_t k0, int lane,
                                           uint8_t* xs, float* sxs) {
   const int b = lane >> 2, t = lane & 3;
   const int64_t k = k0 + b * 32 + t * 8;
   const bool live = k < a.K;
-  uint8_t* dst = xs + b * (TT * 64) + t * 16;
-  float* sdst = sxs + b * TT;
+  uint8_t* dst = xs + b * (kTokens * 64) + t * 16;
+  float* sdst = sxs + b * kTokens;
   if (a.x_kind == GemvArgs::kXBf16) {
     const uint16_t* p = static_cast<const uint16_t*>(a.x) + m0 * a.ld_x + k;
 #pragma unroll 1
@@ -214,14 +211,12 @@ __device__ __forceinline__ void convert_x(const GemvArgs& a, int64_t m0, int tok
 // (128 rows x 4 columns, 512 bytes) that the multiplying warps read: lane l
 // brings rows l, l + 32, l + 64, l + 96. Rows past N repeat the last one.
 template <bool NV>
-__device__ __forceinline__ void convert_sw(const GemvArgs& a, int groups, int64_t n0, int64_t k0, int lane,
-                                           uint8_t* sws) {
+__device__ __forceinline__ void convert_sw(const GemvArgs& a, int64_t n0, int64_t k0, int lane, uint8_t* sws) {
   constexpr int kCols = kStageK / (NV ? 16 : 32);
   const int64_t cols = a.K / (NV ? 16 : 32), c0 = k0 / (NV ? 16 : 32);
-  uint32_t v[kCols / 4][4] = {};
+  uint32_t v[kCols / 4][4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    if (j >= groups) break;
     const uint8_t* p = a.sw + min(n0 + lane + 32 * j, a.N - 1) * cols + c0;
     if ((cols & 3) == 0) {
 #pragma unroll
@@ -326,11 +321,11 @@ __device__ __forceinline__ void finish(const GemvArgs& a, float* red, int ld, in
   if (splits > 1) ptx::cluster_sync();  // peers read this CTA's sums until here
 }
 
-template <int NT, bool NV>
-__global__ void __launch_bounds__(kThreads, NT == 4 ? 1 : 2)
-gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int groups, const int splits) {
-  constexpr int TT = 8 * NT;
-  using S = Smem<TT, NV>;
+template <bool NV>
+__global__ void __launch_bounds__(kThreads, 2)
+gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int splits) {
+  constexpr int groups = kRows / 32, rows = kRows, mma_warps = kMmaWarps;
+  using S = Smem<NV>;
   constexpr int ST = S::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const base = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -340,10 +335,9 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
   const uint32_t full_w = ptx::smem_u32(ctl->full_w), full_x = ptx::smem_u32(ctl->full_x),
                  empty = ptx::smem_u32(ctl->empty);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int mma_warps = groups * kParts, rows = 32 * groups;
   const int rank = (int)(blockIdx.x % (unsigned)splits);
-  const int64_t n0 = (int64_t)(blockIdx.x / (unsigned)splits) * rows, m0 = (int64_t)blockIdx.y * kMaxTokens;
-  const int tokens = (int)min((int64_t)TT, a.M - m0);
+  const int64_t n0 = (int64_t)(blockIdx.x / (unsigned)splits) * rows, m0 = 0;
+  const int tokens = (int)a.M;
   const int stages = (int)((a.K + kStageK - 1) / kStageK);
   const int s0 = (int)((int64_t)stages * rank / splits), s1 = (int)((int64_t)stages * (rank + 1) / splits);
 
@@ -359,11 +353,9 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
   }
   __syncthreads();
 
-  float2 acc[2][NT][2];
+  float2 acc[2][2];
 #pragma unroll
-  for (int r = 0; r < 2; ++r)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) acc[r][n][0] = acc[r][n][1] = make_float2(0.0f, 0.0f);
+  for (int r = 0; r < 2; ++r) acc[r][0] = acc[r][1] = make_float2(0.0f, 0.0f);
   const int g = lane >> 2, t = lane & 3, part = warp / groups, wr = warp - part * groups;
 
   if (warp == kMmaWarps) {
@@ -376,12 +368,12 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
       const uint32_t round = (uint32_t)((s - s0) / ST);
       if (round && !wait_bar(empty + 8 * i, (round - 1) & 1, &ctl->abort)) break;
       const int64_t k0 = (int64_t)s * kStageK;
-      if (!a.mma) convert_sw<NV>(a, groups, n0, k0, lane, sws + i * S::kSw);
-      convert_x<TT>(a, m0, tokens, k0, lane, xs + i * S::kX, sxs + i * (S::kSx / 4));
+      if (!a.mma) convert_sw<NV>(a, n0, k0, lane, sws + i * S::kSw);
+      convert_x(a, m0, tokens, k0, lane, xs + i * S::kX, sxs + i * (S::kSx / 4));
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(full_x + 8 * i);
     }
-  } else if (warp < mma_warps) {
+  } else {
     // ---- multiplying warps: rows 32 wr .. 32 wr + 31, 32-blocks 4 part .. 4 part + 3 of every stage.
     // Blocks past K need no case of their own: their codes (TMA's fill), their x and its factor are
     // finite (zeros), and their scales are taken as zero bytes.
@@ -392,7 +384,7 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
     const int64_t nw = n0 + 32 * wr;
     const uint32_t tile = a.mma ? (uint32_t)((nw >> 7) - (n0 >> 7)) : 0u, quarter = a.mma ? (uint32_t)(nw >> 5) & 3u : wr;
     const uint32_t swoff = tile * (S::kSw / 2) + part * (NV ? 1024 : 512) + g * 16 + quarter * 4;
-    const uint32_t xoff = 4 * part * (TT * 64) + g * 64 + t * 16, sxoff = 4 * part * TT + 2 * t;
+    const uint32_t xoff = 4 * part * (kTokens * 64) + g * 64 + t * 16, sxoff = 4 * part * kTokens + 2 * t;
     int i = 0;
     uint32_t parity = 0;
     for (int s = s0; s < s1; ++s) {
@@ -432,20 +424,17 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
             f[j] = __uint_as_float((b & 1) ? sc[j][b >> 1] & 0xFFFF0000u : sc[j][b >> 1] << 16);
           }
         }
+        const uint4 v = *reinterpret_cast<const uint4*>(x + b * (kTokens * 64));
+        const float2 fx = *reinterpret_cast<const float2*>(sx + b * kTokens);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const uint4 v = *reinterpret_cast<const uint4*>(x + b * (TT * 64) + n * 512);
-          const float2 fx = *reinterpret_cast<const float2*>(sx + b * TT + n * 8);
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            mma16816(c, q[2 * r][0], q[2 * r + 1][0], q[2 * r][1], q[2 * r + 1][1], v.x, v.y);
-            mma16816(c, q[2 * r][2], q[2 * r + 1][2], q[2 * r][3], q[2 * r + 1][3], v.z, v.w);
-            const float2 p0 = NV ? fx : f2mul(fx, make_float2(f[2 * r], f[2 * r]));
-            const float2 p1 = NV ? fx : f2mul(fx, make_float2(f[2 * r + 1], f[2 * r + 1]));
-            acc[r][n][0] = f2fma(make_float2(c[0], c[1]), p0, acc[r][n][0]);
-            acc[r][n][1] = f2fma(make_float2(c[2], c[3]), p1, acc[r][n][1]);
-          }
+        for (int r = 0; r < 2; ++r) {
+          float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          mma16816(c, q[2 * r][0], q[2 * r + 1][0], q[2 * r][1], q[2 * r + 1][1], v.x, v.y);
+          mma16816(c, q[2 * r][2], q[2 * r + 1][2], q[2 * r][3], q[2 * r + 1][3], v.z, v.w);
+          const float2 p0 = NV ? fx : f2mul(fx, make_float2(f[2 * r], f[2 * r]));
+          const float2 p1 = NV ? fx : f2mul(fx, make_float2(f[2 * r + 1], f[2 * r + 1]));
+          acc[r][0] = f2fma(make_float2(c[0], c[1]), p0, acc[r][0]);
+          acc[r][1] = f2fma(make_float2(c[2], c[3]), p1, acc[r][1]);
         }
       }
       // The loads above have to be done before the slot goes back to the producer. The arrival alone
@@ -464,18 +453,16 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
   __syncthreads();  // every load has landed and been read (or the CTA has aborted)
   const bool ok = *reinterpret_cast<volatile uint32_t*>(&ctl->abort) == 0;
   float* const red = reinterpret_cast<float*>(ws);  // [part][token][rows + 4]
-  const int ld = rows + 4, plane = TT * ld;
+  constexpr int ld = rows + 4, plane = kTokens * ld;
   if (ok && warp < mma_warps) {
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float* d = red + part * plane + (8 * n + 2 * t) * ld + 32 * wr + 16 * r + 8 * c + g;
-          d[0] = acc[r][n][c].x;
-          d[ld] = acc[r][n][c].y;
-        }
+      for (int c = 0; c < 2; ++c) {
+        float* d = red + part * plane + 2 * t * ld + 32 * wr + 16 * r + 8 * c + g;
+        d[0] = acc[r][c].x;
+        d[ld] = acc[r][c].y;
+      }
   }
   __syncthreads();
   finish(a, red, ld, plane, kParts, rows, tokens, rank, splits, n0, m0, NV ? a.p2k : 1.0f, nullptr, ok);
@@ -502,15 +489,16 @@ constexpr int kTcStages = 3;                // of kStageK
 constexpr int kTcK = 64;                    // K per tensor-core buffer
 constexpr int kTcBufs = 4, kTcBufsX = 4;    // of the weights (tensor memory), of x (shared memory)
 constexpr int kTcDeq = 8, kTcConv = 4;      // converting warps: weights, x
-// Sums kept in tensor memory, one for each of a buffer's four products, added
-// at the end: the tensor cores round every K = 16 step of a sum toward zero, so
+// Sums kept in tensor memory, two to an issuing thread, in turn, added at the
+// end: the tensor cores round every K = 16 step of a sum toward zero, so
 // one sum over all of K drifts by up to K / 16 units of its last place
 // (measured: 1.1e-5 of sum |x w| at K = 16384), and four by a quarter of that.
 constexpr int kTcSums = 4;
 // tensor-memory columns: the sums, then the buffers of the weights
 constexpr uint32_t kTcA = kTcSums * kTcTokens, kTcACols = kTcK / 2, kTcTmem = kTcA + kTcBufs * kTcACols;
 static_assert(kTcTmem == 256, "two CTAs an SM");
-constexpr int kTcThreads = (kTcDeq + 2 + kTcConv) * 32;
+constexpr int kTcIss = 2;                   // threads that issue products: the even and the odd buffers
+constexpr int kTcThreads = (kTcDeq + 1 + kTcIss + kTcConv) * 32;
 constexpr int kTcB = kTcTokens * kTcK * 2;
 
 struct TcCtl {
@@ -644,7 +632,7 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ C
       ptx::mbar_init(full_b + 8 * i, 1);
       ptx::mbar_init(empty_b + 8 * i, 1);
     }
-    ptx::mbar_init(acc_full, 1);
+    ptx::mbar_init(acc_full, kTcIss);
     ctl->abort = 0;
     ptx::fence_mbar_init();
   }
@@ -660,21 +648,24 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ C
   if (warp == kTcDeq) {
     if (lane == 0) produce<NV, kTcStages>(tm, a, n0, kRows, s0, s1, ws, sws, full_w, empty_w, &ctl->abort);
     __syncwarp();
-  } else if (warp == kTcDeq + 1) {
-    // ---- the thread that issues the products
+  } else if (warp > kTcDeq && warp <= kTcDeq + kTcIss) {
+    // ---- the threads that issue the products; a slot of the rings is always the same one's
     if (lane == 0) {
       // bf16 operands (1 at bits 7 and 10; f16: 0), fp32 sums (1 at bit 4), K-major, N / 8 and M / 16
       const uint32_t idesc = (1u << 4) | (kF16 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)(cols_n >> 3) << 17) | ((kRows >> 4) << 24);
-      for (int b = 0; b < bufs; ++b) {
+      const int me = warp - kTcDeq - 1;
+      const uint64_t b0 = ptx::smem_desc(ptx::smem_u32(bs), 16, 1024, 2);
+      for (int b = me; b < bufs; b += kTcIss) {
         const int i = b % kTcBufs, ix = b % kTcBufsX;
         if (!wait_bar(full_a + 8 * i, (uint32_t)(b / kTcBufs) & 1, &ctl->abort) ||
             !wait_bar(full_b + 8 * ix, (uint32_t)(b / kTcBufsX) & 1, &ctl->abort))
           break;
         ptx::tc_fence_after();
+        const uint64_t bd = b0 + (uint32_t)ix * (kTcB >> 4);
 #pragma unroll
         for (int k = 0; k < kTcK / 16; ++k)
-          ptx::mma_f16_ta(tmem + k * kTcTokens, tmem + kTcA + i * kTcACols + k * 8,
-                          ptx::smem_desc(ptx::smem_u32(bs + ix * kTcB) + k * 32, 16, 1024, 2), idesc, b != 0);
+          ptx::mma_f16_ta(tmem + (2 * me + (k & 1)) * kTcTokens, tmem + kTcA + i * kTcACols + k * 8, bd + 2 * k, idesc,
+                          b != me || k > 1);
         ptx::tc_commit(empty_a + 8 * i);
         ptx::tc_commit(empty_b + 8 * ix);
       }
@@ -686,9 +677,9 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ C
       }
     }
     __syncwarp();
-  } else if (kF16 && warp > kTcDeq + 1) {
+  } else if (kF16 && warp > kTcDeq + kTcIss) {
     // ---- x by TMA, once the rows are written
-    if (warp == kTcDeq + 2 && lane == 0) {
+    if (warp == kTcDeq + kTcIss + 1 && lane == 0) {
       ptx::wait_prior_grid();
       for (int b = 0; b < bufs; ++b) {
         const int i = b % kTcBufsX;
@@ -703,14 +694,14 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ C
       }
     }
     __syncwarp();
-  } else if (warp > kTcDeq + 1) {
+  } else if (warp > kTcDeq + kTcIss) {
     // ---- x: whole buffers in turn, a lane eight elements (16 bytes of bf16) of every fourth row,
     // in the weights' order. A buffer's loads are all in flight before its slot is waited for.
     const int c = lane & 7;
     const int64_t x_bytes = a.x_kind == GemvArgs::kXBf16 ? 2 : 1, x_step = 4 * a.ld_x * x_bytes, s_step = 4 * (a.K >> 5);
     const uint8_t* const x_rows = static_cast<const uint8_t*>(a.x) + (m0 + (lane >> 3)) * a.ld_x * x_bytes;
     const uint8_t* const s_rows = a.sx + (m0 + (lane >> 3)) * (a.K >> 5);
-    for (int b = warp - kTcDeq - 2; b < bufs; b += kTcConv) {
+    for (int b = warp - kTcDeq - kTcIss - 1; b < bufs; b += kTcConv) {
       const int i = b % kTcBufsX;
       const uint32_t round = (uint32_t)(b / kTcBufsX);
       const int64_t k = (int64_t)s0 * kStageK + (int64_t)b * kTcK + 8 * c;
@@ -861,7 +852,7 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ C
   if (warp < 4) {
     for (int c = 0; c < cols_n; c += 16) {
       float f[16] = {};
-      for (int j = 0; j < kTcSums; ++j) {
+      for (int j = 0; j < (bufs > 1 ? kTcSums : kTcSums / kTcIss); ++j) {
         uint32_t v[16];
         ptx::tmem_ld_32x32b_x16(tmem + ((uint32_t)(32 * warp) << 16) + j * kTcTokens + c, v);
         ptx::tc_wait_ld();
@@ -911,17 +902,14 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ C
 constexpr int kMxN = 96;                    // most digit rows per CTA
 constexpr int kMxK = 128;
 constexpr int kMxA = kRows * kMxK, kMxTile = 512;
-#ifndef ISS32
-#define ISS32 2
-#endif
-constexpr int kMxEpi = 4, kMxConv = 4;      // warps: sums out of tensor memory, row-major scales
+// threads that issue products; warps: sums out of tensor memory, row-major scales
+constexpr int kMxIss = 2, kMxEpi = 4, kMxConv = 4;
+constexpr int kMxThreads = (2 + kMxIss + kMxEpi + kMxConv) * 32;
 template <int kN>
 struct MxRing {
   static constexpr int kB = kN * kMxK;
-  // issuing threads, and a multiple of them of slots
-  static constexpr int kIss = kN <= 32 ? ISS32 : 2;
-  static constexpr int kStages = kN <= 32 ? (ISS32 == 4 ? 8 : ISS32 == 3 ? 9 : 10) : kN <= 64 ? 8 : 6;
-  static constexpr int kThreads = (2 + kIss + kMxEpi + kMxConv) * 32;
+  static constexpr int kStages = kN <= 32 ? 10 : kN <= 64 ? 8 : 6;
+  static_assert(kStages % kMxIss == 0 && kStages >= kMxConv, "a slot is always the same issuing thread's");
   static constexpr int kBytes = kStages * (kMxA + kB + 2 * kMxTile) + 1024 + 512;
 };
 // Tensor-memory columns: two buffers of sums (one filled while the other leaves), and four slots of scales
@@ -1026,12 +1014,10 @@ __global__ void __launch_bounds__(256) gemv_digits_kernel(const GemvArgs a, cons
 }
 
 template <int kN>
-__global__ void __launch_bounds__(MxRing<kN>::kThreads, 1)
+__global__ void __launch_bounds__(kMxThreads, 1)
 gemv_mx_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const GemvArgs a,
                const MxShape sh) {
-  constexpr int ST = MxRing<kN>::kStages, kB = MxRing<kN>::kB, kMxIss = MxRing<kN>::kIss,
-                kMxThreads = MxRing<kN>::kThreads;
-  static_assert(ST % kMxIss == 0 && ST >= 4, "a slot is always the same issuing thread's");
+  constexpr int ST = MxRing<kN>::kStages, kB = MxRing<kN>::kB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const base = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
   // A of all stages, then B (both 1024-byte aligned), then the scale tiles
@@ -1345,20 +1331,19 @@ cudaError_t allow_smem(K kernel, int bytes, bool (&set)[kMaxDevices]) {
   return e;
 }
 
-bool codes_map(CUtensorMap* tm, const GemvArgs& a, int rows) {
-  return make_tma_2d(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.qw, a.N, a.K / 2, a.K / 2, rows, kRowBytes);
+bool codes_map(CUtensorMap* tm, const GemvArgs& a) {
+  return make_tma_2d(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.qw, a.N, a.K / 2, a.K / 2, kRows, kRowBytes);
 }
 
-template <int NT, bool NV>
-cudaError_t launch(const GemvArgs& a, int groups, int splits, cudaStream_t st) {
-  constexpr int bytes = Smem<8 * NT, NV>::kBytes;
+template <bool NV>
+cudaError_t launch_few(const GemvArgs& a, int splits, cudaStream_t st) {
+  constexpr int bytes = Smem<NV>::kBytes;
   static bool set[kMaxDevices] = {};
-  if (cudaError_t e = allow_smem(gemv_kernel<NT, NV>, bytes, set)) return e;
+  if (cudaError_t e = allow_smem(gemv_kernel<NV>, bytes, set)) return e;
   CUtensorMap tm;
-  if (!codes_map(&tm, a, 32 * groups)) return cudaErrorInvalidValue;
-  const dim3 grid((unsigned)((a.N + 32 * groups - 1) / (32 * groups)) * (unsigned)splits,
-                  (unsigned)((a.M + kMaxTokens - 1) / kMaxTokens));
-  return launch_cluster(gemv_kernel<NT, NV>, grid, kThreads, bytes, splits, false, st, tm, a, groups, splits);
+  if (!codes_map(&tm, a)) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)((a.N + kRows - 1) / kRows) * (unsigned)splits);
+  return launch_cluster(gemv_kernel<NV>, grid, kThreads, bytes, splits, false, st, tm, a, splits);
 }
 
 template <bool NV, bool kF16>
@@ -1367,7 +1352,7 @@ cudaError_t launch_tc(const GemvArgs& a, int splits, cudaStream_t st) {
   static bool set[kMaxDevices] = {};
   if (cudaError_t e = allow_smem(gemv_tc_kernel<NV, kF16>, bytes, set)) return e;
   CUtensorMap tm, tx;
-  if (!codes_map(&tm, a, kRows)) return cudaErrorInvalidValue;
+  if (!codes_map(&tm, a)) return cudaErrorInvalidValue;
   const TcX x = tc_x(a);
   if (kF16) {
     if (!make_tma_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.ws, (int64_t)x.tiles * x.n, a.K, a.K, x.n, kTcK))
@@ -1392,7 +1377,7 @@ cudaError_t launch_mx(const GemvArgs& a, const MxShape& sh, cudaStream_t st) {
     return cudaErrorInvalidValue;
   gemv_digits_kernel<<<dim3((unsigned)((a.K / 32 + 63) / 64), (unsigned)a.M), 256, 0, st>>>(a, sh);
   if (cudaError_t e = cudaGetLastError()) return e;
-  return launch_cluster(gemv_mx_kernel<kN>, dim3((unsigned)sh.ctas), MxRing<kN>::kThreads, MxRing<kN>::kBytes, 1, true, st, tw, tx,
+  return launch_cluster(gemv_mx_kernel<kN>, dim3((unsigned)sh.ctas), kMxThreads, MxRing<kN>::kBytes, 1, true, st, tw, tx,
                         a, sh);
 }
 
@@ -1403,20 +1388,36 @@ cudaError_t launch_mx(const GemvArgs& a, cudaStream_t st) {
 
 }  // namespace
 
+namespace {
+
 // Whether the MXFP8 products can take it: whole 128-deep steps of MXFP4 weights.
-static bool mx_fits(const GemvArgs& a) {
-  return !a.nv && a.M > 0 && a.M <= 32768 && a.N > 0 && a.K >= kMxK && a.K % kMxK == 0 && (reinterpret_cast<uintptr_t>(a.qw) & 31u) == 0;
+bool mx_fits(const GemvArgs& a) {
+  return !a.nv && a.M > 0 && a.M <= 32768 && a.N > 0 && a.K >= kMxK && a.K % kMxK == 0 &&
+         (reinterpret_cast<uintptr_t>(a.qw) & 31u) == 0;
 }
+
+// K is split over a cluster so that all CTAs (two an SM) end together: what counts is the rounds of CTAs
+// times a CTA's stages and what it costs besides them, about six (64 tiles of 32 stages, 23 rows: 32 us in one
+// slice, 19 in four, 24 in eight; 224 tiles: 50 us in one, 58 in three).
+int k_splits(const GemvArgs& a, int tokens) {
+  const int64_t tiles = (a.N + kRows - 1) / kRows * ((a.M + tokens - 1) / tokens), stages = (a.K + kStageK - 1) / kStageK;
+  int splits = 1;
+  int64_t best = INT64_MAX;
+  for (int n = 1; n <= 8 && n <= stages; ++n) {
+    const int64_t cost = (tiles * n + 2 * kSms - 1) / (2 * kSms) * ((stages + n - 1) / n + 6);
+    if (cost < best) {
+      best = cost;
+      splits = n;
+    }
+  }
+  return splits;
+}
+
+}  // namespace
 
 int64_t gemv_workspace_bytes(const GemvArgs& a) {
   if (mx_fits(a)) return mx_space(mx_shape(a)).bytes;
-  return a.nv && a.M > 8 && a.N > 0 && a.K > 0 ? tc_x(a).bytes : 0;
-}
-
-static cudaError_t tc(const GemvArgs& a, int splits, cudaStream_t st) {
-  if (!a.nv) return launch_tc<false, false>(a, splits, st);
-  return a.ws && a.ws_bytes >= (uint64_t)tc_x(a).bytes ? launch_tc<true, true>(a, splits, st)
-                                                       : launch_tc<true, false>(a, splits, st);
+  return a.nv && a.M > kTokens && a.N > 0 && a.K > 0 ? tc_x(a).bytes : 0;
 }
 
 cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t st) {
@@ -1426,32 +1427,17 @@ cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t st) {
     const size_t es = a.y_f32 ? 4 : 2;
     return cudaMemset2DAsync(a.y, a.ld_y * es, 0, a.N * es, a.M, st);
   }
-  const int nt = a.M <= 8 ? 1 : a.M <= 16 ? 2 : 4;
-  // K is split until two thirds of the SMs have a CTA (a CTA alone on its SM is
-  // bound by its own latency), and on to three CTAs an SM where each keeps 16
-  // stages to itself (shorter ones lose more to filling and emptying the ring).
-  const int64_t tiles = (a.N + kRows - 1) / kRows * ((a.M + kMaxTokens - 1) / kMaxTokens);
-  const int64_t stages = (a.K + kStageK - 1) / kStageK;
-  int groups = 4, splits = 1;
-  while (splits < 8 && ((3 * tiles * splits < 2 * kSms && 2 * splits <= stages) ||
-                        (2 * tiles * splits <= 3 * kSms && 32 * splits <= stages)))
-    splits *= 2;
-#ifdef GEMV_TUNE
-  if (getenv("GEMV_TC") && atoi(getenv("GEMV_TC")) == 2 && a.ws && mx_fits(a) && a.ws_bytes >= (uint64_t)mx_space(mx_shape(a)).bytes) return launch_mx(a, st);
-  if (getenv("GEMV_TC") && atoi(getenv("GEMV_TC"))) {
-    splits = atoi(getenv("GEMV_S"));
-    return tc(a, splits, st);
+  const bool space = a.ws && a.ws_bytes >= (uint64_t)gemv_workspace_bytes(a);
+  if (space && mx_fits(a)) return launch_mx(a, st);
+  // One N of the products for up to eight rows of x (4096 x 4096: 7 us, 11 in tensor memory); from nine on the
+  // weights are converted once for all of them (16 rows, 28672 x 8192: 58 us and 75; with the workspace 32).
+  if (a.M <= kTokens) {
+    const int splits = k_splits(a, kTokens);
+    return a.nv ? launch_few<true>(a, splits, st) : launch_few<false>(a, splits, st);
   }
-  if (getenv("GEMV_R")) groups = atoi(getenv("GEMV_R"));
-  if (getenv("GEMV_S")) splits = atoi(getenv("GEMV_S"));
-#endif
-  if (a.ws && mx_fits(a) && a.ws_bytes >= (uint64_t)mx_space(mx_shape(a)).bytes) return launch_mx(a, st);
-  if (a.M > 8) return tc(a, splits, st);
-  if (a.nv)
-    return nt == 1 ? launch<1, true>(a, groups, splits, st)
-                   : nt == 2 ? launch<2, true>(a, groups, splits, st) : launch<4, true>(a, groups, splits, st);
-  return nt == 1 ? launch<1, false>(a, groups, splits, st)
-                 : nt == 2 ? launch<2, false>(a, groups, splits, st) : launch<4, false>(a, groups, splits, st);
+  const int splits = k_splits(a, kTcTokens);
+  if (!a.nv) return launch_tc<false, false>(a, splits, st);
+  return space ? launch_tc<true, true>(a, splits, st) : launch_tc<true, false>(a, splits, st);
 }
 
 cudaError_t read_gemv_error(uint32_t* err) {

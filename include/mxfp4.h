@@ -452,9 +452,10 @@ enum { MXFP4_GEMV_X_BF16 = 0, MXFP4_GEMV_X_E4M3 = 1, MXFP4_GEMV_X_E5M2 = 2 };
  *      sx [M, K/32] (the quantized outputs above).
  *  y   [M, N] in y_dtype, leading dimension ld_y >= N (any), aligned to its
  *      element.
- * Products are exact and summed in fp32 (in a fixed order) whatever x holds; a
- * NaN scale makes what it enters NaN. M may be 0 .. 65536 (the weights are
- * read again for every 32 rows of x), N any, K a multiple of 32, rows of x
+ * Products are exact (bf16 x above eight rows too; up to eight, x is taken to
+ * 2^-39 of its 32-block's largest magnitude) and summed in fp32, in a fixed
+ * order; a NaN scale makes what it enters NaN. M may be 0 .. 65536 (the weights
+ * are read again for every 32 rows of x), N any, K a multiple of 32, rows of x
  * multiples of 16 bytes; x, qw, sw 16-byte aligned. */
 mxfp4_status mxfp4_gemv(const void* x, int32_t x_kind, int64_t ld_x, const uint8_t* sx,
                         const uint8_t* qw, const uint8_t* sw, int32_t block, int32_t scale_layout,
@@ -462,16 +463,19 @@ mxfp4_status mxfp4_gemv(const void* x, int32_t x_kind, int64_t ld_x, const uint8
                         int32_t y_dtype, int64_t ld_y, void* stream);
 
 /* mxfp4_gemv with an optional workspace, caller-owned device memory, 16-byte
- * aligned (NULL or too small: not used). With at least
- * mxfp4_gemv_workspace_size(x_kind, block, M, N, K) bytes (0: none would be
- * used; E8M0 scales, K a multiple of 128 and a large W have one), and qw
- * 32-byte aligned, the product runs on the block-scaled MXFP8 tensor-core
- * instruction, which reads the 4-bit codes and their scales as they are; x is
- * first written to the workspace as the sum of three E4M3 vectors with block
- * scales (of one if it is MXFP8 codes already). That sum is x to 2^-26 of its
- * 32-block's largest magnitude; a row of x that holds an infinity or a NaN
- * gives NaN. The weights are read again for every 32 rows of bf16 x and every
- * 64 of codes. The workspace contents are scratch. */
+ * aligned (NULL or too small: not used), of mxfp4_gemv_workspace_size(x_kind,
+ * block, M, N, K) bytes (0: none would be used). It pays from about 2^25
+ * weights on (2^27 up to eight rows of x). Its contents are scratch.
+ *  E8M0 scales, K a multiple of 128 and qw 32-byte aligned: the product runs on
+ *    the block-scaled MXFP8 tensor-core instruction, which reads the 4-bit codes
+ *    and their scales as they are; x is first written to the workspace as the
+ *    sum of three E4M3 vectors with block scales (as it is, if it is MXFP8).
+ *    That sum is x to 2^-26 of its 32-block's largest magnitude; a row of x that
+ *    holds an infinity or a NaN gives NaN or infinities.
+ *  NVFP4 weights and more than eight rows: x is written there as f16 under one
+ *    power of two a row: x to 2^-39 of the row's largest magnitude.
+ * The weights are read again for every 32 rows of x (64 of MXFP8 codes with E8M0
+ * scales). */
 mxfp4_status mxfp4_gemv_ex(const void* x, int32_t x_kind, int64_t ld_x, const uint8_t* sx,
                            const uint8_t* qw, const uint8_t* sw, int32_t block,
                            int32_t scale_layout, int32_t tensor_exp, int64_t M, int64_t N,
