@@ -1,6 +1,7 @@
 """ctypes marshalling for libmxfp4.so: torch tensors in, pointers and sizes out.
 
-Nothing here computes: each function checks that tensors live on a CUDA
+Nothing here computes: each function (of the norm, activation and few-row
+calls, its C++ half in csrc/binding.cpp) checks that tensors live on a CUDA
 device with the expected dtype, contiguity and size (the C ABI takes raw
 pointers and cannot check extents), allocates outputs the caller did not
 pass, and forwards raw pointers plus the current CUDA stream to the C ABI.
@@ -521,69 +522,30 @@ def _on(stream, call, *args, **kw):
         return call(*args, **kw)
 
 
-# Code of a matrix's type in the C ABI. Small calls are bound by the host: what
-# follows keeps each argument to one look at it.
-_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
+# The calls below are small and frequent, so their checks, allocations and
+# marshalling are in C++ (csrc/binding.cpp -> _binding.so); each returns its
+# outputs, or the status of a call that the library refused.
+_FAST = ("mxfp4_rmsnorm_quantize", "mxfp4_rmsnorm_backward", "mxfp4_rmsnorm_backward_workspace_size",
+         "mxfp4_swiglu_quantize", "mxfp4_swiglu_backward", "mxfp4_gemv_ex", "mxfp4_gemv_workspace_size")
 
 
-def _dtype_of(t: torch.Tensor, name: str) -> int:
-    dt = _DTYPES.get(t.dtype)
-    if dt is None:
-        raise TypeError(f"{name} must be bfloat16 or float32 (got {t.dtype})")
-    return dt
+def _fast():
+    """The extension's functions and the table of the library in use."""
+    global _ext
+    if _ext is None:
+        try:
+            from . import _binding as _ext
+        except ImportError as e:
+            raise RuntimeError("the _binding extension is not built; run gemm_pt_block_gb300.build.build() "
+                               "(there is no fallback implementation)") from e
+    L = lib()
+    t = getattr(L, "_fast_table", None)
+    if t is None:
+        t = L._fast_table = _ext.make_table(*[ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in _FAST])
+    return _ext, t
 
 
-def _rows_ld(t: torch.Tensor, name: str, rows: int, cols: int, dev: int) -> int:
-    """Leading dimension of a matrix [rows, cols] on CUDA device `dev` with unit
-    column stride. The stride of a single row (or of an empty matrix) is never
-    used."""
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on device {dev} (got {t.device})")
-    if t.shape != (rows, cols):
-        raise ValueError(f"{name} must be [{rows}, {cols}] (got {list(t.shape)})")
-    ld, unit = t.stride()
-    if unit != 1 and cols > 1 and rows:
-        raise ValueError(f"{name} must have unit column stride")
-    return ld if rows > 1 and cols else cols
-
-
-def _device_of(t: torch.Tensor, name: str) -> int:
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D (got {list(t.shape)})")
-    return t.get_device()
-
-
-def _vector(t: torch.Tensor, name: str, n: int, dev: int) -> None:
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on device {dev} (got {t.device})")
-    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a contiguous vector of {n} elements (got {list(t.shape)})")
-
-
-def _dense(t: torch.Tensor, numel: int, dtype: torch.dtype, name: str, dev: int) -> None:
-    """A buffer of at least `numel` dense elements on device `dev`."""
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on device {dev} (got {t.device})")
-    if t.dtype != dtype or t.numel() < numel or not t.is_contiguous():
-        _buffer(t, numel, dtype, name)
-
-
-def _row_out(row: QuantParams, q, s, rows: int, cols: int, device, dev: int):
-    """Codes and scales of a quantized output, allocated or checked."""
-    if q is None:
-        q = torch.empty((rows, row.code_cols(cols)), dtype=torch.uint8, device=device)
-    else:
-        _dense(q, rows * row.code_cols(cols), torch.uint8, "q", dev)
-    if s is None:
-        s = _scales_out(rows, cols, row, device)
-    else:
-        _dense(s, scale_numel(rows, cols, row.block), torch.uint8, "s", dev)
-    return q, s
-
-
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_ext = None
 
 
 def mxfp4_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor | None = None,
@@ -603,46 +565,11 @@ def mxfp4_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor | None = None,
     if stream is not None:
         return _on(stream, mxfp4_rmsnorm_quantize, x, weight, row, residual=residual, eps=eps, y_dtype=y_dtype,
                    with_rstd=with_rstd, h=h, y=y, rstd=rstd, q=q, s=s)
-    dev = _device_of(x, "x")
-    device, dtype = x.device, x.dtype
-    rows, cols = x.shape
-    ldx, dt = _rows_ld(x, "x", rows, cols, dev), _dtype_of(x, "x")
-    ldr = ldh = ldy = cols
-    px, pr, pw, ph, py, ps = x.data_ptr(), None, None, None, None, None
-    wdt = ydt = DTYPE_F32
-    if residual is not None:
-        if residual.dtype != dtype:
-            raise TypeError(f"residual must have x's type {dtype} (got {residual.dtype})")
-        ldr, pr = _rows_ld(residual, "residual", rows, cols, dev), residual.data_ptr()
-        if h is None:
-            h = torch.empty((rows, cols), dtype=dtype, device=device)
-    if weight is not None:
-        _vector(weight, "weight", cols, dev)
-        wdt, pw = _dtype_of(weight, "weight"), weight.data_ptr()
-    if h is not None:
-        if h.dtype != dtype:
-            raise TypeError(f"h must have x's type {dtype} (got {h.dtype})")
-        ldh, ph = _rows_ld(h, "h", rows, cols, dev), h.data_ptr()
-    if y is None and y_dtype is not None:
-        y = torch.empty((rows, cols), dtype=y_dtype, device=device)
-    if y is not None:
-        ydt, ldy, py = _dtype_of(y, "y"), _rows_ld(y, "y", rows, cols, dev), y.data_ptr()
-    if rstd is not None:
-        _dense(rstd, rows, torch.float32, "rstd", dev)
-    elif with_rstd:
-        rstd = torch.empty(rows, dtype=torch.float32, device=device)
-    if rstd is not None:
-        ps = rstd.data_ptr()
-    if row is not None:
-        q, s = _row_out(row, q, s, rows, cols, device, dev)
-        rp, pq, pc = ctypes.byref(row._c()), q.data_ptr(), s.data_ptr()
-    else:
-        q = s = rp = pq = pc = None
-    st = lib().mxfp4_rmsnorm_quantize(px, dt, rows, cols, ldx, pr, ldr, pw, wdt, eps, ph, ldh, py, ydt, ldy, ps, rp,
-                                      pq, pc, _raw_stream(dev))
-    if st:
-        _check(st)
-    return q, s, y, h, rstd
+    f, t = _fast()
+    r = f.rmsnorm_quantize(t, x, weight, row, residual, eps, y_dtype, with_rstd, h, y, rstd, q, s)
+    if r.__class__ is int:
+        _check(r)
+    return r
 
 
 def mxfp4_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor | None, rstd: torch.Tensor,
@@ -656,47 +583,11 @@ def mxfp4_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tens
     if stream is not None:
         return _on(stream, mxfp4_rmsnorm_backward, dy, h, weight, rstd, dh=dh, dx=dx, dw=dw, with_dw=with_dw,
                    workspace=workspace)
-    dev = _device_of(h, "h")
-    device, dtype = h.device, h.dtype
-    rows, cols = h.shape
-    ldh, hdt = _rows_ld(h, "h", rows, cols, dev), _dtype_of(h, "h")
-    ldy, ydt = _rows_ld(dy, "dy", rows, cols, dev), _dtype_of(dy, "dy")
-    _dense(rstd, rows, torch.float32, "rstd", dev)
-    ldd = ldx = cols
-    pw = pd = pg = pws = None
-    if dh is not None:
-        if dh.dtype != dtype:
-            raise TypeError(f"dh must have h's type {dtype} (got {dh.dtype})")
-        ldd, pd = _rows_ld(dh, "dh", rows, cols, dev), dh.data_ptr()
-    if dx is None:
-        dx = torch.empty((rows, cols), dtype=dtype, device=device)
-    else:
-        if dx.dtype != dtype:
-            raise TypeError(f"dx must have h's type {dtype} (got {dx.dtype})")
-        ldx = _rows_ld(dx, "dx", rows, cols, dev)
-    wdt, nbytes = DTYPE_F32, 0
-    L = lib()
-    if weight is not None:
-        _vector(weight, "weight", cols, dev)
-        wdt, pw = _dtype_of(weight, "weight"), weight.data_ptr()
-        if dw is not None:
-            _dense(dw, cols, weight.dtype, "dw", dev)
-        elif with_dw:
-            dw = torch.empty(cols, dtype=weight.dtype, device=device)
-    elif dw is not None:
-        raise ValueError("dw needs a weight")
-    if dw is not None:
-        nbytes = L.mxfp4_rmsnorm_backward_workspace_size(rows, cols)
-        if workspace is None:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        else:
-            _dense(workspace, nbytes, torch.uint8, "workspace", dev)
-        pg, pws = dw.data_ptr(), workspace.data_ptr()
-    st = L.mxfp4_rmsnorm_backward(dy.data_ptr(), ydt, ldy, h.data_ptr(), hdt, ldh, pw, wdt, rstd.data_ptr(), pd, ldd,
-                                  rows, cols, dx.data_ptr(), ldx, pg, pws, nbytes, _raw_stream(dev))
-    if st:
-        _check(st)
-    return dx, dw
+    f, t = _fast()
+    r = f.rmsnorm_backward(t, dy, h, weight, rstd, dh, dx, dw, with_dw, workspace)
+    if r.__class__ is int:
+        _check(r)
+    return r
 
 
 def mxfp4_swiglu_quantize(gate: torch.Tensor, up: torch.Tensor, row: QuantParams | None = None, *,
@@ -707,28 +598,11 @@ def mxfp4_swiglu_quantize(gate: torch.Tensor, up: torch.Tensor, row: QuantParams
     what was not asked for."""
     if stream is not None:
         return _on(stream, mxfp4_swiglu_quantize, gate, up, row, y_dtype=y_dtype, y=y, q=q, s=s)
-    dev = _device_of(gate, "gate")
-    device = gate.device
-    rows, cols = gate.shape
-    ldg, dt = _rows_ld(gate, "gate", rows, cols, dev), _dtype_of(gate, "gate")
-    if up.dtype != gate.dtype:
-        raise TypeError(f"up must have gate's type {gate.dtype} (got {up.dtype})")
-    ldu = _rows_ld(up, "up", rows, cols, dev)
-    if y is None and y_dtype is not None:
-        y = torch.empty((rows, cols), dtype=y_dtype, device=device)
-    ydt, ldy, py = DTYPE_F32, cols, None
-    if y is not None:
-        ydt, ldy, py = _dtype_of(y, "y"), _rows_ld(y, "y", rows, cols, dev), y.data_ptr()
-    if row is not None:
-        q, s = _row_out(row, q, s, rows, cols, device, dev)
-        rp, pq, pc = ctypes.byref(row._c()), q.data_ptr(), s.data_ptr()
-    else:
-        q = s = rp = pq = pc = None
-    st = lib().mxfp4_swiglu_quantize(gate.data_ptr(), ldg, up.data_ptr(), ldu, dt, rows, cols, py, ydt, ldy, rp, pq,
-                                     pc, _raw_stream(dev))
-    if st:
-        _check(st)
-    return q, s, y
+    f, t = _fast()
+    r = f.swiglu_quantize(t, gate, up, row, y_dtype, y, q, s)
+    if r.__class__ is int:
+        _check(r)
+    return r
 
 
 def mxfp4_swiglu_backward(dy: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, *, dgate=None, dup=None,
@@ -737,31 +611,11 @@ def mxfp4_swiglu_backward(dy: torch.Tensor, gate: torch.Tensor, up: torch.Tensor
     (bf16 or fp32). dgate may be gate itself and dup up itself."""
     if stream is not None:
         return _on(stream, mxfp4_swiglu_backward, dy, gate, up, dgate=dgate, dup=dup)
-    dev = _device_of(gate, "gate")
-    dtype = gate.dtype
-    rows, cols = gate.shape
-    ldg, dt = _rows_ld(gate, "gate", rows, cols, dev), _dtype_of(gate, "gate")
-    ldu, ldy, ydt = _rows_ld(up, "up", rows, cols, dev), _rows_ld(dy, "dy", rows, cols, dev), _dtype_of(dy, "dy")
-    if dgate is None:
-        dgate = torch.empty((rows, cols), dtype=dtype, device=gate.device)
-    if dup is None:
-        dup = torch.empty((rows, cols), dtype=dtype, device=gate.device)
-    if not up.dtype == dgate.dtype == dup.dtype == dtype:
-        raise TypeError(f"up, dgate and dup must have gate's type {dtype} (got {up.dtype}, {dgate.dtype}, {dup.dtype})")
-    st = lib().mxfp4_swiglu_backward(
-        dy.data_ptr(), ydt, ldy, gate.data_ptr(), ldg, up.data_ptr(), ldu, dt, rows, cols, dgate.data_ptr(),
-        _rows_ld(dgate, "dgate", rows, cols, dev), dup.data_ptr(), _rows_ld(dup, "dup", rows, cols, dev),
-        _raw_stream(dev))
-    if st:
-        _check(st)
-    return dgate, dup
-
-
-# Weights from which a workspace gains: above eight rows of x, and up to eight
-# (measured at 4096 x 4096: 12 us without, 15 with; 14336 x 4096: 26 and 20;
-# with one row 8192 x 8192: 12 and 16; 28672 x 8192: 32 and 29).
-_GEMV_WORKSPACE_FROM, _GEMV_WORKSPACE_FROM_FEW = 1 << 25, 1 << 27
-_GEMV_CODES = {FORMAT_E4M3: 1, FORMAT_E5M2: 2}     # MXFP4_GEMV_X_*; bf16 is 0
+    f, t = _fast()
+    r = f.swiglu_backward(t, dy, gate, up, dgate, dup)
+    if r.__class__ is int:
+        _check(r)
+    return r
 
 
 def mxfp4_gemv(x: torch.Tensor, qw: torch.Tensor, sw: torch.Tensor, N: int, K: int,
@@ -781,48 +635,11 @@ def mxfp4_gemv(x: torch.Tensor, qw: torch.Tensor, sw: torch.Tensor, N: int, K: i
     if stream is not None:
         return _on(stream, mxfp4_gemv, x, qw, sw, N, K, w, sx=sx, x_format=x_format, out_dtype=out_dtype, y=y,
                    workspace=workspace)
-    w = QuantParams() if w is None else w
-    if w.elem_format != FORMAT_E2M1:
-        raise ValueError("the weights must be 4-bit (E2M1) codes")
-    dev = _device_of(x, "x")
-    M = x.shape[0]
-    ldx = _rows_ld(x, "x", M, K, dev)
-    kind, psx = 0, None
-    if x.dtype == torch.bfloat16:
-        if sx is not None:
-            raise ValueError("sx goes with one-byte codes; x is bfloat16")
-    elif x.dtype == torch.uint8:
-        if sx is None:
-            raise ValueError("one-byte codes need their scales sx")
-        kind = _GEMV_CODES.get(x_format)
-        if kind is None:
-            raise ValueError(f"x_format {x_format} is not E4M3 or E5M2")
-        _dense(sx, M * (K // 32), torch.uint8, "sx", dev)
-        psx = sx.data_ptr()
-    else:
-        raise TypeError(f"x must be bfloat16 or uint8 codes (got {x.dtype})")
-    _dense(qw, N * K // 2, torch.uint8, "qw", dev)
-    _dense(sw, scale_numel(N, K, w.block), torch.uint8, "sw", dev)
-    ldy = N
-    if y is None:
-        y = torch.empty((M, N), dtype=out_dtype, device=x.device)
-    else:
-        ldy = _rows_ld(y, "y", M, N, dev)
-    L, pws, nbytes = lib(), None, 0
-    if workspace is None:
-        if N * K >= (_GEMV_WORKSPACE_FROM if M > 8 else _GEMV_WORKSPACE_FROM_FEW):
-            nbytes = L.mxfp4_gemv_workspace_size(kind, w.block, M, N, K)
-            if nbytes:
-                workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-                pws = workspace.data_ptr()
-    elif workspace is not False:
-        _dense(workspace, 0, torch.uint8, "workspace", dev)
-        pws, nbytes = workspace.data_ptr(), workspace.numel()
-    st = L.mxfp4_gemv_ex(x.data_ptr(), kind, ldx, psx, qw.data_ptr(), sw.data_ptr(), w.block, w.scale_layout,
-                         w.tensor_exp, M, N, K, y.data_ptr(), _dtype_of(y, "y"), ldy, pws, nbytes, _raw_stream(dev))
-    if st:
-        _check(st)
-    return y
+    f, t = _fast()
+    r = f.gemv(t, x, qw, sw, N, K, w, sx, x_format, out_dtype, y, workspace)
+    if r.__class__ is int:
+        _check(r)
+    return r[0]
 
 
 def device_status(stream=None) -> int:

@@ -1,9 +1,11 @@
 """Builds libmxfp4.so in place with nvcc for sm_103a (GB300).
 
 Each translation unit is compiled in parallel, then linked into one shared
-library with a static CUDA runtime. The quantizer unit is compiled with
-``--fmad=false`` (its arithmetic must not be contracted; it also uses explicit
-round-to-nearest intrinsics) and nothing is built with flush-to-zero.
+library with a static CUDA runtime; the Python extension _binding.so (host C++,
+against PyTorch's headers and libraries) is compiled beside them. The quantizer
+unit is compiled with ``--fmad=false`` (its arithmetic must not be contracted; it
+also uses explicit round-to-nearest intrinsics) and nothing is built with
+flush-to-zero.
 """
 from __future__ import annotations
 
@@ -33,6 +35,25 @@ UNITS = {
     "gemv.cu": [],
 }
 HEADERS = ["internal.h", "mx_device.cuh", "ptx.cuh", "quant_device.cuh", "row_device.cuh", "tma_host.h"]
+
+BINDING = os.path.join(HERE, "_binding.so")
+
+
+def _binding_command() -> list[str]:
+    """Compiles csrc/binding.cpp against the installed PyTorch."""
+    import sysconfig
+
+    import torch
+
+    t = os.path.join(os.path.dirname(torch.__file__), "include")
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            f"-I{t}", f"-I{os.path.join(t, 'torch', 'csrc', 'api', 'include')}",
+            f"-I{sysconfig.get_paths()['include']}", f"-I{os.path.join(cuda, 'include')}",
+            os.path.join(CSRC, "binding.cpp"), f"-L{lib}", f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
+            "-ltorch_python", "-o"]
 
 
 def nvcc() -> str:
@@ -64,18 +85,27 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False,
                 cmd.insert(1, "-Xptxas=-v")
             jobs.append(cmd)
 
+    # (the bounds-checking library is called through the same extension)
+    ext = None
+    src = os.path.join(CSRC, "binding.cpp")
+    if not bounds_check and (force or _stale(BINDING, [src, __file__, os.path.join(ROOT, "include", "mxfp4.h")])):
+        ext = BINDING + f".{os.getpid()}.tmp"
+        jobs.append([*_binding_command(), ext])
+
     def run(cmd):
         if verbose:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
 
-    with ThreadPoolExecutor(max_workers=len(UNITS)) as ex:
+    with ThreadPoolExecutor(max_workers=len(UNITS) + 1) as ex:
         for cmd, r in ex.map(run, jobs):
             if verbose or ptxas_v or r.returncode:
                 sys.stderr.write(r.stdout + r.stderr)
             if r.returncode:
-                raise RuntimeError(f"nvcc failed: {' '.join(cmd)}")
+                raise RuntimeError(f"compilation failed: {' '.join(cmd)}")
+    if ext is not None:
+        os.replace(ext, BINDING)
     if force or jobs or _stale(lib_out, objs):
         tmp = lib_out + f".{os.getpid()}.tmp"
         cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
