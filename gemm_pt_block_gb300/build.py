@@ -53,7 +53,7 @@ def _binding_command() -> list[str]:
             f"-I{t}", f"-I{os.path.join(t, 'torch', 'csrc', 'api', 'include')}",
             f"-I{sysconfig.get_paths()['include']}", f"-I{os.path.join(cuda, 'include')}",
             os.path.join(CSRC, "binding.cpp"), f"-L{lib}", f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
-            "-ltorch_python", "-o"]
+            "-ltorch_cuda", "-ltorch_python", "-o"]
 
 
 def nvcc() -> str:

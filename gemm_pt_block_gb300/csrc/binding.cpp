@@ -6,7 +6,7 @@
 // come as a table of addresses, so that any build of it can be called.
 #define PY_SSIZE_T_CLEAN
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -132,9 +132,10 @@ struct Unlocked {
   ~Unlocked() { PyEval_RestoreThread(state); }
 };
 
+// (without the dispatcher's way to the same allocation)
 at::Tensor empty(at::IntArrayRef sizes, at::ScalarType type, const at::Tensor& like) {
   Unlocked u;
-  return at::empty(sizes, at::TensorOptions().dtype(type).device(like.device()));
+  return at::detail::empty_cuda(sizes, type, like.device(), std::nullopt);
 }
 
 // A call of the library.
