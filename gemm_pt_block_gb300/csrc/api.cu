@@ -495,7 +495,7 @@ mxfp4_status mxfp4_rmsnorm_quantize(const void* x, int32_t x_dtype, int64_t rows
 
 size_t mxfp4_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols) {
   if (rows <= 0 || cols <= 0 || cols >= ((int64_t)1 << 31)) return 0;
-  return (size_t)mx::norm_dw_slices(rows, cols) * (size_t)cols * sizeof(float);
+  return (size_t)mx::norm_dw_slices(rows) * (size_t)cols * sizeof(float);
 }
 
 mxfp4_status mxfp4_rmsnorm_backward(const void* dy, int32_t dy_dtype, int64_t ld_dy, const void* h, int32_t h_dtype,

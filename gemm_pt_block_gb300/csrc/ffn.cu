@@ -187,14 +187,17 @@ __global__ void __launch_bounds__(kRowThreads) norm_long_rows_kernel(const NormA
 //   dx = (dn - n mean(dn n)) rstd + dh,   dw = sum over rows of dy n
 // (dh: what reaches h past the norm, through the residual stream).
 //
-// One kernel reads dy, h and dh once: persistent CTAs take rows in turn, whole
-// rows come by bulk copies into a ring of shared memory a few rows ahead, and
-// every thread keeps its columns' part of dw in registers over all of its
-// CTA's rows. The CTAs' parts go to the workspace and a second kernel sums
-// them in order (no atomics: dw has the same bits on every call).
+// One kernel reads dy, h and dh once: one persistent CTA an SM, whose threads
+// form up to twelve groups that take rows in turn. Whole rows come by bulk copies
+// into the group's ring of shared memory, a few rows ahead, and every thread keeps
+// its columns' part of dw in registers over all of its group's rows. The groups'
+// parts are added in shared memory, the CTAs' parts go to the workspace and a
+// second kernel sums them, all in order (no atomics: dw has the same bits on
+// every call).
 constexpr int kGradChunks = 2;
 constexpr int kGradSmem = 192 << 10;    // of the SM's 228 KB
 constexpr int kGradMaxStages = 8;
+constexpr int kGradMaxGroups = 12;      // (a hardware barrier each; 16384 x 1024: 8 groups 29 us, 12 26, 15 27)
 constexpr int kSms = 152;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
@@ -217,56 +220,81 @@ __device__ __forceinline__ void load8_shared(const uint8_t* row, int64_t c, floa
   unpack8(v, f);
 }
 
+// Barrier and sum over the threads of one group (full warps); `part` has a place
+// for each of the CTA's warps.
+__device__ __forceinline__ void group_barrier(uint32_t group, uint32_t threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
+}
+__device__ __forceinline__ float group_sum(float v, float* part, uint32_t group, uint32_t threads) {
+  const uint32_t lane = threadIdx.x & 31, warps = threads >> 5;
+  part += group * warps;
+  v = warp_sum(v);
+  if (lane == 0) part[threadIdx.x >> 5] = v;
+  group_barrier(group, threads);
+  return warp_sum(lane < warps ? part[lane] : 0.0f);
+}
+
+// Keeps bf16 weights packed in their registers: unpacked ahead of the loop they
+// would take twice as many.
+__device__ __forceinline__ void hold(Vec8<uint16_t>& v) {
+  asm volatile("" : "+r"(v.a.x), "+r"(v.a.y), "+r"(v.a.z), "+r"(v.a.w));
+}
+__device__ __forceinline__ void hold(Vec8<float>&) {}
+
+// (what every thread would otherwise hold in registers)
+struct GradRing {
+  uint32_t stages, stage_bytes, dy_bytes, h_bytes, step;  // step: rows between a group's rows
+};
+
 template <typename T, typename G, typename W>
-__global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradArgs a, const int stages) {
+__global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradArgs a, const GradRing r) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float part[2][32];
-  __shared__ uint64_t full[kGradMaxStages];
-  const uint32_t bars = ptx::smem_u32(full), tid = threadIdx.x, warps = blockDim.x >> 5;
-  const uint32_t h_bytes = (uint32_t)a.cols * sizeof(T), d_bytes = (uint32_t)a.cols * sizeof(G);
-  const uint32_t stage_bytes = d_bytes + h_bytes * (a.dh ? 2u : 1u);
-  const uint64_t gstep = gridDim.x;
+  __shared__ uint64_t full[kGradMaxGroups * kGradMaxStages];
+  const uint32_t tid = threadIdx.x, group = threadIdx.y, cols = (uint32_t)a.cols, rows = (uint32_t)a.rows;
+  const uint32_t bars = ptx::smem_u32(full) + 8 * kGradMaxStages * group;
+  const uint32_t first = group * gridDim.x + blockIdx.x, slots = group * r.stages * r.stage_bytes;
   if (tid == 0) {
-    for (int i = 0; i < stages; ++i) ptx::mbar_init(bars + 8 * i, 1);
+    for (uint32_t i = 0; i < r.stages; ++i) ptx::mbar_init(bars + 8 * i, 1);
     ptx::fence_mbar_init();
   }
   __syncthreads();
-  auto fetch = [&](int64_t row, int slot) {
-    const uint32_t dst = ptx::smem_u32(ring) + slot * stage_bytes, bar = bars + 8 * slot;
-    ptx::mbar_arrive_expect_tx(bar, stage_bytes);
-    ptx::bulk_load(dst, static_cast<const G*>(a.dy) + row * a.ld_dy, d_bytes, bar);
-    ptx::bulk_load(dst + d_bytes, static_cast<const T*>(a.h) + row * a.ld_h, h_bytes, bar);
-    if (a.dh) ptx::bulk_load(dst + d_bytes + h_bytes, static_cast<const T*>(a.dh) + row * a.ld_dh, h_bytes, bar);
+  auto fetch = [&](int64_t row, uint32_t slot) {
+    const uint32_t dst = ptx::smem_u32(ring) + slots + slot * r.stage_bytes, bar = bars + 8 * slot;
+    ptx::mbar_arrive_expect_tx(bar, r.stage_bytes);
+    ptx::bulk_load(dst, static_cast<const G*>(a.dy) + row * a.ld_dy, r.dy_bytes, bar);
+    ptx::bulk_load(dst + r.dy_bytes, static_cast<const T*>(a.h) + row * a.ld_h, r.h_bytes, bar);
+    if (a.dh)
+      ptx::bulk_load(dst + r.dy_bytes + r.h_bytes, static_cast<const T*>(a.dh) + row * a.ld_dh, r.h_bytes, bar);
   };
   if (tid == 0)
-    for (int i = 0; i < stages && blockIdx.x + i * gstep < (uint64_t)a.rows; ++i) fetch(blockIdx.x + i * gstep, i);
+    for (uint32_t i = 0; i < r.stages && first + i * r.step < rows; ++i) fetch(first + i * r.step, i);
 
   Vec8<W> wv[kGradChunks];
   float acc[kGradChunks][8];
 #pragma unroll
   for (int i = 0; i < kGradChunks; ++i) {
-    const int64_t c = (int64_t)(i * blockDim.x + tid) * 8;
-    if (a.w && c < a.cols) load8_cached(static_cast<const W*>(a.w) + c, wv[i]);
+    const uint32_t c = (i * blockDim.x + tid) * 8;
+    if (a.w && c < cols) load8_cached(static_cast<const W*>(a.w) + c, wv[i]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
   }
-  int slot = 0, turn = 0;
-  uint32_t parity = 0;
-  float rstd = blockIdx.x < a.rows ? __ldg(a.rstd + blockIdx.x) : 0.0f;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gstep) {
-    const float next = row + gstep < a.rows ? __ldg(a.rstd + row + gstep) : 0.0f;
-    if (!wait_bar(bars + 8 * slot, parity)) break;  // every thread waits on the same bar: all give up alike
-    const uint8_t* dy = ring + slot * stage_bytes;
-    const uint8_t *h = dy + d_bytes, *dh = h + h_bytes;
+  uint32_t slot = 0, parity = 0, turn = 0;
+  float rstd = first < rows ? __ldg(a.rstd + first) : 0.0f;
+  for (uint32_t row = first; row < rows; row += r.step) {
+    const float next = row + r.step < rows ? __ldg(a.rstd + row + r.step) : 0.0f;
+    if (!wait_bar(bars + 8 * slot, parity)) break;  // all of the group wait on the same bar: all give up alike
+    const uint8_t* dy = ring + slots + slot * r.stage_bytes;
     // the row is read twice from shared memory: kept in registers between the
-    // passes, its values would leave too few for two CTAs an SM
+    // passes, its values would leave too few for 1024 threads an SM
     float n[8], d[8], f[8], sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < kGradChunks; ++i) {
-      const int64_t c = (int64_t)(i * blockDim.x + tid) * 8;
-      if (c < a.cols) {
+      hold(wv[i]);
+      const uint32_t c = (i * blockDim.x + tid) * 8;
+      if (c < cols) {
         load8_shared<G>(dy, c, d);
-        load8_shared<T>(h, c, n);
+        load8_shared<T>(dy + r.dy_bytes, c, n);
         if (a.w) unpack8(wv[i], f);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -276,19 +304,15 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradArgs a, c
         }
       }
     }
-    // one barrier a row: the partial sums alternate between two buffers, and
-    // past it every thread is done with the row before this one
-    const float mean = __fdiv_rn(block_sum(sum, part[turn], warps), (float)a.cols);
-    turn ^= 1;
-    if (warps == 1) __syncwarp();
-    const int64_t ahead = row + (stages - 1) * (int64_t)gstep;
-    if (tid == 0 && row != blockIdx.x && ahead < a.rows) fetch(ahead, slot == 0 ? stages - 1 : slot - 1);
+    // (the partial sums alternate between two buffers: one barrier here)
+    const float mean = __fdiv_rn(group_sum(sum, part[turn], group, blockDim.x), (float)cols);
+    turn ^= 1u;
 #pragma unroll
     for (int i = 0; i < kGradChunks; ++i) {
-      const int64_t c = (int64_t)(i * blockDim.x + tid) * 8;
-      if (c < a.cols) {
+      const uint32_t c = (i * blockDim.x + tid) * 8;
+      if (c < cols) {
         load8_shared<G>(dy, c, d);
-        load8_shared<T>(h, c, n);
+        load8_shared<T>(dy + r.dy_bytes, c, n);
         if (a.w) {
           unpack8(wv[i], f);
 #pragma unroll
@@ -297,7 +321,7 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradArgs a, c
 #pragma unroll
         for (int j = 0; j < 8; ++j) d[j] = __fmul_rn(__fmaf_rn(-__fmul_rn(n[j], rstd), mean, d[j]), rstd);
         if (a.dh) {
-          load8_shared<T>(dh, c, f);
+          load8_shared<T>(dy + r.dy_bytes + r.h_bytes, c, f);
 #pragma unroll
           for (int j = 0; j < 8; ++j) d[j] = __fadd_rn(d[j], f[j]);
         }
@@ -307,24 +331,55 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradArgs a, c
       }
     }
     rstd = next;
-    if (++slot == stages) {
+    // the slot's next row at once, for the price of a barrier: past the next
+    // row's own barrier instead, a ring of two slots would have no copy in flight
+    // while that row is read (16384 x 8192: 168 us; this way 156)
+    const uint32_t ahead = row + r.stages * r.step;
+    if (ahead < rows) {
+      group_barrier(group, blockDim.x);
+      if (tid == 0) fetch(ahead, slot);
+    }
+    if (++slot == r.stages) {
       slot = 0;
       parity ^= 1u;
     }
   }
-  if (a.dw) {
+  if (!a.dw) return;
+  if (blockDim.y == 1) {
 #pragma unroll
     for (int i = 0; i < kGradChunks; ++i) {
-      const int64_t c = (int64_t)(i * blockDim.x + tid) * 8;
-      if (c < a.cols) store8_as(a.ws, true, (int64_t)blockIdx.x * a.cols + c, acc[i], a.ws_bytes);
+      const uint32_t c = (i * blockDim.x + tid) * 8;
+      if (c < cols) store8_as(a.ws, true, (int64_t)blockIdx.x * cols + c, acc[i], a.ws_bytes);
     }
+    return;
+  }
+  // the ring holds no row any more; a slot is at least as large as a row of sums
+  __syncthreads();
+  float* sums = reinterpret_cast<float*>(ring);
+#pragma unroll
+  for (int i = 0; i < kGradChunks; ++i) {
+    const uint32_t c = (i * blockDim.x + tid) * 8;
+    if (c < cols) {
+      float4* to = reinterpret_cast<float4*>(sums + group * cols + c);
+      to[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+      to[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+    }
+  }
+  __syncthreads();
+  for (uint32_t c = (group * blockDim.x + tid) * 4; c < cols; c += blockDim.x * blockDim.y * 4) {
+    float4 t = *reinterpret_cast<const float4*>(sums + c);
+    for (uint32_t g = 1; g < blockDim.y; ++g) {
+      const float4 v = *reinterpret_cast<const float4*>(sums + g * cols + c);
+      t = make_float4(__fadd_rn(t.x, v.x), __fadd_rn(t.y, v.y), __fadd_rn(t.z, v.z), __fadd_rn(t.w, v.w));
+    }
+    put_at(reinterpret_cast<float4*>(a.ws + (int64_t)blockIdx.x * cols + c), t, a.ws, a.ws_bytes);
   }
 }
 
 // Short rows: a warp each, straight from HBM (eight warps a CTA, each with a
 // row's loads in flight), dw of the CTA's warps summed in order at the end.
 template <typename T, typename G, typename W, int kChunks>
-__global__ void __launch_bounds__(256, kChunks == 4 ? 1 : 2) norm_short_grad_kernel(const NormGradArgs a) {
+__global__ void __launch_bounds__(256, 2) norm_short_grad_kernel(const NormGradArgs a) {
   __shared__ float part[8][kChunks * 256];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Vec8<W> wv[kChunks];
@@ -473,22 +528,23 @@ __global__ void __launch_bounds__(kColThreads) norm_long_dw_kernel(const NormGra
   store8_as(a.ws, true, (int64_t)blockIdx.y * a.cols + c, acc, a.ws_bytes);
 }
 
-// dw from the partial sums: a CTA takes 32 columns, its eight warps every
-// eighth slice, and the warps' sums are added in order.
+// dw from the partial sums: a CTA takes 32 columns, its warps every kSumWarps'th
+// slice, and the warps' sums are added in order.
+constexpr int kSumWarps = 16;
 template <typename W>
-__global__ void __launch_bounds__(256) norm_dw_sum_kernel(const float* ws, int slices, int64_t cols, W* dw) {
-  __shared__ float part[8][32];
+__global__ void __launch_bounds__(kSumWarps * 32) norm_dw_sum_kernel(const float* ws, int slices, int64_t cols, W* dw) {
+  __shared__ float part[kSumWarps][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   float s = 0.0f;
 #pragma unroll 8
-  for (int i = warp; i < slices; i += 8) s = __fadd_rn(s, ws[i * cols + c]);
+  for (int i = warp; i < slices; i += kSumWarps) s = __fadd_rn(s, ws[i * cols + c]);
   part[warp][lane] = s;
   __syncthreads();
   if (warp) return;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) s = __fadd_rn(s, part[i][lane]);
+  for (int i = 1; i < kSumWarps; ++i) s = __fadd_rn(s, part[i][lane]);
   if (sizeof(W) == 4)
     put_at(dw + c, s, dw, cols * sizeof(W));
   else
@@ -627,28 +683,19 @@ void act_shape(int64_t rows, int64_t per_row, int64_t ctas, dim3* grid, dim3* bl
 bool aligned32(const void* p, int64_t ld_bytes) { return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)ld_bytes) & 31u) == 0; }
 
 // Rows of one warp; the CTAs that take them.
-constexpr int64_t kShortCols = 1024;
+constexpr int64_t kShortCols = 512;
 int64_t short_ctas(int64_t rows) {
   const int64_t ctas = (rows + 7) / 8;
   return ctas < 2 * kSms ? ctas : 2 * kSms;
 }
 
-// The ring kernel's shape for rows of `cols`: threads (kGradChunks vectors
-// each), and CTAs an SM so that about 1024 threads share it.
+// The ring kernel's threads for a row of `cols` (kGradChunks vectors each).
 int grad_threads(int64_t cols) { return (int)((cols / 8 + 32 * kGradChunks - 1) / (32 * kGradChunks) * 32); }
-int grad_ctas(int64_t cols) {
-  const int t = grad_threads(cols);
-  return t >= 1024 ? 1 : t <= 128 ? 8 : 1024 / t;
-}
 
 }  // namespace
 
 // Rows of partial sums that the workspace holds, for either way of taking dw.
-int norm_dw_slices(int64_t rows, int64_t cols) {
-  const int64_t ring = cols <= 1024 * 8 * kGradChunks ? (int64_t)kSms * grad_ctas(cols) : 0;
-  const int64_t most = ring > 2 * kSms ? ring : 2 * kSms;
-  return (int)(rows < most ? rows : most);
-}
+int norm_dw_slices(int64_t rows) { return (int)(rows < 2 * kSms ? rows : 2 * kSms); }
 
 namespace {
 template <typename T, typename W>
@@ -696,16 +743,12 @@ template <typename T, typename G, typename W>
 cudaError_t norm_grad(const NormGradArgs& a, cudaStream_t st) {
   int slices = 0;
   const int64_t stage = a.cols * (int64_t)(sizeof(G) + sizeof(T) * (a.dh ? 2 : 1));
-  int ctas = grad_ctas(a.cols);
-  while (ctas > 1 && 2 * stage * ctas > kGradSmem) --ctas;
   if (a.cols <= kShortCols) {
     slices = (int)short_ctas(a.rows);
     if (slices && a.cols <= 256)
       norm_short_grad_kernel<T, G, W, 1><<<slices, 256, 0, st>>>(a);
-    else if (slices && a.cols <= 512)
-      norm_short_grad_kernel<T, G, W, 2><<<slices, 256, 0, st>>>(a);
     else if (slices)
-      norm_short_grad_kernel<T, G, W, 4><<<slices, 256, 0, st>>>(a);
+      norm_short_grad_kernel<T, G, W, 2><<<slices, 256, 0, st>>>(a);
   } else if (a.cols <= 1024 * 8 * kGradChunks && 2 * stage <= kGradSmem) {
     if (a.rows > 0) {
       int dev = 0;
@@ -722,13 +765,18 @@ cudaError_t norm_grad(const NormGradArgs& a, cudaStream_t st) {
           set[dev] = true;
         }
       }
-      const int64_t fit = kGradSmem / (stage * ctas);
+      // groups: as many as there are threads, slots (two each) and rows for
+      const int threads = grad_threads(a.cols);
+      slices = (int)(a.rows < kSms ? a.rows : kSms);
+      int64_t groups = 1024 / threads, fit = kGradSmem / (2 * stage), each = (a.rows + kSms - 1) / kSms;
+      if (groups > kGradMaxGroups) groups = kGradMaxGroups;
+      if (groups > fit) groups = fit;
+      if (groups > each) groups = each;
+      fit = kGradSmem / (stage * groups);
       const int stages = (int)(fit < kGradMaxStages ? fit : kGradMaxStages);
-      // every CTA adds a row of partial sums to write and read: four rows of work to
-      // each of them, as long as every SM keeps a CTA
-      const int64_t want = a.rows / 4 > kSms ? a.rows / 4 : a.rows < kSms ? a.rows : kSms;
-      slices = (int)(want < (int64_t)kSms * ctas ? want : (int64_t)kSms * ctas);
-      norm_grad_kernel<T, G, W><<<slices, grad_threads(a.cols), stages * stage, st>>>(a, stages);
+      const GradRing r = {(uint32_t)stages, (uint32_t)stage, (uint32_t)(a.cols * sizeof(G)),
+                          (uint32_t)(a.cols * sizeof(T)), (uint32_t)(slices * groups)};
+      norm_grad_kernel<T, G, W><<<slices, dim3(threads, (unsigned)groups), stages * groups * stage, st>>>(a, r);
     }
   } else if (a.rows > 0) {
     norm_long_dx_kernel<T, G, W><<<(unsigned)a.rows, kRowThreads, 0, st>>>(a);
@@ -742,7 +790,7 @@ cudaError_t norm_grad(const NormGradArgs& a, cudaStream_t st) {
   // launched while the kernel before it drains; it waits for that kernel's sums itself
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.cols / 32));
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(kSumWarps * 32);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -68,7 +68,7 @@ struct NormGradArgs {
   const void *dy, *h, *w, *dh;  // w, dh: may be NULL
   const float* rstd;
   void *dx, *dw;                // dw: may be NULL
-  float* ws;                    // norm_dw_slices(rows, cols) x cols partial sums (with dw)
+  float* ws;                    // norm_dw_slices(rows) x cols partial sums (with dw)
   int64_t rows, cols, ld_dy, ld_h, ld_dh, ld_dx;
   uint64_t dx_bytes, ws_bytes;
 };
@@ -139,7 +139,7 @@ cudaError_t launch_gemm(const uint8_t* qa, const uint8_t* sa, const uint8_t* qb,
                         bool c_bf16, int64_t ldc, const OrientArgs* qout, const OrientArgs* qcol,
                         void* ws, size_t ws_bytes, cudaStream_t st, const char** why);
 cudaError_t launch_rmsnorm(const NormArgs& a, bool x_f32, bool w_f32, cudaStream_t st);
-int norm_dw_slices(int64_t rows, int64_t cols);
+int norm_dw_slices(int64_t rows);
 cudaError_t launch_rmsnorm_grad(const NormGradArgs& a, bool h_f32, bool dy_f32, bool w_f32, cudaStream_t st);
 cudaError_t launch_swiglu(const SwigluArgs& a, bool f32, cudaStream_t st);
 cudaError_t launch_swiglu_grad(const SwigluGradArgs& a, bool f32, bool dy_f32, cudaStream_t st);

@@ -248,6 +248,28 @@ def test_norm_backward(rows, cols, dt, gdt, wdt, stream, extra):
     assert mx.device_status() == 0
 
 
+@pytest.mark.parametrize("rows,cols,dt", [
+    (1825, 544, BF16), (40000, 1024, BF16), (151, 1024, F32), (153, 4096, BF16), (304, 2080, F32), (305, 8192, BF16),
+    (1300, 8192, BF16), (700, 8192, F32), (700, 16384, BF16)])
+def test_norm_backward_of_row_counts_around_the_sms_and_their_groups(rows, cols, dt):
+    """Each row's dx has the same bits alone and among others, whichever group
+    of threads and slot of its ring takes it; dw is the sum over all rows."""
+    import gemm_pt_block_gb300 as mx
+
+    h, dy, dh = rand(rows, cols, dt, 31), rand(rows, cols, dt, 32, 1e-2), rand(rows, cols, dt, 33, 1e-2)
+    w = (1 + 0.2 * torch.randn(cols, device=DEV)).to(dt)
+    rstd = mx.mxfp4_rmsnorm_quantize(h, None, with_rstd=True)[4]
+    dx, dw = mx.mxfp4_rmsnorm_backward(dy, h, w, rstd, dh=dh)
+    for lo in range(0, rows, 100):
+        hi = min(lo + 100, rows)
+        part, _ = mx.mxfp4_rmsnorm_backward(dy[lo:hi], h[lo:hi], w, rstd[lo:hi], dh=dh[lo:hi])
+        assert torch.equal(part, dx[lo:hi])
+    _, _, refw, magw = norm_grad_reference(dy, h, w, rstd, None)
+    tolw = (rows + 4) * U
+    assert ((dw.double() - refw).abs() <= tolw * magw + half_ulp(dt) * (refw.abs() + tolw * magw)).all()
+    assert mx.device_status() == 0
+
+
 def test_norm_backward_of_no_rows():
     import gemm_pt_block_gb300 as mx
 
