@@ -207,34 +207,112 @@ __device__ __forceinline__ void convert_x(const GemvArgs& a, int64_t m0, int tok
   }
 }
 
-// One stage of row-major weight scales, rearranged into the tensor-core tiles
-// (128 rows x 4 columns, 512 bytes) that the multiplying warps read: lane l
-// brings rows l, l + 32, l + 64, l + 96. Rows past N repeat the last one.
+// Row-major weight scales of one row and stage: kCols consecutive bytes, which
+// start at any address. Byte loads of them, each lane another row, filled the L1
+// (14336 x 4128, 12 rows: 28 us, and 16 at K = 4096); here the aligned words of
+// kCols bytes that hold them are loaded whole.
 template <bool NV>
-__device__ __forceinline__ void convert_sw(const GemvArgs& a, int64_t n0, int64_t k0, int lane, uint8_t* sws) {
-  constexpr int kCols = kStageK / (NV ? 16 : 32);
-  const int64_t cols = a.K / (NV ? 16 : 32), c0 = k0 / (NV ? 16 : 32);
-  uint32_t v[kCols / 4][4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint8_t* p = a.sw + min(n0 + lane + 32 * j, a.N - 1) * cols + c0;
-    if ((cols & 3) == 0) {
-#pragma unroll
-      for (int c = 0; c < kCols / 4; ++c)
-        v[c][j] = c0 + 4 * c < cols ? __ldg(reinterpret_cast<const uint32_t*>(p) + c) : 0u;
+struct RowScales {
+  static constexpr int kCols = kStageK / (NV ? 16 : 32), kWords = kCols / 4;
+  const uint8_t *p, *end;  // the aligned word of the first stage's scales; the end of the array
+  uint32_t off;            // of the scales in the word
+  int64_t cols;
+  __device__ __forceinline__ RowScales(const GemvArgs& a, int64_t n) : cols(a.K / (NV ? 16 : 32)) {
+    const uint8_t* row = a.sw + min(n, a.N - 1) * cols;  // rows past N repeat the last one
+    off = (uint32_t)reinterpret_cast<uintptr_t>(row) & (kCols - 1);
+    p = row - off;
+    end = a.sw + a.N * cols;
+  }
+  // Word s of the row (the array starts on a multiple of 16 bytes: none begins before it).
+  __device__ __forceinline__ void load(int s, uint32_t (&w)[kWords]) const {
+    const uint8_t* q = p + (int64_t)s * kCols;
+    if (q + kCols <= end) {
+      if (NV) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(q));
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2 % kWords] = v.z;
+        w[3 % kWords] = v.w;
+      } else {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(q));
+        w[0] = v.x;
+        w[1] = v.y;
+      }
     } else {
 #pragma unroll
-      for (int c = 0; c < kCols / 4; ++c) {
-        v[c][j] = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (c0 + 4 * c + i < cols) v[c][j] |= (uint32_t)__ldg(p + 4 * c + i) << (8 * i);
+      for (int i = 0; i < kCols; ++i) {
+        if ((i & 3) == 0) w[i >> 2] = 0;
+        if (q + i < end) w[i >> 2] |= (uint32_t)__ldg(q + i) << (8 * (i & 3));
       }
     }
   }
+  // Stage s's scales out of words s and s + 1 (not looked at when `off` is 0); zero bytes past K.
+  __device__ __forceinline__ void take(int s, const uint32_t (&lo)[kWords], const uint32_t (&hi)[kWords],
+                                       uint32_t (&out)[kWords]) const {
+    uint32_t w[2 * kWords];
 #pragma unroll
-  for (int c = 0; c < kCols / 4; ++c)
-    *reinterpret_cast<uint4*>(sws + c * 512 + lane * 16) = make_uint4(v[c][0], v[c][1], v[c][2], v[c][3]);
+    for (int i = 0; i < kWords; ++i) {
+      w[i] = lo[i];
+      w[kWords + i] = hi[i];
+    }
+    if (NV && (off & 8)) {
+#pragma unroll
+      for (int i = 0; i + 2 < 2 * kWords; ++i) w[i] = w[i + 2];
+    }
+    if (off & 4) {
+#pragma unroll
+      for (int i = 0; i + 1 < 2 * kWords; ++i) w[i] = w[i + 1];
+    }
+    const int64_t left = cols - (int64_t)s * kCols;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      out[i] = __funnelshift_r(w[i], w[i + 1], 8 * (off & 3));
+      if (left < 4 * i + 4) out[i] &= left <= 4 * i ? 0u : 0xFFFFFFFFu >> (32 - 8 * (int)(left - 4 * i));
+    }
+  }
+};
+
+// One stage of row-major weight scales, rearranged into the tensor-core tiles
+// (128 rows x 4 columns, 512 bytes) that the multiplying warps read: lane l
+// brings rows l, l + 32, l + 64, l + 96.
+template <bool NV>
+__device__ __forceinline__ void convert_sw(const GemvArgs& a, int64_t n0, int s, int lane, uint8_t* sws) {
+  using R = RowScales<NV>;
+  constexpr int kWords = R::kWords;
+  const int64_t cols = a.K / (NV ? 16 : 32), c0 = (int64_t)s * R::kCols;
+  uint32_t v[4][kWords];
+  if ((cols & 3) == 0) {
+    // rows of whole 4-byte words need no shifts (14336 x 4160, one row, NVFP4: 15.6 us, 16.8 below)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (cols % R::kCols == 0) {
+        R(a, n0 + lane + 32 * j).load(s, v[j]);
+      } else {
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(a.sw + min(n0 + lane + 32 * j, a.N - 1) * cols + c0);
+#pragma unroll
+        for (int c = 0; c < kWords; ++c) v[j][c] = c0 + 4 * c < cols ? __ldg(p + c) : 0u;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < kWords; ++c)
+      *reinterpret_cast<uint4*>(sws + c * 512 + lane * 16) = make_uint4(v[0][c], v[1][c], v[2][c], v[3][c]);
+    return;
+  }
+#pragma unroll
+  for (int h = 0; h < 4; h += 2) {  // two rows at a time: four take too many registers
+    uint32_t lo[2][kWords], hi[2][kWords];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const R row(a, n0 + lane + 32 * (h + j));
+      row.load(s, lo[j]);
+      row.load(s + 1, hi[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) R(a, n0 + lane + 32 * (h + j)).take(s, lo[j], hi[j], v[j]);
+#pragma unroll
+    for (int c = 0; c < kWords; ++c)
+      *reinterpret_cast<uint2*>(sws + c * 512 + lane * 16 + 4 * h) = make_uint2(v[0][c], v[1][c]);
+  }
 }
 
 // The producer thread: stages s0 .. s1 - 1 of the CTA's codes by TMA, and
@@ -368,7 +446,7 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
       const uint32_t round = (uint32_t)((s - s0) / ST);
       if (round && !wait_bar(empty + 8 * i, (round - 1) & 1, &ctl->abort)) break;
       const int64_t k0 = (int64_t)s * kStageK;
-      if (!a.mma) convert_sw<NV>(a, n0, k0, lane, sws + i * S::kSw);
+      if (!a.mma) convert_sw<NV>(a, n0, s, lane, sws + i * S::kSw);
       convert_x(a, m0, tokens, k0, lane, xs + i * S::kX, sxs + i * (S::kSx / 4));
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(full_x + 8 * i);
@@ -753,30 +831,20 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ C
     constexpr int kWords = NV ? 4 : 2;  // of a row's scales in a stage
     const int r = threadIdx.x & 127, half = threadIdx.x >> 7;
     const int64_t cols = a.K / kPer;
-    const uint8_t* row_sw = a.sw + min(n0 + r, a.N - 1) * cols;  // row-major scales
-    uint32_t sc[kWords] = {}, ahead[kWords] = {};
-    auto fetch = [&](int s) {  // row-major scales of stage s
-      const int64_t c0 = (int64_t)s * (kStageK / kPer);
-#pragma unroll
-      for (int e = 0; e < kWords; ++e) {
-        ahead[e] = 0;
-        if ((cols & 3) == 0) {
-          if (c0 + 4 * e < cols) ahead[e] = __ldg(reinterpret_cast<const uint32_t*>(row_sw + c0) + e);
-        } else {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (c0 + 4 * e + q < cols) ahead[e] |= (uint32_t)__ldg(row_sw + c0 + 4 * e + q) << (8 * q);
-        }
-      }
-    };
-    if (!a.mma) fetch(s0);
+    const RowScales<NV> row(a, n0 + r);  // row-major scales: words of this stage and of the next
+    uint32_t sc[kWords] = {}, now[kWords] = {}, ahead[kWords] = {};
+    if (!a.mma && s0 < s1) {
+      row.load(s0, now);
+      if (row.off || s0 + 1 < s1) row.load(s0 + 1, ahead);
+    }
     bool go = true;
     for (int st = 0; go && st < s1 - s0; ++st) {
       const int slot = st % kTcStages;
       if (!a.mma) {
+        row.take(s0 + st, now, ahead, sc);
 #pragma unroll
-        for (int e = 0; e < kWords; ++e) sc[e] = ahead[e];
-        if (st + 1 < s1 - s0) fetch(s0 + st + 1);
+        for (int e = 0; e < kWords; ++e) now[e] = ahead[e];
+        if (st + 1 < s1 - s0 && (row.off || st + 2 < s1 - s0)) row.load(s0 + st + 2, ahead);
       }
       if (!__all_sync(0xffffffffu, wait_bar(full_w + 8 * slot, (uint32_t)(st / kTcStages) & 1, &ctl->abort))) break;
       if (a.mma) {

@@ -240,6 +240,28 @@ def test_non_finite_values_stay_in_their_rows():
     assert torch.isnan(y4[:, 7]).all() and torch.isfinite(y4[:, :7]).all() and torch.isfinite(y4[:, 8:]).all()
 
 
+@pytest.mark.parametrize("K", [32, 96, 160, 544, 1056, 4128, 4160])
+@pytest.mark.parametrize("nv", [False, True], ids=["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("M", [3, 12])
+def test_scales_of_the_next_row_stay_out(M, nv, K):
+    """Rows of scales of any length, a NaN row after each finite one: what lies
+    past a row's end in memory enters nothing."""
+    import gemm_pt_block_gb300 as mx
+
+    N = 139
+    q, s, w64 = weights(N, K, nv, 41)
+    x, _, x64, _ = activations(M, K, "bf16", 42)
+    s = s.clone()
+    s[1::2] = 0x7F if nv else 255
+    y = mx.mxfp4_gemv(x, q, s, N, K, wparams(nv), out_dtype=F32, workspace=False)
+    check(y[:, ::2].contiguous(), x64, w64[::2])
+    assert torch.isnan(y[:, 1::2]).all()
+    space = torch.zeros(1 << 22, dtype=torch.uint8, device=DEV)
+    z = mx.mxfp4_gemv(x, q, s, N, K, wparams(nv), out_dtype=F32, workspace=space)
+    check(z[:, ::2].contiguous(), x64, w64[::2])
+    assert torch.isnan(z[:, 1::2]).all()
+
+
 @pytest.mark.parametrize("exp", [-100, -10, 0, 30])
 def test_tensor_exponent(exp):
     import gemm_pt_block_gb300 as mx
