@@ -48,6 +48,12 @@ __device__ __forceinline__ float sum8(const float (&f)[8]) {
 // back, differentiates the same function:
 //   y_i = (h_i w_i) rstd,   rstd = 1 / sqrt(sum h^2 / D + eps).
 // bf16 products h_i w_i are exact in fp32, so y has two roundings.
+//
+// A row stays in registers between the sum of squares and the output, so that
+// each input is read once: one warp a row up to 1024 columns, a CTA a row above
+// (up to 32 columns a thread), two passes over rows that registers do not hold.
+// Bound by HBM: 16384 x 8192 bf16 with residual, E4M3 codes, 152 us (6.2 TB/s,
+// 93 % of a copy); few rows by latency (1 x 8192: 2.9 us, a launch is two).
 template <typename T>
 __device__ __forceinline__ void add_stream(Vec8<T>& x, const Vec8<T>& r, float (&h)[8]) {
   float f[8];
@@ -136,6 +142,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_rows_kernel(const NormArgs a
   const RowOut out = row_out(a.quant, row, a.cols);
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {
+    if ((int64_t)i * blockDim.x * 8 >= a.cols) break;  // (the same in the whole CTA)
     const int64_t c = (int64_t)(i * blockDim.x + threadIdx.x) * 8;
     norm_out8<T, W>(a, v[i], c < a.cols, row, c, rstd, out);
   }
@@ -193,7 +200,8 @@ __global__ void __launch_bounds__(kRowThreads) norm_long_rows_kernel(const NormA
 // its columns' part of dw in registers over all of its group's rows. The groups'
 // parts are added in shared memory, the CTAs' parts go to the workspace and a
 // second kernel sums them, all in order (no atomics: dw has the same bits on
-// every call).
+// every call). Bound by HBM: 16384 x 8192 bf16 156 us (6.9 TB/s, a copy's rate);
+// 1001 x 4096 11.3 us, bound by the two launches and the first rows' way in.
 constexpr int kGradChunks = 2;
 constexpr int kGradSmem = 192 << 10;    // of the SM's 228 KB
 constexpr int kGradMaxStages = 8;
@@ -377,7 +385,9 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradArgs a, c
 }
 
 // Short rows: a warp each, straight from HBM (eight warps a CTA, each with a
-// row's loads in flight), dw of the CTA's warps summed in order at the end.
+// row's loads in flight), dw of the CTA's warps summed in order at the end
+// (16384 x 512: 15 us, 4.4 TB/s; the ring takes 23 there, and less from 544
+// columns on: 25 and 27 at 16384 x 640).
 template <typename T, typename G, typename W, int kChunks>
 __global__ void __launch_bounds__(256, 2) norm_short_grad_kernel(const NormGradArgs a) {
   __shared__ float part[8][kChunks * 256];
@@ -552,8 +562,7 @@ __global__ void __launch_bounds__(kSumWarps * 32) norm_dw_sum_kernel(const float
 }
 
 // ---------------------------------------------------------------- SwiGLU ---
-// a = silu(g) u with silu(g) = g / (1 + e^-g). Each thread takes eight
-// elements of a row.
+// a = silu(g) u with silu(g) = g / (1 + e^-g).
 constexpr int kActThreads = 256;
 
 // g / (1 + e^-g) and 1 / (1 + e^-g) of a pair, in fp32 throughout and without a
@@ -591,7 +600,9 @@ __device__ __forceinline__ float2 sigmoid2_24(float2 g) {
 // A thread takes sixteen columns of one row after another (blockDim.y and the
 // grid's height apart), the next row's loads in flight meanwhile: what a thread
 // works out once is spread over many rows. Short rows (blockDim.x below 32)
-// share a warp.
+// share a warp. Bound by HBM and issue alike (IPC 3.2): 8192 x 28672 bf16 to
+// E4M3 codes 191 us (6.2 TB/s, 93 % of a copy); fp32 2048 x 28672 81 us (98 %).
+// `wide`: 32-byte loads where every row allows them (191 us, 193 without).
 template <typename T>
 // bf16: three CTAs an SM (80 registers) measured 191 us at 8192 x 28672 where
 // 126 registers took 225 and 64 (four CTAs) 207; fp32 is at HBM's rate with two.
@@ -632,7 +643,9 @@ __global__ void __launch_bounds__(kActThreads, sizeof(T) == 2 ? 3 : 1) swiglu_ke
   }
 }
 
-// With s = 1 / (1 + e^-g): dg = dy u s (1 + g (1 - s)), du = dy g s.
+// With s = 1 / (1 + e^-g): dg = dy u s (1 + g (1 - s)), du = dy g s. Eight
+// columns of one row a thread; bound by HBM: 4096 x 28672 bf16 169 us (7.0 TB/s,
+// a copy's rate).
 template <typename T, typename G>
 __global__ void __launch_bounds__(kActThreads) swiglu_grad_kernel(const SwigluGradArgs a) {
   const int64_t c = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 8;
@@ -703,22 +716,29 @@ void launch_norm(const NormArgs& a, cudaStream_t st) {
   const int64_t vecs = a.cols / 8;
   const unsigned rows = (unsigned)a.rows;
   if (vecs <= 128) {
-    // one warp a row, eight rows a CTA
+    // one warp a row, eight rows a CTA; as many vectors to a lane as the row needs
+    // (16384 x 512: 11.4 us with two, 16.2 with four of which two hold nothing)
     const dim3 grid((unsigned)((a.rows + 7) / 8)), block(32, 8);
     if (vecs <= 32)
       norm_rows_kernel<T, W, 1, 256><<<grid, block, 0, st>>>(a);
+    else if (vecs <= 64)
+      norm_rows_kernel<T, W, 2, 256><<<grid, block, 0, st>>>(a);
     else
       norm_rows_kernel<T, W, 4, 256><<<grid, block, 0, st>>>(a);
   } else if (vecs <= 1024 && a.rows <= kSms) {
     // an SM or more to each row: the widest CTA has the shortest way through it
+    // (152 x 8192: 3.7 us, 5.0 the other way; 400 x 8192: 7.5 and 6.9)
     norm_rows_kernel<T, W, 1, 1024><<<rows, (unsigned)((vecs + 31) / 32 * 32), 0, st>>>(a);
   } else if (vecs <= 1024) {
     norm_rows_kernel<T, W, 4, 256><<<rows, (unsigned)((vecs + 127) / 128 * 32), 0, st>>>(a);
   } else if (vecs <= 2048) {
     norm_rows_kernel<T, W, 4, 512><<<rows, (unsigned)((vecs + 127) / 128 * 32), 0, st>>>(a);
-  } else if (sizeof(T) == 2 && vecs <= 4096) {
-    norm_rows_kernel<T, W, 4, 1024><<<rows, (unsigned)((vecs + 127) / 128 * 32), 0, st>>>(a);
   } else {
+    if constexpr (sizeof(T) == 2)
+      if (vecs <= 4096) {
+        norm_rows_kernel<T, W, 4, 1024><<<rows, (unsigned)((vecs + 127) / 128 * 32), 0, st>>>(a);
+        return;
+      }
     norm_long_rows_kernel<T, W><<<rows, kRowThreads, 0, st>>>(a);
   }
 }

@@ -2,8 +2,18 @@
 // (sm_103a): the single-token form of the block-scaled GEMM.
 //   y[m, n] = sum_k x[m, k] W[n, k]
 // The weights' codes and scales are all of the traffic (N K (1/2 + 1/32)
-// bytes against M K + M N values), so the kernel is built around streaming
-// them once:
+// bytes, NVFP4 1/2 + 1/16, against M K + M N values), so every kernel here
+// streams them once. launch_gemv chooses:
+//  * gemv_mx_kernel: MXFP4 weights, K a multiple of 128, a workspace: the
+//    tensor cores' MXFP8 products take the codes as they lie in memory;
+//  * gemv_kernel: up to eight rows of x otherwise: codes become f16 in
+//    registers for mma.sync. One launch and no workspace, so also the faster
+//    one for small weights (one row, 8192 x 8192: 12 us against 16);
+//  * gemv_tc_kernel: more rows otherwise: codes become bf16 or f16 in tensor
+//    memory, once for up to 32 rows.
+// Sums are fp32 throughout and added in a fixed order.
+//
+// ------------------------------------------------------- up to eight rows ---
 //  * a CTA owns 128 rows of W and a slice of K; one thread streams the codes
 //    by TMA, 256 of K a stage, into a ring of shared memory (128-byte swizzle);
 //  * converter warps bring x into the same ring as f16, 32 elements under one
@@ -17,11 +27,12 @@
 //    and the block's sum enters the running fp32 sum times (factor of W) x
 //    (factor of x). NVFP4's E4M3 scales are multiplied into the f16 weights
 //    instead (4 + 2 significant bits: exact).
-// tcgen05 is not used: its 4-bit operands would need x in 8 or 4 bits, and at
-// up to 32 rows the loads, not the products, are what costs.
-// Few CTAs: K is split over a cluster of 2, 4 or 8 CTAs, whose sums are added
-// in rank order through distributed shared memory, so results do not depend
-// on timing.
+// K is split over a cluster of up to eight CTAs (k_splits) where there are few
+// row tiles; their sums are added in rank order through distributed shared
+// memory.
+// Bound by the time to fill and empty two CTAs' rings an SM, then by the
+// conversions: 14336 x 4096, one row, 11.7 us (tiled scales; 2.7 TB/s of HBM's
+// 6.7), 13.1 with row-major ones; 1000 x 1024 4.4 us, of which a launch is two.
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -560,8 +571,14 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
 //    second product; NVFP4's scales go in 2^-26 smaller, which the end undoes;
 //  * the pairs that one word of codes gives are elements (i, i + 4) of its
 //    eight: x is laid down in the same order instead of reordering W.
-// Bound by the conversion's issue slots (about 3 instructions a weight), which
-// the number of rows does not change.
+// Two CTAs an SM, so that one converts while the other starts or ends. Bound by
+// the latency of the converting warps' chains (load, convert, store to tensor
+// memory, arrive; sixteen warps an SM issue 1.7 instructions a clock), which the
+// number of rows does not change: NVFP4, tiled scales, 28672 x 8192, 32 rows
+// 52 us, of which about 10 are outside the loop (23 rows, 14336 x 4096: 22 us);
+// MXFP4 without the workspace, 16 rows, 58 us. Tried without gain: waiting for
+// a buffer's store only after the next one's conversion, and codes through
+// byte-permute tables in place of some conversions.
 constexpr int kTcTokens = 32;
 constexpr int kTcStages = 3;                // of kStageK
 constexpr int kTcK = 64;                    // K per tensor-core buffer
@@ -961,6 +978,10 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ C
 // K a stage: TMA spreads the codes into the 8-bit containers that the
 // instruction reads, one thread issues the products, and the row-major scales,
 // where W has those, are arranged into a tile by a warp.
+//
+// Bound by HBM: 28672 x 8192 (125 MB) 28.5 us at one row, the time that a plain
+// read of as many bytes takes here; 31 us at 16 rows, 38 at 32 (three digits of
+// each row are 96 of the instruction's N).
 //
 // One CTA an SM takes an equal run of all (row tile, stage) units, its ring
 // going on from one tile to the next, so that every SM streams to the end

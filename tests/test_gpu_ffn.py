@@ -132,6 +132,14 @@ def test_norm_forward(rows, cols, dt, wdt, res, fmt, layout, extra):
     assert mx.device_status() == 0
 
 
+@pytest.mark.parametrize("rows,cols,dt,layout", [
+    (37, 288, BF16, 0), (256, 512, F32, 1), (11, 544, BF16, 0), (19, 640, F32, 0), (128, 768, BF16, 1),
+    (200, 1056, BF16, 0), (155, 1280, F32, 0), (153, 2592, BF16, 0), (3, 8224, BF16, 0), (2, 16416, F32, 0),
+    (2, 24608, BF16, 0)])
+def test_norm_of_rows_that_fill_their_threads_in_part(rows, cols, dt, layout):
+    test_norm_forward(rows, cols, dt, BF16, True, "e4m3", layout, 0)
+
+
 def test_norm_of_many_rows_takes_every_row():
     """More rows than a grid of resident CTAs, every row different."""
     import gemm_pt_block_gb300 as mx
