@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_long_rows_kernel(const NormA
 // its columns' part of dw in registers over all of its group's rows. The groups'
 // parts are added in shared memory, the CTAs' parts go to the workspace and a
 // second kernel sums them, all in order (no atomics: dw has the same bits on
-// every call). Bound by HBM: 16384 x 8192 bf16 156 us (6.9 TB/s, a copy's rate);
+// every call). Bound by HBM: 16384 x 8192 bf16 157 us (6.8 TB/s, a copy's rate);
 // 1001 x 4096 11.3 us, bound by the two launches and the first rows' way in.
 constexpr int kGradChunks = 2;
 constexpr int kGradSmem = 192 << 10;    // of the SM's 228 KB
@@ -257,13 +257,15 @@ struct GradRing {
 template <typename T, typename G, typename W>
 __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradArgs a, const GradRing r) {
   extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ float part[2][32];
+  __shared__ float part[32];
   __shared__ uint64_t full[kGradMaxGroups * kGradMaxStages];
+  __shared__ volatile uint32_t abort[kGradMaxGroups];
   const uint32_t tid = threadIdx.x, group = threadIdx.y, cols = (uint32_t)a.cols, rows = (uint32_t)a.rows;
   const uint32_t bars = ptx::smem_u32(full) + 8 * kGradMaxStages * group;
   const uint32_t first = group * gridDim.x + blockIdx.x, slots = group * r.stages * r.stage_bytes;
   if (tid == 0) {
     for (uint32_t i = 0; i < r.stages; ++i) ptx::mbar_init(bars + 8 * i, 1);
+    abort[group] = 0;
     ptx::fence_mbar_init();
   }
   __syncthreads();
@@ -287,11 +289,11 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradArgs a, c
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
   }
-  uint32_t slot = 0, parity = 0, turn = 0;
+  uint32_t slot = 0, parity = 0;
   float rstd = first < rows ? __ldg(a.rstd + first) : 0.0f;
   for (uint32_t row = first; row < rows; row += r.step) {
     const float next = row + r.step < rows ? __ldg(a.rstd + row + r.step) : 0.0f;
-    if (!wait_bar(bars + 8 * slot, parity)) break;  // all of the group wait on the same bar: all give up alike
+    if (!wait_bar(bars + 8 * slot, parity)) abort[group] = 1u;
     const uint8_t* dy = ring + slots + slot * r.stage_bytes;
     // the row is read twice from shared memory: kept in registers between the
     // passes, its values would leave too few for 1024 threads an SM
@@ -312,9 +314,21 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradArgs a, c
         }
       }
     }
-    // (the partial sums alternate between two buffers: one barrier here)
-    const float mean = __fdiv_rn(group_sum(sum, part[turn], group, blockDim.x), (float)cols);
-    turn ^= 1u;
+    const float mean = __fdiv_rn(group_sum(sum, part, group, blockDim.x), (float)cols);
+    if (abort[group]) {  // past the barrier: the whole group leaves, or none of it
+      // the copies in flight land (bounded wait) before the CTA's memory goes
+      if (tid == 0)
+        for (uint32_t i = 0; i < r.stages && row + i * r.step < rows; ++i) {
+          const uint64_t t0 = ptx::globaltimer_ns();
+          while (!ptx::mbar_try_wait(bars + 8 * slot, parity) && ptx::globaltimer_ns() - t0 < kWaitLimitNs / 10) {
+          }
+          if (++slot == r.stages) {
+            slot = 0;
+            parity ^= 1u;
+          }
+        }
+      break;
+    }
 #pragma unroll
     for (int i = 0; i < kGradChunks; ++i) {
       const uint32_t c = (i * blockDim.x + tid) * 8;
@@ -341,12 +355,10 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradArgs a, c
     rstd = next;
     // the slot's next row at once, for the price of a barrier: past the next
     // row's own barrier instead, a ring of two slots would have no copy in flight
-    // while that row is read (16384 x 8192: 168 us; this way 156)
+    // while that row is read (16384 x 8192: 168 us; this way 157)
+    group_barrier(group, blockDim.x);
     const uint32_t ahead = row + r.stages * r.step;
-    if (ahead < rows) {
-      group_barrier(group, blockDim.x);
-      if (tid == 0) fetch(ahead, slot);
-    }
+    if (tid == 0 && ahead < rows) fetch(ahead, slot);
     if (++slot == r.stages) {
       slot = 0;
       parity ^= 1u;

@@ -383,6 +383,42 @@ def test_side_stream_and_graph_capture():
         assert torch.equal(out, v)
 
 
+@pytest.mark.parametrize("M,nv", [(2, False), (12, False), (12, True)])
+def test_workspace_forms_on_a_side_stream_and_in_a_graph(M, nv):
+    """The two kernels of the forms with a workspace, one launched under the
+    other, follow what the stream wrote before them."""
+    import gemm_pt_block_gb300 as mx
+
+    N, K = 640, 1024
+    q, s, _ = weights(N, K, nv, 24)
+    x = [activations(M, K, "bf16", 50 + i)[0] for i in range(3)]
+    w = wparams(nv)
+    space = torch.empty(1 << 22, dtype=torch.uint8, device=DEV)
+    want = [mx.mxfp4_gemv(t, q, s, N, K, w, workspace=space) for t in x]
+    plain = [mx.mxfp4_gemv(t, q, s, N, K, w, workspace=False) for t in x]
+    for a, b in zip(want, plain):
+        assert (a.float() - b.float()).abs().max() <= b.float().abs().max() / 64
+    torch.cuda.synchronize()
+    side, buf, out = torch.cuda.Stream(), torch.empty_like(x[0]), torch.empty((M, N), dtype=BF16, device=DEV)
+    side.wait_stream(torch.cuda.current_stream())
+    for t, v in zip(x, want):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(1_000_000)
+            buf.copy_(t)
+        got = mx.mxfp4_gemv(buf, q, s, N, K, w, workspace=space, stream=side)
+        side.synchronize()
+        assert torch.equal(got, v)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(2):                                # the second call's workspace is the first one's
+            mx.mxfp4_gemv(buf, q, s, N, K, w, y=out, workspace=space)
+    for t, v in zip(x, want):
+        buf.copy_(t)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, v)
+
+
 def test_offsets_beyond_32_bits():
     """A weight matrix whose codes pass 4 GiB: rows past the 2^32nd byte are
     read, and land in their own columns."""
