@@ -27,7 +27,7 @@
 //    and the block's sum enters the running fp32 sum times (factor of W) x
 //    (factor of x). NVFP4's E4M3 scales are multiplied into the f16 weights
 //    instead (4 + 2 significant bits: exact).
-// K is split over a cluster of up to eight CTAs (k_splits) where there are few
+// K is split over a cluster of up to 16 CTAs (k_splits) where there are few
 // row tiles; their sums are added in rank order through distributed shared
 // memory.
 // Bound by the time to fill and empty two CTAs' rings an SM, then by the
@@ -66,7 +66,7 @@ constexpr int kConvWarps = 4;
 constexpr int kThreads = (kMmaWarps + 1 + kConvWarps) * 32;
 constexpr int kWBytes = kRows * kRowBytes;
 constexpr int kTokens = 8;                 // rows of x: the N of one product
-constexpr int kSms = 152;
+constexpr int kSms = 152, kMostSplits = 16;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 // Shared memory of one CTA.
@@ -1405,7 +1405,8 @@ cudaError_t launch_cluster(void (*kernel)(P...), dim3 grid, int threads, int byt
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Lets a kernel use `bytes` of dynamic shared memory, once per device.
+// Lets a kernel use `bytes` of dynamic shared memory and clusters above the
+// portable size, once per device.
 template <typename K>
 cudaError_t allow_smem(K kernel, int bytes, bool (&set)[kMaxDevices]) {
   static std::mutex mu;
@@ -1416,6 +1417,7 @@ cudaError_t allow_smem(K kernel, int bytes, bool (&set)[kMaxDevices]) {
   std::lock_guard<std::mutex> lock(mu);
   if (set[dev]) return cudaSuccess;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   set[dev] = e == cudaSuccess;
   return e;
 }
@@ -1487,12 +1489,14 @@ bool mx_fits(const GemvArgs& a) {
 
 // K is split over a cluster so that all CTAs (two an SM) end together: what counts is the rounds of CTAs
 // times a CTA's stages and what it costs besides them, about six (64 tiles of 32 stages, 23 rows: 32 us in one
-// slice, 19 in four, 24 in eight; 224 tiles: 50 us in one, 58 in three).
+// slice, 19 in four, 24 in eight; 224 tiles: 50 us in one, 58 in three). Clusters above eight, the portable
+// size, only where they leave an SM to each CTA: past that they wait for one another's places (16384 of K, 12
+// rows: 256 of N 15.8 us in eight slices, 10.4 in sixteen; 4096 of K, one row: 2048 of N 5.6 and 8.9).
 int k_splits(const GemvArgs& a, int tokens) {
   const int64_t tiles = (a.N + kRows - 1) / kRows * ((a.M + tokens - 1) / tokens), stages = (a.K + kStageK - 1) / kStageK;
   int splits = 1;
   int64_t best = INT64_MAX;
-  for (int n = 1; n <= 8 && n <= stages; ++n) {
+  for (int n = 1; n <= (tiles * n <= kSms ? kMostSplits : 8) && n <= stages; ++n) {
     const int64_t cost = (tiles * n + 2 * kSms - 1) / (2 * kSms) * ((stages + n - 1) / n + 6);
     if (cost < best) {
       best = cost;

@@ -240,6 +240,23 @@ def test_non_finite_values_stay_in_their_rows():
     assert torch.isnan(y4[:, 7]).all() and torch.isfinite(y4[:, :7]).all() and torch.isfinite(y4[:, 8:]).all()
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 130, 4096), (3, 256, 3872), (12, 100, 16384), (20, 1200, 4000), (33, 600, 2816),
+                                   (5, 1217, 8192)])
+@pytest.mark.parametrize("nv", [False, True], ids=["mxfp4", "nvfp4"])
+def test_few_row_tiles_and_long_sums(M, N, K, nv):
+    """K over more slices than stages divide evenly, up to the largest cluster."""
+    import gemm_pt_block_gb300 as mx
+
+    q, s, w64 = weights(N, K, nv, 61)
+    for kind in ("bf16", "e4m3"):
+        x, _, x64, kw = activations(M, K, kind, 62)
+        y = mx.mxfp4_gemv(x, q, s, N, K, wparams(nv), out_dtype=F32, workspace=False, **kw)
+        check(y, x64, w64)
+        z = mx.mxfp4_gemv(x, q, s, N, K, wparams(nv), out_dtype=F32, workspace=False, **kw)
+        assert torch.equal(y, z)
+    assert mx.device_status() == 0
+
+
 @pytest.mark.parametrize("K", [32, 96, 160, 544, 1056, 4128, 4160])
 @pytest.mark.parametrize("nv", [False, True], ids=["mxfp4", "nvfp4"])
 @pytest.mark.parametrize("M", [3, 12])
