@@ -88,9 +88,13 @@ struct Ctl {
 static_assert(sizeof(Ctl) <= 256, "control block");
 
 // Bounded wait (about 2 s): on expiry the CTA stops issuing work and the
-// library's device error word is set.
+// library's device error word is set. kLong: the first look already lets the
+// hardware suspend the thread, for roles that usually have to wait and must not
+// take issue slots from the others (MXFP8 form, 28672 x 8192, one row: 27.0 us,
+// 28.6 without; the converting form 51 us, 49 without; loops that only look: 35).
+template <bool kLong = false>
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint32_t* abort) {
-  if (ptx::mbar_try_wait(bar, parity)) return true;
+  if (kLong ? ptx::mbar_try_wait_sleep(bar, parity, 100000u) : ptx::mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = ptx::globaltimer_ns();
   while (!ptx::mbar_try_wait_sleep(bar, parity, 100000u)) {
     if (*reinterpret_cast<volatile uint32_t*>(abort)) return false;
@@ -583,7 +587,7 @@ constexpr int kTcTokens = 32;
 constexpr int kTcStages = 3;                // of kStageK
 constexpr int kTcK = 64;                    // K per tensor-core buffer
 constexpr int kTcBufs = 4, kTcBufsX = 4;    // of the weights (tensor memory), of x (shared memory)
-constexpr int kTcDeq = 8, kTcConv = 4;      // converting warps: weights, x
+constexpr int kTcDeq = 8;                   // warps that convert weights
 // Sums kept in tensor memory, two to an issuing thread, in turn, added at the
 // end: the tensor cores round every K = 16 step of a sum toward zero, so
 // one sum over all of K drifts by up to K / 16 units of its last place
@@ -593,7 +597,12 @@ constexpr int kTcSums = 4;
 constexpr uint32_t kTcA = kTcSums * kTcTokens, kTcACols = kTcK / 2, kTcTmem = kTcA + kTcBufs * kTcACols;
 static_assert(kTcTmem == 256, "two CTAs an SM");
 constexpr int kTcIss = 2;                   // threads that issue products: the even and the odd buffers
-constexpr int kTcThreads = (kTcDeq + 1 + kTcIss + kTcConv) * 32;
+// Warps that convert x, or (kF16) the one that loads it: fewer threads leave the others more registers (NVFP4, 32
+// rows, 28672 x 8192: 49 us with 80, 52 with 64).
+template <bool kF16>
+struct TcRoles {
+  static constexpr int kConv = kF16 ? 1 : 4, kThreads = (kTcDeq + 1 + kTcIss + kConv) * 32;
+};
 constexpr int kTcB = kTcTokens * kTcK * 2;
 
 struct TcCtl {
@@ -691,7 +700,7 @@ __global__ void __launch_bounds__(kF16Threads) gemv_f16_rows_kernel(const GemvAr
 // conversion, two an instruction, and one packed product with their E4M3 scale
 // (six significant bits: exact) finishes them; x comes by TMA.
 template <bool NV, bool kF16>
-__global__ void __launch_bounds__(kTcThreads, 2)
+__global__ void __launch_bounds__(TcRoles<kF16>::kThreads, 2)
 gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm_x, const GemvArgs a,
                const TcX sx, const int splits) {
   static_assert(NV || !kF16, "E8M0 scales are beyond f16");
@@ -774,7 +783,7 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ C
     __syncwarp();
   } else if (kF16 && warp > kTcDeq + kTcIss) {
     // ---- x by TMA, once the rows are written
-    if (warp == kTcDeq + kTcIss + 1 && lane == 0) {
+    if (lane == 0) {
       ptx::wait_prior_grid();
       for (int b = 0; b < bufs; ++b) {
         const int i = b % kTcBufsX;
@@ -796,7 +805,7 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ C
     const int64_t x_bytes = a.x_kind == GemvArgs::kXBf16 ? 2 : 1, x_step = 4 * a.ld_x * x_bytes, s_step = 4 * (a.K >> 5);
     const uint8_t* const x_rows = static_cast<const uint8_t*>(a.x) + (m0 + (lane >> 3)) * a.ld_x * x_bytes;
     const uint8_t* const s_rows = a.sx + (m0 + (lane >> 3)) * (a.K >> 5);
-    for (int b = warp - kTcDeq - kTcIss - 1; b < bufs; b += kTcConv) {
+    for (int b = warp - kTcDeq - kTcIss - 1; b < bufs; b += TcRoles<kF16>::kConv) {
       const int i = b % kTcBufsX;
       const uint32_t round = (uint32_t)(b / kTcBufsX);
       const int64_t k = (int64_t)s0 * kStageK + (int64_t)b * kTcK + 8 * c;
@@ -937,7 +946,7 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ C
   if (warp < 4) {
     for (int c = 0; c < cols_n; c += 16) {
       float f[16] = {};
-      for (int j = 0; j < (bufs > 1 ? kTcSums : kTcSums / kTcIss); ++j) {
+      for (int j = 0; j < min(bufs, kTcIss) * (kTcSums / kTcIss); ++j) {
         uint32_t v[16];
         ptx::tmem_ld_32x32b_x16(tmem + ((uint32_t)(32 * warp) << 16) + j * kTcTokens + c, v);
         ptx::tc_wait_ld();
@@ -1166,7 +1175,7 @@ gemv_mx_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       int i = 0, y = w ? (int)(row * kRows) : tile * sh.n;
       uint32_t parity = 1;  // the first round finds the slots empty
       for (; left; --left, ++issued) {
-        if (!wait_bar(empty + 8 * i, parity, &ctl->abort)) break;
+        if (!wait_bar<true>(empty + 8 * i, parity, &ctl->abort)) break;
         ptx::mbar_arrive_expect_tx(full + 8 * i, bytes);
         ptx::tma_load_2d(big + i * step, tm, s * kMxK, y, full + 8 * i);
         if (scales) ptx::bulk_load(small + i * kMxTile, from, kMxTile, full + 8 * i);
@@ -1218,12 +1227,12 @@ gemv_mx_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       for (int64_t begin = u0; go && begin < u1; ++seg) {
         const int64_t end = min(u1, (begin / sh.stages + 1) * sh.stages);
         const int buf = seg & 1;
-        if (seg >= 2 && !wait_bar(acc_empty + 8 * buf, (uint32_t)(seg / 2 - 1) & 1, &ctl->abort)) break;
+        if (seg >= 2 && !wait_bar<true>(acc_empty + 8 * buf, (uint32_t)(seg / 2 - 1) & 1, &ctl->abort)) break;
         ptx::tc_fence_after();
         const uint32_t d = tmem + buf * kMxBuf + mine;
         bool begun = false;
         for (; u < end; u += kMxIss) {
-          if (!(go = wait_bar(full + 8 * i, parity, &ctl->abort))) break;
+          if (!(go = wait_bar<true>(full + 8 * i, parity, &ctl->abort))) break;
           ptx::tc_fence_after();
           ptx::tc_cp_32x128b_warpx4(f, fa0 + (uint32_t)i * (kMxTile >> 4));
           ptx::tc_cp_32x128b_warpx4(f + 4, fb0 + (uint32_t)i * (kMxTile >> 4));
@@ -1268,7 +1277,7 @@ gemv_mx_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       // slot 0: the run's first tile, slot 1: its last one
       float* const part = parts + (2 * (int64_t)blockIdx.x + (u == u0 ? 0 : 1)) * plane + r;
       // after an abort the warps still go through the barriers below together, moving nothing
-      const bool ok = __all_sync(0xffffffffu, wait_bar(acc_full + 8 * buf, (uint32_t)(seg / 2) & 1, &ctl->abort));
+      const bool ok = __all_sync(0xffffffffu, wait_bar<true>(acc_full + 8 * buf, (uint32_t)(seg / 2) & 1, &ctl->abort));
       ptx::tc_fence_after();
       auto store = [&](int m, float v) {
         if (n >= a.N) return;
@@ -1366,7 +1375,7 @@ gemv_mx_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       uint32_t v[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = __ldg(row[j] + (u - begin));
-      if (c >= ST && !wait_bar(empty + 8 * i, (uint32_t)(c / ST - 1) & 1, &ctl->abort)) break;
+      if (c >= ST && !wait_bar<true>(empty + 8 * i, (uint32_t)(c / ST - 1) & 1, &ctl->abort)) break;
       *reinterpret_cast<uint4*>(sfa + i * kMxTile + lane * 16) = make_uint4(v[0], v[1], v[2], v[3]);
       ptx::fence_proxy_async();
       __syncwarp();
@@ -1455,7 +1464,7 @@ cudaError_t launch_tc(const GemvArgs& a, int splits, cudaStream_t st) {
   }
   const dim3 grid((unsigned)((a.N + kRows - 1) / kRows) * (unsigned)splits,
                   (unsigned)((a.M + kTcTokens - 1) / kTcTokens));
-  return launch_cluster(gemv_tc_kernel<NV, kF16>, grid, kTcThreads, bytes, splits, kF16, st, tm, tx, a, x, splits);
+  return launch_cluster(gemv_tc_kernel<NV, kF16>, grid, TcRoles<kF16>::kThreads, bytes, splits, kF16, st, tm, tx, a, x, splits);
 }
 
 template <int kN>
