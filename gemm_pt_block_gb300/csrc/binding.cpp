@@ -417,9 +417,10 @@ PyObject* swiglu_backward(PyObject* const* a) {
 }
 
 // Weights from which a workspace gains: above eight rows of x, and up to eight
-// (measured at 4096 x 4096: 12 us without, 15 with; 14336 x 4096: 26 and 20;
-// with one row 8192 x 8192: 12 and 16; 28672 x 8192: 32 and 29).
-constexpr int64_t kWorkspaceFrom = 1 << 25, kWorkspaceFromFew = 1 << 27;
+// (without / with: 12 rows, 4096 x 4096 10.7 / 10.1 us, 8192 x 4096 14.5 / 13.1,
+// 24 rows 11.3 / 12.7 and 15.4 / 16.1, 14336 x 4096 25.6 / 19.2; one row,
+// 8192 x 8192 13.9 / 15.6, 28672 x 4096 19.7 / 18.3, 28672 x 8192 33.5 / 27.7).
+constexpr int64_t kWorkspaceFrom = 1 << 25, kWorkspaceFromFew = 3 << 25;
 
 // (table, x, qw, sw, N, K, w, sx, x_format, out_dtype, y, workspace) -> (y,)
 PyObject* gemv(PyObject* const* a) {

@@ -8,7 +8,7 @@
 //    tensor cores' MXFP8 products take the codes as they lie in memory;
 //  * gemv_kernel: up to eight rows of x otherwise: codes become f16 in
 //    registers for mma.sync. One launch and no workspace, so also the faster
-//    one for small weights (one row, 8192 x 8192: 12 us against 16);
+//    one for small weights (one row, 8192 x 8192: 12 us against 15);
 //  * gemv_tc_kernel: more rows otherwise: codes become bf16 or f16 in tensor
 //    memory, once for up to 32 rows.
 // Sums are fp32 throughout and added in a fixed order.
@@ -576,13 +576,14 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
 //  * the pairs that one word of codes gives are elements (i, i + 4) of its
 //    eight: x is laid down in the same order instead of reordering W.
 // Two CTAs an SM, so that one converts while the other starts or ends. Bound by
-// the latency of the converting warps' chains (load, convert, store to tensor
-// memory, arrive; sixteen warps an SM issue 1.7 instructions a clock), which the
-// number of rows does not change: NVFP4, tiled scales, 28672 x 8192, 32 rows
-// 52 us, of which about 10 are outside the loop (23 rows, 14336 x 4096: 22 us);
-// MXFP4 without the workspace, 16 rows, 58 us. Tried without gain: waiting for
-// a buffer's store only after the next one's conversion, and codes through
-// byte-permute tables in place of some conversions.
+// the hand-over of buffers between the roles (store to tensor memory, barrier,
+// issue, barrier), which the number of rows does not change: without conversions
+// and products 43 of 52 us remained. NVFP4, tiled scales, 28672 x 8192, 32 rows
+// 49 us (23 rows, 14336 x 4096: 21 us); MXFP4 without the workspace, 16 rows,
+// 58 us. Tried without gain: waiting for a buffer's store only after the next
+// one's conversion, buffers handed over in pairs, twice the converting warps (28
+// us where eight take 22), one issuing thread (26) or four (21.6 against 20.9),
+// a deeper ring of x, byte-permute tables in place of some conversions.
 constexpr int kTcTokens = 32;
 constexpr int kTcStages = 3;                // of kStageK
 constexpr int kTcK = 64;                    // K per tensor-core buffer
@@ -988,8 +989,8 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ C
 // instruction reads, one thread issues the products, and the row-major scales,
 // where W has those, are arranged into a tile by a warp.
 //
-// Bound by HBM: 28672 x 8192 (125 MB) 28.5 us at one row, the time that a plain
-// read of as many bytes takes here; 31 us at 16 rows, 38 at 32 (three digits of
+// Bound by HBM: 28672 x 8192 (125 MB) 27 us at one row (4.6 TB/s; a plain read
+// of as many bytes takes 28.5 here); 30 us at 12 rows, 37 at 32 (three digits of
 // each row are 96 of the instruction's N).
 //
 // One CTA an SM takes an equal run of all (row tile, stage) units, its ring
@@ -1532,7 +1533,7 @@ cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t st) {
   const bool space = a.ws && a.ws_bytes >= (uint64_t)gemv_workspace_bytes(a);
   if (space && mx_fits(a)) return launch_mx(a, st);
   // One N of the products for up to eight rows of x (4096 x 4096: 7 us, 11 in tensor memory); from nine on the
-  // weights are converted once for all of them (16 rows, 28672 x 8192: 58 us and 75; with the workspace 32).
+  // weights are converted once for all of them (16 rows, 28672 x 8192: 58 us and 75; with the workspace 31).
   if (a.M <= kTokens) {
     const int splits = k_splits(a, kTokens);
     return a.nv ? launch_few<true>(a, splits, st) : launch_few<false>(a, splits, st);
