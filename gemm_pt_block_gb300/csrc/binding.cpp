@@ -147,8 +147,14 @@ mxfp4_status call(F f, A... a) {
 
 void* stream_of(int dev) { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream(); }
 
-int64_t field(PyObject* o, const char* name) {
-  PyObject* v = PyObject_GetAttrString(o, name);
+// The attributes of QuantParams, as the interpreter's own strings.
+enum Field { kBlock, kScaleMode, kRounding, kScaleLayout, kWht, kSignMask, kSeed, kSrStream, kElemFormat, kTensorExp, kFields };
+const char* const field_names[kFields] = {"block",         "scale_mode", "rounding",  "scale_layout", "wht",
+                                          "wht_sign_mask", "seed",       "sr_stream", "elem_format",  "tensor_exp"};
+PyObject* fields[kFields];
+
+int64_t field(PyObject* o, Field f) {
+  PyObject* v = PyObject_GetAttr(o, fields[f]);
   if (!v) throw Raised{};
   const unsigned long long n = PyLong_AsUnsignedLongLongMask(v);
   Py_DECREF(v);
@@ -158,16 +164,16 @@ int64_t field(PyObject* o, const char* name) {
 
 mxfp4_quant_params params(PyObject* o) {
   mxfp4_quant_params p{};
-  p.block = (int32_t)field(o, "block");
-  p.scale_mode = (int32_t)field(o, "scale_mode");
-  p.rounding = (int32_t)field(o, "rounding");
-  p.scale_layout = (int32_t)field(o, "scale_layout");
-  p.wht = field(o, "wht") != 0;
-  p.wht_sign_mask = (uint32_t)field(o, "wht_sign_mask");
-  p.seed = (uint64_t)field(o, "seed");
-  p.sr_stream = (uint32_t)field(o, "sr_stream");
-  p.elem_format = (uint32_t)field(o, "elem_format");
-  p.tensor_exp = (int32_t)field(o, "tensor_exp");
+  p.block = (int32_t)field(o, kBlock);
+  p.scale_mode = (int32_t)field(o, kScaleMode);
+  p.rounding = (int32_t)field(o, kRounding);
+  p.scale_layout = (int32_t)field(o, kScaleLayout);
+  p.wht = field(o, kWht) != 0;
+  p.wht_sign_mask = (uint32_t)field(o, kSignMask);
+  p.seed = (uint64_t)field(o, kSeed);
+  p.sr_stream = (uint32_t)field(o, kSrStream);
+  p.elem_format = (uint32_t)field(o, kElemFormat);
+  p.tensor_exp = (int32_t)field(o, kTensorExp);
   return p;
 }
 
@@ -551,4 +557,8 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__binding() {
+  for (int i = 0; i < kFields; ++i)
+    if (!(fields[i] = PyUnicode_InternFromString(field_names[i]))) return nullptr;
+  return PyModule_Create(&module);
+}
