@@ -422,11 +422,12 @@ PyObject* swiglu_backward(PyObject* const* a) {
   return tuple({&dg, &du});
 }
 
-// Weights from which a workspace gains: above eight rows of x, and up to eight
-// (without / with: 12 rows, 4096 x 4096 10.7 / 10.1 us, 8192 x 4096 14.5 / 13.1,
-// 24 rows 11.3 / 12.7 and 15.4 / 16.1, 14336 x 4096 25.6 / 19.2; one row,
-// 8192 x 8192 13.9 / 15.6, 28672 x 4096 19.7 / 18.3, 28672 x 8192 33.5 / 27.7).
-constexpr int64_t kWorkspaceFrom = 1 << 25, kWorkspaceFromFew = 3 << 25;
+// Weights from which a workspace gains: above eight rows of x (MXFP4, NVFP4), and
+// up to eight (without / with: MXFP4, 12 rows, 4096 x 4096 10.7 / 10.1 us,
+// 8192 x 4096 14.5 / 13.1, 24 rows 11.3 / 12.7 and 15.4 / 16.1, 14336 x 4096
+// 25.6 / 19.2; NVFP4, 24 rows, 4096 x 2048 9.1 / 9.1, 4096 x 4096 11.6 / 10.6;
+// one row, 8192 x 8192 13.9 / 15.6, 28672 x 4096 19.7 / 18.3).
+constexpr int64_t kWorkspaceFrom = 1 << 25, kWorkspaceFromNv = 1 << 24, kWorkspaceFromFew = 3 << 25;
 
 // (table, x, qw, sw, N, K, w, sx, x_format, out_dtype, y, workspace) -> (y,)
 PyObject* gemv(PyObject* const* a) {
@@ -478,7 +479,7 @@ PyObject* gemv(PyObject* const* a) {
   at::Tensor ws;
   size_t bytes = 0;
   if (!given(a[11])) {
-    if (weights >= (M > 8 ? kWorkspaceFrom : kWorkspaceFromFew)) {
+    if (weights >= (M <= 8 ? kWorkspaceFromFew : block == MXFP4_BLOCK_1X16 ? kWorkspaceFromNv : kWorkspaceFrom)) {
       bytes = lib.gemv_workspace(kind, block, M, N, K);
       if (bytes) ws = empty({(int64_t)bytes}, at::kByte, x);
     }
