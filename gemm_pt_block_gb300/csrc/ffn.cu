@@ -421,9 +421,9 @@ __global__ void __launch_bounds__(256, 2) norm_short_grad_kernel(const NormGradA
     for (int i = 0; i < kChunks; ++i) {
       const int64_t c = (i * 32 + lane) * 8;
       if (c < a.cols) {
-        load8(static_cast<const T*>(a.h) + row * a.ld_h + c, hv[i]);
-        load8(static_cast<const G*>(a.dy) + row * a.ld_dy + c, dv[i]);
-        if (a.dh) load8(static_cast<const T*>(a.dh) + row * a.ld_dh + c, sv[i]);
+        load8_apart(static_cast<const T*>(a.h) + row * a.ld_h + c, hv[i]);
+        load8_apart(static_cast<const G*>(a.dy) + row * a.ld_dy + c, dv[i]);
+        if (a.dh) load8_apart(static_cast<const T*>(a.dh) + row * a.ld_dh + c, sv[i]);
       }
     }
     float n[8], d[8], f[8], sum = 0.0f;

@@ -287,6 +287,42 @@ def test_norm_backward_of_no_rows():
     assert dx.shape == (0, 96) and (dw == 0).all()
 
 
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("cols", [96, 512, 1056, 4096, 20000])
+def test_matrices_on_any_16_bytes(cols, dt):
+    """Inputs and outputs 16 bytes past a 32-byte boundary: the same bits."""
+    import gemm_pt_block_gb300 as mx
+
+    rows, at = 9, 16 // (2 if dt == BF16 else 4)
+
+    def moved(t):
+        buf = torch.empty(t.numel() + at, dtype=t.dtype, device=DEV)
+        assert buf.data_ptr() % 32 == 0
+        v = buf[at:].view(t.shape)
+        return v.copy_(t)
+
+    x, r, g = rand(rows, cols, dt, 71), rand(rows, cols, dt, 72), rand(rows, cols, dt, 73, 1e-2)
+    w = (1 + 0.2 * torch.randn(cols, device=DEV)).to(dt)
+    p = mx.QuantParams(elem_format=mx.FORMAT_E4M3)
+    q, s, y, h, rstd = mx.mxfp4_rmsnorm_quantize(x, w, p, residual=r, y_dtype=dt, with_rstd=True)
+    hm, ym = moved(torch.zeros_like(x)), moved(torch.zeros_like(x))
+    q2, s2, _, _, rstd2 = mx.mxfp4_rmsnorm_quantize(moved(x), w, p, residual=moved(r), h=hm, y=ym, with_rstd=True)
+    assert torch.equal(q, q2) and torch.equal(s, s2) and torch.equal(rstd, rstd2)
+    assert torch.equal(hm, h) and torch.equal(ym, y)
+    dx, dw = mx.mxfp4_rmsnorm_backward(g, h, w, rstd, dh=r)
+    dxm = moved(torch.zeros_like(x))
+    _, dw2 = mx.mxfp4_rmsnorm_backward(moved(g), moved(h), w, rstd, dh=moved(r), dx=dxm)
+    assert torch.equal(dx, dxm) and torch.equal(dw, dw2)
+    q, s, y = mx.mxfp4_swiglu_quantize(x, r, p, y_dtype=dt)
+    q2, s2, _ = mx.mxfp4_swiglu_quantize(moved(x), moved(r), p, y=ym)
+    assert torch.equal(q, q2) and torch.equal(s, s2) and torch.equal(y, ym)
+    dg, du = mx.mxfp4_swiglu_backward(g, x, r)
+    dgm, dum = moved(torch.zeros_like(x)), moved(torch.zeros_like(x))
+    mx.mxfp4_swiglu_backward(moved(g), moved(x), moved(r), dgate=dgm, dup=dum)
+    assert torch.equal(dg, dgm) and torch.equal(du, dum)
+    assert mx.device_status() == 0
+
+
 def test_gradients_match_differences_of_the_forward_kernels():
     """Central differences of the fp32 forward kernels along random directions.
 
