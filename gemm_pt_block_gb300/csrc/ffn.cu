@@ -692,13 +692,21 @@ __global__ void __launch_bounds__(kActThreads) swiglu_grad_kernel(const SwigluGr
 }
 
 // Block and grid of the activation kernels for rows of per_row threads: CTAs of
-// 256 threads, rows of up to 256 (a power of two from 2 below 32, else a
-// multiple of 32), shorter rows side by side; at most `ctas` CTAs.
+// up to 256 threads, a row cut into equal parts of whole warps; rows that leave
+// more than a tenth of those lanes empty (and short rows) in parts of 16, 8 or
+// fewer, side by side (SwiGLU, 4096 x 4480: 28.8 us in parts of 256 lanes, 20.5
+// in two of 160, 18.6 in 18 of 16; 9879 x 1056: 15.9 in 96 lanes, 12.9 in nine
+// times 8); at most `ctas` CTAs.
 void act_shape(int64_t rows, int64_t per_row, int64_t ctas, dim3* grid, dim3* block) {
-  unsigned x = per_row >= kActThreads ? kActThreads : (unsigned)((per_row + 31) / 32 * 32);
+  int64_t wide = (per_row + kActThreads - 1) / kActThreads;
+  unsigned x = (unsigned)((per_row + 32 * wide - 1) / (32 * wide) * 32);
   while (per_row <= x / 2 && x <= 32) x /= 2;
+  for (unsigned c = 16; c >= 8 && c < x; c /= 2)
+    if ((per_row + c - 1) / c * c * 10 < wide * x * 9) {
+      x = c;
+      wide = (per_row + c - 1) / c;
+    }
   const unsigned y = kActThreads / x;
-  const int64_t wide = (per_row + x - 1) / x;
   int64_t tall = (rows + y - 1) / y, most = (ctas + wide - 1) / wide;
   if (most > 65535) most = 65535;
   *block = dim3(x, y);

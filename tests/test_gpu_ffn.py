@@ -413,6 +413,14 @@ def test_swiglu(rows, cols, dt, fmt, layout, extra):
     assert mx.device_status() == 0
 
 
+@pytest.mark.parametrize("rows,cols,dt,fmt,layout", [
+    (70, 1056, BF16, "e4m3", 0), (256, 4480, BF16, "e4m3", 1), (128, 1152, BF16, "nvfp4", 1), (37, 544, F32, "nvfp4", 0),
+    (300, 2336, BF16, "e2m1", 0), (9, 5440, F32, "e5m2", 0), (128, 640, F32, "e4m3floor", 1), (41, 8352, BF16, "nvfp4", 0)])
+def test_swiglu_of_rows_in_parts(rows, cols, dt, fmt, layout):
+    """Rows whose threads come in parts of 8, 16 and whole warps."""
+    test_swiglu(rows, cols, dt, fmt, layout, 0)
+
+
 def test_swiglu_of_large_and_non_finite_values():
     import gemm_pt_block_gb300 as mx
 
