@@ -640,8 +640,9 @@ __global__ void __launch_bounds__(kActThreads, sizeof(T) == 2 ? 3 : 1) swiglu_ke
       load16e(g, wide, gv);
       load16e(u, wide, uv);
     }
+    // (the sigmoid takes the 2^-24: a tiny g, brought down by it, would lose bits from 2^-102 on)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = f2mul(f2mul(f2mul(x[i], pair(0x1p-24f)), sigmoid2_24(x[i])), y[i]);
+    for (int i = 0; i < 8; ++i) y[i] = f2mul(f2mul(f2mul(sigmoid2_24(x[i]), pair(0x1p-24f)), x[i]), y[i]);
     if (a.y && live) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
