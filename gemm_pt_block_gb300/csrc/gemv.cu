@@ -524,10 +524,17 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
           float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
           mma16816(c, q[2 * r][0], q[2 * r + 1][0], q[2 * r][1], q[2 * r + 1][1], v.x, v.y);
           mma16816(c, q[2 * r][2], q[2 * r + 1][2], q[2 * r][3], q[2 * r + 1][3], v.z, v.w);
-          const float2 p0 = NV ? fx : f2mul(fx, make_float2(f[2 * r], f[2 * r]));
-          const float2 p1 = NV ? fx : f2mul(fx, make_float2(f[2 * r + 1], f[2 * r + 1]));
-          acc[r][0] = f2fma(make_float2(c[0], c[1]), p0, acc[r][0]);
-          acc[r][1] = f2fma(make_float2(c[2], c[3]), p1, acc[r][1]);
+          float2 c0 = make_float2(c[0], c[1]), c1 = make_float2(c[2], c[3]), w0 = fx, w1 = fx;
+          if (!NV) {
+            // the block's sum in units of x first, then times the weights' factor: the product of the two
+            // factors may pass fp32 (2^100 by 2^30) where the sum times both does not
+            c0 = f2mul(c0, fx);
+            c1 = f2mul(c1, fx);
+            w0 = make_float2(f[2 * r], f[2 * r]);
+            w1 = make_float2(f[2 * r + 1], f[2 * r + 1]);
+          }
+          acc[r][0] = f2fma(c0, w0, acc[r][0]);
+          acc[r][1] = f2fma(c1, w1, acc[r][1]);
         }
       }
       // The loads above have to be done before the slot goes back to the producer. The arrival alone

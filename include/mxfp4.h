@@ -454,7 +454,9 @@ enum { MXFP4_GEMV_X_BF16 = 0, MXFP4_GEMV_X_E4M3 = 1, MXFP4_GEMV_X_E5M2 = 2 };
  *      element.
  * Products are exact (bf16 x above eight rows too; up to eight, x is taken to
  * 2^-39 of its 32-block's largest magnitude) and summed in fp32, in a fixed
- * order; a NaN scale makes what it enters NaN. M may be 0 .. 65536 (the weights
+ * order; a NaN scale makes what it enters NaN. A 32-block's sum of x times codes,
+ * without the weights' scale, has to stay below fp32's largest value (x below
+ * 2^120 does); the scales themselves may be of any size. M may be 0 .. 65536 (the weights
  * are read again for every 32 rows of x), N any, K a multiple of 32, rows of x
  * multiples of 16 bytes; x, qw, sw 16-byte aligned. */
 mxfp4_status mxfp4_gemv(const void* x, int32_t x_kind, int64_t ld_x, const uint8_t* sx,
