@@ -401,8 +401,9 @@ __device__ __forceinline__ void finish(const GemvArgs& a, float* red, int ld, in
         const uint32_t at = ptx::smem_u32(d);
         for (int c = 0; c < splits; ++c) v = __fadd_rn(v, lds_cluster(ptx::mapa(at, (uint32_t)c)));
       }
-      v = __fmul_rn(v, factor);
+      // (in units of x first: 2^tensor_exp may be 2^100 either way)
       if (per_token) v = __fmul_rn(v, __ldcg(per_token + m0 + m));
+      v = __fmul_rn(v, factor);
       const int64_t o = (m0 + m) * a.ld_y + n;
       if (a.y_f32)
         put_at(static_cast<float*>(a.y) + o, v, a.y, a.y_bytes);

@@ -59,3 +59,35 @@ def test_bf16_blocks_whose_scale_product_passes_fp32(M, ws):
     s = torch.full((N, K // 32), 127 + 26, dtype=torch.uint8, device=DEV)
     y = mx.mxfp4_gemv(x, q, s, N, K, out_dtype=F32, workspace=space(ws, 0, False, M, N, K))
     assert (y[:, 0] == 0).all() and (y[:, 1:] == 2.0 ** 126).all()
+
+
+@pytest.mark.parametrize("exp,shift", [(100, -90), (60, -60), (-100, 90), (0, 0)])
+@pytest.mark.parametrize("M", [3, 12])
+@pytest.mark.parametrize("ws", [False, True])
+def test_tensor_exponents_against_the_size_of_x(exp, shift, M, ws):
+    """NVFP4's 2^tensor_exp with x of the opposite size: the product is of order
+    one, and nothing on the way passes fp32 either way."""
+    import gemm_pt_block_gb300 as mx
+
+    N, K = 130, 512
+    q, s, w64 = weights(N, K, True, 71)
+    x, _, _, _ = activations(M, K, "bf16", 72)
+    x = (x.double() * 2.0 ** shift).to(BF16)
+    y = mx.mxfp4_gemv(x, q, s, N, K, wparams(True, 0, exp), out_dtype=F32, workspace=space(ws, 0, True, M, N, K))
+    check(y, x.double(), w64 * 2.0 ** exp)
+
+
+@pytest.mark.parametrize("M", [3, 12])
+@pytest.mark.parametrize("ws", [False, True])
+def test_large_tensor_exponent_with_sums_of_one_sign(M, ws):
+    """Weights and x of one sign and size: the sums are as large as they get."""
+    import gemm_pt_block_gb300 as mx
+
+    N, K = 130, 4096
+    q, s, _ = weights(N, K, True, 75)
+    q &= 0x77
+    v = E2M1.to(DEV)[torch.stack((q & 15, q >> 4), -1).view(N, K).long()]
+    w64 = v * s.view(torch.float8_e4m3fn).double().repeat_interleave(16, 1)
+    x = torch.full((M, K), 1.5 * 2.0 ** -90, device=DEV, dtype=BF16)
+    y = mx.mxfp4_gemv(x, q, s, N, K, wparams(True, 0, 100), out_dtype=F32, workspace=space(ws, 0, True, M, N, K))
+    check(y, x.double(), w64 * 2.0 ** 100)
