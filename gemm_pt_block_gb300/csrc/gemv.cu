@@ -107,6 +107,13 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint32_t
   return true;
 }
 
+// The same for a whole warp, which goes on or leaves together: lanes that saw the phase end and lanes that saw
+// the abort flag would otherwise wait for one another at the warp's and the CTA's barriers, without a limit.
+template <bool kLong = false>
+__device__ __forceinline__ bool wait_bar_warp(uint32_t bar, uint32_t parity, uint32_t* abort) {
+  return __all_sync(0xffffffffu, wait_bar<kLong>(bar, parity, abort));
+}
+
 // Two codes (low 16 bits) to f16, exact.
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t v) {
   uint32_t r;
@@ -460,7 +467,7 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
     for (int s = s0 + (warp - kMmaWarps - 1); s < s1; s += kConvWarps) {
       const int i = (s - s0) % ST;
       const uint32_t round = (uint32_t)((s - s0) / ST);
-      if (round && !wait_bar(empty + 8 * i, (round - 1) & 1, &ctl->abort)) break;
+      if (round && !wait_bar_warp(empty + 8 * i, (round - 1) & 1, &ctl->abort)) break;
       const int64_t k0 = (int64_t)s * kStageK;
       if (!a.mma) convert_sw<NV>(a, n0, s, lane, sws + i * S::kSw);
       convert_x(a, m0, tokens, k0, lane, xs + i * S::kX, sxs + i * (S::kSx / 4));
@@ -482,10 +489,7 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
     int i = 0;
     uint32_t parity = 0;
     for (int s = s0; s < s1; ++s) {
-      // the whole warp leaves the wait together: lanes that saw the phase end at different polls would
-      // go through the products below in parts
-      const bool in = wait_bar(full_w + 8 * i, parity, &ctl->abort) && wait_bar(full_x + 8 * i, parity, &ctl->abort);
-      if (!__all_sync(0xffffffffu, in)) break;
+      if (!wait_bar_warp(full_w + 8 * i, parity, &ctl->abort) || !wait_bar_warp(full_x + 8 * i, parity, &ctl->abort)) break;
       const bool live = s * kBlocks + 4 * part < (int)(a.K >> 5);
       const uint8_t *w = ws + i * kWBytes, *x = xs + i * S::kX + xoff, *sw = sws + i * S::kSw + swoff;
       const float* sx = sxs + i * (S::kSx / 4) + sxoff;
@@ -836,7 +840,7 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ C
         px += x_step;
         ps += s_step;
       }
-      if (round && !wait_bar(empty_b + 8 * i, (round - 1) & 1, &ctl->abort)) break;
+      if (round && !wait_bar_warp(empty_b + 8 * i, (round - 1) & 1, &ctl->abort)) break;
 #pragma unroll
       for (int e = 0; e < kTcTokens / 4; ++e) {
         const int m = 4 * e + (lane >> 3);
@@ -881,7 +885,7 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ C
         for (int e = 0; e < kWords; ++e) now[e] = ahead[e];
         if (st + 1 < s1 - s0 && (row.off || st + 2 < s1 - s0)) row.load(s0 + st + 2, ahead);
       }
-      if (!__all_sync(0xffffffffu, wait_bar(full_w + 8 * slot, (uint32_t)(st / kTcStages) & 1, &ctl->abort))) break;
+      if (!wait_bar_warp(full_w + 8 * slot, (uint32_t)(st / kTcStages) & 1, &ctl->abort)) break;
       if (a.mma) {
         const int live = (int)min((int64_t)kWords, (cols - (int64_t)(s0 + st) * (kStageK / kPer)) / 4);
 #pragma unroll
@@ -932,7 +936,7 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ C
           for (int e = 0; e < 16; ++e) out[e] = hmul2_bf16(out[e], g);
         }
         // the warp stores together
-        if (round && !(go = __all_sync(0xffffffffu, wait_bar(empty_a + 8 * i, (round - 1) & 1, &ctl->abort)))) break;
+        if (round && !(go = wait_bar_warp(empty_a + 8 * i, (round - 1) & 1, &ctl->abort))) break;
         ptx::tc_fence_after();
         ptx::tmem_st_32x32b_x16(tmem + ((uint32_t)(r & ~31) << 16) + kTcA + i * kTcACols + 16 * half, out);
         ptx::tc_wait_st();
@@ -1286,7 +1290,7 @@ gemv_mx_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       // slot 0: the run's first tile, slot 1: its last one
       float* const part = parts + (2 * (int64_t)blockIdx.x + (u == u0 ? 0 : 1)) * plane + r;
       // after an abort the warps still go through the barriers below together, moving nothing
-      const bool ok = __all_sync(0xffffffffu, wait_bar<true>(acc_full + 8 * buf, (uint32_t)(seg / 2) & 1, &ctl->abort));
+      const bool ok = wait_bar_warp<true>(acc_full + 8 * buf, (uint32_t)(seg / 2) & 1, &ctl->abort);
       ptx::tc_fence_after();
       auto store = [&](int m, float v) {
         if (n >= a.N) return;
@@ -1384,7 +1388,7 @@ gemv_mx_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       uint32_t v[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = __ldg(row[j] + (u - begin));
-      if (c >= ST && !wait_bar<true>(empty + 8 * i, (uint32_t)(c / ST - 1) & 1, &ctl->abort)) break;
+      if (c >= ST && !wait_bar_warp<true>(empty + 8 * i, (uint32_t)(c / ST - 1) & 1, &ctl->abort)) break;
       *reinterpret_cast<uint4*>(sfa + i * kMxTile + lane * 16) = make_uint4(v[0], v[1], v[2], v[3]);
       ptx::fence_proxy_async();
       __syncwarp();
