@@ -821,13 +821,15 @@ cudaError_t norm_grad(const NormGradArgs& a, cudaStream_t st) {
     }
   } else if (a.rows > 0) {
     norm_long_dx_kernel<T, G, W><<<(unsigned)a.rows, kRowThreads, 0, st>>>(a);
+    if (cudaError_t e = cudaGetLastError()) return e;
     if (a.dw) {
       slices = (int)(a.rows < 256 ? a.rows : 256);
       norm_long_dw_kernel<T, G><<<dim3((unsigned)((a.cols / 8 + kColThreads - 1) / kColThreads), slices), kColThreads,
                                   0, st>>>(a);
     }
   }
-  if (!a.dw) return cudaGetLastError();
+  if (cudaError_t e = cudaGetLastError()) return e;
+  if (!a.dw) return cudaSuccess;
   // launched while the kernel before it drains; it waits for that kernel's sums itself
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.cols / 32));
