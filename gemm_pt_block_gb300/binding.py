@@ -517,7 +517,11 @@ def nvfp4_tensor_exp(x: torch.Tensor, stream=None) -> int:
 def _on(stream, call, *args, **kw):
     """`call` with `stream` as PyTorch's current stream, so that what it
     allocates (outputs, workspaces) belongs to the stream that its kernels
-    run on."""
+    run on. The stream has to be one of the tensors' device: another one is
+    not current there, and would be passed over."""
+    dev = getattr(args[0], "device", None)
+    if dev is not None and dev.type == "cuda" and dev != stream.device:
+        raise ValueError(f"stream must be one of the tensors' device {dev} (got {stream.device})")
     with torch.cuda.stream(stream):
         return call(*args, **kw)
 

@@ -7,6 +7,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -145,6 +146,10 @@ mxfp4_status call(F f, A... a) {
   return f(a...);
 }
 
+// The tensors' device is the thread's current one while the library runs: it
+// launches there, and the default stream's handle names no device.
+using OnDevice = c10::cuda::CUDAGuard;
+
 void* stream_of(int dev) { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream(); }
 
 // The attributes of QuantParams, as the interpreter's own strings.
@@ -245,6 +250,7 @@ PyObject* norm(PyObject* const* a) {
   const Table& lib = table(a[0]);
   const at::Tensor& x = tensor(a[1], "x");
   const Shape sh = shape_of(x, "x");
+  const OnDevice current(static_cast<c10::DeviceIndex>(sh.dev));
   const int64_t ldx = rows_ld(x, "x", sh.rows, sh.cols, sh.dev);
   const int32_t dt = dtype_code(x, "x");
   const double eps = PyFloat_AsDouble(a[5]);
@@ -305,6 +311,7 @@ PyObject* norm_backward(PyObject* const* a) {
   const Table& lib = table(a[0]);
   const at::Tensor& h = tensor(a[2], "h");
   const Shape sh = shape_of(h, "h");
+  const OnDevice current(static_cast<c10::DeviceIndex>(sh.dev));
   const int64_t ldh = rows_ld(h, "h", sh.rows, sh.cols, sh.dev);
   const int32_t hdt = dtype_code(h, "h");
   const at::Tensor& dy = tensor(a[1], "dy");
@@ -371,6 +378,7 @@ PyObject* swiglu(PyObject* const* a) {
   const Table& lib = table(a[0]);
   const at::Tensor& g = tensor(a[1], "gate");
   const Shape sh = shape_of(g, "gate");
+  const OnDevice current(static_cast<c10::DeviceIndex>(sh.dev));
   const int64_t ldg = rows_ld(g, "gate", sh.rows, sh.cols, sh.dev);
   const int32_t dt = dtype_code(g, "gate");
   const at::Tensor& u = tensor(a[2], "up");
@@ -400,6 +408,7 @@ PyObject* swiglu_backward(PyObject* const* a) {
   const Table& lib = table(a[0]);
   const at::Tensor& g = tensor(a[2], "gate");
   const Shape sh = shape_of(g, "gate");
+  const OnDevice current(static_cast<c10::DeviceIndex>(sh.dev));
   const int64_t ldg = rows_ld(g, "gate", sh.rows, sh.cols, sh.dev);
   const int32_t dt = dtype_code(g, "gate");
   const at::Tensor& dy = tensor(a[1], "dy");
@@ -434,6 +443,7 @@ PyObject* gemv(PyObject* const* a) {
   const Table& lib = table(a[0]);
   const at::Tensor& x = tensor(a[1], "x");
   const Shape sh = shape_of(x, "x");
+  const OnDevice current(static_cast<c10::DeviceIndex>(sh.dev));
   const int64_t M = sh.rows, N = integer(a[4]), K = integer(a[5]);
   const int64_t ldx = rows_ld(x, "x", M, K, sh.dev);
   int32_t block = MXFP4_BLOCK_1X32, layout = MXFP4_LAYOUT_ROWMAJOR, exponent = 0;
