@@ -31,14 +31,38 @@ def _readable(t: torch.Tensor) -> torch.Tensor:
     return t if ok else t.contiguous()
 
 
+class _FirstOrder(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, what, anchors, *tensors):
+        ctx.what = what
+        return tensors[anchors:]
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError(f"second derivatives of {ctx.what} are not provided")
+
+
+def _first_order(what: str, anchors, *grads):
+    """Gradients that a library kernel computed, on their way out of a backward
+    pass. Where a graph of that pass is wanted (create_graph) and they depend on
+    the tensors `anchors` (those that require grad count), they get a node that
+    raises, so that a second derivative is refused; without one they would pass
+    for constants and their part of it would be missing without a word."""
+    if not torch.is_grad_enabled():
+        return grads
+    anchors = [t for t in anchors if t is not None and t.requires_grad]
+    if not anchors:
+        return grads
+    out = iter(_FirstOrder.apply(what, len(anchors), *anchors, *[g for g in grads if g is not None]))
+    return tuple(None if g is None else next(out) for g in grads)
+
+
 class _RmsNormFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, weight, eps, out_dtype):
         ctx.set_materialize_grads(False)
-        x = _readable(x)
-        _, _, y, h, rstd = mxfp4_rmsnorm_quantize(
-            x, weight, residual=None if residual is None else _readable(residual), eps=eps, y_dtype=out_dtype,
-            with_rstd=True)
+        _, _, y, h, rstd = mxfp4_rmsnorm_quantize(x, weight, residual=residual, eps=eps, y_dtype=out_dtype,
+                                                  with_rstd=True)
         ctx.save_for_backward(x if h is None else h, weight, rstd)
         return y if h is None else (y, h)
 
@@ -50,6 +74,8 @@ class _RmsNormFn(torch.autograd.Function):
             return dh if need_x else None, dh if need_r else None, None, None, None
         dx, dw = mxfp4_rmsnorm_backward(_readable(dy), h, weight, rstd, dh=None if dh is None else _readable(dh),
                                         with_dw=need_w)
+        # (dw alone is linear in what the weight multiplies: it depends on dy only)
+        dx, dw = _first_order("rmsnorm", (dy, dh, h, weight) if need_x or need_r else (dy,), dx, dw)
         return dx if need_x else None, dx if need_r else None, dw, None, None
 
 
@@ -57,10 +83,11 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch
             eps: float = 1e-6, out_dtype: torch.dtype = torch.bfloat16):
     """Differentiable root-mean-square norm over the last dimension (a multiple
     of 32): y in out_dtype, or (y, h) with h = x + residual when a residual is
-    given. x and residual share one type (bf16 or fp32)."""
+    given. x and residual share one type (bf16 or fp32). First derivatives
+    only: a graph of the backward pass raises where it is differentiated."""
     lead, D = x.shape[:-1], x.shape[-1]
-    r = None if residual is None else residual.reshape(-1, D)
-    out = _RmsNormFn.apply(x.reshape(-1, D), r, weight, eps, out_dtype)
+    r = None if residual is None else _readable(residual.reshape(-1, D))
+    out = _RmsNormFn.apply(_readable(x.reshape(-1, D)), r, weight, eps, out_dtype)
     if residual is None:
         return out.reshape(*lead, D)
     return out[0].reshape(*lead, D), out[1].reshape(*lead, D)
@@ -69,7 +96,6 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch
 class _SwigluFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, gate, up, out_dtype):
-        gate, up = _readable(gate), _readable(up)
         ctx.save_for_backward(gate, up)
         return mxfp4_swiglu_quantize(gate, up, y_dtype=out_dtype)[2]
 
@@ -80,14 +106,16 @@ class _SwigluFn(torch.autograd.Function):
         # one buffer for both halves: the gradient of the product that wrote them side by side
         both = torch.empty((rows, 2 * cols), dtype=gate.dtype, device=gate.device)
         dgate, dup = mxfp4_swiglu_backward(_readable(dy), gate, up, dgate=both[:, :cols], dup=both[:, cols:])
-        return dgate, dup, None
+        # (dup alone depends on gate and dy)
+        return *_first_order("swiglu", (dy, gate, up) if ctx.needs_input_grad[0] else (dy,), dgate, dup), None
 
 
 def swiglu(gate: torch.Tensor, up: torch.Tensor, out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """Differentiable gate / (1 + exp(-gate)) * up in out_dtype; the last
-    dimension is a multiple of 32, gate and up share one type (bf16 or fp32)."""
+    dimension is a multiple of 32, gate and up share one type (bf16 or fp32).
+    First derivatives only, as rmsnorm."""
     lead, F = gate.shape[:-1], gate.shape[-1]
-    return _SwigluFn.apply(gate.reshape(-1, F), up.reshape(-1, F), out_dtype).reshape(*lead, F)
+    return _SwigluFn.apply(_readable(gate.reshape(-1, F)), _readable(up.reshape(-1, F)), out_dtype).reshape(*lead, F)
 
 
 class Mxfp4FeedForward(torch.nn.Module):
