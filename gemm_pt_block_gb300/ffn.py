@@ -25,10 +25,18 @@ from .linear import LinearRecipe, Mxfp4Linear
 
 
 def _readable(t: torch.Tensor) -> torch.Tensor:
-    """t, or a copy of it that the kernels can read (unit column stride, rows
-    on 16-byte boundaries): autograd may hand over expanded gradients."""
-    ok = t.stride(-1) == 1 and t.stride(0) >= t.shape[1] and t.stride(0) % 8 == 0 and t.data_ptr() % 16 == 0
-    return t if ok else t.contiguous()
+    """The matrix t, or a copy of it that the kernels can read (unit column
+    stride, rows on 16-byte boundaries): autograd may hand over expanded
+    gradients, and a view may begin anywhere."""
+    rows = t.shape[0] <= 1 or (t.stride(0) >= t.shape[1] and t.stride(0) % 8 == 0)
+    return t if rows and t.stride(1) == 1 and t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
+
+
+def _readable_vector(t: torch.Tensor | None) -> torch.Tensor | None:
+    """The same for a norm's weight (a slice of a flat parameter buffer, say)."""
+    if t is None or (t.is_contiguous() and t.data_ptr() % 16 == 0):
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
 
 
 class _FirstOrder(torch.autograd.Function):
@@ -87,7 +95,7 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch
     only: a graph of the backward pass raises where it is differentiated."""
     lead, D = x.shape[:-1], x.shape[-1]
     r = None if residual is None else _readable(residual.reshape(-1, D))
-    out = _RmsNormFn.apply(_readable(x.reshape(-1, D)), r, weight, eps, out_dtype)
+    out = _RmsNormFn.apply(_readable(x.reshape(-1, D)), r, _readable_vector(weight), eps, out_dtype)
     if residual is None:
         return out.reshape(*lead, D)
     return out[0].reshape(*lead, D), out[1].reshape(*lead, D)
@@ -162,7 +170,7 @@ class Mxfp4FeedForward(torch.nn.Module):
         x2 = _readable(x.reshape(-1, self.dim))
         r2 = None if residual is None else _readable(residual.reshape(-1, self.dim))
         p8 = QuantParams(BLOCK_1X32, SCALE_ROUNDUP, ROUND_RTN, LAYOUT_ROWMAJOR, elem_format=FORMAT_E4M3)
-        q, s, _, h, _ = mxfp4_rmsnorm_quantize(x2, self.norm, p8, residual=r2, eps=self.eps)
+        q, s, _, h, _ = mxfp4_rmsnorm_quantize(x2, _readable_vector(self.norm), p8, residual=r2, eps=self.eps)
         (qg, sg, pg), (qd, sd, pd) = self._decode
         gu = mxfp4_gemv(q, qg, sg, 2 * self.hidden, self.dim, pg, sx=s)
         qa, sa, _ = mxfp4_swiglu_quantize(gu[:, :self.hidden], gu[:, self.hidden:], p8)
