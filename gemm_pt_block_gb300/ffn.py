@@ -139,7 +139,19 @@ class Mxfp4FeedForward(torch.nn.Module):
         self.norm = torch.nn.Parameter(torch.ones(dim, device=device, dtype=dtype))
         self.gate_up = Mxfp4Linear(dim, 2 * hidden, recipe, device=device, dtype=dtype, out_dtype=torch.bfloat16)
         self.down = Mxfp4Linear(hidden, dim, recipe, device=device, dtype=dtype, out_dtype=torch.bfloat16)
-        self._decode = None
+        self._decode_params = None
+        for name in self._DECODE:                        # (they follow the module to a device; not its state)
+            self.register_buffer(name, None, persistent=False)
+
+    _DECODE = ("gate_up_codes", "gate_up_scales", "down_codes", "down_scales")
+
+    @property
+    def _decode(self):
+        """(codes, scales, parameters) of both weights, None before quantize_weights."""
+        if self._decode_params is None:
+            return None
+        t = [getattr(self, name) for name in self._DECODE]
+        return [(t[0], t[1], self._decode_params[0]), (t[2], t[3], self._decode_params[1])]
 
     def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None):
         """(y, h) for bf16 x (and residual) [..., dim] with a multiple of 128 rows."""
@@ -153,13 +165,16 @@ class Mxfp4FeedForward(torch.nn.Module):
     @torch.no_grad()
     def quantize_weights(self) -> None:
         """Quantizes the weights for `decode`, once; call it again after they change."""
-        self._decode = []
+        done = []
         for layer in (self.gate_up, self.down):
             p = layer.recipe.w_row
             if p.wht:
                 raise ValueError("decoding needs weights quantized without rotation along their rows")
             q, s, _, _ = mxfp4_quantize(layer.weight.detach(), p)
-            self._decode.append((q, s, p))
+            done += [q, s]
+        for name, t in zip(self._DECODE, done):
+            setattr(self, name, t)
+        self._decode_params = [layer.recipe.w_row for layer in (self.gate_up, self.down)]
 
     @torch.no_grad()
     def decode(self, x: torch.Tensor, residual: torch.Tensor | None = None):
