@@ -540,8 +540,8 @@ def _fast():
         try:
             from . import _binding as _ext
         except ImportError as e:
-            raise RuntimeError("the _binding extension is not built; run gemm_pt_block_gb300.build.build() "
-                               "(there is no fallback implementation)") from e
+            raise RuntimeError(f"the _binding extension does not load ({e}); run gemm_pt_block_gb300.build.build(), "
+                               "which builds it for the PyTorch at hand (there is no fallback implementation)") from e
     L = lib()
     t = getattr(L, "_fast_table", None)
     if t is None:

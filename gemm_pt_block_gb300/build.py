@@ -37,6 +37,7 @@ UNITS = {
 HEADERS = ["internal.h", "mx_device.cuh", "ptx.cuh", "quant_device.cuh", "row_device.cuh", "tma_host.h"]
 
 BINDING = os.path.join(HERE, "_binding.so")
+BINDING_FOR = os.path.join(BUILD, "binding_for.txt")
 
 
 def _binding_command() -> list[str]:
@@ -54,6 +55,26 @@ def _binding_command() -> list[str]:
             f"-I{sysconfig.get_paths()['include']}", f"-I{os.path.join(cuda, 'include')}",
             os.path.join(CSRC, "binding.cpp"), f"-L{lib}", f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
             "-ltorch_cuda", "-ltorch_python", "-o"]
+
+
+def _built_for() -> str:
+    """What the extension's binary interface hangs on."""
+    import sysconfig
+
+    import torch
+
+    return f"PyTorch {torch.__version__}, Python {sysconfig.get_config_var('SOABI')}\n"
+
+
+def _binding_stale(deps) -> bool:
+    """Whether _binding.so is older than its sources, or was built for another
+    PyTorch or Python than the ones at hand."""
+    try:
+        with open(BINDING_FOR) as f:
+            built = f.read()
+    except OSError:
+        return True
+    return built != _built_for() or _stale(BINDING, deps)
 
 
 def nvcc() -> str:
@@ -88,7 +109,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False,
     # (the bounds-checking library is called through the same extension)
     ext = None
     src = os.path.join(CSRC, "binding.cpp")
-    if not bounds_check and (force or _stale(BINDING, [src, __file__, os.path.join(ROOT, "include", "mxfp4.h")])):
+    if not bounds_check and (force or _binding_stale([src, __file__, os.path.join(ROOT, "include", "mxfp4.h")])):
         ext = BINDING + f".{os.getpid()}.tmp"
         jobs.append([*_binding_command(), ext])
 
@@ -106,6 +127,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False,
                 raise RuntimeError(f"compilation failed: {' '.join(cmd)}")
     if ext is not None:
         os.replace(ext, BINDING)
+        with open(BINDING_FOR, "w") as f:
+            f.write(_built_for())
     if force or jobs or _stale(lib_out, objs):
         tmp = lib_out + f".{os.getpid()}.tmp"
         cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
