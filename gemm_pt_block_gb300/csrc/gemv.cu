@@ -56,12 +56,12 @@ __device__ uint32_t g_gemv_error;
 namespace mx {
 namespace {
 
-constexpr int kRows = 128;                 // most rows of W per CTA
+constexpr int kRows = 128;                 // rows of W per CTA
 constexpr int kStageK = 256;               // K per stage
 constexpr int kBlocks = kStageK / 32;
 constexpr int kRowBytes = kStageK / 2;     // code bytes per row and stage
 constexpr int kParts = 2;                  // parts of a stage's blocks, each a warp's
-constexpr int kMmaWarps = 8;               // (up to four) groups of 32 rows x kParts
+constexpr int kMmaWarps = 8;               // four groups of 32 rows x kParts
 constexpr int kConvWarps = 4;
 constexpr int kThreads = (kMmaWarps + 1 + kConvWarps) * 32;
 constexpr int kWBytes = kRows * kRowBytes;
@@ -73,7 +73,7 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 template <bool NV>
 struct Smem {
   static constexpr int kX = kTokens * kStageK * 2;            // f16 [block][token][32]
-  static constexpr int kSw = 2 * kRows * kStageK / (NV ? 16 : 32);  // two 128-row tiles of scales
+  static constexpr int kSw = kRows * kStageK / (NV ? 16 : 32);  // scales, as tensor-core tiles
   static constexpr int kSx = kTokens * kBlocks * 4;           // float [block][token]
   static constexpr int kStages = NV ? 4 : 5;
   static constexpr int kBytes = kStages * (kWBytes + kX + kSw + kSx) + 256 + 1024;
@@ -162,9 +162,9 @@ __device__ __forceinline__ float lds_cluster(uint32_t a) {
   return r;
 }
 
-// One stage of x rows m0 .. m0 + tokens - 1, K from k0: lane 4 b + t brings
+// One stage of x rows 0 .. tokens - 1, K from k0: lane 4 b + t brings
 // elements 8 t .. 8 t + 7 of block b, a row at a time.
-__device__ __forceinline__ void convert_x(const GemvArgs& a, int64_t m0, int tokens, int64_t k0, int lane,
+__device__ __forceinline__ void convert_x(const GemvArgs& a, int tokens, int64_t k0, int lane,
                                           uint8_t* xs, float* sxs) {
   const int b = lane >> 2, t = lane & 3;
   const int64_t k = k0 + b * 32 + t * 8;
@@ -172,7 +172,7 @@ __device__ __forceinline__ void convert_x(const GemvArgs& a, int64_t m0, int tok
   uint8_t* dst = xs + b * (kTokens * 64) + t * 16;
   float* sdst = sxs + b * kTokens;
   if (a.x_kind == GemvArgs::kXBf16) {
-    const uint16_t* p = static_cast<const uint16_t*>(a.x) + m0 * a.ld_x + k;
+    const uint16_t* p = static_cast<const uint16_t*>(a.x) + k;
 #pragma unroll 1
     for (int m = 0; m < tokens; m += 4) {
       uint4 v[4];
@@ -202,8 +202,8 @@ __device__ __forceinline__ void convert_x(const GemvArgs& a, int64_t m0, int tok
       }
     }
   } else {
-    const uint8_t* p = static_cast<const uint8_t*>(a.x) + m0 * a.ld_x + k;
-    const uint8_t* sp = a.sx + m0 * (a.K >> 5) + (k0 >> 5) + b;
+    const uint8_t* p = static_cast<const uint8_t*>(a.x) + k;
+    const uint8_t* sp = a.sx + (k0 >> 5) + b;
     const bool e5 = a.x_kind == GemvArgs::kXE5m2;
 #pragma unroll 1
     for (int m = 0; m < tokens; m += 4) {
@@ -337,31 +337,22 @@ __device__ __forceinline__ void convert_sw(const GemvArgs& a, int64_t n0, int s,
   }
 }
 
-// The producer thread: stages s0 .. s1 - 1 of the CTA's codes by TMA, and
-// tensor-core scale tiles (two row tiles of them where the CTA's rows span two)
-// as they lie in memory, into rings of ST slots.
+// The producer thread: stages s0 .. s1 - 1 of the codes of the CTA's 128 rows by
+// TMA, and tensor-core scale tiles as they lie in memory, into rings of ST slots.
 template <bool NV, int ST>
-__device__ void produce(const CUtensorMap& tm, const GemvArgs& a, int64_t n0, int rows, int s0, int s1, uint8_t* ws,
-                        uint8_t* sws, uint32_t full, uint32_t empty, uint32_t* abort) {
+__device__ void produce(const CUtensorMap& tm, const GemvArgs& a, int64_t n0, int s0, int s1, uint8_t* ws, uint8_t* sws,
+                        uint32_t full, uint32_t empty, uint32_t* abort) {
   constexpr int kPer = NV ? 16 : 32, kTile = kRows * kStageK / kPer;
-  const int64_t cols = a.K / kPer, tile0 = n0 >> 7, tiles = ((n0 + rows - 1) >> 7) - tile0 + 1;
-  const int64_t last = (a.N >> 7) - 1;  // the scale array's last row tile
+  const int64_t cols = a.K / kPer;
   int i = 0, s = s0;
   uint32_t round = 0;
   for (; s < s1; ++s) {
     if (round && !wait_bar(empty + 8 * i, (round - 1) & 1, abort)) break;
-    uint32_t bytes = (uint32_t)rows * kRowBytes, sb = 0;
     const int64_t c0 = (int64_t)s * (kStageK / kPer);
-    if (a.mma) {
-      sb = (uint32_t)min((int64_t)kTile, (cols - c0) * kRows);
-      bytes += sb * (uint32_t)tiles;
-    }
-    ptx::mbar_arrive_expect_tx(full + 8 * i, bytes);
+    const uint32_t sb = a.mma ? (uint32_t)min((int64_t)kTile, (cols - c0) * kRows) : 0u;
+    ptx::mbar_arrive_expect_tx(full + 8 * i, kWBytes + sb);
     ptx::tma_load_2d(ptx::smem_u32(ws + i * kWBytes), &tm, s * kRowBytes, (int32_t)n0, full + 8 * i);
-    if (a.mma)
-      for (int64_t j = 0; j < tiles; ++j)
-        ptx::bulk_load(ptx::smem_u32(sws + (2 * i + j) * kTile),
-                       a.sw + min(tile0 + j, last) * 128 * cols + c0 * kRows, sb, full + 8 * i);
+    if (a.mma) ptx::bulk_load(ptx::smem_u32(sws + i * kTile), a.sw + n0 * cols + c0 * kRows, sb, full + 8 * i);
     if (++i == ST) {
       i = 0;
       ++round;
@@ -382,14 +373,14 @@ __device__ void produce(const CUtensorMap& tm, const GemvArgs& a, int64_t n0, in
 // The CTA's sums, `planes` of them [token][ld] a plane apart in its shared
 // memory, and those of the cluster's other slices of K, added in fixed order
 // and stored. Every thread of the CTA calls it, the planes written and visible.
-__device__ __forceinline__ void finish(const GemvArgs& a, float* red, int ld, int plane, int planes, int rows,
-                                       int tokens, int rank, int splits, int64_t n0, int64_t m0, float factor,
+__device__ __forceinline__ void finish(const GemvArgs& a, float* red, int ld, int plane, int planes, int tokens,
+                                       int rank, int splits, int64_t n0, int64_t m0, float factor,
                                        const float* per_token, bool ok) {
-  const int total = tokens * rows;
+  const int total = tokens * kRows;
   if (splits > 1) {
     if (ok && planes > 1)
       for (int e = threadIdx.x; e < total; e += blockDim.x) {
-        float* d = red + e / rows * ld + e % rows;
+        float* d = red + e / kRows * ld + e % kRows;
         *d = __fadd_rn(d[0], d[plane]);
       }
     __syncwarp();
@@ -397,7 +388,7 @@ __device__ __forceinline__ void finish(const GemvArgs& a, float* red, int ld, in
   }
   if (ok) {
     for (int e = total * rank / splits + threadIdx.x; e < total * (rank + 1) / splits; e += blockDim.x) {
-      const int m = e / rows, r = e % rows;
+      const int m = e / kRows, r = e % kRows;
       const int64_t n = n0 + r;
       if (n >= a.N) continue;
       const float* d = red + m * ld + r;
@@ -425,7 +416,7 @@ __device__ __forceinline__ void finish(const GemvArgs& a, float* red, int ld, in
 template <bool NV>
 __global__ void __launch_bounds__(kThreads, 2)
 gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int splits) {
-  constexpr int groups = kRows / 32, rows = kRows, mma_warps = kMmaWarps;
+  constexpr int groups = kRows / 32;
   using S = Smem<NV>;
   constexpr int ST = S::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -437,7 +428,7 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
                  empty = ptx::smem_u32(ctl->empty);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)(blockIdx.x % (unsigned)splits);
-  const int64_t n0 = (int64_t)(blockIdx.x / (unsigned)splits) * rows, m0 = 0;
+  const int64_t n0 = (int64_t)(blockIdx.x / (unsigned)splits) * kRows;
   const int tokens = (int)a.M;
   const int stages = (int)((a.K + kStageK - 1) / kStageK);
   const int s0 = (int)((int64_t)stages * rank / splits), s1 = (int)((int64_t)stages * (rank + 1) / splits);
@@ -447,7 +438,7 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
     for (int i = 0; i < ST; ++i) {
       ptx::mbar_init(full_w + 8 * i, 1);
       ptx::mbar_init(full_x + 8 * i, 1);
-      ptx::mbar_init(empty + 8 * i, mma_warps);
+      ptx::mbar_init(empty + 8 * i, kMmaWarps);
     }
     ctl->abort = 0;
     ptx::fence_mbar_init();
@@ -460,7 +451,7 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
   const int g = lane >> 2, t = lane & 3, part = warp / groups, wr = warp - part * groups;
 
   if (warp == kMmaWarps) {
-    if (lane == 0) produce<NV, ST>(tm, a, n0, rows, s0, s1, ws, sws, full_w, empty, &ctl->abort);
+    if (lane == 0) produce<NV, ST>(tm, a, n0, s0, s1, ws, sws, full_w, empty, &ctl->abort);
     __syncwarp();
   } else if (warp > kMmaWarps) {
     // ---- converters: whole stages in turn
@@ -470,7 +461,7 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
       if (round && !wait_bar_warp(empty + 8 * i, (round - 1) & 1, &ctl->abort)) break;
       const int64_t k0 = (int64_t)s * kStageK;
       if (!a.mma) convert_sw<NV>(a, n0, s, lane, sws + i * S::kSw);
-      convert_x(a, m0, tokens, k0, lane, xs + i * S::kX, sxs + i * (S::kSx / 4));
+      convert_x(a, tokens, k0, lane, xs + i * S::kX, sxs + i * (S::kSx / 4));
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(full_x + 8 * i);
     }
@@ -481,10 +472,7 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
     uint32_t chunk[4];
 #pragma unroll
     for (int b = 0; b < 4; ++b) chunk[b] = (uint32_t)(((4 * part + b) ^ g) << 4) + 4 * t + (32 * wr + g) * kRowBytes;
-    // where this warp's 32 rows stand among the 128-row tiles of scales
-    const int64_t nw = n0 + 32 * wr;
-    const uint32_t tile = a.mma ? (uint32_t)((nw >> 7) - (n0 >> 7)) : 0u, quarter = a.mma ? (uint32_t)(nw >> 5) & 3u : wr;
-    const uint32_t swoff = tile * (S::kSw / 2) + part * (NV ? 1024 : 512) + g * 16 + quarter * 4;
+    const uint32_t swoff = part * (NV ? 1024 : 512) + g * 16 + wr * 4;
     const uint32_t xoff = 4 * part * (kTokens * 64) + g * 64 + t * 16, sxoff = 4 * part * kTokens + 2 * t;
     int i = 0;
     uint32_t parity = 0;
@@ -558,8 +546,8 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
   __syncthreads();  // every load has landed and been read (or the CTA has aborted)
   const bool ok = *reinterpret_cast<volatile uint32_t*>(&ctl->abort) == 0;
   float* const red = reinterpret_cast<float*>(ws);  // [part][token][rows + 4]
-  constexpr int ld = rows + 4, plane = kTokens * ld;
-  if (ok && warp < mma_warps) {
+  constexpr int ld = kRows + 4, plane = kTokens * ld;
+  if (ok && warp < kMmaWarps) {
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -570,7 +558,7 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
       }
   }
   __syncthreads();
-  finish(a, red, ld, plane, kParts, rows, tokens, rank, splits, n0, m0, NV ? a.p2k : 1.0f, nullptr, ok);
+  finish(a, red, ld, plane, kParts, tokens, rank, splits, n0, 0, NV ? a.p2k : 1.0f, nullptr, ok);
 }
 
 // ---------------------------------------------------- more rows of x ---
@@ -626,8 +614,7 @@ struct TcCtl {
 
 template <bool NV>
 constexpr int tc_smem() {
-  return kTcBufsX * kTcB + kTcStages * (kWBytes + 2 * kRows * kStageK / (NV ? 16 : 32)) + (int)sizeof(TcCtl) +
-         1024;
+  return kTcBufsX * kTcB + kTcStages * (kWBytes + kRows * kStageK / (NV ? 16 : 32)) + (int)sizeof(TcCtl) + 1024;
 }
 
 __device__ __forceinline__ uint32_t hmul2_bf16(uint32_t a, uint32_t b) {
@@ -721,7 +708,7 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ C
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const base = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t *const ws = base, *const bs = ws + kTcStages * kWBytes, *const sws = bs + kTcBufsX * kTcB;
-  TcCtl* const ctl = reinterpret_cast<TcCtl*>(sws + kTcStages * 2 * kTile);
+  TcCtl* const ctl = reinterpret_cast<TcCtl*>(sws + kTcStages * kTile);
   const uint32_t full_w = ptx::smem_u32(ctl->full_w), empty_w = ptx::smem_u32(ctl->empty_w),
                  full_a = ptx::smem_u32(ctl->full_a), empty_a = ptx::smem_u32(ctl->empty_a),
                  full_b = ptx::smem_u32(ctl->full_b), empty_b = ptx::smem_u32(ctl->empty_b),
@@ -763,7 +750,7 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ C
   const uint32_t tmem = ctl->tmem;
 
   if (warp == kTcDeq) {
-    if (lane == 0) produce<NV, kTcStages>(tm, a, n0, kRows, s0, s1, ws, sws, full_w, empty_w, &ctl->abort);
+    if (lane == 0) produce<NV, kTcStages>(tm, a, n0, s0, s1, ws, sws, full_w, empty_w, &ctl->abort);
     __syncwarp();
   } else if (warp > kTcDeq && warp <= kTcDeq + kTcIss) {
     // ---- the threads that issue the products; a slot of the rings is always the same one's
@@ -890,7 +877,7 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ C
         const int live = (int)min((int64_t)kWords, (cols - (int64_t)(s0 + st) * (kStageK / kPer)) / 4);
 #pragma unroll
         for (int e = 0; e < kWords; ++e)  // words past K were not copied
-          sc[e] = e < live ? *reinterpret_cast<const uint32_t*>(sws + slot * 2 * kTile + e * 512 + (r & 31) * 16 + (r >> 5) * 4)
+          sc[e] = e < live ? *reinterpret_cast<const uint32_t*>(sws + slot * kTile + e * 512 + (r & 31) * 16 + (r >> 5) * 4)
                            : 0u;
       }
 #pragma unroll
@@ -977,7 +964,7 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ C
     ptx::tmem_dealloc(tmem, kTcTmem);
   }
   if (kF16) ptx::wait_prior_grid();  // (the tokens' factors)
-  finish(a, red, ld, 0, 1, kRows, tokens, rank, splits, n0, m0, kF16 ? a.p2k : NV ? a.p2k * 0x1p26f : 1.0f,
+  finish(a, red, ld, 0, 1, tokens, rank, splits, n0, m0, kF16 ? a.p2k : NV ? a.p2k * 0x1p26f : 1.0f,
          kF16 ? reinterpret_cast<const float*>(a.ws + sx.factors) : nullptr, ok);
 }
 
