@@ -985,12 +985,15 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ C
 // workspace; the product's CTAs start under it (programmatic launch) and have
 // their first weights in flight when it ends. They stream 128 rows of W, 128 of
 // K a stage: TMA spreads the codes into the 8-bit containers that the
-// instruction reads, one thread issues the products, and the row-major scales,
-// where W has those, are arranged into a tile by a warp.
+// instruction reads, two threads issue the products in turn, and the row-major
+// scales, where W has those, are arranged into tiles by four warps.
 //
-// Bound by HBM: 28672 x 8192 (125 MB) 27 us at one row (4.6 TB/s; a plain read
-// of as many bytes takes 28.5 here); 30 us at 12 rows, 37 at 32 (three digits of
-// each row are 96 of the instruction's N).
+// 28672 x 8192 (125 MB) takes 27 us at one row, 4.6 TB/s or 69 % of a copy's
+// rate: of the other 8 us about one is the digits' kernel and two are the join of
+// shared tiles; the rest is not shown (a plain read of as many bytes, 28.5 us, has
+// the same start and end of every SM's stream, and is no bound: this kernel is
+// faster). 30 us at 12 rows, 37 at 32 (three digits of each row are 96 of the
+// instruction's N, and leave a ring of six stages).
 //
 // One CTA an SM takes an equal run of all (row tile, stage) units, its ring
 // going on from one tile to the next, so that every SM streams to the end
@@ -1010,12 +1013,13 @@ struct MxRing {
   static_assert(kStages % kMxIss == 0 && kStages >= kMxConv, "a slot is always the same issuing thread's");
   static constexpr int kBytes = kStages * (kMxA + kB + 2 * kMxTile) + 1024 + 512;
 };
-// Tensor-memory columns: two buffers of sums (one filled while the other leaves), and four slots of scales
-// (A's four columns, then B's), so that a stage's copies do not wait for the products of the one before.
+// Tensor-memory columns: two buffers of sums (one filled while the other leaves), and for each issuing thread a
+// slot of scales (A's four columns, then B's), so that one thread's copies do not wait for the other's products.
 constexpr uint32_t kMxTmem = 512, kMxBuf = 240, kMxSf = 480;
+static_assert(2 * kMxBuf <= kMxSf && kMxSf + 8 * kMxIss <= kMxTmem, "columns");
 
 struct MxCtl {
-  uint64_t full[10], empty[10], acc_full[2], acc_empty[2], drain[4];
+  uint64_t full[10], empty[10], acc_full[2], acc_empty[2], drain[kMxIss];
   uint32_t tmem, abort, last;
 };
 static_assert(sizeof(MxCtl) <= 512, "control block");
