@@ -572,7 +572,8 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
 //    bits 8..6 of a bf16 word, are the subnormal that is 2^-126 times its value
 //    (zero and the half included), so one packed product with 2^126 times the
 //    block's scale gives code x scale exactly. Scales above 2 (E8M0) take a
-//    second product; NVFP4's scales go in 2^-26 smaller, which the end undoes;
+//    second product; NVFP4's scales go in 2^-8 smaller, which the end undoes (as
+//    little as their largest allows: sums of tiny x stay above the subnormals);
 //  * the pairs that one word of codes gives are elements (i, i + 4) of its
 //    eight: x is laid down in the same order instead of reordering W.
 // Two CTAs an SM, so that one converts while the other starts or ends. Bound by
@@ -894,8 +895,8 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ C
         } else if (NV) {
           const uint32_t h = e4m3x2_f16x2(sc[j] >> (16 * half));
           const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&h));
-          f0 = bf16x2(q.x * 0x1p100f, q.x * 0x1p100f);
-          f1 = bf16x2(q.y * 0x1p100f, q.y * 0x1p100f);
+          f0 = bf16x2(q.x * 0x1p118f, q.x * 0x1p118f);  // (up to 1.75 2^126)
+          f1 = bf16x2(q.y * 0x1p118f, q.y * 0x1p118f);
         } else {
           // 2^126 2^(c - 127), in two factors above 2^127
           const uint32_t c = (sc[j >> 1] >> (16 * (j & 1) + 8 * half)) & 0xFFu;
@@ -964,7 +965,7 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ C
     ptx::tmem_dealloc(tmem, kTcTmem);
   }
   if (kF16) ptx::wait_prior_grid();  // (the tokens' factors)
-  finish(a, red, ld, 0, 1, tokens, rank, splits, n0, m0, kF16 ? a.p2k : NV ? a.p2k * 0x1p26f : 1.0f,
+  finish(a, red, ld, 0, 1, tokens, rank, splits, n0, m0, kF16 ? a.p2k : NV ? a.p2k * 0x1p8f : 1.0f,
          kF16 ? reinterpret_cast<const float*>(a.ws + sx.factors) : nullptr, ok);
 }
 

@@ -91,3 +91,19 @@ def test_large_tensor_exponent_with_sums_of_one_sign(M, ws):
     x = torch.full((M, K), 1.5 * 2.0 ** -90, device=DEV, dtype=BF16)
     y = mx.mxfp4_gemv(x, q, s, N, K, wparams(True, 0, 100), out_dtype=F32, workspace=space(ws, 0, True, M, N, K))
     check(y, x.double(), w64 * 2.0 ** 100)
+
+
+@pytest.mark.parametrize("nv", [False, True], ids=["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("M", [3, 12, 20])
+def test_x_near_the_smallest_normal_numbers(nv, M):
+    """Rows of x around 2^-116 under weights of order one: the sums are normal
+    fp32 numbers and keep their bits."""
+    import gemm_pt_block_gb300 as mx
+
+    N, K = 130, 1024
+    q, _, _ = weights(N, K, nv, 73)
+    s = torch.full((N, K // (16 if nv else 32)), 0x38 if nv else 127, dtype=torch.uint8, device=DEV)
+    w64 = E2M1.to(DEV)[torch.stack((q & 15, q >> 4), -1).view(N, K).long()]
+    x = (torch.randn((M, K), device=DEV, generator=gen(74)).double() * 2.0 ** -116).to(BF16)
+    y = mx.mxfp4_gemv(x, q, s, N, K, wparams(nv), out_dtype=F32, workspace=False)
+    check(y, x.double(), w64)
