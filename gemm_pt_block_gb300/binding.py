@@ -635,7 +635,10 @@ def mxfp4_gemv(x: torch.Tensor, qw: torch.Tensor, sw: torch.Tensor, N: int, K: i
 
     `workspace`: None (default) lets the call use a scratch tensor where the
     product gains by one (mxfp4_gemv_ex), a CUDA uint8 tensor supplies it,
-    False runs without one."""
+    False runs without one. Not the same bits: bf16 x goes in to 2^-25 of its
+    32-block's largest magnitude (MXFP4 weights) or 2^-39 of its row's (NVFP4
+    above eight rows) with one; without, to 2^-39 of its block's up to eight
+    rows and as it is above."""
     if stream is not None:
         return _on(stream, mxfp4_gemv, x, qw, sw, N, K, w, sx=sx, x_format=x_format, out_dtype=out_dtype, y=y,
                    workspace=workspace)

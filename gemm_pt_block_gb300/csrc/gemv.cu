@@ -11,7 +11,8 @@
 //    one for small weights (one row, 8192 x 8192: 12 us against 15);
 //  * gemv_tc_kernel: more rows otherwise: codes become bf16 or f16 in tensor
 //    memory, once for up to 32 rows.
-// Sums are fp32 throughout and added in a fixed order.
+// Sums are fp32 throughout and added in a fixed order. What each form keeps of x
+// stands at its kernel; the call's choice of one by size changes that.
 //
 // ------------------------------------------------------- up to eight rows ---
 //  * a CTA owns 128 rows of W and a slice of K; one thread streams the codes
@@ -566,8 +567,9 @@ gemv_kernel(const __grid_constant__ CUtensorMap tm, const GemvArgs a, const int 
 // the rows; here the weights become bf16 once, in tensor memory, and tcgen05
 // multiplies them with up to 32 rows of x for one instruction's issue:
 //  * 128 rows of W are the M of the instruction, the rows of x its N; x goes in
-//    as bf16 (E4M3 and E5M2 codes times their factor are exact in bf16), so
-//    both operands are exact and the sums fp32, in tensor memory;
+//    as bf16 (E4M3 and E5M2 codes times their factor are exact in bf16 down to
+//    its smallest step, 2^-133), so both operands are exact and the sums fp32, in
+//    tensor memory;
 //  * eight warps turn codes into bf16: a code's three magnitude bits, moved to
 //    bits 8..6 of a bf16 word, are the subnormal that is 2^-126 times its value
 //    (zero and the half included), so one packed product with 2^126 times the
@@ -977,9 +979,11 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ C
 // that leaves under 2^(e - 4), digit 3 what is left then under 2^(e - 8). Each
 // digit is a row of the instruction's N, and a token's digits are added at the
 // end. E4M3 keeps four significant bits and bf16 has eight, so the digits are
-// exact for magnitudes down to 2^-18 of their block's largest, and off by at
-// most 2^-26 of it below (two digits: 2^-22, which an outlier in a block of
-// small values shows: measured 4.6e-5 of sum |x w|). A block that holds an
+// exact for magnitudes down to 2^-17 of their block's largest, and off by at
+// most 2^-25 of it below: the last digit ends at 2^-17 steps, half of one is
+// 2^-18, and the block's largest is above 224 (two digits: 2^-21, which an outlier
+// in a block of small values shows: measured 4.6e-5 of sum |x w|). Scales end at
+// 2^-127, so a block below 2^-111 is off by up to 2^-137. A block that holds an
 // infinity or a NaN has the NaN scale: its token's sums are NaN.
 //
 // A small kernel makes the digits and their scale tiles once, in the caller's

@@ -452,13 +452,25 @@ enum { MXFP4_GEMV_X_BF16 = 0, MXFP4_GEMV_X_E4M3 = 1, MXFP4_GEMV_X_E5M2 = 2 };
  *      sx [M, K/32] (the quantized outputs above).
  *  y   [M, N] in y_dtype, leading dimension ld_y >= N (any), aligned to its
  *      element.
- * Products are exact (bf16 x above eight rows too; up to eight, x is taken to
- * 2^-39 of its 32-block's largest magnitude) and summed in fp32, in a fixed
- * order; a NaN scale makes what it enters NaN. A 32-block's sum of x times codes,
+ * Accuracy: products of what is kept of x (below) with W are exact, and summed
+ * in fp32 in a fixed order, so that |y - sum_k x W| <= 1e-5 sum_k |x W| and half
+ * a unit of y's type, up to K = 16384. Above eight rows, and in the MXFP8 form of
+ * mxfp4_gemv_ex, the sums are the tensor cores', which round every step (16 or
+ * 32 of K) toward zero: measured 1.1e-5 of sum |x W| for one running sum over K =
+ * 16384 values of one sign; two or four are kept, and K is split over CTAs where
+ * there are few rows of W, but the error grows with K. What is kept of x:
+ *   up to eight rows    bf16 x to 2^-39 of its 32-block's largest magnitude;
+ *   more rows           bf16 x as it is;
+ *   one-byte x          as it is (down to 2^-133);
+ *   with a workspace    see mxfp4_gemv_ex: to 2^-25 of its 32-block's largest
+ *                       magnitude, or 2^-39 of its row's.
+ * An error of x adds sum_k |dx W|: small against sum_k |x W| unless the largest
+ * element of a block meets a zero weight, when nothing of its size is in y.
+ * A NaN scale makes what it enters NaN. A 32-block's sum of x times codes,
  * without the weights' scale, has to stay below fp32's largest value (x below
- * 2^120 does); the scales themselves may be of any size. M may be 0 .. 65536 (the weights
- * are read again for every 32 rows of x), N any, K a multiple of 32, rows of x
- * multiples of 16 bytes; x, qw, sw 16-byte aligned. */
+ * 2^120 does); the scales themselves may be of any size. M may be 0 .. 65536
+ * (the weights are read again for every 32 rows of x), N any, K a multiple of 32,
+ * rows of x multiples of 16 bytes; x, qw, sw 16-byte aligned. */
 mxfp4_status mxfp4_gemv(const void* x, int32_t x_kind, int64_t ld_x, const uint8_t* sx,
                         const uint8_t* qw, const uint8_t* sw, int32_t block, int32_t scale_layout,
                         int32_t tensor_exp, int64_t M, int64_t N, int64_t K, void* y,
@@ -472,8 +484,8 @@ mxfp4_status mxfp4_gemv(const void* x, int32_t x_kind, int64_t ld_x, const uint8
  *    the block-scaled MXFP8 tensor-core instruction, which reads the 4-bit codes
  *    and their scales as they are; x is first written to the workspace as the
  *    sum of three E4M3 vectors with block scales (as it is, if it is MXFP8).
- *    That sum is x to 2^-26 of its 32-block's largest magnitude; a row of x that
- *    holds an infinity or a NaN gives NaN or infinities.
+ *    That sum is x to 2^-25 of its 32-block's largest magnitude (at least 2^-137);
+ *    a row of x that holds an infinity or a NaN gives NaN or infinities.
  *  NVFP4 weights and more than eight rows: x is written there as f16 under one
  *    power of two a row: x to 2^-39 of the row's largest magnitude.
  * The weights are read again for every 32 rows of x (64 of MXFP8 codes with E8M0
