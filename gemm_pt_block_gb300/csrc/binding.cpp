@@ -431,12 +431,20 @@ PyObject* swiglu_backward(PyObject* const* a) {
   return tuple({&dg, &du});
 }
 
-// Weights from which a workspace gains: above eight rows of x (MXFP4, NVFP4), and
-// up to eight (without / with: MXFP4, 12 rows, 4096 x 4096 10.7 / 10.1 us,
-// 8192 x 4096 14.5 / 13.1, 24 rows 11.3 / 12.7 and 15.4 / 16.1, 14336 x 4096
-// 25.6 / 19.2; NVFP4, 24 rows, 4096 x 2048 9.1 / 9.1, 4096 x 4096 11.6 / 10.6;
-// one row, 8192 x 8192 13.9 / 15.6, 28672 x 4096 19.7 / 18.3).
-constexpr int64_t kWorkspaceFrom = 1 << 25, kWorkspaceFromNv = 1 << 24, kWorkspaceFromFew = 3 << 25;
+// Weights from which a workspace gains (times without / with, row-major scales,
+// bf16 x; tiled scales and MXFP8 x cross at the same sizes):
+//  up to 8 rows   4 rows: 8192 x 8192 14.6 / 16.0 us, 28672 x 4096 21.0 / 18.7
+//  9 to 16 rows   12 rows: 4096 x 4096 10.7 / 11.0, 8192 x 4096 15.5 / 14.6
+//  17 to 32 rows  24 rows (one more tile of digits): 8192 x 4096 16.4 / 17.8,
+//                 4096 x 8192 16.6 / 19.3, 11264 x 4096 21.1 / 18.5
+//  more           64 rows: 4096 x 4096 16.7 / 18.5, 8192 x 4096 26.5 / 20.5
+//  NVFP4 above 8  24 rows: 2048 x 4096 10.5 / 9.6 (less than the second launch
+//                 costs the host), 4096 x 4096 11.8 / 10.9
+int64_t workspace_from(int64_t rows, bool nv) {
+  if (rows <= 8) return (int64_t)3 << 25;
+  if (nv) return (int64_t)1 << 24;
+  return rows > 16 && rows <= 32 ? (int64_t)5 << 23 : (int64_t)1 << 25;
+}
 
 // (table, x, qw, sw, N, K, w, sx, x_format, out_dtype, y, workspace) -> (y,)
 PyObject* gemv(PyObject* const* a) {
@@ -489,7 +497,7 @@ PyObject* gemv(PyObject* const* a) {
   at::Tensor ws;
   size_t bytes = 0;
   if (!given(a[11])) {
-    if (weights >= (M <= 8 ? kWorkspaceFromFew : block == MXFP4_BLOCK_1X16 ? kWorkspaceFromNv : kWorkspaceFrom)) {
+    if (weights >= workspace_from(M, block == MXFP4_BLOCK_1X16)) {
       bytes = lib.gemv_workspace(kind, block, M, N, K);
       if (bytes) ws = empty({(int64_t)bytes}, at::kByte, x);
     }

@@ -479,7 +479,8 @@ mxfp4_status mxfp4_gemv(const void* x, int32_t x_kind, int64_t ld_x, const uint8
 /* mxfp4_gemv with an optional workspace, caller-owned device memory, 16-byte
  * aligned (NULL or too small: not used), of mxfp4_gemv_workspace_size(x_kind,
  * block, M, N, K) bytes (0: none would be used). It pays from about 2^25
- * weights on (NVFP4 2^24; 3 * 2^25 up to eight rows of x). Its contents are scratch.
+ * weights on (5 * 2^23 for 17 to 32 rows of x, 3 * 2^25 up to eight; NVFP4 2^24).
+ * Its contents are scratch.
  *  E8M0 scales, K a multiple of 128 and qw 32-byte aligned: the product runs on
  *    the block-scaled MXFP8 tensor-core instruction, which reads the 4-bit codes
  *    and their scales as they are; x is first written to the workspace as the

@@ -89,6 +89,27 @@ def test_the_default_call(M, N, K, nv, form):
     assert ((y[:, rows] - x.double() @ w.t()).abs() <= bound(x.double(), w, form)).all()
 
 
+@pytest.mark.parametrize("M,N,K,nv,ws", [
+    (1, 8192, 8192, False, False), (8, 28672, 4096, False, True), (9, 8192, 4096, False, True), (12, 4096, 4096, False, False),
+    (16, 8192, 4096, False, True), (17, 8192, 4096, False, False), (24, 4096, 8192, False, False), (32, 8192, 4096, False, False),
+    (24, 11264, 4096, False, True), (33, 8192, 4096, False, True), (24, 2048, 4096, True, False), (24, 4096, 4096, True, True)])
+def test_the_form_that_the_default_call_takes(M, N, K, nv, ws):
+    """The faster one of the two that were measured at these sizes (a workspace
+    or none), seen by the bits of its result."""
+    import gemm_pt_block_gb300 as mx
+
+    q, s = weights(N, K, nv, 7, True)
+    x = torch.randn((M, K), device=DEV, generator=gen(8))
+    x.view(M, K // 32, 32)[:, :, 0] = 2.0 ** 36             # meets zero weights: its neighbours lose bits in either form
+    x = x.to(BF16)
+    need = mx.lib().mxfp4_gemv_workspace_size(0, 3 if nv else 0, M, N, K)
+    space = torch.empty(need, dtype=torch.uint8, device=DEV)
+    w = wparams(nv)
+    got, one, none = (mx.mxfp4_gemv(x, q, s, N, K, w, out_dtype=F32, workspace=t) for t in (None, space, False))
+    assert not torch.equal(one, none)
+    assert torch.equal(got, one if ws else none)
+
+
 @pytest.mark.parametrize("M,nv,ws", [(1, False, True), (12, False, True), (12, True, True), (12, False, False), (1, True, False)])
 def test_long_sums_of_one_sign(M, nv, ws):
     """fp32 sums of K = 65536 products of one sign: where the tensor cores add
