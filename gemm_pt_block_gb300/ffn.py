@@ -110,10 +110,7 @@ class _SwigluFn(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy):
         gate, up = ctx.saved_tensors
-        rows, cols = gate.shape
-        # one buffer for both halves: the gradient of the product that wrote them side by side
-        both = torch.empty((rows, 2 * cols), dtype=gate.dtype, device=gate.device)
-        dgate, dup = mxfp4_swiglu_backward(_readable(dy), gate, up, dgate=both[:, :cols], dup=both[:, cols:])
+        dgate, dup = mxfp4_swiglu_backward(_readable(dy), gate, up)
         # (dup alone depends on gate and dy)
         return *_first_order("swiglu", (dy, gate, up) if ctx.needs_input_grad[0] else (dy,), dgate, dup), None
 
@@ -159,6 +156,7 @@ class Mxfp4FeedForward(torch.nn.Module):
             n, h = rmsnorm(x, self.norm, None, self.eps), x
         else:
             n, h = rmsnorm(x, self.norm, residual, self.eps)
+        # (the backward pass of the two slices fills and adds two tensors of gu's size beside the activation's kernel)
         gu = self.gate_up(n)
         return self.down(swiglu(gu[..., :self.hidden], gu[..., self.hidden:])), h
 
