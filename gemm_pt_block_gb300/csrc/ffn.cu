@@ -613,7 +613,7 @@ __device__ __forceinline__ float2 sigmoid2_24(float2 g) {
 // grid's height apart), the next row's loads in flight meanwhile: what a thread
 // works out once is spread over many rows. Short rows (blockDim.x below 32)
 // share a warp. Bound by HBM and issue alike (IPC 3.2): 8192 x 28672 bf16 to
-// E4M3 codes 188 us (6.3 TB/s, 94 % of a copy); fp32 2048 x 28672 80 us (98 %).
+// E4M3 codes 186.5 us (6.3 TB/s, 95 % of a copy); fp32 2048 x 28672 80 us (98 %).
 // `wide`: 32-byte loads where every row allows them (191 us, 193 without).
 template <typename T>
 // bf16: three CTAs an SM (80 registers) measured 191 us at 8192 x 28672 where

@@ -33,7 +33,7 @@
 // memory.
 // Bound by the time to fill and empty two CTAs' rings an SM, then by the
 // conversions: 14336 x 4096, one row, 11.7 us (tiled scales; 2.7 TB/s of HBM's
-// 6.7), 13.1 with row-major ones; 1000 x 1024 4.4 us, of which a launch is two.
+// 6.7), 13.3 with row-major ones; 1000 x 1024 4.2 us, of which a launch is two.
 #include <cuda.h>
 #include <cuda_fp16.h>
 
