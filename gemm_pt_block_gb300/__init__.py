@@ -23,6 +23,9 @@ Calls (same names as the C ABI):
                     mxfp4_swiglu_backward
   mxfp4_gemv        a few activation rows (bf16 or MXFP8) times a 4-bit
                     weight matrix (MXFP4 or NVFP4)
+  mxfp8_cache_append       new keys and values quantized into the pages of an
+                    8-bit cache; mxfp8_cache_read, their values;
+                    mxfp8_cache_attention, attention over them
 """
 from .binding import (  # noqa: F401
     BLOCK_1X32,
@@ -56,6 +59,9 @@ from .binding import (  # noqa: F401
     mxfp4_rmsnorm_quantize,
     mxfp4_swiglu_backward,
     mxfp4_swiglu_quantize,
+    mxfp8_cache_append,
+    mxfp8_cache_attention,
+    mxfp8_cache_read,
     mxfp8_gemm,
     gemm_workspace_size,
     nvfp4_gemm,

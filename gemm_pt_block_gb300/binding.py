@@ -1,7 +1,7 @@
 """ctypes marshalling for libmxfp4.so: torch tensors in, pointers and sizes out.
 
-Nothing here computes: each function (of the norm, activation and few-row
-calls, its C++ half in csrc/binding.cpp) checks that tensors live on a CUDA
+Nothing here computes: each function (of the norm, activation, few-row and
+cache calls, its C++ half in csrc/binding.cpp and csrc/cache_binding.cpp) checks that tensors live on a CUDA
 device with the expected dtype, contiguity and size (the C ABI takes raw
 pointers and cannot check extents), allocates outputs the caller did not
 pass, and forwards raw pointers plus the current CUDA stream to the C ABI.
@@ -50,6 +50,27 @@ class _CParams(ctypes.Structure):
         ("elem_format", ctypes.c_uint32),
         ("tensor_exp", ctypes.c_int32),
     ]
+
+
+class _CCache(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("page_tokens", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class _CBatch(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("ld_table", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+                ("lens", ctypes.c_void_p), ("starts", ctypes.c_void_p), ("sequences", ctypes.c_int64),
+                ("tokens", ctypes.c_int64)]
+
+
+class _CHeads(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("ld_token", ctypes.c_int64),
+                ("ld_head", ctypes.c_int64)]
+
+
+class _CAttention(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p),
+                ("window", ctypes.c_int32)]
 
 
 @dataclass(frozen=True)
@@ -144,6 +165,16 @@ def load_library(path: str) -> ctypes.CDLL:
     L.mxfp4_gemv_ex.argtypes = [P, i32, i64, P, P, P, i32, i32, i32, i64, i64, i64, P, i32, i64, P, sz, P]
     L.mxfp4_gemv_workspace_size.restype = sz
     L.mxfp4_gemv_workspace_size.argtypes = [i32, i32, i64, i64, i64]
+    for n in ("mxfp8_cache_append", "mxfp8_cache_read"):
+        f = getattr(L, n)
+        f.restype = i32
+        f.argtypes = [ctypes.POINTER(_CCache), ctypes.POINTER(_CBatch), ctypes.POINTER(_CHeads),
+                      ctypes.POINTER(_CHeads), P]
+    L.mxfp8_cache_attention.restype = i32
+    L.mxfp8_cache_attention.argtypes = [ctypes.POINTER(_CCache), ctypes.POINTER(_CBatch), ctypes.POINTER(_CHeads), i32,
+                                        ctypes.POINTER(_CAttention), ctypes.POINTER(_CHeads), P, P, sz, P]
+    L.mxfp8_cache_attention_workspace_size.restype = sz
+    L.mxfp8_cache_attention_workspace_size.argtypes = [ctypes.POINTER(_CCache), ctypes.POINTER(_CBatch), i32]
     L.mxfp4_status_string.restype = ctypes.c_char_p
     L.mxfp4_status_string.argtypes = [i32]
     L.mxfp4_last_error.restype = ctypes.c_char_p
@@ -533,6 +564,14 @@ _FAST = ("mxfp4_rmsnorm_quantize", "mxfp4_rmsnorm_backward", "mxfp4_rmsnorm_back
          "mxfp4_swiglu_quantize", "mxfp4_swiglu_backward", "mxfp4_gemv_ex", "mxfp4_gemv_workspace_size")
 
 
+_CACHE = ("mxfp8_cache_append", "mxfp8_cache_read", "mxfp8_cache_attention", "mxfp8_cache_attention_workspace_size")
+
+
+def _no_extension(name: str, e: ImportError) -> RuntimeError:
+    return RuntimeError(f"the {name} extension does not load ({e}); run gemm_pt_block_gb300.build.build(), "
+                        "which builds it for the PyTorch at hand (there is no fallback implementation)")
+
+
 def _fast():
     """The extension's functions and the table of the library in use."""
     global _ext
@@ -540,8 +579,7 @@ def _fast():
         try:
             from . import _binding as _ext
         except ImportError as e:
-            raise RuntimeError(f"the _binding extension does not load ({e}); run gemm_pt_block_gb300.build.build(), "
-                               "which builds it for the PyTorch at hand (there is no fallback implementation)") from e
+            raise _no_extension("_binding", e) from e
     L = lib()
     t = getattr(L, "_fast_table", None)
     if t is None:
@@ -550,6 +588,24 @@ def _fast():
 
 
 _ext = None
+
+
+def _fast_cache():
+    """The same for the calls on the 8-bit cache."""
+    global _cache_ext
+    if _cache_ext is None:
+        try:
+            from . import _cache_binding as _cache_ext
+        except ImportError as e:
+            raise _no_extension("_cache_binding", e) from e
+    L = lib()
+    t = getattr(L, "_cache_table", None)
+    if t is None:
+        t = L._cache_table = _cache_ext.make_table(*[ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in _CACHE])
+    return _cache_ext, t
+
+
+_cache_ext = None
 
 
 def mxfp4_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor | None = None,
@@ -647,6 +703,76 @@ def mxfp4_gemv(x: torch.Tensor, qw: torch.Tensor, sw: torch.Tensor, N: int, K: i
     if r.__class__ is int:
         _check(r)
     return r[0]
+
+
+def mxfp8_cache_append(k: torch.Tensor, v: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                       page_table: torch.Tensor, lens: torch.Tensor, *, starts: torch.Tensor | None = None,
+                       stream=None) -> None:
+    """Quantizes new keys and values k, v [tokens, heads, head_dim] (bf16 or fp32)
+    into the pages of an 8-bit cache: E4M3 codes [pages, 2, heads, page_tokens,
+    head_dim] (keys, then values) with one E8M0 scale for each page, kind and
+    head, scales [pages, 2, heads] (both uint8, updated in place).
+
+    page_table [sequences, max_pages] int32 names each sequence's pages in order,
+    lens [sequences] int32 its tokens, the new ones included; its new tokens are
+    rows starts[b] .. starts[b + 1] - 1 (starts [sequences + 1] int32; None: one
+    row each). A page that holds older tokens keeps the larger of its scale and
+    the new tokens', its codes brought to it; a page written here must belong to
+    one sequence. Pages, lengths and starts outside their ranges are skipped and
+    reported by device_status()."""
+    if stream is not None:
+        return _on(stream, mxfp8_cache_append, k, v, codes, scales, page_table, lens, starts=starts)
+    f, t = _fast_cache()
+    r = f.append(t, k, v, codes, scales, page_table, lens, starts)
+    if r is not None:
+        _check(r)
+
+
+def mxfp8_cache_read(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor, starts: torch.Tensor,
+                     rows: int, *, out_dtype: torch.dtype = torch.bfloat16, k=None, v=None, stream=None):
+    """The values (k, v) [rows, heads, head_dim] in out_dtype (or k's and v's own:
+    bf16 or fp32) of each sequence's first starts[b + 1] - starts[b] tokens, in
+    rows starts[b] .. starts[b + 1] - 1; other rows are left as they are. The
+    cache as in mxfp8_cache_append."""
+    if stream is not None:
+        return _on(stream, mxfp8_cache_read, codes, scales, page_table, starts, rows, out_dtype=out_dtype, k=k, v=v)
+    f, t = _fast_cache()
+    r = f.read(t, codes, scales, page_table, starts, rows, out_dtype, k, v)
+    if r.__class__ is int:
+        _check(r)
+    return r
+
+
+def mxfp8_cache_attention(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor,
+                          lens: torch.Tensor, *, starts: torch.Tensor | None = None, scale: float | None = None,
+                          window: int = 0, softcap: float = 0.0, slopes: torch.Tensor | None = None,
+                          out_dtype: torch.dtype = torch.bfloat16, with_lse: bool = False, out=None, lse=None,
+                          workspace=None, stream=None):
+    """Attention of the new tokens' queries q [tokens, q_heads, head_dim] (bf16)
+    over an 8-bit cache that holds them already (mxfp8_cache_append, with the
+    same page_table, lens and starts). Query i of a sequence's n new tokens
+    stands at position p = lens - n + i and attends tokens 0 .. p, with `window`
+    the last `window` of them; query head h reads head h // (q_heads // heads).
+
+    Scores: scale * (q . k) (scale None: head_dim ** -0.5), then softcap *
+    tanh(score / softcap) where softcap > 0, then slopes[h] * (j - p) for the
+    token of position j (slopes [q_heads] fp32). Returns (out, lse): out
+    [tokens, q_heads, head_dim] in out_dtype (or out's own: bf16 or fp32), lse
+    [tokens, q_heads] fp32 the scores' log-sum-exp, None unless asked for
+    (with_lse or lse). A query without tokens gets zeros and -infinity.
+    `workspace`: a uint8 CUDA tensor for the call's scratch (None: allocated)."""
+    if stream is not None:
+        return _on(stream, mxfp8_cache_attention, q, codes, scales, page_table, lens, starts=starts, scale=scale,
+                   window=window, softcap=softcap, slopes=slopes, out_dtype=out_dtype, with_lse=with_lse, out=out,
+                   lse=lse, workspace=workspace)
+    f, t = _fast_cache()
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    r = f.attention(t, q, codes, scales, page_table, lens, starts, scale, window, softcap, slopes, out_dtype, with_lse,
+                    out, lse, workspace)
+    if r.__class__ is int:
+        _check(r)
+    return r
 
 
 def device_status(stream=None) -> int:

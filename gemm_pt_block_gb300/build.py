@@ -1,8 +1,9 @@
 """Builds libmxfp4.so in place with nvcc for sm_103a (GB300).
 
 Each translation unit is compiled in parallel, then linked into one shared
-library with a static CUDA runtime; the Python extension _binding.so (host C++,
-against PyTorch's headers and libraries) is compiled beside them. The quantizer
+library with a static CUDA runtime; the Python extensions _binding.so and
+_cache_binding.so (host C++, against PyTorch's headers and libraries) are
+compiled beside them. The quantizer
 unit is compiled with ``--fmad=false`` (its arithmetic must not be contracted; it
 also uses explicit round-to-nearest intrinsics) and nothing is built with
 flush-to-zero.
@@ -33,15 +34,17 @@ UNITS = {
     "gemm.cu": ["--fmad=false"],
     "ffn.cu": [],
     "gemv.cu": [],
+    "cache.cu": [],
 }
 HEADERS = ["internal.h", "mx_device.cuh", "ptx.cuh", "quant_device.cuh", "row_device.cuh", "tma_host.h"]
 
 BINDING = os.path.join(HERE, "_binding.so")
+CACHE_BINDING = os.path.join(HERE, "_cache_binding.so")
 BINDING_FOR = os.path.join(BUILD, "binding_for.txt")
 
 
-def _binding_command() -> list[str]:
-    """Compiles csrc/binding.cpp against the installed PyTorch."""
+def _binding_command(source: str) -> list[str]:
+    """Compiles an extension's source in csrc against the installed PyTorch."""
     import sysconfig
 
     import torch
@@ -53,7 +56,7 @@ def _binding_command() -> list[str]:
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             f"-I{t}", f"-I{os.path.join(t, 'torch', 'csrc', 'api', 'include')}",
             f"-I{sysconfig.get_paths()['include']}", f"-I{os.path.join(cuda, 'include')}",
-            os.path.join(CSRC, "binding.cpp"), f"-L{lib}", f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
+            os.path.join(CSRC, source), f"-L{lib}", f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
             "-ltorch_cuda", "-ltorch_python", "-o"]
 
 
@@ -106,12 +109,16 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False,
                 cmd.insert(1, "-Xptxas=-v")
             jobs.append(cmd)
 
-    # (the bounds-checking library is called through the same extension)
-    ext = None
-    src = os.path.join(CSRC, "binding.cpp")
-    if not bounds_check and (force or _binding_stale([src, __file__, os.path.join(ROOT, "include", "mxfp4.h")])):
-        ext = BINDING + f".{os.getpid()}.tmp"
-        jobs.append([*_binding_command(), ext])
+    # (the bounds-checking library is called through the same extensions)
+    exts = []
+    if not bounds_check:
+        srcs = {BINDING: "binding.cpp", CACHE_BINDING: "cache_binding.cpp"}
+        deps = [__file__, os.path.join(ROOT, "include", "mxfp4.h")]
+        deps += [os.path.join(CSRC, n) for n in ("binding_util.h", *srcs.values())]
+        if force or _binding_stale(deps) or _stale(CACHE_BINDING, deps):
+            for so, src in srcs.items():
+                exts.append((so + f".{os.getpid()}.tmp", so))
+                jobs.append([*_binding_command(src), exts[-1][0]])
 
     def run(cmd):
         if verbose:
@@ -119,14 +126,15 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False,
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
 
-    with ThreadPoolExecutor(max_workers=len(UNITS) + 1) as ex:
+    with ThreadPoolExecutor(max_workers=len(UNITS) + 2) as ex:
         for cmd, r in ex.map(run, jobs):
             if verbose or ptxas_v or r.returncode:
                 sys.stderr.write(r.stdout + r.stderr)
             if r.returncode:
                 raise RuntimeError(f"compilation failed: {' '.join(cmd)}")
-    if ext is not None:
-        os.replace(ext, BINDING)
+    for tmp, so in exts:
+        os.replace(tmp, so)
+    if exts:
         with open(BINDING_FOR, "w") as f:
             f.write(_built_for())
     if force or jobs or _stale(lib_out, objs):

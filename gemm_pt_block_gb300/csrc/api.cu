@@ -1,6 +1,6 @@
 // api.cu -- the extern "C" entry points declared in include/mxfp4.h:
 // argument validation, status codes and the thread-local error detail; the
-// work itself is enqueued by the launchers in quant.cu, gemm.cu, ffn.cu and gemv.cu.
+// work itself is enqueued by the launchers in quant.cu, gemm.cu, ffn.cu, gemv.cu and cache.cu.
 #include <cstdarg>
 #include <cstdint>
 #include <cmath>
@@ -677,6 +677,179 @@ mxfp4_status mxfp4_gemv_ex(const void* x, int32_t x_kind, int64_t ld_x, const ui
   return from_cuda(mx::launch_gemv(a, static_cast<cudaStream_t>(stream)), fn);
 }
 
+namespace {
+constexpr int64_t kMaxBlocks = (int64_t)1 << 31;  // pages * 2 * heads
+
+mxfp4_status check_cache(const char* fn, const mxfp8_cache* c, const mxfp8_cache_batch* b, bool lens, mx::CacheArgs* o) {
+  if (!c || !b) return fail(MXFP4_ERR_INVALID_ARG, "%s: cache and batch must be non-NULL", fn);
+  if (c->page_tokens != 16 && c->page_tokens != 32 && c->page_tokens != 64 && c->page_tokens != 128)
+    return fail(MXFP4_ERR_SHAPE, "%s: page_tokens (%d) must be 16, 32, 64 or 128", fn, c->page_tokens);
+  if (c->head_dim != 64 && c->head_dim != 96 && c->head_dim != 128 && c->head_dim != 192 && c->head_dim != 256)
+    return fail(MXFP4_ERR_SHAPE, "%s: head_dim (%d) must be 64, 96, 128, 192 or 256", fn, c->head_dim);
+  if (c->heads < 1 || c->heads > 32767)
+    return fail(MXFP4_ERR_SHAPE, "%s: heads (%d) must be 1 to 32767", fn, c->heads);
+  if (c->pages < 0 || c->pages >= kMaxBlocks / (2 * c->heads))
+    return fail(MXFP4_ERR_SHAPE, "%s: pages (%lld) must be >= 0 with fewer than 2^31 blocks", fn, (long long)c->pages);
+  if (b->sequences < 0 || b->sequences > 65535)
+    return fail(MXFP4_ERR_SHAPE, "%s: sequences (%lld) must be 0 to 65535", fn, (long long)b->sequences);
+  if (b->tokens < 0 || b->tokens >= (1 << 24))
+    return fail(MXFP4_ERR_SHAPE, "%s: tokens (%lld) must be >= 0 and below 2^24", fn, (long long)b->tokens);
+  if (b->max_pages < 0 || b->max_pages >= (1 << 30) / c->page_tokens)
+    return fail(MXFP4_ERR_SHAPE, "%s: max_pages (%lld) * page_tokens must be below 2^30", fn, (long long)b->max_pages);
+  if (b->ld_table < b->max_pages || b->ld_table > kMaxElems)
+    return fail(MXFP4_ERR_SHAPE, "%s: ld_table (%lld) < max_pages, or too large", fn, (long long)b->ld_table);
+  if (!b->starts && b->tokens != b->sequences)
+    return fail(MXFP4_ERR_SHAPE, "%s: without starts tokens (%lld) must equal sequences (%lld)", fn, (long long)b->tokens,
+                (long long)b->sequences);
+  const int64_t blocks = c->pages * 2 * c->heads;
+  if (blocks > 0 && (!c->codes || !c->scales))
+    return fail(MXFP4_ERR_INVALID_ARG, "%s: codes and scales must be non-NULL", fn);
+  if (b->sequences > 0 && ((b->max_pages > 0 && !b->page_table) || (lens && !b->lens)))
+    return fail(MXFP4_ERR_INVALID_ARG, "%s: page_table and lens must be non-NULL", fn);
+  if (!aligned16(c->codes)) return fail(MXFP4_ERR_ALIGN, "%s: codes must be 16-byte aligned", fn);
+  if ((reinterpret_cast<uintptr_t>(b->page_table) | reinterpret_cast<uintptr_t>(b->lens) |
+       reinterpret_cast<uintptr_t>(b->starts)) & 3u)
+    return fail(MXFP4_ERR_ALIGN, "%s: page_table, lens and starts must be 4-byte aligned", fn);
+  o->codes = c->codes;
+  o->scales = c->scales;
+  o->table = b->page_table;
+  o->lens = b->lens;
+  o->starts = b->starts;
+  o->ld_table = b->ld_table;
+  o->pages = (int32_t)c->pages;
+  o->heads = c->heads;
+  o->page_tokens = c->page_tokens;
+  o->head_dim = c->head_dim;
+  o->max_pages = (int32_t)b->max_pages;
+  o->sequences = (int32_t)b->sequences;
+  o->tokens = (int32_t)b->tokens;
+  const int64_t cb = blocks * c->page_tokens * c->head_dim;
+  o->codes_bytes = (uint64_t)(cb > g_extent_shrink ? cb - g_extent_shrink : 0);
+  o->scales_bytes = (uint64_t)(blocks > g_extent_shrink ? blocks - g_extent_shrink : 0);
+  return MXFP4_OK;
+}
+
+// A [tokens, heads, head_dim] tensor; an output's rows may not overlap.
+mxfp4_status check_heads(const char* fn, const char* name, const mxfp8_heads* t, int64_t tokens, int32_t heads,
+                         int32_t head_dim, bool out, mx::Heads* o) {
+  if (!t) return fail(MXFP4_ERR_INVALID_ARG, "%s: %s is NULL", fn, name);
+  if (t->dtype != MXFP4_DTYPE_BF16 && t->dtype != MXFP4_DTYPE_F32)
+    return fail(MXFP4_ERR_INVALID_ARG, "%s: bad dtype %d of %s", fn, t->dtype, name);
+  if (!t->p && tokens > 0) return fail(MXFP4_ERR_INVALID_ARG, "%s: %s is NULL", fn, name);
+  // (the stride of a single head or a single row is not used)
+  const int64_t ld_h = heads > 1 ? t->ld_head : head_dim, ld_t = tokens > 1 ? t->ld_token : 0;
+  if (ld_h < head_dim || ld_h > kMaxElems || ld_t < 0 || ld_t > kMaxElems || (heads > 1 && too_large(heads, ld_h)) ||
+      (tokens > 1 && ld_t > 0 && too_large(tokens, ld_t)))
+    return fail(MXFP4_ERR_SHAPE, "%s: strides (%lld, %lld) of %s out of range (head_dim %d)", fn, (long long)t->ld_token,
+                (long long)t->ld_head, name, head_dim);
+  // disjoint: rows behind one another's heads, or heads behind one another's rows
+  if (tokens > 1 && (out ? ld_t < (heads - 1) * ld_h + head_dim && (ld_t < head_dim || ld_h < (tokens - 1) * ld_t + head_dim)
+                         : false))
+    return fail(MXFP4_ERR_SHAPE, "%s: rows of %s overlap (strides %lld, %lld)", fn, name, (long long)t->ld_token,
+                (long long)t->ld_head);
+  if (!aligned16(t->p) || ld_h % 8 != 0 || ld_t % 8 != 0)
+    return fail(MXFP4_ERR_ALIGN, "%s: %s must be 16-byte aligned with strides %% 8 == 0", fn, name);
+  o->p = t->p;
+  o->ld_t = ld_t;
+  o->ld_h = ld_h;
+  const int64_t n = tokens > 0 ? ((tokens - 1) * ld_t + (heads - 1) * ld_h + head_dim) * elem_bytes(t->dtype) : 0;
+  o->bytes = (uint64_t)(n > g_extent_shrink ? n - g_extent_shrink : 0);
+  return MXFP4_OK;
+}
+
+// Keys and values, in one dtype.
+mxfp4_status check_pair(const char* fn, const mxfp8_heads* k, const mxfp8_heads* v, const mx::CacheArgs& c, bool out,
+                        mx::Heads* ok, mx::Heads* ov) {
+  mxfp4_status st = check_heads(fn, "k", k, c.tokens, c.heads, c.head_dim, out, ok);
+  if (!st) st = check_heads(fn, "v", v, c.tokens, c.heads, c.head_dim, out, ov);
+  if (!st && k->dtype != v->dtype) return fail(MXFP4_ERR_INVALID_ARG, "%s: k and v must have one dtype", fn);
+  return st;
+}
+}  // namespace
+
+mxfp4_status mxfp8_cache_append(const mxfp8_cache* cache, const mxfp8_cache_batch* batch, const mxfp8_heads* k,
+                                const mxfp8_heads* v, void* stream) {
+  const char* fn = "mxfp8_cache_append";
+  mx::CacheArgs c{};
+  mx::Heads hk{}, hv{};
+  mxfp4_status st = check_cache(fn, cache, batch, true, &c);
+  if (!st) st = check_pair(fn, k, v, c, false, &hk, &hv);
+  if (st) return st;
+  return from_cuda(mx::launch_cache_append(c, hk, hv, k->dtype == MXFP4_DTYPE_F32, static_cast<cudaStream_t>(stream)), fn);
+}
+
+mxfp4_status mxfp8_cache_read(const mxfp8_cache* cache, const mxfp8_cache_batch* batch, const mxfp8_heads* k,
+                              const mxfp8_heads* v, void* stream) {
+  const char* fn = "mxfp8_cache_read";
+  mx::CacheArgs c{};
+  mx::Heads hk{}, hv{};
+  mxfp4_status st = check_cache(fn, cache, batch, false, &c);
+  if (st) return st;
+  if (!c.starts && c.sequences > 0) return fail(MXFP4_ERR_INVALID_ARG, "%s: starts is NULL", fn);
+  if ((st = check_pair(fn, k, v, c, true, &hk, &hv))) return st;
+  return from_cuda(mx::launch_cache_read(c, hk, hv, k->dtype == MXFP4_DTYPE_F32, static_cast<cudaStream_t>(stream)), fn);
+}
+
+namespace {
+mxfp4_status check_q_heads(const char* fn, const mx::CacheArgs& c, int32_t q_heads) {
+  if (q_heads < 1 || q_heads > 65535 || q_heads % c.heads != 0)
+    return fail(MXFP4_ERR_SHAPE, "%s: q_heads (%d) must be a multiple of heads (%d), 1 to 65535", fn, q_heads, c.heads);
+  return MXFP4_OK;
+}
+}  // namespace
+
+size_t mxfp8_cache_attention_workspace_size(const mxfp8_cache* cache, const mxfp8_cache_batch* batch, int32_t q_heads) {
+  const char* fn = "mxfp8_cache_attention_workspace_size";
+  mx::AttentionArgs a{};
+  // (sizes alone count: no pointer is looked at)
+  if (!cache || !batch) return 0;
+  mxfp8_cache c = *cache;
+  mxfp8_cache_batch b = *batch;
+  c.codes = c.scales = reinterpret_cast<uint8_t*>(16);
+  b.page_table = b.lens = reinterpret_cast<const int32_t*>(16);
+  if (check_cache(fn, &c, &b, true, &a.c) || check_q_heads(fn, a.c, q_heads)) return 0;
+  a.q_heads = q_heads;
+  return (size_t)mx::cache_attention_workspace_bytes(a);
+}
+
+mxfp4_status mxfp8_cache_attention(const mxfp8_cache* cache, const mxfp8_cache_batch* batch, const mxfp8_heads* q,
+                                   int32_t q_heads, const mxfp8_attention_params* params, const mxfp8_heads* out,
+                                   float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "mxfp8_cache_attention";
+  mx::AttentionArgs a{};
+  mxfp4_status st = check_cache(fn, cache, batch, true, &a.c);
+  if (!st) st = check_q_heads(fn, a.c, q_heads);
+  if (st) return st;
+  if (!params) return fail(MXFP4_ERR_INVALID_ARG, "%s: params is NULL", fn);
+  if (!(params->scale >= -1.0e30f && params->scale <= 1.0e30f))
+    return fail(MXFP4_ERR_INVALID_ARG, "%s: scale must be finite", fn);
+  if (!(params->softcap == 0.0f || (params->softcap >= 1.0e-30f && params->softcap <= 1.0e30f)))
+    return fail(MXFP4_ERR_INVALID_ARG, "%s: softcap must be 0 or a positive number", fn);
+  if (params->window < 0) return fail(MXFP4_ERR_INVALID_ARG, "%s: window (%d) must be >= 0", fn, params->window);
+  if ((reinterpret_cast<uintptr_t>(params->slopes) | reinterpret_cast<uintptr_t>(lse)) & 3u)
+    return fail(MXFP4_ERR_ALIGN, "%s: slopes and lse must be 4-byte aligned", fn);
+  if ((st = check_heads(fn, "q", q, a.c.tokens, q_heads, a.c.head_dim, false, &a.q))) return st;
+  if (q->dtype != MXFP4_DTYPE_BF16) return fail(MXFP4_ERR_INVALID_ARG, "%s: q must be bf16", fn);
+  if ((st = check_heads(fn, "out", out, a.c.tokens, q_heads, a.c.head_dim, true, &a.out))) return st;
+  if (!aligned16(workspace)) return fail(MXFP4_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
+  a.q_heads = q_heads;
+  const size_t need = (size_t)mx::cache_attention_workspace_bytes(a);
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(MXFP4_ERR_INVALID_ARG, "%s: workspace of %zu bytes, %zu are needed", fn, workspace ? workspace_bytes : 0,
+                need);
+  a.ws = static_cast<float*>(workspace);
+  a.ws_bytes = need;
+  a.lse = lse;
+  const int64_t n = (int64_t)a.c.tokens * q_heads * 4;
+  a.lse_bytes = (uint64_t)(n > g_extent_shrink ? n - g_extent_shrink : 0);
+  a.slopes = params->slopes;
+  a.scale = params->scale;
+  a.softcap = params->softcap;
+  a.window = params->window;
+  a.out_f32 = out->dtype == MXFP4_DTYPE_F32;
+  return from_cuda(mx::launch_cache_attention(a, static_cast<cudaStream_t>(stream)), fn);
+}
+
 mxfp4_status mxfp4_device_status(void* stream) {
   uint32_t err = 0;
   cudaError_t e = mx::read_device_error(static_cast<cudaStream_t>(stream), &err);
@@ -685,6 +858,8 @@ mxfp4_status mxfp4_device_status(void* stream) {
     return fail(MXFP4_ERR_TIMEOUT, "a bounded device-side wait in the GEMM ran out");
   if (err == MXFP4_ERR_BOUNDS)
     return fail(MXFP4_ERR_BOUNDS, "a kernel store fell outside its output (skipped)");
+  if (err == MXFP4_ERR_INVALID_ARG)
+    return fail(MXFP4_ERR_INVALID_ARG, "a cache call met a page, a length or a row start outside its range (skipped)");
   return err ? fail(static_cast<mxfp4_status>(err), "device error word %u", err) : MXFP4_OK;
 }
 

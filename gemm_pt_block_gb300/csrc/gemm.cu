@@ -1256,7 +1256,7 @@ cudaError_t read_device_error(cudaStream_t st, uint32_t* err) {
     e = cudaMemcpyToSymbol(g_gemm_error, &zero, sizeof(uint32_t));
     if (e != cudaSuccess) return e;
   }
-  for (auto read : {read_quant_error, read_ffn_error, read_gemv_error}) {
+  for (auto read : {read_quant_error, read_ffn_error, read_gemv_error, read_cache_error}) {
     uint32_t other = 0;
     e = read(&other);
     if (e != cudaSuccess) return e;

@@ -36,6 +36,8 @@ struct OrientArgs {
 
 // Device error word value of a store outside its output (bounds-checking builds).
 constexpr uint32_t kErrBounds = 7;
+// A page, length or row start on the device outside its range.
+constexpr uint32_t kErrIndex = 1;
 
 // A row-wise quantized output of the norm and activation kernels: 1x32 blocks
 // with an E8M0 scale, or 1x16 blocks with an E4M3 scale (NVFP4), nearest-even.
@@ -105,6 +107,36 @@ struct GemvArgs {
   bool nv, mma, y_f32;
 };
 
+// The 8-bit cache of keys and values, and the sequences of a call on it
+// (mxfp8_cache, mxfp8_cache_batch).
+struct CacheArgs {
+  uint8_t *codes, *scales;
+  const int32_t *table, *lens, *starts;  // starts (lens for reads): may be NULL
+  int64_t ld_table;
+  int32_t pages, heads, page_tokens, head_dim;
+  int32_t max_pages, sequences, tokens;
+  uint64_t codes_bytes, scales_bytes;  // extents
+};
+
+// A [tokens, heads, head_dim] tensor by its strides in elements.
+struct Heads {
+  void* p;
+  int64_t ld_t, ld_h;
+  uint64_t bytes;  // extent
+};
+
+struct AttentionArgs {
+  CacheArgs c;
+  Heads q, out;
+  float* lse;           // may be NULL
+  const float* slopes;  // may be NULL
+  float* ws;
+  uint64_t ws_bytes, lse_bytes;
+  float scale, softcap;
+  int32_t q_heads, window;
+  bool out_f32;
+};
+
 // Fills keys, sm_*, xw and sgn from seed and sign_mask.
 void prepare_orient(OrientArgs* o);
 
@@ -146,10 +178,15 @@ cudaError_t launch_swiglu_grad(const SwigluGradArgs& a, bool f32, bool dy_f32, c
 cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t st);
 // Workspace that launch_gemv would use for these arguments (0: none).
 int64_t gemv_workspace_bytes(const GemvArgs& a);
+cudaError_t launch_cache_append(const CacheArgs& c, const Heads& k, const Heads& v, bool f32, cudaStream_t st);
+cudaError_t launch_cache_read(const CacheArgs& c, const Heads& k, const Heads& v, bool f32, cudaStream_t st);
+cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t st);
+int64_t cache_attention_workspace_bytes(const AttentionArgs& a);
 // Each reads and clears the device error word of its translation unit.
 cudaError_t read_quant_error(uint32_t* err);
 cudaError_t read_ffn_error(uint32_t* err);
 cudaError_t read_gemv_error(uint32_t* err);
+cudaError_t read_cache_error(uint32_t* err);
 // Reads and clears the device error words (synchronizes st).
 cudaError_t read_device_error(cudaStream_t st, uint32_t* err);
 // MXFP8 GEMM (E4M3, or E5M2 with e5m2, codes [M, K], [N, K] bytes, both

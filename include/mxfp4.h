@@ -498,6 +498,117 @@ mxfp4_status mxfp4_gemv_ex(const void* x, int32_t x_kind, int64_t ld_x, const ui
                            size_t workspace_bytes, void* stream);
 size_t mxfp4_gemv_workspace_size(int32_t x_kind, int32_t block, int64_t M, int64_t N, int64_t K);
 
+/* ---- A cache of keys and values in 8 bits --------------------------------
+ * (the pages have no counterpart: what a decode step needs beside the few-row
+ * product.) The cache lies in pages of page_tokens tokens:
+ *   codes   E4M3 [pages, 2, heads, page_tokens, head_dim], keys then values;
+ *   scales  E8M0 [pages, 2, heads]: one for each page, kind and head.
+ * A value is code * 2^(scale - 127); under scale 0xFF it is NaN. Codes 0x7F and
+ * 0xFF (E4M3's NaN), which mxfp8_cache_append never writes, are not allowed in
+ * places that hold tokens; places behind a sequence's last token may hold
+ * anything.
+ *  codes 16-byte aligned, below 2^31 blocks (pages * 2 * heads); page_tokens
+ *  16, 32, 64 or 128; head_dim 64, 96, 128, 192 or 256. */
+typedef struct {
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t pages;
+  int32_t heads;
+  int32_t page_tokens;
+  int32_t head_dim;
+} mxfp8_cache;
+
+/* The sequences of a call; all arrays are device memory, 4-byte aligned.
+ *  page_table [sequences, max_pages], leading dimension ld_table: a sequence's
+ *      pages in order. Entries behind its last token are not looked at.
+ *  lens [sequences]: tokens of each sequence, the new ones included.
+ *  starts [sequences + 1]: sequence b's rows of the call's tensors are
+ *      starts[b] .. starts[b + 1] - 1 (its new tokens, in order). NULL: one row
+ *      each, row b (tokens == sequences). Rows before starts[0] and from
+ *      starts[sequences] on are left as they are.
+ *  tokens: rows of the call's tensors.
+ * Up to 65535 sequences, max_pages * page_tokens below 2^30, tokens below 2^24.
+ * What the arrays hold is checked on the device: a sequence whose starts leave
+ * [0, tokens] or fall, or whose length is below 0 (for an append: below its
+ * number of rows) or above max_pages * page_tokens, and a page outside the
+ * cache, touch nothing outside the tensors; the next mxfp4_device_status
+ * returns MXFP4_ERR_INVALID_ARG. Appends and reads skip them; attention gives
+ * NaN where a missing page is attended. */
+typedef struct {
+  const int32_t* page_table;
+  int64_t ld_table;
+  int64_t max_pages;
+  const int32_t* lens;
+  const int32_t* starts;
+  int64_t sequences;
+  int64_t tokens;
+} mxfp8_cache_batch;
+
+/* A [tokens, heads, head_dim] tensor of bf16 or fp32 by its strides in elements
+ * (head_dim contiguous): 16-byte aligned, strides multiples of 8 elements,
+ * ld_head at least head_dim; an output's rows must not overlap. */
+typedef struct {
+  void* p;
+  int32_t dtype;
+  int64_t ld_token;
+  int64_t ld_head;
+} mxfp8_heads;
+
+/* Quantizes new keys and values into their pages: row i of sequence b's n rows
+ * becomes its token lens[b] - n + i. For each page and head the new tokens'
+ * max-abs M asks for the smallest scale with 448 * 2^e >= M (nothing clips; -127
+ * for M = 0). A page that already holds tokens of the sequence (positions below
+ * lens[b] - n) keeps the larger of its scale and that one, and where the scale
+ * grows its older codes are multiplied by the power of two between them and
+ * rounded to nearest-even; a page without any takes the new scale. Codes are
+ * nearest-even. Where the new tokens hold an infinity or a NaN the page's scale
+ * becomes 0xFF and the new codes 0 (MX's rule for a block that is not a
+ * number), and stays so. k, v [tokens, heads, head_dim] in one dtype. A page
+ * that is written must belong to one sequence of the call. */
+mxfp4_status mxfp8_cache_append(const mxfp8_cache* cache, const mxfp8_cache_batch* batch,
+                                const mxfp8_heads* k, const mxfp8_heads* v, void* stream);
+
+/* The values of each sequence's first starts[b + 1] - starts[b] tokens, into
+ * those rows of k and v [tokens, heads, head_dim] (bf16: nearest-even of the
+ * fp32 value). batch->starts must not be NULL; lens is not used. */
+mxfp4_status mxfp8_cache_read(const mxfp8_cache* cache, const mxfp8_cache_batch* batch,
+                              const mxfp8_heads* k, const mxfp8_heads* v, void* stream);
+
+/* Scores of mxfp8_cache_attention, s = scale * (q . k), then
+ *  softcap  > 0: s = softcap * tanh(s / softcap); 0: none.
+ *  slopes   [q_heads] fp32 device memory: s += slopes[h] * (j - p) for the key of
+ *           position j and the query of position p; NULL: none.
+ *  window   > 0: a query attends the last `window` tokens up to its own; 0: all. */
+typedef struct {
+  float scale;
+  float softcap;
+  const float* slopes;
+  int32_t window;
+} mxfp8_attention_params;
+
+/* Attention of the new tokens over the cache that holds them already:
+ *   out[i, h] = sum_j softmax_j(s_j) v_j,   lse[i, h] = ln sum_j exp(s_j)
+ * where query i of sequence b's n has position p = lens[b] - n + i and attends
+ * j in [max(0, p - window + 1), p]; query head h reads head h / (q_heads /
+ * heads) of the cache. A query that attends nothing (p < 0) gets out 0 and lse
+ * -infinity. One token for each sequence is a decode step's form; several
+ * (proposed tokens, a prompt's chunk) attend causally.
+ *  q    bf16 [tokens, q_heads, head_dim]; q_heads a multiple of heads, up to
+ *       65535. It goes in to 2^-39 of its row's largest magnitude.
+ *  out  bf16 or fp32 [tokens, q_heads, head_dim]; lse fp32 [tokens, q_heads]
+ *       contiguous, or NULL.
+ *  workspace  device memory, 16-byte aligned, of
+ *       mxfp8_cache_attention_workspace_size bytes; scratch for the call alone.
+ * Results have the same bits on every call. Scores must stay below fp32's
+ * largest value. A row of q with an infinity or a NaN gives NaN. */
+mxfp4_status mxfp8_cache_attention(const mxfp8_cache* cache, const mxfp8_cache_batch* batch,
+                                   const mxfp8_heads* q, int32_t q_heads,
+                                   const mxfp8_attention_params* params, const mxfp8_heads* out,
+                                   float* lse, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+size_t mxfp8_cache_attention_workspace_size(const mxfp8_cache* cache,
+                                            const mxfp8_cache_batch* batch, int32_t q_heads);
+
 /* Human-readable name of a status code (static string). */
 const char* mxfp4_status_string(mxfp4_status s);
 
