@@ -794,6 +794,8 @@ namespace {
 mxfp4_status check_q_heads(const char* fn, const mx::CacheArgs& c, int32_t q_heads) {
   if (q_heads < 1 || q_heads > 65535 || q_heads % c.heads != 0)
     return fail(MXFP4_ERR_SHAPE, "%s: q_heads (%d) must be a multiple of heads (%d), 1 to 65535", fn, q_heads, c.heads);
+  if ((int64_t)c.tokens * q_heads >= (int64_t)1 << 31)
+    return fail(MXFP4_ERR_SHAPE, "%s: tokens (%d) * q_heads (%d) must be below 2^31", fn, c.tokens, q_heads);
   return MXFP4_OK;
 }
 }  // namespace
@@ -845,7 +847,7 @@ mxfp4_status mxfp8_cache_attention(const mxfp8_cache* cache, const mxfp8_cache_b
   a.slopes = params->slopes;
   a.scale = params->scale;
   a.softcap = params->softcap;
-  a.window = params->window;
+  a.window = params->window < (1 << 30) ? params->window : 1 << 30;  // (no length passes it)
   a.out_f32 = out->dtype == MXFP4_DTYPE_F32;
   return from_cuda(mx::launch_cache_attention(a, static_cast<cudaStream_t>(stream)), fn);
 }

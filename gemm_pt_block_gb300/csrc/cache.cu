@@ -2,10 +2,12 @@
 // written, reading them back, and attention over them.
 #include <cstdint>
 #include <cuda_runtime.h>
+#include <mutex>
 
 #include "internal.h"
 #include "mx_device.cuh"
 #include "ptx.cuh"
+#include "tma_host.h"
 
 namespace mx {
 namespace {
@@ -230,94 +232,748 @@ __global__ void __launch_bounds__(1024) cache_read_kernel(CacheArgs c, Heads k, 
 }
 
 // ----------------------------------------------------------------- attention ---
+//
+// With s_j a row's scores in log2 units and 2^ev_j the scale of token j's values,
+//   out = (sum_j 2^s_j 2^ev_j code_j) / (sum_j 2^s_j)
+// in one pass over the tokens with two running maxima, m = max s_j for the
+// denominator and m + lift, lift = max (s_j - m + ev_j), for the numerator, whose
+// weights are then at most one whatever the pages' scales are.
+//
+// One CTA an SM takes an equal run of units: 256 tokens of one sequence, head of
+// the cache and tile of query rows (the rows of the query heads that share the
+// head, of all its new tokens). One warp fetches 32 tokens a time into a ring in
+// shared memory by TMA; eight warps take them in turn, each with its own maxima
+// and sums, so the loop has no barrier among them. Codes become f16 in registers
+// (exact), keys as the A operand of S^T = K Q^T, values, transposed as they are
+// read, as that of O^T = V^T P^T: query rows are the instruction's N of eight.
+// Eight warps' sums are joined when a tile's run ends; a tile that several CTAs
+// share leaves its parts in the workspace for cache_join_kernel.
 
-// A warp takes one query row: a token a lane for the scores, channels a lane
-// for the values.
-template <int D>
-__global__ void __launch_bounds__(32) cache_attention_kernel(AttentionArgs a) {
-  constexpr int kChannels = D / 32;
-  __shared__ float qs[D];
-  const CacheArgs& c = a.c;
-  const int lane = threadIdx.x, shift = 31 - __clz(c.page_tokens);
-  const int32_t t = blockIdx.x, hq = blockIdx.y, h = hq / (a.q_heads / c.heads);
-  int32_t b = t;
-  if (c.starts) b = find(c.sequences, t, [&](int32_t i) { return (int64_t)__ldg(c.starts + i); });
-  Seq s;
-  if (!rows_of(c, b, &s) || t < s.row || t >= s.row + s.n) return;
-  const int32_t most = c.max_pages << shift;
-  s.len = __ldg(c.lens + b);
-  if (s.len < 0 || s.len > most) {
-    index_fail();
-    s.len = s.len < 0 ? 0 : most + 1;
+constexpr int kSms = 152;
+constexpr int kWarps = 8;                       // that multiply
+constexpr int kThreads = (kWarps + 1) * 32;     // and one that fetches
+constexpr int kChunk = 32;                      // tokens of a warp at a time
+constexpr int kUnit = kWarps * kChunk;
+constexpr float kTop = 15.0f;                   // weights are held times 2^15: f16 keeps 2^-39 of the largest
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+
+template <int D, int NT>
+struct Attn {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kBox = D % 128 == 0 ? 128 : D % 64 == 0 ? 64 : 32;  // bytes of a row in one swizzled slab
+  static constexpr int kHalf = 16 * D;                                     // 16 tokens of keys or values
+  static constexpr int kSlot = 4 * kHalf;                                  // 32 tokens of keys, then of values
+  static constexpr int kPart = kRows * D * 4;                              // a warp's sums
+  static constexpr int kFixed = 4 * kPart + kWarps * kRows * 12 + 1024;    // (below)
+  static constexpr int kFit = (227 * 1024 - 1024 - kFixed) / kSlot;
+  static constexpr int kSlots = kFit < 32 ? kFit : 32;
+  static constexpr int kBytes = 1024 + kSlots * kSlot + kFixed;
+};
+
+struct AttnCtl {
+  uint64_t full[32], empty[32];
+  uint32_t meta[32];  // scales of a slot's halves: keys 0, keys 1, values 0, values 1
+  int64_t at;         // units before the first sequence of this CTA
+  int64_t units;      // of all sequences
+  int32_t first;      // that sequence
+  uint32_t abort;
+};
+static_assert(sizeof(AttnCtl) <= 1024, "control block");
+
+// A split tile's rows, for the join: n_rows of its sequence's rows from row0 on.
+struct Split {
+  int32_t token, row0, rows, head, parts, unused[3];
+};
+
+// Floats of the workspace: a Split for each CTA, then two parts each (a tile
+// that began before it, a tile that goes on behind it): maxima, sums, numerators.
+__host__ __device__ constexpr int64_t part_floats(int rows, int D) { return (int64_t)rows * D + 3 * rows; }
+
+// Bounded wait (about 2 s); the whole warp goes on or leaves together.
+__device__ __forceinline__ bool wait_bar_warp(uint32_t bar, uint32_t parity, uint32_t* abort) {
+  bool ok = ptx::mbar_try_wait(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = ptx::globaltimer_ns();
+    while (!(ok = ptx::mbar_try_wait_sleep(bar, parity, 100000u))) {
+      if (*reinterpret_cast<volatile uint32_t*>(abort)) break;
+      if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
+        *reinterpret_cast<volatile uint32_t*>(abort) = 1u;
+        atomicExch(&g_cache_error, 6u);  // MXFP4_ERR_TIMEOUT
+        break;
+      }
+    }
   }
-  const int32_t p = s.len - s.n + (t - s.row), lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
-  const uint16_t* q = static_cast<const uint16_t*>(a.q.p) + t * a.q.ld_t + hq * a.q.ld_h;
-  for (int d = lane; d < D; d += 32) qs[d] = __uint_as_float((uint32_t)q[d] << 16);
-  __syncwarp();
-  float m = -INFINITY, sum = 0.0f, o[kChannels] = {};
-  const float slope = a.slopes ? __ldg(a.slopes + hq) : 0.0f;
-  for (int32_t j0 = lo; j0 <= p; j0 += 32) {
-    const int32_t j = j0 + lane;
-    float z = -INFINITY, vs = 0.0f;
-    const uint8_t* vrow = nullptr;
-    if (j <= p) {
-      const int32_t page = page_of(c, b, j >> shift);
-      z = __uint_as_float(0x7FC00000u);
-      if (page >= 0) {
-        const int64_t kb = (int64_t)page * 2 * c.heads + h;
-        const int64_t at = (j & (c.page_tokens - 1)) * D;
-        const uint8_t* krow = c.codes + kb * c.page_tokens * D + at;
-        vrow = c.codes + (kb + c.heads) * c.page_tokens * D + at;
-        vs = scale_value(c.scales[kb + c.heads]);
-        float dot = 0.0f;
-        for (int d = 0; d < D; d += 16) {
-          const uint4 w = *reinterpret_cast<const uint4*>(krow + d);
-          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+  return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t f16x2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ void ldsm(uint32_t at, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t at, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void tma_pages(uint32_t dst, const CUtensorMap* map, int32_t half, int32_t block, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %2, %2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(half), "r"(block), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void warps_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); }
+
+// 2^e for a whole e, 0 below the smallest normal number.
+__device__ __forceinline__ float pow2i(int e) { return e < -126 ? 0.0f : __uint_as_float((uint32_t)(min(e, 127) + 127) << 23); }
+
+// The place of a CTA in the order of all units: sequences, their heads, their
+// tiles of kRows query rows, units of 256 tokens. A sequence's tiles count alike
+// (the longest's units): those that a tile has no tokens for are passed over.
+template <int kRows>
+struct Walk {
+  int32_t b, n, row, len, tiles, units;  // sequence: rows, first row, length, tiles, units of each
+  int32_t head, tile, unit;
+  int32_t row0, p0, lo, hi;  // tile: first row, its position, tokens [lo, hi) that a row attends; lo rounded down
+
+  // Sequence s; its number of units.
+  __device__ __forceinline__ int64_t sequence(const AttentionArgs& a, int32_t s) {
+    const int G = a.q_heads / a.c.heads;
+    b = s;
+    Seq q;
+    n = rows_of(a.c, s, &q) ? q.n : 0;
+    if (n == 0) return 0;
+    row = q.row;
+    len = __ldg(a.c.lens + s);
+    const int32_t most = a.c.max_pages * a.c.page_tokens;
+    if (len < 0 || len > most) {
+      index_fail();
+      len = len < 0 ? 0 : most + 1;
+    }
+    tiles = (n * G + kRows - 1) / kRows;
+    const int32_t tokens = (kRows + G - 2) / G + 1;  // that a tile's rows may belong to
+    const int32_t span = a.window > 0 ? min(len, a.window + tokens + kChunk) : len;
+    units = max(1, (span + kUnit - 1) / kUnit);
+    return (int64_t)a.c.heads * tiles * units;
+  }
+  // Unit u of the sequence.
+  __device__ __forceinline__ void place(const AttentionArgs& a, int64_t u) {
+    const int64_t t = u / units;
+    unit = (int32_t)(u - t * units);
+    head = (int32_t)(t / tiles);
+    tile = (int32_t)(t - (int64_t)head * tiles);
+    set_tile(a);
+  }
+  __device__ __forceinline__ void set_tile(const AttentionArgs& a) {
+    const int G = a.q_heads / a.c.heads;
+    row0 = tile * kRows;
+    p0 = len - n + row0 / G;
+    hi = max(0, len - n + (min(row0 + kRows, n * G) - 1) / G + 1);
+    lo = a.window > 0 ? max(0, p0 - a.window + 1) & -kChunk : 0;
+  }
+  // Chunks of this unit that hold tokens to attend.
+  __device__ __forceinline__ int32_t chunks() const {
+    return min(max((hi - (lo + unit * kUnit) + kChunk - 1) / kChunk, 0), kWarps);
+  }
+  // The next unit (there is one).
+  __device__ __forceinline__ void next(const AttentionArgs& a) {
+    if (++unit < units) return;
+    unit = 0;
+    if (++tile == tiles) {
+      tile = 0;
+      if (++head == a.c.heads) {
+        head = 0;
+        while (b + 1 < a.c.sequences && sequence(a, b + 1) == 0) {
+        }
+      }
+    }
+    set_tile(a);
+  }
+};
+
+// Finds the first unit of this CTA: sequence (first) and the units before that
+// sequence (at). All threads; ends with a barrier.
+template <int kRows>
+__device__ __forceinline__ void find_start(const AttentionArgs& a, AttnCtl* ctl, int64_t* sums) {
+  const int32_t B = a.c.sequences, each = (B + kThreads - 1) / kThreads;
+  const int32_t s0 = min((int32_t)threadIdx.x * each, B), s1 = min(s0 + each, B);
+  Walk<kRows> w;
+  int64_t mine = 0;
+  for (int32_t s = s0; s < s1; ++s) mine += w.sequence(a, s);
+  int64_t upto = mine;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float f[4];
-            values4(x[i], f);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) dot = fmaf(f[e], qs[d + 4 * i + e], dot);
+  for (int i = 1; i < 32; i <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, upto, i);
+    if ((threadIdx.x & 31) >= i) upto += v;
+  }
+  if ((threadIdx.x & 31) == 31) sums[threadIdx.x >> 5] = upto;
+  __syncthreads();
+  int64_t before = upto - mine, all = 0;
+  for (int i = 0; i <= kWarps; ++i) {
+    if (i < (int)(threadIdx.x >> 5)) before += sums[i];
+    all += sums[i];
+  }
+  const int64_t ctas = min((int64_t)gridDim.x, all), begin = ctas ? all * min((int64_t)blockIdx.x, ctas) / ctas : 0;
+  if (before <= begin && begin < before + mine) {
+    for (int32_t s = s0; s < s1; ++s) {
+      const int64_t u = w.sequence(a, s);
+      if (begin < before + u) {
+        ctl->first = s;
+        ctl->at = before;
+        break;
+      }
+      before += u;
+    }
+  }
+  if (threadIdx.x == 0) ctl->units = all;
+  __syncthreads();
+}
+
+// Sums of a tile in the accumulators' order, four floats for each of 32 lanes:
+// quad e belongs to rows 8 (e / 32 % NT) + 2 (lane % 4) (elements 0, 2) and the
+// one behind (1, 3), channels 16 (e / 32 / NT) + 2 (lane / 4) and the one behind.
+struct Quad {
+  int row, d;
+};
+template <int NT>
+__device__ __forceinline__ Quad quad(int e) {
+  const int lane = e & 31, i = e >> 5;
+  return Quad{8 * (i % NT) + 2 * (lane & 3), 16 * (i / NT) + 2 * (lane >> 2)};
+}
+
+// Row r of a sequence's n * G rows: the tensors' row and the query head.
+__device__ __forceinline__ int64_t row_of(const Heads& x, int32_t token, int32_t head, int32_t r, int G) {
+  return (int64_t)(token + r / G) * x.ld_t + (int64_t)(head * G + r % G) * x.ld_h;
+}
+__device__ __forceinline__ void put2(const AttentionArgs& a, int64_t at, float x, float y) {
+  if (a.out_f32)
+    put_at(static_cast<float*>(a.out.p) + at, make_float2(x, y), a.out.p, a.out.bytes);
+  else
+    put_at(static_cast<uint16_t*>(a.out.p) + at, bf16x2(x, y), a.out.p, a.out.bytes);
+}
+// What a numerator is multiplied by, one after the other (their product may leave
+// fp32 where the result does not): 1 / sum out of the weights' units, and
+// the values' scale. No token: 0.
+__device__ __forceinline__ float2 last_factors(float lift, float sum) {
+  float e;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(lift));
+  return sum == 0.0f ? make_float2(0.0f, 0.0f) : make_float2((1.0f / sum) * 0x1p-15f, e);
+}
+__device__ __forceinline__ float finite_or_0(float m) { return m == -INFINITY ? 0.0f : m; }
+// Maxima and sum of row r over `count` parts; part i has its rows' maxima at
+// p[at(i)], lifts and sums `rows` and 2 `rows` behind them.
+struct Joined {
+  float m, lift, sum;
+};
+template <typename F>
+__device__ __forceinline__ Joined joined(const float* p, int r, int count, F at, int rows) {
+  Joined j = {-INFINITY, -INFINITY, 0.0f};
+  for (int i = 0; i < count; ++i) j.m = fmaxf(j.m, p[at(i) + r]);
+  const float m = finite_or_0(j.m);
+  for (int i = 0; i < count; ++i) {
+    const float down = p[at(i) + r] - m;
+    j.lift = fmaxf(j.lift, down + p[at(i) + rows + r]);
+    j.sum += p[at(i) + 2 * rows + r] * ex2(down);
+  }
+  return j;
+}
+__device__ __forceinline__ void put_lse(const AttentionArgs& a, int32_t token, int32_t head, int32_t r, int G, float m,
+                                        float sum) {
+  const int64_t at = (int64_t)(token + r / G) * a.q_heads + head * G + r % G;
+  put_at(a.lse + at, sum == 0.0f ? -INFINITY : (m + lg2(sum)) * 0.693147180559945f, a.lse, a.lse_bytes);
+}
+
+template <int D, int NT, bool kExact>
+__global__ void __launch_bounds__(kThreads, 1)
+    cache_attention_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ AttentionArgs a) {
+  using S = Attn<D, NT>;
+  constexpr int kRows = S::kRows, kSegs = D / 16, kSlots = S::kSlots;
+  extern __shared__ uint8_t raw[];
+  uint8_t* base = raw + ((1024u - (ptx::smem_u32(raw) & 1023u)) & 1023u);
+  float4* parts = reinterpret_cast<float4*>(base + kSlots * S::kSlot);  // [4][kSegs * NT * 32]
+  float* stats = reinterpret_cast<float*>(base + kSlots * S::kSlot + 4 * S::kPart);  // [kWarps][3][kRows]
+  AttnCtl* ctl = reinterpret_cast<AttnCtl*>(base + kSlots * S::kSlot + S::kFixed - 1024);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.q_heads / a.c.heads;
+  const uint32_t ring = ptx::smem_u32(base), full = ptx::smem_u32(ctl->full), empty = ptx::smem_u32(ctl->empty);
+
+  ptx::launch_dependents();
+  if (threadIdx.x < kSlots) {
+    ptx::mbar_init(full + 8 * threadIdx.x, 1);
+    ptx::mbar_init(empty + 8 * threadIdx.x, 1);
+  }
+  if (threadIdx.x == 0) {
+    ctl->abort = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tensormap(&map);
+  }
+  find_start<kRows>(a, ctl, reinterpret_cast<int64_t*>(stats));
+  const int64_t all = ctl->units, ctas = min((int64_t)gridDim.x, all);
+  if (blockIdx.x >= ctas) {
+    if (a.ws && threadIdx.x == 0) reinterpret_cast<Split*>(a.ws)[blockIdx.x].parts = 0;
+    return;
+  }
+  const int64_t begin = all * blockIdx.x / ctas, end = all * (blockIdx.x + 1) / ctas;
+  Walk<kRows> w;
+  w.sequence(a, ctl->first);
+  w.place(a, begin - ctl->at);
+
+  if (warp == kWarps) {
+    // ------------------------------------------------------------ fetching ---
+    // Lane i < 16 looks up 16 tokens of the next unit: their page and its scales.
+    const int shift = 31 - __clz(a.c.page_tokens);
+    struct Look {
+      int32_t block, half;  // block of the keys (-1: none to load), place in the page
+      uint32_t scales;      // keys | values << 8
+      int32_t chunks;
+    };
+    auto look = [&]() {
+      Look l{-1, 0, 0xFFFFu, w.chunks()};
+      const int32_t j = w.lo + w.unit * kUnit + 16 * lane;
+      if (lane < 2 * kWarps && j < w.hi) {
+        const int32_t page = page_of(a.c, w.b, j >> shift);
+        if (page >= 0) {
+          const int64_t block = (int64_t)page * 2 * a.c.heads + w.head;
+          l.block = (int32_t)block;
+          l.half = (j & (a.c.page_tokens - 1)) >> 4;
+          l.scales = __ldg(a.c.scales + block) | (uint32_t)__ldg(a.c.scales + block + a.c.heads) << 8;
+        }
+      }
+      return l;
+    };
+    const bool small = a.c.page_tokens == 16;  // each half its own page and its own copies
+    int64_t j = 0;
+    bool go = true;
+    Look l = look();
+    for (int64_t u = begin; u < end && go; ++u) {
+      const Look now = l;
+      if (u + 1 < end) {
+        w.next(a);
+        l = look();
+      }
+      for (int c = 0; c < now.chunks; ++c, ++j) {
+        const int slot = (int)(j % kSlots);
+        if (j >= kSlots && !(go = wait_bar_warp(empty + 8 * slot, (uint32_t)(j / kSlots - 1) & 1, &ctl->abort))) break;
+        const int32_t b0 = __shfl_sync(0xffffffffu, now.block, 2 * c), b1 = __shfl_sync(0xffffffffu, now.block, 2 * c + 1);
+        const int32_t half = __shfl_sync(0xffffffffu, now.half, 2 * c);
+        const uint32_t s0 = __shfl_sync(0xffffffffu, now.scales, 2 * c), s1 = __shfl_sync(0xffffffffu, now.scales, 2 * c + 1);
+        if (lane == 0) {
+          const uint32_t bar = full + 8 * slot, k = ring + slot * S::kSlot, v = k + 2 * S::kHalf;
+          ctl->meta[slot] = (s0 & 0xFFu) | (s1 & 0xFFu) << 8 | (s0 & 0xFF00u) << 8 | (s1 & 0xFF00u) << 16;
+          if (small) {
+            ptx::mbar_arrive_expect_tx(bar, (b0 >= 0 ? 2 * S::kHalf : 0) + (b1 >= 0 ? 2 * S::kHalf : 0));
+            if (b0 >= 0) {
+              tma_pages(k, &map, 0, b0, bar);
+              tma_pages(v, &map, 0, b0 + a.c.heads, bar);
+            }
+            if (b1 >= 0) {
+              tma_pages(k + S::kHalf, &map, 0, b1, bar);
+              tma_pages(v + S::kHalf, &map, 0, b1 + a.c.heads, bar);
+            }
+          } else {
+            ptx::mbar_arrive_expect_tx(bar, b0 >= 0 ? 4 * S::kHalf : 0);
+            if (b0 >= 0) {
+              tma_pages(k, &map, half, b0, bar);
+              tma_pages(v, &map, half, b0 + a.c.heads, bar);
+            }
           }
         }
-        z = dot * (scale_value(c.scales[kb]) * a.scale);
-        if (a.softcap > 0.0f) z = a.softcap * tanhf(z / a.softcap);
-        z += slope * (float)(j - p);
+        __syncwarp();
       }
     }
-    float top = z;
-    for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
-    const float now = fmaxf(m, top), keep = m == now ? 1.0f : expf(m - now);
-    const float e = j <= p ? expf(z - now) : 0.0f;
-    float es = e;
-    for (int i = 16; i; i >>= 1) es += __shfl_xor_sync(0xffffffffu, es, i);
-    sum = sum * keep + es;
-    m = now;
+    if (!go) {
+      // the last load into each slot lands (bounded wait) before the CTA's memory goes
+      const uint64_t t0 = ptx::globaltimer_ns();
+      for (int64_t i = j > kSlots ? j - kSlots : 0; i < j; ++i)
+        while (!ptx::mbar_try_wait(full + 8 * (uint32_t)(i % kSlots), (uint32_t)(i / kSlots) & 1) &&
+               ptx::globaltimer_ns() - t0 < kWaitLimitNs / 10) {
+        }
+    }
+    return;
+  }
+
+  // ----------------------------------------------------------- multiplying ---
+  const int g = lane >> 2, t = lane & 3;
+  // ldmatrix rows: matrix lane / 8 holds tokens 8 (m % 2) .. of half m / 2
+  const int mrow = ((lane >> 3) & 1) * 8 + (lane & 7);
+  const uint32_t swz = S::kBox == 128 ? mrow & 7 : S::kBox == 64 ? (mrow >> 1) & 3 : (mrow >> 2) & 1;
+  const uint32_t lane_at = (lane >> 4) * S::kHalf + mrow * S::kBox + (swz << 4);
+  const float scale2 = a.scale * 1.44269504088896f;
+
+  uint32_t qf[kSegs][NT][2];
+  float o[kSegs][NT][4], m[NT][2], lift[NT][2], sum[NT][2], slope[NT][2];
+  int32_t qe[NT][2], pos[NT][2];
+  int64_t j0 = 0;
+  bool go = true;
+
+  for (int64_t u = begin; u < end; ++u) {
+    if (u == begin || w.unit == 0) {
+      // queries of this tile, row by row times a power of two: the largest in [2^14, 2^15)
+      const int32_t rows = w.n * G - w.row0;
 #pragma unroll
-    for (int i = 0; i < kChannels; ++i) o[i] *= keep;
-    const int count = min(32, p - j0 + 1);
-    for (int i = 0; i < count; ++i) {
-      const float w = __shfl_sync(0xffffffffu, e * vs, i);
-      const uint8_t* row = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, (unsigned long long)vrow, i));
+      for (int nt = 0; nt < NT; ++nt) {
+        const int32_t r = 8 * nt + g;
+        uint2 x[kSegs];
+        uint32_t top = 0;
+        if (r < rows) {
+          const uint16_t* q = static_cast<const uint16_t*>(a.q.p) + row_of(a.q, w.row, w.head, w.row0 + r, G) + 4 * t;
 #pragma unroll
-      for (int ch = 0; ch < kChannels; ++ch) {
-        const float x = row ? f16x2_f32(e4m3x2_f16x2(row[lane + 32 * ch])).x : __uint_as_float(0x7FC00000u);
-        o[ch] = fmaf(w, x, o[ch]);
+          for (int s = 0; s < kSegs; ++s) x[s] = __ldg(reinterpret_cast<const uint2*>(q + 16 * s));
+        } else {
+#pragma unroll
+          for (int s = 0; s < kSegs; ++s) x[s] = make_uint2(0u, 0u);
+        }
+#pragma unroll
+        for (int s = 0; s < kSegs; ++s)
+          top = max(max(top, max((x[s].x << 16) & 0x7FFFFFFFu, x[s].x & 0x7FFF0000u)),
+                    max((x[s].y << 16) & 0x7FFFFFFFu, x[s].y & 0x7FFF0000u));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = max((int)(top >> 23), 1);  // value = f16 * 2^(e - 141)
+        const float f1 = pow2i(min(141 - e, 126)), f2 = pow2i(max(141 - e - 126, 0));
+#pragma unroll
+        for (int s = 0; s < kSegs; ++s) {
+          const float2 lo = unpack2(x[s].x), hi = unpack2(x[s].y);
+          qf[s][nt][0] = e == 255 ? 0u : f16x2(lo.x * f1 * f2, lo.y * f1 * f2);
+          qf[s][nt][1] = e == 255 ? 0u : f16x2(hi.x * f1 * f2, hi.y * f1 * f2);
+        }
+        const int32_t ex = e == 255 ? 1 << 20 : e - 141;
+        qe[nt][0] = __shfl_sync(0xffffffffu, ex, 8 * t);
+        qe[nt][1] = __shfl_sync(0xffffffffu, ex, 8 * t + 4);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int32_t c = min(w.row0 + 8 * nt + 2 * t + i, w.n * G - 1);
+          pos[nt][i] = w.len - w.n + c / G;
+          slope[nt][i] = a.slopes ? __ldg(a.slopes + w.head * G + c % G) * 1.44269504088896f : 0.0f;
+          m[nt][i] = lift[nt][i] = -INFINITY;
+          sum[nt][i] = 0.0f;
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < kSegs; ++s)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[s][nt][i] = 0.0f;
+    }
+
+    const int32_t chunks = w.chunks();
+    if (warp < chunks && go) {
+      const int64_t j = j0 + warp;
+      const int slot = (int)(j % kSlots);
+      const int32_t c0 = w.lo + w.unit * kUnit + warp * kChunk;
+      go = wait_bar_warp(full + 8 * slot, (uint32_t)(j / kSlots) & 1, &ctl->abort);
+      if (go) {
+        const uint32_t meta = ctl->meta[slot];
+        const uint32_t kat = ring + slot * S::kSlot + lane_at, vat = kat + 2 * S::kHalf;
+        float s[2][NT][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[h][nt][i] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kSegs; ++i) {
+          constexpr int kIn = S::kBox / 16;
+          uint32_t r[4];
+          ldsm((kat ^ ((i % kIn) << 4)) + (i / kIn) * 16 * S::kBox, r);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t a0 = e4m3x2_f16x2(r[2 * h]), a2 = e4m3x2_f16x2(r[2 * h] >> 16);
+            const uint32_t a1 = e4m3x2_f16x2(r[2 * h + 1]), a3 = e4m3x2_f16x2(r[2 * h + 1] >> 16);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma(s[h][nt], a0, a1, a2, a3, qf[i][nt][0], qf[i][nt][1]);
+          }
+        }
+
+        // scores in log2 units; -infinity where a row does not attend
+        const bool whole = c0 + kChunk <= w.p0 + 1 && (a.window == 0 || c0 > w.hi - 1 - a.window);
+        float ev[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int ks = (int)((meta >> (8 * h)) & 0xFFu);
+          const uint32_t vs = (meta >> (16 + 8 * h)) & 0xFFu;
+          ev[h] = vs == 255u ? __uint_as_float(0x7FC00000u) : (float)((int)vs - 127);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const bool bad = ks == 255 || qe[nt][i] == 1 << 20;
+              float f = bad ? __uint_as_float(0x7FC00000u) : pow2i(ks - 127 + qe[nt][i]);
+              if (a.softcap > 0.0f) {
+                f *= a.scale / a.softcap;
+#pragma unroll
+                for (int z = i; z < 4; z += 2) s[h][nt][z] = a.softcap * 1.44269504088896f * tanhf(s[h][nt][z] * f);
+              } else {
+                f *= scale2;
+                s[h][nt][i] *= f;
+                s[h][nt][i + 2] *= f;
+              }
+              const int32_t j1 = c0 + 16 * h + g - pos[nt][i];  // token's position less the row's
+              if (a.slopes) {
+                s[h][nt][i] += slope[nt][i] * (float)j1;
+                s[h][nt][i + 2] += slope[nt][i] * (float)(j1 + 8);
+              }
+              if (!whole) {
+                const int32_t most = a.window > 0 ? a.window : 0x7FFFFFFF;
+                if (j1 > 0 || j1 <= -most) s[h][nt][i] = -INFINITY;
+                if (j1 + 8 > 0 || j1 + 8 <= -most) s[h][nt][i + 2] = -INFINITY;
+              }
+            }
+          }
+        }
+        if (c0 + kChunk > w.hi) {
+          // tokens behind the last: whatever lies there must not meet a weight of zero
+          const int first = w.hi - c0;
+          for (int i = lane; i < (kChunk - first) * kSegs; i += 32) {
+            const int r = first + i / kSegs, seg = i % kSegs;
+            constexpr int kIn = S::kBox / 16;
+            const uint32_t at = ring + slot * S::kSlot + 2 * S::kHalf + (r >> 4) * S::kHalf + (seg / kIn) * 16 * S::kBox +
+                                (r & 15) * S::kBox + (seg % kIn) * 16;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+          }
+          ptx::fence_proxy_async();
+          __syncwarp();
+        }
+
+        // running maxima, and the weights
+        const bool one = ((meta >> 16) & 0xFFu) == meta >> 24;  // both halves' values under one scale
+        uint32_t pf[2][NT][2], pl[2][NT][2];
+        bool moved = false;
+        float keep[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float cm[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float h0 = fmaxf(s[0][nt][i], s[0][nt][i + 2]), h1 = fmaxf(s[1][nt][i], s[1][nt][i + 2]);
+            float x = fmaxf(h0, h1);
+#pragma unroll
+            for (int z = 4; z < 32; z <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, z));
+            const float mn = fmaxf(m[nt][i], x);
+            cm[i] = finite_or_0(mn);
+            float y = x - cm[i] + ev[0];
+            if (!one) {
+              y = fmaxf(h0 - cm[i] + ev[0], h1 - cm[i] + ev[1]);
+#pragma unroll
+              for (int z = 4; z < 32; z <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, z));
+            }
+            const float down = m[nt][i] - cm[i], was = down + lift[nt][i], now = fmaxf(was, y);
+            sum[nt][i] *= ex2(down);
+            keep[nt][i] = ex2(was - finite_or_0(now));
+            moved |= was != now;
+            m[nt][i] = mn;
+            lift[nt][i] = now;
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float c[2] = {ev[h] + kTop - finite_or_0(lift[nt][0]), ev[h] + kTop - finite_or_0(lift[nt][1])};
+            float p[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              const float x = s[h][nt][z] - cm[z & 1];
+              sum[nt][z & 1] += ex2(x);
+              p[z] = x == -INFINITY ? 0.0f : ex2(x + c[z & 1]);
+            }
+            const uint32_t u0 = f16x2(p[0], p[1]), u1 = f16x2(p[2], p[3]);
+            pf[h][nt][0] = transposed(u0);
+            pf[h][nt][1] = transposed(u1);
+            if (kExact) {
+              const float2 q0 = f16x2_f32(u0), q1 = f16x2_f32(u1);
+              pl[h][nt][0] = transposed(f16x2(p[0] - q0.x, p[1] - q0.y));
+              pl[h][nt][1] = transposed(f16x2(p[2] - q1.x, p[3] - q1.y));
+            }
+          }
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+          for (int i = 0; i < kSegs; ++i)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int z = 0; z < 4; ++z) o[i][nt][z] *= keep[nt][z & 1];
+        }
+#pragma unroll
+        for (int i = 0; i < kSegs; ++i) {
+          constexpr int kIn = S::kBox / 16;
+          uint32_t r[4];
+          ldsm_t((vat ^ ((i % kIn) << 4)) + (i / kIn) * 16 * S::kBox, r);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            // two tokens of a channel side by side, the even channel below
+            const uint32_t x = __byte_perm(r[2 * h], 0, 0x3120), y = __byte_perm(r[2 * h + 1], 0, 0x3120);
+            const uint32_t a0 = e4m3x2_f16x2(x), a1 = e4m3x2_f16x2(x >> 16), a2 = e4m3x2_f16x2(y), a3 = e4m3x2_f16x2(y >> 16);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma(o[i][nt], a0, a1, a2, a3, pf[h][nt][0], pf[h][nt][1]);
+              if (kExact) mma(o[i][nt], a0, a1, a2, a3, pl[h][nt][0], pl[h][nt][1]);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(empty + 8 * slot);
       }
     }
-  }
-  const int64_t at = t * a.out.ld_t + hq * a.out.ld_h;
+    j0 += chunks;
+
+    if (w.unit == w.units - 1 || u == end - 1) {
+      // the eight warps' sums become one
 #pragma unroll
-  for (int ch = 0; ch < kChannels; ++ch) {
-    const float y = p < 0 ? 0.0f : o[ch] / sum;
-    if (a.out_f32)
-      put_at(static_cast<float*>(a.out.p) + at + lane + 32 * ch, y, a.out.p, a.out.bytes);
-    else
-      put_at(static_cast<uint16_t*>(a.out.p) + at + lane + 32 * ch, (uint16_t)bf16x2(y, 0.0f), a.out.p, a.out.bytes);
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int z = 4; z < 32; z <<= 1) sum[nt][i] += __shfl_xor_sync(0xffffffffu, sum[nt][i], z);
+          if (g == 0) {
+            float* st = stats + warp * 3 * kRows + 8 * nt + 2 * t + i;
+            st[0] = m[nt][i];
+            st[kRows] = lift[nt][i];
+            st[2 * kRows] = sum[nt][i];
+          }
+        }
+      warps_sync();
+      float f[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const Joined x = joined(stats, 8 * nt + 2 * t + i, kWarps, [](int z) { return z * 3 * kRows; }, kRows);
+          f[nt][i] = ex2(m[nt][i] - finite_or_0(x.m) + lift[nt][i] - finite_or_0(x.lift));
+        }
+#pragma unroll
+      for (int round = 0; round < 2; ++round) {
+        if ((warp >= 4) == (round == 0)) {
+          float4* to = parts + (warp & 3) * kSegs * NT * 32 + lane;
+#pragma unroll
+          for (int i = 0; i < kSegs; ++i)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float4 x = make_float4(o[i][nt][0] * f[nt][0], o[i][nt][1] * f[nt][1], o[i][nt][2] * f[nt][0],
+                                     o[i][nt][3] * f[nt][1]);
+              float4* at = to + (i * NT + nt) * 32;
+              if (round) {
+                const float4 y = *at;
+                x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+              }
+              *at = x;
+            }
+        }
+        warps_sync();
+      }
+      const bool whole = w.unit == w.units - 1 && u - w.unit >= begin;
+      const int part = u - w.unit < begin ? 0 : 1;  // began before this CTA, or goes on behind it
+      float* ws = a.ws + gridDim.x * (sizeof(Split) / 4) + (2 * (int64_t)blockIdx.x + part) * part_floats(kRows, D);
+      const int32_t rows = min(w.n * G - w.row0, kRows);
+      for (int e = threadIdx.x; e < kSegs * NT * 32; e += kWarps * 32) {
+        float4 x = parts[e];
+#pragma unroll
+        for (int z = 1; z < 4; ++z) {
+          const float4 y = parts[z * kSegs * NT * 32 + e];
+          x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+        }
+        if (!whole) {
+          put_at(ws + 3 * kRows + 4 * (int64_t)e, x, a.ws, a.ws_bytes);
+          continue;
+        }
+        const Quad qd = quad<NT>(e);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = qd.row + i;
+          if (r >= rows) break;
+          const Joined y = joined(stats, r, kWarps, [](int z) { return z * 3 * kRows; }, kRows);
+          const float2 k = last_factors(y.lift, y.sum);
+          put2(a, row_of(a.out, w.row, w.head, w.row0 + r, G) + qd.d, (i ? x.y : x.x) * k.x * k.y,
+               (i ? x.w : x.z) * k.x * k.y);
+          if (a.lse && qd.d == 0) put_lse(a, w.row, w.head, w.row0 + r, G, y.m, y.sum);
+        }
+      }
+      if (!whole && threadIdx.x < kRows) {
+        const int r = threadIdx.x;
+        const Joined y = joined(stats, r, kWarps, [](int z) { return z * 3 * kRows; }, kRows);
+        put_at(ws + r, y.m, a.ws, a.ws_bytes);
+        put_at(ws + kRows + r, y.lift, a.ws, a.ws_bytes);
+        put_at(ws + 2 * kRows + r, y.sum, a.ws, a.ws_bytes);
+      }
+      if (u == end - 1 && a.ws && threadIdx.x == 0) {
+        // the CTA of the tile's last unit: the largest c with all c / ctas <= it
+        const int64_t last = u - w.unit + w.units - 1;
+        const int32_t to = (int32_t)(((last + 1) * ctas - 1) / all);
+        const Split sp = {w.row, w.row0, rows, w.head, !whole && part == 1 ? to - (int32_t)blockIdx.x + 1 : 0, {0, 0, 0}};
+        put_at(reinterpret_cast<Split*>(a.ws) + blockIdx.x, sp, a.ws, a.ws_bytes);
+      }
+      warps_sync();
+    }
+    if (u + 1 < end) w.next(a);
   }
-  if (a.lse && lane == 0)
-    put_at(a.lse + (int64_t)t * a.q_heads + hq, p < 0 ? -INFINITY : m + logf(sum), a.lse, a.lse_bytes);
+}
+
+// Joins the parts of the tile that goes on behind CTA blockIdx.x.
+template <int D, int NT>
+__global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__ AttentionArgs a, int ctas) {
+  constexpr int kRows = 8 * NT;
+  ptx::wait_prior_grid();
+  const Split sp = reinterpret_cast<const Split*>(a.ws)[blockIdx.x];
+  if (sp.parts == 0) return;
+  __shared__ float2 factor[kRows];
+  const int G = a.q_heads / a.c.heads;
+  // part 0 is this CTA's second, the others the first of the CTAs behind it
+  auto part = [&](int i) {
+    return a.ws + ctas * (int64_t)(sizeof(Split) / 4) + (2 * (int64_t)(blockIdx.x + i) + (i == 0)) * part_floats(kRows, D);
+  };
+  __shared__ float top[kRows], lift[kRows];
+  if (threadIdx.x < kRows) {
+    const int r = threadIdx.x;
+    const Joined x = joined(a.ws, r, sp.parts, [&](int i) { return part(i) - a.ws; }, kRows);
+    factor[r] = last_factors(x.lift, x.sum);
+    top[r] = finite_or_0(x.m);
+    lift[r] = finite_or_0(x.lift);
+    if (a.lse && r < sp.rows) put_lse(a, sp.token, sp.head, sp.row0 + r, G, x.m, x.sum);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < D / 16 * NT * 32; e += 256) {
+    const Quad qd = quad<NT>(e);
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int i = 0; i < sp.parts; ++i) {
+      const float* p = part(i);
+      const float4 y = *reinterpret_cast<const float4*>(p + 3 * kRows + 4 * (int64_t)e);
+      const float f0 = ex2(p[qd.row] - top[qd.row] + p[kRows + qd.row] - lift[qd.row]);
+      const float f1 = ex2(p[qd.row + 1] - top[qd.row + 1] + p[kRows + qd.row + 1] - lift[qd.row + 1]);
+      x = make_float4(fmaf(y.x, f0, x.x), fmaf(y.y, f1, x.y), fmaf(y.z, f0, x.z), fmaf(y.w, f1, x.w));
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = qd.row + i;
+      if (r < sp.rows)
+        put2(a, row_of(a.out, sp.token, sp.head, sp.row0 + r, G) + qd.d, (i ? x.y : x.x) * factor[r].x * factor[r].y,
+             (i ? x.w : x.z) * factor[r].x * factor[r].y);
+    }
+  }
 }
 
 }  // namespace
@@ -347,20 +1003,101 @@ cudaError_t launch_cache_read(const CacheArgs& c, const Heads& k, const Heads& v
   return cudaGetLastError();
 }
 
-int64_t cache_attention_workspace_bytes(const AttentionArgs&) { return 0; }
+namespace {
+// How a call is cut: query rows of a tile, CTAs, and whether a tile may be split.
+struct AttnShape {
+  int nt, ctas;
+  bool split;
+};
+// Sixteen rows to a tile where a sequence has more than eight on average (their
+// products come at half the loads); heads above 128 channels keep to eight, whose
+// sums fill the registers.
+AttnShape attn_shape(const AttentionArgs& a) {
+  const int64_t G = a.q_heads / a.c.heads, rows = a.c.tokens * G;
+  AttnShape s;
+  s.nt = a.c.head_dim <= 128 && rows > 8 * (int64_t)a.c.sequences ? 2 : 1;
+  const int64_t kRows = 8 * s.nt, tiles = rows / kRows + a.c.sequences, most = (int64_t)a.c.max_pages * a.c.page_tokens + 1;
+  const int64_t span = a.window > 0 && a.window + (kRows + G - 2) / G + 1 + kChunk < most
+                           ? a.window + (kRows + G - 2) / G + 1 + kChunk : most;
+  const int64_t units = (span + kUnit - 1) / kUnit, all = tiles * a.c.heads * units;
+  s.ctas = (int)(all < kSms ? all : kSms);
+  s.split = units > 1;
+  return s;
+}
+
+// The pages' codes as [blocks, page_tokens / 16, head_dim / box, 16, box] bytes: a box of 16 (or two of them) tokens
+// lies in shared memory as slabs of `box` bytes a token, swizzled.
+// (A cache without pages, whose pages are never looked at, borrows an address.)
+bool pages_map(CUtensorMap* m, const CacheArgs& c, const void* any, int box) {
+  auto fn = tma_encode_fn();
+  if (!fn) return false;
+  ensure_context();
+  const uint64_t D = c.head_dim, P = c.page_tokens;
+  const cuuint64_t dims[5] = {(cuuint64_t)box, 16, D / box, P / 16, (cuuint64_t)(c.pages ? c.pages : 1) * 2 * c.heads};
+  const cuuint64_t strides[4] = {D, (cuuint64_t)box, 16 * D, P * D};
+  const cuuint32_t boxes[5] = {(cuuint32_t)box, 16, (cuuint32_t)(D / box), P > 16 ? 2u : 1u, 1};
+  const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, c.pages ? c.codes : const_cast<void*>(any), dims, strides, boxes, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            box == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : box == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int NT, bool kExact>
+cudaError_t attend(const AttentionArgs& a, const AttnShape& sh, cudaStream_t st) {
+  using S = Attn<D, NT>;
+  static bool set[kMaxDevices] = {};
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!set[dev]) {
+      e = cudaFuncSetAttribute(cache_attention_kernel<D, NT, kExact>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+      if (e != cudaSuccess) return e;
+      set[dev] = true;
+    }
+  }
+  CUtensorMap map;
+  if (!pages_map(&map, a.c, a.q.p, S::kBox)) return cudaErrorInvalidValue;
+  cache_attention_kernel<D, NT, kExact><<<sh.ctas, kThreads, S::kBytes, st>>>(map, a);
+  if ((e = cudaGetLastError()) != cudaSuccess || !sh.split) return e;
+  // launched while the kernel before it drains; it waits for that kernel's parts itself
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)sh.ctas);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_join_kernel<D, NT>, a, sh.ctas);
+}
+template <int D, int NT>
+cudaError_t attend(const AttentionArgs& a, const AttnShape& sh, cudaStream_t st) {
+  return a.out_f32 ? attend<D, NT, true>(a, sh, st) : attend<D, NT, false>(a, sh, st);
+}
+}  // namespace
+
+int64_t cache_attention_workspace_bytes(const AttentionArgs& a) {
+  const AttnShape s = attn_shape(a);
+  if (!s.split) return 0;
+  return s.ctas * ((int64_t)sizeof(Split) + 8 * part_floats(8 * s.nt, a.c.head_dim));
+}
 
 cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t st) {
-  if (a.c.tokens == 0 || a.c.sequences == 0 || a.q_heads == 0) return cudaSuccess;
+  if (a.c.tokens == 0 || a.c.sequences == 0) return cudaSuccess;
   (void)cudaGetLastError();
-  const dim3 grid((unsigned)a.c.tokens, (unsigned)a.q_heads);
+  const AttnShape sh = attn_shape(a);
   switch (a.c.head_dim) {
-    case 64: cache_attention_kernel<64><<<grid, 32, 0, st>>>(a); break;
-    case 96: cache_attention_kernel<96><<<grid, 32, 0, st>>>(a); break;
-    case 128: cache_attention_kernel<128><<<grid, 32, 0, st>>>(a); break;
-    case 192: cache_attention_kernel<192><<<grid, 32, 0, st>>>(a); break;
-    default: cache_attention_kernel<256><<<grid, 32, 0, st>>>(a); break;
+    case 64: return sh.nt == 2 ? attend<64, 2>(a, sh, st) : attend<64, 1>(a, sh, st);
+    case 96: return sh.nt == 2 ? attend<96, 2>(a, sh, st) : attend<96, 1>(a, sh, st);
+    case 128: return sh.nt == 2 ? attend<128, 2>(a, sh, st) : attend<128, 1>(a, sh, st);
+    case 192: return attend<192, 1>(a, sh, st);
+    default: return attend<256, 1>(a, sh, st);
   }
-  return cudaGetLastError();
 }
 
 cudaError_t read_cache_error(uint32_t* err) {

@@ -81,7 +81,7 @@ def test_refusals_of_one_call(L):
 
 @pytest.mark.parametrize("status,kw", [
     (1, dict(lens=None)), (2, dict(starts=None)), (1, dict(params=False)), (2, dict(q_heads=0)), (2, dict(q_heads=3)),
-    (2, dict(q_heads=65536)), (1, dict(q=None)), (1, dict(out=None)), (1, dict(qd=1)), (1, dict(od=2)),
+    (2, dict(q_heads=65536)), (2, dict(q_heads=1024, tokens=1 << 21)), (1, dict(q=None)), (1, dict(out=None)), (1, dict(qd=1)), (1, dict(od=2)),
     (1, dict(scale=float("nan"))), (1, dict(scale=float("inf"))), (1, dict(softcap=-1.0)), (1, dict(softcap=float("nan"))),
     (1, dict(softcap=float("inf"))), (1, dict(window=-1)), (3, dict(slopes=OFF)), (3, dict(lse=OFF)), (3, dict(ws=OFF8)),
     (2, dict(qh=32)), (2, dict(qt=-8)), (3, dict(qt=260)), (3, dict(q=OFF8)), (2, dict(ot=128)), (2, dict(ot=0)),
