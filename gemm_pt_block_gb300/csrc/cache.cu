@@ -239,54 +239,69 @@ __global__ void __launch_bounds__(1024) cache_read_kernel(CacheArgs c, Heads k, 
 // denominator and m + lift, lift = max (s_j - m + ev_j), for the numerator, whose
 // weights are then at most one whatever the pages' scales are.
 //
-// One CTA an SM takes an equal run of units: 256 tokens of one sequence, head of
-// the cache and tile of query rows (the rows of the query heads that share the
-// head, of all its new tokens). One warp fetches 32 tokens a time into a ring in
-// shared memory by TMA; eight warps take them in turn, each with its own maxima
-// and sums, so the loop has no barrier among them. Codes become f16 in registers
-// (exact), keys as the A operand of S^T = K Q^T, values, transposed as they are
-// read, as that of O^T = V^T P^T: query rows are the instruction's N of eight.
-// Eight warps' sums are joined when a tile's run ends; a tile that several CTAs
-// share leaves its parts in the workspace for cache_join_kernel.
+// The work is cut into units of 32 tokens of one sequence, one head of the cache
+// and one tile of query rows (the rows of the query heads that share the head,
+// over the sequence's new tokens), and every warp of the GPU takes an equal run of
+// them, whatever the lengths: eight warps of a CTA an SM that multiply, and a
+// ninth that fetches for them by TMA, keys and values apart, into a ring for each.
+// A warp holds maxima and sums of its tile by itself; nothing in its loop waits for
+// another. Codes become f16 in registers (exact), keys as the A operand of S^T = K
+// Q^T, values, transposed as they are read, as that of O^T = V^T P^T: query rows
+// are the instruction's N of eight. Tiles that several warps share are joined in
+// the CTA when its runs end; those that several CTAs share leave their parts in
+// the workspace for cache_join_kernel.
 
 constexpr int kSms = 152;
 constexpr int kWarps = 8;                       // that multiply
 constexpr int kThreads = (kWarps + 1) * 32;     // and one that fetches
-constexpr int kChunk = 32;                      // tokens of a warp at a time
-constexpr int kUnit = kWarps * kChunk;
+constexpr int kChunk = 32;                      // tokens of a unit
 constexpr float kTop = 15.0f;                   // weights are held times 2^15: f16 keeps 2^-39 of the largest
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr int kMostStages = 16;
 
 template <int D, int NT>
 struct Attn {
   static constexpr int kRows = 8 * NT;
   static constexpr int kBox = D % 128 == 0 ? 128 : D % 64 == 0 ? 64 : 32;  // bytes of a row in one swizzled slab
   static constexpr int kHalf = 16 * D;                                     // 16 tokens of keys or values
-  static constexpr int kSlot = 4 * kHalf;                                  // 32 tokens of keys, then of values
-  static constexpr int kPart = kRows * D * 4;                              // a warp's sums
-  static constexpr int kFixed = 4 * kPart + kWarps * kRows * 12 + 1024;    // (below)
-  static constexpr int kFit = (227 * 1024 - 1024 - kFixed) / kSlot;
-  static constexpr int kSlots = kFit < 32 ? kFit : 32;
-  static constexpr int kBytes = 1024 + kSlots * kSlot + kFixed;
+  static constexpr int kStage = 2 * kHalf;                                 // 32 tokens of keys or values
+  static constexpr int kQuads = D / 16 * NT * 32;                          // of a tile's sums (below)
+  static constexpr int kFixed = 2 * kWarps * 3 * kRows * 4 + kWarps * kRows * 4 + 4096;
+  static constexpr int kFit = (227 * 1024 - 1024 - kFixed) / (kWarps * kStage);
+  static constexpr int kStages = kFit < kMostStages ? kFit : kMostStages;  // of a warp's ring
+  static constexpr int kBytes = 1024 + kWarps * kStages * kStage + kFixed;
+  static_assert(kStages >= 3 && kQuads * 16 <= kStages * kStage, "ring");
+};
+
+// A tile: rows row0 .. row0 + rows - 1 of a sequence's (first token `token`), of one head.
+struct Tile {
+  int32_t token, row0, rows, head;
 };
 
 struct AttnCtl {
-  uint64_t full[32], empty[32];
-  uint32_t meta[32];  // scales of a slot's halves: keys 0, keys 1, values 0, values 1
-  int64_t at;         // units before the first sequence of this CTA
-  int64_t units;      // of all sequences
-  int32_t first;      // that sequence
+  uint64_t full[kWarps][kMostStages], empty[kWarps][kMostStages];
+  uint16_t scales[kWarps][kMostStages];  // of a stage's halves
+  Tile head[kWarps], open[kWarps];       // tiles that a warp shares with the one before it, and behind it
+  int64_t at[kWarps];                    // units before the first sequence of a warp's run
+  int64_t units;                         // of all sequences
+  int32_t first[kWarps];                 // that sequence
+  int32_t left[kWarps];                  // units of the open tile behind a warp's run
+  uint8_t has[kWarps];                   // kHead, kOpen, kBegan
   uint32_t abort;
 };
-static_assert(sizeof(AttnCtl) <= 1024, "control block");
+static_assert(sizeof(AttnCtl) <= 4096, "control block");
+// A warp's run ended a tile that began before it; it ends inside a tile; that tile began before it.
+enum : uint8_t { kHead = 1, kOpen = 2, kBegan = 4 };
 
-// A split tile's rows, for the join: n_rows of its sequence's rows from row0 on.
+// A tile that goes on behind a CTA, for the join: over so many CTAs (0: none does).
 struct Split {
-  int32_t token, row0, rows, head, parts, unused[3];
+  Tile tile;
+  int32_t parts, unused[3];
 };
 
 // Floats of the workspace: a Split for each CTA, then two parts each (a tile
-// that began before it, a tile that goes on behind it): maxima, sums, numerators.
+// that began before it, a tile that goes on behind it): maxima, lifts, sums and
+// numerators; then the numerators of each warp's first tile.
 __host__ __device__ constexpr int64_t part_floats(int rows, int D) { return (int64_t)rows * D + 3 * rows; }
 
 // Bounded wait (about 2 s); the whole warp goes on or leaves together.
@@ -304,6 +319,24 @@ __device__ __forceinline__ bool wait_bar_warp(uint32_t bar, uint32_t parity, uin
     }
   }
   return __all_sync(0xffffffffu, ok);
+}
+
+// The same with a barrier for each lane that `need`s it.
+__device__ __forceinline__ bool wait_bars(uint32_t bar, uint32_t parity, bool need, uint32_t* abort) {
+  bool ok = !need || ptx::mbar_try_wait(bar, parity);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  for (;;) {
+    if (!ok) ok = ptx::mbar_try_wait_sleep(bar, parity, 10000u);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    bool out = *reinterpret_cast<volatile uint32_t*>(abort) != 0;
+    if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
+      *reinterpret_cast<volatile uint32_t*>(abort) = 1u;
+      atomicExch(&g_cache_error, 6u);  // MXFP4_ERR_TIMEOUT
+      out = true;
+    }
+    if (__any_sync(0xffffffffu, out)) return false;
+  }
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -352,24 +385,36 @@ __device__ __forceinline__ void warps_sync() { asm volatile("bar.sync 1, %0;" ::
 // 2^e for a whole e, 0 below the smallest normal number.
 __device__ __forceinline__ float pow2i(int e) { return e < -126 ? 0.0f : __uint_as_float((uint32_t)(min(e, 127) + 127) << 23); }
 
-// The place of a CTA in the order of all units: sequences, their heads, their
-// tiles of kRows query rows, units of 256 tokens. A sequence's tiles count alike
-// (the longest's units): those that a tile has no tokens for are passed over.
+// What a call says of one sequence, as it lies in memory.
+struct Said {
+  int32_t row, end, len;
+};
+__device__ __forceinline__ Said said(const CacheArgs& c, int32_t b) {
+  return Said{c.starts ? __ldg(c.starts + b) : b, c.starts ? __ldg(c.starts + b + 1) : b + 1, __ldg(c.lens + b)};
+}
+
+// A place in the order of all units: sequences, their heads, their tiles of
+// kRows query rows, 32 tokens at a time. A sequence's tiles count alike (the
+// longest's units): units that a tile has no tokens for are passed over.
 template <int kRows>
 struct Walk {
   int32_t b, n, row, len, tiles, units;  // sequence: rows, first row, length, tiles, units of each
   int32_t head, tile, unit;
   int32_t row0, p0, lo, hi;  // tile: first row, its position, tokens [lo, hi) that a row attends; lo rounded down
+  Said ahead;                // of sequence b + 1
 
-  // Sequence s; its number of units.
-  __device__ __forceinline__ int64_t sequence(const AttentionArgs& a, int32_t s) {
+  // Takes sequence s, of which the call says x; its number of units.
+  __device__ __forceinline__ int64_t take(const AttentionArgs& a, int32_t s, const Said& x) {
     const int G = a.q_heads / a.c.heads;
     b = s;
-    Seq q;
-    n = rows_of(a.c, s, &q) ? q.n : 0;
+    row = x.row;
+    n = x.end - x.row;
+    if (x.row < 0 || x.end < x.row || x.end > a.c.tokens) {
+      index_fail();
+      n = 0;
+    }
     if (n == 0) return 0;
-    row = q.row;
-    len = __ldg(a.c.lens + s);
+    len = x.len;
     const int32_t most = a.c.max_pages * a.c.page_tokens;
     if (len < 0 || len > most) {
       index_fail();
@@ -378,11 +423,13 @@ struct Walk {
     tiles = (n * G + kRows - 1) / kRows;
     const int32_t tokens = (kRows + G - 2) / G + 1;  // that a tile's rows may belong to
     const int32_t span = a.window > 0 ? min(len, a.window + tokens + kChunk) : len;
-    units = max(1, (span + kUnit - 1) / kUnit);
+    units = max(1, (span + kChunk - 1) / kChunk);
     return (int64_t)a.c.heads * tiles * units;
   }
-  // Unit u of the sequence.
-  __device__ __forceinline__ void place(const AttentionArgs& a, int64_t u) {
+  // Unit u of sequence s, where a run begins.
+  __device__ __forceinline__ void place(const AttentionArgs& a, int32_t s, int64_t u) {
+    take(a, s, said(a.c, s));
+    ahead = said(a.c, min(s + 1, a.c.sequences - 1));
     const int64_t t = u / units;
     unit = (int32_t)(u - t * units);
     head = (int32_t)(t / tiles);
@@ -396,10 +443,11 @@ struct Walk {
     hi = max(0, len - n + (min(row0 + kRows, n * G) - 1) / G + 1);
     lo = a.window > 0 ? max(0, p0 - a.window + 1) & -kChunk : 0;
   }
-  // Chunks of this unit that hold tokens to attend.
-  __device__ __forceinline__ int32_t chunks() const {
-    return min(max((hi - (lo + unit * kUnit) + kChunk - 1) / kChunk, 0), kWarps);
-  }
+  __device__ __forceinline__ int32_t token() const { return lo + unit * kChunk; }
+  // Whether this unit holds tokens to attend.
+  __device__ __forceinline__ bool live() const { return token() < hi; }
+  __device__ __forceinline__ bool last() const { return unit == units - 1; }
+  __device__ __forceinline__ Tile rows(int G) const { return Tile{row, row0, min(n * G - row0, kRows), head}; }
   // The next unit (there is one).
   __device__ __forceinline__ void next(const AttentionArgs& a) {
     if (++unit < units) return;
@@ -408,7 +456,10 @@ struct Walk {
       tile = 0;
       if (++head == a.c.heads) {
         head = 0;
-        while (b + 1 < a.c.sequences && sequence(a, b + 1) == 0) {
+        bool some = false;
+        while (!some && b + 1 < a.c.sequences) {
+          some = take(a, b + 1, ahead) != 0;
+          ahead = said(a.c, min(b + 1, a.c.sequences - 1));
         }
       }
     }
@@ -416,15 +467,28 @@ struct Walk {
   }
 };
 
-// Finds the first unit of this CTA: sequence (first) and the units before that
-// sequence (at). All threads; ends with a barrier.
+// The run of units of warp w of a CTA, in equal parts of all units: the CTAs and
+// warps that work, and where this one begins and ends.
+struct Run {
+  int64_t begin, end;
+};
+__device__ __forceinline__ int64_t working_ctas(int64_t units) {
+  return min((int64_t)gridDim.x, (units + kWarps - 1) / kWarps);
+}
+__device__ __forceinline__ Run run_of(int64_t units, int64_t ctas, int w) {
+  const int64_t i = (int64_t)blockIdx.x * kWarps + w;
+  return Run{units * i / (ctas * kWarps), units * (i + 1) / (ctas * kWarps)};
+}
+
+// Finds where the runs of this CTA's warps begin: sequence (first) and the units
+// before that sequence (at). All threads; ends with a barrier.
 template <int kRows>
-__device__ __forceinline__ void find_start(const AttentionArgs& a, AttnCtl* ctl, int64_t* sums) {
+__device__ __forceinline__ void find_starts(const AttentionArgs& a, AttnCtl* ctl, int64_t* sums) {
   const int32_t B = a.c.sequences, each = (B + kThreads - 1) / kThreads;
   const int32_t s0 = min((int32_t)threadIdx.x * each, B), s1 = min(s0 + each, B);
   Walk<kRows> w;
   int64_t mine = 0;
-  for (int32_t s = s0; s < s1; ++s) mine += w.sequence(a, s);
+  for (int32_t s = s0; s < s1; ++s) mine += w.take(a, s, said(a.c, s));
   int64_t upto = mine;
 #pragma unroll
   for (int i = 1; i < 32; i <<= 1) {
@@ -438,16 +502,21 @@ __device__ __forceinline__ void find_start(const AttentionArgs& a, AttnCtl* ctl,
     if (i < (int)(threadIdx.x >> 5)) before += sums[i];
     all += sums[i];
   }
-  const int64_t ctas = min((int64_t)gridDim.x, all), begin = ctas ? all * min((int64_t)blockIdx.x, ctas) / ctas : 0;
-  if (before <= begin && begin < before + mine) {
-    for (int32_t s = s0; s < s1; ++s) {
-      const int64_t u = w.sequence(a, s);
-      if (begin < before + u) {
-        ctl->first = s;
-        ctl->at = before;
-        break;
+  const int64_t ctas = working_ctas(all);
+  if (blockIdx.x < ctas && mine > 0) {
+    for (int i = 0; i < kWarps; ++i) {
+      const int64_t begin = run_of(all, ctas, i).begin;
+      if (begin < before || begin >= before + mine) continue;
+      int64_t at = before;
+      for (int32_t s = s0; s < s1; ++s) {
+        const int64_t u = each == 1 ? mine : w.take(a, s, said(a.c, s));
+        if (begin < at + u) {
+          ctl->first[i] = s;
+          ctl->at[i] = at;
+          break;
+        }
+        at += u;
       }
-      before += u;
     }
   }
   if (threadIdx.x == 0) ctl->units = all;
@@ -512,104 +581,128 @@ template <int D, int NT, bool kExact>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_attention_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ AttentionArgs a) {
   using S = Attn<D, NT>;
-  constexpr int kRows = S::kRows, kSegs = D / 16, kSlots = S::kSlots;
+  constexpr int kRows = S::kRows, kSegs = D / 16, kStages = S::kStages, kStat = 3 * kRows;
+  constexpr int kIn = S::kBox / 16;  // segments of 16 channels in a slab
   extern __shared__ uint8_t raw[];
   uint8_t* base = raw + ((1024u - (ptx::smem_u32(raw) & 1023u)) & 1023u);
-  float4* parts = reinterpret_cast<float4*>(base + kSlots * S::kSlot);  // [4][kSegs * NT * 32]
-  float* stats = reinterpret_cast<float*>(base + kSlots * S::kSlot + 4 * S::kPart);  // [kWarps][3][kRows]
-  AttnCtl* ctl = reinterpret_cast<AttnCtl*>(base + kSlots * S::kSlot + S::kFixed - 1024);
+  float* stats = reinterpret_cast<float*>(base + kWarps * kStages * S::kStage);  // of warps' open tiles, then of their heads
+  float* factors = stats + 2 * kWarps * kStat;                                   // [kWarps][kRows]
+  AttnCtl* ctl = reinterpret_cast<AttnCtl*>(base + kWarps * kStages * S::kStage + S::kFixed - 4096);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.q_heads / a.c.heads;
   const uint32_t ring = ptx::smem_u32(base), full = ptx::smem_u32(ctl->full), empty = ptx::smem_u32(ctl->empty);
 
   ptx::launch_dependents();
-  if (threadIdx.x < kSlots) {
-    ptx::mbar_init(full + 8 * threadIdx.x, 1);
-    ptx::mbar_init(empty + 8 * threadIdx.x, 1);
+  for (int i = threadIdx.x; i < kWarps * kMostStages; i += kThreads) {
+    ptx::mbar_init(full + 8 * i, 1);
+    ptx::mbar_init(empty + 8 * i, 1);
   }
   if (threadIdx.x == 0) {
     ctl->abort = 0;
-    ptx::fence_mbar_init();
     ptx::prefetch_tensormap(&map);
   }
-  find_start<kRows>(a, ctl, reinterpret_cast<int64_t*>(stats));
-  const int64_t all = ctl->units, ctas = min((int64_t)gridDim.x, all);
+  ptx::fence_mbar_init();
+  find_starts<kRows>(a, ctl, reinterpret_cast<int64_t*>(stats));
+  const int64_t all = ctl->units, ctas = working_ctas(all);
   if (blockIdx.x >= ctas) {
-    if (a.ws && threadIdx.x == 0) reinterpret_cast<Split*>(a.ws)[blockIdx.x].parts = 0;
+    if (a.ws && threadIdx.x == 0) put_at(&reinterpret_cast<Split*>(a.ws)[blockIdx.x].parts, (int32_t)0, a.ws, a.ws_bytes);
     return;
   }
-  const int64_t begin = all * blockIdx.x / ctas, end = all * (blockIdx.x + 1) / ctas;
   Walk<kRows> w;
-  w.sequence(a, ctl->first);
-  w.place(a, begin - ctl->at);
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ fetching ---
-    // Lane i < 16 looks up 16 tokens of the next unit: their page and its scales.
-    const int shift = 31 - __clz(a.c.page_tokens);
-    struct Look {
-      int32_t block, half;  // block of the keys (-1: none to load), place in the page
-      uint32_t scales;      // keys | values << 8
-      int32_t chunks;
+    // Lanes i and i + 8 walk warp i's run, one for each half of its units: the
+    // table is read two units ahead, the page's scales one.
+    const int i = lane & 7, shift = 31 - __clz(a.c.page_tokens);
+    const bool small = a.c.page_tokens == 16;  // each half in a page of its own, by copies of its own
+    Run run = run_of(all, ctas, i);
+    if (lane >= 16) run.end = run.begin;
+    int32_t units = (int32_t)(run.end - run.begin), rounds = units;
+    rounds = max(rounds, __shfl_xor_sync(0xffffffffu, rounds, 1));
+    rounds = max(rounds, __shfl_xor_sync(0xffffffffu, rounds, 2));
+    rounds = max(rounds, __shfl_xor_sync(0xffffffffu, rounds, 4));
+    rounds = __shfl_sync(0xffffffffu, rounds, 0);
+    struct Page {
+      int32_t page, head, place;  // page: -1 a wrong one, -2 none to load
+      bool live;
     };
-    auto look = [&]() {
-      Look l{-1, 0, 0xFFFFu, w.chunks()};
-      const int32_t j = w.lo + w.unit * kUnit + 16 * lane;
-      if (lane < 2 * kWarps && j < w.hi) {
-        const int32_t page = page_of(a.c, w.b, j >> shift);
-        if (page >= 0) {
-          const int64_t block = (int64_t)page * 2 * a.c.heads + w.head;
-          l.block = (int32_t)block;
-          l.half = (j & (a.c.page_tokens - 1)) >> 4;
-          l.scales = __ldg(a.c.scales + block) | (uint32_t)__ldg(a.c.scales + block + a.c.heads) << 8;
-        }
+    struct Block {
+      int32_t block, place;  // block of the keys (-1: none to load)
+      uint32_t keys, values;
+      bool live;
+    };
+    auto page_at = [&]() {
+      Page x{-2, w.head, 0, w.live()};
+      const int32_t j = w.token() + 8 * 2 * (lane >> 3);
+      if (j < w.hi) {
+        x.place = (j & (a.c.page_tokens - 1)) >> 4;
+        x.page = j >> shift < a.c.max_pages ? __ldg(a.c.table + (int64_t)w.b * a.c.ld_table + (j >> shift)) : -1;
       }
-      return l;
+      return x;
     };
-    const bool small = a.c.page_tokens == 16;  // each half its own page and its own copies
-    int64_t j = 0;
-    bool go = true;
-    Look l = look();
-    for (int64_t u = begin; u < end && go; ++u) {
-      const Look now = l;
-      if (u + 1 < end) {
+    auto block_of = [&](const Page& x) {
+      Block y{-1, x.place, 255u, 255u, x.live};
+      if (x.page >= 0 && x.page < a.c.pages) {
+        y.block = x.page * 2 * a.c.heads + x.head;
+        y.keys = __ldg(a.c.scales + y.block);
+        y.values = __ldg(a.c.scales + (int64_t)y.block + a.c.heads);
+      } else if (x.page != -2) {
+        index_fail();
+      }
+      return y;
+    };
+    Page p1{-2, 0, 0, false};
+    Block b1{-1, 0, 255u, 255u, false};
+    int32_t r = 0;  // units walked
+    if (units > 0) {
+      w.place(a, ctl->first[i], run.begin - ctl->at[i]);
+      b1 = block_of(page_at());
+      if (units > 1) {
         w.next(a);
-        l = look();
+        p1 = page_at();
       }
-      for (int c = 0; c < now.chunks; ++c, ++j) {
-        const int slot = (int)(j % kSlots);
-        if (j >= kSlots && !(go = wait_bar_warp(empty + 8 * slot, (uint32_t)(j / kSlots - 1) & 1, &ctl->abort))) break;
-        const int32_t b0 = __shfl_sync(0xffffffffu, now.block, 2 * c), b1 = __shfl_sync(0xffffffffu, now.block, 2 * c + 1);
-        const int32_t half = __shfl_sync(0xffffffffu, now.half, 2 * c);
-        const uint32_t s0 = __shfl_sync(0xffffffffu, now.scales, 2 * c), s1 = __shfl_sync(0xffffffffu, now.scales, 2 * c + 1);
-        if (lane == 0) {
-          const uint32_t bar = full + 8 * slot, k = ring + slot * S::kSlot, v = k + 2 * S::kHalf;
-          ctl->meta[slot] = (s0 & 0xFFu) | (s1 & 0xFFu) << 8 | (s0 & 0xFF00u) << 8 | (s1 & 0xFF00u) << 16;
-          if (small) {
-            ptx::mbar_arrive_expect_tx(bar, (b0 >= 0 ? 2 * S::kHalf : 0) + (b1 >= 0 ? 2 * S::kHalf : 0));
-            if (b0 >= 0) {
-              tma_pages(k, &map, 0, b0, bar);
-              tma_pages(v, &map, 0, b0 + a.c.heads, bar);
-            }
-            if (b1 >= 0) {
-              tma_pages(k + S::kHalf, &map, 0, b1, bar);
-              tma_pages(v + S::kHalf, &map, 0, b1 + a.c.heads, bar);
-            }
-          } else {
-            ptx::mbar_arrive_expect_tx(bar, b0 >= 0 ? 4 * S::kHalf : 0);
-            if (b0 >= 0) {
-              tma_pages(k, &map, half, b0, bar);
-              tma_pages(v, &map, half, b0 + a.c.heads, bar);
-            }
+      r = 2;
+    }
+    const uint32_t my_ring = ring + i * kStages * S::kStage, my_full = full + 8 * kMostStages * i, my_empty = empty + 8 * kMostStages * i;
+    int32_t tiles = 0, stage = 0;
+    uint32_t parity = 1;  // of the stage's reader
+    bool go = true;
+    for (int32_t round = 0; round < rounds && go; ++round) {
+      const Block now = b1;
+      b1 = Block{-1, 0, 255u, 255u, false};
+      if (round + 1 < units) b1 = block_of(p1);
+      if (r < units) {
+        w.next(a);
+        p1 = page_at();
+        ++r;
+      }
+      const int32_t other = __shfl_down_sync(0xffffffffu, now.block, 8);
+      const uint32_t keys = now.keys | __shfl_down_sync(0xffffffffu, now.keys, 8) << 8;
+      const uint32_t values = now.values | __shfl_down_sync(0xffffffffu, now.values, 8) << 8;
+      const bool mine = lane < 8 && round < units && now.live;
+#pragma unroll
+      for (int kind = 0; kind < 2; ++kind) {
+        go = go && wait_bars(my_empty + 8 * stage, parity, mine && tiles >= kStages, &ctl->abort);
+        if (mine && go) {
+          const uint32_t bar = my_full + 8 * stage, to = my_ring + stage * S::kStage;
+          const int32_t skip = kind ? a.c.heads : 0;
+          ctl->scales[i][stage] = (uint16_t)(kind ? values : keys);
+          ptx::mbar_arrive_expect_tx(bar, (now.block >= 0 ? (small ? 1 : 2) * S::kHalf : 0) + (small && other >= 0 ? S::kHalf : 0));
+          if (now.block >= 0) tma_pages(to, &map, now.place, now.block + skip, bar);
+          if (small && other >= 0) tma_pages(to + S::kHalf, &map, 0, other + skip, bar);
+          ++tiles;
+          if (++stage == kStages) {
+            stage = 0;
+            parity ^= 1u;
           }
         }
-        __syncwarp();
       }
     }
     if (!go) {
-      // the last load into each slot lands (bounded wait) before the CTA's memory goes
+      // the last load into each stage lands (bounded wait) before the CTA's memory goes
       const uint64_t t0 = ptx::globaltimer_ns();
-      for (int64_t i = j > kSlots ? j - kSlots : 0; i < j; ++i)
-        while (!ptx::mbar_try_wait(full + 8 * (uint32_t)(i % kSlots), (uint32_t)(i / kSlots) & 1) &&
+      for (int32_t z = max(tiles - kStages, 0); z < tiles; ++z)
+        while (!ptx::mbar_try_wait(my_full + 8 * (uint32_t)(z % kStages), (uint32_t)(z / kStages) & 1) &&
                ptx::globaltimer_ns() - t0 < kWaitLimitNs / 10) {
         }
     }
@@ -621,17 +714,39 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ldmatrix rows: matrix lane / 8 holds tokens 8 (m % 2) .. of half m / 2
   const int mrow = ((lane >> 3) & 1) * 8 + (lane & 7);
   const uint32_t swz = S::kBox == 128 ? mrow & 7 : S::kBox == 64 ? (mrow >> 1) & 3 : (mrow >> 2) & 1;
-  const uint32_t lane_at = (lane >> 4) * S::kHalf + mrow * S::kBox + (swz << 4);
+  const uint32_t my_ring = ring + warp * kStages * S::kStage;
+  const uint32_t lane_at = my_ring + (lane >> 4) * S::kHalf + mrow * S::kBox + (swz << 4);
+  const uint32_t my_full = full + 8 * kMostStages * warp, my_empty = empty + 8 * kMostStages * warp;
   const float scale2 = a.scale * 1.44269504088896f;
+  float* heads = a.ws + gridDim.x * (sizeof(Split) / 4 + 2 * part_floats(kRows, D));  // (used with a workspace only)
 
   uint32_t qf[kSegs][NT][2];
   float o[kSegs][NT][4], m[NT][2], lift[NT][2], sum[NT][2], slope[NT][2];
   int32_t qe[NT][2], pos[NT][2];
-  int64_t j0 = 0;
+  auto clear = [&]() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        m[nt][i] = lift[nt][i] = -INFINITY;
+        sum[nt][i] = 0.0f;
+      }
+#pragma unroll
+      for (int s = 0; s < kSegs; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[s][nt][i] = 0.0f;
+    }
+  };
+  clear();
+  int32_t stage = 0;
+  uint32_t parity = 0;
   bool go = true;
+  uint8_t has = 0;
+  const Run run = run_of(all, ctas, warp);
+  if (run.begin < run.end) w.place(a, ctl->first[warp], run.begin - ctl->at[warp]);
 
-  for (int64_t u = begin; u < end; ++u) {
-    if (u == begin || w.unit == 0) {
+  for (int64_t u = run.begin; u < run.end; ++u) {
+    if (u == run.begin || w.unit == 0) {
       // queries of this tile, row by row times a power of two: the largest in [2^14, 2^15)
       const int32_t rows = w.n * G - w.row0;
 #pragma unroll
@@ -669,39 +784,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int32_t c = min(w.row0 + 8 * nt + 2 * t + i, w.n * G - 1);
           pos[nt][i] = w.len - w.n + c / G;
           slope[nt][i] = a.slopes ? __ldg(a.slopes + w.head * G + c % G) * 1.44269504088896f : 0.0f;
-          m[nt][i] = lift[nt][i] = -INFINITY;
-          sum[nt][i] = 0.0f;
         }
       }
+    }
+
+    if (w.live() && go) go = wait_bar_warp(my_full + 8 * stage, parity, &ctl->abort);
+    if (w.live() && go) {
+      const int32_t c0 = w.token();
+      const uint32_t keys = ctl->scales[warp][stage];
+      float s[2][NT][4];
 #pragma unroll
-      for (int s = 0; s < kSegs; ++s)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[s][nt][i] = 0.0f;
-    }
-
-    const int32_t chunks = w.chunks();
-    if (warp < chunks && go) {
-      const int64_t j = j0 + warp;
-      const int slot = (int)(j % kSlots);
-      const int32_t c0 = w.lo + w.unit * kUnit + warp * kChunk;
-      go = wait_bar_warp(full + 8 * slot, (uint32_t)(j / kSlots) & 1, &ctl->abort);
-      if (go) {
-        const uint32_t meta = ctl->meta[slot];
-        const uint32_t kat = ring + slot * S::kSlot + lane_at, vat = kat + 2 * S::kHalf;
-        float s[2][NT][4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[h][nt][i] = 0.0f;
+          for (int i = 0; i < 4; ++i) s[h][nt][i] = 0.0f;
+      {
+        const uint32_t at = lane_at + stage * S::kStage;
 #pragma unroll
         for (int i = 0; i < kSegs; ++i) {
-          constexpr int kIn = S::kBox / 16;
           uint32_t r[4];
-          ldsm((kat ^ ((i % kIn) << 4)) + (i / kIn) * 16 * S::kBox, r);
+          ldsm((at ^ ((i % kIn) << 4)) + (i / kIn) * 16 * S::kBox, r);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint32_t a0 = e4m3x2_f16x2(r[2 * h]), a2 = e4m3x2_f16x2(r[2 * h] >> 16);
@@ -710,226 +813,315 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int nt = 0; nt < NT; ++nt) mma(s[h][nt], a0, a1, a2, a3, qf[i][nt][0], qf[i][nt][1]);
           }
         }
-
-        // scores in log2 units; -infinity where a row does not attend
-        const bool whole = c0 + kChunk <= w.p0 + 1 && (a.window == 0 || c0 > w.hi - 1 - a.window);
-        float ev[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int ks = (int)((meta >> (8 * h)) & 0xFFu);
-          const uint32_t vs = (meta >> (16 + 8 * h)) & 0xFFu;
-          ev[h] = vs == 255u ? __uint_as_float(0x7FC00000u) : (float)((int)vs - 127);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const bool bad = ks == 255 || qe[nt][i] == 1 << 20;
-              float f = bad ? __uint_as_float(0x7FC00000u) : pow2i(ks - 127 + qe[nt][i]);
-              if (a.softcap > 0.0f) {
-                f *= a.scale / a.softcap;
-#pragma unroll
-                for (int z = i; z < 4; z += 2) s[h][nt][z] = a.softcap * 1.44269504088896f * tanhf(s[h][nt][z] * f);
-              } else {
-                f *= scale2;
-                s[h][nt][i] *= f;
-                s[h][nt][i + 2] *= f;
-              }
-              const int32_t j1 = c0 + 16 * h + g - pos[nt][i];  // token's position less the row's
-              if (a.slopes) {
-                s[h][nt][i] += slope[nt][i] * (float)j1;
-                s[h][nt][i + 2] += slope[nt][i] * (float)(j1 + 8);
-              }
-              if (!whole) {
-                const int32_t most = a.window > 0 ? a.window : 0x7FFFFFFF;
-                if (j1 > 0 || j1 <= -most) s[h][nt][i] = -INFINITY;
-                if (j1 + 8 > 0 || j1 + 8 <= -most) s[h][nt][i + 2] = -INFINITY;
-              }
-            }
-          }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(my_empty + 8 * stage);
+        if (++stage == kStages) {
+          stage = 0;
+          parity ^= 1u;
         }
-        if (c0 + kChunk > w.hi) {
-          // tokens behind the last: whatever lies there must not meet a weight of zero
-          const int first = w.hi - c0;
-          for (int i = lane; i < (kChunk - first) * kSegs; i += 32) {
-            const int r = first + i / kSegs, seg = i % kSegs;
-            constexpr int kIn = S::kBox / 16;
-            const uint32_t at = ring + slot * S::kSlot + 2 * S::kHalf + (r >> 4) * S::kHalf + (seg / kIn) * 16 * S::kBox +
-                                (r & 15) * S::kBox + (seg % kIn) * 16;
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
-          }
-          ptx::fence_proxy_async();
-          __syncwarp();
-        }
+      }
 
-        // running maxima, and the weights
-        const bool one = ((meta >> 16) & 0xFFu) == meta >> 24;  // both halves' values under one scale
-        uint32_t pf[2][NT][2], pl[2][NT][2];
-        bool moved = false;
-        float keep[NT][2];
+      // scores in log2 units; -infinity where a row does not attend
+      const bool whole = c0 + kChunk <= w.p0 + 1 && (a.window == 0 || c0 > w.hi - 1 - a.window);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int ks = (int)((keys >> (8 * h)) & 0xFFu);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float cm[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float h0 = fmaxf(s[0][nt][i], s[0][nt][i + 2]), h1 = fmaxf(s[1][nt][i], s[1][nt][i + 2]);
-            float x = fmaxf(h0, h1);
+            const bool bad = ks == 255 || qe[nt][i] == 1 << 20;
+            float f = bad ? __uint_as_float(0x7FC00000u) : pow2i(ks - 127 + qe[nt][i]);
+            if (a.softcap > 0.0f) {
+              f *= a.scale / a.softcap;
 #pragma unroll
-            for (int z = 4; z < 32; z <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, z));
-            const float mn = fmaxf(m[nt][i], x);
-            cm[i] = finite_or_0(mn);
-            float y = x - cm[i] + ev[0];
-            if (!one) {
-              y = fmaxf(h0 - cm[i] + ev[0], h1 - cm[i] + ev[1]);
-#pragma unroll
-              for (int z = 4; z < 32; z <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, z));
+              for (int z = i; z < 4; z += 2) s[h][nt][z] = a.softcap * 1.44269504088896f * tanhf(s[h][nt][z] * f);
+            } else {
+              f *= scale2;
+              s[h][nt][i] *= f;
+              s[h][nt][i + 2] *= f;
             }
-            const float down = m[nt][i] - cm[i], was = down + lift[nt][i], now = fmaxf(was, y);
-            sum[nt][i] *= ex2(down);
-            keep[nt][i] = ex2(was - finite_or_0(now));
-            moved |= was != now;
-            m[nt][i] = mn;
-            lift[nt][i] = now;
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float c[2] = {ev[h] + kTop - finite_or_0(lift[nt][0]), ev[h] + kTop - finite_or_0(lift[nt][1])};
-            float p[4];
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              const float x = s[h][nt][z] - cm[z & 1];
-              sum[nt][z & 1] += ex2(x);
-              p[z] = x == -INFINITY ? 0.0f : ex2(x + c[z & 1]);
+            const int32_t j1 = c0 + 16 * h + g - pos[nt][i];  // token's position less the row's
+            if (a.slopes) {
+              s[h][nt][i] += slope[nt][i] * (float)j1;
+              s[h][nt][i + 2] += slope[nt][i] * (float)(j1 + 8);
             }
-            const uint32_t u0 = f16x2(p[0], p[1]), u1 = f16x2(p[2], p[3]);
-            pf[h][nt][0] = transposed(u0);
-            pf[h][nt][1] = transposed(u1);
-            if (kExact) {
-              const float2 q0 = f16x2_f32(u0), q1 = f16x2_f32(u1);
-              pl[h][nt][0] = transposed(f16x2(p[0] - q0.x, p[1] - q0.y));
-              pl[h][nt][1] = transposed(f16x2(p[2] - q1.x, p[3] - q1.y));
+            if (!whole) {
+              const int32_t most = a.window > 0 ? a.window : 0x7FFFFFFF;
+              if (j1 > 0 || j1 <= -most) s[h][nt][i] = -INFINITY;
+              if (j1 + 8 > 0 || j1 + 8 <= -most) s[h][nt][i + 2] = -INFINITY;
             }
           }
         }
-        if (__any_sync(0xffffffffu, moved)) {
+      }
+
+      if (go) go = wait_bar_warp(my_full + 8 * stage, parity, &ctl->abort);
+      const uint32_t values = ctl->scales[warp][stage];
+      float ev[2];
 #pragma unroll
-          for (int i = 0; i < kSegs; ++i)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int z = 0; z < 4; ++z) o[i][nt][z] *= keep[nt][z & 1];
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t vs = (values >> (8 * h)) & 0xFFu;
+        ev[h] = vs == 255u ? __uint_as_float(0x7FC00000u) : (float)((int)vs - 127);
+      }
+      if (c0 + kChunk > w.hi) {
+        // tokens behind the last: whatever lies there must not meet a weight of zero
+        const int first = w.hi - c0;
+        for (int i = lane; i < (kChunk - first) * kSegs; i += 32) {
+          const int r = first + i / kSegs, seg = i % kSegs;
+          const uint32_t at = my_ring + stage * S::kStage + (r >> 4) * S::kHalf + (seg / kIn) * 16 * S::kBox +
+                              (r & 15) * S::kBox + (seg % kIn) * 16;
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
         }
-#pragma unroll
-        for (int i = 0; i < kSegs; ++i) {
-          constexpr int kIn = S::kBox / 16;
-          uint32_t r[4];
-          ldsm_t((vat ^ ((i % kIn) << 4)) + (i / kIn) * 16 * S::kBox, r);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            // two tokens of a channel side by side, the even channel below
-            const uint32_t x = __byte_perm(r[2 * h], 0, 0x3120), y = __byte_perm(r[2 * h + 1], 0, 0x3120);
-            const uint32_t a0 = e4m3x2_f16x2(x), a1 = e4m3x2_f16x2(x >> 16), a2 = e4m3x2_f16x2(y), a3 = e4m3x2_f16x2(y >> 16);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma(o[i][nt], a0, a1, a2, a3, pf[h][nt][0], pf[h][nt][1]);
-              if (kExact) mma(o[i][nt], a0, a1, a2, a3, pl[h][nt][0], pl[h][nt][1]);
-            }
-          }
-        }
+        ptx::fence_proxy_async();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(empty + 8 * slot);
+      }
+
+      // running maxima, and the weights
+      const bool one = (values & 0xFFu) == values >> 8;  // both halves' values under one scale
+      uint32_t pf[2][NT][2], pl[2][NT][2];
+      bool moved = false;
+      float keep[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float cm[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float h0 = fmaxf(s[0][nt][i], s[0][nt][i + 2]), h1 = fmaxf(s[1][nt][i], s[1][nt][i + 2]);
+          float x = fmaxf(h0, h1);
+#pragma unroll
+          for (int z = 4; z < 32; z <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, z));
+          const float mn = fmaxf(m[nt][i], x);
+          cm[i] = finite_or_0(mn);
+          float y = x - cm[i] + ev[0];
+          if (!one) {
+            y = fmaxf(h0 - cm[i] + ev[0], h1 - cm[i] + ev[1]);
+#pragma unroll
+            for (int z = 4; z < 32; z <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, z));
+          }
+          const float down = m[nt][i] - cm[i], was = down + lift[nt][i], now = fmaxf(was, y);
+          sum[nt][i] *= ex2(down);
+          keep[nt][i] = ex2(was - finite_or_0(now));
+          moved |= was != now;
+          m[nt][i] = mn;
+          lift[nt][i] = now;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float c[2] = {ev[h] + kTop - finite_or_0(lift[nt][0]), ev[h] + kTop - finite_or_0(lift[nt][1])};
+          float p[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const float x = s[h][nt][z] - cm[z & 1];
+            sum[nt][z & 1] += ex2(x);
+            p[z] = x == -INFINITY ? 0.0f : ex2(x + c[z & 1]);
+          }
+          const uint32_t u0 = f16x2(p[0], p[1]), u1 = f16x2(p[2], p[3]);
+          pf[h][nt][0] = transposed(u0);
+          pf[h][nt][1] = transposed(u1);
+          if (kExact) {
+            const float2 q0 = f16x2_f32(u0), q1 = f16x2_f32(u1);
+            pl[h][nt][0] = transposed(f16x2(p[0] - q0.x, p[1] - q0.y));
+            pl[h][nt][1] = transposed(f16x2(p[2] - q1.x, p[3] - q1.y));
+          }
+        }
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int i = 0; i < kSegs; ++i)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int z = 0; z < 4; ++z) o[i][nt][z] *= keep[nt][z & 1];
+      }
+      const uint32_t at = lane_at + stage * S::kStage;
+#pragma unroll
+      for (int i = 0; i < kSegs; ++i) {
+        uint32_t r[4];
+        ldsm_t((at ^ ((i % kIn) << 4)) + (i / kIn) * 16 * S::kBox, r);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          // two tokens of a channel side by side, the even channel below
+          const uint32_t x = __byte_perm(r[2 * h], 0, 0x3120), y = __byte_perm(r[2 * h + 1], 0, 0x3120);
+          const uint32_t a0 = e4m3x2_f16x2(x), a1 = e4m3x2_f16x2(x >> 16), a2 = e4m3x2_f16x2(y), a3 = e4m3x2_f16x2(y >> 16);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma(o[i][nt], a0, a1, a2, a3, pf[h][nt][0], pf[h][nt][1]);
+            if (kExact) mma(o[i][nt], a0, a1, a2, a3, pl[h][nt][0], pl[h][nt][1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(my_empty + 8 * stage);
+      if (++stage == kStages) {
+        stage = 0;
+        parity ^= 1u;
       }
     }
-    j0 += chunks;
 
-    if (w.unit == w.units - 1 || u == end - 1) {
-      // the eight warps' sums become one
+    has = kOpen | (u - w.unit < run.begin ? kBegan : 0) | (has & kHead);
+    if (w.last()) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int z = 4; z < 32; z <<= 1) sum[nt][i] += __shfl_xor_sync(0xffffffffu, sum[nt][i], z);
-          if (g == 0) {
-            float* st = stats + warp * 3 * kRows + 8 * nt + 2 * t + i;
-            st[0] = m[nt][i];
-            st[kRows] = lift[nt][i];
-            st[2 * kRows] = sum[nt][i];
+      const Tile tile = w.rows(G);
+      if (u - w.unit >= run.begin) {
+        // a tile of this warp alone
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int r = 8 * nt + 2 * t + i;
+            if (r < tile.rows) {
+              const float2 k = last_factors(lift[nt][i], sum[nt][i]);
+              const int64_t at = row_of(a.out, tile.token, tile.head, tile.row0 + r, G) + 2 * g;
+#pragma unroll
+              for (int s = 0; s < kSegs; ++s)
+                put2(a, at + 16 * s, o[s][nt][i] * k.x * k.y, o[s][nt][i + 2] * k.x * k.y);
+              if (a.lse && g == 0) put_lse(a, tile.token, tile.head, tile.row0 + r, G, m[nt][i], sum[nt][i]);
+            }
           }
-        }
-      warps_sync();
-      float f[NT][2];
+        has &= kHead;
+      } else {
+        // the end of a tile that began before
+        float4* to = reinterpret_cast<float4*>(heads) + ((int64_t)blockIdx.x * kWarps + warp) * S::kQuads + lane;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int s = 0; s < kSegs; ++s)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const Joined x = joined(stats, 8 * nt + 2 * t + i, kWarps, [](int z) { return z * 3 * kRows; }, kRows);
-          f[nt][i] = ex2(m[nt][i] - finite_or_0(x.m) + lift[nt][i] - finite_or_0(x.lift));
-        }
+          for (int nt = 0; nt < NT; ++nt)
+            put_at(to + (s * NT + nt) * 32, make_float4(o[s][nt][0], o[s][nt][1], o[s][nt][2], o[s][nt][3]), a.ws, a.ws_bytes);
+        if (g == 0) {
 #pragma unroll
-      for (int round = 0; round < 2; ++round) {
-        if ((warp >= 4) == (round == 0)) {
-          float4* to = parts + (warp & 3) * kSegs * NT * 32 + lane;
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < kSegs; ++i)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              float4 x = make_float4(o[i][nt][0] * f[nt][0], o[i][nt][1] * f[nt][1], o[i][nt][2] * f[nt][0],
-                                     o[i][nt][3] * f[nt][1]);
-              float4* at = to + (i * NT + nt) * 32;
-              if (round) {
-                const float4 y = *at;
-                x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-              }
-              *at = x;
+            for (int i = 0; i < 2; ++i) {
+              float* st = stats + (kWarps + warp) * kStat + 8 * nt + 2 * t + i;
+              st[0] = m[nt][i];
+              st[kRows] = lift[nt][i];
+              st[2 * kRows] = sum[nt][i];
             }
         }
-        warps_sync();
+        if (lane == 0) ctl->head[warp] = tile;
+        has = kHead;
       }
-      const bool whole = w.unit == w.units - 1 && u - w.unit >= begin;
-      const int part = u - w.unit < begin ? 0 : 1;  // began before this CTA, or goes on behind it
-      float* ws = a.ws + gridDim.x * (sizeof(Split) / 4) + (2 * (int64_t)blockIdx.x + part) * part_floats(kRows, D);
-      const int32_t rows = min(w.n * G - w.row0, kRows);
-      for (int e = threadIdx.x; e < kSegs * NT * 32; e += kWarps * 32) {
-        float4 x = parts[e];
-#pragma unroll
-        for (int z = 1; z < 4; ++z) {
-          const float4 y = parts[z * kSegs * NT * 32 + e];
-          x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-        }
-        if (!whole) {
-          put_at(ws + 3 * kRows + 4 * (int64_t)e, x, a.ws, a.ws_bytes);
-          continue;
-        }
-        const Quad qd = quad<NT>(e);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = qd.row + i;
-          if (r >= rows) break;
-          const Joined y = joined(stats, r, kWarps, [](int z) { return z * 3 * kRows; }, kRows);
-          const float2 k = last_factors(y.lift, y.sum);
-          put2(a, row_of(a.out, w.row, w.head, w.row0 + r, G) + qd.d, (i ? x.y : x.x) * k.x * k.y,
-               (i ? x.w : x.z) * k.x * k.y);
-          if (a.lse && qd.d == 0) put_lse(a, w.row, w.head, w.row0 + r, G, y.m, y.sum);
-        }
-      }
-      if (!whole && threadIdx.x < kRows) {
-        const int r = threadIdx.x;
-        const Joined y = joined(stats, r, kWarps, [](int z) { return z * 3 * kRows; }, kRows);
-        put_at(ws + r, y.m, a.ws, a.ws_bytes);
-        put_at(ws + kRows + r, y.lift, a.ws, a.ws_bytes);
-        put_at(ws + 2 * kRows + r, y.sum, a.ws, a.ws_bytes);
-      }
-      if (u == end - 1 && a.ws && threadIdx.x == 0) {
-        // the CTA of the tile's last unit: the largest c with all c / ctas <= it
-        const int64_t last = u - w.unit + w.units - 1;
-        const int32_t to = (int32_t)(((last + 1) * ctas - 1) / all);
-        const Split sp = {w.row, w.row0, rows, w.head, !whole && part == 1 ? to - (int32_t)blockIdx.x + 1 : 0, {0, 0, 0}};
-        put_at(reinterpret_cast<Split*>(a.ws) + blockIdx.x, sp, a.ws, a.ws_bytes);
-      }
-      warps_sync();
+      clear();
     }
-    if (u + 1 < end) w.next(a);
+    if (u + 1 < run.end) w.next(a);
   }
+
+  // ---------------------------------------------------- joining in the CTA ---
+  const bool empty_run = run.begin == run.end;  // adds nothing to the tile around it
+  if ((has & kOpen) || empty_run) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int z = 4; z < 32; z <<= 1) sum[nt][i] += __shfl_xor_sync(0xffffffffu, sum[nt][i], z);
+        if (g == 0) {
+          float* st = stats + warp * kStat + 8 * nt + 2 * t + i;
+          st[0] = m[nt][i];
+          st[kRows] = lift[nt][i];
+          st[2 * kRows] = sum[nt][i];
+        }
+      }
+    // (this warp's ring: its loads have all been read)
+    float4* to = reinterpret_cast<float4*>(base + warp * kStages * S::kStage) + lane;
+    __syncwarp();
+#pragma unroll
+    for (int s = 0; s < kSegs; ++s)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        to[(s * NT + nt) * 32] = make_float4(o[s][nt][0], o[s][nt][1], o[s][nt][2], o[s][nt][3]);
+  }
+  if (lane == 0) {
+    ctl->has[warp] = has;
+    if (has & kOpen) {
+      ctl->open[warp] = w.rows(G);
+      ctl->left[warp] = w.units - 1 - w.unit;
+    }
+  }
+  warps_sync();
+
+  // A tile that warps first .. last share: open in all but the last, which ends
+  // it (closed) or is the CTA's last. `before`: it began before this CTA.
+  auto join = [&](int first, int last, bool closed, bool before, const Tile& tile) {
+    auto stat = [&](int z) { return ((closed && z == last - first ? kWarps : 0) + first + z) * kStat; };
+    const int count = last - first + 1;
+    const bool final = closed && !before;
+    float* ws = a.ws + gridDim.x * (sizeof(Split) / 4) + (2 * (int64_t)blockIdx.x + !before) * part_floats(kRows, D);
+    if (threadIdx.x < kRows) {
+      const int x = threadIdx.x;
+      const Joined j = joined(stats, x, count, stat, kRows);
+      for (int z = 0; z < count; ++z)
+        factors[z * kRows + x] = ex2(stats[stat(z) + x] - finite_or_0(j.m) + stats[stat(z) + kRows + x] - finite_or_0(j.lift));
+      if (final) {
+        // (the first member's statistics have done their part)
+        const float2 k = last_factors(j.lift, j.sum);
+        stats[stat(0) + x] = k.x;
+        stats[stat(0) + kRows + x] = k.y;
+        if (a.lse && x < tile.rows) put_lse(a, tile.token, tile.head, tile.row0 + x, G, j.m, j.sum);
+      } else {
+        put_at(ws + x, j.m, a.ws, a.ws_bytes);
+        put_at(ws + kRows + x, j.lift, a.ws, a.ws_bytes);
+        put_at(ws + 2 * kRows + x, j.sum, a.ws, a.ws_bytes);
+      }
+    }
+    warps_sync();
+    for (int e = threadIdx.x; e < S::kQuads; e += kWarps * 32) {
+      const Quad qd = quad<NT>(e);
+      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int z = 0; z < count; ++z) {
+        const float4 y = closed && z == count - 1
+                             ? reinterpret_cast<const float4*>(heads)[((int64_t)blockIdx.x * kWarps + last) * S::kQuads + e]
+                             : reinterpret_cast<const float4*>(base + (first + z) * kStages * S::kStage)[e];
+        const float f0 = factors[z * kRows + qd.row], f1 = factors[z * kRows + qd.row + 1];
+        x = make_float4(fmaf(y.x, f0, x.x), fmaf(y.y, f1, x.y), fmaf(y.z, f0, x.z), fmaf(y.w, f1, x.w));
+      }
+      if (!final) {
+        put_at(ws + 3 * kRows + 4 * (int64_t)e, x, a.ws, a.ws_bytes);
+        continue;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = qd.row + i;
+        if (r >= tile.rows) break;
+        const float k1 = stats[stat(0) + r], k2 = stats[stat(0) + kRows + r];
+        put2(a, row_of(a.out, tile.token, tile.head, tile.row0 + r, G) + qd.d, (i ? x.y : x.x) * k1 * k2,
+             (i ? x.w : x.z) * k1 * k2);
+      }
+    }
+    warps_sync();
+  };
+  int first = -1, tail = 0;  // of the tile that is open: the first warp that has it, the last
+  bool before = false;
+  for (int z = 0; z < kWarps; ++z) {
+    const uint8_t h = ctl->has[z];
+    if (h & kHead) {
+      join(first < 0 ? z : first, z, true, first < 0 || before, ctl->head[z]);
+      first = -1;
+    }
+    if (h & kOpen) {
+      if (first < 0) {
+        first = z;
+        before = h & kBegan;
+      }
+      tail = z;
+    }
+  }
+  Split sp = {{0, 0, 0, 0}, 0, {0, 0, 0}};
+  if (first >= 0) {
+    join(first, kWarps - 1, false, before, ctl->open[first]);
+    if (!before) {
+      // the CTA of the tile's last unit: the largest c with floor(all c / ctas) up to it
+      const int64_t at = run_of(all, ctas, kWarps - 1).end - 1 + ctl->left[tail];
+      sp.tile = ctl->open[first];
+      sp.parts = (int32_t)(((at + 1) * ctas - 1) / all) - (int32_t)blockIdx.x + 1;
+    }
+  }
+  if (threadIdx.x == 0 && a.ws) put_at(reinterpret_cast<Split*>(a.ws) + blockIdx.x, sp, a.ws, a.ws_bytes);
 }
 
 // Joins the parts of the tile that goes on behind CTA blockIdx.x.
@@ -952,7 +1144,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__
     factor[r] = last_factors(x.lift, x.sum);
     top[r] = finite_or_0(x.m);
     lift[r] = finite_or_0(x.lift);
-    if (a.lse && r < sp.rows) put_lse(a, sp.token, sp.head, sp.row0 + r, G, x.m, x.sum);
+    if (a.lse && r < sp.tile.rows) put_lse(a, sp.tile.token, sp.tile.head, sp.tile.row0 + r, G, x.m, x.sum);
   }
   __syncthreads();
   for (int e = threadIdx.x; e < D / 16 * NT * 32; e += 256) {
@@ -969,8 +1161,8 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = qd.row + i;
-      if (r < sp.rows)
-        put2(a, row_of(a.out, sp.token, sp.head, sp.row0 + r, G) + qd.d, (i ? x.y : x.x) * factor[r].x * factor[r].y,
+      if (r < sp.tile.rows)
+        put2(a, row_of(a.out, sp.tile.token, sp.tile.head, sp.tile.row0 + r, G) + qd.d, (i ? x.y : x.x) * factor[r].x * factor[r].y,
              (i ? x.w : x.z) * factor[r].x * factor[r].y);
     }
   }
@@ -1019,8 +1211,8 @@ AttnShape attn_shape(const AttentionArgs& a) {
   const int64_t kRows = 8 * s.nt, tiles = rows / kRows + a.c.sequences, most = (int64_t)a.c.max_pages * a.c.page_tokens + 1;
   const int64_t span = a.window > 0 && a.window + (kRows + G - 2) / G + 1 + kChunk < most
                            ? a.window + (kRows + G - 2) / G + 1 + kChunk : most;
-  const int64_t units = (span + kUnit - 1) / kUnit, all = tiles * a.c.heads * units;
-  s.ctas = (int)(all < kSms ? all : kSms);
+  const int64_t units = (span + kChunk - 1) / kChunk, all = tiles * a.c.heads * units, ctas = (all + kWarps - 1) / kWarps;
+  s.ctas = (int)(ctas < kSms ? ctas : kSms);
   s.split = units > 1;
   return s;
 }
@@ -1084,7 +1276,8 @@ cudaError_t attend(const AttentionArgs& a, const AttnShape& sh, cudaStream_t st)
 int64_t cache_attention_workspace_bytes(const AttentionArgs& a) {
   const AttnShape s = attn_shape(a);
   if (!s.split) return 0;
-  return s.ctas * ((int64_t)sizeof(Split) + 8 * part_floats(8 * s.nt, a.c.head_dim));
+  return s.ctas * ((int64_t)sizeof(Split) + 8 * part_floats(8 * s.nt, a.c.head_dim) +
+                   (int64_t)kWarps * 8 * s.nt * a.c.head_dim * 4);
 }
 
 cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t st) {
