@@ -252,15 +252,17 @@ __global__ void __launch_bounds__(1024) cache_read_kernel(CacheArgs c, Heads k, 
 // the workspace for cache_join_kernel.
 
 constexpr int kSms = 152;
-constexpr int kWarps = 8;                       // that multiply
-constexpr int kThreads = (kWarps + 1) * 32;     // and one that fetches
 constexpr int kChunk = 32;                      // tokens of a unit
 constexpr float kTop = 15.0f;                   // weights are held times 2^15: f16 keeps 2^-39 of the largest
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
-constexpr int kMostStages = 16;
+constexpr int kMostWarps = 15, kMostStages = 8;
 
 template <int D, int NT>
 struct Attn {
+  // Warps that multiply, beside the one that fetches: as many as their registers
+  // (sums D NT / 4, queries D NT / 8 of them) leave room for on the SM.
+  static constexpr int kWarps = D * NT <= 128 ? 15 : D * NT < 256 ? 11 : 7;
+  static constexpr int kThreads = (kWarps + 1) * 32;
   static constexpr int kRows = 8 * NT;
   static constexpr int kBox = D % 128 == 0 ? 128 : D % 64 == 0 ? 64 : 32;  // bytes of a row in one swizzled slab
   static constexpr int kHalf = 16 * D;                                     // 16 tokens of keys or values
@@ -279,14 +281,14 @@ struct Tile {
 };
 
 struct AttnCtl {
-  uint64_t full[kWarps][kMostStages], empty[kWarps][kMostStages];
-  uint16_t scales[kWarps][kMostStages];  // of a stage's halves
-  Tile head[kWarps], open[kWarps];       // tiles that a warp shares with the one before it, and behind it
-  int64_t at[kWarps];                    // units before the first sequence of a warp's run
+  uint64_t full[kMostWarps][kMostStages], empty[kMostWarps][kMostStages];
+  uint16_t scales[kMostWarps][kMostStages];  // of a stage's halves
+  Tile head[kMostWarps], open[kMostWarps];       // tiles that a warp shares with the one before it, and behind it
+  int64_t at[kMostWarps];                    // units before the first sequence of a warp's run
   int64_t units;                         // of all sequences
-  int32_t first[kWarps];                 // that sequence
-  int32_t left[kWarps];                  // units of the open tile behind a warp's run
-  uint8_t has[kWarps];                   // kHead, kOpen, kBegan
+  int32_t first[kMostWarps];                 // that sequence
+  int32_t left[kMostWarps];                  // units of the open tile behind a warp's run
+  uint8_t has[kMostWarps];                   // kHead, kOpen, kBegan
   uint32_t abort;
 };
 static_assert(sizeof(AttnCtl) <= 4096, "control block");
@@ -380,10 +382,18 @@ __device__ __forceinline__ void tma_pages(uint32_t dst, const CUtensorMap* map, 
       "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(half), "r"(block), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void warps_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); }
+template <int kWarps>
+__device__ __forceinline__ void warps_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+}
 
 // 2^e for a whole e, 0 below the smallest normal number.
 __device__ __forceinline__ float pow2i(int e) { return e < -126 ? 0.0f : __uint_as_float((uint32_t)(min(e, 127) + 127) << 23); }
+
+// Whole numbers of 32 bits divide in a fraction of the time that those of 64 take.
+__device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
+  return ((x | y) >> 31) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
+}
 
 // What a call says of one sequence, as it lies in memory.
 struct Said {
@@ -430,9 +440,9 @@ struct Walk {
   __device__ __forceinline__ void place(const AttentionArgs& a, int32_t s, int64_t u) {
     take(a, s, said(a.c, s));
     ahead = said(a.c, min(s + 1, a.c.sequences - 1));
-    const int64_t t = u / units;
+    const int64_t t = divide(u, units);
     unit = (int32_t)(u - t * units);
-    head = (int32_t)(t / tiles);
+    head = (int32_t)divide(t, tiles);
     tile = (int32_t)(t - (int64_t)head * tiles);
     set_tile(a);
   }
@@ -467,23 +477,28 @@ struct Walk {
   }
 };
 
-// The run of units of warp w of a CTA, in equal parts of all units: the CTAs and
-// warps that work, and where this one begins and ends.
-struct Run {
-  int64_t begin, end;
+// All units in equal runs, one for each warp of the CTAs that work: warp i of
+// them (CTA i / kWarps) begins at begin(i).
+struct Cut {
+  int64_t each;
+  int32_t more, ctas;  // the first `more` runs have one more
+  __device__ __forceinline__ int64_t begin(int32_t i) const { return each * i + min(i, more); }
 };
-__device__ __forceinline__ int64_t working_ctas(int64_t units) {
-  return min((int64_t)gridDim.x, (units + kWarps - 1) / kWarps);
-}
-__device__ __forceinline__ Run run_of(int64_t units, int64_t ctas, int w) {
-  const int64_t i = (int64_t)blockIdx.x * kWarps + w;
-  return Run{units * i / (ctas * kWarps), units * (i + 1) / (ctas * kWarps)};
+template <int kWarps>
+__device__ __forceinline__ Cut cut(int64_t units) {
+  Cut c;
+  c.ctas = units < (int64_t)gridDim.x * kWarps ? (int32_t)((uint32_t)(units + kWarps - 1) / (uint32_t)kWarps) : (int32_t)gridDim.x;
+  const int32_t runs = max(c.ctas, 1) * kWarps;
+  c.each = divide(units, runs);
+  c.more = (int32_t)(units - c.each * runs);
+  return c;
 }
 
 // Finds where the runs of this CTA's warps begin: sequence (first) and the units
 // before that sequence (at). All threads; ends with a barrier.
-template <int kRows>
+template <int kRows, int kWarps>
 __device__ __forceinline__ void find_starts(const AttentionArgs& a, AttnCtl* ctl, int64_t* sums) {
+  constexpr int kThreads = (kWarps + 1) * 32;
   const int32_t B = a.c.sequences, each = (B + kThreads - 1) / kThreads;
   const int32_t s0 = min((int32_t)threadIdx.x * each, B), s1 = min(s0 + each, B);
   Walk<kRows> w;
@@ -502,10 +517,10 @@ __device__ __forceinline__ void find_starts(const AttentionArgs& a, AttnCtl* ctl
     if (i < (int)(threadIdx.x >> 5)) before += sums[i];
     all += sums[i];
   }
-  const int64_t ctas = working_ctas(all);
-  if (blockIdx.x < ctas && mine > 0) {
+  const Cut runs = cut<kWarps>(all);
+  if (blockIdx.x < runs.ctas && mine > 0) {
     for (int i = 0; i < kWarps; ++i) {
-      const int64_t begin = run_of(all, ctas, i).begin;
+      const int64_t begin = runs.begin(blockIdx.x * kWarps + i);
       if (begin < before || begin >= before + mine) continue;
       int64_t at = before;
       for (int32_t s = s0; s < s1; ++s) {
@@ -553,7 +568,8 @@ __device__ __forceinline__ float2 last_factors(float lift, float sum) {
   asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(lift));
   return sum == 0.0f ? make_float2(0.0f, 0.0f) : make_float2((1.0f / sum) * 0x1p-15f, e);
 }
-__device__ __forceinline__ float finite_or_0(float m) { return m == -INFINITY ? 0.0f : m; }
+// The maximum of no scores: finite, so that differences with it are numbers.
+constexpr float kLowest = -3.4e38f;
 // Maxima and sum of row r over `count` parts; part i has its rows' maxima at
 // p[at(i)], lifts and sums `rows` and 2 `rows` behind them.
 struct Joined {
@@ -561,11 +577,10 @@ struct Joined {
 };
 template <typename F>
 __device__ __forceinline__ Joined joined(const float* p, int r, int count, F at, int rows) {
-  Joined j = {-INFINITY, -INFINITY, 0.0f};
+  Joined j = {kLowest, -INFINITY, 0.0f};
   for (int i = 0; i < count; ++i) j.m = fmaxf(j.m, p[at(i) + r]);
-  const float m = finite_or_0(j.m);
   for (int i = 0; i < count; ++i) {
-    const float down = p[at(i) + r] - m;
+    const float down = p[at(i) + r] - j.m;
     j.lift = fmaxf(j.lift, down + p[at(i) + rows + r]);
     j.sum += p[at(i) + 2 * rows + r] * ex2(down);
   }
@@ -578,10 +593,10 @@ __device__ __forceinline__ void put_lse(const AttentionArgs& a, int32_t token, i
 }
 
 template <int D, int NT, bool kExact>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
     cache_attention_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ AttentionArgs a) {
   using S = Attn<D, NT>;
-  constexpr int kRows = S::kRows, kSegs = D / 16, kStages = S::kStages, kStat = 3 * kRows;
+  constexpr int kWarps = S::kWarps, kRows = S::kRows, kSegs = D / 16, kStages = S::kStages, kStat = 3 * kRows;
   constexpr int kIn = S::kBox / 16;  // segments of 16 channels in a slab
   extern __shared__ uint8_t raw[];
   uint8_t* base = raw + ((1024u - (ptx::smem_u32(raw) & 1023u)) & 1023u);
@@ -592,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t ring = ptx::smem_u32(base), full = ptx::smem_u32(ctl->full), empty = ptx::smem_u32(ctl->empty);
 
   ptx::launch_dependents();
-  for (int i = threadIdx.x; i < kWarps * kMostStages; i += kThreads) {
+  for (int i = threadIdx.x; i < kWarps * kMostStages; i += S::kThreads) {
     ptx::mbar_init(full + 8 * i, 1);
     ptx::mbar_init(empty + 8 * i, 1);
   }
@@ -601,9 +616,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::prefetch_tensormap(&map);
   }
   ptx::fence_mbar_init();
-  find_starts<kRows>(a, ctl, reinterpret_cast<int64_t*>(stats));
-  const int64_t all = ctl->units, ctas = working_ctas(all);
-  if (blockIdx.x >= ctas) {
+  find_starts<kRows, kWarps>(a, ctl, reinterpret_cast<int64_t*>(stats));
+  const Cut runs = cut<kWarps>(ctl->units);
+  if (blockIdx.x >= runs.ctas) {
     if (a.ws && threadIdx.x == 0) put_at(&reinterpret_cast<Split*>(a.ws)[blockIdx.x].parts, (int32_t)0, a.ws, a.ws_bytes);
     return;
   }
@@ -611,17 +626,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ fetching ---
-    // Lanes i and i + 8 walk warp i's run, one for each half of its units: the
+    // Lanes i and i + 16 walk warp i's run, one for each half of its units: the
     // table is read two units ahead, the page's scales one.
-    const int i = lane & 7, shift = 31 - __clz(a.c.page_tokens);
+    const int i = min(lane & 15, kWarps - 1), shift = 31 - __clz(a.c.page_tokens);
     const bool small = a.c.page_tokens == 16;  // each half in a page of its own, by copies of its own
-    Run run = run_of(all, ctas, i);
-    if (lane >= 16) run.end = run.begin;
-    int32_t units = (int32_t)(run.end - run.begin), rounds = units;
-    rounds = max(rounds, __shfl_xor_sync(0xffffffffu, rounds, 1));
-    rounds = max(rounds, __shfl_xor_sync(0xffffffffu, rounds, 2));
-    rounds = max(rounds, __shfl_xor_sync(0xffffffffu, rounds, 4));
-    rounds = __shfl_sync(0xffffffffu, rounds, 0);
+    const bool owner = (lane & 15) < kWarps;
+    const int64_t begin = runs.begin(blockIdx.x * kWarps + i);
+    const int32_t units = owner ? (int32_t)(runs.begin(blockIdx.x * kWarps + i + 1) - begin) : 0;
+    const int32_t rounds = __reduce_max_sync(0xffffffffu, units);
     struct Page {
       int32_t page, head, place;  // page: -1 a wrong one, -2 none to load
       bool live;
@@ -633,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto page_at = [&]() {
       Page x{-2, w.head, 0, w.live()};
-      const int32_t j = w.token() + 8 * 2 * (lane >> 3);
+      const int32_t j = w.token() + (lane & 16);
       if (j < w.hi) {
         x.place = (j & (a.c.page_tokens - 1)) >> 4;
         x.page = j >> shift < a.c.max_pages ? __ldg(a.c.table + (int64_t)w.b * a.c.ld_table + (j >> shift)) : -1;
@@ -655,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Block b1{-1, 0, 255u, 255u, false};
     int32_t r = 0;  // units walked
     if (units > 0) {
-      w.place(a, ctl->first[i], run.begin - ctl->at[i]);
+      w.place(a, ctl->first[i], begin - ctl->at[i]);
       b1 = block_of(page_at());
       if (units > 1) {
         w.next(a);
@@ -676,10 +688,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         p1 = page_at();
         ++r;
       }
-      const int32_t other = __shfl_down_sync(0xffffffffu, now.block, 8);
-      const uint32_t keys = now.keys | __shfl_down_sync(0xffffffffu, now.keys, 8) << 8;
-      const uint32_t values = now.values | __shfl_down_sync(0xffffffffu, now.values, 8) << 8;
-      const bool mine = lane < 8 && round < units && now.live;
+      const int32_t other = __shfl_down_sync(0xffffffffu, now.block, 16);
+      const uint32_t keys = now.keys | __shfl_down_sync(0xffffffffu, now.keys, 16) << 8;
+      const uint32_t values = now.values | __shfl_down_sync(0xffffffffu, now.values, 16) << 8;
+      const bool mine = lane < 16 && round < units && now.live;
 #pragma unroll
       for (int kind = 0; kind < 2; ++kind) {
         go = go && wait_bars(my_empty + 8 * stage, parity, mine && tiles >= kStages, &ctl->abort);
@@ -717,19 +729,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t my_ring = ring + warp * kStages * S::kStage;
   const uint32_t lane_at = my_ring + (lane >> 4) * S::kHalf + mrow * S::kBox + (swz << 4);
   const uint32_t my_full = full + 8 * kMostStages * warp, my_empty = empty + 8 * kMostStages * warp;
-  const float scale2 = a.scale * 1.44269504088896f;
+  const float scale2 = a.scale * 1.44269504088896f, cap = a.softcap > 0.0f ? a.scale / a.softcap : 0.0f;
   float* heads = a.ws + gridDim.x * (sizeof(Split) / 4 + 2 * part_floats(kRows, D));  // (used with a workspace only)
 
   uint32_t qf[kSegs][NT][2];
-  float o[kSegs][NT][4], m[NT][2], lift[NT][2], sum[NT][2], slope[NT][2];
-  int32_t qe[NT][2], pos[NT][2];
+  float o[kSegs][NT][4], m[NT][2], lift[NT][2], sum[NT][2], slope[NT][2], unit_q[NT][2];
+  int32_t pos[NT][2];
   auto clear = [&]() {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        m[nt][i] = lift[nt][i] = -INFINITY;
-        sum[nt][i] = 0.0f;
+        m[nt][i] = kLowest;
+        lift[nt][i] = sum[nt][i] = 0.0f;
       }
 #pragma unroll
       for (int s = 0; s < kSegs; ++s)
@@ -742,11 +754,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t parity = 0;
   bool go = true;
   uint8_t has = 0;
-  const Run run = run_of(all, ctas, warp);
-  if (run.begin < run.end) w.place(a, ctl->first[warp], run.begin - ctl->at[warp]);
+  const int64_t begin = runs.begin(blockIdx.x * kWarps + warp);
+  const int32_t units = (int32_t)(runs.begin(blockIdx.x * kWarps + warp + 1) - begin);
+  if (units) w.place(a, ctl->first[warp], begin - ctl->at[warp]);
 
-  for (int64_t u = run.begin; u < run.end; ++u) {
-    if (u == run.begin || w.unit == 0) {
+  for (int32_t u = 0; u < units; ++u) {
+    if (u == 0 || w.unit == 0) {
       // queries of this tile, row by row times a power of two: the largest in [2^14, 2^15)
       const int32_t rows = w.n * G - w.row0;
 #pragma unroll
@@ -776,9 +789,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           qf[s][nt][0] = e == 255 ? 0u : f16x2(lo.x * f1 * f2, lo.y * f1 * f2);
           qf[s][nt][1] = e == 255 ? 0u : f16x2(hi.x * f1 * f2, hi.y * f1 * f2);
         }
-        const int32_t ex = e == 255 ? 1 << 20 : e - 141;
-        qe[nt][0] = __shfl_sync(0xffffffffu, ex, 8 * t);
-        qe[nt][1] = __shfl_sync(0xffffffffu, ex, 8 * t + 4);
+        // 2^(e - 141), down to 2^-140
+        const float uq = e == 255 ? __uint_as_float(0x7FC00000u) : e > 14 ? pow2i(e - 141) : __uint_as_float(1u << (e + 8));
+        unit_q[nt][0] = __shfl_sync(0xffffffffu, uq, 8 * t);
+        unit_q[nt][1] = __shfl_sync(0xffffffffu, uq, 8 * t + 4);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int32_t c = min(w.row0 + 8 * nt + 2 * t + i, w.n * G - 1);
@@ -825,21 +839,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = c0 + kChunk <= w.p0 + 1 && (a.window == 0 || c0 > w.hi - 1 - a.window);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int ks = (int)((keys >> (8 * h)) & 0xFFu);
+        const float ks = scale_value((keys >> (8 * h)) & 0xFFu);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const bool bad = ks == 255 || qe[nt][i] == 1 << 20;
-            float f = bad ? __uint_as_float(0x7FC00000u) : pow2i(ks - 127 + qe[nt][i]);
+            const float f = unit_q[nt][i] * ks;  // (exact)
             if (a.softcap > 0.0f) {
-              f *= a.scale / a.softcap;
 #pragma unroll
-              for (int z = i; z < 4; z += 2) s[h][nt][z] = a.softcap * 1.44269504088896f * tanhf(s[h][nt][z] * f);
+              for (int z = i; z < 4; z += 2) s[h][nt][z] = a.softcap * 1.44269504088896f * tanhf(s[h][nt][z] * (f * cap));
             } else {
-              f *= scale2;
-              s[h][nt][i] *= f;
-              s[h][nt][i + 2] *= f;
+              s[h][nt][i] *= f * scale2;
+              s[h][nt][i + 2] *= f * scale2;
             }
             const int32_t j1 = c0 + 16 * h + g - pos[nt][i];  // token's position less the row's
             if (a.slopes) {
@@ -890,8 +901,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float x = fmaxf(h0, h1);
 #pragma unroll
           for (int z = 4; z < 32; z <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, z));
-          const float mn = fmaxf(m[nt][i], x);
-          cm[i] = finite_or_0(mn);
+          cm[i] = fmaxf(m[nt][i], x);
           float y = x - cm[i] + ev[0];
           if (!one) {
             y = fmaxf(h0 - cm[i] + ev[0], h1 - cm[i] + ev[1]);
@@ -900,20 +910,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float down = m[nt][i] - cm[i], was = down + lift[nt][i], now = fmaxf(was, y);
           sum[nt][i] *= ex2(down);
-          keep[nt][i] = ex2(was - finite_or_0(now));
+          keep[nt][i] = ex2(was - now);
           moved |= was != now;
-          m[nt][i] = mn;
+          m[nt][i] = cm[i];
           lift[nt][i] = now;
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float c[2] = {ev[h] + kTop - finite_or_0(lift[nt][0]), ev[h] + kTop - finite_or_0(lift[nt][1])};
+          const float c[2] = {ev[h] + kTop - lift[nt][0], ev[h] + kTop - lift[nt][1]};
           float p[4];
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
             const float x = s[h][nt][z] - cm[z & 1];
             sum[nt][z & 1] += ex2(x);
-            p[z] = x == -INFINITY ? 0.0f : ex2(x + c[z & 1]);
+            p[z] = ex2(x + c[z & 1]);
+          }
+          if (ev[h] != ev[h]) {
+            // values that are no numbers: where a row attends them
+#pragma unroll
+            for (int z = 0; z < 4; ++z) p[z] = s[h][nt][z] == -INFINITY ? 0.0f : ev[h];
           }
           const uint32_t u0 = f16x2(p[0], p[1]), u1 = f16x2(p[2], p[3]);
           pf[h][nt][0] = transposed(u0);
@@ -958,7 +973,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
 
-    has = kOpen | (u - w.unit < run.begin ? kBegan : 0) | (has & kHead);
+    has = kOpen | (u < w.unit ? kBegan : 0) | (has & kHead);
     if (w.last()) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -967,7 +982,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int z = 4; z < 32; z <<= 1) sum[nt][i] += __shfl_xor_sync(0xffffffffu, sum[nt][i], z);
       const Tile tile = w.rows(G);
-      if (u - w.unit >= run.begin) {
+      if (u >= w.unit) {
         // a tile of this warp alone
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -1008,12 +1023,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       clear();
     }
-    if (u + 1 < run.end) w.next(a);
+    if (u + 1 < units) w.next(a);
   }
 
   // ---------------------------------------------------- joining in the CTA ---
-  const bool empty_run = run.begin == run.end;  // adds nothing to the tile around it
-  if ((has & kOpen) || empty_run) {
+  if ((has & kOpen) || units == 0) {  // (an empty run adds nothing to the tile around it)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1043,7 +1057,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ctl->left[warp] = w.units - 1 - w.unit;
     }
   }
-  warps_sync();
+  warps_sync<kWarps>();
 
   // A tile that warps first .. last share: open in all but the last, which ends
   // it (closed) or is the CTA's last. `before`: it began before this CTA.
@@ -1056,7 +1070,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int x = threadIdx.x;
       const Joined j = joined(stats, x, count, stat, kRows);
       for (int z = 0; z < count; ++z)
-        factors[z * kRows + x] = ex2(stats[stat(z) + x] - finite_or_0(j.m) + stats[stat(z) + kRows + x] - finite_or_0(j.lift));
+        factors[z * kRows + x] = ex2(stats[stat(z) + x] - j.m + stats[stat(z) + kRows + x] - j.lift);
       if (final) {
         // (the first member's statistics have done their part)
         const float2 k = last_factors(j.lift, j.sum);
@@ -1069,7 +1083,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         put_at(ws + 2 * kRows + x, j.sum, a.ws, a.ws_bytes);
       }
     }
-    warps_sync();
+    warps_sync<kWarps>();
     for (int e = threadIdx.x; e < S::kQuads; e += kWarps * 32) {
       const Quad qd = quad<NT>(e);
       float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -1093,7 +1107,7 @@ __global__ void __launch_bounds__(kThreads, 1)
              (i ? x.w : x.z) * k1 * k2);
       }
     }
-    warps_sync();
+    warps_sync<kWarps>();
   };
   int first = -1, tail = 0;  // of the tile that is open: the first warp that has it, the last
   bool before = false;
@@ -1115,56 +1129,95 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (first >= 0) {
     join(first, kWarps - 1, false, before, ctl->open[first]);
     if (!before) {
-      // the CTA of the tile's last unit: the largest c with floor(all c / ctas) up to it
-      const int64_t at = run_of(all, ctas, kWarps - 1).end - 1 + ctl->left[tail];
+      // the CTAs up to the tile's last unit
+      const int64_t at = runs.begin((blockIdx.x + 1) * kWarps) - 1 + ctl->left[tail];
+      int32_t c = blockIdx.x + 1;
+      while (c < runs.ctas && runs.begin(c * kWarps) <= at) ++c;
       sp.tile = ctl->open[first];
-      sp.parts = (int32_t)(((at + 1) * ctas - 1) / all) - (int32_t)blockIdx.x + 1;
+      sp.parts = c - (int32_t)blockIdx.x;
     }
   }
   if (threadIdx.x == 0 && a.ws) put_at(reinterpret_cast<Split*>(a.ws) + blockIdx.x, sp, a.ws, a.ws_bytes);
 }
 
-// Joins the parts of the tile that goes on behind CTA blockIdx.x.
+// Joins the parts of the tile that goes on behind CTA blockIdx.x: a warp for a
+// row's statistics, a lane for a part; then as many groups of threads as fit take
+// every so many-th part each.
+constexpr int kJoinThreads = 512;
 template <int D, int NT>
-__global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__ AttentionArgs a, int ctas) {
-  constexpr int kRows = 8 * NT;
+__global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ AttentionArgs a) {
+  constexpr int kRows = 8 * NT, kQuads = Attn<D, NT>::kQuads, kGroups = kQuads < kJoinThreads ? kJoinThreads / kQuads : 1;
+  __shared__ float factors[kSms][kRows];
+  __shared__ float2 last[kRows];
+  __shared__ float4 sums[kGroups > 1 ? kJoinThreads : 1];
+  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
   ptx::wait_prior_grid();
   const Split sp = reinterpret_cast<const Split*>(a.ws)[blockIdx.x];
   if (sp.parts == 0) return;
-  __shared__ float2 factor[kRows];
   const int G = a.q_heads / a.c.heads;
   // part 0 is this CTA's second, the others the first of the CTAs behind it
-  auto part = [&](int i) {
-    return a.ws + ctas * (int64_t)(sizeof(Split) / 4) + (2 * (int64_t)(blockIdx.x + i) + (i == 0)) * part_floats(kRows, D);
-  };
-  __shared__ float top[kRows], lift[kRows];
-  if (threadIdx.x < kRows) {
-    const int r = threadIdx.x;
-    const Joined x = joined(a.ws, r, sp.parts, [&](int i) { return part(i) - a.ws; }, kRows);
-    factor[r] = last_factors(x.lift, x.sum);
-    top[r] = finite_or_0(x.m);
-    lift[r] = finite_or_0(x.lift);
-    if (a.lse && r < sp.tile.rows) put_lse(a, sp.tile.token, sp.tile.head, sp.tile.row0 + r, G, x.m, x.sum);
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < D / 16 * NT * 32; e += 256) {
-    const Quad qd = quad<NT>(e);
-    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int i = 0; i < sp.parts; ++i) {
-      const float* p = part(i);
-      const float4 y = *reinterpret_cast<const float4*>(p + 3 * kRows + 4 * (int64_t)e);
-      const float f0 = ex2(p[qd.row] - top[qd.row] + p[kRows + qd.row] - lift[qd.row]);
-      const float f1 = ex2(p[qd.row + 1] - top[qd.row + 1] + p[kRows + qd.row + 1] - lift[qd.row + 1]);
-      x = make_float4(fmaf(y.x, f0, x.x), fmaf(y.y, f1, x.y), fmaf(y.z, f0, x.z), fmaf(y.w, f1, x.w));
+  const float* parts = a.ws + gridDim.x * (sizeof(Split) / 4) + 2 * (int64_t)blockIdx.x * part_floats(kRows, D);
+  auto part = [&](int i) { return parts + (2 * i + (i == 0)) * part_floats(kRows, D); };
+  if (row < kRows) {
+    constexpr int kMost = (kSms + 31) / 32;
+    float m[kMost], lift[kMost], sum[kMost], top = kLowest, high = -INFINITY, all = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      const bool some = 32 * i + lane < sp.parts;
+      const float* p = part(some ? 32 * i + lane : 0) + row;
+      m[i] = some ? p[0] : kLowest;
+      lift[i] = some ? p[kRows] : 0.0f;
+      sum[i] = some ? p[2 * kRows] : 0.0f;
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = qd.row + i;
-      if (r < sp.tile.rows)
-        put2(a, row_of(a.out, sp.tile.token, sp.tile.head, sp.tile.row0 + r, G) + qd.d, (i ? x.y : x.x) * factor[r].x * factor[r].y,
-             (i ? x.w : x.z) * factor[r].x * factor[r].y);
+    for (int i = 0; i < kMost; ++i) top = fmaxf(top, m[i]);
+    for (int z = 16; z; z >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, z));
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      high = fmaxf(high, m[i] - top + lift[i]);
+      all += sum[i] * ex2(m[i] - top);
     }
+    for (int z = 16; z; z >>= 1) {
+      high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, z));
+      all += __shfl_xor_sync(0xffffffffu, all, z);
+    }
+#pragma unroll
+    for (int i = 0; i < kMost; ++i)
+      if (32 * i + lane < sp.parts) factors[32 * i + lane][row] = ex2(m[i] - top + lift[i] - high);
+    if (lane == 0) {
+      last[row] = last_factors(high, all);
+      if (a.lse && row < sp.tile.rows) put_lse(a, sp.tile.token, sp.tile.head, sp.tile.row0 + row, G, top, all);
+    }
+  }
+  __syncthreads();
+  static_assert(kQuads <= kJoinThreads, "a quad a thread");
+  const int group = threadIdx.x / kQuads, e = threadIdx.x % kQuads;
+  const Quad qd = quad<NT>(e);
+  float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (group < kGroups) {
+#pragma unroll 8
+    for (int i = group; i < sp.parts; i += kGroups) {
+      const float4 y = *reinterpret_cast<const float4*>(part(i) + 3 * kRows + 4 * e);
+      const float f0 = factors[i][qd.row], f1 = factors[i][qd.row + 1];
+      x = make_float4(fmaf(y.x, f0, x.x), fmaf(y.y, f1, x.y), fmaf(y.z, f0, x.z), fmaf(y.w, f1, x.w));
+    }
+  }
+  if (kGroups > 1) {
+    sums[threadIdx.x] = x;
+    __syncthreads();
+  }
+  if (group > 0) return;
+#pragma unroll
+  for (int i = 1; i < kGroups; ++i) {
+    const float4 y = sums[i * kQuads + e];
+    x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = qd.row + i;
+    if (r < sp.tile.rows)
+      put2(a, row_of(a.out, sp.tile.token, sp.tile.head, sp.tile.row0 + r, G) + qd.d, (i ? x.y : x.x) * last[r].x * last[r].y,
+           (i ? x.w : x.z) * last[r].x * last[r].y);
   }
 }
 
@@ -1198,7 +1251,7 @@ cudaError_t launch_cache_read(const CacheArgs& c, const Heads& k, const Heads& v
 namespace {
 // How a call is cut: query rows of a tile, CTAs, and whether a tile may be split.
 struct AttnShape {
-  int nt, ctas;
+  int nt, warps, ctas;
   bool split;
 };
 // Sixteen rows to a tile where a sequence has more than eight on average (their
@@ -1208,10 +1261,12 @@ AttnShape attn_shape(const AttentionArgs& a) {
   const int64_t G = a.q_heads / a.c.heads, rows = a.c.tokens * G;
   AttnShape s;
   s.nt = a.c.head_dim <= 128 && rows > 8 * (int64_t)a.c.sequences ? 2 : 1;
+  const int width = a.c.head_dim * s.nt;
+  s.warps = width <= 128 ? 15 : width < 256 ? 11 : 7;  // (Attn::kWarps)
   const int64_t kRows = 8 * s.nt, tiles = rows / kRows + a.c.sequences, most = (int64_t)a.c.max_pages * a.c.page_tokens + 1;
   const int64_t span = a.window > 0 && a.window + (kRows + G - 2) / G + 1 + kChunk < most
                            ? a.window + (kRows + G - 2) / G + 1 + kChunk : most;
-  const int64_t units = (span + kChunk - 1) / kChunk, all = tiles * a.c.heads * units, ctas = (all + kWarps - 1) / kWarps;
+  const int64_t units = (span + kChunk - 1) / kChunk, all = tiles * a.c.heads * units, ctas = (all + s.warps - 1) / s.warps;
   s.ctas = (int)(ctas < kSms ? ctas : kSms);
   s.split = units > 1;
   return s;
@@ -1253,19 +1308,19 @@ cudaError_t attend(const AttentionArgs& a, const AttnShape& sh, cudaStream_t st)
   }
   CUtensorMap map;
   if (!pages_map(&map, a.c, a.q.p, S::kBox)) return cudaErrorInvalidValue;
-  cache_attention_kernel<D, NT, kExact><<<sh.ctas, kThreads, S::kBytes, st>>>(map, a);
+  cache_attention_kernel<D, NT, kExact><<<sh.ctas, S::kThreads, S::kBytes, st>>>(map, a);
   if ((e = cudaGetLastError()) != cudaSuccess || !sh.split) return e;
   // launched while the kernel before it drains; it waits for that kernel's parts itself
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)sh.ctas);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_join_kernel<D, NT>, a, sh.ctas);
+  return cudaLaunchKernelEx(&cfg, cache_join_kernel<D, NT>, a);
 }
 template <int D, int NT>
 cudaError_t attend(const AttentionArgs& a, const AttnShape& sh, cudaStream_t st) {
@@ -1277,7 +1332,7 @@ int64_t cache_attention_workspace_bytes(const AttentionArgs& a) {
   const AttnShape s = attn_shape(a);
   if (!s.split) return 0;
   return s.ctas * ((int64_t)sizeof(Split) + 8 * part_floats(8 * s.nt, a.c.head_dim) +
-                   (int64_t)kWarps * 8 * s.nt * a.c.head_dim * 4);
+                   (int64_t)s.warps * 8 * s.nt * a.c.head_dim * 4);
 }
 
 cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t st) {
