@@ -268,7 +268,7 @@ struct Attn {
   static constexpr int kHalf = 16 * D;                                     // 16 tokens of keys or values
   static constexpr int kStage = 2 * kHalf;                                 // 32 tokens of keys or values
   static constexpr int kQuads = D / 16 * NT * 32;                          // of a tile's sums (below)
-  static constexpr int kFixed = 2 * kWarps * 3 * kRows * 4 + kWarps * kRows * 4 + 4096;
+  static constexpr int kFixed = 2 * kWarps * 3 * kRows * 4 + 4096;
   static constexpr int kFit = (227 * 1024 - 1024 - kFixed) / (kWarps * kStage);
   static constexpr int kStages = kFit < kMostStages ? kFit : kMostStages;  // of a warp's ring
   static constexpr int kBytes = 1024 + kWarps * kStages * kStage + kFixed;
@@ -570,22 +570,10 @@ __device__ __forceinline__ float2 last_factors(float lift, float sum) {
 }
 // The maximum of no scores: finite, so that differences with it are numbers.
 constexpr float kLowest = -3.4e38f;
-// Maxima and sum of row r over `count` parts; part i has its rows' maxima at
-// p[at(i)], lifts and sums `rows` and 2 `rows` behind them.
+// A row's maximum, lift and sum of several parts.
 struct Joined {
   float m, lift, sum;
 };
-template <typename F>
-__device__ __forceinline__ Joined joined(const float* p, int r, int count, F at, int rows) {
-  Joined j = {kLowest, -INFINITY, 0.0f};
-  for (int i = 0; i < count; ++i) j.m = fmaxf(j.m, p[at(i) + r]);
-  for (int i = 0; i < count; ++i) {
-    const float down = p[at(i) + r] - j.m;
-    j.lift = fmaxf(j.lift, down + p[at(i) + rows + r]);
-    j.sum += p[at(i) + 2 * rows + r] * ex2(down);
-  }
-  return j;
-}
 __device__ __forceinline__ void put_lse(const AttentionArgs& a, int32_t token, int32_t head, int32_t r, int G, float m,
                                         float sum) {
   const int64_t at = (int64_t)(token + r / G) * a.q_heads + head * G + r % G;
@@ -601,7 +589,6 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
   extern __shared__ uint8_t raw[];
   uint8_t* base = raw + ((1024u - (ptx::smem_u32(raw) & 1023u)) & 1023u);
   float* stats = reinterpret_cast<float*>(base + kWarps * kStages * S::kStage);  // of warps' open tiles, then of their heads
-  float* factors = stats + 2 * kWarps * kStat;                                   // [kWarps][kRows]
   AttnCtl* ctl = reinterpret_cast<AttnCtl*>(base + kWarps * kStages * S::kStage + S::kFixed - 4096);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.q_heads / a.c.heads;
   const uint32_t ring = ptx::smem_u32(base), full = ptx::smem_u32(ctl->full), empty = ptx::smem_u32(ctl->empty);
@@ -1059,85 +1046,107 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
   }
   warps_sync<kWarps>();
 
-  // A tile that warps first .. last share: open in all but the last, which ends
-  // it (closed) or is the CTA's last. `before`: it began before this CTA.
-  auto join = [&](int first, int last, bool closed, bool before, const Tile& tile) {
-    auto stat = [&](int z) { return ((closed && z == last - first ? kWarps : 0) + first + z) * kStat; };
-    const int count = last - first + 1;
-    const bool final = closed && !before;
-    float* ws = a.ws + gridDim.x * (sizeof(Split) / 4) + (2 * (int64_t)blockIdx.x + !before) * part_floats(kRows, D);
-    if (threadIdx.x < kRows) {
-      const int x = threadIdx.x;
-      const Joined j = joined(stats, x, count, stat, kRows);
-      for (int z = 0; z < count; ++z)
-        factors[z * kRows + x] = ex2(stats[stat(z) + x] - j.m + stats[stat(z) + kRows + x] - j.lift);
-      if (final) {
-        // (the first member's statistics have done their part)
-        const float2 k = last_factors(j.lift, j.sum);
-        stats[stat(0) + x] = k.x;
-        stats[stat(0) + kRows + x] = k.y;
-        if (a.lse && x < tile.rows) put_lse(a, tile.token, tile.head, tile.row0 + x, G, j.m, j.sum);
-      } else {
-        put_at(ws + x, j.m, a.ws, a.ws_bytes);
-        put_at(ws + kRows + x, j.lift, a.ws, a.ws_bytes);
-        put_at(ws + 2 * kRows + x, j.sum, a.ws, a.ws_bytes);
-      }
-    }
-    warps_sync<kWarps>();
-    for (int e = threadIdx.x; e < S::kQuads; e += kWarps * 32) {
-      const Quad qd = quad<NT>(e);
-      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int z = 0; z < count; ++z) {
-        const float4 y = closed && z == count - 1
-                             ? reinterpret_cast<const float4*>(heads)[((int64_t)blockIdx.x * kWarps + last) * S::kQuads + e]
-                             : reinterpret_cast<const float4*>(base + (first + z) * kStages * S::kStage)[e];
-        const float f0 = factors[z * kRows + qd.row], f1 = factors[z * kRows + qd.row + 1];
-        x = make_float4(fmaf(y.x, f0, x.x), fmaf(y.y, f1, x.y), fmaf(y.z, f0, x.z), fmaf(y.w, f1, x.w));
-      }
-      if (!final) {
-        put_at(ws + 3 * kRows + 4 * (int64_t)e, x, a.ws, a.ws_bytes);
-        continue;
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = qd.row + i;
-        if (r >= tile.rows) break;
-        const float k1 = stats[stat(0) + r], k2 = stats[stat(0) + kRows + r];
-        put2(a, row_of(a.out, tile.token, tile.head, tile.row0 + r, G) + qd.d, (i ? x.y : x.x) * k1 * k2,
-             (i ? x.w : x.z) * k1 * k2);
-      }
-    }
-    warps_sync<kWarps>();
+  // Tiles that warps share, all of them at once. Warps first .. last have one: open
+  // in all but the last, which ends it, or open to the CTA's end. `before`: it
+  // began before this CTA.
+  const uint8_t h = lane < kWarps ? ctl->has[lane] : 0;
+  const uint32_t heads_in = __ballot_sync(0xffffffffu, h & kHead), open_in = __ballot_sync(0xffffffffu, h & kOpen);
+  const uint32_t begun_in = open_in & ~__ballot_sync(0xffffffffu, h & kBegan);
+  // (a warp ends a tile before it leaves one open)
+  const int ended = __popc(heads_in), groups = ended + (open_in != 0 && open_in >= 1u << max(31 - __clz(heads_in), 0));
+  struct Group {
+    int first, last;
+    bool closed, before;
   };
-  int first = -1, tail = 0;  // of the tile that is open: the first warp that has it, the last
-  bool before = false;
-  for (int z = 0; z < kWarps; ++z) {
-    const uint8_t h = ctl->has[z];
-    if (h & kHead) {
-      join(first < 0 ? z : first, z, true, first < 0 || before, ctl->head[z]);
-      first = -1;
+  auto group = [&](int i) {
+    Group x{0, kWarps - 1, i < ended, false};
+    uint32_t up_to = 0xffffffffu;  // warps in which the tile may have begun
+    if (x.closed) {
+      uint32_t left = heads_in;
+      for (int z = 0; z < i; ++z) left &= left - 1;
+      x.last = __ffs(left) - 1;
+      up_to = (1u << x.last) - 1;
     }
-    if (h & kOpen) {
-      if (first < 0) {
-        first = z;
-        before = h & kBegan;
-      }
-      tail = z;
+    const uint32_t in = begun_in & up_to, ends = heads_in & up_to;
+    const int at = 31 - __clz(in);  // -1: none
+    x.before = at < 31 - __clz(ends) || !in;
+    x.first = x.before ? 0 : at;
+    return x;
+  };
+  auto stat = [&](const Group& x, int z) { return ((x.closed && z == x.last ? kWarps : 0) + z) * kStat; };
+  auto part_of = [&](const Group& x) {
+    return a.ws + gridDim.x * (sizeof(Split) / 4) + (2 * (int64_t)blockIdx.x + !x.before) * part_floats(kRows, D);
+  };
+  for (int i = threadIdx.x; i < groups * kRows; i += kWarps * 32) {
+    const Group x = group(i / kRows);
+    const int r = i % kRows;
+    Joined j = {kLowest, -INFINITY, 0.0f};
+    for (int z = x.first; z <= x.last; ++z) j.m = fmaxf(j.m, stats[stat(x, z) + r]);
+    for (int z = x.first; z <= x.last; ++z) {
+      const float* st = stats + stat(x, z) + r;
+      const float down = st[0] - j.m;
+      j.lift = fmaxf(j.lift, down + st[kRows]);
+      j.sum += st[2 * kRows] * ex2(down);
+    }
+    for (int z = x.first; z <= x.last; ++z) {
+      // (a member's maximum has done its part: its factor takes the place)
+      float* st = stats + stat(x, z) + r;
+      st[0] = ex2(st[0] - j.m + st[kRows] - j.lift);
+    }
+    float* st = stats + stat(x, x.last) + r;
+    if (x.closed && !x.before) {
+      const float2 k = last_factors(j.lift, j.sum);
+      st[kRows] = k.x;
+      st[2 * kRows] = k.y;
+      const Tile& tile = ctl->head[x.last];
+      if (a.lse && r < tile.rows) put_lse(a, tile.token, tile.head, tile.row0 + r, G, j.m, j.sum);
+    } else {
+      float* ws = part_of(x);
+      put_at(ws + r, j.m, a.ws, a.ws_bytes);
+      put_at(ws + kRows + r, j.lift, a.ws, a.ws_bytes);
+      put_at(ws + 2 * kRows + r, j.sum, a.ws, a.ws_bytes);
     }
   }
-  Split sp = {{0, 0, 0, 0}, 0, {0, 0, 0}};
-  if (first >= 0) {
-    join(first, kWarps - 1, false, before, ctl->open[first]);
-    if (!before) {
+  warps_sync<kWarps>();
+  for (int i = threadIdx.x; i < groups * S::kQuads; i += kWarps * 32) {
+    const Group y = group(i / S::kQuads);
+    const int e = i % S::kQuads;
+    const Quad qd = quad<NT>(e);
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int z = y.first; z <= y.last; ++z) {
+      const float4 q = y.closed && z == y.last
+                           ? reinterpret_cast<const float4*>(heads)[((int64_t)blockIdx.x * kWarps + z) * S::kQuads + e]
+                           : reinterpret_cast<const float4*>(base + z * kStages * S::kStage)[e];
+      const float f0 = stats[stat(y, z) + qd.row], f1 = stats[stat(y, z) + qd.row + 1];
+      x = make_float4(fmaf(q.x, f0, x.x), fmaf(q.y, f1, x.y), fmaf(q.z, f0, x.z), fmaf(q.w, f1, x.w));
+    }
+    if (!y.closed || y.before) {
+      put_at(part_of(y) + 3 * kRows + 4 * (int64_t)e, x, a.ws, a.ws_bytes);
+      continue;
+    }
+    const Tile& tile = ctl->head[y.last];
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      const int r = qd.row + z;
+      if (r >= tile.rows) break;
+      const float* st = stats + stat(y, y.last) + r;
+      put2(a, row_of(a.out, tile.token, tile.head, tile.row0 + r, G) + qd.d, (z ? x.y : x.x) * st[kRows] * st[2 * kRows],
+           (z ? x.w : x.z) * st[kRows] * st[2 * kRows]);
+    }
+  }
+  if (threadIdx.x == 0 && a.ws) {
+    Split sp = {{0, 0, 0, 0}, 0, {0, 0, 0}};
+    const Group x = group(ended);
+    if (groups > ended && !x.before) {
       // the CTAs up to the tile's last unit
-      const int64_t at = runs.begin((blockIdx.x + 1) * kWarps) - 1 + ctl->left[tail];
+      const int64_t at = runs.begin((blockIdx.x + 1) * kWarps) - 1 + ctl->left[31 - __clz(open_in)];
       int32_t c = blockIdx.x + 1;
       while (c < runs.ctas && runs.begin(c * kWarps) <= at) ++c;
-      sp.tile = ctl->open[first];
+      sp.tile = ctl->open[x.first];
       sp.parts = c - (int32_t)blockIdx.x;
     }
+    put_at(reinterpret_cast<Split*>(a.ws) + blockIdx.x, sp, a.ws, a.ws_bytes);
   }
-  if (threadIdx.x == 0 && a.ws) put_at(reinterpret_cast<Split*>(a.ws) + blockIdx.x, sp, a.ws, a.ws_bytes);
 }
 
 // Joins the parts of the tile that goes on behind CTA blockIdx.x: a warp for a
