@@ -791,11 +791,19 @@ mxfp4_status mxfp8_cache_read(const mxfp8_cache* cache, const mxfp8_cache_batch*
 }
 
 namespace {
-mxfp4_status check_q_heads(const char* fn, const mx::CacheArgs& c, int32_t q_heads) {
+mxfp4_status check_q_heads(const char* fn, mx::AttentionArgs* a, int32_t q_heads, int32_t window) {
+  const mx::CacheArgs& c = a->c;
   if (q_heads < 1 || q_heads > 65535 || q_heads % c.heads != 0)
     return fail(MXFP4_ERR_SHAPE, "%s: q_heads (%d) must be a multiple of heads (%d), 1 to 65535", fn, q_heads, c.heads);
   if ((int64_t)c.tokens * q_heads >= (int64_t)1 << 31)
     return fail(MXFP4_ERR_SHAPE, "%s: tokens (%d) * q_heads (%d) must be below 2^31", fn, c.tokens, q_heads);
+  a->q_heads = q_heads;
+  a->group = q_heads / c.heads;
+  a->shift = c.page_tokens == 16 ? 4 : c.page_tokens == 32 ? 5 : c.page_tokens == 64 ? 6 : 7;
+  a->window = window < (1 << 30) ? window : 1 << 30;  // (no length passes it)
+  if (mx::cache_attention_units(*a) >= (int64_t)1 << 31)
+    return fail(MXFP4_ERR_SHAPE, "%s: too many tokens (%d) of %d heads over %d pages for one call", fn, c.tokens, q_heads,
+                c.max_pages);
   return MXFP4_OK;
 }
 }  // namespace
@@ -809,8 +817,7 @@ size_t mxfp8_cache_attention_workspace_size(const mxfp8_cache* cache, const mxfp
   mxfp8_cache_batch b = *batch;
   c.codes = c.scales = reinterpret_cast<uint8_t*>(16);
   b.page_table = b.lens = reinterpret_cast<const int32_t*>(16);
-  if (check_cache(fn, &c, &b, true, &a.c) || check_q_heads(fn, a.c, q_heads)) return 0;
-  a.q_heads = q_heads;
+  if (check_cache(fn, &c, &b, true, &a.c) || check_q_heads(fn, &a, q_heads, 0)) return 0;
   return (size_t)mx::cache_attention_workspace_bytes(a);
 }
 
@@ -820,21 +827,20 @@ mxfp4_status mxfp8_cache_attention(const mxfp8_cache* cache, const mxfp8_cache_b
   const char* fn = "mxfp8_cache_attention";
   mx::AttentionArgs a{};
   mxfp4_status st = check_cache(fn, cache, batch, true, &a.c);
-  if (!st) st = check_q_heads(fn, a.c, q_heads);
   if (st) return st;
   if (!params) return fail(MXFP4_ERR_INVALID_ARG, "%s: params is NULL", fn);
+  if (params->window < 0) return fail(MXFP4_ERR_INVALID_ARG, "%s: window (%d) must be >= 0", fn, params->window);
+  if ((st = check_q_heads(fn, &a, q_heads, params->window))) return st;
   if (!(params->scale >= -1.0e30f && params->scale <= 1.0e30f))
     return fail(MXFP4_ERR_INVALID_ARG, "%s: scale must be finite", fn);
   if (!(params->softcap == 0.0f || (params->softcap >= 1.0e-30f && params->softcap <= 1.0e30f)))
     return fail(MXFP4_ERR_INVALID_ARG, "%s: softcap must be 0 or a positive number", fn);
-  if (params->window < 0) return fail(MXFP4_ERR_INVALID_ARG, "%s: window (%d) must be >= 0", fn, params->window);
   if ((reinterpret_cast<uintptr_t>(params->slopes) | reinterpret_cast<uintptr_t>(lse)) & 3u)
     return fail(MXFP4_ERR_ALIGN, "%s: slopes and lse must be 4-byte aligned", fn);
   if ((st = check_heads(fn, "q", q, a.c.tokens, q_heads, a.c.head_dim, false, &a.q))) return st;
   if (q->dtype != MXFP4_DTYPE_BF16) return fail(MXFP4_ERR_INVALID_ARG, "%s: q must be bf16", fn);
   if ((st = check_heads(fn, "out", out, a.c.tokens, q_heads, a.c.head_dim, true, &a.out))) return st;
   if (!aligned16(workspace)) return fail(MXFP4_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
-  a.q_heads = q_heads;
   const size_t need = (size_t)mx::cache_attention_workspace_bytes(a);
   if (need && (!workspace || workspace_bytes < need))
     return fail(MXFP4_ERR_INVALID_ARG, "%s: workspace of %zu bytes, %zu are needed", fn, workspace ? workspace_bytes : 0,
@@ -847,7 +853,6 @@ mxfp4_status mxfp8_cache_attention(const mxfp8_cache* cache, const mxfp8_cache_b
   a.slopes = params->slopes;
   a.scale = params->scale;
   a.softcap = params->softcap;
-  a.window = params->window < (1 << 30) ? params->window : 1 << 30;  // (no length passes it)
   a.out_f32 = out->dtype == MXFP4_DTYPE_F32;
   return from_cuda(mx::launch_cache_attention(a, static_cast<cudaStream_t>(stream)), fn);
 }

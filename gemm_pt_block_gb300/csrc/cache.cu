@@ -282,10 +282,10 @@ struct Tile {
 
 struct AttnCtl {
   uint64_t full[kMostWarps][kMostStages], empty[kMostWarps][kMostStages];
-  uint16_t scales[kMostWarps][kMostStages];  // of a stage's halves
+  int32_t block[kMostWarps][kMostStages][2];  // of the keys in a stage's halves (-1: not loaded)
   Tile head[kMostWarps], open[kMostWarps];       // tiles that a warp shares with the one before it, and behind it
-  int64_t at[kMostWarps];                    // units before the first sequence of a warp's run
-  int64_t units;                         // of all sequences
+  int32_t at[kMostWarps];                    // units before the first sequence of a warp's run
+  int32_t units;                         // of all sequences
   int32_t first[kMostWarps];                 // that sequence
   int32_t left[kMostWarps];                  // units of the open tile behind a warp's run
   uint8_t has[kMostWarps];                   // kHead, kOpen, kBegan
@@ -390,11 +390,6 @@ __device__ __forceinline__ void warps_sync() {
 // 2^e for a whole e, 0 below the smallest normal number.
 __device__ __forceinline__ float pow2i(int e) { return e < -126 ? 0.0f : __uint_as_float((uint32_t)(min(e, 127) + 127) << 23); }
 
-// Whole numbers of 32 bits divide in a fraction of the time that those of 64 take.
-__device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
-  return ((x | y) >> 31) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
-}
-
 // What a call says of one sequence, as it lies in memory.
 struct Said {
   int32_t row, end, len;
@@ -413,9 +408,9 @@ struct Walk {
   int32_t row0, p0, lo, hi;  // tile: first row, its position, tokens [lo, hi) that a row attends; lo rounded down
   Said ahead;                // of sequence b + 1
 
-  // Takes sequence s, of which the call says x; its number of units.
-  __device__ __forceinline__ int64_t take(const AttentionArgs& a, int32_t s, const Said& x) {
-    const int G = a.q_heads / a.c.heads;
+  // Takes sequence s, of which the call says x; its number of units (a call's stay below 2^31).
+  __device__ __forceinline__ int32_t take(const AttentionArgs& a, int32_t s, const Said& x) {
+    const int G = a.group;
     b = s;
     row = x.row;
     n = x.end - x.row;
@@ -434,20 +429,19 @@ struct Walk {
     const int32_t tokens = (kRows + G - 2) / G + 1;  // that a tile's rows may belong to
     const int32_t span = a.window > 0 ? min(len, a.window + tokens + kChunk) : len;
     units = max(1, (span + kChunk - 1) / kChunk);
-    return (int64_t)a.c.heads * tiles * units;
+    return a.c.heads * tiles * units;
   }
-  // Unit u of sequence s, where a run begins.
-  __device__ __forceinline__ void place(const AttentionArgs& a, int32_t s, int64_t u) {
-    take(a, s, said(a.c, s));
-    ahead = said(a.c, min(s + 1, a.c.sequences - 1));
-    const int64_t t = divide(u, units);
-    unit = (int32_t)(u - t * units);
-    head = (int32_t)divide(t, tiles);
-    tile = (int32_t)(t - (int64_t)head * tiles);
+  // Unit u of the sequence, where a run begins.
+  __device__ __forceinline__ void place(const AttentionArgs& a, int32_t u) {
+    ahead = said(a.c, min(b + 1, a.c.sequences - 1));
+    const uint32_t t = (uint32_t)u / (uint32_t)units;
+    unit = u - (int32_t)t * units;
+    head = (int32_t)(t / (uint32_t)tiles);
+    tile = (int32_t)t - head * tiles;
     set_tile(a);
   }
   __device__ __forceinline__ void set_tile(const AttentionArgs& a) {
-    const int G = a.q_heads / a.c.heads;
+    const int G = a.group;
     row0 = tile * kRows;
     p0 = len - n + row0 / G;
     hi = max(0, len - n + (min(row0 + kRows, n * G) - 1) / G + 1);
@@ -480,39 +474,68 @@ struct Walk {
 // All units in equal runs, one for each warp of the CTAs that work: warp i of
 // them (CTA i / kWarps) begins at begin(i).
 struct Cut {
-  int64_t each;
-  int32_t more, ctas;  // the first `more` runs have one more
-  __device__ __forceinline__ int64_t begin(int32_t i) const { return each * i + min(i, more); }
+  int32_t each, more, ctas;  // the first `more` runs have one more
+  __device__ __forceinline__ int32_t begin(int32_t i) const { return each * i + min(i, more); }
 };
 template <int kWarps>
-__device__ __forceinline__ Cut cut(int64_t units) {
+__device__ __forceinline__ Cut cut(int32_t units) {
   Cut c;
-  c.ctas = units < (int64_t)gridDim.x * kWarps ? (int32_t)((uint32_t)(units + kWarps - 1) / (uint32_t)kWarps) : (int32_t)gridDim.x;
-  const int32_t runs = max(c.ctas, 1) * kWarps;
-  c.each = divide(units, runs);
-  c.more = (int32_t)(units - c.each * runs);
+  c.ctas = (int32_t)min(gridDim.x, ((uint32_t)units + kWarps - 1) / kWarps);
+  const uint32_t runs = (uint32_t)max(c.ctas, 1) * kWarps;
+  c.each = (int32_t)((uint32_t)units / runs);
+  c.more = units - c.each * (int32_t)runs;
   return c;
 }
 
-// Finds where the runs of this CTA's warps begin: sequence (first) and the units
-// before that sequence (at). All threads; ends with a barrier.
+// Where a warp's run begins (lanes of the fetching warp: that of warp lane % 16),
+// for up to 32 sequences: each lane looks at one. Returns the call's units.
 template <int kRows, int kWarps>
-__device__ __forceinline__ void find_starts(const AttentionArgs& a, AttnCtl* ctl, int64_t* sums) {
+__device__ __forceinline__ int32_t find_start_32(const AttentionArgs& a, int warp, int lane, Cut* runs, Walk<kRows>* w) {
+  int32_t mine = 0;
+  Walk<kRows> x{};
+  if (lane < a.c.sequences) mine = x.take(a, lane, said(a.c, lane));
+  int32_t upto = mine;
+#pragma unroll
+  for (int i = 1; i < 32; i <<= 1) {
+    const int32_t v = __shfl_up_sync(0xffffffffu, upto, i);
+    if (lane >= i) upto += v;
+  }
+  const int32_t all = __shfl_sync(0xffffffffu, upto, 31);
+  *runs = cut<kWarps>(all);
+  const int32_t begin = runs->begin(blockIdx.x * kWarps + (warp < kWarps ? warp : min(lane & 15, kWarps - 1)));
+  int32_t s = 0;  // sequences that end before
+  for (int32_t i = 0; i < a.c.sequences; ++i) s += __shfl_sync(0xffffffffu, upto, i) <= begin;
+  s = min(s, a.c.sequences - 1);
+  w->b = s;
+  w->n = __shfl_sync(0xffffffffu, x.n, s);
+  w->row = __shfl_sync(0xffffffffu, x.row, s);
+  w->len = __shfl_sync(0xffffffffu, x.len, s);
+  w->tiles = __shfl_sync(0xffffffffu, x.tiles, s);
+  w->units = __shfl_sync(0xffffffffu, x.units, s);
+  const int32_t at = begin - __shfl_sync(0xffffffffu, upto - mine, s);
+  if (w->n > 0) w->place(a, at);
+  return all;
+}
+
+// The same for any number of sequences, by all threads, into ctl: the sequence
+// (first) and the units before it (at). Ends with a barrier.
+template <int kRows, int kWarps>
+__device__ __noinline__ void find_starts(const AttentionArgs& a, AttnCtl* ctl, int32_t* sums) {
   constexpr int kThreads = (kWarps + 1) * 32;
   const int32_t B = a.c.sequences, each = (B + kThreads - 1) / kThreads;
   const int32_t s0 = min((int32_t)threadIdx.x * each, B), s1 = min(s0 + each, B);
   Walk<kRows> w;
-  int64_t mine = 0;
+  int32_t mine = 0;
   for (int32_t s = s0; s < s1; ++s) mine += w.take(a, s, said(a.c, s));
-  int64_t upto = mine;
+  int32_t upto = mine;
 #pragma unroll
   for (int i = 1; i < 32; i <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, upto, i);
+    const int32_t v = __shfl_up_sync(0xffffffffu, upto, i);
     if ((threadIdx.x & 31) >= i) upto += v;
   }
   if ((threadIdx.x & 31) == 31) sums[threadIdx.x >> 5] = upto;
   __syncthreads();
-  int64_t before = upto - mine, all = 0;
+  int32_t before = upto - mine, all = 0;
   for (int i = 0; i <= kWarps; ++i) {
     if (i < (int)(threadIdx.x >> 5)) before += sums[i];
     all += sums[i];
@@ -520,11 +543,11 @@ __device__ __forceinline__ void find_starts(const AttentionArgs& a, AttnCtl* ctl
   const Cut runs = cut<kWarps>(all);
   if (blockIdx.x < runs.ctas && mine > 0) {
     for (int i = 0; i < kWarps; ++i) {
-      const int64_t begin = runs.begin(blockIdx.x * kWarps + i);
+      const int32_t begin = runs.begin(blockIdx.x * kWarps + i);
       if (begin < before || begin >= before + mine) continue;
-      int64_t at = before;
+      int32_t at = before;
       for (int32_t s = s0; s < s1; ++s) {
-        const int64_t u = each == 1 ? mine : w.take(a, s, said(a.c, s));
+        const int32_t u = each == 1 ? mine : w.take(a, s, said(a.c, s));
         if (begin < at + u) {
           ctl->first[i] = s;
           ctl->at[i] = at;
@@ -590,44 +613,47 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
   uint8_t* base = raw + ((1024u - (ptx::smem_u32(raw) & 1023u)) & 1023u);
   float* stats = reinterpret_cast<float*>(base + kWarps * kStages * S::kStage);  // of warps' open tiles, then of their heads
   AttnCtl* ctl = reinterpret_cast<AttnCtl*>(base + kWarps * kStages * S::kStage + S::kFixed - 4096);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.q_heads / a.c.heads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.group;
   const uint32_t ring = ptx::smem_u32(base), full = ptx::smem_u32(ctl->full), empty = ptx::smem_u32(ctl->empty);
 
   ptx::launch_dependents();
-  for (int i = threadIdx.x; i < kWarps * kMostStages; i += S::kThreads) {
-    ptx::mbar_init(full + 8 * i, 1);
-    ptx::mbar_init(empty + 8 * i, 1);
+  if (warp == kWarps) {
+    for (int i = lane; i < kWarps * kMostStages; i += 32) {
+      ptx::mbar_init(full + 8 * i, 1);
+      ptx::mbar_init(empty + 8 * i, 1);
+    }
+    if (lane == 0) {
+      ctl->abort = 0;
+      ptx::prefetch_tensormap(&map);
+    }
+    ptx::fence_mbar_init();
   }
-  if (threadIdx.x == 0) {
-    ctl->abort = 0;
-    ptx::prefetch_tensormap(&map);
+  Walk<kRows> w;
+  Cut runs;
+  const bool few = a.c.sequences <= 32;
+  if (few) {
+    find_start_32<kRows, kWarps>(a, warp, lane, &runs, &w);
+    __syncthreads();
+  } else {
+    find_starts<kRows, kWarps>(a, ctl, reinterpret_cast<int32_t*>(stats));
+    runs = cut<kWarps>(ctl->units);
   }
-  ptx::fence_mbar_init();
-  find_starts<kRows, kWarps>(a, ctl, reinterpret_cast<int64_t*>(stats));
-  const Cut runs = cut<kWarps>(ctl->units);
   if (blockIdx.x >= runs.ctas) {
     if (a.ws && threadIdx.x == 0) put_at(&reinterpret_cast<Split*>(a.ws)[blockIdx.x].parts, (int32_t)0, a.ws, a.ws_bytes);
     return;
   }
-  Walk<kRows> w;
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ fetching ---
-    // Lanes i and i + 16 walk warp i's run, one for each half of its units: the
-    // table is read two units ahead, the page's scales one.
-    const int i = min(lane & 15, kWarps - 1), shift = 31 - __clz(a.c.page_tokens);
+    // Lanes i and i + 16 walk warp i's run, one for each half of its units; the
+    // table is read a unit ahead.
+    const int i = min(lane & 15, kWarps - 1);
     const bool small = a.c.page_tokens == 16;  // each half in a page of its own, by copies of its own
-    const bool owner = (lane & 15) < kWarps;
-    const int64_t begin = runs.begin(blockIdx.x * kWarps + i);
-    const int32_t units = owner ? (int32_t)(runs.begin(blockIdx.x * kWarps + i + 1) - begin) : 0;
+    const int32_t begin = runs.begin(blockIdx.x * kWarps + i);
+    const int32_t units = (lane & 15) < kWarps ? runs.begin(blockIdx.x * kWarps + i + 1) - begin : 0;
     const int32_t rounds = __reduce_max_sync(0xffffffffu, units);
     struct Page {
       int32_t page, head, place;  // page: -1 a wrong one, -2 none to load
-      bool live;
-    };
-    struct Block {
-      int32_t block, place;  // block of the keys (-1: none to load)
-      uint32_t keys, values;
       bool live;
     };
     auto page_at = [&]() {
@@ -635,49 +661,34 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
       const int32_t j = w.token() + (lane & 16);
       if (j < w.hi) {
         x.place = (j & (a.c.page_tokens - 1)) >> 4;
-        x.page = j >> shift < a.c.max_pages ? __ldg(a.c.table + (int64_t)w.b * a.c.ld_table + (j >> shift)) : -1;
+        x.page = j >> a.shift < a.c.max_pages ? __ldg(a.c.table + (int64_t)w.b * a.c.ld_table + (j >> a.shift)) : -1;
       }
       return x;
     };
-    auto block_of = [&](const Page& x) {
-      Block y{-1, x.place, 255u, 255u, x.live};
-      if (x.page >= 0 && x.page < a.c.pages) {
-        y.block = x.page * 2 * a.c.heads + x.head;
-        y.keys = __ldg(a.c.scales + y.block);
-        y.values = __ldg(a.c.scales + (int64_t)y.block + a.c.heads);
-      } else if (x.page != -2) {
-        index_fail();
-      }
-      return y;
-    };
-    Page p1{-2, 0, 0, false};
-    Block b1{-1, 0, 255u, 255u, false};
-    int32_t r = 0;  // units walked
+    Page ahead{-2, 0, 0, false};
     if (units > 0) {
-      w.place(a, ctl->first[i], begin - ctl->at[i]);
-      b1 = block_of(page_at());
-      if (units > 1) {
-        w.next(a);
-        p1 = page_at();
+      if (!few) {
+        w.take(a, ctl->first[i], said(a.c, ctl->first[i]));
+        w.place(a, begin - ctl->at[i]);
       }
-      r = 2;
+      ahead = page_at();
     }
     const uint32_t my_ring = ring + i * kStages * S::kStage, my_full = full + 8 * kMostStages * i, my_empty = empty + 8 * kMostStages * i;
     int32_t tiles = 0, stage = 0;
     uint32_t parity = 1;  // of the stage's reader
     bool go = true;
     for (int32_t round = 0; round < rounds && go; ++round) {
-      const Block now = b1;
-      b1 = Block{-1, 0, 255u, 255u, false};
-      if (round + 1 < units) b1 = block_of(p1);
-      if (r < units) {
+      const Page now = ahead;
+      if (round + 1 < units) {
         w.next(a);
-        p1 = page_at();
-        ++r;
+        ahead = page_at();
       }
-      const int32_t other = __shfl_down_sync(0xffffffffu, now.block, 16);
-      const uint32_t keys = now.keys | __shfl_down_sync(0xffffffffu, now.keys, 16) << 8;
-      const uint32_t values = now.values | __shfl_down_sync(0xffffffffu, now.values, 16) << 8;
+      int32_t block = -1;
+      if (now.page >= 0 && now.page < a.c.pages)
+        block = now.page * 2 * a.c.heads + now.head;
+      else if (now.page != -2)
+        index_fail();
+      const int32_t other = __shfl_down_sync(0xffffffffu, block, 16);
       const bool mine = lane < 16 && round < units && now.live;
 #pragma unroll
       for (int kind = 0; kind < 2; ++kind) {
@@ -685,9 +696,9 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
         if (mine && go) {
           const uint32_t bar = my_full + 8 * stage, to = my_ring + stage * S::kStage;
           const int32_t skip = kind ? a.c.heads : 0;
-          ctl->scales[i][stage] = (uint16_t)(kind ? values : keys);
-          ptx::mbar_arrive_expect_tx(bar, (now.block >= 0 ? (small ? 1 : 2) * S::kHalf : 0) + (small && other >= 0 ? S::kHalf : 0));
-          if (now.block >= 0) tma_pages(to, &map, now.place, now.block + skip, bar);
+          if (kind == 0) *reinterpret_cast<int2*>(ctl->block[i][stage]) = make_int2(block, other);
+          ptx::mbar_arrive_expect_tx(bar, (block >= 0 ? (small ? 1 : 2) * S::kHalf : 0) + (small && other >= 0 ? S::kHalf : 0));
+          if (block >= 0) tma_pages(to, &map, now.place, block + skip, bar);
           if (small && other >= 0) tma_pages(to + S::kHalf, &map, 0, other + skip, bar);
           ++tiles;
           if (++stage == kStages) {
@@ -741,9 +752,12 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
   uint32_t parity = 0;
   bool go = true;
   uint8_t has = 0;
-  const int64_t begin = runs.begin(blockIdx.x * kWarps + warp);
-  const int32_t units = (int32_t)(runs.begin(blockIdx.x * kWarps + warp + 1) - begin);
-  if (units) w.place(a, ctl->first[warp], begin - ctl->at[warp]);
+  const int32_t begin = runs.begin(blockIdx.x * kWarps + warp);
+  const int32_t units = runs.begin(blockIdx.x * kWarps + warp + 1) - begin;
+  if (units && !few) {
+    w.take(a, ctl->first[warp], said(a.c, ctl->first[warp]));
+    w.place(a, begin - ctl->at[warp]);
+  }
 
   for (int32_t u = 0; u < units; ++u) {
     if (u == 0 || w.unit == 0) {
@@ -792,7 +806,10 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
     if (w.live() && go) go = wait_bar_warp(my_full + 8 * stage, parity, &ctl->abort);
     if (w.live() && go) {
       const int32_t c0 = w.token();
-      const uint32_t keys = ctl->scales[warp][stage];
+      // scales: keys of the two halves (lanes 0, 1 of four), then values
+      const int32_t block = ctl->block[warp][stage][lane & 1];
+      uint32_t scale = 255u;
+      if (block >= 0) scale = __ldg(a.c.scales + block + (lane & 2 ? a.c.heads : 0));
       float s[2][NT][4];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -826,7 +843,7 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
       const bool whole = c0 + kChunk <= w.p0 + 1 && (a.window == 0 || c0 > w.hi - 1 - a.window);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float ks = scale_value((keys >> (8 * h)) & 0xFFu);
+        const float ks = scale_value(__shfl_sync(0xffffffffu, scale, h));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -854,11 +871,10 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
       }
 
       if (go) go = wait_bar_warp(my_full + 8 * stage, parity, &ctl->abort);
-      const uint32_t values = ctl->scales[warp][stage];
       float ev[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t vs = (values >> (8 * h)) & 0xFFu;
+        const uint32_t vs = __shfl_sync(0xffffffffu, scale, 2 + h);
         ev[h] = vs == 255u ? __uint_as_float(0x7FC00000u) : (float)((int)vs - 127);
       }
       if (c0 + kChunk > w.hi) {
@@ -875,7 +891,7 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
       }
 
       // running maxima, and the weights
-      const bool one = (values & 0xFFu) == values >> 8;  // both halves' values under one scale
+      const bool one = ev[0] == ev[1];  // both halves' values under one scale
       uint32_t pf[2][NT][2], pl[2][NT][2];
       bool moved = false;
       float keep[NT][2];
@@ -1139,7 +1155,7 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
     const Group x = group(ended);
     if (groups > ended && !x.before) {
       // the CTAs up to the tile's last unit
-      const int64_t at = runs.begin((blockIdx.x + 1) * kWarps) - 1 + ctl->left[31 - __clz(open_in)];
+      const int32_t at = runs.begin((blockIdx.x + 1) * kWarps) - 1 + ctl->left[31 - __clz(open_in)];
       int32_t c = blockIdx.x + 1;
       while (c < runs.ctas && runs.begin(c * kWarps) <= at) ++c;
       sp.tile = ctl->open[x.first];
@@ -1163,7 +1179,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   ptx::wait_prior_grid();
   const Split sp = reinterpret_cast<const Split*>(a.ws)[blockIdx.x];
   if (sp.parts == 0) return;
-  const int G = a.q_heads / a.c.heads;
+  const int G = a.group;
   // part 0 is this CTA's second, the others the first of the CTAs behind it
   const float* parts = a.ws + gridDim.x * (sizeof(Split) / 4) + 2 * (int64_t)blockIdx.x * part_floats(kRows, D);
   auto part = [&](int i) { return parts + (2 * i + (i == 0)) * part_floats(kRows, D); };
@@ -1262,6 +1278,7 @@ namespace {
 struct AttnShape {
   int nt, warps, ctas;
   bool split;
+  int64_t units;  // at most
 };
 // Sixteen rows to a tile where a sequence has more than eight on average (their
 // products come at half the loads); heads above 128 channels keep to eight, whose
@@ -1278,6 +1295,7 @@ AttnShape attn_shape(const AttentionArgs& a) {
   const int64_t units = (span + kChunk - 1) / kChunk, all = tiles * a.c.heads * units, ctas = (all + s.warps - 1) / s.warps;
   s.ctas = (int)(ctas < kSms ? ctas : kSms);
   s.split = units > 1;
+  s.units = all;
   return s;
 }
 
@@ -1336,6 +1354,8 @@ cudaError_t attend(const AttentionArgs& a, const AttnShape& sh, cudaStream_t st)
   return a.out_f32 ? attend<D, NT, true>(a, sh, st) : attend<D, NT, false>(a, sh, st);
 }
 }  // namespace
+
+int64_t cache_attention_units(const AttentionArgs& a) { return attn_shape(a).units; }
 
 int64_t cache_attention_workspace_bytes(const AttentionArgs& a) {
   const AttnShape s = attn_shape(a);

@@ -134,6 +134,7 @@ struct AttentionArgs {
   uint64_t ws_bytes, lse_bytes;
   float scale, softcap;
   int32_t q_heads, window;
+  int32_t group, shift;  // query heads to a head of the cache; page_tokens = 1 << shift
   bool out_f32;
 };
 
@@ -182,6 +183,8 @@ cudaError_t launch_cache_append(const CacheArgs& c, const Heads& k, const Heads&
 cudaError_t launch_cache_read(const CacheArgs& c, const Heads& k, const Heads& v, bool f32, cudaStream_t st);
 cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t st);
 int64_t cache_attention_workspace_bytes(const AttentionArgs& a);
+// Units of work that a call may have; launch_cache_attention takes fewer than 2^31.
+int64_t cache_attention_units(const AttentionArgs& a);
 // Each reads and clears the device error word of its translation unit.
 cudaError_t read_quant_error(uint32_t* err);
 cudaError_t read_ffn_error(uint32_t* err);
