@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(1024) cache_read_kernel(CacheArgs c, Heads k, 
 // denominator and m + lift, lift = max (s_j - m + ev_j), for the numerator, whose
 // weights are then at most one whatever the pages' scales are.
 //
-// The work is cut into units of 32 tokens of one sequence, one head of the cache
+// The work is cut into units of 32 or 64 tokens of one sequence, one head of the cache
 // and one tile of query rows (the rows of the query heads that share the head,
 // over the sequence's new tokens), and every warp of the GPU takes an equal run of
 // them, whatever the lengths: eight warps of a CTA an SM that multiply, and a
@@ -252,7 +252,6 @@ __global__ void __launch_bounds__(1024) cache_read_kernel(CacheArgs c, Heads k, 
 // the workspace for cache_join_kernel.
 
 constexpr int kSms = 152;
-constexpr int kChunk = 32;                      // tokens of a unit
 constexpr float kTop = 15.0f;                   // weights are held times 2^15: f16 keeps 2^-39 of the largest
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr int kMostWarps = 15, kMostStages = 8;
@@ -265,10 +264,12 @@ struct Attn {
   static constexpr int kThreads = (kWarps + 1) * 32;
   static constexpr int kRows = 8 * NT;
   static constexpr int kBox = D % 128 == 0 ? 128 : D % 64 == 0 ? 64 : 32;  // bytes of a row in one swizzled slab
-  static constexpr int kHalf = 16 * D;                                     // 16 tokens of keys or values
-  static constexpr int kStage = 2 * kHalf;                                 // 32 tokens of keys or values
+  static constexpr int kChunk = D == 64 ? 64 : 32;                         // tokens of a unit, in parts of 16
+  static constexpr int kParts = kChunk / 16;
+  static constexpr int kPart = 16 * D;                                     // a part's keys or values
+  static constexpr int kStage = kChunk * D;                                // a unit's
   static constexpr int kQuads = D / 16 * NT * 32;                          // of a tile's sums (below)
-  static constexpr int kFixed = 2 * kWarps * 3 * kRows * 4 + 4096;
+  static constexpr int kFixed = 2 * kWarps * 3 * kRows * 4 + 5120;
   static constexpr int kFit = (227 * 1024 - 1024 - kFixed) / (kWarps * kStage);
   static constexpr int kStages = kFit < kMostStages ? kFit : kMostStages;  // of a warp's ring
   static constexpr int kBytes = 1024 + kWarps * kStages * kStage + kFixed;
@@ -280,18 +281,22 @@ struct Tile {
   int32_t token, row0, rows, head;
 };
 
+// Where a run begins: its sequence, as Walk has it, and the unit in that.
+struct Start {
+  int32_t b, n, row, len, tiles, units, at, unused;
+};
+
 struct AttnCtl {
   uint64_t full[kMostWarps][kMostStages], empty[kMostWarps][kMostStages];
-  int32_t block[kMostWarps][kMostStages][2];  // of the keys in a stage's halves (-1: not loaded)
+  int32_t block[kMostWarps][kMostStages][4];  // of the keys in a stage's parts (-1: none)
   Tile head[kMostWarps], open[kMostWarps];       // tiles that a warp shares with the one before it, and behind it
-  int32_t at[kMostWarps];                    // units before the first sequence of a warp's run
   int32_t units;                         // of all sequences
-  int32_t first[kMostWarps];                 // that sequence
+  Start start[kMostWarps];               // of the warps' runs
   int32_t left[kMostWarps];                  // units of the open tile behind a warp's run
   uint8_t has[kMostWarps];                   // kHead, kOpen, kBegan
   uint32_t abort;
 };
-static_assert(sizeof(AttnCtl) <= 4096, "control block");
+static_assert(sizeof(AttnCtl) <= 5120, "control block");
 // A warp's run ended a tile that began before it; it ends inside a tile; that tile began before it.
 enum : uint8_t { kHead = 1, kOpen = 2, kBegan = 4 };
 
@@ -399,9 +404,9 @@ __device__ __forceinline__ Said said(const CacheArgs& c, int32_t b) {
 }
 
 // A place in the order of all units: sequences, their heads, their tiles of
-// kRows query rows, 32 tokens at a time. A sequence's tiles count alike (the
+// kRows query rows, kChunk tokens at a time. A sequence's tiles count alike (the
 // longest's units): units that a tile has no tokens for are passed over.
-template <int kRows>
+template <int kRows, int kChunk>
 struct Walk {
   int32_t b, n, row, len, tiles, units;  // sequence: rows, first row, length, tiles, units of each
   int32_t head, tile, unit;
@@ -439,6 +444,15 @@ struct Walk {
     head = (int32_t)(t / (uint32_t)tiles);
     tile = (int32_t)t - head * tiles;
     set_tile(a);
+  }
+  __device__ __forceinline__ void begin(const AttentionArgs& a, const Start& x) {
+    b = x.b;
+    n = x.n;
+    row = x.row;
+    len = x.len;
+    tiles = x.tiles;
+    units = x.units;
+    place(a, x.at);
   }
   __device__ __forceinline__ void set_tile(const AttentionArgs& a) {
     const int G = a.group;
@@ -489,10 +503,11 @@ __device__ __forceinline__ Cut cut(int32_t units) {
 
 // Where a warp's run begins (lanes of the fetching warp: that of warp lane % 16),
 // for up to 32 sequences: each lane looks at one. Returns the call's units.
-template <int kRows, int kWarps>
-__device__ __forceinline__ int32_t find_start_32(const AttentionArgs& a, int warp, int lane, Cut* runs, Walk<kRows>* w) {
+template <int kRows, int kChunk, int kWarps>
+__device__ __forceinline__ int32_t find_start_32(const AttentionArgs& a, int warp, int lane, Cut* runs,
+                                                 Walk<kRows, kChunk>* w) {
   int32_t mine = 0;
-  Walk<kRows> x{};
+  Walk<kRows, kChunk> x{};
   if (lane < a.c.sequences) mine = x.take(a, lane, said(a.c, lane));
   int32_t upto = mine;
 #pragma unroll
@@ -517,14 +532,13 @@ __device__ __forceinline__ int32_t find_start_32(const AttentionArgs& a, int war
   return all;
 }
 
-// The same for any number of sequences, by all threads, into ctl: the sequence
-// (first) and the units before it (at). Ends with a barrier.
-template <int kRows, int kWarps>
+// The same for any number of sequences, by all threads, into ctl. Ends with a barrier.
+template <int kRows, int kChunk, int kWarps>
 __device__ __noinline__ void find_starts(const AttentionArgs& a, AttnCtl* ctl, int32_t* sums) {
   constexpr int kThreads = (kWarps + 1) * 32;
   const int32_t B = a.c.sequences, each = (B + kThreads - 1) / kThreads;
   const int32_t s0 = min((int32_t)threadIdx.x * each, B), s1 = min(s0 + each, B);
-  Walk<kRows> w;
+  Walk<kRows, kChunk> w;
   int32_t mine = 0;
   for (int32_t s = s0; s < s1; ++s) mine += w.take(a, s, said(a.c, s));
   int32_t upto = mine;
@@ -549,8 +563,7 @@ __device__ __noinline__ void find_starts(const AttentionArgs& a, AttnCtl* ctl, i
       for (int32_t s = s0; s < s1; ++s) {
         const int32_t u = each == 1 ? mine : w.take(a, s, said(a.c, s));
         if (begin < at + u) {
-          ctl->first[i] = s;
-          ctl->at[i] = at;
+          ctl->start[i] = Start{s, w.n, w.row, w.len, w.tiles, w.units, begin - at, 0};
           break;
         }
         at += u;
@@ -608,11 +621,12 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
     cache_attention_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ AttentionArgs a) {
   using S = Attn<D, NT>;
   constexpr int kWarps = S::kWarps, kRows = S::kRows, kSegs = D / 16, kStages = S::kStages, kStat = 3 * kRows;
+  constexpr int kChunk = S::kChunk, kParts = S::kParts;
   constexpr int kIn = S::kBox / 16;  // segments of 16 channels in a slab
   extern __shared__ uint8_t raw[];
   uint8_t* base = raw + ((1024u - (ptx::smem_u32(raw) & 1023u)) & 1023u);
   float* stats = reinterpret_cast<float*>(base + kWarps * kStages * S::kStage);  // of warps' open tiles, then of their heads
-  AttnCtl* ctl = reinterpret_cast<AttnCtl*>(base + kWarps * kStages * S::kStage + S::kFixed - 4096);
+  AttnCtl* ctl = reinterpret_cast<AttnCtl*>(base + kWarps * kStages * S::kStage + S::kFixed - 5120);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.group;
   const uint32_t ring = ptx::smem_u32(base), full = ptx::smem_u32(ctl->full), empty = ptx::smem_u32(ctl->empty);
 
@@ -628,14 +642,14 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
     }
     ptx::fence_mbar_init();
   }
-  Walk<kRows> w;
+  Walk<kRows, kChunk> w;
   Cut runs;
   const bool few = a.c.sequences <= 32;
   if (few) {
-    find_start_32<kRows, kWarps>(a, warp, lane, &runs, &w);
+    find_start_32<kRows, kChunk, kWarps>(a, warp, lane, &runs, &w);
     __syncthreads();
   } else {
-    find_starts<kRows, kWarps>(a, ctl, reinterpret_cast<int32_t*>(stats));
+    find_starts<kRows, kChunk, kWarps>(a, ctl, reinterpret_cast<int32_t*>(stats));
     runs = cut<kWarps>(ctl->units);
   }
   if (blockIdx.x >= runs.ctas) {
@@ -645,61 +659,76 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ fetching ---
-    // Lanes i and i + 16 walk warp i's run, one for each half of its units; the
-    // table is read a unit ahead.
+    // Lanes i and i + 16 walk warp i's run and fetch half of its units' parts each;
+    // the table is read a unit ahead. A copy is of a page's tokens, or a unit's.
     const int i = min(lane & 15, kWarps - 1);
-    const bool small = a.c.page_tokens == 16;  // each half in a page of its own, by copies of its own
-    const int32_t begin = runs.begin(blockIdx.x * kWarps + i);
-    const int32_t units = (lane & 15) < kWarps ? runs.begin(blockIdx.x * kWarps + i + 1) - begin : 0;
+    const int32_t units =
+        (lane & 15) < kWarps ? runs.begin(blockIdx.x * kWarps + i + 1) - runs.begin(blockIdx.x * kWarps + i) : 0;
     const int32_t rounds = __reduce_max_sync(0xffffffffu, units);
-    struct Page {
-      int32_t page, head, place;  // page: -1 a wrong one, -2 none to load
+    constexpr int kMine = kParts / 2;
+    const int copy = min(a.c.page_tokens, kChunk), from = (lane >> 4) * kMine;
+    struct Pages {
+      int32_t page[kMine], head, place;  // page: -1 a wrong one, -2 none to load; place of the first in it
       bool live;
     };
-    auto page_at = [&]() {
-      Page x{-2, w.head, 0, w.live()};
-      const int32_t j = w.token() + (lane & 16);
-      if (j < w.hi) {
-        x.place = (j & (a.c.page_tokens - 1)) >> 4;
-        x.page = j >> a.shift < a.c.max_pages ? __ldg(a.c.table + (int64_t)w.b * a.c.ld_table + (j >> a.shift)) : -1;
+    auto pages_at = [&]() {
+      Pages x;
+      x.head = w.head;
+      x.live = w.live();
+      const int32_t j0 = w.token() + 16 * from;
+      x.place = (j0 & (a.c.page_tokens - 1)) >> 4;
+#pragma unroll
+      for (int q = 0; q < kMine; ++q) {
+        const int32_t j = j0 + 16 * q;
+        x.page[q] = -2;
+        if (j < w.hi) x.page[q] = j >> a.shift < a.c.max_pages ? __ldg(a.c.table + (int64_t)w.b * a.c.ld_table + (j >> a.shift)) : -1;
       }
       return x;
     };
-    Page ahead{-2, 0, 0, false};
+    Pages ahead{};
     if (units > 0) {
-      if (!few) {
-        w.take(a, ctl->first[i], said(a.c, ctl->first[i]));
-        w.place(a, begin - ctl->at[i]);
-      }
-      ahead = page_at();
+      if (!few) w.begin(a, ctl->start[i]);
+      ahead = pages_at();
     }
     const uint32_t my_ring = ring + i * kStages * S::kStage, my_full = full + 8 * kMostStages * i, my_empty = empty + 8 * kMostStages * i;
     int32_t tiles = 0, stage = 0;
     uint32_t parity = 1;  // of the stage's reader
     bool go = true;
     for (int32_t round = 0; round < rounds && go; ++round) {
-      const Page now = ahead;
+      const Pages now = ahead;
       if (round + 1 < units) {
         w.next(a);
-        ahead = page_at();
+        ahead = pages_at();
       }
-      int32_t block = -1;
-      if (now.page >= 0 && now.page < a.c.pages)
-        block = now.page * 2 * a.c.heads + now.head;
-      else if (now.page != -2)
-        index_fail();
-      const int32_t other = __shfl_down_sync(0xffffffffu, block, 16);
-      const bool mine = lane < 16 && round < units && now.live;
+      const bool mine = round < units && now.live;
+      int32_t block[kMine], bytes = 0;
+#pragma unroll
+      for (int q = 0; q < kMine; ++q) {
+        block[q] = -1;
+        if (!mine) continue;
+        if (now.page[q] >= 0 && now.page[q] < a.c.pages)
+          block[q] = now.page[q] * 2 * a.c.heads + now.head;
+        else if (now.page[q] != -2)
+          index_fail();
+        if (block[q] >= 0 && (16 * (from + q) & (copy - 1)) == 0) bytes += copy * D;
+      }
+      bytes += __shfl_down_sync(0xffffffffu, bytes, 16);
 #pragma unroll
       for (int kind = 0; kind < 2; ++kind) {
         go = go && wait_bars(my_empty + 8 * stage, parity, mine && tiles >= kStages, &ctl->abort);
+        if (kind == 0 && mine && go) {
+#pragma unroll
+          for (int q = 0; q < kMine; ++q) ctl->block[i][stage][from + q] = block[q];
+        }
+        __syncwarp();
         if (mine && go) {
           const uint32_t bar = my_full + 8 * stage, to = my_ring + stage * S::kStage;
-          const int32_t skip = kind ? a.c.heads : 0;
-          if (kind == 0) *reinterpret_cast<int2*>(ctl->block[i][stage]) = make_int2(block, other);
-          ptx::mbar_arrive_expect_tx(bar, (block >= 0 ? (small ? 1 : 2) * S::kHalf : 0) + (small && other >= 0 ? S::kHalf : 0));
-          if (block >= 0) tma_pages(to, &map, now.place, block + skip, bar);
-          if (small && other >= 0) tma_pages(to + S::kHalf, &map, 0, other + skip, bar);
+          if (lane < 16) ptx::mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+          for (int q = 0; q < kMine; ++q)
+            if (block[q] >= 0 && (16 * (from + q) & (copy - 1)) == 0)
+              tma_pages(to + (from + q) * S::kPart, &map, (now.place + q) & ((a.c.page_tokens >> 4) - 1),
+                        block[q] + (kind ? a.c.heads : 0), bar);
           ++tiles;
           if (++stage == kStages) {
             stage = 0;
@@ -721,11 +750,11 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
 
   // ----------------------------------------------------------- multiplying ---
   const int g = lane >> 2, t = lane & 3;
-  // ldmatrix rows: matrix lane / 8 holds tokens 8 (m % 2) .. of half m / 2
+  // ldmatrix rows: matrix lane / 8 holds tokens 8 (m % 2) .. of part m / 2 of two
   const int mrow = ((lane >> 3) & 1) * 8 + (lane & 7);
   const uint32_t swz = S::kBox == 128 ? mrow & 7 : S::kBox == 64 ? (mrow >> 1) & 3 : (mrow >> 2) & 1;
   const uint32_t my_ring = ring + warp * kStages * S::kStage;
-  const uint32_t lane_at = my_ring + (lane >> 4) * S::kHalf + mrow * S::kBox + (swz << 4);
+  const uint32_t lane_at = my_ring + (lane >> 4) * S::kPart + mrow * S::kBox + (swz << 4);
   const uint32_t my_full = full + 8 * kMostStages * warp, my_empty = empty + 8 * kMostStages * warp;
   const float scale2 = a.scale * 1.44269504088896f, cap = a.softcap > 0.0f ? a.scale / a.softcap : 0.0f;
   float* heads = a.ws + gridDim.x * (sizeof(Split) / 4 + 2 * part_floats(kRows, D));  // (used with a workspace only)
@@ -752,12 +781,8 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
   uint32_t parity = 0;
   bool go = true;
   uint8_t has = 0;
-  const int32_t begin = runs.begin(blockIdx.x * kWarps + warp);
-  const int32_t units = runs.begin(blockIdx.x * kWarps + warp + 1) - begin;
-  if (units && !few) {
-    w.take(a, ctl->first[warp], said(a.c, ctl->first[warp]));
-    w.place(a, begin - ctl->at[warp]);
-  }
+  const int32_t units = runs.begin(blockIdx.x * kWarps + warp + 1) - runs.begin(blockIdx.x * kWarps + warp);
+  if (units && !few) w.begin(a, ctl->start[warp]);
 
   for (int32_t u = 0; u < units; ++u) {
     if (u == 0 || w.unit == 0) {
@@ -806,13 +831,13 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
     if (w.live() && go) go = wait_bar_warp(my_full + 8 * stage, parity, &ctl->abort);
     if (w.live() && go) {
       const int32_t c0 = w.token();
-      // scales: keys of the two halves (lanes 0, 1 of four), then values
-      const int32_t block = ctl->block[warp][stage][lane & 1];
+      // scales: a lane a part, the keys', then the values'
+      const int32_t block = ctl->block[warp][stage][lane % kParts];
       uint32_t scale = 255u;
-      if (block >= 0) scale = __ldg(a.c.scales + block + (lane & 2 ? a.c.heads : 0));
-      float s[2][NT][4];
+      if (block >= 0) scale = __ldg(a.c.scales + block + (lane & kParts ? a.c.heads : 0));
+      float s[kParts][NT][4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < kParts; ++h)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -821,14 +846,17 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
         const uint32_t at = lane_at + stage * S::kStage;
 #pragma unroll
         for (int i = 0; i < kSegs; ++i) {
-          uint32_t r[4];
-          ldsm((at ^ ((i % kIn) << 4)) + (i / kIn) * 16 * S::kBox, r);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t a0 = e4m3x2_f16x2(r[2 * h]), a2 = e4m3x2_f16x2(r[2 * h] >> 16);
-            const uint32_t a1 = e4m3x2_f16x2(r[2 * h + 1]), a3 = e4m3x2_f16x2(r[2 * h + 1] >> 16);
+          for (int h = 0; h < kParts; h += 2) {
+            uint32_t r[4];
+            ldsm((at ^ ((i % kIn) << 4)) + (i / kIn) * 16 * S::kBox + h * S::kPart, r);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma(s[h][nt], a0, a1, a2, a3, qf[i][nt][0], qf[i][nt][1]);
+            for (int z = 0; z < 2; ++z) {
+              const uint32_t a0 = e4m3x2_f16x2(r[2 * z]), a2 = e4m3x2_f16x2(r[2 * z] >> 16);
+              const uint32_t a1 = e4m3x2_f16x2(r[2 * z + 1]), a3 = e4m3x2_f16x2(r[2 * z + 1] >> 16);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma(s[h + z][nt], a0, a1, a2, a3, qf[i][nt][0], qf[i][nt][1]);
+            }
           }
         }
         __syncwarp();
@@ -842,7 +870,7 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
       // scores in log2 units; -infinity where a row does not attend
       const bool whole = c0 + kChunk <= w.p0 + 1 && (a.window == 0 || c0 > w.hi - 1 - a.window);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < kParts; ++h) {
         const float ks = scale_value(__shfl_sync(0xffffffffu, scale, h));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -871,18 +899,20 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
       }
 
       if (go) go = wait_bar_warp(my_full + 8 * stage, parity, &ctl->abort);
-      float ev[2];
+      float ev[kParts];
+      bool one = true;  // all values under one scale
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t vs = __shfl_sync(0xffffffffu, scale, 2 + h);
+      for (int h = 0; h < kParts; ++h) {
+        const uint32_t vs = __shfl_sync(0xffffffffu, scale, kParts + h);
         ev[h] = vs == 255u ? __uint_as_float(0x7FC00000u) : (float)((int)vs - 127);
+        one = one && ev[h] == ev[0];
       }
       if (c0 + kChunk > w.hi) {
         // tokens behind the last: whatever lies there must not meet a weight of zero
         const int first = w.hi - c0;
         for (int i = lane; i < (kChunk - first) * kSegs; i += 32) {
           const int r = first + i / kSegs, seg = i % kSegs;
-          const uint32_t at = my_ring + stage * S::kStage + (r >> 4) * S::kHalf + (seg / kIn) * 16 * S::kBox +
+          const uint32_t at = my_ring + stage * S::kStage + (r >> 4) * S::kPart + (seg / kIn) * 16 * S::kBox +
                               (r & 15) * S::kBox + (seg % kIn) * 16;
           asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
         }
@@ -891,8 +921,7 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
       }
 
       // running maxima, and the weights
-      const bool one = ev[0] == ev[1];  // both halves' values under one scale
-      uint32_t pf[2][NT][2], pl[2][NT][2];
+      uint32_t pf[kParts][NT][2], pl[kParts][NT][2];
       bool moved = false;
       float keep[NT][2];
 #pragma unroll
@@ -900,14 +929,20 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
         float cm[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float h0 = fmaxf(s[0][nt][i], s[0][nt][i + 2]), h1 = fmaxf(s[1][nt][i], s[1][nt][i + 2]);
-          float x = fmaxf(h0, h1);
+          float part[kParts], x = -INFINITY;
+#pragma unroll
+          for (int h = 0; h < kParts; ++h) {
+            part[h] = fmaxf(s[h][nt][i], s[h][nt][i + 2]);
+            x = fmaxf(x, part[h]);
+          }
 #pragma unroll
           for (int z = 4; z < 32; z <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, z));
           cm[i] = fmaxf(m[nt][i], x);
           float y = x - cm[i] + ev[0];
           if (!one) {
-            y = fmaxf(h0 - cm[i] + ev[0], h1 - cm[i] + ev[1]);
+            y = -INFINITY;
+#pragma unroll
+            for (int h = 0; h < kParts; ++h) y = fmaxf(y, part[h] - cm[i] + ev[h]);
 #pragma unroll
             for (int z = 4; z < 32; z <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, z));
           }
@@ -919,7 +954,7 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
           lift[nt][i] = now;
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < kParts; ++h) {
           const float c[2] = {ev[h] + kTop - lift[nt][0], ev[h] + kTop - lift[nt][1]};
           float p[4];
 #pragma unroll
@@ -954,17 +989,20 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
       const uint32_t at = lane_at + stage * S::kStage;
 #pragma unroll
       for (int i = 0; i < kSegs; ++i) {
-        uint32_t r[4];
-        ldsm_t((at ^ ((i % kIn) << 4)) + (i / kIn) * 16 * S::kBox, r);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          // two tokens of a channel side by side, the even channel below
-          const uint32_t x = __byte_perm(r[2 * h], 0, 0x3120), y = __byte_perm(r[2 * h + 1], 0, 0x3120);
-          const uint32_t a0 = e4m3x2_f16x2(x), a1 = e4m3x2_f16x2(x >> 16), a2 = e4m3x2_f16x2(y), a3 = e4m3x2_f16x2(y >> 16);
+        for (int h = 0; h < kParts; h += 2) {
+          uint32_t r[4];
+          ldsm_t((at ^ ((i % kIn) << 4)) + (i / kIn) * 16 * S::kBox + h * S::kPart, r);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma(o[i][nt], a0, a1, a2, a3, pf[h][nt][0], pf[h][nt][1]);
-            if (kExact) mma(o[i][nt], a0, a1, a2, a3, pl[h][nt][0], pl[h][nt][1]);
+          for (int z = 0; z < 2; ++z) {
+            // two tokens of a channel side by side, the even channel below
+            const uint32_t x = __byte_perm(r[2 * z], 0, 0x3120), y = __byte_perm(r[2 * z + 1], 0, 0x3120);
+            const uint32_t a0 = e4m3x2_f16x2(x), a1 = e4m3x2_f16x2(x >> 16), a2 = e4m3x2_f16x2(y), a3 = e4m3x2_f16x2(y >> 16);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma(o[i][nt], a0, a1, a2, a3, pf[h + z][nt][0], pf[h + z][nt][1]);
+              if (kExact) mma(o[i][nt], a0, a1, a2, a3, pl[h + z][nt][0], pl[h + z][nt][1]);
+            }
           }
         }
       }
@@ -1093,34 +1131,39 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
   auto part_of = [&](const Group& x) {
     return a.ws + gridDim.x * (sizeof(Split) / 4) + (2 * (int64_t)blockIdx.x + !x.before) * part_floats(kRows, D);
   };
-  for (int i = threadIdx.x; i < groups * kRows; i += kWarps * 32) {
+  // a warp for a row of a group, a lane for a member
+  for (int i = warp; i < groups * kRows; i += kWarps) {
     const Group x = group(i / kRows);
-    const int r = i % kRows;
-    Joined j = {kLowest, -INFINITY, 0.0f};
-    for (int z = x.first; z <= x.last; ++z) j.m = fmaxf(j.m, stats[stat(x, z) + r]);
-    for (int z = x.first; z <= x.last; ++z) {
-      const float* st = stats + stat(x, z) + r;
-      const float down = st[0] - j.m;
-      j.lift = fmaxf(j.lift, down + st[kRows]);
-      j.sum += st[2 * kRows] * ex2(down);
+    const int r = i % kRows, z = min(x.first + lane, x.last);
+    const bool some = x.first + lane <= x.last;
+    float* st = stats + stat(x, z) + r;
+    const float mine = some ? st[0] : kLowest, high = some ? st[kRows] : 0.0f;
+    Joined j = {mine, 0.0f, some ? st[2 * kRows] : 0.0f};
+#pragma unroll
+    for (int d = 16; d; d >>= 1) j.m = fmaxf(j.m, __shfl_xor_sync(0xffffffffu, j.m, d));
+    const float down = mine - j.m;
+    j.lift = down + high;
+    j.sum *= ex2(down);
+#pragma unroll
+    for (int d = 8; d; d >>= 1) {
+      j.lift = fmaxf(j.lift, __shfl_xor_sync(0xffffffffu, j.lift, d));
+      j.sum += __shfl_xor_sync(0xffffffffu, j.sum, d);
     }
-    for (int z = x.first; z <= x.last; ++z) {
-      // (a member's maximum has done its part: its factor takes the place)
-      float* st = stats + stat(x, z) + r;
-      st[0] = ex2(st[0] - j.m + st[kRows] - j.lift);
-    }
-    float* st = stats + stat(x, x.last) + r;
-    if (x.closed && !x.before) {
-      const float2 k = last_factors(j.lift, j.sum);
-      st[kRows] = k.x;
-      st[2 * kRows] = k.y;
-      const Tile& tile = ctl->head[x.last];
-      if (a.lse && r < tile.rows) put_lse(a, tile.token, tile.head, tile.row0 + r, G, j.m, j.sum);
-    } else {
-      float* ws = part_of(x);
-      put_at(ws + r, j.m, a.ws, a.ws_bytes);
-      put_at(ws + kRows + r, j.lift, a.ws, a.ws_bytes);
-      put_at(ws + 2 * kRows + r, j.sum, a.ws, a.ws_bytes);
+    // (a member's maximum has done its part: its factor takes the place)
+    if (some) st[0] = ex2(down + high - j.lift);
+    if (x.first + lane == x.last) {
+      if (x.closed && !x.before) {
+        const float2 k = last_factors(j.lift, j.sum);
+        st[kRows] = k.x;
+        st[2 * kRows] = k.y;
+        const Tile& tile = ctl->head[x.last];
+        if (a.lse && r < tile.rows) put_lse(a, tile.token, tile.head, tile.row0 + r, G, j.m, j.sum);
+      } else {
+        float* ws = part_of(x);
+        put_at(ws + r, j.m, a.ws, a.ws_bytes);
+        put_at(ws + kRows + r, j.lift, a.ws, a.ws_bytes);
+        put_at(ws + 2 * kRows + r, j.sum, a.ws, a.ws_bytes);
+      }
     }
   }
   warps_sync<kWarps>();
@@ -1129,13 +1172,16 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
     const int e = i % S::kQuads;
     const Quad qd = quad<NT>(e);
     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int z = y.first; z <= y.last; ++z) {
-      const float4 q = y.closed && z == y.last
-                           ? reinterpret_cast<const float4*>(heads)[((int64_t)blockIdx.x * kWarps + z) * S::kQuads + e]
-                           : reinterpret_cast<const float4*>(base + z * kStages * S::kStage)[e];
-      const float f0 = stats[stat(y, z) + qd.row], f1 = stats[stat(y, z) + qd.row + 1];
-      x = make_float4(fmaf(q.x, f0, x.x), fmaf(q.y, f1, x.y), fmaf(q.z, f0, x.z), fmaf(q.w, f1, x.w));
-    }
+    float4 ending = x;
+    if (y.closed) ending = reinterpret_cast<const float4*>(heads)[((int64_t)blockIdx.x * kWarps + y.last) * S::kQuads + e];
+    auto add = [&](const float4& q, const float* st) {
+      x = make_float4(fmaf(q.x, st[0], x.x), fmaf(q.y, st[1], x.y), fmaf(q.z, st[0], x.z), fmaf(q.w, st[1], x.w));
+    };
+    const int opens = y.last + !y.closed;
+#pragma unroll 4
+    for (int z = y.first; z < opens; ++z)
+      add(reinterpret_cast<const float4*>(base + z * kStages * S::kStage)[e], stats + z * kStat + qd.row);
+    if (y.closed) add(ending, stats + (kWarps + y.last) * kStat + qd.row);
     if (!y.closed || y.before) {
       put_at(part_of(y) + 3 * kRows + 4 * (int64_t)e, x, a.ws, a.ws_bytes);
       continue;
@@ -1288,6 +1334,7 @@ AttnShape attn_shape(const AttentionArgs& a) {
   AttnShape s;
   s.nt = a.c.head_dim <= 128 && rows > 8 * (int64_t)a.c.sequences ? 2 : 1;
   const int width = a.c.head_dim * s.nt;
+  const int kChunk = a.c.head_dim == 64 ? 64 : 32;      // (Attn::kChunk)
   s.warps = width <= 128 ? 15 : width < 256 ? 11 : 7;  // (Attn::kWarps)
   const int64_t kRows = 8 * s.nt, tiles = rows / kRows + a.c.sequences, most = (int64_t)a.c.max_pages * a.c.page_tokens + 1;
   const int64_t span = a.window > 0 && a.window + (kRows + G - 2) / G + 1 + kChunk < most
@@ -1299,17 +1346,17 @@ AttnShape attn_shape(const AttentionArgs& a) {
   return s;
 }
 
-// The pages' codes as [blocks, page_tokens / 16, head_dim / box, 16, box] bytes: a box of 16 (or two of them) tokens
-// lies in shared memory as slabs of `box` bytes a token, swizzled.
+// The pages' codes as [blocks, page_tokens / 16, head_dim / box, 16, box] bytes, copied a page's tokens at a time, or
+// `chunk`: 16 tokens lie in shared memory as slabs of `box` bytes a token, swizzled.
 // (A cache without pages, whose pages are never looked at, borrows an address.)
-bool pages_map(CUtensorMap* m, const CacheArgs& c, const void* any, int box) {
+bool pages_map(CUtensorMap* m, const CacheArgs& c, const void* any, int box, int chunk) {
   auto fn = tma_encode_fn();
   if (!fn) return false;
   ensure_context();
   const uint64_t D = c.head_dim, P = c.page_tokens;
   const cuuint64_t dims[5] = {(cuuint64_t)box, 16, D / box, P / 16, (cuuint64_t)(c.pages ? c.pages : 1) * 2 * c.heads};
   const cuuint64_t strides[4] = {D, (cuuint64_t)box, 16 * D, P * D};
-  const cuuint32_t boxes[5] = {(cuuint32_t)box, 16, (cuuint32_t)(D / box), P > 16 ? 2u : 1u, 1};
+  const cuuint32_t boxes[5] = {(cuuint32_t)box, 16, (cuuint32_t)(D / box), (cuuint32_t)(c.page_tokens < chunk ? P / 16 : chunk / 16), 1};
   const cuuint32_t es[5] = {1, 1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, c.pages ? c.codes : const_cast<void*>(any), dims, strides, boxes, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
             box == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : box == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
@@ -1334,7 +1381,7 @@ cudaError_t attend(const AttentionArgs& a, const AttnShape& sh, cudaStream_t st)
     }
   }
   CUtensorMap map;
-  if (!pages_map(&map, a.c, a.q.p, S::kBox)) return cudaErrorInvalidValue;
+  if (!pages_map(&map, a.c, a.q.p, S::kBox, S::kChunk)) return cudaErrorInvalidValue;
   cache_attention_kernel<D, NT, kExact><<<sh.ctas, S::kThreads, S::kBytes, st>>>(map, a);
   if ((e = cudaGetLastError()) != cudaSuccess || !sh.split) return e;
   // launched while the kernel before it drains; it waits for that kernel's parts itself
