@@ -260,7 +260,7 @@ template <int D, int NT>
 struct Attn {
   // Warps that multiply, beside the one that fetches: as many as their registers
   // (sums D NT / 4, queries D NT / 8 of them) leave room for on the SM.
-  static constexpr int kWarps = D * NT <= 128 ? 15 : D * NT < 256 ? 11 : 7;
+  static constexpr int kWarps = D * NT <= 64 ? 15 : D * NT <= 128 ? 11 : 7;
   static constexpr int kThreads = (kWarps + 1) * 32;
   static constexpr int kRows = 8 * NT;
   static constexpr int kBox = D % 128 == 0 ? 128 : D % 64 == 0 ? 64 : 32;  // bytes of a row in one swizzled slab
@@ -290,7 +290,6 @@ struct AttnCtl {
   uint64_t full[kMostWarps][kMostStages], empty[kMostWarps][kMostStages];
   int32_t block[kMostWarps][kMostStages][4];  // of the keys in a stage's parts (-1: none)
   Tile head[kMostWarps], open[kMostWarps];       // tiles that a warp shares with the one before it, and behind it
-  int32_t units;                         // of all sequences
   Start start[kMostWarps];               // of the warps' runs
   int32_t left[kMostWarps];                  // units of the open tile behind a warp's run
   uint8_t has[kMostWarps];                   // kHead, kOpen, kBegan
@@ -501,52 +500,73 @@ __device__ __forceinline__ Cut cut(int32_t units) {
   return c;
 }
 
-// Where a warp's run begins (lanes of the fetching warp: that of warp lane % 16),
-// for up to 32 sequences: each lane looks at one. Returns the call's units.
-template <int kRows, int kChunk, int kWarps>
-__device__ __forceinline__ int32_t find_start_32(const AttentionArgs& a, int warp, int lane, Cut* runs,
-                                                 Walk<kRows, kChunk>* w) {
-  int32_t mine = 0;
-  Walk<kRows, kChunk> x{};
-  if (lane < a.c.sequences) mine = x.take(a, lane, said(a.c, lane));
-  int32_t upto = mine;
+// Inclusive sums over a warp's lanes.
+__device__ __forceinline__ int32_t warp_sums(int32_t v, int lane) {
 #pragma unroll
   for (int i = 1; i < 32; i <<= 1) {
-    const int32_t v = __shfl_up_sync(0xffffffffu, upto, i);
-    if (lane >= i) upto += v;
+    const int32_t u = __shfl_up_sync(0xffffffffu, v, i);
+    if (lane >= i) v += u;
   }
-  const int32_t all = __shfl_sync(0xffffffffu, upto, 31);
-  *runs = cut<kWarps>(all);
-  const int32_t begin = runs->begin(blockIdx.x * kWarps + (warp < kWarps ? warp : min(lane & 15, kWarps - 1)));
-  int32_t s = 0;  // sequences that end before
-  for (int32_t i = 0; i < a.c.sequences; ++i) s += __shfl_sync(0xffffffffu, upto, i) <= begin;
-  s = min(s, a.c.sequences - 1);
-  w->b = s;
-  w->n = __shfl_sync(0xffffffffu, x.n, s);
-  w->row = __shfl_sync(0xffffffffu, x.row, s);
-  w->len = __shfl_sync(0xffffffffu, x.len, s);
-  w->tiles = __shfl_sync(0xffffffffu, x.tiles, s);
-  w->units = __shfl_sync(0xffffffffu, x.units, s);
-  const int32_t at = begin - __shfl_sync(0xffffffffu, upto - mine, s);
-  if (w->n > 0) w->place(a, at);
-  return all;
+  return v;
 }
 
-// The same for any number of sequences, by all threads, into ctl. Ends with a barrier.
+// Where the runs of this CTA's warps begin. Up to 32 sequences every warp looks at
+// them for itself, a lane at one, and has its run's first unit in w (lanes of the
+// fetching warp: that of warp lane % 16); up to the CTA's threads a thread looks at
+// one, and the runs' beginnings go to ctl. Ends with a barrier.
 template <int kRows, int kChunk, int kWarps>
-__device__ __noinline__ void find_starts(const AttentionArgs& a, AttnCtl* ctl, int32_t* sums) {
+__device__ __forceinline__ Cut find_start(const AttentionArgs& a, int warp, int lane, AttnCtl* ctl, int32_t* sums,
+                                          Walk<kRows, kChunk>* w) {
+  const bool few = a.c.sequences <= 32;
+  const int32_t mine_at = few ? lane : (int32_t)threadIdx.x;
+  Walk<kRows, kChunk> x{};
+  const int32_t mine = mine_at < a.c.sequences ? x.take(a, mine_at, said(a.c, mine_at)) : 0;
+  const int32_t upto = warp_sums(mine, lane);
+  if (few) {
+    const Cut runs = cut<kWarps>(__shfl_sync(0xffffffffu, upto, 31));
+    const int32_t begin = runs.begin(blockIdx.x * kWarps + (warp < kWarps ? warp : min(lane & 15, kWarps - 1)));
+    int32_t s = 0;  // sequences that end before
+    for (int32_t i = 0; i < a.c.sequences; ++i) s += __shfl_sync(0xffffffffu, upto, i) <= begin;
+    s = min(s, a.c.sequences - 1);
+    Start y;
+    y.b = s;
+    y.n = __shfl_sync(0xffffffffu, x.n, s);
+    y.row = __shfl_sync(0xffffffffu, x.row, s);
+    y.len = __shfl_sync(0xffffffffu, x.len, s);
+    y.tiles = __shfl_sync(0xffffffffu, x.tiles, s);
+    y.units = __shfl_sync(0xffffffffu, x.units, s);
+    y.at = begin - __shfl_sync(0xffffffffu, upto - mine, s);
+    if (y.n > 0) w->begin(a, y);
+    __syncthreads();
+    return runs;
+  }
+  if (lane == 31) sums[warp] = upto;
+  __syncthreads();
+  int32_t before = upto - mine, all = 0;
+#pragma unroll
+  for (int i = 0; i <= kWarps; ++i) {
+    if (i < warp) before += sums[i];
+    all += sums[i];
+  }
+  const Cut runs = cut<kWarps>(all);
+  for (int i = 0; i < kWarps; ++i) {
+    const int32_t at = runs.begin(blockIdx.x * kWarps + i) - before;
+    if (at >= 0 && at < mine) ctl->start[i] = Start{mine_at, x.n, x.row, x.len, x.tiles, x.units, at, 0};
+  }
+  __syncthreads();
+  return runs;
+}
+
+// The same for more sequences than threads.
+template <int kRows, int kChunk, int kWarps>
+__device__ __noinline__ Cut find_starts(const AttentionArgs& a, AttnCtl* ctl, int32_t* sums) {
   constexpr int kThreads = (kWarps + 1) * 32;
   const int32_t B = a.c.sequences, each = (B + kThreads - 1) / kThreads;
   const int32_t s0 = min((int32_t)threadIdx.x * each, B), s1 = min(s0 + each, B);
   Walk<kRows, kChunk> w;
   int32_t mine = 0;
   for (int32_t s = s0; s < s1; ++s) mine += w.take(a, s, said(a.c, s));
-  int32_t upto = mine;
-#pragma unroll
-  for (int i = 1; i < 32; i <<= 1) {
-    const int32_t v = __shfl_up_sync(0xffffffffu, upto, i);
-    if ((threadIdx.x & 31) >= i) upto += v;
-  }
+  const int32_t upto = warp_sums(mine, threadIdx.x & 31);
   if ((threadIdx.x & 31) == 31) sums[threadIdx.x >> 5] = upto;
   __syncthreads();
   int32_t before = upto - mine, all = 0;
@@ -561,7 +581,7 @@ __device__ __noinline__ void find_starts(const AttentionArgs& a, AttnCtl* ctl, i
       if (begin < before || begin >= before + mine) continue;
       int32_t at = before;
       for (int32_t s = s0; s < s1; ++s) {
-        const int32_t u = each == 1 ? mine : w.take(a, s, said(a.c, s));
+        const int32_t u = w.take(a, s, said(a.c, s));
         if (begin < at + u) {
           ctl->start[i] = Start{s, w.n, w.row, w.len, w.tiles, w.units, begin - at, 0};
           break;
@@ -570,8 +590,8 @@ __device__ __noinline__ void find_starts(const AttentionArgs& a, AttnCtl* ctl, i
       }
     }
   }
-  if (threadIdx.x == 0) ctl->units = all;
   __syncthreads();
+  return runs;
 }
 
 // Sums of a tile in the accumulators' order, four floats for each of 32 lanes:
@@ -643,15 +663,10 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
     ptx::fence_mbar_init();
   }
   Walk<kRows, kChunk> w;
-  Cut runs;
   const bool few = a.c.sequences <= 32;
-  if (few) {
-    find_start_32<kRows, kChunk, kWarps>(a, warp, lane, &runs, &w);
-    __syncthreads();
-  } else {
-    find_starts<kRows, kChunk, kWarps>(a, ctl, reinterpret_cast<int32_t*>(stats));
-    runs = cut<kWarps>(ctl->units);
-  }
+  int32_t* sums = reinterpret_cast<int32_t*>(stats);
+  const Cut runs = a.c.sequences <= S::kThreads ? find_start<kRows, kChunk, kWarps>(a, warp, lane, ctl, sums, &w)
+                                                : find_starts<kRows, kChunk, kWarps>(a, ctl, sums);
   if (blockIdx.x >= runs.ctas) {
     if (a.ws && threadIdx.x == 0) put_at(&reinterpret_cast<Split*>(a.ws)[blockIdx.x].parts, (int32_t)0, a.ws, a.ws_bytes);
     return;
@@ -696,10 +711,6 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
     bool go = true;
     for (int32_t round = 0; round < rounds && go; ++round) {
       const Pages now = ahead;
-      if (round + 1 < units) {
-        w.next(a);
-        ahead = pages_at();
-      }
       const bool mine = round < units && now.live;
       int32_t block[kMine], bytes = 0;
 #pragma unroll
@@ -735,6 +746,10 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
             parity ^= 1u;
           }
         }
+      }
+      if (round + 1 < units) {
+        w.next(a);
+        ahead = pages_at();
       }
     }
     if (!go) {
@@ -1166,14 +1181,21 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
       }
     }
   }
+  // (what is read from the workspace is asked for one step ahead)
+  auto ending_at = [&](int i) {
+    if (i >= ended * S::kQuads) return make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    return reinterpret_cast<const float4*>(heads)[((int64_t)blockIdx.x * kWarps + group(i / S::kQuads).last) * S::kQuads + i % S::kQuads];
+  };
+  float4 next = ending_at(threadIdx.x);
   warps_sync<kWarps>();
+#pragma unroll 1
   for (int i = threadIdx.x; i < groups * S::kQuads; i += kWarps * 32) {
+    const float4 ending = next;
+    next = ending_at(i + kWarps * 32);
     const Group y = group(i / S::kQuads);
     const int e = i % S::kQuads;
     const Quad qd = quad<NT>(e);
     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float4 ending = x;
-    if (y.closed) ending = reinterpret_cast<const float4*>(heads)[((int64_t)blockIdx.x * kWarps + y.last) * S::kQuads + e];
     auto add = [&](const float4& q, const float* st) {
       x = make_float4(fmaf(q.x, st[0], x.x), fmaf(q.y, st[1], x.y), fmaf(q.z, st[0], x.z), fmaf(q.w, st[1], x.w));
     };
@@ -1335,7 +1357,7 @@ AttnShape attn_shape(const AttentionArgs& a) {
   s.nt = a.c.head_dim <= 128 && rows > 8 * (int64_t)a.c.sequences ? 2 : 1;
   const int width = a.c.head_dim * s.nt;
   const int kChunk = a.c.head_dim == 64 ? 64 : 32;      // (Attn::kChunk)
-  s.warps = width <= 128 ? 15 : width < 256 ? 11 : 7;  // (Attn::kWarps)
+  s.warps = width <= 64 ? 15 : width <= 128 ? 11 : 7;  // (Attn::kWarps)
   const int64_t kRows = 8 * s.nt, tiles = rows / kRows + a.c.sequences, most = (int64_t)a.c.max_pages * a.c.page_tokens + 1;
   const int64_t span = a.window > 0 && a.window + (kRows + G - 2) / G + 1 + kChunk < most
                            ? a.window + (kRows + G - 2) / G + 1 + kChunk : most;
