@@ -255,20 +255,20 @@ constexpr int kSms = 152;
 constexpr float kTop = 15.0f;                   // weights are held times 2^15: f16 keeps 2^-39 of the largest
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr int kMostWarps = 15, kMostStages = 8;
+constexpr int kRows = 8;  // of a tile: sixteen, for half the conversions, gained 7 % at 16 rows and lost 20 % at 4 to 16
 
-template <int D, int NT>
+template <int D>
 struct Attn {
   // Warps that multiply, beside the one that fetches: as many as their registers
-  // (sums D NT / 4, queries D NT / 8 of them) leave room for on the SM.
-  static constexpr int kWarps = D * NT <= 64 ? 15 : D * NT <= 128 ? 11 : 7;
+  // (sums D / 4, queries D / 8 of them) leave room for on the SM without spilling.
+  static constexpr int kWarps = D <= 64 ? 15 : D <= 128 ? 11 : 7;
   static constexpr int kThreads = (kWarps + 1) * 32;
-  static constexpr int kRows = 8 * NT;
   static constexpr int kBox = D % 128 == 0 ? 128 : D % 64 == 0 ? 64 : 32;  // bytes of a row in one swizzled slab
   static constexpr int kChunk = D == 64 ? 64 : 32;                         // tokens of a unit, in parts of 16
   static constexpr int kParts = kChunk / 16;
   static constexpr int kPart = 16 * D;                                     // a part's keys or values
   static constexpr int kStage = kChunk * D;                                // a unit's
-  static constexpr int kQuads = D / 16 * NT * 32;                          // of a tile's sums (below)
+  static constexpr int kQuads = D / 16 * 32;                               // of a tile's sums (below)
   static constexpr int kFixed = 2 * kWarps * 3 * kRows * 4 + 5120;
   static constexpr int kFit = (227 * 1024 - 1024 - kFixed) / (kWarps * kStage);
   static constexpr int kStages = kFit < kMostStages ? kFit : kMostStages;  // of a warp's ring
@@ -308,7 +308,7 @@ struct Split {
 // Floats of the workspace: a Split for each CTA, then two parts each (a tile
 // that began before it, a tile that goes on behind it): maxima, lifts, sums and
 // numerators; then the numerators of each warp's first tile.
-__host__ __device__ constexpr int64_t part_floats(int rows, int D) { return (int64_t)rows * D + 3 * rows; }
+__host__ __device__ constexpr int64_t part_floats(int D) { return (int64_t)kRows * D + 3 * kRows; }
 
 // Bounded wait (about 2 s); the whole warp goes on or leaves together.
 __device__ __forceinline__ bool wait_bar_warp(uint32_t bar, uint32_t parity, uint32_t* abort) {
@@ -405,7 +405,7 @@ __device__ __forceinline__ Said said(const CacheArgs& c, int32_t b) {
 // A place in the order of all units: sequences, their heads, their tiles of
 // kRows query rows, kChunk tokens at a time. A sequence's tiles count alike (the
 // longest's units): units that a tile has no tokens for are passed over.
-template <int kRows, int kChunk>
+template <int kChunk>
 struct Walk {
   int32_t b, n, row, len, tiles, units;  // sequence: rows, first row, length, tiles, units of each
   int32_t head, tile, unit;
@@ -514,12 +514,12 @@ __device__ __forceinline__ int32_t warp_sums(int32_t v, int lane) {
 // them for itself, a lane at one, and has its run's first unit in w (lanes of the
 // fetching warp: that of warp lane % 16); up to the CTA's threads a thread looks at
 // one, and the runs' beginnings go to ctl. Ends with a barrier.
-template <int kRows, int kChunk, int kWarps>
+template <int kChunk, int kWarps>
 __device__ __forceinline__ Cut find_start(const AttentionArgs& a, int warp, int lane, AttnCtl* ctl, int32_t* sums,
-                                          Walk<kRows, kChunk>* w) {
+                                          Walk<kChunk>* w) {
   const bool few = a.c.sequences <= 32;
   const int32_t mine_at = few ? lane : (int32_t)threadIdx.x;
-  Walk<kRows, kChunk> x{};
+  Walk<kChunk> x{};
   const int32_t mine = mine_at < a.c.sequences ? x.take(a, mine_at, said(a.c, mine_at)) : 0;
   const int32_t upto = warp_sums(mine, lane);
   if (few) {
@@ -558,12 +558,12 @@ __device__ __forceinline__ Cut find_start(const AttentionArgs& a, int warp, int 
 }
 
 // The same for more sequences than threads.
-template <int kRows, int kChunk, int kWarps>
+template <int kChunk, int kWarps>
 __device__ __noinline__ Cut find_starts(const AttentionArgs& a, AttnCtl* ctl, int32_t* sums) {
   constexpr int kThreads = (kWarps + 1) * 32;
   const int32_t B = a.c.sequences, each = (B + kThreads - 1) / kThreads;
   const int32_t s0 = min((int32_t)threadIdx.x * each, B), s1 = min(s0 + each, B);
-  Walk<kRows, kChunk> w;
+  Walk<kChunk> w;
   int32_t mine = 0;
   for (int32_t s = s0; s < s1; ++s) mine += w.take(a, s, said(a.c, s));
   const int32_t upto = warp_sums(mine, threadIdx.x & 31);
@@ -595,15 +595,14 @@ __device__ __noinline__ Cut find_starts(const AttentionArgs& a, AttnCtl* ctl, in
 }
 
 // Sums of a tile in the accumulators' order, four floats for each of 32 lanes:
-// quad e belongs to rows 8 (e / 32 % NT) + 2 (lane % 4) (elements 0, 2) and the
-// one behind (1, 3), channels 16 (e / 32 / NT) + 2 (lane / 4) and the one behind.
+// quad e belongs to rows 2 (lane % 4) (elements 0, 2) and the one behind (1, 3),
+// channels 16 (e / 32) + 2 (lane / 4) and the one behind.
 struct Quad {
   int row, d;
 };
-template <int NT>
 __device__ __forceinline__ Quad quad(int e) {
   const int lane = e & 31, i = e >> 5;
-  return Quad{8 * (i % NT) + 2 * (lane & 3), 16 * (i / NT) + 2 * (lane >> 2)};
+  return Quad{2 * (lane & 3), 16 * i + 2 * (lane >> 2)};
 }
 
 // Row r of a sequence's n * G rows: the tensors' row and the query head.
@@ -636,11 +635,11 @@ __device__ __forceinline__ void put_lse(const AttentionArgs& a, int32_t token, i
   put_at(a.lse + at, sum == 0.0f ? -INFINITY : (m + lg2(sum)) * 0.693147180559945f, a.lse, a.lse_bytes);
 }
 
-template <int D, int NT, bool kExact>
-__global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
+template <int D, bool kExact>
+__global__ void __launch_bounds__(Attn<D>::kThreads, 1)
     cache_attention_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ AttentionArgs a) {
-  using S = Attn<D, NT>;
-  constexpr int kWarps = S::kWarps, kRows = S::kRows, kSegs = D / 16, kStages = S::kStages, kStat = 3 * kRows;
+  using S = Attn<D>;
+  constexpr int kWarps = S::kWarps, kSegs = D / 16, kStages = S::kStages, kStat = 3 * kRows;
   constexpr int kChunk = S::kChunk, kParts = S::kParts;
   constexpr int kIn = S::kBox / 16;  // segments of 16 channels in a slab
   extern __shared__ uint8_t raw[];
@@ -662,11 +661,11 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
     }
     ptx::fence_mbar_init();
   }
-  Walk<kRows, kChunk> w;
+  Walk<kChunk> w;
   const bool few = a.c.sequences <= 32;
   int32_t* sums = reinterpret_cast<int32_t*>(stats);
-  const Cut runs = a.c.sequences <= S::kThreads ? find_start<kRows, kChunk, kWarps>(a, warp, lane, ctl, sums, &w)
-                                                : find_starts<kRows, kChunk, kWarps>(a, ctl, sums);
+  const Cut runs = a.c.sequences <= S::kThreads ? find_start<kChunk, kWarps>(a, warp, lane, ctl, sums, &w)
+                                                : find_starts<kChunk, kWarps>(a, ctl, sums);
   if (blockIdx.x >= runs.ctas) {
     if (a.ws && threadIdx.x == 0) put_at(&reinterpret_cast<Split*>(a.ws)[blockIdx.x].parts, (int32_t)0, a.ws, a.ws_bytes);
     return;
@@ -772,23 +771,22 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
   const uint32_t lane_at = my_ring + (lane >> 4) * S::kPart + mrow * S::kBox + (swz << 4);
   const uint32_t my_full = full + 8 * kMostStages * warp, my_empty = empty + 8 * kMostStages * warp;
   const float scale2 = a.scale * 1.44269504088896f, cap = a.softcap > 0.0f ? a.scale / a.softcap : 0.0f;
-  float* heads = a.ws + gridDim.x * (sizeof(Split) / 4 + 2 * part_floats(kRows, D));  // (used with a workspace only)
+  float* heads = a.ws + gridDim.x * (sizeof(Split) / 4 + 2 * part_floats(D));  // (used with a workspace only)
 
-  uint32_t qf[kSegs][NT][2];
-  float o[kSegs][NT][4], m[NT][2], lift[NT][2], sum[NT][2], slope[NT][2], unit_q[NT][2];
-  int32_t pos[NT][2];
+  uint32_t qf[kSegs][2];
+  float o[kSegs][4], m[2], lift[2], sum[2], slope[2], unit_q[2];
+  int32_t pos[2];
   auto clear = [&]() {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        m[nt][i] = kLowest;
-        lift[nt][i] = sum[nt][i] = 0.0f;
+        m[i] = kLowest;
+        lift[i] = sum[i] = 0.0f;
       }
 #pragma unroll
       for (int s = 0; s < kSegs; ++s)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[s][nt][i] = 0.0f;
+        for (int i = 0; i < 4; ++i) o[s][i] = 0.0f;
     }
   };
   clear();
@@ -803,9 +801,8 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
     if (u == 0 || w.unit == 0) {
       // queries of this tile, row by row times a power of two: the largest in [2^14, 2^15)
       const int32_t rows = w.n * G - w.row0;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int32_t r = 8 * nt + g;
+      {
+        const int32_t r = g;
         uint2 x[kSegs];
         uint32_t top = 0;
         if (r < rows) {
@@ -827,18 +824,18 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
 #pragma unroll
         for (int s = 0; s < kSegs; ++s) {
           const float2 lo = unpack2(x[s].x), hi = unpack2(x[s].y);
-          qf[s][nt][0] = e == 255 ? 0u : f16x2(lo.x * f1 * f2, lo.y * f1 * f2);
-          qf[s][nt][1] = e == 255 ? 0u : f16x2(hi.x * f1 * f2, hi.y * f1 * f2);
+          qf[s][0] = e == 255 ? 0u : f16x2(lo.x * f1 * f2, lo.y * f1 * f2);
+          qf[s][1] = e == 255 ? 0u : f16x2(hi.x * f1 * f2, hi.y * f1 * f2);
         }
         // 2^(e - 141), down to 2^-140
         const float uq = e == 255 ? __uint_as_float(0x7FC00000u) : e > 14 ? pow2i(e - 141) : __uint_as_float(1u << (e + 8));
-        unit_q[nt][0] = __shfl_sync(0xffffffffu, uq, 8 * t);
-        unit_q[nt][1] = __shfl_sync(0xffffffffu, uq, 8 * t + 4);
+        unit_q[0] = __shfl_sync(0xffffffffu, uq, 8 * t);
+        unit_q[1] = __shfl_sync(0xffffffffu, uq, 8 * t + 4);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int32_t c = min(w.row0 + 8 * nt + 2 * t + i, w.n * G - 1);
-          pos[nt][i] = w.len - w.n + c / G;
-          slope[nt][i] = a.slopes ? __ldg(a.slopes + w.head * G + c % G) * 1.44269504088896f : 0.0f;
+          const int32_t c = min(w.row0 + 2 * t + i, w.n * G - 1);
+          pos[i] = w.len - w.n + c / G;
+          slope[i] = a.slopes ? __ldg(a.slopes + w.head * G + c % G) * 1.44269504088896f : 0.0f;
         }
       }
     }
@@ -850,13 +847,11 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
       const int32_t block = ctl->block[warp][stage][lane % kParts];
       uint32_t scale = 255u;
       if (block >= 0) scale = __ldg(a.c.scales + block + (lane & kParts ? a.c.heads : 0));
-      float s[kParts][NT][4];
+      float s[kParts][4];
 #pragma unroll
       for (int h = 0; h < kParts; ++h)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[h][nt][i] = 0.0f;
+          for (int i = 0; i < 4; ++i) s[h][i] = 0.0f;
       {
         const uint32_t at = lane_at + stage * S::kStage;
 #pragma unroll
@@ -869,8 +864,7 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
             for (int z = 0; z < 2; ++z) {
               const uint32_t a0 = e4m3x2_f16x2(r[2 * z]), a2 = e4m3x2_f16x2(r[2 * z] >> 16);
               const uint32_t a1 = e4m3x2_f16x2(r[2 * z + 1]), a3 = e4m3x2_f16x2(r[2 * z + 1] >> 16);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma(s[h + z][nt], a0, a1, a2, a3, qf[i][nt][0], qf[i][nt][1]);
+            mma(s[h + z], a0, a1, a2, a3, qf[i][0], qf[i][1]);
             }
           }
         }
@@ -887,27 +881,26 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
 #pragma unroll
       for (int h = 0; h < kParts; ++h) {
         const float ks = scale_value(__shfl_sync(0xffffffffu, scale, h));
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float f = unit_q[nt][i] * ks;  // (exact)
+            const float f = unit_q[i] * ks;  // (exact)
             if (a.softcap > 0.0f) {
 #pragma unroll
-              for (int z = i; z < 4; z += 2) s[h][nt][z] = a.softcap * 1.44269504088896f * tanhf(s[h][nt][z] * (f * cap));
+              for (int z = i; z < 4; z += 2) s[h][z] = a.softcap * 1.44269504088896f * tanhf(s[h][z] * (f * cap));
             } else {
-              s[h][nt][i] *= f * scale2;
-              s[h][nt][i + 2] *= f * scale2;
+              s[h][i] *= f * scale2;
+              s[h][i + 2] *= f * scale2;
             }
-            const int32_t j1 = c0 + 16 * h + g - pos[nt][i];  // token's position less the row's
+            const int32_t j1 = c0 + 16 * h + g - pos[i];  // token's position less the row's
             if (a.slopes) {
-              s[h][nt][i] += slope[nt][i] * (float)j1;
-              s[h][nt][i + 2] += slope[nt][i] * (float)(j1 + 8);
+              s[h][i] += slope[i] * (float)j1;
+              s[h][i + 2] += slope[i] * (float)(j1 + 8);
             }
             if (!whole) {
               const int32_t most = a.window > 0 ? a.window : 0x7FFFFFFF;
-              if (j1 > 0 || j1 <= -most) s[h][nt][i] = -INFINITY;
-              if (j1 + 8 > 0 || j1 + 8 <= -most) s[h][nt][i + 2] = -INFINITY;
+              if (j1 > 0 || j1 <= -most) s[h][i] = -INFINITY;
+              if (j1 + 8 > 0 || j1 + 8 <= -most) s[h][i + 2] = -INFINITY;
             }
           }
         }
@@ -936,23 +929,22 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
       }
 
       // running maxima, and the weights
-      uint32_t pf[kParts][NT][2], pl[kParts][NT][2];
+      uint32_t pf[kParts][2], pl[kParts][2];
       bool moved = false;
-      float keep[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      float keep[2];
+      {
         float cm[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           float part[kParts], x = -INFINITY;
 #pragma unroll
           for (int h = 0; h < kParts; ++h) {
-            part[h] = fmaxf(s[h][nt][i], s[h][nt][i + 2]);
+            part[h] = fmaxf(s[h][i], s[h][i + 2]);
             x = fmaxf(x, part[h]);
           }
 #pragma unroll
           for (int z = 4; z < 32; z <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, z));
-          cm[i] = fmaxf(m[nt][i], x);
+          cm[i] = fmaxf(m[i], x);
           float y = x - cm[i] + ev[0];
           if (!one) {
             y = -INFINITY;
@@ -961,35 +953,35 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
 #pragma unroll
             for (int z = 4; z < 32; z <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, z));
           }
-          const float down = m[nt][i] - cm[i], was = down + lift[nt][i], now = fmaxf(was, y);
-          sum[nt][i] *= ex2(down);
-          keep[nt][i] = ex2(was - now);
+          const float down = m[i] - cm[i], was = down + lift[i], now = fmaxf(was, y);
+          sum[i] *= ex2(down);
+          keep[i] = ex2(was - now);
           moved |= was != now;
-          m[nt][i] = cm[i];
-          lift[nt][i] = now;
+          m[i] = cm[i];
+          lift[i] = now;
         }
 #pragma unroll
         for (int h = 0; h < kParts; ++h) {
-          const float c[2] = {ev[h] + kTop - lift[nt][0], ev[h] + kTop - lift[nt][1]};
+          const float c[2] = {ev[h] + kTop - lift[0], ev[h] + kTop - lift[1]};
           float p[4];
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
-            const float x = s[h][nt][z] - cm[z & 1];
-            sum[nt][z & 1] += ex2(x);
+            const float x = s[h][z] - cm[z & 1];
+            sum[z & 1] += ex2(x);
             p[z] = ex2(x + c[z & 1]);
           }
           if (ev[h] != ev[h]) {
             // values that are no numbers: where a row attends them
 #pragma unroll
-            for (int z = 0; z < 4; ++z) p[z] = s[h][nt][z] == -INFINITY ? 0.0f : ev[h];
+            for (int z = 0; z < 4; ++z) p[z] = s[h][z] == -INFINITY ? 0.0f : ev[h];
           }
           const uint32_t u0 = f16x2(p[0], p[1]), u1 = f16x2(p[2], p[3]);
-          pf[h][nt][0] = transposed(u0);
-          pf[h][nt][1] = transposed(u1);
+          pf[h][0] = transposed(u0);
+          pf[h][1] = transposed(u1);
           if (kExact) {
             const float2 q0 = f16x2_f32(u0), q1 = f16x2_f32(u1);
-            pl[h][nt][0] = transposed(f16x2(p[0] - q0.x, p[1] - q0.y));
-            pl[h][nt][1] = transposed(f16x2(p[2] - q1.x, p[3] - q1.y));
+            pl[h][0] = transposed(f16x2(p[0] - q0.x, p[1] - q0.y));
+            pl[h][1] = transposed(f16x2(p[2] - q1.x, p[3] - q1.y));
           }
         }
       }
@@ -997,9 +989,7 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < kSegs; ++i)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int z = 0; z < 4; ++z) o[i][nt][z] *= keep[nt][z & 1];
+            for (int z = 0; z < 4; ++z) o[i][z] *= keep[z & 1];
       }
       const uint32_t at = lane_at + stage * S::kStage;
 #pragma unroll
@@ -1013,10 +1003,9 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
             // two tokens of a channel side by side, the even channel below
             const uint32_t x = __byte_perm(r[2 * z], 0, 0x3120), y = __byte_perm(r[2 * z + 1], 0, 0x3120);
             const uint32_t a0 = e4m3x2_f16x2(x), a1 = e4m3x2_f16x2(x >> 16), a2 = e4m3x2_f16x2(y), a3 = e4m3x2_f16x2(y >> 16);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma(o[i][nt], a0, a1, a2, a3, pf[h + z][nt][0], pf[h + z][nt][1]);
-              if (kExact) mma(o[i][nt], a0, a1, a2, a3, pl[h + z][nt][0], pl[h + z][nt][1]);
+            {
+              mma(o[i], a0, a1, a2, a3, pf[h + z][0], pf[h + z][1]);
+              if (kExact) mma(o[i], a0, a1, a2, a3, pl[h + z][0], pl[h + z][1]);
             }
           }
         }
@@ -1032,26 +1021,22 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
     has = kOpen | (u < w.unit ? kBegan : 0) | (has & kHead);
     if (w.last()) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int z = 4; z < 32; z <<= 1) sum[nt][i] += __shfl_xor_sync(0xffffffffu, sum[nt][i], z);
+          for (int z = 4; z < 32; z <<= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], z);
       const Tile tile = w.rows(G);
       if (u >= w.unit) {
         // a tile of this warp alone
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int r = 8 * nt + 2 * t + i;
+            const int r = 2 * t + i;
             if (r < tile.rows) {
-              const float2 k = last_factors(lift[nt][i], sum[nt][i]);
+              const float2 k = last_factors(lift[i], sum[i]);
               const int64_t at = row_of(a.out, tile.token, tile.head, tile.row0 + r, G) + 2 * g;
 #pragma unroll
               for (int s = 0; s < kSegs; ++s)
-                put2(a, at + 16 * s, o[s][nt][i] * k.x * k.y, o[s][nt][i + 2] * k.x * k.y);
-              if (a.lse && g == 0) put_lse(a, tile.token, tile.head, tile.row0 + r, G, m[nt][i], sum[nt][i]);
+                put2(a, at + 16 * s, o[s][i] * k.x * k.y, o[s][i + 2] * k.x * k.y);
+              if (a.lse && g == 0) put_lse(a, tile.token, tile.head, tile.row0 + r, G, m[i], sum[i]);
             }
           }
         has &= kHead;
@@ -1060,18 +1045,14 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
         float4* to = reinterpret_cast<float4*>(heads) + ((int64_t)blockIdx.x * kWarps + warp) * S::kQuads + lane;
 #pragma unroll
         for (int s = 0; s < kSegs; ++s)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            put_at(to + (s * NT + nt) * 32, make_float4(o[s][nt][0], o[s][nt][1], o[s][nt][2], o[s][nt][3]), a.ws, a.ws_bytes);
+            put_at(to + s * 32, make_float4(o[s][0], o[s][1], o[s][2], o[s][3]), a.ws, a.ws_bytes);
         if (g == 0) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
             for (int i = 0; i < 2; ++i) {
-              float* st = stats + (kWarps + warp) * kStat + 8 * nt + 2 * t + i;
-              st[0] = m[nt][i];
-              st[kRows] = lift[nt][i];
-              st[2 * kRows] = sum[nt][i];
+              float* st = stats + (kWarps + warp) * kStat + 2 * t + i;
+              st[0] = m[i];
+              st[kRows] = lift[i];
+              st[2 * kRows] = sum[i];
             }
         }
         if (lane == 0) ctl->head[warp] = tile;
@@ -1085,16 +1066,14 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
   // ---------------------------------------------------- joining in the CTA ---
   if ((has & kOpen) || units == 0) {  // (an empty run adds nothing to the tile around it)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
       for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int z = 4; z < 32; z <<= 1) sum[nt][i] += __shfl_xor_sync(0xffffffffu, sum[nt][i], z);
+        for (int z = 4; z < 32; z <<= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], z);
         if (g == 0) {
-          float* st = stats + warp * kStat + 8 * nt + 2 * t + i;
-          st[0] = m[nt][i];
-          st[kRows] = lift[nt][i];
-          st[2 * kRows] = sum[nt][i];
+          float* st = stats + warp * kStat + 2 * t + i;
+          st[0] = m[i];
+          st[kRows] = lift[i];
+          st[2 * kRows] = sum[i];
         }
       }
     // (this warp's ring: its loads have all been read)
@@ -1102,9 +1081,7 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
     __syncwarp();
 #pragma unroll
     for (int s = 0; s < kSegs; ++s)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        to[(s * NT + nt) * 32] = make_float4(o[s][nt][0], o[s][nt][1], o[s][nt][2], o[s][nt][3]);
+        to[s * 32] = make_float4(o[s][0], o[s][1], o[s][2], o[s][3]);
   }
   if (lane == 0) {
     ctl->has[warp] = has;
@@ -1144,7 +1121,7 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
   };
   auto stat = [&](const Group& x, int z) { return ((x.closed && z == x.last ? kWarps : 0) + z) * kStat; };
   auto part_of = [&](const Group& x) {
-    return a.ws + gridDim.x * (sizeof(Split) / 4) + (2 * (int64_t)blockIdx.x + !x.before) * part_floats(kRows, D);
+    return a.ws + gridDim.x * (sizeof(Split) / 4) + (2 * (int64_t)blockIdx.x + !x.before) * part_floats(D);
   };
   // a warp for a row of a group, a lane for a member
   for (int i = warp; i < groups * kRows; i += kWarps) {
@@ -1194,7 +1171,7 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
     next = ending_at(i + kWarps * 32);
     const Group y = group(i / S::kQuads);
     const int e = i % S::kQuads;
-    const Quad qd = quad<NT>(e);
+    const Quad qd = quad(e);
     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     auto add = [&](const float4& q, const float* st) {
       x = make_float4(fmaf(q.x, st[0], x.x), fmaf(q.y, st[1], x.y), fmaf(q.z, st[0], x.z), fmaf(q.w, st[1], x.w));
@@ -1237,9 +1214,9 @@ __global__ void __launch_bounds__(Attn<D, NT>::kThreads, 1)
 // row's statistics, a lane for a part; then as many groups of threads as fit take
 // every so many-th part each.
 constexpr int kJoinThreads = 512;
-template <int D, int NT>
+template <int D>
 __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ AttentionArgs a) {
-  constexpr int kRows = 8 * NT, kQuads = Attn<D, NT>::kQuads, kGroups = kQuads < kJoinThreads ? kJoinThreads / kQuads : 1;
+  constexpr int kQuads = Attn<D>::kQuads, kGroups = kQuads < kJoinThreads ? kJoinThreads / kQuads : 1;
   __shared__ float factors[kSms][kRows];
   __shared__ float2 last[kRows];
   __shared__ float4 sums[kGroups > 1 ? kJoinThreads : 1];
@@ -1249,8 +1226,8 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   if (sp.parts == 0) return;
   const int G = a.group;
   // part 0 is this CTA's second, the others the first of the CTAs behind it
-  const float* parts = a.ws + gridDim.x * (sizeof(Split) / 4) + 2 * (int64_t)blockIdx.x * part_floats(kRows, D);
-  auto part = [&](int i) { return parts + (2 * i + (i == 0)) * part_floats(kRows, D); };
+  const float* parts = a.ws + gridDim.x * (sizeof(Split) / 4) + 2 * (int64_t)blockIdx.x * part_floats(D);
+  auto part = [&](int i) { return parts + (2 * i + (i == 0)) * part_floats(D); };
   if (row < kRows) {
     constexpr int kMost = (kSms + 31) / 32;
     float m[kMost], lift[kMost], sum[kMost], top = kLowest, high = -INFINITY, all = 0.0f;
@@ -1285,7 +1262,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   __syncthreads();
   static_assert(kQuads <= kJoinThreads, "a quad a thread");
   const int group = threadIdx.x / kQuads, e = threadIdx.x % kQuads;
-  const Quad qd = quad<NT>(e);
+  const Quad qd = quad(e);
   float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (group < kGroups) {
 #pragma unroll 8
@@ -1342,30 +1319,30 @@ cudaError_t launch_cache_read(const CacheArgs& c, const Heads& k, const Heads& v
 }
 
 namespace {
-// How a call is cut: query rows of a tile, CTAs, and whether a tile may be split.
+// How a call is cut, by what the host knows of it: warps of a CTA, CTAs, whether a
+// tile may be split, units at most.
 struct AttnShape {
-  int nt, warps, ctas;
+  int warps, ctas;
   bool split;
-  int64_t units;  // at most
+  int64_t units;
 };
-// Sixteen rows to a tile where a sequence has more than eight on average (their
-// products come at half the loads); heads above 128 channels keep to eight, whose
-// sums fill the registers.
+template <int D>
 AttnShape attn_shape(const AttentionArgs& a) {
-  const int64_t G = a.q_heads / a.c.heads, rows = a.c.tokens * G;
-  AttnShape s;
-  s.nt = a.c.head_dim <= 128 && rows > 8 * (int64_t)a.c.sequences ? 2 : 1;
-  const int width = a.c.head_dim * s.nt;
-  const int kChunk = a.c.head_dim == 64 ? 64 : 32;      // (Attn::kChunk)
-  s.warps = width <= 64 ? 15 : width <= 128 ? 11 : 7;  // (Attn::kWarps)
-  const int64_t kRows = 8 * s.nt, tiles = rows / kRows + a.c.sequences, most = (int64_t)a.c.max_pages * a.c.page_tokens + 1;
-  const int64_t span = a.window > 0 && a.window + (kRows + G - 2) / G + 1 + kChunk < most
-                           ? a.window + (kRows + G - 2) / G + 1 + kChunk : most;
-  const int64_t units = (span + kChunk - 1) / kChunk, all = tiles * a.c.heads * units, ctas = (all + s.warps - 1) / s.warps;
-  s.ctas = (int)(ctas < kSms ? ctas : kSms);
-  s.split = units > 1;
-  s.units = all;
-  return s;
+  using S = Attn<D>;
+  const int64_t G = a.group, rows = a.c.tokens * G, tiles = rows / kRows + a.c.sequences;
+  const int64_t most = (int64_t)a.c.max_pages * a.c.page_tokens + 1, windowed = a.window + (kRows + G - 2) / G + 1 + S::kChunk;
+  const int64_t span = a.window > 0 && windowed < most ? windowed : most;
+  const int64_t units = (span + S::kChunk - 1) / S::kChunk, all = tiles * a.c.heads * units, ctas = (all + S::kWarps - 1) / S::kWarps;
+  return AttnShape{S::kWarps, (int)(ctas < kSms ? ctas : kSms), units > 1, all};
+}
+AttnShape attn_shape(const AttentionArgs& a) {
+  switch (a.c.head_dim) {
+    case 64: return attn_shape<64>(a);
+    case 96: return attn_shape<96>(a);
+    case 128: return attn_shape<128>(a);
+    case 192: return attn_shape<192>(a);
+    default: return attn_shape<256>(a);
+  }
 }
 
 // The pages' codes as [blocks, page_tokens / 16, head_dim / box, 16, box] bytes, copied a page's tokens at a time, or
@@ -1385,9 +1362,9 @@ bool pages_map(CUtensorMap* m, const CacheArgs& c, const void* any, int box, int
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int NT, bool kExact>
+template <int D, bool kExact>
 cudaError_t attend(const AttentionArgs& a, const AttnShape& sh, cudaStream_t st) {
-  using S = Attn<D, NT>;
+  using S = Attn<D>;
   static bool set[kMaxDevices] = {};
   static std::mutex mu;
   int dev = 0;
@@ -1397,14 +1374,14 @@ cudaError_t attend(const AttentionArgs& a, const AttnShape& sh, cudaStream_t st)
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!set[dev]) {
-      e = cudaFuncSetAttribute(cache_attention_kernel<D, NT, kExact>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+      e = cudaFuncSetAttribute(cache_attention_kernel<D, kExact>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
       if (e != cudaSuccess) return e;
       set[dev] = true;
     }
   }
   CUtensorMap map;
   if (!pages_map(&map, a.c, a.q.p, S::kBox, S::kChunk)) return cudaErrorInvalidValue;
-  cache_attention_kernel<D, NT, kExact><<<sh.ctas, S::kThreads, S::kBytes, st>>>(map, a);
+  cache_attention_kernel<D, kExact><<<sh.ctas, S::kThreads, S::kBytes, st>>>(map, a);
   if ((e = cudaGetLastError()) != cudaSuccess || !sh.split) return e;
   // launched while the kernel before it drains; it waits for that kernel's parts itself
   cudaLaunchConfig_t cfg = {};
@@ -1416,11 +1393,11 @@ cudaError_t attend(const AttentionArgs& a, const AttnShape& sh, cudaStream_t st)
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_join_kernel<D, NT>, a);
+  return cudaLaunchKernelEx(&cfg, cache_join_kernel<D>, a);
 }
-template <int D, int NT>
+template <int D>
 cudaError_t attend(const AttentionArgs& a, const AttnShape& sh, cudaStream_t st) {
-  return a.out_f32 ? attend<D, NT, true>(a, sh, st) : attend<D, NT, false>(a, sh, st);
+  return a.out_f32 ? attend<D, true>(a, sh, st) : attend<D, false>(a, sh, st);
 }
 }  // namespace
 
@@ -1429,8 +1406,7 @@ int64_t cache_attention_units(const AttentionArgs& a) { return attn_shape(a).uni
 int64_t cache_attention_workspace_bytes(const AttentionArgs& a) {
   const AttnShape s = attn_shape(a);
   if (!s.split) return 0;
-  return s.ctas * ((int64_t)sizeof(Split) + 8 * part_floats(8 * s.nt, a.c.head_dim) +
-                   (int64_t)s.warps * 8 * s.nt * a.c.head_dim * 4);
+  return s.ctas * ((int64_t)sizeof(Split) + 8 * part_floats(a.c.head_dim) + (int64_t)s.warps * kRows * a.c.head_dim * 4);
 }
 
 cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t st) {
@@ -1438,11 +1414,11 @@ cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t st) {
   (void)cudaGetLastError();
   const AttnShape sh = attn_shape(a);
   switch (a.c.head_dim) {
-    case 64: return sh.nt == 2 ? attend<64, 2>(a, sh, st) : attend<64, 1>(a, sh, st);
-    case 96: return sh.nt == 2 ? attend<96, 2>(a, sh, st) : attend<96, 1>(a, sh, st);
-    case 128: return sh.nt == 2 ? attend<128, 2>(a, sh, st) : attend<128, 1>(a, sh, st);
-    case 192: return attend<192, 1>(a, sh, st);
-    default: return attend<256, 1>(a, sh, st);
+    case 64: return attend<64>(a, sh, st);
+    case 96: return attend<96>(a, sh, st);
+    case 128: return attend<128>(a, sh, st);
+    case 192: return attend<192>(a, sh, st);
+    default: return attend<256>(a, sh, st);
   }
 }
 
