@@ -512,8 +512,8 @@ __device__ __forceinline__ int32_t warp_sums(int32_t v, int lane) {
 
 // Where the runs of this CTA's warps begin. Up to 32 sequences every warp looks at
 // them for itself, a lane at one, and has its run's first unit in w (lanes of the
-// fetching warp: that of warp lane % 16); up to the CTA's threads a thread looks at
-// one, and the runs' beginnings go to ctl. Ends with a barrier.
+// fetching warp: that of warp lane % 16); more are the whole CTA's, a thread looks
+// at one, and the runs' beginnings go to ctl. Ends with a barrier.
 template <int kChunk, int kWarps>
 __device__ __forceinline__ Cut find_start(const AttentionArgs& a, int warp, int lane, AttnCtl* ctl, int32_t* sums,
                                           Walk<kChunk>* w) {
@@ -540,54 +540,37 @@ __device__ __forceinline__ Cut find_start(const AttentionArgs& a, int warp, int 
     __syncthreads();
     return runs;
   }
-  if (lane == 31) sums[warp] = upto;
-  __syncthreads();
-  int32_t before = upto - mine, all = 0;
-#pragma unroll
-  for (int i = 0; i <= kWarps; ++i) {
-    if (i < warp) before += sums[i];
-    all += sums[i];
-  }
-  const Cut runs = cut<kWarps>(all);
-  for (int i = 0; i < kWarps; ++i) {
-    const int32_t at = runs.begin(blockIdx.x * kWarps + i) - before;
-    if (at >= 0 && at < mine) ctl->start[i] = Start{mine_at, x.n, x.row, x.len, x.tiles, x.units, at, 0};
-  }
-  __syncthreads();
-  return runs;
-}
-
-// The same for more sequences than threads.
-template <int kChunk, int kWarps>
-__device__ __noinline__ Cut find_starts(const AttentionArgs& a, AttnCtl* ctl, int32_t* sums) {
+  // all units, then the sequences again, as many at a time as there are threads
   constexpr int kThreads = (kWarps + 1) * 32;
-  const int32_t B = a.c.sequences, each = (B + kThreads - 1) / kThreads;
-  const int32_t s0 = min((int32_t)threadIdx.x * each, B), s1 = min(s0 + each, B);
-  Walk<kChunk> w;
-  int32_t mine = 0;
-  for (int32_t s = s0; s < s1; ++s) mine += w.take(a, s, said(a.c, s));
-  const int32_t upto = warp_sums(mine, threadIdx.x & 31);
-  if ((threadIdx.x & 31) == 31) sums[threadIdx.x >> 5] = upto;
+  const bool once = a.c.sequences <= kThreads;
+  int32_t more = mine;
+  for (int32_t s = mine_at + kThreads; s < a.c.sequences; s += kThreads) more += x.take(a, s, said(a.c, s));
+  more = warp_sums(more, lane);
+  if (lane == 31) sums[warp] = more;
   __syncthreads();
-  int32_t before = upto - mine, all = 0;
-  for (int i = 0; i <= kWarps; ++i) {
-    if (i < (int)(threadIdx.x >> 5)) before += sums[i];
-    all += sums[i];
-  }
+  int32_t all = 0, before = 0;
+#pragma unroll
+  for (int i = 0; i <= kWarps; ++i) all += sums[i];
   const Cut runs = cut<kWarps>(all);
-  if (blockIdx.x < runs.ctas && mine > 0) {
+  for (int32_t from = 0; from < a.c.sequences; from += kThreads) {
+    const int32_t s = from + mine_at;
+    int32_t units = mine, within = upto;
+    if (!once) {
+      units = s < a.c.sequences ? x.take(a, s, said(a.c, s)) : 0;
+      within = warp_sums(units, lane);
+      __syncthreads();
+      if (lane == 31) sums[warp] = within;
+      __syncthreads();
+    }
+    int32_t at = before + within - units;  // units before this sequence
+#pragma unroll
+    for (int i = 0; i <= kWarps; ++i) {
+      if (i < warp) at += sums[i];
+      before += sums[i];
+    }
     for (int i = 0; i < kWarps; ++i) {
-      const int32_t begin = runs.begin(blockIdx.x * kWarps + i);
-      if (begin < before || begin >= before + mine) continue;
-      int32_t at = before;
-      for (int32_t s = s0; s < s1; ++s) {
-        const int32_t u = w.take(a, s, said(a.c, s));
-        if (begin < at + u) {
-          ctl->start[i] = Start{s, w.n, w.row, w.len, w.tiles, w.units, begin - at, 0};
-          break;
-        }
-        at += u;
-      }
+      const int32_t u = runs.begin(blockIdx.x * kWarps + i) - at;
+      if (u >= 0 && u < units) ctl->start[i] = Start{s, x.n, x.row, x.len, x.tiles, x.units, u, 0};
     }
   }
   __syncthreads();
@@ -663,9 +646,7 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
   }
   Walk<kChunk> w;
   const bool few = a.c.sequences <= 32;
-  int32_t* sums = reinterpret_cast<int32_t*>(stats);
-  const Cut runs = a.c.sequences <= S::kThreads ? find_start<kChunk, kWarps>(a, warp, lane, ctl, sums, &w)
-                                                : find_starts<kChunk, kWarps>(a, ctl, sums);
+  const Cut runs = find_start<kChunk, kWarps>(a, warp, lane, ctl, reinterpret_cast<int32_t*>(stats), &w);
   if (blockIdx.x >= runs.ctas) {
     if (a.ws && threadIdx.x == 0) put_at(&reinterpret_cast<Split*>(a.ws)[blockIdx.x].parts, (int32_t)0, a.ws, a.ws_bytes);
     return;
@@ -1119,80 +1100,79 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
     x.first = x.before ? 0 : at;
     return x;
   };
-  auto stat = [&](const Group& x, int z) { return ((x.closed && z == x.last ? kWarps : 0) + z) * kStat; };
-  auto part_of = [&](const Group& x) {
-    return a.ws + gridDim.x * (sizeof(Split) / 4) + (2 * (int64_t)blockIdx.x + !x.before) * part_floats(D);
-  };
-  // a warp for a row of a group, a lane for a member
-  for (int i = warp; i < groups * kRows; i += kWarps) {
-    const Group x = group(i / kRows);
-    const int r = i % kRows, z = min(x.first + lane, x.last);
-    const bool some = x.first + lane <= x.last;
-    float* st = stats + stat(x, z) + r;
-    const float mine = some ? st[0] : kLowest, high = some ? st[kRows] : 0.0f;
-    Joined j = {mine, 0.0f, some ? st[2 * kRows] : 0.0f};
+  // a warp a tile, and nothing waits for another from here on
+#pragma unroll 1
+  for (int i = warp; i < groups; i += kWarps) {
+    const Group x = group(i);
+    const bool final = x.closed && !x.before;
+    const int opens = x.last + !x.closed;  // members that have it open: first .. opens - 1
+    const float4* ending = reinterpret_cast<const float4*>(heads) + ((int64_t)blockIdx.x * kWarps + x.last) * S::kQuads + lane;
+    float4 sums[kSegs];
 #pragma unroll
-    for (int d = 16; d; d >>= 1) j.m = fmaxf(j.m, __shfl_xor_sync(0xffffffffu, j.m, d));
-    const float down = mine - j.m;
-    j.lift = down + high;
-    j.sum *= ex2(down);
+    for (int s = 0; s < kSegs; ++s) sums[s] = x.closed ? ending[32 * s] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    // statistics: a lane a row, four lanes take its members in turn
+    const int r = lane & 7;
+    auto stat = [&](int z) { return stats + ((z == opens ? kWarps : 0) + z) * kStat + r; };
+    Joined j = {kLowest, -INFINITY, 0.0f};
+    for (int z = x.first + (lane >> 3); z <= x.last; z += 4) j.m = fmaxf(j.m, stat(z)[0]);
 #pragma unroll
-    for (int d = 8; d; d >>= 1) {
+    for (int d = 8; d < 32; d <<= 1) j.m = fmaxf(j.m, __shfl_xor_sync(0xffffffffu, j.m, d));
+    for (int z = x.first + (lane >> 3); z <= x.last; z += 4) {
+      const float* st = stat(z);
+      const float down = st[0] - j.m;
+      j.lift = fmaxf(j.lift, down + st[kRows]);
+      j.sum += st[2 * kRows] * ex2(down);
+    }
+#pragma unroll
+    for (int d = 8; d < 32; d <<= 1) {
       j.lift = fmaxf(j.lift, __shfl_xor_sync(0xffffffffu, j.lift, d));
       j.sum += __shfl_xor_sync(0xffffffffu, j.sum, d);
     }
-    // (a member's maximum has done its part: its factor takes the place)
-    if (some) st[0] = ex2(down + high - j.lift);
-    if (x.first + lane == x.last) {
-      if (x.closed && !x.before) {
-        const float2 k = last_factors(j.lift, j.sum);
-        st[kRows] = k.x;
-        st[2 * kRows] = k.y;
-        const Tile& tile = ctl->head[x.last];
-        if (a.lse && r < tile.rows) put_lse(a, tile.token, tile.head, tile.row0 + r, G, j.m, j.sum);
-      } else {
-        float* ws = part_of(x);
+    for (int z = x.first + (lane >> 3); z <= x.last; z += 4) {
+      // (a member's maximum has done its part: its factor takes the place)
+      float* st = stat(z);
+      st[0] = ex2(st[0] - j.m + st[kRows] - j.lift);
+    }
+    __syncwarp();
+    // numerators: this lane's quads
+    float2 f;
+    if (x.closed) {
+      f = *reinterpret_cast<const float2*>(stats + (kWarps + x.last) * kStat + 2 * t);
+#pragma unroll
+      for (int s = 0; s < kSegs; ++s) sums[s] = make_float4(sums[s].x * f.x, sums[s].y * f.y, sums[s].z * f.x, sums[s].w * f.y);
+    }
+    for (int z = x.first; z < opens; ++z) {
+      f = *reinterpret_cast<const float2*>(stats + z * kStat + 2 * t);
+      const float4* from = reinterpret_cast<const float4*>(base + z * kStages * S::kStage) + lane;
+#pragma unroll
+      for (int s = 0; s < kSegs; ++s) {
+        const float4 y = from[32 * s];
+        sums[s] = make_float4(fmaf(y.x, f.x, sums[s].x), fmaf(y.y, f.y, sums[s].y), fmaf(y.z, f.x, sums[s].z),
+                              fmaf(y.w, f.y, sums[s].w));
+      }
+    }
+    if (final) {
+      const Tile tile = ctl->head[x.last];
+      const float2 k = last_factors(j.lift, j.sum);
+      if (a.lse && lane < tile.rows && lane < kRows) put_lse(a, tile.token, tile.head, tile.row0 + r, G, j.m, j.sum);
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const float k1 = __shfl_sync(0xffffffffu, k.x, 2 * t + z), k2 = __shfl_sync(0xffffffffu, k.y, 2 * t + z);
+        if (2 * t + z >= tile.rows) continue;
+        const int64_t at = row_of(a.out, tile.token, tile.head, tile.row0 + 2 * t + z, G) + 2 * g;
+#pragma unroll
+        for (int s = 0; s < kSegs; ++s)
+          put2(a, at + 16 * s, (z ? sums[s].y : sums[s].x) * k1 * k2, (z ? sums[s].w : sums[s].z) * k1 * k2);
+      }
+    } else {
+      float* ws = a.ws + gridDim.x * (sizeof(Split) / 4) + (2 * (int64_t)blockIdx.x + !x.before) * part_floats(D);
+      if (lane < kRows) {
         put_at(ws + r, j.m, a.ws, a.ws_bytes);
         put_at(ws + kRows + r, j.lift, a.ws, a.ws_bytes);
         put_at(ws + 2 * kRows + r, j.sum, a.ws, a.ws_bytes);
       }
-    }
-  }
-  // (what is read from the workspace is asked for one step ahead)
-  auto ending_at = [&](int i) {
-    if (i >= ended * S::kQuads) return make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    return reinterpret_cast<const float4*>(heads)[((int64_t)blockIdx.x * kWarps + group(i / S::kQuads).last) * S::kQuads + i % S::kQuads];
-  };
-  float4 next = ending_at(threadIdx.x);
-  warps_sync<kWarps>();
-#pragma unroll 1
-  for (int i = threadIdx.x; i < groups * S::kQuads; i += kWarps * 32) {
-    const float4 ending = next;
-    next = ending_at(i + kWarps * 32);
-    const Group y = group(i / S::kQuads);
-    const int e = i % S::kQuads;
-    const Quad qd = quad(e);
-    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    auto add = [&](const float4& q, const float* st) {
-      x = make_float4(fmaf(q.x, st[0], x.x), fmaf(q.y, st[1], x.y), fmaf(q.z, st[0], x.z), fmaf(q.w, st[1], x.w));
-    };
-    const int opens = y.last + !y.closed;
-#pragma unroll 4
-    for (int z = y.first; z < opens; ++z)
-      add(reinterpret_cast<const float4*>(base + z * kStages * S::kStage)[e], stats + z * kStat + qd.row);
-    if (y.closed) add(ending, stats + (kWarps + y.last) * kStat + qd.row);
-    if (!y.closed || y.before) {
-      put_at(part_of(y) + 3 * kRows + 4 * (int64_t)e, x, a.ws, a.ws_bytes);
-      continue;
-    }
-    const Tile& tile = ctl->head[y.last];
 #pragma unroll
-    for (int z = 0; z < 2; ++z) {
-      const int r = qd.row + z;
-      if (r >= tile.rows) break;
-      const float* st = stats + stat(y, y.last) + r;
-      put2(a, row_of(a.out, tile.token, tile.head, tile.row0 + r, G) + qd.d, (z ? x.y : x.x) * st[kRows] * st[2 * kRows],
-           (z ? x.w : x.z) * st[kRows] * st[2 * kRows]);
+      for (int s = 0; s < kSegs; ++s) put_at(reinterpret_cast<float4*>(ws + 3 * kRows) + 32 * s + lane, sums[s], a.ws, a.ws_bytes);
     }
   }
   if (threadIdx.x == 0 && a.ws) {
