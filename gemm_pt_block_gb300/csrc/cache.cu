@@ -1192,35 +1192,52 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
 
 // Joins the parts of the tile that goes on behind CTA blockIdx.x: a warp for a
 // row's statistics, a lane for a part; then as many groups of threads as fit take
-// every so many-th part each.
+// every so many-th part each. How many parts there are is known only when the first
+// load is back: statistics of 32 parts and the first numerators are asked for
+// beside it, whatever they hold.
 constexpr int kJoinThreads = 512;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ AttentionArgs a) {
-  constexpr int kQuads = Attn<D>::kQuads, kGroups = kQuads < kJoinThreads ? kJoinThreads / kQuads : 1;
+  constexpr int kQuads = Attn<D>::kQuads, kGroups = kJoinThreads / kQuads, kEarly = 4;
+  static_assert(kGroups >= 1, "a quad a thread");
   __shared__ float factors[kSms][kRows];
   __shared__ float2 last[kRows];
   __shared__ float4 sums[kGroups > 1 ? kJoinThreads : 1];
-  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
-  ptx::wait_prior_grid();
-  const Split sp = reinterpret_cast<const Split*>(a.ws)[blockIdx.x];
-  if (sp.parts == 0) return;
-  const int G = a.group;
+  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5, group = threadIdx.x / kQuads, e = threadIdx.x % kQuads;
   // part 0 is this CTA's second, the others the first of the CTAs behind it
   const float* parts = a.ws + gridDim.x * (sizeof(Split) / 4) + 2 * (int64_t)blockIdx.x * part_floats(D);
   auto part = [&](int i) { return parts + (2 * i + (i == 0)) * part_floats(D); };
+  const int behind = gridDim.x - blockIdx.x;  // parts that the workspace has room for
+  ptx::wait_prior_grid();
+  const Split sp = reinterpret_cast<const Split*>(a.ws)[blockIdx.x];
+  constexpr int kMost = (kSms + 31) / 32;
+  float m[kMost], lift[kMost], sum[kMost];
+  auto statistics = [&](int i, int count) {
+    const bool some = 32 * i + lane < count;
+    const float* p = part(some ? 32 * i + lane : 0) + (row < kRows ? row : 0);
+    m[i] = p[0];
+    lift[i] = p[kRows];
+    sum[i] = p[2 * kRows];
+  };
+  statistics(0, behind);
+  float4 early[kEarly];
+#pragma unroll
+  for (int k = 0; k < kEarly; ++k) {
+    const int i = group + k * kGroups;
+    early[k] = *reinterpret_cast<const float4*>(part(i < behind ? i : 0) + 3 * kRows + 4 * e);
+  }
+  if (sp.parts == 0) return;
   if (row < kRows) {
-    constexpr int kMost = (kSms + 31) / 32;
-    float m[kMost], lift[kMost], sum[kMost], top = kLowest, high = -INFINITY, all = 0.0f;
+    float top = kLowest, high = -INFINITY, all = 0.0f;
 #pragma unroll
     for (int i = 0; i < kMost; ++i) {
-      const bool some = 32 * i + lane < sp.parts;
-      const float* p = part(some ? 32 * i + lane : 0) + row;
-      m[i] = some ? p[0] : kLowest;
-      lift[i] = some ? p[kRows] : 0.0f;
-      sum[i] = some ? p[2 * kRows] : 0.0f;
+      if (i > 0 && 32 * i < sp.parts) statistics(i, sp.parts);
+      if (32 * i + lane >= sp.parts) {
+        m[i] = kLowest;
+        lift[i] = sum[i] = 0.0f;
+      }
+      top = fmaxf(top, m[i]);
     }
-#pragma unroll
-    for (int i = 0; i < kMost; ++i) top = fmaxf(top, m[i]);
     for (int z = 16; z; z >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, z));
 #pragma unroll
     for (int i = 0; i < kMost; ++i) {
@@ -1236,21 +1253,23 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
       if (32 * i + lane < sp.parts) factors[32 * i + lane][row] = ex2(m[i] - top + lift[i] - high);
     if (lane == 0) {
       last[row] = last_factors(high, all);
-      if (a.lse && row < sp.tile.rows) put_lse(a, sp.tile.token, sp.tile.head, sp.tile.row0 + row, G, top, all);
+      if (a.lse && row < sp.tile.rows) put_lse(a, sp.tile.token, sp.tile.head, sp.tile.row0 + row, a.group, top, all);
     }
   }
   __syncthreads();
-  static_assert(kQuads <= kJoinThreads, "a quad a thread");
-  const int group = threadIdx.x / kQuads, e = threadIdx.x % kQuads;
   const Quad qd = quad(e);
   float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  auto add = [&](int i, const float4& y) {
+    const float f0 = factors[i][qd.row], f1 = factors[i][qd.row + 1];
+    x = make_float4(fmaf(y.x, f0, x.x), fmaf(y.y, f1, x.y), fmaf(y.z, f0, x.z), fmaf(y.w, f1, x.w));
+  };
   if (group < kGroups) {
+#pragma unroll
+    for (int k = 0; k < kEarly; ++k)
+      if (group + k * kGroups < sp.parts) add(group + k * kGroups, early[k]);
 #pragma unroll 8
-    for (int i = group; i < sp.parts; i += kGroups) {
-      const float4 y = *reinterpret_cast<const float4*>(part(i) + 3 * kRows + 4 * e);
-      const float f0 = factors[i][qd.row], f1 = factors[i][qd.row + 1];
-      x = make_float4(fmaf(y.x, f0, x.x), fmaf(y.y, f1, x.y), fmaf(y.z, f0, x.z), fmaf(y.w, f1, x.w));
-    }
+    for (int i = group + kEarly * kGroups; i < sp.parts; i += kGroups)
+      add(i, *reinterpret_cast<const float4*>(part(i) + 3 * kRows + 4 * e));
   }
   if (kGroups > 1) {
     sums[threadIdx.x] = x;
@@ -1266,8 +1285,8 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   for (int i = 0; i < 2; ++i) {
     const int r = qd.row + i;
     if (r < sp.tile.rows)
-      put2(a, row_of(a.out, sp.tile.token, sp.tile.head, sp.tile.row0 + r, G) + qd.d, (i ? x.y : x.x) * last[r].x * last[r].y,
-           (i ? x.w : x.z) * last[r].x * last[r].y);
+      put2(a, row_of(a.out, sp.tile.token, sp.tile.head, sp.tile.row0 + r, a.group) + qd.d,
+           (i ? x.y : x.x) * last[r].x * last[r].y, (i ? x.w : x.z) * last[r].x * last[r].y);
   }
 }
 
