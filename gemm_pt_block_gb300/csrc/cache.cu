@@ -21,6 +21,8 @@ __device__ uint32_t g_cache_error;
 namespace mx {
 namespace {
 
+constexpr int kSms = 152;
+
 __device__ __forceinline__ void index_fail() { atomicExch(&g_cache_error, kErrIndex); }
 
 // One sequence of a call: its rows, its first row's position and its length.
@@ -52,21 +54,6 @@ __device__ __forceinline__ int32_t page_of(const CacheArgs& c, int32_t b, int32_
   return -1;
 }
 
-// The last sequence b with start(b) <= slot, start being monotonic (where it is
-// not, some sequence). start(0) <= slot.
-template <typename F>
-__device__ __forceinline__ int32_t find(int32_t count, int64_t slot, F start) {
-  int32_t lo = 0, hi = count;
-  while (hi - lo > 1) {
-    const int32_t mid = (lo + hi) >> 1;
-    if (start(mid) <= slot)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  return lo;
-}
-
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t v) {
   uint32_t r;
   asm("{.reg .b16 t, u;\n\tmov.b32 {t, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;}" : "=r"(r) : "r"(v));
@@ -93,10 +80,18 @@ __device__ __forceinline__ float scale_value(uint32_t s) {
 }
 
 // ---------------------------------------------------------- append and read ---
+//
+// What one call writes (or reads) of a page is a slot; a slot's keys and values of
+// all heads lie block by block, 2 heads of them. Streams of bytes, bound by HBM:
+// 2 + 1 bytes an element for bf16. For long appends and reads some threads take a
+// block, 32 elements each, and a CTA goes from block to block of its slot with the
+// next one's loads under way; for a token or so a sequence a warp takes a block.
 
-// A block of threads takes one page, one head, keys or values: 32 elements a
-// thread, four vectors of eight.
-constexpr int kPerThread = 32;
+// A slot's sequence and page, tokens [lo, hi) of the page.
+struct Slot {
+  Seq s;
+  int32_t page, at, lo, hi;
+};
 
 // Where each sequence's slots of the grid begin: one for each page that its n
 // rows may touch. Rows that go on inside a page (kExtra 2) touch at most
@@ -104,19 +99,30 @@ constexpr int kPerThread = 32;
 // and floor(end / P) - floor(begin / P) >= floor(n / P).
 template <int kExtra>
 __device__ __forceinline__ int64_t first_slot(const CacheArgs& c, int32_t b, int shift) {
-  return c.starts ? (int64_t)(__ldg(c.starts + b) >> shift) + (int64_t)kExtra * b : b;
+  return (int64_t)(__ldg(c.starts + b) >> shift) + (int64_t)kExtra * b;
 }
 
-// The page a block works on: sequence, page number in it, tokens [lo, hi) of the page.
-struct Task {
-  Seq s;
-  int32_t page, at, lo, hi;
-};
+// The last sequence whose slots begin at or before `slot` (where starts falls, some
+// sequence), by whole warps: 32 places at a time.
 template <int kExtra>
-__device__ __forceinline__ bool task(const CacheArgs& c, Task* t) {
+__device__ __forceinline__ int32_t find_sequence(const CacheArgs& c, int64_t slot, int shift, int lane) {
+  int32_t lo = 0, count = c.sequences;
+  while (count > 1) {
+    const int32_t step = (count + 31) >> 5, at = lo + lane * step;
+    const bool before = at < lo + count && first_slot<kExtra>(c, at, shift) <= slot;
+    const int32_t k = max(__popc(__ballot_sync(0xffffffffu, before)) - 1, 0) * step;
+    count = min(step, count - k);
+    lo += k;
+  }
+  return lo;
+}
+
+// All lanes of a warp; false: nothing to do there.
+template <int kExtra>
+__device__ __forceinline__ bool slot_of(const CacheArgs& c, int lane, Slot* t) {
   const int shift = 31 - __clz(c.page_tokens);
   const int64_t slot = blockIdx.x;
-  const int32_t b = find(c.sequences, slot, [&](int32_t i) { return first_slot<kExtra>(c, i, shift); });
+  const int32_t b = c.starts ? find_sequence<kExtra>(c, slot, shift, lane) : (int32_t)slot;
   if (!rows_of(c, b, &t->s)) return false;
   if (kExtra == 2) {
     t->s.len = __ldg(c.lens + b);
@@ -129,7 +135,7 @@ __device__ __forceinline__ bool task(const CacheArgs& c, Task* t) {
     index_fail();
     return false;
   }
-  const int64_t k = slot - first_slot<kExtra>(c, b, shift);
+  const int64_t k = c.starts ? slot - first_slot<kExtra>(c, b, shift) : 0;
   const int32_t first = t->s.pos >> shift;
   if (t->s.n == 0 || k < 0 || first + k > (t->s.len - 1) >> shift) return false;
   t->at = (first + (int32_t)k) << shift;
@@ -140,93 +146,221 @@ __device__ __forceinline__ bool task(const CacheArgs& c, Task* t) {
   return true;
 }
 
+// The E8M0 scale of a block whose largest magnitude has the bits m (as whole
+// numbers: magnitudes, then infinity, then NaN): 448 = 1.75 * 2^8, one more where
+// the fraction passes it.
+__device__ __forceinline__ uint32_t scale_for(uint32_t m) {
+  return m >= 0x7F800000u ? 255u : (uint32_t)max((int)(m >> 23) - 8 + ((m & 0x7FFFFFu) > 0x600000u), 0);
+}
+// What values are multiplied by under a scale, and older codes where it grows (below
+// 2^-30 every code rounds to zero).
+__device__ __forceinline__ float scale_factor(uint32_t scale) {
+  return scale == 255u ? 0.0f : __uint_as_float((254u - scale) << 23);
+}
+__device__ __forceinline__ float older_factor(uint32_t old, uint32_t scale) {
+  return __uint_as_float((127u - min(scale - old, 64u)) << 23);
+}
+__device__ __forceinline__ uint32_t scaled4(uint32_t codes, float f) {
+  float v[4];
+  values4(codes, v);
+  return e4m3x4(v[0] * f, v[1] * f, v[2] * f, v[3] * f);
+}
+__device__ __forceinline__ float most8(float m, const float (&f)[8]) {
+  return absmax3_nan(absmax3_nan(m, f[0], f[1]), absmax3_nan(f[2], f[3], f[4]), absmax3_nan(f[5], f[6], f[7]));
+}
+__device__ __forceinline__ uint2 quantized8(const float (&f)[8], float mul, uint32_t scale) {
+  if (scale == 255u) return make_uint2(0u, 0u);
+  return make_uint2(e4m3x4(f[0] * mul, f[1] * mul, f[2] * mul, f[3] * mul),
+                    e4m3x4(f[4] * mul, f[5] * mul, f[6] * mul, f[7] * mul));
+}
+
+// A few new tokens a page: a warp takes a block, eight elements a lane. Values
+// past the first 256 are read twice.
 template <typename T>
-__global__ void __launch_bounds__(1024) cache_append_kernel(CacheArgs c, Heads k, Heads v) {
-  __shared__ uint32_t most[32];
-  Task t;
-  if (!task<2>(c, &t)) return;
-  const int h = blockIdx.y >> 1, kind = blockIdx.y & 1, per = c.head_dim >> 3;
+__global__ void __launch_bounds__(256) cache_append_few_kernel(CacheArgs c, Heads k, Heads v) {
+  const int lane = threadIdx.x & 31, task = blockIdx.y * 8 + (threadIdx.x >> 5);
+  if (task >= 2 * c.heads) return;
+  Slot t;
+  if (!slot_of<2>(c, lane, &t)) return;
+  const int kind = task >= c.heads, h = task - kind * c.heads, per = c.head_dim >> 3;
   const Heads& x = kind ? v : k;
-  const int64_t block = ((int64_t)t.page * 2 + kind) * c.heads + h;
+  const int64_t block = (int64_t)t.page * 2 * c.heads + task;
   uint8_t* codes = c.codes + block * c.page_tokens * c.head_dim;
-  float f[kPerThread / 8][8];
-  float m = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kPerThread / 8; ++i) {
-    const int at = i * blockDim.x + threadIdx.x, token = at / per, d = (at - token * per) * 8;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[i][j] = 0.0f;
-    if (token >= t.lo && token < t.hi) {
-      const int64_t row = t.s.row + (t.at + token - t.s.pos);
-      Vec8<T> w;
-      load8(static_cast<const T*>(x.p) + row * x.ld_t + (int64_t)h * x.ld_h + d, w);
-      unpack8(w, f[i]);
-      m = absmax3_nan(m, absmax3_nan(f[i][0], f[i][1], f[i][2]),
-                      absmax3_nan(absmax3_nan(f[i][3], f[i][4], f[i][5]), f[i][6], f[i][7]));
-    }
-  }
-  // as whole numbers: magnitudes, then infinity, then NaN
-  uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(m) & 0x7FFFFFFFu);
-  if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = bits;
   const uint32_t old = t.lo > 0 ? c.scales[block] : 0u;
-  __syncthreads();
-  bits = 0;
-  for (int w = 0; w < (int)(blockDim.x + 31) >> 5; ++w) bits = max(bits, most[w]);
-  // 448 = 1.75 * 2^8: one more where the fraction passes it
-  uint32_t scale = bits >= 0x7F800000u ? 255u : (uint32_t)max((int)(bits >> 23) - 8 + ((bits & 0x7FFFFFu) > 0x600000u), 0);
-  scale = max(scale, old);
-  const float mul = scale == 255u ? 0.0f : __uint_as_float((254u - scale) << 23);
-  const bool shrink = t.lo > 0 && old < scale && scale != 255u;
-  // (below 2^-30 every older code rounds to zero)
-  const float less = __uint_as_float((127u - min(scale - old, 64u)) << 23);
-#pragma unroll
-  for (int i = 0; i < kPerThread / 8; ++i) {
-    const int at = i * blockDim.x + threadIdx.x, token = at / per, d = (at - token * per) * 8;
-    uint2* to = reinterpret_cast<uint2*>(codes + token * c.head_dim + d);
-    if (token >= t.lo && token < t.hi) {
-      uint2 q = make_uint2(e4m3x4(f[i][0] * mul, f[i][1] * mul, f[i][2] * mul, f[i][3] * mul),
-                           e4m3x4(f[i][4] * mul, f[i][5] * mul, f[i][6] * mul, f[i][7] * mul));
-      if (scale == 255u) q = make_uint2(0u, 0u);
-      put_at(to, q, c.codes, c.codes_bytes);
-    } else if (shrink && token < t.lo) {
-      const uint2 q = *to;
-      float a[4], b[4];
-      values4(q.x, a);
-      values4(q.y, b);
-      put_at(to, make_uint2(e4m3x4(a[0] * less, a[1] * less, a[2] * less, a[3] * less),
-                            e4m3x4(b[0] * less, b[1] * less, b[2] * less, b[3] * less)),
-             c.codes, c.codes_bytes);
+  const T* from = static_cast<const T*>(x.p) + (int64_t)(t.s.row + (t.at + t.lo - t.s.pos)) * x.ld_t + (int64_t)h * x.ld_h;
+  const int count = (t.hi - t.lo) * per;
+  auto take = [&](int i, float (&f)[8]) {
+    const int token = i / per;
+    Vec8<T> w;
+    load8(from + token * x.ld_t + (i - token * per) * 8, w);
+    unpack8(w, f);
+  };
+  float first[8] = {}, f[8];
+  if (lane < count) take(lane, first);
+  float m = most8(0.0f, first);
+  for (int i = lane + 32; i < count; i += 32) {
+    take(i, f);
+    m = most8(m, f);
+  }
+  const uint32_t scale = max(scale_for(__reduce_max_sync(0xffffffffu, __float_as_uint(m) & 0x7FFFFFFFu)), old);
+  const float mul = scale_factor(scale);
+  uint2* to = reinterpret_cast<uint2*>(codes) + t.lo * per;
+  if (lane < count) put_at(to + lane, quantized8(first, mul, scale), c.codes, c.codes_bytes);
+  for (int i = lane + 32; i < count; i += 32) {
+    take(i, f);
+    put_at(to + i, quantized8(f, mul, scale), c.codes, c.codes_bytes);
+  }
+  if (t.lo > 0 && old < scale && scale != 255u) {
+    const float less = older_factor(old, scale);
+    uint2* older = reinterpret_cast<uint2*>(codes);
+    for (int i = lane; i < t.lo * per; i += 32) {
+      const uint2 q = older[i];
+      put_at(older + i, make_uint2(scaled4(q.x, less), scaled4(q.y, less)), c.codes, c.codes_bytes);
     }
   }
-  if (threadIdx.x == 0) put_at(c.scales + block, (uint8_t)scale, c.scales, c.scales_bytes);
+  if (lane == 0) put_at(c.scales + block, (uint8_t)scale, c.scales, c.scales_bytes);
+}
+
+// How threads share blocks: `each` of them (whole warps) take a block, two vectors
+// of sixteen elements a thread, `at_once` blocks of a slot at a time.
+struct Share {
+  int32_t each, at_once;
+};
+
+template <typename T, int kMost>
+__global__ void __launch_bounds__(kMost) cache_append_kernel(CacheArgs c, Heads k, Heads v, Share sh) {
+  __shared__ uint32_t most[2][32];
+  Slot t;
+  if (!slot_of<2>(c, threadIdx.x & 31, &t)) return;
+  const int mine = threadIdx.x / sh.each, in = threadIdx.x - mine * sh.each, per = c.head_dim >> 4;
+  const int blocks = 2 * c.heads, stride = gridDim.y * sh.at_once;
+  int token[2], d[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int at = in + i * sh.each;
+    token[i] = at / per;
+    d[i] = (at - token[i] * per) << 4;
+  }
+  const int64_t row0 = t.s.row + (t.at - t.s.pos);
+  Vec16<T> ahead[2];
+  uint32_t ahead_old = 0;
+  auto fetch = [&](int task) {
+    const int kind = task >= c.heads, h = task - kind * c.heads;
+    const Heads& x = kind ? v : k;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (token[i] < t.lo || token[i] >= t.hi) continue;
+      const T* p = static_cast<const T*>(x.p) + (row0 + token[i]) * x.ld_t + (int64_t)h * x.ld_h + d[i];
+      load16e(p, on32(p), ahead[i]);
+    }
+    if (t.lo > 0) ahead_old = c.scales[(int64_t)t.page * blocks + task];
+  };
+  int task = blockIdx.y * sh.at_once + mine;
+  if (task < blocks) fetch(task);
+  // (all threads go round alike: a CTA's blocks end together)
+  for (int round = 0; blockIdx.y * sh.at_once + round * stride < blocks; ++round, task += stride) {
+    const bool some = task < blocks;
+    const uint32_t old = ahead_old;
+    const Vec16<T> now[2] = {ahead[0], ahead[1]};
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (some && token[i] >= t.lo && token[i] < t.hi) {
+        float2 f[8];
+        unpack16(now[i], f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = absmax3_nan(m, f[j].x, f[j].y);
+      }
+    }
+    if (task + stride < blocks) fetch(task + stride);
+    const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(m) & 0x7FFFFFFFu);
+    uint32_t all = bits;
+    if (sh.each > 32) {
+      uint32_t* slots = most[round & 1];
+      if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = bits;
+      __syncthreads();
+      const int w0 = mine * sh.each >> 5;
+      for (int w = 0; w < sh.each >> 5; ++w) all = max(all, slots[w0 + w]);
+    }
+    if (!some) continue;
+    const int64_t block = (int64_t)t.page * blocks + task;
+    uint8_t* codes = c.codes + block * c.page_tokens * c.head_dim;
+    const uint32_t scale = max(scale_for(all), old);
+    const float mul = scale_factor(scale);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint4* to = reinterpret_cast<uint4*>(codes + token[i] * c.head_dim + d[i]);
+      if (token[i] >= t.lo && token[i] < t.hi) {
+        float2 f[8];
+        unpack16(now[i], f);
+        uint4 q = make_uint4(0u, 0u, 0u, 0u);
+        if (scale != 255u)
+          q = make_uint4(e4m3x4(f[0].x * mul, f[0].y * mul, f[1].x * mul, f[1].y * mul),
+                         e4m3x4(f[2].x * mul, f[2].y * mul, f[3].x * mul, f[3].y * mul),
+                         e4m3x4(f[4].x * mul, f[4].y * mul, f[5].x * mul, f[5].y * mul),
+                         e4m3x4(f[6].x * mul, f[6].y * mul, f[7].x * mul, f[7].y * mul));
+        put_at(to, q, c.codes, c.codes_bytes);
+      } else if (token[i] < t.lo && old < scale && scale != 255u) {
+        const float less = older_factor(old, scale);
+        const uint4 q = *to;
+        put_at(to, make_uint4(scaled4(q.x, less), scaled4(q.y, less), scaled4(q.z, less), scaled4(q.w, less)), c.codes,
+               c.codes_bytes);
+      }
+    }
+    if (in == 0) put_at(c.scales + block, (uint8_t)scale, c.scales, c.scales_bytes);
+  }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(1024) cache_read_kernel(CacheArgs c, Heads k, Heads v) {
-  Task t;
-  if (!task<1>(c, &t)) return;
-  const int h = blockIdx.y >> 1, kind = blockIdx.y & 1, per = c.head_dim >> 3;
-  const Heads& x = kind ? v : k;
-  const int64_t block = ((int64_t)t.page * 2 + kind) * c.heads + h;
-  const uint8_t* codes = c.codes + block * c.page_tokens * c.head_dim;
-  const float mul = scale_value(c.scales[block]);
+__global__ void __launch_bounds__(1024) cache_read_kernel(CacheArgs c, Heads k, Heads v, Share sh) {
+  Slot t;
+  if (!slot_of<1>(c, threadIdx.x & 31, &t)) return;
+  const int mine = threadIdx.x / sh.each, in = threadIdx.x - mine * sh.each, per = c.head_dim >> 4;
+  const int blocks = 2 * c.heads, stride = gridDim.y * sh.at_once;
+  int token[2], d[2];
 #pragma unroll
-  for (int i = 0; i < kPerThread / 8; ++i) {
-    const int at = i * blockDim.x + threadIdx.x, token = at / per, d = (at - token * per) * 8;
-    if (token < t.hi) {
-      const uint2 q = *reinterpret_cast<const uint2*>(codes + token * c.head_dim + d);
-      float a[4], b[4];
-      values4(q.x, a);
-      values4(q.y, b);
-      float f[8];
+  for (int i = 0; i < 2; ++i) {
+    const int at = in + i * sh.each;
+    token[i] = at / per;
+    d[i] = (at - token[i] * per) << 4;
+  }
+  uint4 ahead[2];
+  uint32_t ahead_scale = 0;
+  auto fetch = [&](int task) {
+    const int64_t block = (int64_t)t.page * blocks + task;
+    const uint8_t* codes = c.codes + block * c.page_tokens * c.head_dim;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        f[j] = a[j] * mul;
-        f[j + 4] = b[j] * mul;
+    for (int i = 0; i < 2; ++i)
+      if (token[i] < t.hi) ahead[i] = load16(codes + token[i] * c.head_dim + d[i]);
+    ahead_scale = c.scales[block];
+  };
+  int task = blockIdx.y * sh.at_once + mine;
+  if (task < blocks) fetch(task);
+  for (; task < blocks; task += stride) {
+    const uint4 now[2] = {ahead[0], ahead[1]};
+    const float mul = scale_value(ahead_scale);
+    if (task + stride < blocks) fetch(task + stride);
+    const int kind = task >= c.heads, h = task - kind * c.heads;
+    const Heads& x = kind ? v : k;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (token[i] >= t.hi) continue;
+      const uint32_t q[4] = {now[i].x, now[i].y, now[i].z, now[i].w};
+      T* to = static_cast<T*>(x.p) + (int64_t)(t.s.row + t.at + token[i]) * x.ld_t + (int64_t)h * x.ld_h + d[i];
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        float a[4], b[4], f[8];
+        values4(q[2 * z], a);
+        values4(q[2 * z + 1], b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f[j] = a[j] * mul;
+          f[j + 4] = b[j] * mul;
+        }
+        Vec8<T> w;
+        pack8(f, w);
+        store8(to + 8 * z, w, x.p, x.bytes);
       }
-      Vec8<T> w;
-      pack8(f, w);
-      store8(static_cast<T*>(x.p) + (int64_t)(t.s.row + t.at + token) * x.ld_t + (int64_t)h * x.ld_h + d, w, x.p, x.bytes);
     }
   }
 }
@@ -251,7 +385,6 @@ __global__ void __launch_bounds__(1024) cache_read_kernel(CacheArgs c, Heads k, 
 // the CTA when its runs end; those that several CTAs share leave their parts in
 // the workspace for cache_join_kernel.
 
-constexpr int kSms = 152;
 constexpr float kTop = 15.0f;                   // weights are held times 2^15: f16 keeps 2^-39 of the largest
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr int kMostWarps = 15, kMostStages = 8;
@@ -1292,28 +1425,53 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
 
 }  // namespace
 
+namespace {
+// A block's threads, blocks at once and a slot's CTAs: about 256 threads to a CTA,
+// which goes round at most four times (the lookups before a CTA's first load cost as
+// much as a round: 15503 tokens in bf16 24.7 us with one round, 21.7 with two, 20.6
+// with four; read back, 63622 tokens, 81, 76 and 73, and 79 with sixteen, whose CTAs
+// end unevenly), and fewer times where there are not six CTAs an SM otherwise.
+struct Launch {
+  Share share;
+  dim3 grid, block;
+};
+Launch launch_shape(const CacheArgs& c, int64_t slots) {
+  Launch l;
+  l.share.each = (c.page_tokens * c.head_dim / 32 + 31) / 32 * 32;
+  l.share.at_once = l.share.each < 256 ? 256 / l.share.each : 1;
+  const int blocks = 2 * c.heads, threads = l.share.each * l.share.at_once, most = (blocks + l.share.at_once - 1) / l.share.at_once;
+  const int64_t fill = ((int64_t)kSms * 6 * 256 + slots * threads - 1) / (slots * threads), four = (most + 3) / 4;
+  const int64_t want = fill > four ? fill : four;
+  l.grid = dim3((unsigned)slots, (unsigned)(want < most ? want : most));
+  l.block = dim3((unsigned)threads);
+  return l;
+}
+}  // namespace
+
 cudaError_t launch_cache_append(const CacheArgs& c, const Heads& k, const Heads& v, bool f32, cudaStream_t st) {
   if (c.tokens == 0 || c.sequences == 0) return cudaSuccess;
   (void)cudaGetLastError();
   const int64_t slots = c.starts ? c.tokens / c.page_tokens + 2 * (int64_t)c.sequences : c.sequences;
-  const dim3 grid((unsigned)slots, (unsigned)(2 * c.heads));
-  const int threads = c.page_tokens * c.head_dim / kPerThread;
-  if (f32)
-    cache_append_kernel<float><<<grid, threads, 0, st>>>(c, k, v);
-  else
-    cache_append_kernel<uint16_t><<<grid, threads, 0, st>>>(c, k, v);
+  if (c.tokens <= 4 * (int64_t)c.sequences) {
+    const dim3 grid((unsigned)slots, (unsigned)((2 * c.heads + 7) / 8));
+    if (f32)
+      cache_append_few_kernel<float><<<grid, 256, 0, st>>>(c, k, v);
+    else
+      cache_append_few_kernel<uint16_t><<<grid, 256, 0, st>>>(c, k, v);
+    return cudaGetLastError();
+  }
+  const Launch l = launch_shape(c, slots);
+  (f32 ? l.block.x <= 512 ? cache_append_kernel<float, 512> : cache_append_kernel<float, 1024>
+       : l.block.x <= 512 ? cache_append_kernel<uint16_t, 512> : cache_append_kernel<uint16_t, 1024>)
+      <<<l.grid, l.block, 0, st>>>(c, k, v, l.share);
   return cudaGetLastError();
 }
 
 cudaError_t launch_cache_read(const CacheArgs& c, const Heads& k, const Heads& v, bool f32, cudaStream_t st) {
   if (c.tokens == 0 || c.sequences == 0) return cudaSuccess;
   (void)cudaGetLastError();
-  const dim3 grid((unsigned)(c.tokens / c.page_tokens + (int64_t)c.sequences), (unsigned)(2 * c.heads));
-  const int threads = c.page_tokens * c.head_dim / kPerThread;
-  if (f32)
-    cache_read_kernel<float><<<grid, threads, 0, st>>>(c, k, v);
-  else
-    cache_read_kernel<uint16_t><<<grid, threads, 0, st>>>(c, k, v);
+  const Launch l = launch_shape(c, c.tokens / c.page_tokens + (int64_t)c.sequences);
+  (f32 ? cache_read_kernel<float> : cache_read_kernel<uint16_t>)<<<l.grid, l.block, 0, st>>>(c, k, v, l.share);
   return cudaGetLastError();
 }
 

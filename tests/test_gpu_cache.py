@@ -31,6 +31,9 @@ APPENDS = [
     ([17, 16, 33, 40, 15], [17, 16, 1, 25, 15], 3, 64, 16), ([200, 0, 90, 31], [130, 0, 90, 0], 2, 96, 32),
     ([1000, 555], [1000, 300], 4, 192, 128), ([129, 7, 300], [129, 3, 172], 5, 256, 128),
     ([2000], [1999], 1, 256, 16), ([63, 64, 65], [62, 63, 64], 16, 96, 64),
+    ([50, 3, 100, 17], [50, 2, 41, 17], 3, 96, 16), ([300, 9, 64], [3, 2, 4], 9, 256, 64),
+    ([i % 70 + 1 for i in range(700)], [i % 3 if i % 70 > 3 else 1 for i in range(700)], 2, 64, 16),
+    ([300 + i for i in range(40)], [100 + 3 * i for i in range(40)], 2, 128, 32),
 ]
 
 
