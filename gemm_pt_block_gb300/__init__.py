@@ -72,3 +72,4 @@ from .binding import (  # noqa: F401
 )
 from .linear import LinearRecipe, Mxfp4Linear, mxfp4_linear, recipe_1d, recipe_2d_sr  # noqa: F401
 from .ffn import Mxfp4FeedForward, rmsnorm, swiglu  # noqa: F401
+from .attention import KvCache, Mxfp4Attention  # noqa: F401

@@ -186,3 +186,37 @@ def test_a_failed_load_says_why(monkeypatch):
     monkeypatch.setitem(sys.modules, "gemm_pt_block_gb300._cache_binding", None)
     with pytest.raises(RuntimeError, match="does not load .*_cache_binding.*build"):
         mx.mxfp8_cache_read(torch.zeros(1), torch.zeros(1), torch.zeros(1), torch.zeros(1), 1)
+
+
+def test_the_block_refuses_sizes_off_the_tiles():
+    import gemm_pt_block_gb300 as mx
+
+    for kw in (dict(dim=200, heads=2, head_dim=128), dict(dim=256, heads=3, kv_heads=2), dict(dim=256, heads=3, head_dim=64),
+               dict(dim=256, heads=2, kv_heads=0, head_dim=64)):
+        with pytest.raises(ValueError):
+            mx.Mxfp4Attention(**kw)
+    block = mx.Mxfp4Attention(256, 4, 2, 64)
+    with pytest.raises(RuntimeError, match="quantize_weights"):
+        block.decode(torch.zeros(1, 256), None, None, None)
+    assert set(block.state_dict()) == {"norm", "qkv.weight", "out.weight"}
+
+
+def test_waits_are_whole_warps():
+    """The attention kernel's waits, read from the source: every loop that waits on a barrier has a limit, and
+    code of whole warps goes on or leaves together."""
+    import os
+    import re
+
+    import gemm_pt_block_gb300 as mx
+
+    with open(os.path.join(os.path.dirname(mx.__file__), "csrc", "cache.cu")) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    tries = [m.start() for m in re.finditer(r"mbar_try_wait(_sleep)?\(", text)]
+    assert len(tries) == 5
+    for at in tries:
+        around = text[max(0, at - 400):at + 700]
+        assert "kWaitLimitNs" in around
+    for name in ("wait_bar_warp", "wait_bars"):
+        body = text[text.index(f"bool {name}("):]
+        body = body[:body.index("\n}")]
+        assert "__all_sync" in body and "kWaitLimitNs" in body
