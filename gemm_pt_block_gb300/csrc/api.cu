@@ -795,8 +795,8 @@ mxfp4_status check_q_heads(const char* fn, mx::AttentionArgs* a, int32_t q_heads
   const mx::CacheArgs& c = a->c;
   if (q_heads < 1 || q_heads > 65535 || q_heads % c.heads != 0)
     return fail(MXFP4_ERR_SHAPE, "%s: q_heads (%d) must be a multiple of heads (%d), 1 to 65535", fn, q_heads, c.heads);
-  if ((int64_t)c.tokens * q_heads >= (int64_t)1 << 31)
-    return fail(MXFP4_ERR_SHAPE, "%s: tokens (%d) * q_heads (%d) must be below 2^31", fn, c.tokens, q_heads);
+  if ((int64_t)c.tokens * q_heads >= (int64_t)1 << 30)
+    return fail(MXFP4_ERR_SHAPE, "%s: tokens (%d) * q_heads (%d) must be below 2^30", fn, c.tokens, q_heads);
   a->q_heads = q_heads;
   a->group = q_heads / c.heads;
   a->shift = c.page_tokens == 16 ? 4 : c.page_tokens == 32 ? 5 : c.page_tokens == 64 ? 6 : 7;

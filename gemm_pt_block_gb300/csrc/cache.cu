@@ -550,11 +550,11 @@ struct Walk {
     const int G = a.group;
     b = s;
     row = x.row;
-    n = x.end - x.row;
-    if (x.row < 0 || x.end < x.row || x.end > a.c.tokens) {
+    n = 0;
+    if (x.row < 0 || x.end < x.row || x.end > a.c.tokens)
       index_fail();
-      n = 0;
-    }
+    else
+      n = x.end - x.row;
     if (n == 0) return 0;
     len = x.len;
     const int32_t most = a.c.max_pages * a.c.page_tokens;
@@ -891,17 +891,15 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
   float o[kSegs][4], m[2], lift[2], sum[2], slope[2], unit_q[2];
   int32_t pos[2];
   auto clear = [&]() {
-    {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        m[i] = kLowest;
-        lift[i] = sum[i] = 0.0f;
-      }
-#pragma unroll
-      for (int s = 0; s < kSegs; ++s)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[s][i] = 0.0f;
+    for (int i = 0; i < 2; ++i) {
+      m[i] = kLowest;
+      lift[i] = sum[i] = 0.0f;
     }
+#pragma unroll
+    for (int s = 0; s < kSegs; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[s][i] = 0.0f;
   };
   clear();
   int32_t stage = 0;
@@ -914,43 +912,38 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
   for (int32_t u = 0; u < units; ++u) {
     if (u == 0 || w.unit == 0) {
       // queries of this tile, row by row times a power of two: the largest in [2^14, 2^15)
-      const int32_t rows = w.n * G - w.row0;
-      {
-        const int32_t r = g;
-        uint2 x[kSegs];
-        uint32_t top = 0;
-        if (r < rows) {
-          const uint16_t* q = static_cast<const uint16_t*>(a.q.p) + row_of(a.q, w.row, w.head, w.row0 + r, G) + 4 * t;
+      uint2 x[kSegs];
+      uint32_t top = 0;
 #pragma unroll
-          for (int s = 0; s < kSegs; ++s) x[s] = __ldg(reinterpret_cast<const uint2*>(q + 16 * s));
-        } else {
+      for (int s = 0; s < kSegs; ++s) x[s] = make_uint2(0u, 0u);
+      if (w.row0 + g < w.n * G) {
+        const uint16_t* q = static_cast<const uint16_t*>(a.q.p) + row_of(a.q, w.row, w.head, w.row0 + g, G) + 4 * t;
 #pragma unroll
-          for (int s = 0; s < kSegs; ++s) x[s] = make_uint2(0u, 0u);
-        }
+        for (int s = 0; s < kSegs; ++s) x[s] = __ldg(reinterpret_cast<const uint2*>(q + 16 * s));
+      }
 #pragma unroll
-        for (int s = 0; s < kSegs; ++s)
-          top = max(max(top, max((x[s].x << 16) & 0x7FFFFFFFu, x[s].x & 0x7FFF0000u)),
-                    max((x[s].y << 16) & 0x7FFFFFFFu, x[s].y & 0x7FFF0000u));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = max((int)(top >> 23), 1);  // value = f16 * 2^(e - 141)
-        const float f1 = pow2i(min(141 - e, 126)), f2 = pow2i(max(141 - e - 126, 0));
+      for (int s = 0; s < kSegs; ++s)
+        top = max(max(top, max((x[s].x << 16) & 0x7FFFFFFFu, x[s].x & 0x7FFF0000u)),
+                  max((x[s].y << 16) & 0x7FFFFFFFu, x[s].y & 0x7FFF0000u));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int e = max((int)(top >> 23), 1);  // value = f16 * 2^(e - 141); 255: no number
+      const float f1 = pow2i(min(141 - e, 126)), f2 = pow2i(max(141 - e - 126, 0));
 #pragma unroll
-        for (int s = 0; s < kSegs; ++s) {
-          const float2 lo = unpack2(x[s].x), hi = unpack2(x[s].y);
-          qf[s][0] = e == 255 ? 0u : f16x2(lo.x * f1 * f2, lo.y * f1 * f2);
-          qf[s][1] = e == 255 ? 0u : f16x2(hi.x * f1 * f2, hi.y * f1 * f2);
-        }
-        // 2^(e - 141), down to 2^-140
-        const float uq = e == 255 ? __uint_as_float(0x7FC00000u) : e > 14 ? pow2i(e - 141) : __uint_as_float(1u << (e + 8));
-        unit_q[0] = __shfl_sync(0xffffffffu, uq, 8 * t);
-        unit_q[1] = __shfl_sync(0xffffffffu, uq, 8 * t + 4);
+      for (int s = 0; s < kSegs; ++s) {
+        const float2 lo = unpack2(x[s].x), hi = unpack2(x[s].y);
+        qf[s][0] = e == 255 ? 0u : f16x2(lo.x * f1 * f2, lo.y * f1 * f2);
+        qf[s][1] = e == 255 ? 0u : f16x2(hi.x * f1 * f2, hi.y * f1 * f2);
+      }
+      // 2^(e - 141), down to 2^-140
+      const float uq = e == 255 ? __uint_as_float(0x7FC00000u) : e > 14 ? pow2i(e - 141) : __uint_as_float(1u << (e + 8));
+      // (the lanes' scores are of rows 2 t and 2 t + 1)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int32_t c = min(w.row0 + 2 * t + i, w.n * G - 1);
-          pos[i] = w.len - w.n + c / G;
-          slope[i] = a.slopes ? __ldg(a.slopes + w.head * G + c % G) * 1.44269504088896f : 0.0f;
-        }
+      for (int i = 0; i < 2; ++i) {
+        unit_q[i] = __shfl_sync(0xffffffffu, uq, 8 * t + 4 * i);
+        const int32_t r = min(w.row0 + 2 * t + i, w.n * G - 1);
+        pos[i] = w.len - w.n + r / G;
+        slope[i] = a.slopes ? __ldg(a.slopes + w.head * G + r % G) * 1.44269504088896f : 0.0f;
       }
     }
 
@@ -965,7 +958,7 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
 #pragma unroll
       for (int h = 0; h < kParts; ++h)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[h][i] = 0.0f;
+        for (int i = 0; i < 4; ++i) s[h][i] = 0.0f;
       {
         const uint32_t at = lane_at + stage * S::kStage;
 #pragma unroll
@@ -978,7 +971,7 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
             for (int z = 0; z < 2; ++z) {
               const uint32_t a0 = e4m3x2_f16x2(r[2 * z]), a2 = e4m3x2_f16x2(r[2 * z] >> 16);
               const uint32_t a1 = e4m3x2_f16x2(r[2 * z + 1]), a3 = e4m3x2_f16x2(r[2 * z + 1] >> 16);
-            mma(s[h + z], a0, a1, a2, a3, qf[i][0], qf[i][1]);
+              mma(s[h + z], a0, a1, a2, a3, qf[i][0], qf[i][1]);
             }
           }
         }
@@ -995,27 +988,25 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
 #pragma unroll
       for (int h = 0; h < kParts; ++h) {
         const float ks = scale_value(__shfl_sync(0xffffffffu, scale, h));
-        {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float f = unit_q[i] * ks;  // (exact)
-            if (a.softcap > 0.0f) {
+        for (int i = 0; i < 2; ++i) {
+          const float f = unit_q[i] * ks;  // (a power of two)
+          if (a.softcap > 0.0f) {
 #pragma unroll
-              for (int z = i; z < 4; z += 2) s[h][z] = a.softcap * 1.44269504088896f * tanhf(s[h][z] * (f * cap));
-            } else {
-              s[h][i] *= f * scale2;
-              s[h][i + 2] *= f * scale2;
-            }
-            const int32_t j1 = c0 + 16 * h + g - pos[i];  // token's position less the row's
-            if (a.slopes) {
-              s[h][i] += slope[i] * (float)j1;
-              s[h][i + 2] += slope[i] * (float)(j1 + 8);
-            }
-            if (!whole) {
-              const int32_t most = a.window > 0 ? a.window : 0x7FFFFFFF;
-              if (j1 > 0 || j1 <= -most) s[h][i] = -INFINITY;
-              if (j1 + 8 > 0 || j1 + 8 <= -most) s[h][i + 2] = -INFINITY;
-            }
+            for (int z = i; z < 4; z += 2) s[h][z] = a.softcap * 1.44269504088896f * tanhf(s[h][z] * (f * cap));
+          } else {
+            s[h][i] *= f * scale2;
+            s[h][i + 2] *= f * scale2;
+          }
+          const int32_t j = c0 + 16 * h + g - pos[i];  // the token's position less the row's
+          if (a.slopes) {
+            s[h][i] += slope[i] * (float)j;
+            s[h][i + 2] += slope[i] * (float)(j + 8);
+          }
+          if (!whole) {
+            const int32_t most = a.window > 0 ? a.window : 0x7FFFFFFF;
+            if (j > 0 || j <= -most) s[h][i] = -INFINITY;
+            if (j + 8 > 0 || j + 8 <= -most) s[h][i + 2] = -INFINITY;
           }
         }
       }
@@ -1046,64 +1037,62 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
       uint32_t pf[kParts][2], pl[kParts][2];
       bool moved = false;
       float keep[2];
-      {
-        float cm[2];
+      float cm[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float part[kParts], x = -INFINITY;
-#pragma unroll
-          for (int h = 0; h < kParts; ++h) {
-            part[h] = fmaxf(s[h][i], s[h][i + 2]);
-            x = fmaxf(x, part[h]);
-          }
-#pragma unroll
-          for (int z = 4; z < 32; z <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, z));
-          cm[i] = fmaxf(m[i], x);
-          float y = x - cm[i] + ev[0];
-          if (!one) {
-            y = -INFINITY;
-#pragma unroll
-            for (int h = 0; h < kParts; ++h) y = fmaxf(y, part[h] - cm[i] + ev[h]);
-#pragma unroll
-            for (int z = 4; z < 32; z <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, z));
-          }
-          const float down = m[i] - cm[i], was = down + lift[i], now = fmaxf(was, y);
-          sum[i] *= ex2(down);
-          keep[i] = ex2(was - now);
-          moved |= was != now;
-          m[i] = cm[i];
-          lift[i] = now;
-        }
+      for (int i = 0; i < 2; ++i) {
+        float part[kParts], x = -INFINITY;
 #pragma unroll
         for (int h = 0; h < kParts; ++h) {
-          const float c[2] = {ev[h] + kTop - lift[0], ev[h] + kTop - lift[1]};
-          float p[4];
+          part[h] = fmaxf(s[h][i], s[h][i + 2]);
+          x = fmaxf(x, part[h]);
+        }
 #pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            const float x = s[h][z] - cm[z & 1];
-            sum[z & 1] += ex2(x);
-            p[z] = ex2(x + c[z & 1]);
-          }
-          if (ev[h] != ev[h]) {
-            // values that are no numbers: where a row attends them
+        for (int z = 4; z < 32; z <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, z));
+        cm[i] = fmaxf(m[i], x);
+        float y = x - cm[i] + ev[0];
+        if (!one) {
+          y = -INFINITY;
 #pragma unroll
-            for (int z = 0; z < 4; ++z) p[z] = s[h][z] == -INFINITY ? 0.0f : ev[h];
-          }
-          const uint32_t u0 = f16x2(p[0], p[1]), u1 = f16x2(p[2], p[3]);
-          pf[h][0] = transposed(u0);
-          pf[h][1] = transposed(u1);
-          if (kExact) {
-            const float2 q0 = f16x2_f32(u0), q1 = f16x2_f32(u1);
-            pl[h][0] = transposed(f16x2(p[0] - q0.x, p[1] - q0.y));
-            pl[h][1] = transposed(f16x2(p[2] - q1.x, p[3] - q1.y));
-          }
+          for (int h = 0; h < kParts; ++h) y = fmaxf(y, part[h] - cm[i] + ev[h]);
+#pragma unroll
+          for (int z = 4; z < 32; z <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, z));
+        }
+        const float down = m[i] - cm[i], was = down + lift[i], now = fmaxf(was, y);
+        sum[i] *= ex2(down);
+        keep[i] = ex2(was - now);
+        moved |= was != now;
+        m[i] = cm[i];
+        lift[i] = now;
+      }
+#pragma unroll
+      for (int h = 0; h < kParts; ++h) {
+        const float c[2] = {ev[h] + kTop - lift[0], ev[h] + kTop - lift[1]};
+        float p[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          const float x = s[h][z] - cm[z & 1];
+          sum[z & 1] += ex2(x);
+          p[z] = ex2(x + c[z & 1]);
+        }
+        if (ev[h] != ev[h]) {
+          // values that are no numbers: where a row attends them
+#pragma unroll
+          for (int z = 0; z < 4; ++z) p[z] = s[h][z] == -INFINITY ? 0.0f : ev[h];
+        }
+        const uint32_t u0 = f16x2(p[0], p[1]), u1 = f16x2(p[2], p[3]);
+        pf[h][0] = transposed(u0);
+        pf[h][1] = transposed(u1);
+        if (kExact) {
+          const float2 q0 = f16x2_f32(u0), q1 = f16x2_f32(u1);
+          pl[h][0] = transposed(f16x2(p[0] - q0.x, p[1] - q0.y));
+          pl[h][1] = transposed(f16x2(p[2] - q1.x, p[3] - q1.y));
         }
       }
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
         for (int i = 0; i < kSegs; ++i)
 #pragma unroll
-            for (int z = 0; z < 4; ++z) o[i][z] *= keep[z & 1];
+          for (int z = 0; z < 4; ++z) o[i][z] *= keep[z & 1];
       }
       const uint32_t at = lane_at + stage * S::kStage;
 #pragma unroll
@@ -1117,10 +1106,8 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
             // two tokens of a channel side by side, the even channel below
             const uint32_t x = __byte_perm(r[2 * z], 0, 0x3120), y = __byte_perm(r[2 * z + 1], 0, 0x3120);
             const uint32_t a0 = e4m3x2_f16x2(x), a1 = e4m3x2_f16x2(x >> 16), a2 = e4m3x2_f16x2(y), a3 = e4m3x2_f16x2(y >> 16);
-            {
-              mma(o[i], a0, a1, a2, a3, pf[h + z][0], pf[h + z][1]);
-              if (kExact) mma(o[i], a0, a1, a2, a3, pl[h + z][0], pl[h + z][1]);
-            }
+            mma(o[i], a0, a1, a2, a3, pf[h + z][0], pf[h + z][1]);
+            if (kExact) mma(o[i], a0, a1, a2, a3, pl[h + z][0], pl[h + z][1]);
           }
         }
       }
@@ -1135,39 +1122,37 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
     has = kOpen | (u < w.unit ? kBegan : 0) | (has & kHead);
     if (w.last()) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int z = 4; z < 32; z <<= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], z);
+        for (int z = 4; z < 32; z <<= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], z);
       const Tile tile = w.rows(G);
       if (u >= w.unit) {
         // a tile of this warp alone
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int r = 2 * t + i;
-            if (r < tile.rows) {
-              const float2 k = last_factors(lift[i], sum[i]);
-              const int64_t at = row_of(a.out, tile.token, tile.head, tile.row0 + r, G) + 2 * g;
+        for (int i = 0; i < 2; ++i) {
+          const int r = 2 * t + i;
+          if (r < tile.rows) {
+            const float2 k = last_factors(lift[i], sum[i]);
+            const int64_t at = row_of(a.out, tile.token, tile.head, tile.row0 + r, G) + 2 * g;
 #pragma unroll
-              for (int s = 0; s < kSegs; ++s)
-                put2(a, at + 16 * s, o[s][i] * k.x * k.y, o[s][i + 2] * k.x * k.y);
-              if (a.lse && g == 0) put_lse(a, tile.token, tile.head, tile.row0 + r, G, m[i], sum[i]);
-            }
+            for (int s = 0; s < kSegs; ++s) put2(a, at + 16 * s, o[s][i] * k.x * k.y, o[s][i + 2] * k.x * k.y);
+            if (a.lse && g == 0) put_lse(a, tile.token, tile.head, tile.row0 + r, G, m[i], sum[i]);
           }
+        }
         has &= kHead;
       } else {
         // the end of a tile that began before
         float4* to = reinterpret_cast<float4*>(heads) + ((int64_t)blockIdx.x * kWarps + warp) * S::kQuads + lane;
 #pragma unroll
-        for (int s = 0; s < kSegs; ++s)
-            put_at(to + s * 32, make_float4(o[s][0], o[s][1], o[s][2], o[s][3]), a.ws, a.ws_bytes);
+        for (int s = 0; s < kSegs; ++s) put_at(to + 32 * s, make_float4(o[s][0], o[s][1], o[s][2], o[s][3]), a.ws, a.ws_bytes);
         if (g == 0) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float* st = stats + (kWarps + warp) * kStat + 2 * t + i;
-              st[0] = m[i];
-              st[kRows] = lift[i];
-              st[2 * kRows] = sum[i];
-            }
+          for (int i = 0; i < 2; ++i) {
+            float* st = stats + (kWarps + warp) * kStat + 2 * t + i;
+            st[0] = m[i];
+            st[kRows] = lift[i];
+            st[2 * kRows] = sum[i];
+          }
         }
         if (lane == 0) ctl->head[warp] = tile;
         has = kHead;
@@ -1180,22 +1165,21 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
   // ---------------------------------------------------- joining in the CTA ---
   if ((has & kOpen) || units == 0) {  // (an empty run adds nothing to the tile around it)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int z = 4; z < 32; z <<= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], z);
-        if (g == 0) {
-          float* st = stats + warp * kStat + 2 * t + i;
-          st[0] = m[i];
-          st[kRows] = lift[i];
-          st[2 * kRows] = sum[i];
-        }
+      for (int z = 4; z < 32; z <<= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], z);
+      if (g == 0) {
+        float* st = stats + warp * kStat + 2 * t + i;
+        st[0] = m[i];
+        st[kRows] = lift[i];
+        st[2 * kRows] = sum[i];
       }
+    }
     // (this warp's ring: its loads have all been read)
     float4* to = reinterpret_cast<float4*>(base + warp * kStages * S::kStage) + lane;
     __syncwarp();
 #pragma unroll
-    for (int s = 0; s < kSegs; ++s)
-        to[s * 32] = make_float4(o[s][0], o[s][1], o[s][2], o[s][3]);
+    for (int s = 0; s < kSegs; ++s) to[32 * s] = make_float4(o[s][0], o[s][1], o[s][2], o[s][3]);
   }
   if (lane == 0) {
     ctl->has[warp] = has;

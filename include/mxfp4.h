@@ -594,8 +594,8 @@ typedef struct {
  * -infinity. One token for each sequence is a decode step's form; several
  * (proposed tokens, a prompt's chunk) attend causally.
  *  q    bf16 [tokens, q_heads, head_dim]; q_heads a multiple of heads, up to
- *       65535, tokens * q_heads below 2^31 (and the work of a call, about
- *       tokens * q_heads * max_pages * page_tokens / 256, too). It goes in to 2^-39 of its row's largest magnitude.
+ *       65535, tokens * q_heads below 2^30 (and the work of a call, about
+ *       tokens * q_heads * max_pages * page_tokens / 256, below 2^31). It goes in to 2^-39 of its row's largest magnitude.
  *  out  bf16 or fp32 [tokens, q_heads, head_dim]; lse fp32 [tokens, q_heads]
  *       contiguous, or NULL.
  *  workspace  device memory, 16-byte aligned, of
