@@ -799,6 +799,11 @@ mxfp4_status check_q_heads(const char* fn, mx::AttentionArgs* a, int32_t q_heads
     return fail(MXFP4_ERR_SHAPE, "%s: tokens (%d) * q_heads (%d) must be below 2^30", fn, c.tokens, q_heads);
   a->q_heads = q_heads;
   a->group = q_heads / c.heads;
+  // l = ceil(log2 group), floor(2^32 (2^l - group) / group) + 1
+  const int l = a->group > 1 ? 32 - __builtin_clz((unsigned)a->group - 1) : 0;
+  a->group_mul = (uint32_t)(((((uint64_t)1 << l) - (uint64_t)a->group) << 32) / (uint64_t)a->group + 1);
+  a->group_shift[0] = l < 1 ? 0 : 1;
+  a->group_shift[1] = (uint8_t)(l > 1 ? l - 1 : 0);
   a->shift = c.page_tokens == 16 ? 4 : c.page_tokens == 32 ? 5 : c.page_tokens == 64 ? 6 : 7;
   a->window = window < (1 << 30) ? window : 1 << 30;  // (no length passes it)
   if (mx::cache_attention_units(*a) >= (int64_t)1 << 31)

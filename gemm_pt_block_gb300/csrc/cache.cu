@@ -387,18 +387,22 @@ __global__ void __launch_bounds__(1024) cache_read_kernel(CacheArgs c, Heads k, 
 
 constexpr float kTop = 15.0f;                   // weights are held times 2^15: f16 keeps 2^-39 of the largest
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
-constexpr int kMostWarps = 15, kMostStages = 8;
+constexpr int kMostWarps = 14, kMostStages = 8;
 constexpr int kRows = 8;  // of a tile: sixteen, for half the conversions, gained 7 % at 16 rows and lost 20 % at 4 to 16
 
 template <int D>
 struct Attn {
-  // Warps that multiply, beside the one that fetches: as many as their registers
-  // (sums D / 4, queries D / 8 of them) leave room for on the SM without spilling.
-  static constexpr int kWarps = D <= 64 ? 15 : D <= 128 ? 11 : 7;
-  static constexpr int kThreads = (kWarps + 1) * 32;
+  // Warps that multiply: as many as their registers (sums D / 4, queries D / 8 of
+  // them) leave room for on the SM without spilling. Then those that fetch for them,
+  // a lane for 16 tokens of a unit.
+  static constexpr int kWarps = D <= 64 ? 14 : D <= 128 ? 11 : 7;
+  static constexpr int kFetch = D <= 64 ? 2 : 1;
+  static constexpr int kFetched = kWarps / kFetch;  // warps that one fetches for
+  static constexpr int kThreads = (kWarps + kFetch) * 32;
   static constexpr int kBox = D % 128 == 0 ? 128 : D % 64 == 0 ? 64 : 32;  // bytes of a row in one swizzled slab
   static constexpr int kChunk = D == 64 ? 64 : 32;                         // tokens of a unit, in parts of 16
   static constexpr int kParts = kChunk / 16;
+  static constexpr int kLanes = 32 / kParts;                               // of a fetching warp for one part
   static constexpr int kPart = 16 * D;                                     // a part's keys or values
   static constexpr int kStage = kChunk * D;                                // a unit's
   static constexpr int kQuads = D / 16 * 32;                               // of a tile's sums (below)
@@ -406,7 +410,11 @@ struct Attn {
   static constexpr int kFit = (227 * 1024 - 1024 - kFixed) / (kWarps * kStage);
   static constexpr int kStages = kFit < kMostStages ? kFit : kMostStages;  // of a warp's ring
   static constexpr int kBytes = 1024 + kWarps * kStages * kStage + kFixed;
-  static_assert(kStages >= 3 && kQuads * 16 <= kStages * kStage, "ring");
+  // The warp that a fetching warp's lane fetches for.
+  static __device__ __forceinline__ int fetched(int warp, int lane) {
+    return (warp - kWarps) * kFetched + min(lane % kLanes, kFetched - 1);
+  }
+  static_assert(kStages >= 3 && kQuads * 16 <= kStages * kStage && kFetched <= kLanes, "ring");
 };
 
 // A tile: rows row0 .. row0 + rows - 1 of a sequence's (first token `token`), of one head.
@@ -527,6 +535,13 @@ __device__ __forceinline__ void warps_sync() {
 // 2^e for a whole e, 0 below the smallest normal number.
 __device__ __forceinline__ float pow2i(int e) { return e < -126 ? 0.0f : __uint_as_float((uint32_t)(min(e, 127) + 127) << 23); }
 
+// r / G for a tile's rows: the multiplication for an invariant divisor of Granlund
+// and Montgomery (1994), its numbers from the host.
+__device__ __forceinline__ int32_t token_of(const AttentionArgs& a, int32_t r) {
+  const uint32_t t = __umulhi(a.group_mul, (uint32_t)r);
+  return (int32_t)((t + (((uint32_t)r - t) >> a.group_shift[0])) >> a.group_shift[1]);
+}
+
 // What a call says of one sequence, as it lies in memory.
 struct Said {
   int32_t row, end, len;
@@ -589,8 +604,8 @@ struct Walk {
   __device__ __forceinline__ void set_tile(const AttentionArgs& a) {
     const int G = a.group;
     row0 = tile * kRows;
-    p0 = len - n + row0 / G;
-    hi = max(0, len - n + (min(row0 + kRows, n * G) - 1) / G + 1);
+    p0 = len - n + token_of(a, row0);
+    hi = max(0, len - n + token_of(a, min(row0 + kRows, n * G) - 1) + 1);
     lo = a.window > 0 ? max(0, p0 - a.window + 1) & -kChunk : 0;
   }
   __device__ __forceinline__ int32_t token() const { return lo + unit * kChunk; }
@@ -645,11 +660,13 @@ __device__ __forceinline__ int32_t warp_sums(int32_t v, int lane) {
 
 // Where the runs of this CTA's warps begin. Up to 32 sequences every warp looks at
 // them for itself, a lane at one, and has its run's first unit in w (lanes of the
-// fetching warp: that of warp lane % 16); more are the whole CTA's, a thread looks
+// fetching warp: that of the warp they fetch for); more are the whole CTA's, a thread looks
 // at one, and the runs' beginnings go to ctl. Ends with a barrier.
-template <int kChunk, int kWarps>
+template <int D, int kChunk>
 __device__ __forceinline__ Cut find_start(const AttentionArgs& a, int warp, int lane, AttnCtl* ctl, int32_t* sums,
                                           Walk<kChunk>* w) {
+  using S = Attn<D>;
+  constexpr int kWarps = S::kWarps;
   const bool few = a.c.sequences <= 32;
   const int32_t mine_at = few ? lane : (int32_t)threadIdx.x;
   Walk<kChunk> x{};
@@ -657,7 +674,7 @@ __device__ __forceinline__ Cut find_start(const AttentionArgs& a, int warp, int 
   const int32_t upto = warp_sums(mine, lane);
   if (few) {
     const Cut runs = cut<kWarps>(__shfl_sync(0xffffffffu, upto, 31));
-    const int32_t begin = runs.begin(blockIdx.x * kWarps + (warp < kWarps ? warp : min(lane & 15, kWarps - 1)));
+    const int32_t begin = runs.begin(blockIdx.x * kWarps + (warp < kWarps ? warp : S::fetched(warp, lane)));
     int32_t s = 0;  // sequences that end before
     for (int32_t i = 0; i < a.c.sequences; ++i) s += __shfl_sync(0xffffffffu, upto, i) <= begin;
     s = min(s, a.c.sequences - 1);
@@ -674,7 +691,7 @@ __device__ __forceinline__ Cut find_start(const AttentionArgs& a, int warp, int 
     return runs;
   }
   // all units, then the sequences again, as many at a time as there are threads
-  constexpr int kThreads = (kWarps + 1) * 32;
+  constexpr int kThreads = S::kThreads;
   const bool once = a.c.sequences <= kThreads;
   int32_t more = mine;
   for (int32_t s = mine_at + kThreads; s < a.c.sequences; s += kThreads) more += x.take(a, s, said(a.c, s));
@@ -683,7 +700,7 @@ __device__ __forceinline__ Cut find_start(const AttentionArgs& a, int warp, int 
   __syncthreads();
   int32_t all = 0, before = 0;
 #pragma unroll
-  for (int i = 0; i <= kWarps; ++i) all += sums[i];
+  for (int i = 0; i < kThreads / 32; ++i) all += sums[i];
   const Cut runs = cut<kWarps>(all);
   for (int32_t from = 0; from < a.c.sequences; from += kThreads) {
     const int32_t s = from + mine_at;
@@ -697,7 +714,7 @@ __device__ __forceinline__ Cut find_start(const AttentionArgs& a, int warp, int 
     }
     int32_t at = before + within - units;  // units before this sequence
 #pragma unroll
-    for (int i = 0; i <= kWarps; ++i) {
+    for (int i = 0; i < kThreads / 32; ++i) {
       if (i < warp) at += sums[i];
       before += sums[i];
     }
@@ -722,8 +739,9 @@ __device__ __forceinline__ Quad quad(int e) {
 }
 
 // Row r of a sequence's n * G rows: the tensors' row and the query head.
-__device__ __forceinline__ int64_t row_of(const Heads& x, int32_t token, int32_t head, int32_t r, int G) {
-  return (int64_t)(token + r / G) * x.ld_t + (int64_t)(head * G + r % G) * x.ld_h;
+__device__ __forceinline__ int64_t row_of(const AttentionArgs& a, const Heads& x, int32_t token, int32_t head, int32_t r) {
+  const int32_t i = token_of(a, r);
+  return (int64_t)(token + i) * x.ld_t + (int64_t)(head * a.group + r - i * a.group) * x.ld_h;
 }
 __device__ __forceinline__ void put2(const AttentionArgs& a, int64_t at, float x, float y) {
   if (a.out_f32)
@@ -745,9 +763,9 @@ constexpr float kLowest = -3.4e38f;
 struct Joined {
   float m, lift, sum;
 };
-__device__ __forceinline__ void put_lse(const AttentionArgs& a, int32_t token, int32_t head, int32_t r, int G, float m,
-                                        float sum) {
-  const int64_t at = (int64_t)(token + r / G) * a.q_heads + head * G + r % G;
+__device__ __forceinline__ void put_lse(const AttentionArgs& a, int32_t token, int32_t head, int32_t r, float m, float sum) {
+  const int32_t i = token_of(a, r);
+  const int64_t at = (int64_t)(token + i) * a.q_heads + head * a.group + r - i * a.group;
   put_at(a.lse + at, sum == 0.0f ? -INFINITY : (m + lg2(sum)) * 0.693147180559945f, a.lse, a.lse_bytes);
 }
 
@@ -779,80 +797,67 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
   }
   Walk<kChunk> w;
   const bool few = a.c.sequences <= 32;
-  const Cut runs = find_start<kChunk, kWarps>(a, warp, lane, ctl, reinterpret_cast<int32_t*>(stats), &w);
+  const Cut runs = find_start<D, kChunk>(a, warp, lane, ctl, reinterpret_cast<int32_t*>(stats), &w);
   if (blockIdx.x >= runs.ctas) {
     if (a.ws && threadIdx.x == 0) put_at(&reinterpret_cast<Split*>(a.ws)[blockIdx.x].parts, (int32_t)0, a.ws, a.ws_bytes);
     return;
   }
 
-  if (warp == kWarps) {
+  if (warp >= kWarps) {
     // ------------------------------------------------------------ fetching ---
-    // Lanes i and i + 16 walk warp i's run and fetch half of its units' parts each;
+    // Lanes i, i + kLanes, .. walk warp i's run and fetch a part of its units each;
     // the table is read a unit ahead. A copy is of a page's tokens, or a unit's.
-    const int i = min(lane & 15, kWarps - 1);
-    const int32_t units =
-        (lane & 15) < kWarps ? runs.begin(blockIdx.x * kWarps + i + 1) - runs.begin(blockIdx.x * kWarps + i) : 0;
+    const int i = S::fetched(warp, lane), part = lane / S::kLanes;
+    const int32_t units = lane % S::kLanes < S::kFetched
+                              ? runs.begin(blockIdx.x * kWarps + i + 1) - runs.begin(blockIdx.x * kWarps + i) : 0;
     const int32_t rounds = __reduce_max_sync(0xffffffffu, units);
-    constexpr int kMine = kParts / 2;
-    const int copy = min(a.c.page_tokens, kChunk), from = (lane >> 4) * kMine;
-    struct Pages {
-      int32_t page[kMine], head, place;  // page: -1 a wrong one, -2 none to load; place of the first in it
+    const int copy = min(a.c.page_tokens, kChunk);
+    const bool leads = (16 * part & (copy - 1)) == 0;  // a copy begins with this part
+    struct Page {
+      int32_t page, head, place;  // page: -1 a wrong one, -2 none to load
       bool live;
     };
-    auto pages_at = [&]() {
-      Pages x;
-      x.head = w.head;
-      x.live = w.live();
-      const int32_t j0 = w.token() + 16 * from;
-      x.place = (j0 & (a.c.page_tokens - 1)) >> 4;
-#pragma unroll
-      for (int q = 0; q < kMine; ++q) {
-        const int32_t j = j0 + 16 * q;
-        x.page[q] = -2;
-        if (j < w.hi) x.page[q] = j >> a.shift < a.c.max_pages ? __ldg(a.c.table + (int64_t)w.b * a.c.ld_table + (j >> a.shift)) : -1;
+    auto page_at = [&]() {
+      Page x{-2, w.head, 0, w.live()};
+      const int32_t j = w.token() + 16 * part;
+      if (j < w.hi) {
+        x.place = (j & (a.c.page_tokens - 1)) >> 4;
+        x.page = j >> a.shift < a.c.max_pages ? __ldg(a.c.table + (int64_t)w.b * a.c.ld_table + (j >> a.shift)) : -1;
       }
       return x;
     };
-    Pages ahead{};
+    Page ahead{-2, 0, 0, false};
     if (units > 0) {
       if (!few) w.begin(a, ctl->start[i]);
-      ahead = pages_at();
+      ahead = page_at();
     }
     const uint32_t my_ring = ring + i * kStages * S::kStage, my_full = full + 8 * kMostStages * i, my_empty = empty + 8 * kMostStages * i;
     int32_t tiles = 0, stage = 0;
     uint32_t parity = 1;  // of the stage's reader
     bool go = true;
     for (int32_t round = 0; round < rounds && go; ++round) {
-      const Pages now = ahead;
+      const Page now = ahead;
       const bool mine = round < units && now.live;
-      int32_t block[kMine], bytes = 0;
-#pragma unroll
-      for (int q = 0; q < kMine; ++q) {
-        block[q] = -1;
-        if (!mine) continue;
-        if (now.page[q] >= 0 && now.page[q] < a.c.pages)
-          block[q] = now.page[q] * 2 * a.c.heads + now.head;
-        else if (now.page[q] != -2)
+      int32_t block = -1;
+      if (mine) {
+        if (now.page >= 0 && now.page < a.c.pages)
+          block = now.page * 2 * a.c.heads + now.head;
+        else if (now.page != -2)
           index_fail();
-        if (block[q] >= 0 && (16 * (from + q) & (copy - 1)) == 0) bytes += copy * D;
       }
-      bytes += __shfl_down_sync(0xffffffffu, bytes, 16);
+      int32_t bytes = block >= 0 && leads ? copy * D : 0;
+#pragma unroll
+      for (int z = S::kLanes; z < 32; z <<= 1) bytes += __shfl_xor_sync(0xffffffffu, bytes, z);
 #pragma unroll
       for (int kind = 0; kind < 2; ++kind) {
         go = go && wait_bars(my_empty + 8 * stage, parity, mine && tiles >= kStages, &ctl->abort);
-        if (kind == 0 && mine && go) {
-#pragma unroll
-          for (int q = 0; q < kMine; ++q) ctl->block[i][stage][from + q] = block[q];
-        }
+        if (kind == 0 && mine && go) ctl->block[i][stage][part] = block;
         __syncwarp();
         if (mine && go) {
-          const uint32_t bar = my_full + 8 * stage, to = my_ring + stage * S::kStage;
-          if (lane < 16) ptx::mbar_arrive_expect_tx(bar, bytes);
-#pragma unroll
-          for (int q = 0; q < kMine; ++q)
-            if (block[q] >= 0 && (16 * (from + q) & (copy - 1)) == 0)
-              tma_pages(to + (from + q) * S::kPart, &map, (now.place + q) & ((a.c.page_tokens >> 4) - 1),
-                        block[q] + (kind ? a.c.heads : 0), bar);
+          const uint32_t bar = my_full + 8 * stage;
+          if (part == 0) ptx::mbar_arrive_expect_tx(bar, bytes);
+          if (block >= 0 && leads)
+            tma_pages(my_ring + stage * S::kStage + part * S::kPart, &map, now.place, block + (kind ? a.c.heads : 0), bar);
           ++tiles;
           if (++stage == kStages) {
             stage = 0;
@@ -862,7 +867,7 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
       }
       if (round + 1 < units) {
         w.next(a);
-        ahead = pages_at();
+        ahead = page_at();
       }
     }
     if (!go) {
@@ -917,7 +922,7 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
 #pragma unroll
       for (int s = 0; s < kSegs; ++s) x[s] = make_uint2(0u, 0u);
       if (w.row0 + g < w.n * G) {
-        const uint16_t* q = static_cast<const uint16_t*>(a.q.p) + row_of(a.q, w.row, w.head, w.row0 + g, G) + 4 * t;
+        const uint16_t* q = static_cast<const uint16_t*>(a.q.p) + row_of(a, a.q, w.row, w.head, w.row0 + g) + 4 * t;
 #pragma unroll
         for (int s = 0; s < kSegs; ++s) x[s] = __ldg(reinterpret_cast<const uint2*>(q + 16 * s));
       }
@@ -942,8 +947,9 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
       for (int i = 0; i < 2; ++i) {
         unit_q[i] = __shfl_sync(0xffffffffu, uq, 8 * t + 4 * i);
         const int32_t r = min(w.row0 + 2 * t + i, w.n * G - 1);
-        pos[i] = w.len - w.n + r / G;
-        slope[i] = a.slopes ? __ldg(a.slopes + w.head * G + r % G) * 1.44269504088896f : 0.0f;
+        const int32_t token = token_of(a, r);
+        pos[i] = w.len - w.n + token;
+        slope[i] = a.slopes ? __ldg(a.slopes + w.head * G + r - token * G) * 1.44269504088896f : 0.0f;
       }
     }
 
@@ -1133,10 +1139,10 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
           const int r = 2 * t + i;
           if (r < tile.rows) {
             const float2 k = last_factors(lift[i], sum[i]);
-            const int64_t at = row_of(a.out, tile.token, tile.head, tile.row0 + r, G) + 2 * g;
+            const int64_t at = row_of(a, a.out, tile.token, tile.head, tile.row0 + r) + 2 * g;
 #pragma unroll
             for (int s = 0; s < kSegs; ++s) put2(a, at + 16 * s, o[s][i] * k.x * k.y, o[s][i + 2] * k.x * k.y);
-            if (a.lse && g == 0) put_lse(a, tile.token, tile.head, tile.row0 + r, G, m[i], sum[i]);
+            if (a.lse && g == 0) put_lse(a, tile.token, tile.head, tile.row0 + r, m[i], sum[i]);
           }
         }
         has &= kHead;
@@ -1271,12 +1277,12 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
     if (final) {
       const Tile tile = ctl->head[x.last];
       const float2 k = last_factors(j.lift, j.sum);
-      if (a.lse && lane < tile.rows && lane < kRows) put_lse(a, tile.token, tile.head, tile.row0 + r, G, j.m, j.sum);
+      if (a.lse && lane < tile.rows && lane < kRows) put_lse(a, tile.token, tile.head, tile.row0 + r, j.m, j.sum);
 #pragma unroll
       for (int z = 0; z < 2; ++z) {
         const float k1 = __shfl_sync(0xffffffffu, k.x, 2 * t + z), k2 = __shfl_sync(0xffffffffu, k.y, 2 * t + z);
         if (2 * t + z >= tile.rows) continue;
-        const int64_t at = row_of(a.out, tile.token, tile.head, tile.row0 + 2 * t + z, G) + 2 * g;
+        const int64_t at = row_of(a, a.out, tile.token, tile.head, tile.row0 + 2 * t + z) + 2 * g;
 #pragma unroll
         for (int s = 0; s < kSegs; ++s)
           put2(a, at + 16 * s, (z ? sums[s].y : sums[s].x) * k1 * k2, (z ? sums[s].w : sums[s].z) * k1 * k2);
@@ -1370,7 +1376,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
       if (32 * i + lane < sp.parts) factors[32 * i + lane][row] = ex2(m[i] - top + lift[i] - high);
     if (lane == 0) {
       last[row] = last_factors(high, all);
-      if (a.lse && row < sp.tile.rows) put_lse(a, sp.tile.token, sp.tile.head, sp.tile.row0 + row, a.group, top, all);
+      if (a.lse && row < sp.tile.rows) put_lse(a, sp.tile.token, sp.tile.head, sp.tile.row0 + row, top, all);
     }
   }
   __syncthreads();
@@ -1402,7 +1408,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   for (int i = 0; i < 2; ++i) {
     const int r = qd.row + i;
     if (r < sp.tile.rows)
-      put2(a, row_of(a.out, sp.tile.token, sp.tile.head, sp.tile.row0 + r, a.group) + qd.d,
+      put2(a, row_of(a, a.out, sp.tile.token, sp.tile.head, sp.tile.row0 + r) + qd.d,
            (i ? x.y : x.x) * last[r].x * last[r].y, (i ? x.w : x.z) * last[r].x * last[r].y);
   }
 }
