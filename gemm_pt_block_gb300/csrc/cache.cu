@@ -179,6 +179,7 @@ __device__ __forceinline__ uint2 quantized8(const float (&f)[8], float mul, uint
 template <typename T>
 __global__ void __launch_bounds__(256) cache_append_few_kernel(CacheArgs c, Heads k, Heads v) {
   const int lane = threadIdx.x & 31, task = blockIdx.y * 8 + (threadIdx.x >> 5);
+  ptx::launch_dependents();
   if (task >= 2 * c.heads) return;
   Slot t;
   if (!slot_of<2>(c, lane, &t)) return;
@@ -230,6 +231,7 @@ struct Share {
 template <typename T, int kMost>
 __global__ void __launch_bounds__(kMost) cache_append_kernel(CacheArgs c, Heads k, Heads v, Share sh) {
   __shared__ uint32_t most[2][32];
+  ptx::launch_dependents();
   Slot t;
   if (!slot_of<2>(c, threadIdx.x & 31, &t)) return;
   const int mine = threadIdx.x / sh.each, in = threadIdx.x - mine * sh.each, per = c.head_dim >> 4;
@@ -798,6 +800,7 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
     }
     ptx::fence_mbar_init();
   }
+  ptx::wait_prior_grid();  // (nothing of the call's is read or written before)
   Walk<kChunk> w;
   const bool few = a.c.sequences <= 32;
   const Cut runs = find_start<D, kChunk>(a, warp, lane, ctl, reinterpret_cast<int32_t*>(stats), &w);
@@ -1337,6 +1340,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   const float* parts = a.ws + gridDim.x * (sizeof(Split) / 4) + 2 * (int64_t)blockIdx.x * part_floats(D);
   auto part = [&](int i) { return parts + (2 * i + (i == 0)) * part_floats(D); };
   const int behind = gridDim.x - blockIdx.x;  // parts that the workspace has room for
+  ptx::launch_dependents();
   ptx::wait_prior_grid();
   const Split sp = reinterpret_cast<const Split*>(a.ws)[blockIdx.x];
   constexpr int kMost = (kSms + 31) / 32;
@@ -1534,18 +1538,21 @@ cudaError_t attend(const AttentionArgs& a, const AttnShape& sh, cudaStream_t st)
   }
   CUtensorMap map;
   if (!pages_map(&map, a.c, a.q.p, S::kBox, S::kChunk)) return cudaErrorInvalidValue;
-  cache_attention_kernel<D, kExact><<<sh.ctas, S::kThreads, S::kBytes, st>>>(map, a);
-  if ((e = cudaGetLastError()) != cudaSuccess || !sh.split) return e;
-  // launched while the kernel before it drains; it waits for that kernel's parts itself
+  // Both kernels are launched while the one before them drains, and wait for its
+  // end themselves.
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)sh.ctas);
-  cfg.blockDim = dim3(kJoinThreads);
+  cfg.blockDim = dim3(S::kThreads);
+  cfg.dynamicSmemBytes = S::kBytes;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, cache_attention_kernel<D, kExact>, map, a)) != cudaSuccess || !sh.split) return e;
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, cache_join_kernel<D>, a);
 }
 template <int D>
