@@ -174,6 +174,24 @@ __device__ __forceinline__ uint2 quantized8(const float (&f)[8], float mul, uint
                     e4m3x4(f[4] * mul, f[5] * mul, f[6] * mul, f[7] * mul));
 }
 
+// Largest magnitude's bits of sixteen elements (as fp32; bf16 two at a time, as the
+// whole numbers that its bits are).
+__device__ __forceinline__ uint32_t most16(const Vec16<uint16_t>& v) {
+  const uint32_t w[8] = {v.v.a.x, v.v.a.y, v.v.a.z, v.v.a.w, v.v.b.x, v.v.b.y, v.v.b.z, v.v.b.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+  return max(m << 16, m & 0xFFFF0000u);
+}
+__device__ __forceinline__ uint32_t most16(const Vec16<float>& v) {
+  float2 f[8];
+  unpack16(v, f);
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = absmax3_nan(m, f[i].x, f[i].y);
+  return __float_as_uint(m) & 0x7FFFFFFFu;
+}
+
 // A few new tokens a page: a warp takes a block, eight elements a lane. Values
 // past the first 256 are read twice.
 template <typename T>
@@ -264,18 +282,12 @@ __global__ void __launch_bounds__(kMost) cache_append_kernel(CacheArgs c, Heads 
     const bool some = task < blocks;
     const uint32_t old = ahead_old;
     const Vec16<T> now[2] = {ahead[0], ahead[1]};
-    float m = 0.0f;
+    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (some && token[i] >= t.lo && token[i] < t.hi) {
-        float2 f[8];
-        unpack16(now[i], f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = absmax3_nan(m, f[j].x, f[j].y);
-      }
-    }
+    for (int i = 0; i < 2; ++i)
+      if (some && token[i] >= t.lo && token[i] < t.hi) m = max(m, most16(now[i]));
     if (task + stride < blocks) fetch(task + stride);
-    const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(m) & 0x7FFFFFFFu);
+    const uint32_t bits = __reduce_max_sync(0xffffffffu, m);
     uint32_t all = bits;
     if (sh.each > 32) {
       uint32_t* slots = most[round & 1];
@@ -296,11 +308,11 @@ __global__ void __launch_bounds__(kMost) cache_append_kernel(CacheArgs c, Heads 
         float2 f[8];
         unpack16(now[i], f);
         uint4 q = make_uint4(0u, 0u, 0u, 0u);
-        if (scale != 255u)
-          q = make_uint4(e4m3x4(f[0].x * mul, f[0].y * mul, f[1].x * mul, f[1].y * mul),
-                         e4m3x4(f[2].x * mul, f[2].y * mul, f[3].x * mul, f[3].y * mul),
-                         e4m3x4(f[4].x * mul, f[4].y * mul, f[5].x * mul, f[5].y * mul),
-                         e4m3x4(f[6].x * mul, f[6].y * mul, f[7].x * mul, f[7].y * mul));
+        if (scale != 255u) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[j] = f2mul(f[j], make_float2(mul, mul));
+          q = encode16_fp8(f, false);
+        }
         put_at(to, q, c.codes, c.codes_bytes);
       } else if (token[i] < t.lo && old < scale && scale != 255u) {
         const float less = older_factor(old, scale);
