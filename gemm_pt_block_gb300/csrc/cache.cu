@@ -914,8 +914,7 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
   float* heads = a.ws + gridDim.x * (sizeof(Split) / 4 + 2 * part_floats(D));  // (used with a workspace only)
 
   uint32_t qf[kSegs][2];
-  float o[kSegs][4], m[2], lift[2], sum[2], slope[2], unit_q[2];
-  int32_t pos[2];
+  float o[kSegs][4], m[2], lift[2], sum[2], unit_q[2];
   auto clear = [&]() {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -967,10 +966,6 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         unit_q[i] = __shfl_sync(0xffffffffu, uq, 8 * t + 4 * i);
-        const int32_t r = min(w.row0 + 2 * t + i, w.n * G - 1);
-        const int32_t token = token_of(a, r);
-        pos[i] = w.len - w.n + token;
-        slope[i] = a.slopes ? __ldg(a.slopes + w.head * G + r - token * G) * 1.44269504088896f : 0.0f;
       }
     }
 
@@ -1025,15 +1020,21 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
             s[h][i] *= f * scale2;
             s[h][i + 2] *= f * scale2;
           }
-          const int32_t j = c0 + 16 * h + g - pos[i];  // the token's position less the row's
-          if (a.slopes) {
-            s[h][i] += slope[i] * (float)j;
-            s[h][i + 2] += slope[i] * (float)(j + 8);
-          }
-          if (!whole) {
-            const int32_t most = a.window > 0 ? a.window : 0x7FFFFFFF;
-            if (j > 0 || j <= -most) s[h][i] = -INFINITY;
-            if (j + 8 > 0 || j + 8 <= -most) s[h][i + 2] = -INFINITY;
+        }
+      }
+      if (a.slopes || !whole) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int32_t r = min(w.row0 + 2 * t + i, w.n * G - 1), token = token_of(a, r);
+          const int32_t j0 = c0 + g - (w.len - w.n + token);  // the first token's position less the row's
+          const float slope = a.slopes ? __ldg(a.slopes + w.head * G + r - token * G) * 1.44269504088896f : 0.0f;
+          const int32_t most = a.window > 0 ? a.window : 0x7FFFFFFF;
+#pragma unroll
+          for (int z = 0; z < 2 * kParts; ++z) {
+            const int32_t j = j0 + 8 * z;
+            float& x = s[z >> 1][i + 2 * (z & 1)];
+            x += slope * (float)j;
+            if (j > 0 || j <= -most) x = -INFINITY;
           }
         }
       }
