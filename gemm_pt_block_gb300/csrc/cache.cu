@@ -838,7 +838,8 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
     auto page_at = [&]() {
       Page x{-2, w.head, 0, w.live()};
       const int32_t j = w.token() + 16 * part;
-      if (j < w.hi) {
+      // (pages that end before every row's window may be gone)
+      if (j < w.hi && (a.window == 0 || (j | (a.c.page_tokens - 1)) > w.p0 - a.window)) {
         x.place = (j & (a.c.page_tokens - 1)) >> 4;
         x.page = j >> a.shift < a.c.max_pages ? __ldg(a.c.table + (int64_t)w.b * a.c.ld_table + (j >> a.shift)) : -1;
       }
@@ -1048,11 +1049,13 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
         ev[h] = vs == 255u ? __uint_as_float(0x7FC00000u) : (float)((int)vs - 127);
         one = one && ev[h] == ev[0];
       }
-      if (c0 + kChunk > w.hi) {
-        // tokens behind the last: whatever lies there must not meet a weight of zero
-        const int first = w.hi - c0;
-        for (int i = lane; i < (kChunk - first) * kSegs; i += 32) {
-          const int r = first + i / kSegs, seg = i % kSegs;
+      const uint32_t gone = __ballot_sync(0xffffffffu, block < 0);
+      if (c0 + kChunk > w.hi || gone) {
+        // tokens behind the last, parts without a page: whatever lies there must not
+        // meet a weight of zero
+        for (int i = lane; i < kChunk * kSegs; i += 32) {
+          const int r = i / kSegs, seg = i % kSegs;
+          if (c0 + r < w.hi && !(gone >> (r >> 4) & 1)) continue;
           const uint32_t at = my_ring + stage * S::kStage + (r >> 4) * S::kPart + (seg / kIn) * 16 * S::kBox +
                               (r & 15) * S::kBox + (seg % kIn) * 16;
           asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");

@@ -520,7 +520,9 @@ typedef struct {
 
 /* The sequences of a call; all arrays are device memory, 4-byte aligned.
  *  page_table [sequences, max_pages], leading dimension ld_table: a sequence's
- *      pages in order. Entries behind its last token are not looked at.
+ *      pages in order. Entries behind its last token are not looked at, nor does
+ *      attention look at those of pages that end before every window of a call's
+ *      queries: such pages may be given to others.
  *  lens [sequences]: tokens of each sequence, the new ones included.
  *  starts [sequences + 1]: sequence b's rows of the call's tensors are
  *      starts[b] .. starts[b + 1] - 1 (its new tokens, in order). NULL: one row
@@ -595,7 +597,8 @@ typedef struct {
  * (proposed tokens, a prompt's chunk) attend causally.
  *  q    bf16 [tokens, q_heads, head_dim]; q_heads a multiple of heads, up to
  *       65535, tokens * q_heads below 2^30 (and the work of a call, about
- *       tokens * q_heads * max_pages * page_tokens / 256, below 2^31). It goes in to 2^-39 of its row's largest magnitude.
+ *       tokens * q_heads * max_pages * page_tokens / 256, below 2^31). It goes in
+ *       to 2^-39 of its row's largest magnitude.
  *  out  bf16 or fp32 [tokens, q_heads, head_dim]; lse fp32 [tokens, q_heads]
  *       contiguous, or NULL.
  *  workspace  device memory, 16-byte aligned, of

@@ -281,3 +281,40 @@ def test_the_check_fires(bc_lib):  # noqa: F811
             fn()
             assert mx.device_status() == 0, name
     assert fired == {"attention", "read", "append"}
+
+
+@pytest.mark.parametrize("L,n,H,G,D,P,window", [([200, 77, 33], [1, 1, 1], 2, 2, 64, 16, 5), ([300, 95], [4, 9], 1, 4, 128, 16, 20),
+                                                ([300, 130], [3, 40], 2, 1, 64, 32, 40), ([500, 200], [1, 7], 1, 8, 96, 64, 64),
+                                                ([700], [1], 1, 16, 256, 128, 200)])
+def test_pages_before_the_window_may_be_gone(L, n, H, G, D, P, window):
+    import gemm_pt_block_gb300 as mx
+
+    c = make_cache(L, n, H, D, P, seed=40)
+    q = torch.randn((c.T, H * G, D), device=DEV, generator=gen(41)).to(BF16)
+    gone = make_cache(L, n, H, D, P, seed=40)
+    for b in range(len(L)):
+        first = max(0, L[b] - n[b] - window + 1)            # that a query attends
+        gone.table[b, :first // P] = torch.tensor([-1, 1 << 30], device=DEV).int().repeat(first // P)[:first // P]
+    for dtype in (BF16, F32):
+        out, lse = mx.mxfp8_cache_attention(q, c.codes, c.scales, gone.table, c.lens, starts=c.starts, with_lse=True,
+                                            out_dtype=dtype, window=window)
+        assert mx.device_status() == 0
+        check(c, q, out, lse, dtype, window=window)
+
+
+def test_a_missing_page_beside_rows_that_do_not_attend_it():
+    import gemm_pt_block_gb300 as mx
+
+    # (what lies in shared memory in its place: NaN codes behind other sequences' ends)
+    c = make_cache([49], [1], 1, 64, 16, seed=42)
+    B = 152 * 14 * 3
+    q = torch.randn((B, 1, 64), device=DEV, generator=gen(43)).to(BF16)
+    mx.mxfp8_cache_attention(q, c.codes, c.scales, c.table.expand(B, -1).contiguous(), c.lens.expand(B).contiguous())
+    c = make_cache([51], [5], 1, 64, 16, seed=44)
+    c.table[0, 3] = -1
+    out, lse = mx.mxfp8_cache_attention(q[:5], c.codes, c.scales, c.table, c.lens, starts=c.starts, with_lse=True)
+    assert mx.device_status() == BAD
+    assert bool(torch.isnan(out[2:]).all()) and bool(torch.isnan(lse[2:]).all())
+    c.table[0, 3] = c.table[0, 0]
+    c.L, c.n = [48], [2]
+    check(c, q[:2], out[:2], lse[:2], BF16)
