@@ -806,7 +806,7 @@ mxfp4_status check_q_heads(const char* fn, mx::AttentionArgs* a, int32_t q_heads
   a->group_shift[1] = (uint8_t)(l > 1 ? l - 1 : 0);
   a->shift = c.page_tokens == 16 ? 4 : c.page_tokens == 32 ? 5 : c.page_tokens == 64 ? 6 : 7;
   a->window = window < (1 << 30) ? window : 1 << 30;  // (no length passes it)
-  if (mx::cache_attention_units(*a) >= (int64_t)1 << 31)
+  if (mx::cache_attention_units(*a) >= mx::kMostUnits)
     return fail(MXFP4_ERR_SHAPE, "%s: too many tokens (%d) of %d heads over %d pages for one call", fn, c.tokens, q_heads,
                 c.max_pages);
   return MXFP4_OK;

@@ -577,7 +577,7 @@ struct Walk {
   int32_t row0, p0, lo, hi;  // tile: first row, its position, tokens [lo, hi) that a row attends; lo rounded down
   Said ahead;                // of sequence b + 1
 
-  // Takes sequence s, of which the call says x; its number of units (a call's stay below 2^31).
+  // Takes sequence s, of which the call says x; its number of units (below kMostUnits).
   __device__ __forceinline__ int32_t take(const AttentionArgs& a, int32_t s, const Said& x) {
     const int G = a.group;
     b = s;
@@ -675,6 +675,17 @@ __device__ __forceinline__ int32_t warp_sums(int32_t v, int lane) {
   return v;
 }
 
+// Row starts that fall may name rows twice, and more units than 32 bits count: such a
+// call does nothing. Units are summed over 2^10 for this; what that rounds off (65535
+// sequences) keeps the limit below 2^31, and the host's keeps right calls below the limit.
+constexpr uint32_t kTooHigh = ((1u << 31) - (1u << 26)) >> 10;
+static_assert(kMostUnits <= (1ll << 31) - (1 << 27), "limits");
+__device__ __forceinline__ int32_t counted(int32_t units, uint32_t high) {
+  if (high < kTooHigh) return units;
+  index_fail();
+  return 0;
+}
+
 // Where the runs of this CTA's warps begin. Up to 32 sequences every warp looks at
 // them for itself, a lane at one, and has its run's first unit in w (lanes of the
 // fetching warp: that of the warp they fetch for); more are the whole CTA's, a thread looks
@@ -690,7 +701,8 @@ __device__ __forceinline__ Cut find_start(const AttentionArgs& a, int warp, int 
   const int32_t mine = mine_at < a.c.sequences ? x.take(a, mine_at, said(a.c, mine_at)) : 0;
   const int32_t upto = warp_sums(mine, lane);
   if (few) {
-    const Cut runs = cut<kWarps>(__shfl_sync(0xffffffffu, upto, 31));
+    const uint32_t high = __reduce_add_sync(0xffffffffu, (uint32_t)mine >> 10);
+    const Cut runs = cut<kWarps>(counted(__shfl_sync(0xffffffffu, upto, 31), high));
     const int32_t begin = runs.begin(blockIdx.x * kWarps + (warp < kWarps ? warp : S::fetched(warp, lane)));
     int32_t s = 0;  // sequences that end before
     for (int32_t i = 0; i < a.c.sequences; ++i) s += __shfl_sync(0xffffffffu, upto, i) <= begin;
@@ -710,15 +722,27 @@ __device__ __forceinline__ Cut find_start(const AttentionArgs& a, int warp, int 
   // all units, then the sequences again, as many at a time as there are threads
   constexpr int kThreads = S::kThreads;
   const bool once = a.c.sequences <= kThreads;
-  int32_t more = mine;
-  for (int32_t s = mine_at + kThreads; s < a.c.sequences; s += kThreads) more += x.take(a, s, said(a.c, s));
+  uint32_t more = mine, high = more >> 10;
+  for (int32_t s = mine_at + kThreads; s < a.c.sequences; s += kThreads) {
+    const uint32_t units = x.take(a, s, said(a.c, s));
+    more += units;
+    high = min(high + (units >> 10), 1u << 22);  // (past the limit)
+  }
   more = warp_sums(more, lane);
-  if (lane == 31) sums[warp] = more;
+  high = __reduce_add_sync(0xffffffffu, high);
+  if (lane == 31) {
+    sums[warp] = more;
+    sums[kThreads / 32 + warp] = high;
+  }
   __syncthreads();
-  int32_t all = 0, before = 0;
+  uint32_t all = 0, all_high = 0;
+  int32_t before = 0;
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) all += sums[i];
-  const Cut runs = cut<kWarps>(all);
+  for (int i = 0; i < kThreads / 32; ++i) {
+    all += sums[i];
+    all_high += sums[kThreads / 32 + i];
+  }
+  const Cut runs = cut<kWarps>(counted(all, all_high));
   for (int32_t from = 0; from < a.c.sequences; from += kThreads) {
     const int32_t s = from + mine_at;
     int32_t units = mine, within = upto;

@@ -185,7 +185,8 @@ cudaError_t launch_cache_append(const CacheArgs& c, const Heads& k, const Heads&
 cudaError_t launch_cache_read(const CacheArgs& c, const Heads& k, const Heads& v, bool f32, cudaStream_t st);
 cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t st);
 int64_t cache_attention_workspace_bytes(const AttentionArgs& a);
-// Units of work that a call may have; launch_cache_attention takes fewer than 2^31.
+// Units of work that a call may have; launch_cache_attention takes fewer than kMostUnits.
+constexpr int64_t kMostUnits = ((int64_t)1 << 31) - (1 << 27);
 int64_t cache_attention_units(const AttentionArgs& a);
 // Each reads and clears the device error word of its translation unit.
 cudaError_t read_quant_error(uint32_t* err);

@@ -535,7 +535,8 @@ typedef struct {
  * number of rows) or above max_pages * page_tokens, and a page outside the
  * cache, touch nothing outside the tensors; the next mxfp4_device_status
  * returns MXFP4_ERR_INVALID_ARG. Appends and reads skip them; attention gives
- * NaN where a missing page is attended. */
+ * NaN where a missing page is attended (and does nothing at all where starts
+ * that fall name rows so often that the work passes its limit). */
 typedef struct {
   const int32_t* page_table;
   int64_t ld_table;
@@ -597,7 +598,7 @@ typedef struct {
  * (proposed tokens, a prompt's chunk) attend causally.
  *  q    bf16 [tokens, q_heads, head_dim]; q_heads a multiple of heads, up to
  *       65535, tokens * q_heads below 2^30 (and the work of a call, about
- *       tokens * q_heads * max_pages * page_tokens / 256, below 2^31). It goes in
+ *       tokens * q_heads * max_pages * page_tokens / 256, below 15 * 2^27). It goes in
  *       to 2^-39 of its row's largest magnitude.
  *  out  bf16 or fp32 [tokens, q_heads, head_dim]; lse fp32 [tokens, q_heads]
  *       contiguous, or NULL.

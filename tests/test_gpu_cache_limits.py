@@ -318,3 +318,20 @@ def test_a_missing_page_beside_rows_that_do_not_attend_it():
     c.table[0, 3] = c.table[0, 0]
     c.L, c.n = [48], [2]
     check(c, q[:2], out[:2], lse[:2], BF16)
+
+
+@pytest.mark.parametrize("B,rows", [(4, 1600), (34, 600)])
+def test_falling_starts_of_more_work_than_is_counted(B, rows):
+    """Rows named again and again, each time with as many tokens as a call may have: nothing is done."""
+    import gemm_pt_block_gb300 as mx
+
+    codes = torch.zeros((1, 2, 1, 128, 64), dtype=torch.uint8, device=DEV)
+    scales = torch.zeros((1, 2, 1), dtype=torch.uint8, device=DEV)
+    table = torch.zeros((B, (1 << 22) - 1 if B == 4 else 1 << 21), dtype=torch.int32, device=DEV)
+    lens = torch.full((B,), table.shape[1] * 128, dtype=torch.int32, device=DEV)
+    starts = (torch.arange(B + 1, device=DEV) % 2 * rows).int()
+    q = torch.zeros((rows, 1, 64), dtype=BF16, device=DEV)
+    out = torch.full((rows, 1, 64), 7.0, device=DEV)
+    mx.mxfp8_cache_attention(q, codes, scales, table, lens, starts=starts, out=out)
+    assert mx.device_status() == BAD
+    assert bool((out == 7).all())
