@@ -559,12 +559,14 @@ __device__ __forceinline__ int32_t token_of(const AttentionArgs& a, int32_t r) {
   return (int32_t)((t + (((uint32_t)r - t) >> a.group_shift[0])) >> a.group_shift[1]);
 }
 
-// What a call says of one sequence, as it lies in memory.
+// What a call says of one sequence, as it lies in memory. (This kernel starts while
+// the one before it runs, which may write any of its inputs: ordinary loads, none
+// by the path for data that stay as they are for a kernel's whole life.)
 struct Said {
   int32_t row, end, len;
 };
 __device__ __forceinline__ Said said(const CacheArgs& c, int32_t b) {
-  return Said{c.starts ? __ldg(c.starts + b) : b, c.starts ? __ldg(c.starts + b + 1) : b + 1, __ldg(c.lens + b)};
+  return Said{c.starts ? c.starts[b] : b, c.starts ? c.starts[b + 1] : b + 1, c.lens[b]};
 }
 
 // A place in the order of all units: sequences, their heads, their tiles of
@@ -865,7 +867,7 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
       // (pages that end before every row's window may be gone)
       if (j < w.hi && (a.window == 0 || (j | (a.c.page_tokens - 1)) > w.p0 - a.window)) {
         x.place = (j & (a.c.page_tokens - 1)) >> 4;
-        x.page = j >> a.shift < a.c.max_pages ? __ldg(a.c.table + (int64_t)w.b * a.c.ld_table + (j >> a.shift)) : -1;
+        x.page = j >> a.shift < a.c.max_pages ? a.c.table[(int64_t)w.b * a.c.ld_table + (j >> a.shift)] : -1;
       }
       return x;
     };
@@ -969,7 +971,7 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
       if (w.row0 + g < w.n * G) {
         const uint16_t* q = static_cast<const uint16_t*>(a.q.p) + row_of(a, a.q, w.row, w.head, w.row0 + g) + 4 * t;
 #pragma unroll
-        for (int s = 0; s < kSegs; ++s) x[s] = __ldg(reinterpret_cast<const uint2*>(q + 16 * s));
+        for (int s = 0; s < kSegs; ++s) x[s] = *reinterpret_cast<const uint2*>(q + 16 * s);
       }
 #pragma unroll
       for (int s = 0; s < kSegs; ++s)
@@ -1000,7 +1002,7 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
       // scales: a lane a part, the keys', then the values'
       const int32_t block = ctl->block[warp][stage][lane % kParts];
       uint32_t scale = 255u;
-      if (block >= 0) scale = __ldg(a.c.scales + block + (lane & kParts ? a.c.heads : 0));
+      if (block >= 0) scale = a.c.scales[block + (lane & kParts ? a.c.heads : 0)];
       float s[kParts][4];
 #pragma unroll
       for (int h = 0; h < kParts; ++h)
@@ -1052,7 +1054,7 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
         for (int i = 0; i < 2; ++i) {
           const int32_t r = min(w.row0 + 2 * t + i, w.n * G - 1), token = token_of(a, r);
           const int32_t j0 = c0 + g - (w.len - w.n + token);  // the first token's position less the row's
-          const float slope = a.slopes ? __ldg(a.slopes + w.head * G + r - token * G) * 1.44269504088896f : 0.0f;
+          const float slope = a.slopes ? a.slopes[w.head * G + r - token * G] * 1.44269504088896f : 0.0f;
           const int32_t most = a.window > 0 ? a.window : 0x7FFFFFFF;
 #pragma unroll
           for (int z = 0; z < 2 * kParts; ++z) {
