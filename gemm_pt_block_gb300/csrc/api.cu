@@ -806,9 +806,6 @@ mxfp4_status check_q_heads(const char* fn, mx::AttentionArgs* a, int32_t q_heads
   a->group_shift[1] = (uint8_t)(l > 1 ? l - 1 : 0);
   a->shift = c.page_tokens == 16 ? 4 : c.page_tokens == 32 ? 5 : c.page_tokens == 64 ? 6 : 7;
   a->window = window < (1 << 30) ? window : 1 << 30;  // (no length passes it)
-  if (mx::cache_attention_units(*a) >= mx::kMostUnits)
-    return fail(MXFP4_ERR_SHAPE, "%s: too many tokens (%d) of %d heads over %d pages for one call", fn, c.tokens, q_heads,
-                c.max_pages);
   return MXFP4_OK;
 }
 }  // namespace
@@ -836,6 +833,9 @@ mxfp4_status mxfp8_cache_attention(const mxfp8_cache* cache, const mxfp8_cache_b
   if (!params) return fail(MXFP4_ERR_INVALID_ARG, "%s: params is NULL", fn);
   if (params->window < 0) return fail(MXFP4_ERR_INVALID_ARG, "%s: window (%d) must be >= 0", fn, params->window);
   if ((st = check_q_heads(fn, &a, q_heads, params->window))) return st;
+  if (mx::cache_attention_units(a) >= mx::kMostUnits)
+    return fail(MXFP4_ERR_SHAPE, "%s: too many tokens (%d) of %d heads over %d pages for one call", fn, a.c.tokens, q_heads,
+                a.c.max_pages);
   if (!(params->scale >= -1.0e30f && params->scale <= 1.0e30f))
     return fail(MXFP4_ERR_INVALID_ARG, "%s: scale must be finite", fn);
   if (!(params->softcap == 0.0f || (params->softcap >= 1.0e-30f && params->softcap <= 1.0e30f)))

@@ -220,3 +220,12 @@ def test_waits_are_whole_warps():
         body = text[text.index(f"bool {name}("):]
         body = body[:body.index("\n}")]
         assert "__all_sync" in body and "kWaitLimitNs" in body
+
+
+def test_a_window_bounds_the_work(fake):  # noqa: F811
+    """A table that would be too wide without one: its workspace is known, and suffices."""
+    fake.fake_fail_at(-1)
+    wide = dict(tokens=1 << 20, max_pages=1 << 20, ld_table=1 << 20)
+    need = call(fake, "size", **wide)
+    assert need > 0 and call(fake, "attention", **wide) == 2
+    assert call(fake, "attention", window=100, ws_bytes=need, **wide) == 0
