@@ -247,3 +247,82 @@ def test_several_threads():
         t.join()
     assert not bad
     assert mx.device_status() == 0
+
+
+def test_a_step_captured_from_two_streams():
+    """Keys and queries made on streams of their own: the attention follows two kernels, or a copy."""
+    import gemm_pt_block_gb300 as mx
+
+    H, D, P, B = 2, 64, 32, 40
+    cache, eager = mx.KvCache(B * 20, H, D, P, DEV), mx.KvCache(B * 20, H, D, P, DEV)
+    table = torch.randperm(B * 20, device=DEV, generator=gen(110)).int().view(B, 20).contiguous()
+    lens = torch.zeros(B, dtype=torch.int32, device=DEV)
+    kv, q = torch.zeros((B, 2, H, D), device=DEV, dtype=BF16), torch.zeros((B, 4, D), device=DEV, dtype=BF16)
+    given = torch.zeros_like(q)
+
+    def step(c, side, copies):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            c.append(kv[:, 0], kv[:, 1], table, lens)
+        if copies:
+            q.copy_(given)
+        else:
+            torch.mul(given, 1.0, out=q)
+        main.wait_stream(side)
+        return c.attend(q, table, lens, with_lse=True)
+
+    graphs = []
+    warm, side = torch.cuda.Stream(), torch.cuda.Stream()
+    warm.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(warm):
+        step(cache, side, False)
+    assert mx.device_status() == 1                          # (lengths of no token yet: nothing was appended)
+    for copies in (False, True):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = step(cache, side, copies)
+        graphs.append((g, out))
+    for i in range(300):
+        lens += 1 + torch.arange(B, device=DEV).int() % 2
+        kv.normal_(generator=gen(111 + i))
+        given.normal_(generator=gen(500 + i))
+        graphs[i % 2][0].replay()
+        got, lse = graphs[i % 2][1]
+        eager.append(kv[:, 0], kv[:, 1], table, lens)
+        want, want_lse = eager.attend(given, table, lens, with_lse=True)
+        if i % 7 == 0:
+            torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(lse, want_lse), i
+    assert torch.equal(cache.codes, eager.codes) and torch.equal(cache.scales, eager.scales)
+    assert mx.device_status() == 0
+
+
+def test_pages_behind_the_window_are_used_again():
+    """Steps of a model with a window: pages that no query reaches any more go to other sequences."""
+    import gemm_pt_block_gb300 as mx
+
+    H, G, D, P, window, B = 2, 2, 64, 16, 40, 3
+    pages, whole = Pages(B * 5, P, B, 30), Pages(200, P, B, 30)
+    cache, full = mx.KvCache(B * 5, H, D, P, DEV), mx.KvCache(200, H, D, P, DEV)
+    g = gen(120)
+    new = [30, 17, 1]
+    for i in range(90):
+        table, lens, starts = pages.step(new)
+        table2, lens2, _ = whole.step(new)
+        x = torch.randn((sum(new), 2, H, D), device=DEV, generator=g).to(BF16)
+        q = torch.randn((sum(new), H * G, D), device=DEV, generator=g).to(BF16)
+        cache.append(x[:, 0], x[:, 1], table, lens, starts)
+        full.append(x[:, 0], x[:, 1], table2, lens2, starts)
+        out, lse = cache.attend(q, table, lens, starts, with_lse=True, window=window)
+        want, want_lse = full.attend(q, table2, lens2, starts, with_lse=True, window=window)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse), i
+        for b in range(B):
+            for j in range(max(0, pages.lens[b] - window + 1) // P):
+                if int(pages.table[b, j]) >= 0:
+                    pages.free.append(int(pages.table[b, j]))
+                    pages.table[b, j] = -1
+        new = [1 + (i + b) % 3 for b in range(B)]
+        if max(pages.lens) + 3 > 30 * P:
+            break
+    assert mx.device_status() == 0
