@@ -804,6 +804,7 @@ mxfp4_status check_q_heads(const char* fn, mx::AttentionArgs* a, int32_t q_heads
   a->group_mul = (uint32_t)(((((uint64_t)1 << l) - (uint64_t)a->group) << 32) / (uint64_t)a->group + 1);
   a->group_shift[0] = l < 1 ? 0 : 1;
   a->group_shift[1] = (uint8_t)(l > 1 ? l - 1 : 0);
+  a->spare = c.sequences > 1;
   a->shift = c.page_tokens == 16 ? 4 : c.page_tokens == 32 ? 5 : c.page_tokens == 64 ? 6 : 7;
   a->window = window < (1 << 30) ? window : 1 << 30;  // (no length passes it)
   return MXFP4_OK;

@@ -449,7 +449,7 @@ struct AttnCtl {
   int32_t block[kMostWarps][kMostStages][4];  // of the keys in a stage's parts (-1: none)
   Tile head[kMostWarps], open[kMostWarps];       // tiles that a warp shares with the one before it, and behind it
   Start start[kMostWarps];               // of the warps' runs
-  int32_t left[kMostWarps];                  // units of the open tile behind a warp's run
+  int32_t left[kMostWarps];                  // units of the open tile behind a warp's run, but for the spare one
   uint8_t has[kMostWarps];                   // kHead, kOpen, kBegan
   uint32_t abort;
 };
@@ -571,7 +571,12 @@ __device__ __forceinline__ Said said(const CacheArgs& c, int32_t b) {
 
 // A place in the order of all units: sequences, their heads, their tiles of
 // kRows query rows, kChunk tokens at a time. A sequence's tiles count alike (the
-// longest's units): units that a tile has no tokens for are passed over.
+// longest's units): units that a tile has no tokens for are passed over. So is, where
+// there are several sequences, one more of each tile (a.spare), which stands for what a
+// tile costs by itself, its queries and results, about a unit's time: 200 sequences of 9
+// to 601 tokens, 64 channels, 34.7 us and 37.9 without; 64 of 130 to 8192, 128 channels,
+// 50.7 and 52.8; but 256 of 300 tokens each 53.8 and 51.4, and one of a single token
+// would take 6.7 and takes 6.1.
 template <int kChunk>
 struct Walk {
   int32_t b, n, row, len, tiles, units;  // sequence: rows, first row, length, tiles, units of each
@@ -599,7 +604,7 @@ struct Walk {
     tiles = (n * G + kRows - 1) / kRows;
     const int32_t tokens = (kRows + G - 2) / G + 1;  // that a tile's rows may belong to
     const int32_t span = a.window > 0 ? min(len, a.window + tokens + kChunk) : len;
-    units = max(1, (span + kChunk - 1) / kChunk);
+    units = max(1, (span + kChunk - 1) / kChunk) + a.spare;
     return a.c.heads * tiles * units;
   }
   // Unit u of the sequence, where a run begins.
@@ -630,7 +635,8 @@ struct Walk {
   __device__ __forceinline__ int32_t token() const { return lo + unit * kChunk; }
   // Whether this unit holds tokens to attend.
   __device__ __forceinline__ bool live() const { return token() < hi; }
-  __device__ __forceinline__ bool last() const { return unit == units - 1; }
+  __device__ __forceinline__ bool last(const AttentionArgs& a) const { return unit == units - 1 - a.spare; }
+  __device__ __forceinline__ bool spare(const AttentionArgs& a) const { return unit == units - a.spare; }
   __device__ __forceinline__ Tile rows(int G) const { return Tile{row, row0, min(n * G - row0, kRows), head}; }
   // The next unit (there is one).
   __device__ __forceinline__ void next(const AttentionArgs& a) {
@@ -962,6 +968,10 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
   if (units && !few) w.begin(a, ctl->start[warp]);
 
   for (int32_t u = 0; u < units; ++u) {
+    if (w.spare(a)) {
+      if (u + 1 < units) w.next(a);
+      continue;
+    }
     if (u == 0 || w.unit == 0) {
       // queries of this tile, row by row times a power of two: the largest in [2^14, 2^15)
       uint2 x[kSegs];
@@ -1177,7 +1187,7 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
     }
 
     has = kOpen | (u < w.unit ? kBegan : 0) | (has & kHead);
-    if (w.last()) {
+    if (w.last(a)) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -1242,7 +1252,7 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
     ctl->has[warp] = has;
     if (has & kOpen) {
       ctl->open[warp] = w.rows(G);
-      ctl->left[warp] = w.units - 1 - w.unit;
+      ctl->left[warp] = w.units - 1 - a.spare - w.unit;
     }
   }
   warps_sync<kWarps>();
@@ -1531,7 +1541,7 @@ AttnShape attn_shape(const AttentionArgs& a) {
   const int64_t G = a.group, rows = a.c.tokens * G, tiles = rows / kRows + a.c.sequences;
   const int64_t most = (int64_t)a.c.max_pages * a.c.page_tokens + 1, windowed = a.window + (kRows + G - 2) / G + 1 + S::kChunk;
   const int64_t span = a.window > 0 && windowed < most ? windowed : most;
-  const int64_t units = (span + S::kChunk - 1) / S::kChunk, all = tiles * a.c.heads * units, ctas = (all + S::kWarps - 1) / S::kWarps;
+  const int64_t units = (span + S::kChunk - 1) / S::kChunk, all = tiles * a.c.heads * (units + a.spare), ctas = (all + S::kWarps - 1) / S::kWarps;
   return AttnShape{S::kWarps, (int)(ctas < kSms ? ctas : kSms), units > 1, all};
 }
 AttnShape attn_shape(const AttentionArgs& a) {

@@ -135,6 +135,7 @@ struct AttentionArgs {
   float scale, softcap;
   int32_t q_heads, window;
   int32_t group, shift;  // query heads to a head of the cache; page_tokens = 1 << shift
+  int32_t spare;         // 1 where there are several sequences: units that a tile counts for its beginning and end
   uint32_t group_mul;    // x / group = (t + ((x - t) >> group_shift[0])) >> group_shift[1], t the high half of
   uint8_t group_shift[2];  // group_mul * x
   bool out_f32;
