@@ -390,14 +390,20 @@ __global__ void __launch_bounds__(1024) cache_read_kernel(CacheArgs c, Heads k, 
 // The work is cut into units of 32 or 64 tokens of one sequence, one head of the cache
 // and one tile of query rows (the rows of the query heads that share the head,
 // over the sequence's new tokens), and every warp of the GPU takes an equal run of
-// them, whatever the lengths: eight warps of a CTA an SM that multiply, and a
-// ninth that fetches for them by TMA, keys and values apart, into a ring for each.
+// them, whatever the lengths: seven to fourteen warps of a CTA an SM that multiply, and
+// one or two that fetch for them by TMA, keys and values apart, into a ring for each.
 // A warp holds maxima and sums of its tile by itself; nothing in its loop waits for
 // another. Codes become f16 in registers (exact), keys as the A operand of S^T = K
 // Q^T, values, transposed as they are read, as that of O^T = V^T P^T: query rows
 // are the instruction's N of eight. Tiles that several warps share are joined in
 // the CTA when its runs end; those that several CTAs share leave their parts in
 // the workspace for cache_join_kernel.
+//
+// One tile a head is bound by HBM from 96 channels on (1 x 131072 tokens, 8 heads of
+// 128: 50.6 us, 78 % of a copy's rate), by the instructions of scores and conversions
+// at 64 (32 x 4096 tokens 32 us, 62 %); several tiles a head read again from L2 and
+// convert again (16 sequences of 1000 to 16384 tokens, 16 rows a head: 52 us, 54 %). A
+// call's least is its start and the join, about 6 us.
 
 constexpr float kTop = 15.0f;                   // weights are held times 2^15: f16 keeps 2^-39 of the largest
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
@@ -407,8 +413,11 @@ constexpr int kRows = 8;  // of a tile: sixteen, for half the conversions, gaine
 template <int D>
 struct Attn {
   // Warps that multiply: as many as their registers (sums D / 4, queries D / 8 of
-  // them) leave room for on the SM without spilling. Then those that fetch for them,
-  // a lane for 16 tokens of a unit.
+  // them) leave room for on the SM without spilling (128 channels: 50.6 us at 131072
+  // tokens with eleven, 57 with fifteen, which spill, 58 with seven). Then those that
+  // fetch for them, a lane for 16 tokens of a unit; a warp's copies go out one after
+  // the other, and pages of 16 tokens of 64 channels need two (32 x 4096 tokens 33 us;
+  // 48 with one).
   static constexpr int kWarps = D <= 64 ? 14 : D <= 128 ? 11 : 7;
   static constexpr int kFetch = D <= 64 ? 2 : 1;
   static constexpr int kFetched = kWarps / kFetch;  // warps that one fetches for
@@ -417,7 +426,9 @@ struct Attn {
   // different banks. 96 bytes are not swizzled: rows three apart meet in pairs, which
   // costs less than copies in slabs of 32 (32 x 4096 tokens: 43.8 us, 48.7).
   static constexpr int kBox = D == 96 ? 96 : D % 128 == 0 ? 128 : 64;
-  static constexpr int kChunk = D == 64 ? 64 : 32;                         // tokens of a unit, in parts of 16
+  // Tokens of a unit, in parts of 16 (64 channels: 200 sequences of 9 to 601 tokens 33 us
+  // with 64, 39 with 32; more than 64 channels have no registers for 64).
+  static constexpr int kChunk = D == 64 ? 64 : 32;
   static constexpr int kParts = kChunk / 16;
   static constexpr int kLanes = 32 / kParts;                               // of a fetching warp for one part
   static constexpr int kPart = 16 * D;                                     // a part's keys or values
@@ -574,7 +585,7 @@ __device__ __forceinline__ Said said(const CacheArgs& c, int32_t b) {
 // longest's units): units that a tile has no tokens for are passed over. So is, where
 // there are several sequences, one more of each tile (a.spare), which stands for what a
 // tile costs by itself, its queries and results, about a unit's time: 200 sequences of 9
-// to 601 tokens, 64 channels, 34.7 us and 37.9 without; 64 of 130 to 8192, 128 channels,
+// to 601 tokens, 64 channels, 34.7 us, 37.9 without; 64 of 130 to 8192, 128 channels,
 // 50.7 and 52.8; but 256 of 300 tokens each 53.8 and 51.4, and one of a single token
 // would take 6.7 and takes 6.1.
 template <int kChunk>
@@ -1043,6 +1054,10 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
       }
 
       // scores in log2 units; -infinity where a row does not attend
+      // (a tile of one row: odd rows, which no lane needs, are left out. At 64 channels,
+      // where scores are most of the work: 200 sequences 34.8 us without, 33.5 with; at 96,
+      // 32 x 4096 tokens 42.3 and 42.8)
+      const bool single = D == 64 && w.n * G - w.row0 == 1;
       const bool whole = c0 + kChunk <= w.p0 + 1 && (a.window == 0 || c0 > w.hi - 1 - a.window);
 #pragma unroll
       for (int h = 0; h < kParts; ++h) {
@@ -1062,6 +1077,7 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
       if (a.slopes || !whole) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
+          if (i == 1 && single) continue;
           const int32_t r = min(w.row0 + 2 * t + i, w.n * G - 1), token = token_of(a, r);
           const int32_t j0 = c0 + g - (w.len - w.n + token);  // the first token's position less the row's
           const float slope = a.slopes ? a.slopes[w.head * G + r - token * G] * 1.44269504088896f : 0.0f;
@@ -1107,6 +1123,9 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
       float cm[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
+        cm[i] = m[i];
+        keep[i] = 1.0f;
+        if (i == 1 && single) continue;
         float part[kParts], x = -INFINITY;
 #pragma unroll
         for (int h = 0; h < kParts; ++h) {
@@ -1137,6 +1156,8 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
         float p[4];
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
+          p[z] = 0.0f;
+          if ((z & 1) && single) continue;
           const float x = s[h][z] - cm[z & 1];
           sum[z & 1] += ex2(x);
           p[z] = ex2(x + c[z & 1]);
