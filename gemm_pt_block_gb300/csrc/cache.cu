@@ -192,9 +192,9 @@ __device__ __forceinline__ uint32_t most16(const Vec16<float>& v) {
   return __float_as_uint(m) & 0x7FFFFFFFu;
 }
 
-// A few new tokens a page: a warp takes a block, eight elements a lane. Values
-// past the first 256 are read twice.
-template <typename T>
+// A few new tokens a page: a warp takes a block, eight elements a lane at a time.
+// Values past the first 256 * kHeld are read twice.
+template <typename T, int kHeld>
 __global__ void __launch_bounds__(256) cache_append_few_kernel(CacheArgs c, Heads k, Heads v) {
   const int lane = threadIdx.x & 31, task = blockIdx.y * 8 + (threadIdx.x >> 5);
   ptx::launch_dependents();
@@ -208,25 +208,38 @@ __global__ void __launch_bounds__(256) cache_append_few_kernel(CacheArgs c, Head
   const uint32_t old = t.lo > 0 ? c.scales[block] : 0u;
   const T* from = static_cast<const T*>(x.p) + (int64_t)(t.s.row + (t.at + t.lo - t.s.pos)) * x.ld_t + (int64_t)h * x.ld_h;
   const int count = (t.hi - t.lo) * per;
-  auto take = [&](int i, float (&f)[8]) {
+  auto take = [&](int i, Vec8<T>& w) {
     const int token = i / per;
-    Vec8<T> w;
     load8(from + token * x.ld_t + (i - token * per) * 8, w);
-    unpack8(w, f);
   };
-  float first[8] = {}, f[8];
-  if (lane < count) take(lane, first);
-  float m = most8(0.0f, first);
-  for (int i = lane + 32; i < count; i += 32) {
-    take(i, f);
+  Vec8<T> held[kHeld], w;
+  float f[8], m = 0.0f;
+#pragma unroll
+  for (int z = 0; z < kHeld; ++z)
+    if (lane + 32 * z < count) take(lane + 32 * z, held[z]);
+#pragma unroll
+  for (int z = 0; z < kHeld; ++z)
+    if (lane + 32 * z < count) {
+      unpack8(held[z], f);
+      m = most8(m, f);
+    }
+  for (int i = lane + 32 * kHeld; i < count; i += 32) {
+    take(i, w);
+    unpack8(w, f);
     m = most8(m, f);
   }
   const uint32_t scale = max(scale_for(__reduce_max_sync(0xffffffffu, __float_as_uint(m) & 0x7FFFFFFFu)), old);
   const float mul = scale_factor(scale);
   uint2* to = reinterpret_cast<uint2*>(codes) + t.lo * per;
-  if (lane < count) put_at(to + lane, quantized8(first, mul, scale), c.codes, c.codes_bytes);
-  for (int i = lane + 32; i < count; i += 32) {
-    take(i, f);
+#pragma unroll
+  for (int z = 0; z < kHeld; ++z)
+    if (lane + 32 * z < count) {
+      unpack8(held[z], f);
+      put_at(to + lane + 32 * z, quantized8(f, mul, scale), c.codes, c.codes_bytes);
+    }
+  for (int i = lane + 32 * kHeld; i < count; i += 32) {
+    take(i, w);
+    unpack8(w, f);
     put_at(to + i, quantized8(f, mul, scale), c.codes, c.codes_bytes);
   }
   if (t.lo > 0 && old < scale && scale != 255u) {
@@ -1525,12 +1538,14 @@ cudaError_t launch_cache_append(const CacheArgs& c, const Heads& k, const Heads&
   if (c.tokens == 0 || c.sequences == 0) return cudaSuccess;
   (void)cudaGetLastError();
   const int64_t slots = c.starts ? c.tokens / c.page_tokens + 2 * (int64_t)c.sequences : c.sequences;
-  if (c.tokens <= 4 * (int64_t)c.sequences) {
+  // A warp a block up to eight tokens a sequence (8 heads of 128 in bf16: 8 and 256
+  // sequences of 8 tokens 3.2 and 6.1 us, 3.1 and 14.1 by whole CTAs; of 16, 5.3 and
+  // 10.7, but 3.2 and 15.6); one row each is 256 elements at most.
+  if (c.tokens <= 8 * (int64_t)c.sequences) {
     const dim3 grid((unsigned)slots, (unsigned)((2 * c.heads + 7) / 8));
-    if (f32)
-      cache_append_few_kernel<float><<<grid, 256, 0, st>>>(c, k, v);
-    else
-      cache_append_few_kernel<uint16_t><<<grid, 256, 0, st>>>(c, k, v);
+    (f32 ? c.starts ? cache_append_few_kernel<float, 4> : cache_append_few_kernel<float, 1>
+         : c.starts ? cache_append_few_kernel<uint16_t, 4> : cache_append_few_kernel<uint16_t, 1>)
+        <<<grid, 256, 0, st>>>(c, k, v);
     return cudaGetLastError();
   }
   const Launch l = launch_shape(c, slots);
