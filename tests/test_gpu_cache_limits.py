@@ -335,3 +335,18 @@ def test_falling_starts_of_more_work_than_is_counted(B, rows):
     mx.mxfp8_cache_attention(q, codes, scales, table, lens, starts=starts, out=out)
     assert mx.device_status() == BAD
     assert bool((out == 7).all())
+
+
+@pytest.mark.parametrize("B,H,G,n,D,L,window", [(19, 8, 4, 1, 128, 700, 0), (20, 8, 4, 1, 128, 700, 0), (19, 8, 1, 1, 64, 1500, 0),
+                                                (32, 1, 20, 2, 96, 900, 0), (16, 3, 9, 2, 64, 650, 300), (3, 2, 8, 1, 256, 30, 0)])
+def test_as_many_tiles_as_processors(B, H, G, n, D, L, window):
+    """A tile to a processor, one more, sequences without rows or tokens among them."""
+    import gemm_pt_block_gb300 as mx
+
+    Ls, ns = [L - 3 * (i % 5) for i in range(B)], [n] * B
+    Ls[2], ns[1] = 0, 0
+    c = make_cache(Ls, ns, H, D, 32, seed=50)
+    q = torch.randn((c.T, H * G, D), device=DEV, generator=gen(51)).to(BF16)
+    out, lse = mx.mxfp8_cache_attention(q, c.codes, c.scales, c.table, c.lens, starts=c.starts, with_lse=True, window=window)
+    assert mx.device_status() == 0
+    check(c, q, out, lse, BF16, window=window)
