@@ -1562,13 +1562,18 @@ cudaError_t launch_cache_append(const CacheArgs& c, const Heads& k, const Heads&
   if (c.tokens == 0 || c.sequences == 0) return cudaSuccess;
   (void)cudaGetLastError();
   const int64_t slots = c.starts ? c.tokens / c.page_tokens + 2 * (int64_t)c.sequences : c.sequences;
-  // A warp a block up to eight tokens a sequence (8 heads of 128 in bf16: 8 and 256
-  // sequences of 8 tokens 3.2 and 6.1 us, 3.1 and 14.1 by whole CTAs; of 16, 5.3 and
-  // 10.7, but 3.2 and 15.6); one row each is 256 elements at most.
-  if (c.tokens <= 8 * (int64_t)c.sequences) {
+  // A warp a block while it holds a sequence's new elements in registers: 1024 (heads of
+  // 128: 256 sequences of 8 tokens 6.1 us, 14.1 by whole CTAs; 8 of them 3.2 and 3.1),
+  // or 2048 where there are blocks enough (32 sequences of 16 tokens on 8 heads 4.2 and 5.0,
+  // 256 of them 8.7 and 15.4; but 16 of them 4.1 and 3.5). One row each is 256 at most.
+  const int64_t elems = (int64_t)c.tokens * c.head_dim, blocks = 2 * (int64_t)c.heads * c.sequences;
+  const bool held4 = elems <= 1024 * (int64_t)c.sequences, held8 = elems <= 2048 * (int64_t)c.sequences && blocks >= 512;
+  if (!c.starts || held4 || held8) {
     const dim3 grid((unsigned)slots, (unsigned)((2 * c.heads + 7) / 8));
-    (f32 ? c.starts ? cache_append_few_kernel<float, 4> : cache_append_few_kernel<float, 1>
-         : c.starts ? cache_append_few_kernel<uint16_t, 4> : cache_append_few_kernel<uint16_t, 1>)
+    (f32 ? !c.starts ? cache_append_few_kernel<float, 1>
+           : held4 ? cache_append_few_kernel<float, 4> : cache_append_few_kernel<float, 8>
+         : !c.starts ? cache_append_few_kernel<uint16_t, 1>
+           : held4 ? cache_append_few_kernel<uint16_t, 4> : cache_append_few_kernel<uint16_t, 8>)
         <<<grid, 256, 0, st>>>(c, k, v);
     return cudaGetLastError();
   }

@@ -350,3 +350,24 @@ def test_as_many_tiles_as_processors(B, H, G, n, D, L, window):
     out, lse = mx.mxfp8_cache_attention(q, c.codes, c.scales, c.table, c.lens, starts=c.starts, with_lse=True, window=window)
     assert mx.device_status() == 0
     check(c, q, out, lse, BF16, window=window)
+
+
+@pytest.mark.parametrize("B,H,D,P,few,many", [(130, 2, 128, 64, 13, 300), (130, 2, 64, 128, 24, 500), (9, 4, 256, 64, 3, 6),
+                                              (260, 1, 96, 32, 20, 90), (128, 2, 256, 64, 7, 60), (5, 8, 128, 64, 8, 9)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_appends_of_a_few_tokens(B, H, D, P, few, many, dtype):
+    """A few tokens a sequence, more than a warp holds in one of them, none in others."""
+    import gemm_pt_block_gb300 as mx
+
+    n = [few - i % 3 for i in range(B)]
+    n[B // 2], n[1] = many, 0
+    L = [n[i] + 11 * i % 150 for i in range(B)]
+    c = make_cache(L, n, H, D, P, seed=60, filled=[a - b for a, b in zip(L, n)])
+    kv = torch.randn((c.T, 2, H, D), device=DEV, generator=gen(61))
+    kv[:, :, 0] *= torch.exp2(torch.randint(-4, 9, (c.T, 2, 1), device=DEV, generator=gen(62)).float())
+    kv = kv.to(dtype)
+    want = append(c, kv[:, 0], kv[:, 1])
+    mx.mxfp8_cache_append(kv[:, 0], kv[:, 1], c.codes, c.scales, c.table, c.lens, starts=c.starts)
+    same(c.codes, want[0])
+    same(c.scales, want[1])
+    assert mx.device_status() == 0
