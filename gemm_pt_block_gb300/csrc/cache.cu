@@ -873,7 +873,6 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.group;
   const uint32_t ring = ptx::smem_u32(base), full = ptx::smem_u32(ctl->full), empty = ptx::smem_u32(ctl->empty);
 
-  ptx::launch_dependents();
   if (warp == kWarps) {
     for (int i = lane; i < kWarps * kMostStages; i += 32) {
       ptx::mbar_init(full + 8 * i, 1);
@@ -886,6 +885,7 @@ __global__ void __launch_bounds__(Attn<D>::kThreads, 1)
     ptx::fence_mbar_init();
   }
   ptx::wait_prior_grid();  // (nothing of the call's is read or written before)
+  ptx::launch_dependents();  // (only now: what starts next may count on all before this kernel)
   Walk<kChunk> w;
   const bool few = a.c.sequences <= 32;
   const Cut runs = find_start<D, kChunk>(a, warp, lane, ctl, reinterpret_cast<int32_t*>(stats), &w);
@@ -1450,8 +1450,8 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   const float* parts = a.ws + gridDim.x * (sizeof(Split) / 4) + 2 * (int64_t)blockIdx.x * part_floats(D);
   auto part = [&](int i) { return parts + (2 * i + (i == 0)) * part_floats(D); };
   const int behind = gridDim.x - blockIdx.x;  // parts that the workspace has room for
-  ptx::launch_dependents();
   ptx::wait_prior_grid();
+  ptx::launch_dependents();
   const Split sp = reinterpret_cast<const Split*>(a.ws)[blockIdx.x];
   constexpr int kMost = (kSms + 31) / 32;
   float m[kMost], lift[kMost], sum[kMost];
