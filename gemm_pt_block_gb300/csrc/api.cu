@@ -851,7 +851,7 @@ mxfp4_status mxfp8_cache_attention(const mxfp8_cache* cache, const mxfp8_cache_b
   if (need && (!workspace || workspace_bytes < need))
     return fail(MXFP4_ERR_INVALID_ARG, "%s: workspace of %zu bytes, %zu are needed", fn, workspace ? workspace_bytes : 0,
                 need);
-  a.ws = static_cast<float*>(workspace);
+  a.ws = need ? static_cast<float*>(workspace) : nullptr;  // (one that no call asked for is not written)
   a.ws_bytes = need;
   a.lse = lse;
   const int64_t n = (int64_t)a.c.tokens * q_heads * 4;

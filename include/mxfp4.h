@@ -603,7 +603,8 @@ typedef struct {
  *  out  bf16 or fp32 [tokens, q_heads, head_dim]; lse fp32 [tokens, q_heads]
  *       contiguous, or NULL.
  *  workspace  device memory, 16-byte aligned, of
- *       mxfp8_cache_attention_workspace_size bytes; scratch for the call alone.
+ *       mxfp8_cache_attention_workspace_size bytes; scratch for the call alone
+ *       (not touched where that is 0).
  * Results have the same bits on every call. Scores must stay below fp32's
  * largest value. A row of q with an infinity or a NaN gives NaN. */
 mxfp4_status mxfp8_cache_attention(const mxfp8_cache* cache, const mxfp8_cache_batch* batch,
