@@ -152,10 +152,11 @@ __device__ __forceinline__ bool slot_of(const CacheArgs& c, int lane, Slot* t) {
 __device__ __forceinline__ uint32_t scale_for(uint32_t m) {
   return m >= 0x7F800000u ? 255u : (uint32_t)max((int)(m >> 23) - 8 + ((m & 0x7FFFFFu) > 0x600000u), 0);
 }
-// What values are multiplied by under a scale, and older codes where it grows (below
-// 2^-30 every code rounds to zero).
+// What values are multiplied by under a scale (254, which only a page's older tokens can
+// bring: 2^-127, below the normal numbers), and older codes where it grows (below 2^-30
+// every code rounds to zero).
 __device__ __forceinline__ float scale_factor(uint32_t scale) {
-  return scale == 255u ? 0.0f : __uint_as_float((254u - scale) << 23);
+  return scale == 255u ? 0.0f : __uint_as_float(max((254u - scale) << 23, 0x400000u));
 }
 __device__ __forceinline__ float older_factor(uint32_t old, uint32_t scale) {
   return __uint_as_float((127u - min(scale - old, 64u)) << 23);
