@@ -87,6 +87,15 @@ class Mxfp4Attention(torch.nn.Module):
         for name in self._DECODE:                        # (they follow the module to a device; not its state)
             self.register_buffer(name, None, persistent=False)
 
+    def _apply(self, fn, recurse=True):
+        """The slopes follow the block to a device, not to a type: the kernel reads fp32, and
+        rounded ones would not come back."""
+        slopes = self.slopes
+        super()._apply(fn, recurse)
+        if slopes is not None and self.slopes.dtype != slopes.dtype:
+            self.slopes = slopes.to(self.slopes.device)
+        return self
+
     def cache(self, pages: int, page_tokens: int = 64) -> KvCache:
         """A cache for this layer, on its device."""
         return KvCache(pages, self.kv_heads, self.head_dim, page_tokens, self.norm.device)

@@ -1,0 +1,40 @@
+"""The attention block's arguments and buffers (no GPU needed)."""
+from __future__ import annotations
+
+import copy
+
+import pytest
+import torch
+
+
+def block(slopes, **kw):
+    import gemm_pt_block_gb300 as mx
+
+    return mx.Mxfp4Attention(256, 4, 2, 64, slopes=slopes, **kw)
+
+
+SLOPES = torch.tensor([1 / 3, -0.7, 1e-3, 2.0 ** 20 + 1])     # (three of them do not fit bf16)
+
+
+@pytest.mark.parametrize("cast", [lambda m: m.to(torch.bfloat16), lambda m: m.bfloat16(), lambda m: m.half(), lambda m: m.double(),
+                                  lambda m: m.to(torch.bfloat16).float(), lambda m: torch.nn.Sequential(m).bfloat16()[0],
+                                  lambda m: copy.deepcopy(m).half()])
+def test_slopes_keep_their_type_and_values(cast):
+    m = cast(block(SLOPES))
+    assert m.slopes.dtype == torch.float32 and torch.equal(m.slopes, SLOPES)
+    assert "slopes" in dict(m.named_buffers())
+
+
+def test_the_rest_of_the_block_is_cast():
+    m = block(SLOPES).half()
+    assert m.norm.dtype == m.qkv.weight.dtype == m.out.weight.dtype == torch.float16
+    assert block(None).half().slopes is None
+
+
+def test_slopes_follow_the_block_to_a_device():
+    m = block(SLOPES).to("meta", torch.bfloat16)
+    assert m.slopes.device.type == "meta" and m.slopes.dtype == torch.float32
+    m = m.to_empty(device="cpu")
+    assert m.slopes.device.type == "cpu" and m.slopes.dtype == torch.float32
+    m.load_state_dict(block(SLOPES).state_dict())
+    assert torch.equal(m.slopes, SLOPES)
