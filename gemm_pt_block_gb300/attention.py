@@ -23,6 +23,11 @@ from .ffn import _readable, _readable_vector
 from .linear import LinearRecipe, Mxfp4Linear
 
 
+def _check_head_dim(head_dim: int) -> None:
+    if head_dim not in (64, 96, 128, 192, 256):
+        raise ValueError(f"head_dim must be 64, 96, 128, 192 or 256 (got {head_dim})")
+
+
 class KvCache:
     """Keys and values of one layer in 8 bits: E4M3 codes [pages, 2, heads,
     page_tokens, head_dim] and one E8M0 scale for each page, kind and head,
@@ -32,8 +37,7 @@ class KvCache:
     def __init__(self, pages: int, heads: int, head_dim: int, page_tokens: int = 64, device=None):
         if page_tokens not in (16, 32, 64, 128):
             raise ValueError(f"page_tokens must be 16, 32, 64 or 128 (got {page_tokens})")
-        if head_dim not in (64, 96, 128, 192, 256):
-            raise ValueError(f"head_dim must be 64, 96, 128, 192 or 256 (got {head_dim})")
+        _check_head_dim(head_dim)
         self.codes = torch.zeros((pages, 2, heads, page_tokens, head_dim), dtype=torch.uint8, device=device)
         self.scales = torch.zeros((pages, 2, heads), dtype=torch.uint8, device=device)
 
@@ -59,7 +63,8 @@ class KvCache:
 class Mxfp4Attention(torch.nn.Module):
     """The attention half of a pre-norm layer, for decoding (see the module's
     text). `heads` query heads share `kv_heads` heads of the cache (default: as
-    many). dim, heads * head_dim and (heads + 2 kv_heads) * head_dim are multiples
+    many), of head_dim channels (default: dim // heads; 64, 96, 128, 192 or 256).
+    dim, heads * head_dim and (heads + 2 kv_heads) * head_dim are multiples
     of 128. The projections' parameters are those of Mxfp4Linear; no backward pass
     through the attention is provided."""
 
@@ -70,9 +75,10 @@ class Mxfp4Attention(torch.nn.Module):
                  slopes: torch.Tensor | None = None, device=None, dtype: torch.dtype = torch.bfloat16):
         super().__init__()
         kv_heads = heads if kv_heads is None else kv_heads
-        head_dim = dim // heads if head_dim is None else head_dim
-        if kv_heads < 1 or heads % kv_heads:
+        if heads < 1 or kv_heads < 1 or heads % kv_heads:
             raise ValueError(f"heads must be a multiple of kv_heads (got {heads}, {kv_heads})")
+        head_dim = dim // heads if head_dim is None else head_dim
+        _check_head_dim(head_dim)
         wide = (heads + 2 * kv_heads) * head_dim
         if dim % 128 or heads * head_dim % 128 or wide % 128:
             raise ValueError(f"dim, heads * head_dim and (heads + 2 kv_heads) * head_dim must be multiples of 128 "

@@ -38,3 +38,29 @@ def test_slopes_follow_the_block_to_a_device():
     assert m.slopes.device.type == "cpu" and m.slopes.dtype == torch.float32
     m.load_state_dict(block(SLOPES).state_dict())
     assert torch.equal(m.slopes, SLOPES)
+
+
+@pytest.mark.parametrize("kw", [dict(dim=256, heads=4, kv_heads=2, head_dim=32), dict(dim=1280, heads=16, head_dim=80),
+                                dict(dim=512, heads=4, kv_heads=2, head_dim=512), dict(dim=1024, heads=64), dict(dim=512, heads=1)],
+                         ids=str)
+def test_head_sizes_that_no_cache_has_are_refused(kw):
+    import gemm_pt_block_gb300 as mx
+
+    with pytest.raises(ValueError, match="head_dim must be 64, 96, 128, 192 or 256"):
+        mx.Mxfp4Attention(**kw)
+
+
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+def test_head_sizes_of_a_cache_are_taken(dim):
+    import gemm_pt_block_gb300 as mx
+
+    m = mx.Mxfp4Attention(256, 4, 2, dim)
+    assert m.cache(3, 16).codes.shape == (3, 2, 2, 16, dim)
+
+
+@pytest.mark.parametrize("heads,kv_heads", [(0, None), (-2, 1), (4, 0), (4, -4), (4, 3)])
+def test_head_counts_are_checked(heads, kv_heads):
+    import gemm_pt_block_gb300 as mx
+
+    with pytest.raises(ValueError, match="multiple of kv_heads"):
+        mx.Mxfp4Attention(256, heads, kv_heads)
