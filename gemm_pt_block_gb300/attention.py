@@ -64,8 +64,8 @@ class Mxfp4Attention(torch.nn.Module):
     """The attention half of a pre-norm layer, for decoding (see the module's
     text). `heads` query heads share `kv_heads` heads of the cache (default: as
     many), of head_dim channels (default: dim // heads; 64, 96, 128, 192 or 256).
-    dim, heads * head_dim and (heads + 2 kv_heads) * head_dim are multiples
-    of 128. The projections' parameters are those of Mxfp4Linear; no backward pass
+    slopes: [heads], kept as fp32. dim, heads * head_dim and (heads + 2 kv_heads) *
+    head_dim are multiples of 128. The projections' parameters are those of Mxfp4Linear; no backward pass
     through the attention is provided."""
 
     _DECODE = ("qkv_codes", "qkv_scales", "out_codes", "out_scales")
@@ -88,7 +88,11 @@ class Mxfp4Attention(torch.nn.Module):
         self.norm = torch.nn.Parameter(torch.ones(dim, device=device, dtype=dtype))
         self.qkv = Mxfp4Linear(dim, wide, recipe, device=device, dtype=dtype, out_dtype=torch.bfloat16)
         self.out = Mxfp4Linear(heads * head_dim, dim, recipe, device=device, dtype=dtype, out_dtype=torch.bfloat16)
-        self.register_buffer("slopes", None if slopes is None else slopes.to(device=device, dtype=torch.float32))
+        if slopes is not None:
+            if slopes.shape != (heads,):
+                raise ValueError(f"slopes must be [{heads}] (got {list(slopes.shape)})")
+            slopes = slopes.detach().to(device=device, dtype=torch.float32, copy=True).contiguous()
+        self.register_buffer("slopes", slopes)
         self._decode_params = None
         for name in self._DECODE:                        # (they follow the module to a device; not its state)
             self.register_buffer(name, None, persistent=False)

@@ -64,3 +64,21 @@ def test_head_counts_are_checked(heads, kv_heads):
 
     with pytest.raises(ValueError, match="multiple of kv_heads"):
         mx.Mxfp4Attention(256, heads, kv_heads)
+
+
+@pytest.mark.parametrize("slopes", [torch.ones(3), torch.ones(5), torch.ones(1, 4), torch.tensor(1.0)], ids=lambda t: str(tuple(t.shape)))
+def test_slopes_of_another_number_are_refused(slopes):
+    with pytest.raises(ValueError, match=r"slopes must be \[4\]"):
+        block(slopes)
+
+
+@pytest.mark.parametrize("slopes", [torch.ones(1).expand(4), torch.arange(8.0)[::2], torch.nn.Parameter(torch.arange(4.0)),
+                                    torch.arange(4).double()], ids=["expanded", "every other", "parameter", "double"])
+def test_slopes_are_the_blocks_own(slopes):
+    want = slopes.detach().float().clone()
+    m = block(slopes)
+    assert m.slopes.dtype == torch.float32 and m.slopes.is_contiguous() and not m.slopes.requires_grad
+    with torch.no_grad():
+        slopes[:1] = 9.0
+    assert torch.equal(m.slopes, want)
+    assert "slopes" not in dict(m.named_parameters())
