@@ -597,9 +597,12 @@ typedef struct {
  * -infinity. One token for each sequence is a decode step's form; several
  * (proposed tokens, a prompt's chunk) attend causally.
  *  q    bf16 [tokens, q_heads, head_dim]; q_heads a multiple of heads, up to
- *       65535, tokens * q_heads below 2^30 (and the work of a call, about
- *       tokens * q_heads * max_pages * page_tokens / 256, below 15 * 2^27). It goes in
- *       to 2^-39 of its row's largest magnitude.
+ *       65535, tokens * q_heads below 2^30. It goes in to 2^-39 of its row's largest
+ *       magnitude. With group = q_heads / heads a call has up to heads * (floor(tokens *
+ *       group / 8) + sequences) tiles of ceil(span / 32) units (64 in place of 32 at
+ *       head_dim 64), one more each where there are several sequences; span is
+ *       max_pages * page_tokens + 1, with a window at most window + floor((group + 6) /
+ *       group) + 1 + 32 (64). All its units together must be below 15 * 2^27.
  *  out  bf16 or fp32 [tokens, q_heads, head_dim]; lse fp32 [tokens, q_heads]
  *       contiguous, or NULL.
  *  workspace  device memory, 16-byte aligned, of
