@@ -841,6 +841,10 @@ mxfp4_status mxfp8_cache_attention(const mxfp8_cache* cache, const mxfp8_cache_b
     return fail(MXFP4_ERR_INVALID_ARG, "%s: scale must be finite", fn);
   if (!(params->softcap == 0.0f || (params->softcap >= 1.0e-30f && params->softcap <= 1.0e30f)))
     return fail(MXFP4_ERR_INVALID_ARG, "%s: softcap must be 0 or a positive number", fn);
+  // (what the kernel multiplies by; an infinity would make scores of 0 no numbers)
+  if (params->softcap > 0.0f && std::fabs((double)params->scale) > 1.0e30 * (double)params->softcap)
+    return fail(MXFP4_ERR_INVALID_ARG, "%s: scale / softcap must be at most 1e30 (got %g / %g)", fn, params->scale,
+                params->softcap);
   if ((reinterpret_cast<uintptr_t>(params->slopes) | reinterpret_cast<uintptr_t>(lse)) & 3u)
     return fail(MXFP4_ERR_ALIGN, "%s: slopes and lse must be 4-byte aligned", fn);
   if ((st = check_heads(fn, "q", q, a.c.tokens, q_heads, a.c.head_dim, false, &a.q))) return st;

@@ -578,7 +578,9 @@ mxfp4_status mxfp8_cache_read(const mxfp8_cache* cache, const mxfp8_cache_batch*
                               const mxfp8_heads* k, const mxfp8_heads* v, void* stream);
 
 /* Scores of mxfp8_cache_attention, s = scale * (q . k), then
- *  softcap  > 0: s = softcap * tanh(s / softcap); 0: none.
+ *  scale    of magnitude up to 1e30.
+ *  softcap  > 0: s = softcap * tanh(s / softcap); 0: none. 1e-30 to 1e30, and
+ *           scale / softcap of magnitude up to 1e30.
  *  slopes   [q_heads] fp32 device memory: s += slopes[h] * (j - p) for the key of
  *           position j and the query of position p; NULL: none.
  *  window   > 0: a query attends the last `window` tokens up to its own; 0: all. */

@@ -58,6 +58,16 @@ def test_the_widest_window_that_is_taken(fake, D, group):  # noqa: F811
     assert call(fake, "attention", window=hi, **kw) == 2
 
 
+@pytest.mark.parametrize("status,scale,softcap", [
+    (1, 1e30, 1e-30), (1, -1e30, 1e-30), (1, 1e10, 1e-21), (1, 2.0, 1e-30), (0, 0.5, 1e-30), (0, -0.5, 1e-30), (0, 1e30, 1.5), (0, 1e-30, 1e30),
+    (0, 0.0, 1e-30), (0, 0.125, 50.0), (0, 1e30, 0.0), (1, 0.125, 1e-31), (1, 0.125, 2e30), (1, 2e30, 0.0), (1, -2e30, 0.0),
+])
+def test_scales_and_caps(fake, status, scale, softcap):  # noqa: F811
+    fake.fake_fail_at(-1)
+    assert call(fake, "attention", scale=scale, softcap=softcap) == status
+    assert fake.fake_launches() == (2 if status == 0 else 0)
+
+
 def test_the_case_of_many_sequences_of_one_row_a_head():
     """Nine times the work of the rows alone: at group 1 each sequence's tile holds one row of eight."""
     assert units(4096, 4096, 32, 32, 128, 64, 1 << 14) >= LIMIT
