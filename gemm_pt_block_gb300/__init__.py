@@ -46,6 +46,7 @@ from .binding import (  # noqa: F401
     Mxfp4Error,
     QuantParams,
     device_status,
+    selftest_cache_wait_timeout,
     selftest_wait_timeout,
     hadamard32,
     lib,

@@ -183,6 +183,8 @@ def load_library(path: str) -> ctypes.CDLL:
     L.mxfp4_device_status.argtypes = [P]
     L.mxfp4_selftest_wait_timeout.restype = i32
     L.mxfp4_selftest_wait_timeout.argtypes = [P]
+    L.mxfp8_selftest_cache_wait_timeout.restype = i32
+    L.mxfp8_selftest_cache_wait_timeout.argtypes = [P]
     L.mxfp4_bounds_check_shrink.restype = i32
     L.mxfp4_bounds_check_shrink.argtypes = [i64]
     return L
@@ -776,7 +778,7 @@ def mxfp8_cache_attention(q: torch.Tensor, codes: torch.Tensor, scales: torch.Te
 
 
 def device_status(stream=None) -> int:
-    """Synchronizes the stream and returns (and clears) the GEMM's device error word."""
+    """Synchronizes the stream and returns (and clears) the device error word."""
     s = torch.cuda.current_stream() if stream is None else stream
     return int(lib().mxfp4_device_status(ctypes.c_void_p(s.cuda_stream)))
 
@@ -786,3 +788,9 @@ def selftest_wait_timeout(stream=None) -> None:
     outcome, MXFP4_ERR_TIMEOUT, is then read with device_status()."""
     s = torch.cuda.current_stream() if stream is None else stream
     _check(lib().mxfp4_selftest_wait_timeout(ctypes.c_void_p(s.cuda_stream)))
+
+
+def selftest_cache_wait_timeout(stream=None) -> None:
+    """The same for the waits of mxfp8_cache_attention."""
+    s = torch.cuda.current_stream() if stream is None else stream
+    _check(lib().mxfp8_selftest_cache_wait_timeout(ctypes.c_void_p(s.cuda_stream)))

@@ -872,7 +872,7 @@ mxfp4_status mxfp4_device_status(void* stream) {
   cudaError_t e = mx::read_device_error(static_cast<cudaStream_t>(stream), &err);
   if (e != cudaSuccess) return from_cuda(e, "mxfp4_device_status");
   if (err == MXFP4_ERR_TIMEOUT)
-    return fail(MXFP4_ERR_TIMEOUT, "a bounded device-side wait in the GEMM ran out");
+    return fail(MXFP4_ERR_TIMEOUT, "a bounded device-side wait ran out");
   if (err == MXFP4_ERR_BOUNDS)
     return fail(MXFP4_ERR_BOUNDS, "a kernel store fell outside its output (skipped)");
   if (err == MXFP4_ERR_INVALID_ARG)
@@ -895,6 +895,10 @@ mxfp4_status mxfp4_selftest_wait_timeout(void* stream) {
   cudaError_t e = mx::launch_wait_probe(static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return from_cuda(e, "mxfp4_selftest_wait_timeout");
   return MXFP4_OK;
+}
+
+mxfp4_status mxfp8_selftest_cache_wait_timeout(void* stream) {
+  return from_cuda(mx::launch_cache_wait_probe(static_cast<cudaStream_t>(stream)), "mxfp8_selftest_cache_wait_timeout");
 }
 
 }  // extern "C"

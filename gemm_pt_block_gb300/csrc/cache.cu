@@ -1701,6 +1701,37 @@ cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t st) {
   }
 }
 
+namespace {
+// Both waits on barriers that nothing signals: the first warp as a warp that multiplies,
+// the second with one lane in need as a warp that fetches. Each runs out by its limit and
+// says so to all of its lanes; the word is kErrIndex instead where one of them was told
+// otherwise.
+__global__ void __launch_bounds__(64) cache_wait_probe_kernel() {
+  __shared__ uint64_t bars[2];
+  __shared__ uint32_t abort[2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t bar = ptx::smem_u32(bars + warp);
+  if (lane == 0) {
+    ptx::mbar_init(bar, 1);
+    abort[warp] = 0;
+    ptx::fence_mbar_init();
+  }
+  __syncthreads();
+  bool ok = warp == 0 ? wait_bar_warp(bar, 0, abort) : wait_bars(bar, 0, lane == 3, abort + 1);
+  // (once the flag is up they give up without a limit's wait, and one that is over still goes on)
+  ok |= warp == 0 ? wait_bar_warp(bar, 0, abort) : wait_bars(bar, 0, lane == 30, abort + 1);
+  ok |= warp == 0 ? !wait_bar_warp(bar, 1, abort) : !wait_bars(bar, 1, true, abort + 1);
+  __syncthreads();
+  if (ok || abort[warp] != 1u) index_fail();
+}
+}  // namespace
+
+cudaError_t launch_cache_wait_probe(cudaStream_t st) {
+  (void)cudaGetLastError();
+  cache_wait_probe_kernel<<<1, 64, 0, st>>>();
+  return cudaGetLastError();
+}
+
 cudaError_t read_cache_error(uint32_t* err) {
   cudaError_t e = cudaMemcpyFromSymbol(err, g_cache_error, sizeof(uint32_t));
   if (e == cudaSuccess && *err) {

@@ -211,5 +211,7 @@ cudaError_t launch_gemm_nv(const uint8_t* qa, const uint8_t* sa, const uint8_t* 
                            cudaStream_t st, const char** why);
 // One-thread kernel whose bounded wait never completes (sets the error word).
 cudaError_t launch_wait_probe(cudaStream_t st);
+// The same for the waits of the attention over the 8-bit cache (in its own error word).
+cudaError_t launch_cache_wait_probe(cudaStream_t st);
 
 }  // namespace mx

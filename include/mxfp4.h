@@ -651,6 +651,12 @@ mxfp4_status mxfp4_bounds_check_shrink(int64_t bytes);
  * mxfp4_device_status (which also clears it). */
 mxfp4_status mxfp4_selftest_wait_timeout(void* stream);
 
+/* The same for the waits of mxfp8_cache_attention: whole warps that wait, for
+ * loads and for room, on barriers that nothing signals. MXFP4_ERR_TIMEOUT where
+ * every lane was told so within the limit, MXFP4_ERR_INVALID_ARG where one was
+ * not. */
+mxfp4_status mxfp8_selftest_cache_wait_timeout(void* stream);
+
 #ifdef __cplusplus
 }
 #endif
