@@ -414,8 +414,9 @@ __global__ void __launch_bounds__(1024) cache_read_kernel(CacheArgs c, Heads k, 
 // the workspace for cache_join_kernel.
 //
 // One tile a head is bound by HBM from 96 channels on (1 x 131072 tokens, 8 heads of
-// 128: 51 us, 77 % of a copy's rate), by the instructions of scores and conversions
-// at 64 (32 x 4096 tokens 32 us, 62 %); several tiles a head read again from L2 and
+// 128: 51 us, 77 % of a copy's rate), by the latency of scores and conversions
+// at 64 (32 x 4096 tokens 32 us, 62 %; half of the issue slots are empty: what follows one
+// another in a unit is not overlapped inside a warp); several tiles a head read again from L2 and
 // convert again (16 sequences of 1000 to 16384 tokens, 16 rows a head: 53 us, 53 %). A
 // call's least is its start and the join, about 6 us.
 
@@ -427,8 +428,9 @@ constexpr int kRows = 8;  // of a tile: sixteen, for half the conversions, gaine
 template <int D>
 struct Attn {
   // Warps that multiply: as many as their registers (sums D / 4, queries D / 8 of
-  // them) leave room for on the SM without spilling (128 channels: 50.6 us at 131072
-  // tokens with eleven, 57 with fifteen, which spill, 58 with seven). Then those that
+  // them) leave room for on the SM without spilling in earnest (at most 4 bytes, at 64
+  // channels and for fp32 results at 192 and 256; 128 channels: 50.6 us at 131072
+  // tokens with eleven, 57 with fifteen, which spill 180 and more, 58 with seven). Then those that
   // fetch for them, a lane for 16 tokens of a unit; a warp's copies go out one after
   // the other, and pages of 16 tokens of 64 channels need two (32 x 4096 tokens 33 us;
   // 48 with one).
@@ -1579,6 +1581,8 @@ cudaError_t launch_cache_append(const CacheArgs& c, const Heads& k, const Heads&
     return cudaGetLastError();
   }
   const Launch l = launch_shape(c, slots);
+  // (fp32 in blocks of more than 512 threads, pages of 128 tokens of 192 and 256 channels, spills 104 bytes:
+  // 8 prompts of 2048 tokens, 256 channels, 52 % of a copy's rate; 76 % at 128)
   (f32 ? l.block.x <= 512 ? cache_append_kernel<float, 512> : cache_append_kernel<float, 1024>
        : l.block.x <= 512 ? cache_append_kernel<uint16_t, 512> : cache_append_kernel<uint16_t, 1024>)
       <<<l.grid, l.block, 0, st>>>(c, k, v, l.share);
